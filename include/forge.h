@@ -21,8 +21,10 @@
  *     W <- W - lr (m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps).
  *     SGD follows torch.optim.SGD (dampening 0, no Nesterov):
  *     g' = g + wd W; buf <- mu buf + g'; W <- W - lr buf.
- *   - Gradient clipping is not offered: exact global-norm clipping cannot be
- *     fused ("Math verified, not asserted", P2).
+ *   - The fused steps offer no gradient clipping: exact global-norm clipping
+ *     cannot be fused ("Math verified, not asserted", P2).  The paths that
+ *     hold gradients in memory clip them with forge_grad_norm and
+ *     forge_clip_grads before the owner's step.
  *   - A routed (expert) weight whose expert received no tokens still takes
  *     the step with g = 0, i.e. m and v decay by b1, b2 and W by its weight
  *     decay (P5).
@@ -39,7 +41,7 @@
  * the current device (cudaMalloc, a memory pool or a virtual-memory mapping;
  * host memory, managed memory and a peer GPU's memory are refused) and the
  * library keeps no pointer after the call returns.  Calls whose operands TMA
- * can address allocate nothing.  Two cases take stream-ordered scratch from
+ * can address allocate nothing.  Four cases take stream-ordered scratch from
  * a memory pool the library creates per device (allocated and freed on
  * `stream`; the pool keeps what it has reserved, at most the largest scratch
  * in use at once, until the process ends):
@@ -53,7 +55,9 @@
  *     with cp.async instead; other rows need the copy, and a failed
  *     allocation returns FORGE_ERR_CUDA.  forge_wgrad_adamw_noalloc stages
  *     into a fixed buffer instead;
- *   - forge_backward_adamw without a bf16 weight copy (see there).
+ *   - forge_backward_adamw without a bf16 weight copy (see there);
+ *   - forge_embedding_grad and forge_embedding_adamw (the order of the tokens);
+ *   - forge_grad_norm (partial sums).
  * W, m, v, buf are updated in place.  Calls are asynchronous and ordered on
  * `stream`, and can be captured in a CUDA graph once a first call has run
  * on the device; the return value reports only host-side validation and
@@ -129,7 +133,9 @@ typedef enum {
 typedef enum {
     FORGE_BF16 = 0, /* bfloat16 */
     FORGE_E4M3 = 1, /* OCP fp8 E4M3 ("fn": no infinities, max 448) */
-    FORGE_F32 = 2   /* IEEE binary32 */
+    FORGE_F32 = 2,  /* IEEE binary32 */
+    FORGE_I32 = 3,  /* token ids only: 32-bit signed integers */
+    FORGE_I64 = 4   /* token ids only: 64-bit signed integers */
 } forge_dtype;
 
 /*
@@ -361,6 +367,152 @@ FORGE_API forge_status forge_owner_adamw(const float* G, float* W, void* m, void
 FORGE_API forge_status forge_owner_sgdm(const float* G, float* W, void* mom, int64_t n,
                                         forge_dtype state_dtype, float lr, float momentum,
                                         float wd, forge_stream_t stream);
+
+/*
+ * Log-probabilities of given tokens under rows of logits, with entropy and the
+ * top alternatives: the loss, the scoring of given answers and the answers of
+ * a decode step, in one pass over the logits.  For row r, z = scale * logits[r],
+ *   lse = ln sum_j exp z_j,   p_j = exp(z_j - lse),
+ *   logprob = z_t - lse (t = targets[r]),   entropy = -sum_j p_j ln p_j.
+ *   logits  device [R, V] of dtype (FORGE_BF16 or FORGE_F32), rows ld elements
+ *           apart (ld >= V: a padded vocabulary).  Rows of any alignment.
+ *   targets device [R] of id_dtype (FORGE_I32 or FORGE_I64), or NULL (then
+ *           logprob is NULL too and every row counts).  A negative target
+ *           marks padding: the row is not read, its logprob, lse, entropy and
+ *           top_logprob are 0 and its top_index -1.  A target >= V is recorded
+ *           as FORGE_ERR_INVALID_ARG in the device status word and its row
+ *           taken as padding.
+ *   scale   > 0: the inverse temperature.
+ *   logprob, lse, entropy  device fp32 [R], written; each may be NULL.
+ *   top_k   0 <= top_k <= min(V, 32); top_index (device int32) and top_logprob
+ *           (device fp32), [R, top_k], receive the top_k largest logits' columns
+ *           and log-probabilities, largest first; equal logits by the lower
+ *           column.
+ * Masked entries are -inf: their p is 0.  A row with no other entry has
+ * lse = logprob = top_logprob = -inf and entropy 0.  A NaN or +inf among a
+ * row's logits makes its logprob, lse, entropy and top_logprob NaN; NaN
+ * ranks above every number in the top entries.  Maxima, sums and results are
+ * held in fp32 or wider.  Allocates nothing.  R = 0 does nothing.
+ */
+FORGE_API forge_status forge_token_logprob(const void* logits, forge_dtype dtype, int64_t R,
+                                           int64_t V, int64_t ld, const void* targets,
+                                           forge_dtype id_dtype, float scale, float* logprob,
+                                           float* lse, float* entropy, int32_t top_k,
+                                           int32_t* top_index, float* top_logprob,
+                                           forge_stream_t stream);
+
+/*
+ * The gradient of sum_r (grad_logprob[r] logprob[r] + grad_entropy[r] entropy[r])
+ * by the logits of forge_token_logprob:
+ *   dlogits[r][j] = scale (a (1[j = t] - p_j) - b p_j (ln p_j + entropy[r])),
+ *   a = grad_logprob[r], b = grad_entropy[r], p_j = exp(scale logits[r][j] - lse[r]).
+ * With a = -1 / (rows that count), dlogits is the gradient of the mean
+ * cross-entropy: the bf16 dY of the head's forge_backward_adamw.
+ *   logits, dtype, R, V, ld, targets, id_dtype, scale  as given to
+ *           forge_token_logprob (targets not NULL); a row whose target is
+ *           padding, or whose lse is -inf, gets zeros.
+ *   lse     device fp32 [R], from forge_token_logprob.
+ *   grad_logprob  device fp32 [R].
+ *   entropy, grad_entropy  device fp32 [R]; grad_entropy may be NULL (no
+ *           entropy term), then entropy is not read.
+ *   dlogits device [R, V] of out_dtype (FORGE_BF16, rounded once to nearest
+ *           even, or FORGE_F32), rows ld_out >= V elements apart, written.  It
+ *           may be logits itself when out_dtype and ld_out equal dtype and ld;
+ *           any other overlap is not supported.
+ * Allocates nothing.
+ */
+FORGE_API forge_status forge_token_logprob_grad(
+    const void* logits, forge_dtype dtype, int64_t R, int64_t V, int64_t ld, const void* targets,
+    forge_dtype id_dtype, float scale, const float* lse, const float* grad_logprob,
+    const float* entropy, const float* grad_entropy, void* dlogits, forge_dtype out_dtype,
+    int64_t ld_out, forge_stream_t stream);
+
+/*
+ * The embedding lookup with scaling: Y[t] = scale * W[ids[t]].
+ *   ids     device [T] of id_dtype (FORGE_I32 or FORGE_I64).  A negative id is
+ *           padding: Y[t] = 0.  An id >= V is recorded as FORGE_ERR_INVALID_ARG
+ *           in the device status word and taken as padding.
+ *   W       device [V, D] of w_dtype (FORGE_BF16 or FORGE_F32).
+ *   Y       device [T, D] of y_dtype (FORGE_BF16, the fp32 product rounded once
+ *           to nearest even, or FORGE_F32), written.
+ * W and Y of any width and alignment.  Allocates nothing.  T = 0 does nothing.
+ */
+FORGE_API forge_status forge_embedding(const void* ids, forge_dtype id_dtype, int64_t T,
+                                       const void* W, forge_dtype w_dtype, int64_t V, int64_t D,
+                                       float scale, void* Y, forge_dtype y_dtype,
+                                       forge_stream_t stream);
+
+/*
+ * The gradient of forge_embedding by W, summed by tokens:
+ *   dW[r] = scale * sum over {t : ids[t] = r} of dY[t]   (+ dW[r] if accumulate)
+ *   dY      device [T, D] of dy_dtype (FORGE_BF16 or FORGE_F32); rows of padding
+ *           tokens are not read.
+ *   ids     as forge_embedding's.
+ *   dW      device fp32 [V, D].  accumulate = 0: written whole, rows without a
+ *           token as zeros.  accumulate != 0: added to; rows without a token are
+ *           neither read nor written.
+ * The tokens are first ordered by row on the device; a row's sum is taken in
+ * fp32 in an order that the ids alone determine, so results are bitwise
+ * reproducible.  The order, a table of the rows and the partial sums of rows
+ * with many tokens take stream-ordered scratch from the library's memory pool;
+ * a failed allocation returns FORGE_ERR_CUDA.
+ */
+FORGE_API forge_status forge_embedding_grad(const void* dY, forge_dtype dy_dtype, const void* ids,
+                                            forge_dtype id_dtype, int64_t T, int64_t V, int64_t D,
+                                            float scale, float* dW, int32_t accumulate,
+                                            forge_stream_t stream);
+
+/*
+ * forge_embedding_grad fused with one AdamW step on W, m, v: the gradient of a
+ * row is used where it is summed and never reaches device memory.  Rows
+ * without a token take the step with g = 0, as an expert without tokens does
+ * (P5).  W device fp32 [V, D]; m, v device [V, D] of state_dtype (FORGE_F32 or
+ * FORGE_BF16); lr ... step as forge_wgrad_adamw; the other arguments, the order
+ * of sums and the scratch as forge_embedding_grad.  W must not be read by
+ * another operation of the same step afterwards (the single-use guard of P1:
+ * an embedding tied to the head takes forge_embedding_grad).
+ */
+FORGE_API forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dtype, const void* ids,
+                                             forge_dtype id_dtype, int64_t T, int64_t V, int64_t D,
+                                             float scale, float* W, void* m, void* v,
+                                             forge_dtype state_dtype, float lr, float beta1,
+                                             float beta2, float eps, float wd, int64_t step,
+                                             forge_stream_t stream);
+
+/*
+ * The global norm of P gradient tensors, norm[0] = sqrt(sum of all g^2), for
+ * the paths that hold gradients in memory (forge_wgrad_only,
+ * forge_embedding_grad, an owner's shard): exact clipping needs every gradient
+ * before it may touch one, so the fused steps cannot offer it (P2).
+ *   grads   host array of P device pointers (NULL only where n[j] = 0) to n[j]
+ *           elements of dtype (FORGE_BF16 or FORGE_F32); read during the call only.
+ *   norm    device fp32[1], written (0 for P = 0).
+ * Squares are summed in fp32 over at most a few hundred elements and in fp64
+ * from there, in a fixed order: bitwise reproducible.  NaN and infinities
+ * propagate; a |g| above 1.8e19 counts as infinite.  Takes a few KB of
+ * stream-ordered scratch from the library's memory pool.
+ */
+FORGE_API forge_status forge_grad_norm(const void* const* grads, const int64_t* n, int32_t P,
+                                       forge_dtype dtype, float* norm, forge_stream_t stream);
+
+/*
+ * Clipping by a global norm: out[j] = grads[j] * min(1, max_norm / (norm[0] + 1e-6)),
+ * element by element, in fp32 and rounded once to out_dtype.
+ *   grads, n, P, dtype  as forge_grad_norm.
+ *   norm    device fp32[1]: forge_grad_norm's (under data parallelism, after
+ *           its square was summed over the ranks).  A NaN norm makes every
+ *           output NaN, as torch.nn.utils.clip_grad_norm_ does.
+ *   max_norm  >= 0 (infinity: never clips).
+ *   out     host array of P device pointers to n[j] elements of out_dtype.
+ *           out[j] may be grads[j] (clipping in place) when out_dtype is dtype;
+ *           a tensor clipped in place by a factor of exactly 1 is left as it is.
+ *           Other overlaps are not supported.
+ * Allocates nothing.
+ */
+FORGE_API forge_status forge_clip_grads(const void* const* grads, const int64_t* n, int32_t P,
+                                        forge_dtype dtype, const float* norm, float max_norm,
+                                        void* const* out, forge_dtype out_dtype,
+                                        forge_stream_t stream);
 
 /* Static description of a status code; never NULL. */
 FORGE_API const char* forge_status_string(forge_status status);

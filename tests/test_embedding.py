@@ -1,0 +1,310 @@
+"""The embedding lookup, its gradient by tokens and the gradient fused with
+AdamW, against the formulas in 64 bits on the CPU.
+
+Bounds: a product rounds once; a sum of n fp32 terms in any fixed order is off
+by at most (n + 2) 2^-24 times the sum of their magnitudes.  AdamW's m and v are
+two-term fp32 sums (2^-22 of their terms' magnitudes); W's step divides by
+sqrt(v') + eps with hardware approximations of a few 2^-23 (2^-19 of the step).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import weight_grad_gemm_gb300 as fg
+
+gpu = pytest.mark.gpu
+FAKE = ctypes.c_void_p(0x10000)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, wd=0.01, step=3)
+
+
+def token_ids(T, V, seed, kind="zipf"):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "zipf":
+        ids = (torch.exp(torch.rand(T, generator=g, dtype=torch.float64) * np.log(V + 1)) - 1).long()
+    elif kind == "one":
+        ids = torch.full((T,), V // 2)
+    elif kind == "two":
+        ids = torch.where(torch.rand(T, generator=g) < 0.5, 0, V - 1)
+    elif kind == "pad":
+        return torch.full((T,), -1)
+    elif kind == "ordered":
+        ids = torch.arange(T) * V // max(T, 1)
+    else:
+        ids = torch.randint(0, V, (T,), generator=g)
+    ids = ids.clamp(0, V - 1)
+    return torch.where(torch.rand(T, generator=g) < 0.1, -5, ids)
+
+
+def randn(shape, seed, dtype, std=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(DT[dtype])
+
+
+def shifted(t, offset):
+    """t on the GPU, `offset` elements past an aligned base."""
+    buf = torch.empty(t.numel() + offset + 8, dtype=t.dtype, device="cuda")
+    view = buf[offset:offset + t.numel()].view(t.shape)
+    view.copy_(t.cuda())
+    return view
+
+
+def sums(dY, ids, V, scale):
+    """The gradient, the sum of its terms' magnitudes and the terms' number, in 64 bits."""
+    D = dY.shape[1]
+    live = ids >= 0
+    G = torch.zeros(V, D, dtype=torch.float64).index_add_(0, ids[live], dY[live].double()) * scale
+    A = torch.zeros(V, D, dtype=torch.float64).index_add_(0, ids[live], dY[live].double().abs()) * abs(scale)
+    n = torch.bincount(ids[live], minlength=V).double()[:, None]
+    return G, A, n
+
+
+# ---- lookup ------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("weight", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,offset", [(1, 1, 1, 0), (1, 50, 4096, 0), (5, 7, 3, 0), (3, 9, 1023, 0),
+                                          (257, 1000, 264, 0), (64, 300, 520, 1), (64, 300, 520, 4),
+                                          (1000, 77, 130, 2), (3000, 5000, 1024, 0), (16, 40, 16384, 0)])
+def test_lookup(cuda_device, T, V, D, offset, weight, out):
+    W = randn((V, D), T + D, weight)
+    ids = token_ids(T, V, T)
+    Y = shifted(torch.full((T, D), 9.0).to(DT[out]), offset)
+    for idt, scale in ((torch.int32, 1.0), (torch.int64, -0.3)):
+        fg.forge_embedding(ids.to(idt).cuda(), shifted(W, offset), Y, scale=scale)
+        s32 = torch.tensor(scale)
+        want = (W.float()[ids.clamp(min=0)] * s32).masked_fill_((ids < 0)[:, None], 0.0).to(DT[out])
+        assert torch.equal(Y.cpu() + 0.0, want + 0.0)  # one fp32 product, one rounding
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+
+
+@gpu
+def test_lookup_refuses_nothing_for_no_tokens_and_records_bad_ids(cuda_device):
+    W = torch.ones(10, 8, device="cuda")
+    Y = torch.full((3, 8), 5.0, device="cuda")
+    fg.forge_embedding(torch.empty(0, dtype=torch.int64, device="cuda"), W, Y[:0])
+    fg.forge_embedding(torch.tensor([9, 10, 1 << 40], device="cuda"), W, Y)
+    assert fg.forge_get_device_status() == fg.FORGE_ERR_INVALID_ARG
+    assert Y[0].eq(1).all() and not Y[1:].any()
+
+
+@gpu
+def test_lookup_past_32_bit_offsets(cuda_device):
+    V, D = 70000, 32768
+    W = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    W[V - 1] = 3.0
+    Y = torch.empty(2, D, dtype=torch.bfloat16, device="cuda")
+    fg.forge_embedding(torch.tensor([V - 1, 0], device="cuda"), W, Y, scale=2.0)
+    assert Y[0].eq(6).all() and not Y[1].any()
+
+
+# ---- gradient ------------------------------------------------------------------
+
+GRADS = [(0, 5, 3, "zipf"), (1, 1, 1, "zipf"), (1, 1000, 4096, "uniform"), (7, 3, 5, "zipf"),
+         (130, 1000, 264, "zipf"), (1000, 50, 1023, "zipf"), (1000, 70000, 8, "uniform"),
+         (5000, 300, 520, "zipf"), (4097, 2, 130, "two"), (3000, 100, 256, "one"), (20000, 1, 16, "one"),
+         (513, 40, 72, "pad"), (4096, 4096, 96, "ordered"), (300, 20000, 1000, "zipf"),
+         (40000, 3000, 33, "zipf"), (2048, 128, 2056, "zipf")]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,kind", GRADS)
+def test_gradient_matches_the_formula(cuda_device, T, V, D, kind, dtype):
+    ids = token_ids(T, V, T + V, kind)
+    dY = randn((T, D), T + D, dtype)
+    scale = 1.5
+    G, A, n = sums(dY, ids, V, scale)
+    tol = (n + 2) * 2.0 ** -24 * A
+    dW = torch.full((V, D), 7.0, device="cuda")
+    fg.forge_embedding_grad(dY.cuda(), ids.to(torch.int32).cuda(), dW, scale=scale)
+    assert torch.all((dW.cpu().double() - G).abs() <= tol)
+    again = torch.full((V, D), 8.0, device="cuda")
+    fg.forge_embedding_grad(dY.cuda(), ids.cuda(), again, scale=scale)  # 64-bit ids, bitwise the same
+    assert torch.equal(dW, again)
+    start = randn((V, D), 5, "f32")
+    acc = start.cuda()
+    fg.forge_embedding_grad(dY.cuda(), ids.cuda(), acc, scale=scale, accumulate=True)
+    want = start.double() + G
+    assert torch.all((acc.cpu().double() - want).abs() <= tol + want.abs() * 2.0 ** -23)
+    untouched = (n[:, 0] == 0).nonzero()[:, 0]
+    assert torch.equal(acc.cpu()[untouched], start[untouched])
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+
+
+@gpu
+@pytest.mark.parametrize("offset", [1, 2, 4])
+@pytest.mark.parametrize("D", [1, 130, 264])
+def test_gradient_alignment(cuda_device, D, offset):
+    T, V = 500, 60
+    ids = token_ids(T, V, 3)
+    dY = randn((T, D), 4, "bf16")
+    G, A, n = sums(dY, ids, V, 1.0)
+    dW = shifted(torch.zeros(V, D), offset)
+    fg.forge_embedding_grad(shifted(dY, offset), ids.cuda(), dW)
+    assert torch.all((dW.cpu().double() - G).abs() <= (n + 2) * 2.0 ** -24 * A)
+
+
+@gpu
+def test_gradient_is_the_adjoint_of_the_lookup(cuda_device):
+    """<dW, E> = <dY, lookup(E)> for any E: the difference quotient of a linear
+    map.  Both inner products are taken in 64 bits of fp32 results."""
+    T, V, D = 700, 90, 200
+    ids = token_ids(T, V, 8).cuda()
+    dY = randn((T, D), 1, "f32").cuda()
+    E = randn((V, D), 2, "f32").cuda()
+    Y, dW = torch.empty(T, D, device="cuda"), torch.empty(V, D, device="cuda")
+    fg.forge_embedding(ids, E, Y, scale=0.5)
+    fg.forge_embedding_grad(dY, ids, dW, scale=0.5)
+    left, right = (dW.double() * E.double()).sum(), (dY.double() * Y.double()).sum()
+    size = (dY.double().abs() * Y.double().abs()).sum()
+    assert (left - right).abs() <= 100 * 2.0 ** -24 * size
+
+
+@gpu
+def test_gradient_bad_ids_streams_and_graphs(cuda_device):
+    T, V, D = 600, 100, 264
+    ids = token_ids(T, V, 2)
+    dY = randn((T, D), 1, "bf16").cuda()
+    dW = torch.empty(V, D, device="cuda")
+    fg.forge_embedding_grad(dY, ids.cuda(), dW)
+    bad = ids.clone()
+    bad[ids < 0] = V + 3
+    other = torch.empty(V, D, device="cuda")
+    fg.forge_embedding_grad(dY, bad.cuda(), other)
+    assert fg.forge_get_device_status() == fg.FORGE_ERR_INVALID_ARG
+    assert torch.equal(dW, other)
+    idg = ids.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other.zero_()
+        fg.forge_embedding_grad(dY, idg, other)
+    side.synchronize()
+    assert torch.equal(dW, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fg.forge_embedding_grad(dY, idg, other)
+    for _ in range(2):
+        other.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dW, other)
+
+
+# ---- gradient + AdamW -----------------------------------------------------------
+
+def adamw_reference(G, A, n, W, m, v, hp):
+    hp = {k: float(np.float32(x)) for k, x in hp.items()}
+    b1, b2, step = hp["beta1"], hp["beta2"], int(hp["step"])
+    m1 = b1 * m + (1 - b1) * G
+    v1 = b2 * v + (1 - b2) * G * G
+    den = torch.sqrt(v1 / (1 - b2 ** step)) + hp["eps"]
+    up = hp["lr"] / (1 - b1 ** step) * m1 / den
+    W1 = W * float(np.float32(1 - hp["lr"] * hp["wd"])) - up  # the decay factor is a 32-bit value
+    dG = (n + 2) * 2.0 ** -24 * A                        # of the sum
+    dm = (1 - b1) * dG + 2.0 ** -22 * (b1 * m.abs() + (1 - b1) * G.abs())
+    dv = (1 - b2) * 2 * G.abs() * dG + 2.0 ** -22 * v1 + 2.0 ** -130
+    dW = hp["lr"] / (1 - b1 ** step) * dm / den + up.abs() * (2.0 ** -19 + dv / v1.clamp(min=1e-37)) \
+        + 2.0 ** -23 * W.abs()
+    return (W1, dW), (m1, dm), (v1, dv)
+
+
+@gpu
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,kind,offset", [(0, 9, 5, "zipf", 0), (1, 1, 1, "zipf", 0), (40, 700, 264, "zipf", 0),
+                                               (3000, 90, 130, "zipf", 0), (900, 50, 1023, "zipf", 0),
+                                               (5000, 3, 72, "one", 0), (513, 2000, 520, "zipf", 2),
+                                               (64, 30, 4096, "uniform", 0)])
+def test_fused_step_matches_the_formula(cuda_device, T, V, D, kind, offset, dtype, state):
+    ids = token_ids(T, V, T + 1, kind)
+    dY = randn((T, D), 3, dtype, 1e-2)
+    W, m = randn((V, D), 4, "f32", 0.02), randn((V, D), 5, state, 1e-3)
+    v = (randn((V, D), 6, "f32", 1e-3) ** 2 + 1e-9).to(DT[state])
+    G, A, n = sums(dY, ids, V, 0.5)
+    gpu_state = [shifted(t, offset) for t in (W, m, v)]
+    fg.forge_embedding_adamw(shifted(dY, offset), ids.cuda(), *gpu_state, scale=0.5, **HP)
+    want = adamw_reference(G, A, n, W.double(), m.double(), v.double(), HP)
+    for name, got, (x, tol) in zip("Wmv", gpu_state, want):
+        if name != "W" and state == "bf16":
+            tol = tol + x.abs() * 2.0 ** -8
+        err = (got.cpu().double() - x).abs()
+        assert torch.all(err <= tol), (name, float((err / tol.clamp(min=1e-300)).max()))
+
+
+@gpu
+def test_fused_step_equals_gradient_then_owner_step(cuda_device):
+    T, V, D = 3000, 400, 264
+    ids = token_ids(T, V, 1).cuda()
+    dY = randn((T, D), 3, "bf16", 1e-2).cuda()
+    W, m = randn((V, D), 4, "f32", 0.02).cuda(), torch.zeros(V, D, device="cuda")
+    v = torch.zeros(V, D, device="cuda")
+    dW = torch.empty(V, D, device="cuda")
+    fg.forge_embedding_grad(dY, ids, dW, scale=2.0)
+    a = [t.clone() for t in (W, m, v)]
+    fg.forge_owner_adamw(dW, *a, **HP)
+    b = [t.clone() for t in (W, m, v)]
+    fg.forge_embedding_adamw(dY, ids, *b, scale=2.0, **HP)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ---- refusals --------------------------------------------------------------------
+
+def test_refusals_before_any_launch():
+    L = fg.lib()
+    hp = (1e-3, 0.9, 0.999, 1e-8, 0.01)
+
+    def e(ids=FAKE, idt=fg.FORGE_I32, T=4, W=FAKE, wdt=fg.FORGE_F32, V=8, D=8, scale=1.0, Y=FAKE, ydt=fg.FORGE_BF16):
+        return L.forge_embedding(ids, idt, T, W, wdt, V, D, scale, Y, ydt, None)
+
+    def g(dY=FAKE, dt=fg.FORGE_BF16, ids=FAKE, idt=fg.FORGE_I32, T=4, V=8, D=8, scale=1.0, dW=FAKE):
+        return L.forge_embedding_grad(dY, dt, ids, idt, T, V, D, scale, dW, 0, None)
+
+    def a(dY=FAKE, dt=fg.FORGE_BF16, ids=FAKE, idt=fg.FORGE_I32, T=4, V=8, D=8, scale=1.0, W=FAKE, m=FAKE, v=FAKE,
+          st=fg.FORGE_F32, hp=hp, step=1):
+        return L.forge_embedding_adamw(dY, dt, ids, idt, T, V, D, scale, W, m, v, st, *hp, step, None)
+    bad, dtype, mis = fg.FORGE_ERR_INVALID_ARG, fg.FORGE_ERR_UNSUPPORTED_DTYPE, fg.FORGE_ERR_MISALIGNED
+    odd = ctypes.c_void_p(0x10001)
+    for kw in (dict(ids=None), dict(W=None), dict(Y=None), dict(T=-1), dict(V=0), dict(D=0),
+               dict(scale=float("inf")), dict(T=1 << 31), dict(D=1 << 31)):
+        assert e(**kw) == bad, kw
+    for kw in (dict(idt=fg.FORGE_F32), dict(wdt=fg.FORGE_E4M3), dict(ydt=fg.FORGE_I32)):
+        assert e(**kw) == dtype, kw
+    for kw in (dict(ids=odd), dict(W=odd), dict(Y=odd)):
+        assert e(**kw) == mis, kw
+    for fn in (g, a):
+        for kw in (dict(dY=None), dict(ids=None), dict(T=-1), dict(V=0), dict(D=-1), dict(scale=float("nan"))):
+            assert fn(**kw) == bad, kw
+        for kw in (dict(dt=fg.FORGE_E4M3), dict(idt=fg.FORGE_BF16)):
+            assert fn(**kw) == dtype, kw
+        for kw in (dict(dY=odd), dict(ids=odd)):
+            assert fn(**kw) == mis, kw
+    assert g(dW=None) == bad and g(dW=odd) == mis
+    assert a(W=None) == bad and a(m=None) == bad and a(v=None) == bad and a(step=0) == bad
+    assert a(hp=(1e-3, 1.0, 0.999, 1e-8, 0.0)) == bad and a(st=fg.FORGE_E4M3) == dtype
+    assert a(m=odd) == mis and a(W=ctypes.c_void_p(0x10002)) == mis
+
+
+@gpu
+def test_binding_refuses_what_does_not_fit(cuda_device):
+    W = torch.zeros(6, 8, device="cuda")
+    Y = torch.zeros(3, 8, device="cuda")
+    ids = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        fg.forge_embedding(ids[:2], W, Y)
+    with pytest.raises(ValueError):
+        fg.forge_embedding(ids, W[:, :4], Y)
+    with pytest.raises(TypeError):
+        fg.forge_embedding(ids.float(), W, Y)
+    with pytest.raises(TypeError):
+        fg.forge_embedding(ids, W.half(), Y)
+    with pytest.raises(TypeError):
+        fg.forge_embedding_grad(Y, ids, W.bfloat16())
+    with pytest.raises(ValueError):
+        fg.forge_embedding_adamw(Y, ids, W, W[:5], W, **HP)
+    with pytest.raises(ValueError):
+        fg.forge_embedding_grad(Y, ids.cpu(), W)

@@ -32,11 +32,15 @@ FORGE_ERR_SCRATCH_TOO_SMALL = -7
 FORGE_BF16 = 0
 FORGE_E4M3 = 1
 FORGE_F32 = 2
+FORGE_I32 = 3
+FORGE_I64 = 4
 
 EXPORTS = ("forge_wgrad_adamw", "forge_wgrad_adamw_noalloc", "forge_wgrad_adamw_multi",
            "forge_wgrad_sgdm", "forge_wgrad_only",
            "forge_quantize_e4m3", "forge_dgrad", "forge_backward_adamw",
            "forge_grouped_wgrad_adamw", "forge_owner_adamw", "forge_owner_sgdm",
+           "forge_token_logprob", "forge_token_logprob_grad", "forge_embedding",
+           "forge_embedding_grad", "forge_embedding_adamw", "forge_grad_norm", "forge_clip_grads",
            "forge_status_string", "forge_get_device_status",
            "forge_selftest_wait_timeout", "forge_version")
 
@@ -74,7 +78,18 @@ def lib() -> ctypes.CDLL:
                                             F, F, I64, P, P]
     L.forge_owner_adamw.argtypes = [P, P, P, P, I64, I, F, F, F, F, F, I64, P]
     L.forge_owner_sgdm.argtypes = [P, P, P, I64, I, F, F, F, P]
-    for f in ("forge_wgrad_adamw", "forge_wgrad_adamw_noalloc", "forge_wgrad_adamw_multi",
+    L.forge_token_logprob.argtypes = [P, I, I64, I64, I64, P, I, F, P, P, P, I32, P, P, P]
+    L.forge_token_logprob_grad.argtypes = [P, I, I64, I64, I64, P, I, F, P, P, P, P, P, I, I64, P]
+    L.forge_embedding.argtypes = [P, I, I64, P, I, I64, I64, F, P, I, P]
+    L.forge_embedding_grad.argtypes = [P, I, P, I, I64, I64, I64, F, P, I32, P]
+    L.forge_embedding_adamw.argtypes = [P, I, P, I, I64, I64, I64, F, P, P, P, I, F, F, F, F, F,
+                                        I64, P]
+    L.forge_grad_norm.argtypes = [P, P, I32, I, P, P]
+    L.forge_clip_grads.argtypes = [P, P, I32, I, P, F, P, I, P]
+    for f in ("forge_token_logprob", "forge_token_logprob_grad", "forge_embedding",
+              "forge_embedding_grad", "forge_embedding_adamw", "forge_grad_norm",
+              "forge_clip_grads",
+              "forge_wgrad_adamw", "forge_wgrad_adamw_noalloc", "forge_wgrad_adamw_multi",
               "forge_wgrad_sgdm",
               "forge_wgrad_only", "forge_quantize_e4m3", "forge_dgrad", "forge_backward_adamw",
               "forge_grouped_wgrad_adamw", "forge_owner_adamw", "forge_owner_sgdm",
@@ -310,6 +325,173 @@ def forge_owner_sgdm(G, W, mom, *, lr, momentum, wd, stream=None):
     s = lib().forge_owner_sgdm(_ptr(G), _ptr(W), _ptr(mom), G.numel(), _dtype_code(mom), lr,
                                momentum, wd, _stream(stream, W))
     _check(s, "forge_owner_sgdm")
+
+
+def _id_code(t) -> int:
+    import torch
+    if t.dtype == torch.int32:
+        return FORGE_I32
+    if t.dtype == torch.int64:
+        return FORGE_I64
+    raise TypeError(f"token ids must be int32 or int64, got {t.dtype}")
+
+
+def _float_code(t) -> int:
+    code = _dtype_code(t)
+    if code == FORGE_E4M3:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _rows(t, what):
+    """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [R, V] with contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"the rows of {what} overlap")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _vector(t, n, what):
+    """Pointer of an fp32 tensor of n elements, or None."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.float32 or t.numel() != n:
+        raise ValueError(f"{what} must be float32 with {n} elements")
+    return _ptr(t)
+
+
+def forge_token_logprob(logits, targets, logprob, *, lse=None, entropy=None, top_index=None,
+                        top_logprob=None, scale=1.0, stream=None):
+    """logprob [R] of the target tokens under logits [R, V] (bf16 or fp32, rows
+    of any stride), and where given lse [R], entropy [R] and the k best
+    entries top_index [R, k] (int32), top_logprob [R, k] of each row.  targets
+    [R] int32 or int64, negative for padding; logprob and targets may both be
+    None (see include/forge.h)."""
+    import torch
+    lp, ld = _rows(logits, "logits")
+    R, V = logits.shape
+    if targets is not None and targets.numel() != R:
+        raise ValueError(f"targets must have {R} elements")
+    k = 0
+    if (top_index is None) != (top_logprob is None):
+        raise ValueError("top_index and top_logprob go together")
+    if top_index is not None:
+        k = top_index.shape[-1]
+        if tuple(top_index.shape) != (R, k) or tuple(top_logprob.shape) != (R, k):
+            raise ValueError(f"top_index and top_logprob must be [R={R}, k]")
+        if top_index.dtype != torch.int32 or top_logprob.dtype != torch.float32:
+            raise TypeError("top_index must be int32 and top_logprob float32")
+    s = lib().forge_token_logprob(lp, _float_code(logits), R, V, ld, _ptr(targets),
+                                  FORGE_I32 if targets is None else _id_code(targets), scale,
+                                  _vector(logprob, R, "logprob"), _vector(lse, R, "lse"),
+                                  _vector(entropy, R, "entropy"), k, _ptr(top_index),
+                                  _ptr(top_logprob), _stream(stream, logits))
+    _check(s, "forge_token_logprob")
+
+
+def forge_token_logprob_grad(logits, targets, lse, grad_logprob, dlogits, *, entropy=None,
+                             grad_entropy=None, scale=1.0, stream=None):
+    """dlogits [R, V] (bf16 or fp32, rows of any stride; may be logits itself)
+    of sum(grad_logprob * logprob + grad_entropy * entropy), from the lse and
+    entropy that forge_token_logprob gave."""
+    lp, ld = _rows(logits, "logits")
+    dp, ldo = _rows(dlogits, "dlogits")
+    R, V = logits.shape
+    if tuple(dlogits.shape) != (R, V) or targets.numel() != R:
+        raise ValueError(f"dlogits must be [R={R}, V={V}] and targets [R]")
+    s = lib().forge_token_logprob_grad(lp, _float_code(logits), R, V, ld, _ptr(targets),
+                                       _id_code(targets), scale, _vector(lse, R, "lse"),
+                                       _vector(grad_logprob, R, "grad_logprob"),
+                                       _vector(entropy, R, "entropy"),
+                                       _vector(grad_entropy, R, "grad_entropy"), dp,
+                                       _float_code(dlogits), ldo, _stream(stream, logits))
+    _check(s, "forge_token_logprob_grad")
+
+
+def _embedding_sizes(ids, rows, V_D):
+    if len(V_D) != 2 or rows.dim() != 2 or tuple(rows.shape) != (ids.numel(), V_D[1]):
+        raise ValueError(f"ids of T elements, [T, D] and [V, D] expected, got {tuple(ids.shape)}, "
+                         f"{tuple(rows.shape)}, {tuple(V_D)}")
+    return ids.numel(), V_D[0], V_D[1]
+
+
+def forge_embedding(ids, W, Y, *, scale=1.0, stream=None):
+    """Y [T, D] = scale * W[ids] for ids of T elements (int32 or int64, negative
+    for padding: a zero row) and W [V, D]; W and Y bf16 or fp32 each."""
+    T, V, D = _embedding_sizes(ids, Y, W.shape)
+    s = lib().forge_embedding(_ptr(ids), _id_code(ids), T, _ptr(W), _float_code(W), V, D, scale,
+                              _ptr(Y), _float_code(Y), _stream(stream, Y))
+    _check(s, "forge_embedding")
+
+
+def forge_embedding_grad(dY, ids, dW, *, scale=1.0, accumulate=False, stream=None):
+    """dW [V, D] (fp32) = scale * the sum of dY [T, D] (bf16 or fp32) by ids, or
+    that added to dW (accumulate)."""
+    import torch
+    T, V, D = _embedding_sizes(ids, dY, dW.shape)
+    if dW.dtype != torch.float32:
+        raise TypeError("dW must be float32")
+    s = lib().forge_embedding_grad(_ptr(dY), _float_code(dY), _ptr(ids), _id_code(ids), T, V, D,
+                                   scale, _ptr(dW), int(bool(accumulate)), _stream(stream, dW))
+    _check(s, "forge_embedding_grad")
+
+
+def forge_embedding_adamw(dY, ids, W, m, v, *, lr, beta1, beta2, eps, wd, step, scale=1.0,
+                          stream=None):
+    """The sum of dY [T, D] by ids as the gradient of one AdamW step on W (fp32),
+    m, v (fp32 or bf16), all [V, D], in one pass over them."""
+    import torch
+    T, V, D = _embedding_sizes(ids, dY, W.shape)
+    if tuple(m.shape) != (V, D) or tuple(v.shape) != (V, D):
+        raise ValueError(f"W/m/v must be [V={V}, D={D}]")
+    if W.dtype != torch.float32 or m.dtype != v.dtype:
+        raise TypeError("W must be float32, m and v one dtype")
+    s = lib().forge_embedding_adamw(_ptr(dY), _float_code(dY), _ptr(ids), _id_code(ids), T, V, D,
+                                    scale, _ptr(W), _ptr(m), _ptr(v), _float_code(m), lr, beta1,
+                                    beta2, eps, wd, int(step), _stream(stream, W))
+    _check(s, "forge_embedding_adamw")
+
+
+def _tensor_list(ts, what):
+    """Pointers, element counts and the common dtype of a list of tensors."""
+    n = len(ts)
+    dtype = ts[0].dtype if n else None
+    for t in ts:
+        if t.dtype != dtype:
+            raise TypeError(f"{what} must share one dtype")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous CUDA tensors")
+    ptrs = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in ts])
+    sizes = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in ts])
+    return ptrs, sizes, FORGE_F32 if n == 0 else _float_code(ts[0])
+
+
+def forge_grad_norm(grads, norm, *, stream=None):
+    """norm (fp32 [1]) = the square root of the sum of squares over all tensors
+    of grads (a list, bf16 or fp32)."""
+    ptrs, sizes, code = _tensor_list(grads, "grads")
+    s = lib().forge_grad_norm(ptrs, sizes, len(grads), code, _vector(norm, 1, "norm"),
+                              _stream(stream, norm))
+    _check(s, "forge_grad_norm")
+
+
+def forge_clip_grads(grads, norm, out=None, *, max_norm, stream=None):
+    """out[j] = grads[j] * min(1, max_norm / (norm + 1e-6)); in place without
+    out, whose tensors may be of the other dtype (bf16 or fp32)."""
+    ptrs, sizes, code = _tensor_list(grads, "grads")
+    optrs, ocode = ptrs, code
+    if out is not None:
+        if [t.numel() for t in out] != [t.numel() for t in grads]:
+            raise ValueError("out must have one tensor of the same size for each of grads")
+        optrs, _, ocode = _tensor_list(out, "out")
+    s = lib().forge_clip_grads(ptrs, sizes, len(grads), code, _vector(norm, 1, "norm"), max_norm,
+                               optrs, ocode, _stream(stream, norm))
+    _check(s, "forge_clip_grads")
 
 
 def forge_status_string(status: int) -> str:

@@ -1,6 +1,6 @@
 """Build libforge.so in-tree with nvcc for sm_103a (GB300).
 
-The three translation units (host API, bf16 kernels, e4m3 kernels) compile
+The translation units (host API, the kernels by type and operation) compile
 in parallel, then link into weight_grad_gemm_gb300/libforge.so with the CUDA
 runtime linked statically, so loading the library needs no GPU and no
 libcuda until the first CUDA call.
@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libforge.so")
 
 SOURCES = ["forge_api.cu", "kernels_bf16.cu", "kernels_e4m3.cu", "kernels_pair_bf16.cu",
            "kernels_pair_e4m3.cu", "forge_static_stage.cu", "forge_quant.cu", "forge_dgrad.cu",
-           "forge_owner.cu"]
+           "forge_owner.cu", "forge_logprob.cu", "forge_embedding.cu", "forge_clip.cu"]
 HEADERS = ["forge_ptx.cuh", "forge_kernel.cuh", "forge_launch.cuh", "forge_static_stage.h",
            "forge_device.h"]
 

@@ -845,6 +845,14 @@ forge_status forge::adamw_checks(const void* X, const void* dY, const float* W, 
     return FORGE_OK;
 }
 
+forge_status forge::adamw_params(Params* p, float lr, float beta1, float beta2, float eps,
+                                 float wd, int64_t step)
+{
+    const forge_status s = check_adam(lr, beta1, beta2, eps, wd, step);
+    if (s == FORGE_OK) fill_adam(*p, lr, beta1, beta2, eps, wd, step);
+    return s;
+}
+
 namespace {
 
 // The owner-side step behind a reduce-scatter: checks, then one HBM-bound

@@ -65,4 +65,8 @@ forge_status adamw_checks(const void* X, const void* dY, const float* W, const v
                           forge_dtype state_dtype, float lr, float beta1, float beta2, float eps,
                           float wd, int64_t step);
 
+// The AdamW hyperparameter checks, then the step's coefficients into *p.
+forge_status adamw_params(Params* p, float lr, float beta1, float beta2, float eps, float wd,
+                          int64_t step);
+
 }  // namespace forge
