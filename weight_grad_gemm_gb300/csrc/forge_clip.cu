@@ -20,7 +20,35 @@ namespace forge {
 namespace clip {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 512;
+constexpr int kBlocksPerSm = 8;
+constexpr int kTable = 512;                       // tensors of one launch
+constexpr int kMinChunkBits = 11, kMaxChunkBits = 15;
+constexpr int kFlight = 4;                        // 16-byte loads in flight per thread
+
+// The tensors of one launch, cut into chunks of 2^chunk_bits elements; tensor
+// j's chunks are [begin[j], begin[j + 1]) of the launch's.
+struct Table {
+    const void* in[kTable];
+    void* out[kTable];
+    int64_t n[kTable];
+    uint32_t begin[kTable + 1];
+    int32_t count;
+    int32_t chunk_bits;
+};
+
+// The tensor that chunk c belongs to: begin[j] <= c < begin[j + 1].
+__device__ __forceinline__ int tensor_of(const Table& t, uint32_t c)
+{
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.begin[mid] <= c)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
 
 __device__ __forceinline__ float load1(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p, int64_t i)
@@ -33,51 +61,159 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, int64_t i, float x)
     p[i] = __float2bfloat16_rn(x);
 }
 
-__device__ __forceinline__ double block_sum(double x, double* sh)
+__device__ __forceinline__ void to_float(const uint4& u, float (&x)[4])
 {
-    sh[threadIdx.x] = x;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
-        __syncthreads();
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void to_float(const uint4& u, float (&x)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-    return sh[0];
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+}
+template <int N>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
+{
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (N == 8)
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
 }
 
+__device__ __forceinline__ bool is_aligned(const void* p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+__device__ __forceinline__ double block_sum(double x, double* sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double s = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
+    return s;
+}
+
+// part[block] = the sum of squares over this block's chunks.  A thread adds at
+// most 2^15 / 256 = 128 squares in fp32 before it goes on in fp64.  Bound by
+// HBM: each gradient is read once.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    forge_square_sum_kernel(const T* g, int64_t n, double* part)
+    forge_square_sum_kernel(const __grid_constant__ Table t, double* part)
 {
-    __shared__ double sh[kThreads];
-    float s = 0.0f;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(kBlocks) * kThreads) {
-        const float x = load1(g, i);
-        s = fmaf(x, x, s);
+    __shared__ double sh[kThreads / 32];
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    double total = 0.0;
+    for (uint32_t c = blockIdx.x; c < t.begin[t.count]; c += gridDim.x) {
+        const int j = tensor_of(t, c);
+        const int64_t first = static_cast<int64_t>(c - t.begin[j]) << t.chunk_bits;
+        const T* g = static_cast<const T*>(t.in[j]) + first;
+        const int64_t left = t.n[j] - first;
+        const int n = static_cast<int>(left < (1 << t.chunk_bits) ? left : 1 << t.chunk_bits);
+        float s[4] = {};
+        int done = 0;
+        if (is_aligned(g, 16)) {
+            const int nv = n / N;
+            for (int v0 = threadIdx.x; v0 < nv; v0 += kFlight * kThreads) {
+                uint4 u[kFlight];
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f)
+                    u[f] = v0 + f * kThreads < nv
+                               ? __ldg(reinterpret_cast<const uint4*>(g) + v0 + f * kThreads)
+                               : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f) {
+                    float x[N];
+                    to_float(u[f], x);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) s[k & 3] = fmaf(x[k], x[k], s[k & 3]);
+                }
+            }
+            done = nv * N;
+        }
+        for (int i = done + threadIdx.x; i < n; i += kThreads) {
+            const float x = load1(g, i);
+            s[0] = fmaf(x, x, s[0]);
+        }
+        total += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
     }
-    const double total = block_sum(s, sh);
+    total = block_sum(total, sh);
     if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
 __global__ void __launch_bounds__(kThreads)
     forge_norm_fold_kernel(const double* part, int64_t n, float* norm)
 {
-    __shared__ double sh[kThreads];
+    __shared__ double sh[kThreads / 32];
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) s += part[i];
     s = block_sum(s, sh);
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
 }
 
+// out = in times the factor.  The chunks are walked from the last to the
+// first: what the norm's pass read last is still in L2.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads)
-    forge_clip_kernel(const T* g, O* out, int64_t n, const float* norm, float max_norm)
+    forge_clip_kernel(const __grid_constant__ Table t, const float* norm, float max_norm)
 {
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
     const float q = max_norm / (*norm + 1e-6f);
-    const float c = q > 1.0f ? 1.0f : q;  // a NaN stays
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(kBlocks) * kThreads)
-        store1(out, i, load1(g, i) * c);
+    const float m = q > 1.0f ? 1.0f : q;  // a NaN stays
+    const uint32_t chunks = t.begin[t.count];
+    for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+        const uint32_t c = chunks - 1 - b;
+        const int j = tensor_of(t, c);
+        if (m == 1.0f && t.in[j] == t.out[j]) continue;  // in place, nothing to scale
+        const int64_t first = static_cast<int64_t>(c - t.begin[j]) << t.chunk_bits;
+        const T* g = static_cast<const T*>(t.in[j]) + first;
+        O* o = static_cast<O*>(t.out[j]) + first;
+        const int64_t left = t.n[j] - first;
+        const int n = static_cast<int>(left < (1 << t.chunk_bits) ? left : 1 << t.chunk_bits);
+        int done = 0;
+        if (is_aligned(g, 16) && is_aligned(o, N * sizeof(O) < 16 ? 8 : 16)) {
+            const int nv = n / N;
+            for (int v0 = threadIdx.x; v0 < nv; v0 += kFlight * kThreads) {
+                uint4 u[kFlight];
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f)
+                    if (v0 + f * kThreads < nv)
+                        u[f] = __ldcs(reinterpret_cast<const uint4*>(g) + v0 + f * kThreads);
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f) {
+                    if (v0 + f * kThreads >= nv) continue;
+                    float x[N];
+                    to_float(u[f], x);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) x[k] *= m;
+                    store_vec<N>(o + static_cast<int64_t>(v0 + f * kThreads) * N, x);
+                }
+            }
+            done = nv * N;
+        }
+        for (int i = done + threadIdx.x; i < n; i += kThreads) store1(o, i, load1(g, i) * m);
+    }
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -103,6 +239,44 @@ forge_status check_memory(const void* const* ptr, const int64_t* n, int32_t P, f
     return FORGE_OK;
 }
 
+// Cuts the tensors into tables of at most kTable and calls launch(table,
+// blocks) for each that has elements.  Chunks are as long as leaves every
+// block four of them, within limits.
+template <typename F>
+forge_status for_tables(const void* const* in, void* const* out, const int64_t* n, int32_t P,
+                        int sms, F launch)
+{
+    const uint32_t full = static_cast<uint32_t>(kBlocksPerSm) * sms;
+    int32_t j = 0;
+    while (j < P) {
+        Table t;
+        int64_t total = 0;
+        int32_t k = j;
+        t.count = 0;
+        for (; k < P && t.count < kTable; ++k) {
+            if (n[k] == 0) continue;
+            t.in[t.count] = in[k];
+            t.out[t.count] = out ? out[k] : nullptr;
+            t.n[t.count++] = n[k];
+            total += n[k];
+        }
+        j = k;
+        if (t.count == 0) break;
+        t.chunk_bits = kMaxChunkBits;
+        while (t.chunk_bits > kMinChunkBits && (total >> t.chunk_bits) < 4 * full) --t.chunk_bits;
+        int64_t chunks = 0;
+        for (int32_t i = 0; i < t.count; ++i) {
+            t.begin[i] = static_cast<uint32_t>(chunks);
+            chunks += (t.n[i] + (int64_t{1} << t.chunk_bits) - 1) >> t.chunk_bits;
+            if (chunks > UINT32_MAX / 2) return FORGE_ERR_INVALID_ARG;
+        }
+        t.begin[t.count] = static_cast<uint32_t>(chunks);
+        launch(t, static_cast<uint32_t>(chunks) < full ? static_cast<uint32_t>(chunks) : full);
+        if (cudaGetLastError() != cudaSuccess) return FORGE_ERR_CUDA;
+    }
+    return FORGE_OK;
+}
+
 }  // namespace clip
 }  // namespace forge
 
@@ -123,27 +297,28 @@ extern "C" forge_status forge_grad_norm(const void* const* grads, const int64_t*
     if ((st = check_memory(grads, n, P, dtype)) != FORGE_OK) return st;
     if (!aligned(norm, 4)) return FORGE_ERR_MISALIGNED;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t parts = static_cast<int64_t>(P) * kBlocks;
+    const int64_t tables = (P + kTable - 1) / kTable;
     void* scratch = nullptr;
-    if (scratch_alloc(&scratch, (parts + 1) * sizeof(double), s) != cudaSuccess) {
+    if (scratch_alloc(&scratch, (tables * kBlocksPerSm * sms + 1) * sizeof(double), s) !=
+        cudaSuccess) {
         cudaGetLastError();
         return FORGE_ERR_CUDA;
     }
     double* part = static_cast<double*>(scratch);
-    for (int32_t j = 0; j < P; ++j) {
+    int64_t parts = 0;
+    st = for_tables(grads, nullptr, n, P, sms, [&](const Table& t, uint32_t blocks) {
         if (dtype == FORGE_F32)
-            forge_square_sum_kernel<<<kBlocks, kThreads, 0, s>>>(
-                static_cast<const float*>(grads[j]), n[j], part + static_cast<int64_t>(j) * kBlocks);
+            forge_square_sum_kernel<float><<<blocks, kThreads, 0, s>>>(t, part + parts);
         else
-            forge_square_sum_kernel<<<kBlocks, kThreads, 0, s>>>(
-                static_cast<const __nv_bfloat16*>(grads[j]), n[j],
-                part + static_cast<int64_t>(j) * kBlocks);
+            forge_square_sum_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(t, part + parts);
+        parts += blocks;
+    });
+    if (st == FORGE_OK) {
+        forge_norm_fold_kernel<<<1, kThreads, 0, s>>>(part, parts, norm);
+        if (cudaGetLastError() != cudaSuccess) st = FORGE_ERR_CUDA;
     }
-    forge_norm_fold_kernel<<<1, kThreads, 0, s>>>(part, parts, norm);
-    cudaError_t e = cudaGetLastError();
-    const cudaError_t fe = scratch_free(scratch, s);
-    if (e == cudaSuccess) e = fe;
-    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    if (scratch_free(scratch, s) != cudaSuccess && st == FORGE_OK) st = FORGE_ERR_CUDA;
+    return st;
 }
 
 extern "C" forge_status forge_clip_grads(const void* const* grads, const int64_t* n, int32_t P,
@@ -165,21 +340,15 @@ extern "C" forge_status forge_clip_grads(const void* const* grads, const int64_t
         return st;
     if (!aligned(norm, 4)) return FORGE_ERR_MISALIGNED;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    for (int32_t j = 0; j < P; ++j) {
-        if (n[j] == 0) continue;
-        auto go = [&](auto* g, auto* o) {
-            forge_clip_kernel<<<kBlocks, kThreads, 0, s>>>(g, o, n[j], norm, max_norm);
-        };
-        auto in = [&](auto* g) {
-            if (out_dtype == FORGE_F32)
-                go(g, static_cast<float*>(out[j]));
-            else
-                go(g, static_cast<__nv_bfloat16*>(out[j]));
-        };
-        if (dtype == FORGE_F32)
-            in(static_cast<const float*>(grads[j]));
+    return for_tables(grads, out, n, P, sms, [&](const Table& t, uint32_t blocks) {
+        if (dtype == FORGE_F32 && out_dtype == FORGE_F32)
+            forge_clip_kernel<float, float><<<blocks, kThreads, 0, s>>>(t, norm, max_norm);
+        else if (dtype == FORGE_F32)
+            forge_clip_kernel<float, __nv_bfloat16><<<blocks, kThreads, 0, s>>>(t, norm, max_norm);
+        else if (out_dtype == FORGE_F32)
+            forge_clip_kernel<__nv_bfloat16, float><<<blocks, kThreads, 0, s>>>(t, norm, max_norm);
         else
-            in(static_cast<const __nv_bfloat16*>(grads[j]));
-    }
-    return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+            forge_clip_kernel<__nv_bfloat16, __nv_bfloat16>
+                <<<blocks, kThreads, 0, s>>>(t, norm, max_norm);
+    });
 }
