@@ -20,7 +20,12 @@ namespace forge {
 namespace logprob {
 
 constexpr int kMaxTop = 32;
-constexpr int kThreads = 256;
+constexpr int kFlight = 4;      // 16-byte vectors in flight per thread
+constexpr int kGroups = 64;     // the row's maxima that bound the top entries from below
+constexpr int kRoom = 128;      // candidates a warp holds before it keeps its best
+constexpr float kFloor = -1000.0f;  // 2^kFloor is 0, and 0 * kFloor is not a NaN
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float load1(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p, int64_t i)
@@ -31,6 +36,125 @@ __device__ __forceinline__ void store1(float* p, int64_t i, float x) { p[i] = x;
 __device__ __forceinline__ void store1(__nv_bfloat16* p, int64_t i, float x)
 {
     p[i] = __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float nan_max(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Two fp32 operations an instruction.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float a, float b)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ void split(Pair p, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// All blocks of the cluster have come here, and see what the others wrote.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared variable of the cluster's block q.
+template <typename X>
+__device__ __forceinline__ const X* remote(const X* p, int q)
+{
+    uint64_t a;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(q));
+    return reinterpret_cast<const X*>(a);
+}
+
+// 16 bytes of a row: four fp32 or eight bf16 logits.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static constexpr uint32_t kNone = 0xFF800000u;  // -inf
+    static __device__ __forceinline__ Pair two(const uint4& u, int i)
+    {
+        return i == 0 ? pair(__uint_as_float(u.x), __uint_as_float(u.y))
+                      : pair(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    static __device__ __forceinline__ float max(const uint4& u)
+    {
+        return nan_max(nan_max(__uint_as_float(u.x), __uint_as_float(u.y)),
+                       nan_max(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static constexpr uint32_t kNone = 0xFF80FF80u;
+    static __device__ __forceinline__ Pair two(const uint4& u, int i)
+    {
+        const uint32_t w = i == 0 ? u.x : (i == 1 ? u.y : (i == 2 ? u.z : u.w));
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t y;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    static __device__ __forceinline__ float max(const uint4& u)
+    {
+        const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+        return nan_max(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+};
+
+// A row (or a block's part of it) as whole 16-byte vectors and the elements
+// before and after them.
+struct Split {
+    int64_t head;  // elements before the first aligned vector
+    int64_t nvec;
+    int64_t tail;  // elements after the last
+};
+template <typename T>
+__device__ __forceinline__ Split split_row(const T* x, int64_t V)
+{
+    constexpr int N = Vec<T>::N;
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T);
+    int64_t head = off == 0 ? 0 : N - off;
+    if (head > V) head = V;
+    const int64_t nvec = (V - head) / N;
+    return {head, nvec, V - head - nvec * N};
 }
 
 // The target of row r: -1 for padding.  A target past the vocabulary is
@@ -48,22 +172,40 @@ __device__ __forceinline__ int64_t target_of(const void* targets, bool wide, int
     return t;
 }
 
-__device__ __forceinline__ float nan_max(float a, float b)
+// A logit and its column as one number: larger for the larger logit, then for
+// the lower column.  NaN is the largest, and -0 equals 0.
+__device__ __forceinline__ uint32_t key_of(float v)
 {
-    return (a != a) ? a : ((b != b) ? b : fmaxf(a, b));
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return v != v ? 0xFFFFFFFFu : b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ uint64_t rank_of(float v, int64_t column)
+{
+    return static_cast<uint64_t>(key_of(v)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(column));
 }
 
-// A value and its column, ordered by value and then by the lower column; a
-// NaN stands above every number.
-struct Ranked {
-    float v;
-    int i;
+// The online softmax of what a thread has seen: the largest logit m (raw), s =
+// sum 2^d and w = sum 2^d d over d = (x - m) scale log2 e, and whether there was
+// a NaN.
+struct Stats {
+    float m, s, w;
+    bool nan;
 };
-__device__ __forceinline__ bool above(const Ranked& a, const Ranked& b)
+__device__ __forceinline__ void join(Stats& a, const Stats& b, float c)
 {
-    const bool an = a.v != a.v, bn = b.v != b.v;
-    if (an || bn) return an && (!bn || a.i < b.i);
-    return a.v > b.v || (a.v == b.v && a.i < b.i);
+    const float m = fmaxf(a.m, b.m);
+    // a part without entries has s = w = 0 and m = -inf
+    const float da = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * c, kFloor);
+    const float db = b.m == -INFINITY ? 0.0f : fmaxf((b.m - m) * c, kFloor);
+    const float fa = exp2_approx(da), fb = exp2_approx(db);
+    a.w = fa * fmaf(da, a.s, a.w) + fb * fmaf(db, b.s, b.w);
+    a.s = fa * a.s + fb * b.s;
+    a.m = m;
+    a.nan = a.nan || b.nan;
 }
 
 struct Args {
@@ -80,87 +222,319 @@ struct Args {
     int* status;
 };
 
-template <typename F>
-__device__ __forceinline__ float block_fold(float x, float* sh, F f)
+// Candidates for the top entries: each warp appends what passes the bound, and
+// keeps its best top_k when its room runs out.
+template <int WARPS>
+struct Tops {
+    uint64_t room[WARPS][kRoom];
+    uint64_t best[kMaxTop];
+    float group[kGroups];
+    int count[WARPS];
+};
+
+// The warp's n candidates cut to the best k, in order; returns their number.
+__device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
 {
-    __syncthreads();
-    sh[threadIdx.x] = x;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) sh[threadIdx.x] = f(sh[threadIdx.x], sh[threadIdx.x + o]);
-        __syncthreads();
+    uint64_t mine[kRoom / 32];
+    int rank[kRoom / 32] = {};
+#pragma unroll
+    for (int i = 0; i < kRoom / 32; ++i) mine[i] = lane + 32 * i < n ? room[lane + 32 * i] : 0;
+    for (int j = 0; j < n; ++j) {
+        const uint64_t other = room[j];
+#pragma unroll
+        for (int i = 0; i < kRoom / 32; ++i) rank[i] += other > mine[i];
     }
-    return sh[0];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRoom / 32; ++i)
+        if (lane + 32 * i < n && rank[i] < k) room[rank[i]] = mine[i];
+    __syncwarp();
+    return n < k ? n : k;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) forge_token_logprob_kernel(const T* logits, const Args p)
+// One row per block of WARPS warps, or per cluster of such blocks where the
+// rows are too few to fill the SMs; each block reads its part of the row once.
+//
+// A thread holds four vectors while the next four are on their way.  Their
+// maximum moves the thread's reference only where it grows, so an element
+// costs one exponential, one addition to s and one to w; the parts are joined
+// by lanes, warps and blocks.  The entropy follows from the same sums: H =
+// ln s - ln 2 w / s, both terms not negative.
+//
+// Top entries: the threads' maxima so far, by groups of lanes, are distinct
+// entries of the row, so the k-th largest of them bounds the k-th largest
+// entry from below; after the first tile and again after four and sixteen it
+// becomes the bound.  Only vectors whose maximum reaches the bound are looked
+// at element by element.
+template <typename T, int WARPS, bool TOP>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
+    forge_token_logprob_kernel(const T* logits, const Args p, int split)
 {
-    __shared__ float sh[kThreads];
-    __shared__ Ranked sr[kThreads];
-    const int64_t r = blockIdx.x;
-    const T* x = logits + r * p.ld;
+    constexpr int N = Vec<T>::N;
+    constexpr int kThreads = 32 * WARPS;
+    constexpr int kGroupLanes = kThreads > kGroups ? kThreads / kGroups : 1;
+    constexpr int kUsed = kThreads / kGroupLanes;  // groups: 32 or 64
+    __shared__ Tops<TOP ? WARPS : 1> tops;
+    __shared__ Stats s_stats[WARPS];
+    __shared__ Stats s_block;
+    __shared__ int s_n;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = blockIdx.x / split;
+    const int part = static_cast<int>(blockIdx.x - r * split);
+    const int k = p.top_k;
     int64_t t = 0;
     if (p.targets) t = target_of(p.targets, p.wide, r, p.V, p.status);
-    if (t < 0) {
-        if (threadIdx.x == 0) {
-            if (p.logprob) p.logprob[r] = 0.0f;
-            if (p.lse) p.lse[r] = 0.0f;
-            if (p.entropy) p.entropy[r] = 0.0f;
-        }
-        for (int k = threadIdx.x; k < p.top_k; k += kThreads) {
-            p.top_index[r * p.top_k + k] = -1;
-            p.top_logprob[r * p.top_k + k] = 0.0f;
+    if (t < 0) {  // padding: the whole cluster leaves
+        if (part == 0) {
+            if (threadIdx.x == 0) {
+                if (p.logprob) p.logprob[r] = 0.0f;
+                if (p.lse) p.lse[r] = 0.0f;
+                if (p.entropy) p.entropy[r] = 0.0f;
+            }
+            if constexpr (TOP)
+                for (int i = threadIdx.x; i < k; i += kThreads) {
+                    p.top_index[r * k + i] = -1;
+                    p.top_logprob[r * k + i] = 0.0f;
+                }
         }
         return;
     }
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < p.V; j += kThreads) m = nan_max(m, load1(x, j));
-    m = block_fold(m, sh, nan_max) * p.scale;
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f, w = 0.0f;
-    for (int64_t j = threadIdx.x; j < p.V; j += kThreads) {
-        const float d = load1(x, j) * p.scale - ref;
-        const float e = expf(d);
-        s += e;
-        if (!(e == 0.0f)) w += e * d;
-    }
-    auto add = [](float a, float b) { return a + b; };
-    s = block_fold(s, sh, add);
-    w = block_fold(w, sh, add);
-    const bool none = m == -INFINITY;
-    const float lse = ref + logf(s);
-    if (threadIdx.x == 0) {
-        if (p.logprob) p.logprob[r] = none ? -INFINITY : load1(x, t) * p.scale - lse;
-        if (p.lse) p.lse[r] = lse;
-        if (p.entropy) p.entropy[r] = none ? 0.0f : logf(s) - w / s;
-    }
-    // the top alternatives, one pass each: the best entry below the last one
-    Ranked last{0.0f, -1};
-    for (int k = 0; k < p.top_k; ++k) {
-        Ranked best{0.0f, -1};
-        for (int64_t j = threadIdx.x; j < p.V; j += kThreads) {
-            const Ranked c{load1(x, j), static_cast<int>(j)};
-            if (k > 0 && !above(last, c)) continue;
-            if (best.i < 0 || above(c, best)) best = c;
+
+    const T* x = logits + r * p.ld;
+    const float c = p.scale * kLog2e;
+    const Split sp = split_row(x, p.V);
+    const int64_t per = (sp.nvec + split - 1) / split;
+    const int64_t v0 = part * per < sp.nvec ? part * per : sp.nvec;
+    const int64_t nv = v0 + per < sp.nvec ? per : sp.nvec - v0;  // this block's vectors
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head) + v0;
+    const int64_t col0 = sp.head + v0 * N;
+
+    Stats st{-INFINITY, 0.0f, 0.0f, false};
+    int count = 0;                 // the warp's candidates
+    uint64_t bound = 0;            // rank that an entry has to reach
+    float bound_v = -INFINITY;     // its value
+
+    auto offer = [&](float v, int64_t column, bool live) {  // one element of each lane
+        const uint64_t rank = rank_of(v, column);
+        const bool pass = live && rank >= bound;
+        const uint32_t all = __ballot_sync(0xffffffffu, pass);
+        if (all == 0) return;
+        if (pass) tops.room[warp][count + __popc(all & ((1u << lane) - 1u))] = rank;
+        count += __popc(all);
+        __syncwarp();
+        if (count > kRoom - 32) {
+            count = keep_best(tops.room[warp], count, k, lane);
+            if (count == k && tops.room[warp][k - 1] > bound) {
+                bound = tops.room[warp][k - 1];
+                bound_v = value_of(static_cast<uint32_t>(bound >> 32));
+            }
         }
-        __syncthreads();
-        sr[threadIdx.x] = best;
-        __syncthreads();
-        for (int o = kThreads / 2; o > 0; o >>= 1) {
-            if (threadIdx.x < o) {
-                const Ranked c = sr[threadIdx.x + o];
-                if (c.i >= 0 && (sr[threadIdx.x].i < 0 || above(c, sr[threadIdx.x])))
-                    sr[threadIdx.x] = c;
+    };
+    auto raise = [&](float m) {  // m moves the reference of the thread's sums
+        if (m > st.m) {
+            if (st.m != -INFINITY) {
+                const float d = fmaxf((st.m - m) * c, kFloor);
+                const float f = exp2_approx(d);
+                st.w = f * fmaf(d, st.s, st.w);
+                st.s *= f;
+            }
+            st.m = m;
+        }
+    };
+
+    // the elements outside whole vectors: the first block's first warp
+    if (part == 0 && warp == 0 && sp.head + sp.tail > 0) {
+        const bool live = lane < 8 ? lane < sp.head : lane - 8 < sp.tail;
+        const int64_t column = lane < 8 ? lane : p.V - sp.tail + (lane - 8);
+        const float v = live ? load1(x, column) : -INFINITY;
+        st.nan = v != v;
+        raise(v);
+        if (v > -INFINITY) {
+            const float d = fmaxf((v - st.m) * c, kFloor);
+            const float e = exp2_approx(d);
+            st.s += e;
+            st.w = fmaf(e, d, st.w);
+        }
+        if constexpr (TOP) offer(v, column, live);
+    }
+
+    const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+    auto fetch = [&](int64_t tile, uint4 (&u)[kFlight]) {
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t v = (tile * kFlight + f) * kThreads + threadIdx.x;
+            u[f] = v < nv ? __ldcs(xv + v) : none;
+        }
+    };
+    const int64_t tiles = (nv + kFlight * kThreads - 1) / (kFlight * kThreads);
+    uint4 next[kFlight];
+    if (tiles > 0) fetch(0, next);
+    for (int64_t tile = 0; tile < tiles; ++tile) {
+        uint4 u[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) u[f] = next[f];
+        if (tile + 1 < tiles) fetch(tile + 1, next);
+        float vm[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) vm[f] = Vec<T>::max(u[f]);
+        const float tm = nan_max(nan_max(vm[0], vm[1]), nan_max(vm[2], vm[3]));
+        st.nan = st.nan || tm != tm;
+        raise(tm);
+        const float mr = st.m == -INFINITY ? 0.0f : st.m;
+        const Pair mm = pair(-mr, -mr), cc = pair(c, c);
+        Pair s2 = pair(0.0f, 0.0f), w2 = pair(0.0f, 0.0f);
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                float d0, d1;
+                ::forge::logprob::split(mul2(add2(Vec<T>::two(u[f], i), mm), cc), d0, d1);
+                d0 = fmaxf(d0, kFloor);
+                d1 = fmaxf(d1, kFloor);
+                const Pair e = pair(exp2_approx(d0), exp2_approx(d1));
+                s2 = add2(s2, e);
+                w2 = fma2(e, pair(d0, d1), w2);
+            }
+        float a, b;
+        ::forge::logprob::split(s2, a, b);
+        st.s += a + b;
+        ::forge::logprob::split(w2, a, b);
+        st.w += a + b;
+
+        if constexpr (TOP) {
+            if (tile == 0 || tile == 3 || tile == 15) {
+                float g = st.m;
+#pragma unroll
+                for (int o = 1; o < kGroupLanes; o <<= 1)
+                    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+                if (tile != 0) __syncthreads();  // the last reading of the groups
+                if (lane % kGroupLanes == 0) tops.group[threadIdx.x / kGroupLanes] = g;
+                __syncthreads();
+                int above[2] = {};
+                const float g0 = tops.group[lane], g1 = tops.group[(lane + 32) % kUsed];
+                for (int j = 0; j < kUsed; ++j) {
+                    const float o = tops.group[j];
+                    above[0] += o > g0 || (o == g0 && j < lane);
+                    above[1] += o > g1 || (o == g1 && j < lane + 32);
+                }
+                const uint32_t at0 = __ballot_sync(0xffffffffu, above[0] == k - 1);
+                const uint32_t at1 = __ballot_sync(0xffffffffu, kUsed > 32 && above[1] == k - 1);
+                const float kth = at0 ? __shfl_sync(0xffffffffu, g0, __ffs(at0) - 1)
+                                      : __shfl_sync(0xffffffffu, g1, __ffs(at1) - 1);
+                const uint64_t floor = static_cast<uint64_t>(key_of(kth)) << 32;
+                if (floor > bound) {
+                    bound = floor;
+                    bound_v = kth;
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (__ballot_sync(0xffffffffu, !(vm[f] < bound_v)) == 0) continue;
+                const int64_t v = (tile * kFlight + f) * kThreads + threadIdx.x;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    float a0, a1;
+                    ::forge::logprob::split(Vec<T>::two(u[f], i), a0, a1);
+                    offer(a0, col0 + v * N + 2 * i, v < nv);
+                    offer(a1, col0 + v * N + 2 * i + 1, v < nv);
+                }
+            }
+        }
+    }
+
+    // lanes, then warps
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stats b;
+        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        b.w = __shfl_xor_sync(0xffffffffu, st.w, o);
+        b.nan = __shfl_xor_sync(0xffffffffu, st.nan ? 1 : 0, o) != 0;
+        join(st, b, c);
+    }
+    if (lane == 0) {
+        s_stats[warp] = st;
+        if constexpr (TOP) tops.count[warp] = count;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        st = s_stats[0];
+        for (int w = 1; w < WARPS; ++w) join(st, s_stats[w], c);
+        s_block = st;
+    }
+    if constexpr (TOP) {
+        // the block's best: an entry's place is the number of better ones
+        int n = 0;
+        for (int w = 0; w < WARPS; ++w) n += tops.count[w];
+        for (int i = threadIdx.x; i < WARPS * kRoom; i += kThreads) {
+            const int w = i / kRoom, e = i % kRoom;
+            if (e >= tops.count[w]) continue;
+            const uint64_t mine = tops.room[w][e];
+            int rank = 0;
+            for (int ww = 0; ww < WARPS; ++ww)
+                for (int j = 0; j < tops.count[ww]; ++j) rank += tops.room[ww][j] > mine;
+            if (rank < k) tops.best[rank] = mine;
+        }
+        if (threadIdx.x == 0) s_n = n < k ? n : k;
+    }
+    __syncthreads();
+
+    // blocks of the row: the first one joins what the others left in shared memory
+    if (split > 1) {
+        cluster_barrier();
+        if (part == 0) {
+            if (threadIdx.x == 0)
+                for (int q = 1; q < split; ++q) {
+                    const Stats* o = remote(&s_block, q);
+                    const Stats b{o->m, o->s, o->w, o->nan};
+                    join(s_block, b, c);
+                }
+            if constexpr (TOP) {
+                // gather every block's best into this block's room, then rank them again
+                uint64_t* all = &tops.room[0][0];  // split * k <= 8 * 32 <= WARPS * kRoom
+                int n = 0;
+                for (int q = 0; q < split; ++q) {
+                    const int nq = *remote(&s_n, q);
+                    const uint64_t* best = remote(&tops.best[0], q);
+                    for (int i = threadIdx.x; i < nq; i += kThreads) all[n + i] = best[i];
+                    n += nq;
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i < n; i += kThreads) {
+                    int rank = 0;
+                    for (int j = 0; j < n; ++j) rank += all[j] > all[i];
+                    if (rank < k) tops.best[rank] = all[i];
+                }
             }
             __syncthreads();
         }
-        last = sr[0];
-        if (threadIdx.x == 0) {
-            p.top_index[r * p.top_k + k] = last.i;
-            p.top_logprob[r * p.top_k + k] = none ? -INFINITY : last.v * p.scale - lse;
-        }
+        cluster_barrier();  // no block leaves while its shared memory is read
+        if (part != 0) return;
     }
+
+    const Stats all = s_block;
+    const bool bad = all.nan || all.m == INFINITY;
+    const bool empty = !bad && all.m == -INFINITY;
+    // relative to the largest logit; the sum of both in 64 bits rounds once
+    const float ln_s = logf(all.s);
+    const double lse = static_cast<double>(p.scale) * all.m + ln_s;
+    auto logprob_of = [&](float v) {
+        if (bad) return NAN;
+        if (empty || v == -INFINITY) return -INFINITY;
+        return static_cast<float>(static_cast<double>(p.scale) * (static_cast<double>(v) - all.m) - ln_s);
+    };
+    if (threadIdx.x == 0) {
+        if (p.logprob) p.logprob[r] = logprob_of(load1(x, t));
+        if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : static_cast<float>(lse));
+        if (p.entropy) p.entropy[r] = bad ? NAN : (empty ? 0.0f : ln_s - kLn2 * all.w / all.s);
+    }
+    if constexpr (TOP)
+        for (int i = threadIdx.x; i < k; i += kThreads) {
+            const uint64_t e = tops.best[i];
+            p.top_index[r * k + i] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
+            p.top_logprob[r * k + i] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)));
+        }
 }
 
 struct GradArgs {
@@ -175,11 +549,43 @@ struct GradArgs {
     int* status;
 };
 
-template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads)
-    forge_token_logprob_grad_kernel(const T* logits, O* dlogits, const GradArgs p)
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[N])
 {
-    const int64_t r = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+}
+template <int N>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
+{
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (N == 8)
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+}
+
+// dx_j = s (a (1[j = t] - p_j) - b p_j (ln p_j + H)) = [j = t] s a - p_j (A + B d_j) with
+// d = log2 p, A = s (a + b H), B = s b ln 2: one exponential an element, no
+// reduction.  A block takes 4 vectors a thread of one row; rows whose vectors
+// do not meet the output's alignment go element by element.
+constexpr int kGradThreads = 256;
+template <typename T>
+constexpr int kGradSpan = kGradThreads * kFlight * Vec<T>::N;
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kGradThreads)
+    forge_token_logprob_grad_kernel(const T* logits, O* dlogits, const GradArgs p, uint32_t spans)
+{
+    constexpr int N = Vec<T>::N;
+    const int64_t r = blockIdx.x / spans;
+    const int64_t span = blockIdx.x - r * spans;
     const T* x = logits + r * p.ld;
     O* dx = dlogits + r * p.ld_out;
     const int64_t t = target_of(p.targets, p.wide, r, p.V, p.status);
@@ -188,17 +594,122 @@ __global__ void __launch_bounds__(kThreads)
     const float a = p.grad_logprob[r];
     const float b = p.grad_entropy ? p.grad_entropy[r] : 0.0f;
     const float h = p.grad_entropy ? p.entropy[r] : 0.0f;
-    for (int64_t j = threadIdx.x; j < p.V; j += kThreads) {
-        float g = 0.0f;
-        if (!dead) {
-            const float d = load1(x, j) * p.scale - lse;
-            const float e = expf(d);
-            g = -e * (a + b * ((e == 0.0f ? 0.0f : d) + h));
-            if (j == t) g += a;
-            g *= p.scale;
-        }
-        store1(dx, j, g);
+    // a NaN among the logits has come as a NaN lse
+    const float A = lse != lse ? lse : p.scale * fmaf(b, h, a), B = p.scale * b * kLn2;
+    const float at_t = p.scale * a;
+    auto one = [&](float v, int64_t j) {
+        const float d = fmaxf(fmaf(v, p.scale, -lse) * kLog2e, kFloor);
+        const float g = -exp2_approx(d) * fmaf(B, d, A);
+        return j == t ? g + at_t : g;
+    };
+
+    const Split sp = split_row(x, p.V);
+    constexpr uintptr_t oa = N * sizeof(O) < 16 ? 8 : 16;
+    const bool vec = (reinterpret_cast<uintptr_t>(dx + sp.head) & (oa - 1)) == 0;
+    if (!vec) {
+        const int64_t end = (span + 1) * kGradSpan<T> < p.V ? (span + 1) * kGradSpan<T> : p.V;
+#pragma unroll 8
+        for (int64_t j = span * kGradSpan<T> + threadIdx.x; j < end; j += kGradThreads)
+            store1(dx, j, dead ? 0.0f : one(load1(x, j), j));
+        return;
     }
+    if (span == 0 && threadIdx.x < 16) {
+        const int i = threadIdx.x & 7;
+        if (i < (threadIdx.x < 8 ? sp.head : sp.tail)) {
+            const int64_t j = threadIdx.x < 8 ? i : p.V - sp.tail + i;
+            store1(dx, j, dead ? 0.0f : one(load1(x, j), j));
+        }
+    }
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+    const int64_t v0 = span * kFlight * kGradThreads + threadIdx.x;
+    uint4 u[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+        u[f] = !dead && v0 + f * kGradThreads < sp.nvec ? __ldcs(xv + v0 + f * kGradThreads)
+                                                       : make_uint4(0, 0, 0, 0);
+    const Pair ss = pair(p.scale, p.scale), ll = pair(-lse, -lse), ee = pair(kLog2e, kLog2e);
+    const Pair AA = pair(-A, -A), BB = pair(-B, -B);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+        const int64_t v = v0 + f * kGradThreads;
+        if (v >= sp.nvec) continue;
+        float g[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            float d0, d1;
+            ::forge::logprob::split(mul2(fma2(Vec<T>::two(u[f], i), ss, ll), ee), d0, d1);
+            d0 = fmaxf(d0, kFloor);
+            d1 = fmaxf(d1, kFloor);
+            const Pair e = pair(exp2_approx(d0), exp2_approx(d1));
+            ::forge::logprob::split(mul2(e, fma2(BB, pair(d0, d1), AA)), g[2 * i], g[2 * i + 1]);
+        }
+        const int64_t j0 = sp.head + v * N;
+        if (dead) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = 0.0f;
+        } else if (t >= j0 && t < j0 + N) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (j0 + i == t) g[i] += at_t;
+        }
+        store_vec<N>(dx + j0, g);
+    }
+}
+
+template <typename T, int WARPS, bool TOP>
+cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.R * split));
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, forge_token_logprob_kernel<T, WARPS, TOP>, x, p, split);
+}
+
+// Blocks of one, two or eight warps by the row's length, so that a thread has
+// a few vectors at least; long rows are split over clusters of up to eight
+// blocks while the rows alone leave SMs without work.
+template <typename T>
+cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
+{
+    const int64_t nvec = p.V / Vec<T>::N;
+    if (nvec <= 256)
+        return p.top_k > 0 ? launch_forward<T, 1, true>(x, p, 1, s)
+                           : launch_forward<T, 1, false>(x, p, 1, s);
+    if (nvec <= 1024)
+        return p.top_k > 0 ? launch_forward<T, 2, true>(x, p, 1, s)
+                           : launch_forward<T, 2, false>(x, p, 1, s);
+    int split = 1;
+    while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
+    return p.top_k > 0 ? launch_forward<T, 8, true>(x, p, split, s)
+                       : launch_forward<T, 8, false>(x, p, split, s);
+}
+
+template <typename T, typename O>
+cudaError_t backward(const T* x, O* dx, const GradArgs& p, cudaStream_t s)
+{
+    const int64_t spans = (p.V + kGradSpan<T> - 1) / kGradSpan<T>;
+    const int64_t rows_at_once = INT32_MAX / spans;
+    for (int64_t r = 0; r < p.R; r += rows_at_once) {
+        GradArgs q = p;
+        q.R = p.R - r < rows_at_once ? p.R - r : rows_at_once;
+        q.targets = static_cast<const uint8_t*>(p.targets) + r * (p.wide ? 8 : 4);
+        q.lse += r;
+        q.grad_logprob += r;
+        if (q.grad_entropy) {
+            q.entropy += r;
+            q.grad_entropy += r;
+        }
+        forge_token_logprob_grad_kernel<<<static_cast<unsigned>(q.R * spans), kGradThreads, 0, s>>>(
+            x + r * p.ld, dx + r * p.ld_out, q, static_cast<uint32_t>(spans));
+    }
+    return cudaGetLastError();
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -246,13 +757,11 @@ extern "C" forge_status forge_token_logprob(const void* logits, forge_dtype dtyp
     const Args p{R,   V,       ld,    targets,   id_dtype == FORGE_I64, scale, logprob,
                  lse, entropy, top_k, top_index, top_logprob,           device_status_word()};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = static_cast<int>(R);
-    if (dtype == FORGE_F32)
-        forge_token_logprob_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float*>(logits), p);
-    else
-        forge_token_logprob_kernel<<<grid, kThreads, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(logits), p);
-    return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    const cudaError_t e =
+        dtype == FORGE_F32 ? forward(static_cast<const float*>(logits), p, sms, s)
+                           : forward(static_cast<const __nv_bfloat16*>(logits), p, sms, s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }
 
 extern "C" forge_status forge_token_logprob_grad(
@@ -282,19 +791,11 @@ extern "C" forge_status forge_token_logprob_grad(
     const GradArgs p{R,   V,            ld,      ld_out,       targets, id_dtype == FORGE_I64, scale,
                      lse, grad_logprob, entropy, grad_entropy, device_status_word()};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = static_cast<int>(R);
-    auto go = [&](auto* x, auto* dx) {
-        forge_token_logprob_grad_kernel<<<grid, kThreads, 0, s>>>(x, dx, p);
-    };
     auto in = [&](auto* x) {
-        if (out_dtype == FORGE_F32)
-            go(x, static_cast<float*>(dlogits));
-        else
-            go(x, static_cast<__nv_bfloat16*>(dlogits));
+        return out_dtype == FORGE_F32 ? backward(x, static_cast<float*>(dlogits), p, s)
+                                      : backward(x, static_cast<__nv_bfloat16*>(dlogits), p, s);
     };
-    if (dtype == FORGE_F32)
-        in(static_cast<const float*>(logits));
-    else
-        in(static_cast<const __nv_bfloat16*>(logits));
-    return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    const cudaError_t e = dtype == FORGE_F32 ? in(static_cast<const float*>(logits))
+                                             : in(static_cast<const __nv_bfloat16*>(logits));
+    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }
