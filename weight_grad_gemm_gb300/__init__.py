@@ -130,9 +130,10 @@ def _ptr(t):
 
 
 def _stream(stream, like):
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream(like.device)
+        import torch
+        # the current stream's handle without a Stream object around it: 0.2 instead of 2 us a call
+        return torch._C._cuda_getCurrentRawStream(like.device.index)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -460,12 +461,10 @@ def forge_embedding_adamw(dY, ids, W, m, v, *, lr, beta1, beta2, eps, wd, step, 
 def _tensor_list(ts, what):
     """Pointers, element counts and the common dtype of a list of tensors."""
     n = len(ts)
-    dtype = ts[0].dtype if n else None
-    for t in ts:
-        if t.dtype != dtype:
-            raise TypeError(f"{what} must share one dtype")
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous CUDA tensors")
+    if len({t.dtype for t in ts}) > 1:
+        raise TypeError(f"{what} must share one dtype")
+    if not all([t.is_cuda and t.is_contiguous() for t in ts]):
+        raise ValueError(f"{what} must be contiguous CUDA tensors")
     ptrs = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in ts])
     sizes = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in ts])
     return ptrs, sizes, FORGE_F32 if n == 0 else _float_code(ts[0])
@@ -486,9 +485,9 @@ def forge_clip_grads(grads, norm, out=None, *, max_norm, stream=None):
     ptrs, sizes, code = _tensor_list(grads, "grads")
     optrs, ocode = ptrs, code
     if out is not None:
-        if [t.numel() for t in out] != [t.numel() for t in grads]:
+        optrs, osizes, ocode = _tensor_list(out, "out")
+        if len(out) != len(grads) or bytes(osizes) != bytes(sizes):
             raise ValueError("out must have one tensor of the same size for each of grads")
-        optrs, _, ocode = _tensor_list(out, "out")
     s = lib().forge_clip_grads(ptrs, sizes, len(grads), code, _vector(norm, 1, "norm"), max_norm,
                                optrs, ocode, _stream(stream, norm))
     _check(s, "forge_clip_grads")

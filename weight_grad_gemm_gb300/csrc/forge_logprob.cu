@@ -21,8 +21,10 @@ namespace logprob {
 
 constexpr int kMaxTop = 32;
 constexpr int kFlight = 4;      // 16-byte vectors in flight per thread
-constexpr int kGroups = 64;     // the row's maxima that bound the top entries from below
-constexpr int kRoom = 128;      // candidates a warp holds before it keeps its best
+constexpr int kWarps = 8;       // of a block
+constexpr int kGroups = 64;     // most maxima that bound the top entries from below
+constexpr int kList = 128;      // vectors a warp notes before it looks into them
+constexpr int kRoom = 128;      // entries a warp holds before it keeps its best
 constexpr float kFloor = -1000.0f;  // 2^kFloor is 0, and 0 * kFloor is not a NaN
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -222,17 +224,14 @@ struct Args {
     int* status;
 };
 
-// Candidates for the top entries: each warp appends what passes the bound, and
-// keeps its best top_k when its room runs out.
-template <int WARPS>
+// What a warp holds of the top entries' candidates: vectors whose maximum
+// reached the bound when they passed, and entries taken out of such vectors.
 struct Tops {
-    uint64_t room[WARPS][kRoom];
-    uint64_t best[kMaxTop];
-    float group[kGroups];
-    int count[WARPS];
+    uint64_t room[kRoom];
+    int32_t list[kList];
 };
 
-// The warp's n candidates cut to the best k, in order; returns their number.
+// The warp's n entries cut to the best k, in order; returns their number.
 __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
 {
     uint64_t mine[kRoom / 32];
@@ -252,8 +251,49 @@ __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
     return n < k ? n : k;
 }
 
-// One row per block of WARPS warps, or per cluster of such blocks where the
-// rows are too few to fill the SMs; each block reads its part of the row once.
+// Adds one entry of each lane to the warp's room where it reaches the bound.
+__device__ __forceinline__ void offer(Tops& w, int& held, uint64_t& bound, float v, int64_t column,
+                                      bool live, int k, int lane)
+{
+    const uint64_t rank = rank_of(v, column);
+    const bool pass = live && rank >= bound;
+    const uint32_t all = __ballot_sync(0xffffffffu, pass);
+    if (all == 0) return;
+    if (pass) w.room[held + __popc(all & ((1u << lane) - 1u))] = rank;
+    held += __popc(all);
+    __syncwarp();
+    if (held > kRoom - 32) {
+        held = keep_best(w.room, held, k, lane);
+        if (held == k && w.room[k - 1] > bound) bound = w.room[k - 1];
+    }
+}
+
+// Reads the noted vectors again (they are in L2 as a rule) and offers their
+// entries, 32 vectors at a time.
+template <typename T>
+__device__ __noinline__ void look_into(Tops& w, int noted, int& held, uint64_t& bound,
+                                       const uint4* xv, int64_t col0, int k, int lane)
+{
+    constexpr int N = Vec<T>::N;
+    __syncwarp();
+    for (int i0 = 0; i0 < noted; i0 += 32) {
+        const bool live = i0 + lane < noted;
+        const int64_t v = live ? w.list[i0 + lane] : 0;
+        const uint4 u = live ? __ldg(xv + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            float a, b;
+            split(Vec<T>::two(u, i), a, b);
+            offer(w, held, bound, a, col0 + v * N + 2 * i, live, k, lane);
+            offer(w, held, bound, b, col0 + v * N + 2 * i + 1, live, k, lane);
+        }
+    }
+    __syncwarp();
+}
+
+// A row is the work of WARPS warps of a block (eight, or fewer where rows are
+// short and a block takes several), or of a cluster of whole blocks where the
+// rows are too few to fill the SMs.  Each element is read from memory once.
 //
 // A thread holds four vectors while the next four are on their way.  Their
 // maximum moves the thread's reference only where it grows, so an element
@@ -263,37 +303,57 @@ __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
 //
 // Top entries: the threads' maxima so far, by groups of lanes, are distinct
 // entries of the row, so the k-th largest of them bounds the k-th largest
-// entry from below; after the first tile and again after four and sixteen it
-// becomes the bound.  Only vectors whose maximum reaches the bound are looked
-// at element by element.
+// entry from below.  It becomes the bound after the first and the fourth tile
+// and after the last.  In the loop a vector costs one comparison of its
+// maximum with the bound; those that reach it are noted by number only, and
+// looked into after the last bound, which leaves a few entries more than k.
 template <typename T, int WARPS, bool TOP>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
+__global__ void __launch_bounds__(32 * kWarps, 4)
     forge_token_logprob_kernel(const T* logits, const Args p, int split)
 {
     constexpr int N = Vec<T>::N;
-    constexpr int kThreads = 32 * WARPS;
+    constexpr int kThreads = 32 * WARPS;       // of a row
+    constexpr int kRows = kWarps / WARPS;      // of a block
     constexpr int kGroupLanes = kThreads > kGroups ? kThreads / kGroups : 1;
-    constexpr int kUsed = kThreads / kGroupLanes;  // groups: 32 or 64
-    __shared__ Tops<TOP ? WARPS : 1> tops;
-    __shared__ Stats s_stats[WARPS];
-    __shared__ Stats s_block;
-    __shared__ int s_n;
+    constexpr int kUsed = kThreads / kGroupLanes;  // groups of a row: 32 or 64
+    __shared__ Tops s_tops[TOP ? kWarps : 1];
+    __shared__ float s_group[kRows][kUsed];
+    __shared__ float s_kth[kRows];
+    __shared__ int s_held[kWarps];
+    __shared__ Stats s_stats[kWarps];
+    __shared__ Stats s_row[kRows];
+    __shared__ uint64_t s_best[TOP ? kRows : 1][kMaxTop];
+    __shared__ int s_n[kRows];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = blockIdx.x / split;
-    const int part = static_cast<int>(blockIdx.x - r * split);
+    const int mine = warp / WARPS;             // the row's place in the block
+    const int tid = threadIdx.x - mine * kThreads;
+    const int rwarp = warp - mine * WARPS;
+    auto sync = [&] {
+        if constexpr (WARPS == 1)
+            __syncwarp();
+        else if constexpr (WARPS == kWarps)
+            __syncthreads();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "n"(kThreads) : "memory");
+    };
+
+    const int64_t block = blockIdx.x / split;
+    const int part = static_cast<int>(blockIdx.x - block * split);
+    const int64_t r = block * kRows + mine;
+    if (r >= p.R) return;
     const int k = p.top_k;
     int64_t t = 0;
     if (p.targets) t = target_of(p.targets, p.wide, r, p.V, p.status);
-    if (t < 0) {  // padding: the whole cluster leaves
+    if (t < 0) {  // padding: all the row's warps leave
         if (part == 0) {
-            if (threadIdx.x == 0) {
+            if (tid == 0) {
                 if (p.logprob) p.logprob[r] = 0.0f;
                 if (p.lse) p.lse[r] = 0.0f;
                 if (p.entropy) p.entropy[r] = 0.0f;
             }
             if constexpr (TOP)
-                for (int i = threadIdx.x; i < k; i += kThreads) {
+                for (int i = tid; i < k; i += kThreads) {
                     p.top_index[r * k + i] = -1;
                     p.top_logprob[r * k + i] = 0.0f;
                 }
@@ -306,31 +366,16 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
     const Split sp = split_row(x, p.V);
     const int64_t per = (sp.nvec + split - 1) / split;
     const int64_t v0 = part * per < sp.nvec ? part * per : sp.nvec;
-    const int64_t nv = v0 + per < sp.nvec ? per : sp.nvec - v0;  // this block's vectors
+    const int32_t nv = static_cast<int32_t>(v0 + per < sp.nvec ? per : sp.nvec - v0);
     const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head) + v0;
     const int64_t col0 = sp.head + v0 * N;
 
     Stats st{-INFINITY, 0.0f, 0.0f, false};
-    int count = 0;                 // the warp's candidates
+    Tops& tops = s_tops[TOP ? warp : 0];
+    int held = 0, noted = 0;       // the warp's entries and vectors
     uint64_t bound = 0;            // rank that an entry has to reach
     float bound_v = -INFINITY;     // its value
 
-    auto offer = [&](float v, int64_t column, bool live) {  // one element of each lane
-        const uint64_t rank = rank_of(v, column);
-        const bool pass = live && rank >= bound;
-        const uint32_t all = __ballot_sync(0xffffffffu, pass);
-        if (all == 0) return;
-        if (pass) tops.room[warp][count + __popc(all & ((1u << lane) - 1u))] = rank;
-        count += __popc(all);
-        __syncwarp();
-        if (count > kRoom - 32) {
-            count = keep_best(tops.room[warp], count, k, lane);
-            if (count == k && tops.room[warp][k - 1] > bound) {
-                bound = tops.room[warp][k - 1];
-                bound_v = value_of(static_cast<uint32_t>(bound >> 32));
-            }
-        }
-    };
     auto raise = [&](float m) {  // m moves the reference of the thread's sums
         if (m > st.m) {
             if (st.m != -INFINITY) {
@@ -342,9 +387,37 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
             st.m = m;
         }
     };
+    // The k-th largest of the groups' maxima as the bound: a thread counts its
+    // share of the groups above its own.
+    auto tighten = [&] {
+        float g = st.m;
+#pragma unroll
+        for (int o = 1; o < kGroupLanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        const int group = tid / kGroupLanes, share = tid % kGroupLanes;
+        sync();  // the last reading of the groups
+        if (share == 0) s_group[mine][group] = g;
+        sync();
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < kUsed / kGroupLanes; ++i) {
+            const int j = i * kGroupLanes + share;
+            const float o = s_group[mine][j];
+            above += o > g || (o == g && j < group);
+        }
+#pragma unroll
+        for (int o = 1; o < kGroupLanes; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+        if (above == k - 1) s_kth[mine] = g;
+        sync();
+        const float kth = s_kth[mine];
+        const uint64_t floor = static_cast<uint64_t>(key_of(kth)) << 32;
+        if (floor > bound) {
+            bound = floor;
+            bound_v = kth;
+        }
+    };
 
-    // the elements outside whole vectors: the first block's first warp
-    if (part == 0 && warp == 0 && sp.head + sp.tail > 0) {
+    // the elements outside whole vectors: the first warp of the row
+    if (part == 0 && rwarp == 0 && sp.head + sp.tail > 0) {
         const bool live = lane < 8 ? lane < sp.head : lane - 8 < sp.tail;
         const int64_t column = lane < 8 ? lane : p.V - sp.tail + (lane - 8);
         const float v = live ? load1(x, column) : -INFINITY;
@@ -356,21 +429,21 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
             st.s += e;
             st.w = fmaf(e, d, st.w);
         }
-        if constexpr (TOP) offer(v, column, live);
+        if constexpr (TOP) offer(tops, held, bound, v, column, live, k, lane);
     }
 
     const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
-    auto fetch = [&](int64_t tile, uint4 (&u)[kFlight]) {
+    auto fetch = [&](int32_t tile, uint4 (&u)[kFlight]) {
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            const int64_t v = (tile * kFlight + f) * kThreads + threadIdx.x;
+            const int32_t v = (tile * kFlight + f) * kThreads + tid;
             u[f] = v < nv ? __ldcs(xv + v) : none;
         }
     };
-    const int64_t tiles = (nv + kFlight * kThreads - 1) / (kFlight * kThreads);
+    const int32_t tiles = (nv + kFlight * kThreads - 1) / (kFlight * kThreads);
     uint4 next[kFlight];
     if (tiles > 0) fetch(0, next);
-    for (int64_t tile = 0; tile < tiles; ++tile) {
+    for (int32_t tile = 0; tile < tiles; ++tile) {
         uint4 u[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) u[f] = next[f];
@@ -403,44 +476,27 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
         st.w += a + b;
 
         if constexpr (TOP) {
-            if (tile == 0 || tile == 3 || tile == 15) {
-                float g = st.m;
+            if (tile == 0 || tile == 3) tighten();
+            if (__any_sync(0xffffffffu, !(tm < bound_v))) {
 #pragma unroll
-                for (int o = 1; o < kGroupLanes; o <<= 1)
-                    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-                if (tile != 0) __syncthreads();  // the last reading of the groups
-                if (lane % kGroupLanes == 0) tops.group[threadIdx.x / kGroupLanes] = g;
-                __syncthreads();
-                int above[2] = {};
-                const float g0 = tops.group[lane], g1 = tops.group[(lane + 32) % kUsed];
-                for (int j = 0; j < kUsed; ++j) {
-                    const float o = tops.group[j];
-                    above[0] += o > g0 || (o == g0 && j < lane);
-                    above[1] += o > g1 || (o == g1 && j < lane + 32);
-                }
-                const uint32_t at0 = __ballot_sync(0xffffffffu, above[0] == k - 1);
-                const uint32_t at1 = __ballot_sync(0xffffffffu, kUsed > 32 && above[1] == k - 1);
-                const float kth = at0 ? __shfl_sync(0xffffffffu, g0, __ffs(at0) - 1)
-                                      : __shfl_sync(0xffffffffu, g1, __ffs(at1) - 1);
-                const uint64_t floor = static_cast<uint64_t>(key_of(kth)) << 32;
-                if (floor > bound) {
-                    bound = floor;
-                    bound_v = kth;
-                }
-            }
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                if (__ballot_sync(0xffffffffu, !(vm[f] < bound_v)) == 0) continue;
-                const int64_t v = (tile * kFlight + f) * kThreads + threadIdx.x;
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    float a0, a1;
-                    ::forge::logprob::split(Vec<T>::two(u[f], i), a0, a1);
-                    offer(a0, col0 + v * N + 2 * i, v < nv);
-                    offer(a1, col0 + v * N + 2 * i + 1, v < nv);
+                for (int f = 0; f < kFlight; ++f) {
+                    const int32_t v = (tile * kFlight + f) * kThreads + tid;
+                    const bool pass = !(vm[f] < bound_v) && v < nv;
+                    const uint32_t all = __ballot_sync(0xffffffffu, pass);
+                    if (pass) tops.list[noted + __popc(all & ((1u << lane) - 1u))] = v;
+                    noted += __popc(all);
+                    if (noted > kList - 32) {
+                        look_into<T>(tops, noted, held, bound, xv, col0, k, lane);
+                        noted = 0;
+                        bound_v = value_of(static_cast<uint32_t>(bound >> 32));
+                    }
                 }
             }
         }
+    }
+    if constexpr (TOP) {
+        if (tiles > 1) tighten();
+        look_into<T>(tops, noted, held, bound, xv, col0, k, lane);
     }
 
     // lanes, then warps
@@ -455,65 +511,68 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
     }
     if (lane == 0) {
         s_stats[warp] = st;
-        if constexpr (TOP) tops.count[warp] = count;
+        s_held[warp] = held;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        st = s_stats[0];
-        for (int w = 1; w < WARPS; ++w) join(st, s_stats[w], c);
-        s_block = st;
+    sync();
+    if (tid == 0) {
+        st = s_stats[warp];
+        for (int w = 1; w < WARPS; ++w) join(st, s_stats[warp + w], c);
+        s_row[mine] = st;
     }
     if constexpr (TOP) {
-        // the block's best: an entry's place is the number of better ones
+        // the best of the row's warps: an entry's place is the number of better ones
         int n = 0;
-        for (int w = 0; w < WARPS; ++w) n += tops.count[w];
-        for (int i = threadIdx.x; i < WARPS * kRoom; i += kThreads) {
-            const int w = i / kRoom, e = i % kRoom;
-            if (e >= tops.count[w]) continue;
-            const uint64_t mine = tops.room[w][e];
+        for (int w = 0; w < WARPS; ++w) n += s_held[mine * WARPS + w];
+        for (int e = lane; e < held; e += 32) {
+            const uint64_t own = tops.room[e];
             int rank = 0;
-            for (int ww = 0; ww < WARPS; ++ww)
-                for (int j = 0; j < tops.count[ww]; ++j) rank += tops.room[ww][j] > mine;
-            if (rank < k) tops.best[rank] = mine;
+            for (int w = 0; w < WARPS; ++w) {
+                const uint64_t* room = s_tops[mine * WARPS + w].room;
+                const int nw = s_held[mine * WARPS + w];
+                for (int j = 0; j < nw; ++j) rank += room[j] > own;
+            }
+            if (rank < k) s_best[mine][rank] = own;
         }
-        if (threadIdx.x == 0) s_n = n < k ? n : k;
+        if (tid == 0) s_n[mine] = n < k ? n : k;
     }
-    __syncthreads();
+    sync();
 
     // blocks of the row: the first one joins what the others left in shared memory
-    if (split > 1) {
-        cluster_barrier();
-        if (part == 0) {
-            if (threadIdx.x == 0)
-                for (int q = 1; q < split; ++q) {
-                    const Stats* o = remote(&s_block, q);
-                    const Stats b{o->m, o->s, o->w, o->nan};
-                    join(s_block, b, c);
-                }
-            if constexpr (TOP) {
-                // gather every block's best into this block's room, then rank them again
-                uint64_t* all = &tops.room[0][0];  // split * k <= 8 * 32 <= WARPS * kRoom
-                int n = 0;
-                for (int q = 0; q < split; ++q) {
-                    const int nq = *remote(&s_n, q);
-                    const uint64_t* best = remote(&tops.best[0], q);
-                    for (int i = threadIdx.x; i < nq; i += kThreads) all[n + i] = best[i];
-                    n += nq;
+    if constexpr (WARPS == kWarps)
+        if (split > 1) {
+            cluster_barrier();
+            if (part == 0) {
+                if (threadIdx.x == 0)
+                    for (int q = 1; q < split; ++q) {
+                        const Stats* o = remote(&s_row[0], q);
+                        const Stats b{o->m, o->s, o->w, o->nan};
+                        join(s_row[0], b, c);
+                    }
+                if constexpr (TOP) {
+                    // every block's best, 32 to a warp's room, ranked again
+                    static_assert(kWarps * kMaxTop <= kWarps * kRoom);
+                    if (warp < split) {
+                        const int nq = *remote(&s_n[0], warp);
+                        const uint64_t* best = remote(&s_best[0][0], warp);
+                        if (lane < nq) tops.room[lane] = best[lane];
+                        if (lane == 0) s_held[warp] = nq;
+                    }
+                    __syncthreads();
+                    if (warp < split && lane < s_held[warp]) {
+                        const uint64_t own = tops.room[lane];
+                        int rank = 0;
+                        for (int w = 0; w < split; ++w)
+                            for (int j = 0; j < s_held[w]; ++j) rank += s_tops[w].room[j] > own;
+                        if (rank < k) s_best[0][rank] = own;
+                    }
                 }
                 __syncthreads();
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    int rank = 0;
-                    for (int j = 0; j < n; ++j) rank += all[j] > all[i];
-                    if (rank < k) tops.best[rank] = all[i];
-                }
             }
-            __syncthreads();
+            cluster_barrier();  // no block leaves while its shared memory is read
+            if (part != 0) return;
         }
-        cluster_barrier();  // no block leaves while its shared memory is read
-        if (part != 0) return;
-    }
 
-    const Stats all = s_block;
+    const Stats all = s_row[mine];
     const bool bad = all.nan || all.m == INFINITY;
     const bool empty = !bad && all.m == -INFINITY;
     // relative to the largest logit; the sum of both in 64 bits rounds once
@@ -524,14 +583,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1)
         if (empty || v == -INFINITY) return -INFINITY;
         return static_cast<float>(static_cast<double>(p.scale) * (static_cast<double>(v) - all.m) - ln_s);
     };
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         if (p.logprob) p.logprob[r] = logprob_of(load1(x, t));
         if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : static_cast<float>(lse));
         if (p.entropy) p.entropy[r] = bad ? NAN : (empty ? 0.0f : ln_s - kLn2 * all.w / all.s);
     }
     if constexpr (TOP)
-        for (int i = threadIdx.x; i < k; i += kThreads) {
-            const uint64_t e = tops.best[i];
+        for (int i = tid; i < k; i += kThreads) {
+            const uint64_t e = s_best[mine][i];
             p.top_index[r * k + i] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
             p.top_logprob[r * k + i] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)));
         }
@@ -656,12 +715,13 @@ __global__ void __launch_bounds__(kGradThreads)
     }
 }
 
-template <typename T, int WARPS, bool TOP>
+template <typename T, int WARPS>
 cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
 {
+    constexpr int rows = kWarps / WARPS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.R * split));
-    cfg.blockDim = dim3(32 * WARPS);
+    cfg.gridDim = dim3(static_cast<unsigned>((p.R + rows - 1) / rows * split));
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -669,26 +729,22 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, forge_token_logprob_kernel<T, WARPS, TOP>, x, p, split);
+    return p.top_k > 0 ? cudaLaunchKernelEx(&cfg, forge_token_logprob_kernel<T, WARPS, true>, x, p, split)
+                       : cudaLaunchKernelEx(&cfg, forge_token_logprob_kernel<T, WARPS, false>, x, p, split);
 }
 
-// Blocks of one, two or eight warps by the row's length, so that a thread has
-// a few vectors at least; long rows are split over clusters of up to eight
-// blocks while the rows alone leave SMs without work.
+// One, two or eight warps a row by its length, so that a thread has a few
+// vectors at least; long rows are split over clusters of up to eight blocks
+// while the rows alone leave SMs without work.
 template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
-    if (nvec <= 256)
-        return p.top_k > 0 ? launch_forward<T, 1, true>(x, p, 1, s)
-                           : launch_forward<T, 1, false>(x, p, 1, s);
-    if (nvec <= 1024)
-        return p.top_k > 0 ? launch_forward<T, 2, true>(x, p, 1, s)
-                           : launch_forward<T, 2, false>(x, p, 1, s);
+    if (nvec <= 256) return launch_forward<T, 1>(x, p, 1, s);
+    if (nvec <= 1024) return launch_forward<T, 2>(x, p, 1, s);
     int split = 1;
     while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
-    return p.top_k > 0 ? launch_forward<T, 8, true>(x, p, split, s)
-                       : launch_forward<T, 8, false>(x, p, split, s);
+    return launch_forward<T, 8>(x, p, split, s);
 }
 
 template <typename T, typename O>
