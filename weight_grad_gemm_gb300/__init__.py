@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libforge.so")
@@ -465,16 +466,21 @@ def _tensor_list(ts, what):
         raise TypeError(f"{what} must share one dtype")
     if not all([t.is_cuda and t.is_contiguous() for t in ts]):
         raise ValueError(f"{what} must be contiguous CUDA tensors")
-    ptrs = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in ts])
-    sizes = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in ts])
+    ptrs = array("q", [t.data_ptr() for t in ts])
+    sizes = array("q", [t.numel() for t in ts])
     return ptrs, sizes, FORGE_F32 if n == 0 else _float_code(ts[0])
+
+
+def _address(a):
+    """The host address of an array; the caller holds the array during the call."""
+    return a.buffer_info()[0] or None
 
 
 def forge_grad_norm(grads, norm, *, stream=None):
     """norm (fp32 [1]) = the square root of the sum of squares over all tensors
     of grads (a list, bf16 or fp32)."""
     ptrs, sizes, code = _tensor_list(grads, "grads")
-    s = lib().forge_grad_norm(ptrs, sizes, len(grads), code, _vector(norm, 1, "norm"),
+    s = lib().forge_grad_norm(_address(ptrs), _address(sizes), len(grads), code, _vector(norm, 1, "norm"),
                               _stream(stream, norm))
     _check(s, "forge_grad_norm")
 
@@ -486,10 +492,10 @@ def forge_clip_grads(grads, norm, out=None, *, max_norm, stream=None):
     optrs, ocode = ptrs, code
     if out is not None:
         optrs, osizes, ocode = _tensor_list(out, "out")
-        if len(out) != len(grads) or bytes(osizes) != bytes(sizes):
+        if len(out) != len(grads) or osizes != sizes:
             raise ValueError("out must have one tensor of the same size for each of grads")
-    s = lib().forge_clip_grads(ptrs, sizes, len(grads), code, _vector(norm, 1, "norm"), max_norm,
-                               optrs, ocode, _stream(stream, norm))
+    s = lib().forge_clip_grads(_address(ptrs), _address(sizes), len(grads), code,
+                               _vector(norm, 1, "norm"), max_norm, _address(optrs), ocode, _stream(stream, norm))
     _check(s, "forge_clip_grads")
 
 

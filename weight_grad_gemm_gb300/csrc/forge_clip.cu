@@ -230,11 +230,15 @@ forge_status check_list(const void* const* ptr, const int64_t* n, int32_t P)
 
 forge_status check_memory(const void* const* ptr, const int64_t* n, int32_t P, forge_dtype dt)
 {
-    for (int32_t j = 0; j < P; ++j) {
-        if (n[j] == 0) continue;
-        const forge_status st = device_resident(&ptr[j], 1);
+    // runs of tensors with elements (an empty tensor's pointer means nothing)
+    for (int32_t j = 0, first = 0; j <= P; ++j) {
+        if (j < P && n[j] > 0) {
+            if (!aligned(ptr[j], size_of(dt))) return FORGE_ERR_MISALIGNED;
+            continue;
+        }
+        const forge_status st = device_resident(ptr + first, j - first);
         if (st != FORGE_OK) return st;
-        if (!aligned(ptr[j], size_of(dt))) return FORGE_ERR_MISALIGNED;
+        first = j + 1;
     }
     return FORGE_OK;
 }

@@ -32,19 +32,12 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, int64_t i, float x)
     p[i] = __float2bfloat16_rn(x);
 }
 
-// The row of token t: -1 for padding.  An id past the vocabulary is recorded
-// in the status word and taken as padding.
-__device__ __forceinline__ int64_t id_of(const void* ids, bool wide, int64_t t, int64_t V,
-                                         int* status)
+// A negative id is padding.  An id past the vocabulary is recorded in the
+// status word and taken as padding.  (The loads stand apart from the check, so
+// that a batch of them is in flight at once.)
+__device__ __forceinline__ void bad_id(int* status)
 {
-    const int64_t r = wide ? static_cast<const int64_t*>(ids)[t]
-                           : static_cast<const int32_t*>(ids)[t];
-    if (r < 0) return -1;
-    if (r >= V) {
-        *reinterpret_cast<volatile int*>(status) = kDevInvalidArg;
-        return -1;
-    }
-    return r;
+    *reinterpret_cast<volatile int*>(status) = kDevInvalidArg;
 }
 
 // ------------------------------------------------------------------ lookup
@@ -110,7 +103,12 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
          u < T * spans; u += warps) {
         const int64_t t = u / spans, c0 = (u - t * spans) * S::columns + lane * S::vec;
-        const int64_t r = id_of(ids, wide, t, V, status);
+        int64_t r = wide ? __ldg(static_cast<const int64_t*>(ids) + t)
+                         : __ldg(static_cast<const int32_t*>(ids) + t);
+        if (r >= V) {
+            bad_id(status);
+            r = -1;
+        }
         const W* src = w + r * D;
         Y* dst = y + t * D;
         if constexpr (VEC) {
@@ -167,19 +165,22 @@ constexpr int kDigitBits = 5;
 constexpr int kOrderShared = 4096;  // items of a list that is sorted in shared memory
 constexpr int kOrderSmem = 2 * kOrderShared * static_cast<int>(sizeof(int2));
 
-// Token order: order[i] the token at place i, seg[r] the places [x, y) of row
-// r, *total the number of tokens that are not padding.  listA, listB: room for
-// T items where a block's list exceeds shared memory.
+// Token order: order[i] the token at place i and row[i] its row (-1 past the
+// tokens that are not padding), seg[r] the places [x, y) of row r.  listA,
+// listB: room for T items where a block's list exceeds shared memory.
 struct Order {
     int32_t* order;
+    int32_t* row;
     int2* seg;
-    int32_t* total;
     int2* listA;
     int2* listB;
 };
 
+constexpr int kIdFlight = 8;  // loads of ids in flight per lane
+
+template <typename ID>
 __global__ void __launch_bounds__(kOrderThreads, 1)
-    forge_token_order_kernel(const void* ids, bool wide, int64_t T, int64_t V, Order o, int* status)
+    forge_token_order_kernel(const ID* __restrict__ ids, int64_t T, int64_t V, Order o, int* status)
 {
     extern __shared__ int2 s_list[];
     __shared__ uint32_t s_count[kOrderThreads];  // digit-major: [digit][warp]
@@ -188,50 +189,65 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     const uint32_t before = (1u << lane) - 1u;
     const int32_t cls = blockIdx.x;
 
-    // rows without a token
-    const int64_t local_rows = (V + kClasses - 1) / kClasses;
-    for (int64_t k = threadIdx.x; k < local_rows; k += kOrderThreads)
-        if (k * kClasses + cls < V) o.seg[k * kClasses + cls] = make_int2(0, 0);
-
-    // count
+    // count, this warp's ids [lo, hi)
     const int64_t chunk = (T + kOrderThreads - 1) / kOrderThreads * 32;
     const int64_t lo = warp * chunk, hi = lo + chunk < T ? lo + chunk : T;
+    auto fetch = [&](int64_t i0, int32_t (&r)[kIdFlight], bool& bad) {
+        ID id[kIdFlight];
+#pragma unroll
+        for (int u = 0; u < kIdFlight; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            id[u] = i < hi ? __ldg(ids + i) : static_cast<ID>(-1);
+        }
+#pragma unroll
+        for (int u = 0; u < kIdFlight; ++u) {
+            const bool past = id[u] >= V;
+            bad = bad || past;
+            r[u] = past || id[u] < 0 ? -1 : static_cast<int32_t>(id[u]);
+        }
+    };
     uint32_t own = 0, less = 0;
-#pragma unroll 8
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-        const int64_t r = id_of(ids, wide, i, V, status);
-        const int32_t c = static_cast<int32_t>(r) & (kClasses - 1);
-        own += r >= 0 && c == cls;
-        less += r >= 0 && c < cls;
+    bool bad = false;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kIdFlight) {
+        int32_t r[kIdFlight];
+        fetch(i0, r, bad);
+#pragma unroll
+        for (int u = 0; u < kIdFlight; ++u) {
+            const int32_t c = r[u] & (kClasses - 1);
+            own += r[u] >= 0 && c == cls;
+            less += r[u] >= 0 && c < cls;
+        }
     }
+    if (bad && cls == 0) bad_id(status);
     own = __reduce_add_sync(0xffffffffu, own);
     less = __reduce_add_sync(0xffffffffu, less);
     if (lane == 0) {
         s_own[warp] = own;
         s_less[warp] = less;
     }
+
+    // rows without a token
+    const int64_t local_rows = (V + kClasses - 1) / kClasses;
+    for (int64_t k = threadIdx.x; k < local_rows; k += kOrderThreads)
+        if (k * kClasses + cls < V) o.seg[k * kClasses + cls] = make_int2(0, 0);
     __syncthreads();
-    int32_t base = 0, n = 0, at = 0;
-    for (int w = 0; w < kOrderWarps; ++w) {
-        base += s_less[w];
-        if (w == warp) at = n;
-        n += s_own[w];
-    }
-    if (cls == kClasses - 1 && threadIdx.x == 0) *o.total = base + n;
+    own = s_own[lane];
+    less = __reduce_add_sync(0xffffffffu, s_less[lane]);
+    const int32_t base = less;
+    const int32_t n = __reduce_add_sync(0xffffffffu, own);
+    int32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? own : 0u);
+    if (cls == kClasses - 1)
+        for (int64_t i = base + n + threadIdx.x; i < T; i += kOrderThreads) o.row[i] = -1;
 
     // collect
     const bool shared = n <= kOrderShared;
     int2* src = shared ? s_list : o.listA + base;
     int2* dst = shared ? s_list + kOrderShared : o.listB + base;
-    for (int64_t i0 = lo; i0 < hi; i0 += 32 * 8) {
-        int32_t r[8];
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kIdFlight) {
+        int32_t r[kIdFlight];
+        fetch(i0, r, bad);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t i = i0 + 32 * u + lane;
-            r[u] = i < hi ? static_cast<int32_t>(id_of(ids, wide, i, V, status)) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kIdFlight; ++u) {
             const bool mine = r[u] >= 0 && (r[u] & (kClasses - 1)) == cls;
             const uint32_t all = __ballot_sync(0xffffffffu, mine);
             if (mine)
@@ -268,8 +284,7 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         }
         if (lane == 31) s_own[warp] = inc;
         __syncthreads();
-        uint32_t ahead = 0;
-        for (int w = 0; w < warp; ++w) ahead += s_own[w];
+        const uint32_t ahead = __reduce_add_sync(0xffffffffu, lane < warp ? s_own[lane] : 0u);
         s_count[threadIdx.x] = ahead + inc - v;
         __syncthreads();
         for (int32_t i0 = p0; i0 < p1; i0 += 32) {
@@ -290,8 +305,10 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
 
     for (int32_t i = threadIdx.x; i < n; i += kOrderThreads) {
         const int2 item = src[i];
+        const int32_t r = (item.x << kClassBits) + cls;
         o.order[base + i] = item.y;
-        int2* s = &o.seg[static_cast<int64_t>(item.x) * kClasses + cls];
+        o.row[base + i] = r;
+        int2* s = &o.seg[r];
         if (i == 0 || src[i - 1].x != item.x) s->x = base + i;
         if (i == n - 1 || src[i + 1].x != item.x) s->y = base + i + 1;
     }
@@ -299,205 +316,277 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
 
 // ------------------------------------------------------------------ sums
 
-// A warp sums 256 columns of a row: lane l holds columns 4 l .. 4 l + 3 and
-// 128 + 4 l .. of the slice, so that loads and stores are whole vectors
-// (VEC: D a multiple of 4, every base aligned to four elements), or columns
-// l + 32 k one by one.
-constexpr int kSlice = 256;
-constexpr int kPer = kSlice / 32;
-
-template <bool VEC>
-__device__ __forceinline__ int64_t column(int64_t slice, int lane, int k)
-{
-    return slice * kSlice + (VEC ? (k >> 2) * 128 + 4 * lane + (k & 3) : 32 * k + lane);
-}
-
-__device__ __forceinline__ void load4(const float* p, float* o)
-{
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    o[0] = v.x;
-    o[1] = v.y;
-    o[2] = v.z;
-    o[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* o)
-{
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    o[0] = __uint_as_float(u.x << 16);
-    o[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    o[2] = __uint_as_float(u.y << 16);
-    o[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
-
-template <bool VEC, typename G>
-__device__ __forceinline__ void load_slice(const G* row, int64_t slice, int64_t D, int lane,
-                                           float (&x)[kPer])
-{
-    if constexpr (VEC) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t c = column<true>(slice, lane, 4 * h);
-            if (c < D)
-                load4(row + c, x + 4 * h);
-            else
-                x[4 * h] = x[4 * h + 1] = x[4 * h + 2] = x[4 * h + 3] = 0.0f;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int64_t c = column<false>(slice, lane, k);
-            x[k] = c < D ? load1(row, c) : 0.0f;
-        }
+// Columns come in vectors of four (VEC: D a multiple of 4, every base aligned
+// to four elements) or one by one.
+template <typename G, int N>
+struct Raw;
+template <>
+struct Raw<float, 4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void add_to(float (&g)[4]) const
+    {
+        g[0] += v.x;
+        g[1] += v.y;
+        g[2] += v.z;
+        g[3] += v.w;
     }
-}
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void add_to(float (&g)[4]) const
+    {
+        g[0] += __uint_as_float(v.x << 16);
+        g[1] += __uint_as_float(v.x & 0xFFFF0000u);
+        g[2] += __uint_as_float(v.y << 16);
+        g[3] += __uint_as_float(v.y & 0xFFFF0000u);
+    }
+};
+template <typename G>
+struct Raw<G, 1> {
+    G v;
+    __device__ __forceinline__ void load(const G* p) { v = *p; }
+    __device__ __forceinline__ void add_to(float (&g)[1]) const { g[0] += static_cast<float>(v); }
+};
 
-// acc += the slices of n rows of a [*, D] array, the i-th being row of(i), in
-// that order, kFlight rows in flight.
-constexpr int kFlight = 4;
-template <bool VEC, typename G, typename F>
-__device__ __forceinline__ void add_rows(const G* base, int32_t n, F of, int64_t slice, int64_t D,
-                                         int lane, float (&acc)[kPer])
+// g += the entries at `column` of n rows of a [*, D] array, the i-th being row
+// of(i), in that order, F rows in flight.
+template <int F, int N, typename G, typename ROW>
+__device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int64_t D, float (&g)[N])
 {
-    for (int32_t i0 = 0; i0 < n; i0 += 32) {
-        const int32_t m = n - i0 < 32 ? n - i0 : 32;
-        const int64_t mine = lane < m ? of(i0 + lane) : 0;
-        for (int32_t j0 = 0; j0 < m; j0 += kFlight) {
-            float x[kFlight][kPer];
+    for (int32_t i0 = 0; i0 < n; i0 += F) {
+        int32_t at[F];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                const int64_t r = __shfl_sync(0xffffffffu, mine, (j0 + u) & 31);
-                if (j0 + u < m)
-                    load_slice<VEC>(base + r * D, slice, D, lane, x[u]);
-                else
+        for (int u = 0; u < F; ++u) at[u] = i0 + u < n ? of(i0 + u) : 0;
+        Raw<G, N> x[F];
 #pragma unroll
-                    for (int k = 0; k < kPer; ++k) x[u][k] = 0.0f;
-            }
+        for (int u = 0; u < F; ++u)
+            if (i0 + u < n) x[u].load(column + static_cast<int64_t>(at[u]) * D);
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) acc[k] += x[u][k];
-        }
+        for (int u = 0; u < F; ++u)
+            if (i0 + u < n) x[u].add_to(g);
     }
 }
 
 // A row with more than P = 2^piece_bits tokens (a frequent token, or one that
 // fills the batch) is summed in pieces: its places are cut at the multiples
-// of P, and a block of this kernel adds one piece's tokens, eight warps a
-// part each, into a row of `partial`.  Within the P places b P .. there are at
-// most two such pieces: one of a row that goes on from the places before
-// (slot 2 b) and one of a row that starts here (slot 2 b + 1).
-template <bool VEC, typename G>
+// of P, and a block of this kernel adds 256 columns of one piece's tokens,
+// its warps a part each, into a row of `partial`.  Within the P places b P ..
+// there are at most two such pieces: one of a row that goes on from the places
+// before (slot 2 b) and one of a row that starts here (slot 2 b + 1).
+constexpr int kSlice = 256;
+template <typename G, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    forge_embedding_pieces_kernel(const G* dY, const void* ids, bool wide, int64_t D, Order o,
-                                  int32_t piece_bits, float* partial)
+    forge_embedding_pieces_kernel(const G* dY, int64_t T, int64_t D, Order o, int32_t piece_bits,
+                                  float* partial)
 {
-    __shared__ float sh[kThreads / 32][kSlice];
+    constexpr int kWarps = kThreads / 32;
+    constexpr int N = VEC ? 4 : 1;
+    __shared__ float sh[kWarps][kSlice];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t slices = static_cast<int32_t>((D + kSlice - 1) / kSlice);
-    const int64_t slice = blockIdx.x % slices;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % slices) * kSlice;
     const int32_t b = blockIdx.x / slices, P = 1 << piece_bits;
-    const int32_t total = *o.total;
-    const int32_t p0 = b << piece_bits;
-    if (p0 >= total) return;
-    const int32_t p1 = total - p0 < P ? total : p0 + P;
-    int64_t row = -1;
+    const int64_t p0 = static_cast<int64_t>(b) << piece_bits;
+    const int64_t p1 = p0 + P < T ? p0 + P : T;
+    int32_t row = -1;
     for (int which = 0; which < 2; ++which) {
-        const int32_t t = o.order[which ? p1 - 1 : p0];
-        const int64_t r = wide ? static_cast<const int64_t*>(ids)[t]
-                               : static_cast<const int32_t*>(ids)[t];
+        // the last place of the block may be past the tokens: then its row is
+        // that of the last token before, if that one is in the block at all
+        int32_t r = o.row[which ? p1 - 1 : p0];
+        if (r < 0) {
+            if (which == 0) return;
+            int64_t a = p0, e = p1 - 1;  // row[a] >= 0, row[e] < 0
+            while (e - a > 1) {
+                const int64_t m = (a + e) >> 1;
+                if (o.row[m] >= 0)
+                    a = m;
+                else
+                    e = m;
+            }
+            r = o.row[a];
+        }
         if (r == row) break;
         row = r;
         const int2 s = o.seg[r];
         if (s.y - s.x <= P) continue;
-        const int32_t a = s.x > p0 ? s.x : p0, e = s.y < p1 ? s.y : p1;
-        const int32_t per = (e - a + kThreads / 32 - 1) / (kThreads / 32);
+        const int32_t a = s.x > p0 ? s.x : static_cast<int32_t>(p0);
+        const int32_t e = s.y < p1 ? s.y : static_cast<int32_t>(p1);
+        const int32_t per = (e - a + kWarps - 1) / kWarps;
         const int32_t wa = a + warp * per < e ? a + warp * per : e;
         const int32_t we = wa + per < e ? wa + per : e;
-        float acc[kPer] = {};
-        add_rows<VEC>(dY, we - wa, [&](int32_t i) { return o.order[wa + i]; }, slice, D, lane, acc);
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) sh[warp][column<VEC>(0, lane, k)] = acc[k];
+        for (int h = 0; h < kSlice / (32 * N); ++h) {
+            const int64_t c = c0 + (32 * h + lane) * N;
+            float g[N] = {};
+            if (c < D)
+                add_rows<8>(dY + c, we - wa, [&](int32_t i) { return o.order[wa + i]; }, D, g);
+#pragma unroll
+            for (int k = 0; k < N; ++k) sh[warp][(32 * h + lane) * N + k] = g[k];
+        }
         __syncthreads();
         float x = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) x += sh[w][threadIdx.x];
-        const int64_t c = slice * kSlice + threadIdx.x;
+        for (int w = 0; w < kWarps; ++w) x += sh[w][threadIdx.x];
         const int64_t slot = 2 * static_cast<int64_t>(b) + (s.x >= p0 ? 1 : 0);
-        if (c < D) partial[slot * D + c] = x;
+        if (c0 + threadIdx.x < D) partial[slot * D + c0 + threadIdx.x] = x;
     }
 }
 
-enum { SUM_STORE = 0, SUM_ADD = 1, SUM_ADAMW = 2 };
-
-// One warp per (row, slice), the slices of a row side by side: the sum of the
-// row's tokens (or of its pieces), then the store, the addition to dW or the
-// AdamW step.  Bound by HBM: dW written, or W, m, v read and written, once.
-template <typename G, int MODE, int ST, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    forge_embedding_grad_kernel(const G* dY, int64_t V, int64_t D, float scale, float* dW, Order o,
-                                int32_t piece_bits, const float* partial, const Params p)
+// The sum over a row's tokens at one column (vector): token by token, or
+// piece by piece.
+template <int F, int N, typename G>
+__device__ __forceinline__ void row_sum(const G* dY, const Order& o, const float* partial,
+                                        int32_t piece_bits, int2 s, int64_t D, int64_t c, float (&g)[N])
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t slices = (D + kSlice - 1) / kSlice;
-    const int64_t units = V * slices;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    const int32_t P = 1 << piece_bits;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-         u < units; u += warps) {
-        const int64_t row = u / slices, slice = u - row * slices;
-        const int2 s = o.seg ? o.seg[row] : make_int2(0, 0);
-        const int32_t n = s.y - s.x;
-        if (MODE == SUM_ADD && n == 0) continue;
-        float g[kPer] = {};
-        if (n > P) {
-            const int32_t b0 = s.x >> piece_bits, b1 = (s.y - 1) >> piece_bits;
-            add_rows<VEC>(
-                partial, b1 - b0 + 1,
-                [&](int32_t i) { return 2 * static_cast<int64_t>(b0 + i) + (i == 0 ? 1 : 0); },
-                slice, D, lane, g);
-        } else if (n > 0) {
-            add_rows<VEC>(dY, n, [&](int32_t i) { return o.order[s.x + i]; }, slice, D, lane, g);
+    const int32_t n = s.y - s.x;
+    if (n <= (1 << piece_bits)) {
+        add_rows<F>(dY + c, n, [&](int32_t i) { return __ldg(o.order + s.x + i); }, D, g);
+    } else {
+        const int32_t b0 = s.x >> piece_bits, b1 = (s.y - 1) >> piece_bits;
+        add_rows<F>(
+            partial + c, b1 - b0 + 1,
+            [&](int32_t i) { return 2 * (b0 + i) + (i == 0 ? 1 : 0); }, D, g);
+    }
+}
+
+enum { SUM_STORE = 0, SUM_ADAMW = 1 };
+
+template <bool VEC>
+constexpr int kUnits = VEC ? 2 : 4;
+
+// dW or the AdamW step over all V D elements, flat, so that no width leaves
+// lanes idle: a block takes `turns` tiles of U vectors a thread, one after the
+// other, and a thread carries row and column along instead of dividing.  Two
+// vectors (VEC; four single elements otherwise) are in hand at once, with the
+// places of the next ones already on their way: most rows of a large
+// vocabulary have no token, and their zeros (or their decay) must not wait for
+// a table.  Blocks are many and start in order of the rows, so that those with
+// frequent tokens, which a vocabulary has in front, are not the last to end.
+// Bound by HBM: dW written, or W, m, v read and written, once.
+template <typename G, int MODE, int ST, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4)
+    forge_embedding_grad_kernel(const G* dY, int32_t V, int32_t D, float scale, float* dW, Order o,
+                                int32_t piece_bits, const float* partial, int32_t turns,
+                                const Params p)
+{
+    constexpr int N = VEC ? 4 : 1;
+    constexpr int U = kUnits<VEC>;
+    constexpr int F = MODE == SUM_ADAMW ? 2 : 4;
+    const uint32_t width = D / N;  // vectors of a row
+    constexpr uint32_t step = kThreads * U;
+    const uint32_t step_rows = step / width, step_columns = step - step_rows * width;
+    auto places = [&](uint32_t r) {
+        return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
+    };
+    uint32_t row[U], column[U];
+    int2 s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t q = static_cast<int64_t>(blockIdx.x) * turns * step + u * kThreads + threadIdx.x;
+        row[u] = static_cast<uint32_t>(q / width);
+        column[u] = static_cast<uint32_t>(q - static_cast<int64_t>(row[u]) * width);
+        s[u] = places(row[u]);
+    }
+    for (int32_t turn = 0; turn < turns && row[0] < V; ++turn) {
+        float g[U * N], w[U * N], a[U * N], b[U * N];
+        if constexpr (MODE == SUM_ADAMW) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = static_cast<int64_t>(row[u]) * D + column[u] * N;
+                if (row[u] >= V) continue;
+                if constexpr (VEC) {
+                    StateIO<ST_F32>::ld4(p.W, at, w + 4 * u);
+                    StateIO<ST>::ld4(p.s1, at, a + 4 * u);
+                    StateIO<ST>::ld4(p.s2, at, b + 4 * u);
+                } else {
+                    w[u] = StateIO<ST_F32>::ld(p.W, at);
+                    a[u] = StateIO<ST>::ld(p.s1, at);
+                    b[u] = StateIO<ST>::ld(p.s2, at);
+                }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) g[k] *= scale;
+        for (int u = 0; u < U; ++u) {
+            float x[N] = {};
+            if (s[u].y > s[u].x)
+                row_sum<F>(dY, o, partial, piece_bits, s[u], D, column[u] * N, x);
 #pragma unroll
-        for (int h = 0; h < (VEC ? 2 : kPer); ++h) {
-            const int64_t c = column<VEC>(slice, lane, VEC ? 4 * h : h);
-            if (c >= D) continue;
-            const int64_t at = row * D + c;
-            if constexpr (VEC) {
-                float* gh = g + 4 * h;
-                if constexpr (MODE == SUM_ADAMW) {
-                    float w[4], a[4], b[4];
-                    StateIO<ST_F32>::ld4(p.W, at, w);
-                    StateIO<ST>::ld4(p.s1, at, a);
-                    StateIO<ST>::ld4(p.s2, at, b);
-                    step4<OP_ADAMW>(p, gh, w, a, b);
-                    StateIO<ST_F32>::st4(p.W, at, w);
-                    StateIO<ST>::st4(p.s1, at, a);
-                    StateIO<ST>::st4(p.s2, at, b);
+            for (int k = 0; k < N; ++k) g[u * N + k] = x[k] * scale;
+        }
+#pragma unroll
+        for (int h = 0; h < U * N / 4; ++h)
+            if constexpr (MODE == SUM_ADAMW)
+                step4<OP_ADAMW>(p, g + 4 * h, w + 4 * h, a + 4 * h, b + 4 * h);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = static_cast<int64_t>(row[u]) * D + column[u] * N;
+            if (row[u] < V) {
+                if constexpr (MODE == SUM_ADAMW && VEC) {
+                    StateIO<ST_F32>::st4(p.W, at, w + 4 * u);
+                    StateIO<ST>::st4(p.s1, at, a + 4 * u);
+                    StateIO<ST>::st4(p.s2, at, b + 4 * u);
+                } else if constexpr (MODE == SUM_ADAMW) {
+                    StateIO<ST_F32>::st(p.W, at, w[u]);
+                    StateIO<ST>::st(p.s1, at, a[u]);
+                    StateIO<ST>::st(p.s2, at, b[u]);
+                } else if constexpr (VEC) {
+                    StateIO<ST_F32>::st4(dW, at, g + 4 * u);
                 } else {
-                    if constexpr (MODE == SUM_ADD) {
-                        float d[4];
-                        StateIO<ST_F32>::ld4(dW, at, d);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) gh[i] += d[i];
-                    }
-                    StateIO<ST_F32>::st4(dW, at, gh);
+                    StateIO<ST_F32>::st(dW, at, g[u]);
                 }
-            } else if constexpr (MODE == SUM_ADAMW) {
-                float gs[4] = {g[h], g[h], g[h], g[h]}, w[4], a[4], b[4];
-                w[0] = w[1] = w[2] = w[3] = StateIO<ST_F32>::ld(p.W, at);
-                a[0] = a[1] = a[2] = a[3] = StateIO<ST>::ld(p.s1, at);
-                b[0] = b[1] = b[2] = b[3] = StateIO<ST>::ld(p.s2, at);
-                step4<OP_ADAMW>(p, gs, w, a, b);
-                StateIO<ST_F32>::st(p.W, at, w[0]);
-                StateIO<ST>::st(p.s1, at, a[0]);
-                StateIO<ST>::st(p.s2, at, b[0]);
-            } else {
-                dW[at] = MODE == SUM_ADD ? dW[at] + g[h] : g[h];
             }
+            row[u] += step_rows;
+            column[u] += step_columns;
+            if (column[u] >= width) {
+                column[u] -= width;
+                ++row[u];
+            }
+            s[u] = places(row[u]);
+        }
+    }
+}
+
+// dW += the sums, over the rows that have a token only: flat over (place,
+// column); the first place of a row takes it.
+template <typename G, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    forge_embedding_accumulate_kernel(const G* dY, int64_t T, int64_t D, float scale, float* dW,
+                                      Order o, int32_t piece_bits, const float* partial)
+{
+    constexpr int N = VEC ? 4 : 1;
+    const int64_t width = D / N;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t step_places = step / width, step_columns = step - step_places * width;
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    int64_t i = q / width, column = q - i * width;
+    while (i < T) {
+        const int32_t r = __ldg(o.row + i);
+        if (r < 0) return;  // past the tokens, and so is what follows
+        const int2 s = __ldg(o.seg + r);
+        if (s.x == i) {
+            const int64_t c = column * N, at = r * D + c;
+            float d[N], g[N] = {};
+            if constexpr (VEC)
+                StateIO<ST_F32>::ld4(dW, at, d);
+            else
+                d[0] = StateIO<ST_F32>::ld(dW, at);
+            row_sum<4>(dY, o, partial, piece_bits, s, D, c, g);
+#pragma unroll
+            for (int k = 0; k < N; ++k) d[k] = fmaf(scale, g[k], d[k]);
+            if constexpr (VEC)
+                StateIO<ST_F32>::st4(dW, at, d);
+            else
+                StateIO<ST_F32>::st(dW, at, d[0]);
+        }
+        i += step_places;
+        column += step_columns;
+        if (column >= width) {
+            column -= width;
+            ++i;
         }
     }
 }
@@ -533,6 +622,7 @@ int32_t piece_bits_of(int64_t T)
 }
 
 // The order kernel's shared memory, allowed once per device.
+template <typename ID>
 cudaError_t allow_order_smem()
 {
     static unsigned long long done = 0;  // one bit per device ordinal < 64
@@ -541,50 +631,85 @@ cudaError_t allow_order_smem()
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (__atomic_load_n(&done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(forge_token_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kOrderSmem);
+    e = cudaFuncSetAttribute(forge_token_order_kernel<ID>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kOrderSmem);
     if (e == cudaSuccess) __atomic_fetch_or(&done, bit, __ATOMIC_ACQ_REL);
     return e;
 }
 
-template <typename G, int MODE, int ST, bool VEC>
-cudaError_t launch_grad(const G* dY, const void* ids, bool wide, int64_t T, int64_t V, int64_t D,
-                        float scale, float* dW, const Params& p, int sms, cudaStream_t s)
+template <typename ID>
+cudaError_t order_tokens(const void* ids, int64_t T, int64_t V, const Order& o, int* status,
+                         cudaStream_t s)
 {
-    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const cudaError_t e = allow_order_smem<ID>();
+    if (e != cudaSuccess) return e;
+    forge_token_order_kernel<ID><<<kClasses, kOrderThreads, kOrderSmem, s>>>(
+        static_cast<const ID*>(ids), T, V, o, status);
+    return cudaGetLastError();
+}
+
+// What becomes of the sums: dW written, dW added to, or the AdamW step.
+enum class Sum { Store, Add, AdamW };
+
+template <typename G, bool VEC>
+cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids, bool wide,
+                        int64_t T, int64_t V, int64_t D, float scale, float* dW, const Params& p,
+                        int sms, cudaStream_t s)
+{
+    if (what == Sum::Add && T == 0) return cudaSuccess;
     const int32_t bits = piece_bits_of(T);
-    const int64_t pieces = (T + (int64_t{1} << bits) - 1) >> bits;
     Order o{};
     float* partial = nullptr;
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
+        const int64_t pieces = T > (int64_t{1} << bits) ? (T + (int64_t{1} << bits) - 1) >> bits : 0;
         auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
         const int64_t order_b = up(T * 4), list_b = up(T * 8), seg_b = up(V * 8);
-        const int64_t partial_b = up(2 * pieces * D * 4);
-        e = scratch_alloc(&scratch, 256 + order_b + 2 * list_b + seg_b + partial_b, s);
+        e = scratch_alloc(&scratch, 2 * order_b + 2 * list_b + seg_b + 2 * pieces * D * 4, s);
         if (e != cudaSuccess) return e;
         uint8_t* at = static_cast<uint8_t*>(scratch);
-        o.total = reinterpret_cast<int32_t*>(at);
-        o.order = reinterpret_cast<int32_t*>(at += 256);
+        o.order = reinterpret_cast<int32_t*>(at);
+        o.row = reinterpret_cast<int32_t*>(at += order_b);
         o.listA = reinterpret_cast<int2*>(at += order_b);
         o.listB = reinterpret_cast<int2*>(at += list_b);
         o.seg = reinterpret_cast<int2*>(at += list_b);
         partial = reinterpret_cast<float*>(at += seg_b);
-        e = allow_order_smem();
-        if (e == cudaSuccess) {
-            forge_token_order_kernel<<<kClasses, kOrderThreads, kOrderSmem, s>>>(ids, wide, T, V, o,
-                                                                               p.status);
-            forge_embedding_pieces_kernel<VEC>
-                <<<static_cast<unsigned>(slices * pieces), kThreads, 0, s>>>(dY, ids, wide, D, o,
-                                                                           bits, partial);
+        e = wide ? order_tokens<int64_t>(ids, T, V, o, p.status, s)
+                 : order_tokens<int32_t>(ids, T, V, o, p.status, s);
+        if (e == cudaSuccess && pieces > 0) {
+            const int64_t blocks = pieces * ((D + kSlice - 1) / kSlice);
+            forge_embedding_pieces_kernel<G, VEC>
+                <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(dY, T, D, o, bits, partial);
+            e = cudaGetLastError();
         }
     }
     if (e == cudaSuccess) {
-        const int64_t want = (V * slices + kThreads / 32 - 1) / (kThreads / 32);
-        const int blocks = static_cast<int>(want < 8LL * sms ? want : 8LL * sms);
-        forge_embedding_grad_kernel<G, MODE, ST, VEC>
-            <<<blocks, kThreads, 0, s>>>(dY, V, D, scale, dW, o, bits, partial, p);
+        const int64_t width = VEC ? D / 4 : D;
+        if (what == Sum::Add) {
+            const int64_t want = (T * width + kThreads - 1) / kThreads;
+            const int blocks = static_cast<int>(want < 8LL * sms ? want : 8LL * sms);
+            forge_embedding_accumulate_kernel<G, VEC>
+                <<<blocks, kThreads, 0, s>>>(dY, T, D, scale, dW, o, bits, partial);
+        } else {
+            // as many turns, up to eight, as leave each SM 32 blocks
+            const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);
+            int64_t turns = tiles / (32LL * sms);
+            turns = turns < 1 ? 1 : (turns > 8 ? 8 : turns);
+            while ((tiles + turns - 1) / turns > INT32_MAX) turns *= 2;
+            const int blocks = static_cast<int>((tiles + turns - 1) / turns);
+            auto go = [&](auto kernel) {
+                kernel<<<blocks, kThreads, 0, s>>>(dY, static_cast<int32_t>(V), static_cast<int32_t>(D),
+                                                   scale, dW, o, bits, partial,
+                                                   static_cast<int32_t>(turns), p);
+            };
+            if (what == Sum::Store)
+                go(forge_embedding_grad_kernel<G, SUM_STORE, ST_F32, VEC>);
+            else if (state_bf16)
+                go(forge_embedding_grad_kernel<G, SUM_ADAMW, ST_BF16, VEC>);
+            else
+                go(forge_embedding_grad_kernel<G, SUM_ADAMW, ST_F32, VEC>);
+        }
         e = cudaGetLastError();
     }
     if (scratch) {
@@ -594,20 +719,18 @@ cudaError_t launch_grad(const G* dY, const void* ids, bool wide, int64_t T, int6
     return e;
 }
 
-template <int MODE, int ST>
-cudaError_t grad(const void* dY, forge_dtype dy_dtype, const void* ids, forge_dtype id_dtype,
-                 int64_t T, int64_t V, int64_t D, float scale, float* dW, const Params& p, int sms,
-                 cudaStream_t s)
+cudaError_t grad(Sum what, bool state_bf16, const void* dY, forge_dtype dy_dtype, const void* ids,
+                 forge_dtype id_dtype, int64_t T, int64_t V, int64_t D, float scale, float* dW,
+                 const Params& p, int sms, cudaStream_t s)
 {
     const bool wide = id_dtype == FORGE_I64;
-    const uintptr_t sa = ST == ST_BF16 ? 8 : 16;
-    const bool vec = D % 4 == 0 && aligned(dY, 4 * size_of(dy_dtype)) &&
-                     (MODE == SUM_ADAMW ? aligned(p.W, 16) && aligned(p.s1, sa) && aligned(p.s2, sa)
-                                        : aligned(dW, 16));
+    const uintptr_t sa = state_bf16 ? 8 : 16;
+    const bool vec = D % 4 == 0 && aligned(dY, 4 * size_of(dy_dtype)) && aligned(dW, 16) &&
+                     aligned(p.W, 16) && aligned(p.s1, sa) && aligned(p.s2, sa);
     auto go = [&](auto* d) {
         using G = std::remove_cv_t<std::remove_pointer_t<decltype(d)>>;
-        return vec ? launch_grad<G, MODE, ST, true>(d, ids, wide, T, V, D, scale, dW, p, sms, s)
-                   : launch_grad<G, MODE, ST, false>(d, ids, wide, T, V, D, scale, dW, p, sms, s);
+        return vec ? launch_grad<G, true>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s)
+                   : launch_grad<G, false>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s);
     };
     return dy_dtype == FORGE_F32 ? go(static_cast<const float*>(dY))
                                  : go(static_cast<const __nv_bfloat16*>(dY));
@@ -686,9 +809,8 @@ extern "C" forge_status forge_embedding_grad(const void* dY, forge_dtype dy_dtyp
     Params p{};
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e =
-        accumulate ? grad<SUM_ADD, ST_F32>(dY, dy_dtype, ids, id_dtype, T, V, D, scale, dW, p, sms, s)
-                   : grad<SUM_STORE, ST_F32>(dY, dy_dtype, ids, id_dtype, T, V, D, scale, dW, p, sms, s);
+    const cudaError_t e = grad(accumulate ? Sum::Add : Sum::Store, false, dY, dy_dtype, ids, id_dtype,
+                               T, V, D, scale, dW, p, sms, s);
     return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }
 
@@ -718,9 +840,7 @@ extern "C" forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dty
     p.s2 = v;
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e =
-        state_dtype == FORGE_F32
-            ? grad<SUM_ADAMW, ST_F32>(dY, dy_dtype, ids, id_dtype, T, V, D, scale, nullptr, p, sms, s)
-            : grad<SUM_ADAMW, ST_BF16>(dY, dy_dtype, ids, id_dtype, T, V, D, scale, nullptr, p, sms, s);
+    const cudaError_t e = grad(Sum::AdamW, state_dtype == FORGE_BF16, dY, dy_dtype, ids, id_dtype, T,
+                               V, D, scale, nullptr, p, sms, s);
     return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }

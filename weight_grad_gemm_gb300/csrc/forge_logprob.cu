@@ -12,6 +12,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "forge.h"
 #include "forge_device.h"
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     constexpr int kGroupLanes = kThreads > kGroups ? kThreads / kGroups : 1;
     constexpr int kUsed = kThreads / kGroupLanes;  // groups of a row: 32 or 64
     __shared__ Tops s_tops[TOP ? kWarps : 1];
-    __shared__ float s_group[kRows][kUsed];
+    __shared__ float s_group[2][kRows][kUsed];
     __shared__ float s_kth[kRows];
     __shared__ int s_held[kWarps];
     __shared__ Stats s_stats[kWarps];
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     Stats st{-INFINITY, 0.0f, 0.0f, false};
     Tops& tops = s_tops[TOP ? warp : 0];
     int held = 0, noted = 0;       // the warp's entries and vectors
+    int turn = 0;                  // times the bound was set
     uint64_t bound = 0;            // rank that an entry has to reach
     float bound_v = -INFINITY;     // its value
 
@@ -394,14 +396,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 #pragma unroll
         for (int o = 1; o < kGroupLanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
         const int group = tid / kGroupLanes, share = tid % kGroupLanes;
-        sync();  // the last reading of the groups
-        if (share == 0) s_group[mine][group] = g;
+        float* groups = s_group[turn & 1][mine];  // the other half may still be read
+        ++turn;
+        if (share == 0) groups[group] = g;
         sync();
         int above = 0;
 #pragma unroll
         for (int i = 0; i < kUsed / kGroupLanes; ++i) {
             const int j = i * kGroupLanes + share;
-            const float o = s_group[mine][j];
+            const float o = groups[j];
             above += o > g || (o == g && j < group);
         }
 #pragma unroll
@@ -575,17 +578,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     const Stats all = s_row[mine];
     const bool bad = all.nan || all.m == INFINITY;
     const bool empty = !bad && all.m == -INFINITY;
-    // relative to the largest logit; the sum of both in 64 bits rounds once
+    // relative to the largest logit, so that near entries keep their digits
     const float ln_s = logf(all.s);
-    const double lse = static_cast<double>(p.scale) * all.m + ln_s;
     auto logprob_of = [&](float v) {
         if (bad) return NAN;
         if (empty || v == -INFINITY) return -INFINITY;
-        return static_cast<float>(static_cast<double>(p.scale) * (static_cast<double>(v) - all.m) - ln_s);
+        return fmaf(p.scale, v - all.m, -ln_s);
     };
     if (tid == 0) {
         if (p.logprob) p.logprob[r] = logprob_of(load1(x, t));
-        if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : static_cast<float>(lse));
+        if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : fmaf(p.scale, all.m, ln_s));
         if (p.entropy) p.entropy[r] = bad ? NAN : (empty ? 0.0f : ln_s - kLn2 * all.w / all.s);
     }
     if constexpr (TOP)
@@ -742,6 +744,7 @@ cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
     const int64_t nvec = p.V / Vec<T>::N;
     if (nvec <= 256) return launch_forward<T, 1>(x, p, 1, s);
     if (nvec <= 1024) return launch_forward<T, 2>(x, p, 1, s);
+    if (const char* e = getenv("FORGE_LP_W"); e && atoi(e) == 4) return launch_forward<T, 4>(x, p, 1, s);
     int split = 1;
     while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
     return launch_forward<T, 8>(x, p, split, s);
