@@ -100,17 +100,31 @@ __global__ void __launch_bounds__(kThreads)
     const int lane = threadIdx.x & 31;
     const int64_t spans = (D + S::columns - 1) / S::columns;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-         u < T * spans; u += warps) {
-        const int64_t t = u / spans, c0 = (u - t * spans) * S::columns + lane * S::vec;
-        int64_t r = wide ? __ldg(static_cast<const int64_t*>(ids) + t)
-                         : __ldg(static_cast<const int32_t*>(ids) + t);
+    const int64_t step_tokens = warps / spans, step_spans = warps - step_tokens * spans;
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    int64_t t = u / spans, span = u - t * spans;
+    auto id_at = [&](int64_t i) -> int64_t {
+        if (i >= T) return -1;
+        return wide ? __ldg(static_cast<const int64_t*>(ids) + i)
+                    : __ldg(static_cast<const int32_t*>(ids) + i);
+    };
+    int64_t next = id_at(t);
+    while (t < T) {
+        int64_t r = next;
+        const int64_t c0 = span * S::columns + lane * S::vec;
         if (r >= V) {
             bad_id(status);
             r = -1;
         }
-        const W* src = w + r * D;
+        W const* const src = w + r * D;
         Y* dst = y + t * D;
+        t += step_tokens;
+        span += step_spans;
+        if (span >= spans) {
+            span -= spans;
+            ++t;
+        }
+        next = id_at(t);  // on its way while this span is moved
         if constexpr (VEC) {
             uint4 v[S::flight];
 #pragma unroll
@@ -165,12 +179,13 @@ constexpr int kDigitBits = 5;
 constexpr int kOrderShared = 4096;  // items of a list that is sorted in shared memory
 constexpr int kOrderSmem = 2 * kOrderShared * static_cast<int>(sizeof(int2));
 
-// Token order: order[i] the token at place i and row[i] its row (-1 past the
-// tokens that are not padding), seg[r] the places [x, y) of row r.  listA,
+// Token order: order[i] the token at place i; at[i] = {its row, and the number
+// of the row's places if this is the first of them, else 0} ({-1, 0} past the
+// tokens that are not padding); seg[r] the places [x, y) of row r.  listA,
 // listB: room for T items where a block's list exceeds shared memory.
 struct Order {
     int32_t* order;
-    int32_t* row;
+    int2* at;
     int2* seg;
     int2* listA;
     int2* listB;
@@ -237,7 +252,8 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     const int32_t n = __reduce_add_sync(0xffffffffu, own);
     int32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? own : 0u);
     if (cls == kClasses - 1)
-        for (int64_t i = base + n + threadIdx.x; i < T; i += kOrderThreads) o.row[i] = -1;
+        for (int64_t i = base + n + threadIdx.x; i < T; i += kOrderThreads)
+            o.at[i] = make_int2(-1, 0);
 
     // collect
     const bool shared = n <= kOrderShared;
@@ -265,13 +281,20 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     for (int shift = 0; (local_rows - 1) >> shift; shift += kDigitBits) {
         s_count[threadIdx.x] = 0;
         __syncthreads();
-        for (int32_t i0 = p0; i0 < p1; i0 += 32) {
-            const bool in = i0 + lane < p1;
-            const uint32_t d =
-                in ? (static_cast<uint32_t>(src[i0 + lane].x) >> shift) & 31u : 32u;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in && (same & before) == 0) s_count[d * 32 + warp] += __popc(same);
-            __syncwarp();
+        for (int32_t i0 = p0; i0 < p1; i0 += 32 * kIdFlight) {
+            uint32_t d[kIdFlight];
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u) {
+                const int32_t i = i0 + 32 * u + lane;
+                d[u] = i < p1 ? (static_cast<uint32_t>(src[i].x) >> shift) & 31u : 32u;
+            }
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u) {
+                if (i0 + 32 * u >= p1) break;
+                const uint32_t same = __match_any_sync(0xffffffffu, d[u]);
+                if (d[u] < 32u && (same & before) == 0) s_count[d[u] * 32 + warp] += __popc(same);
+                __syncwarp();
+            }
         }
         __syncthreads();
         // exclusive scan over (digit, warp)
@@ -287,15 +310,24 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         const uint32_t ahead = __reduce_add_sync(0xffffffffu, lane < warp ? s_own[lane] : 0u);
         s_count[threadIdx.x] = ahead + inc - v;
         __syncthreads();
-        for (int32_t i0 = p0; i0 < p1; i0 += 32) {
-            const bool in = i0 + lane < p1;
-            const int2 item = in ? src[i0 + lane] : make_int2(0, 0);
-            const uint32_t d = in ? (static_cast<uint32_t>(item.x) >> shift) & 31u : 32u;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in) dst[s_count[d * 32 + warp] + __popc(same & before)] = item;
-            __syncwarp();
-            if (in && (same & before) == 0) s_count[d * 32 + warp] += __popc(same);
-            __syncwarp();
+        for (int32_t i0 = p0; i0 < p1; i0 += 32 * kIdFlight) {
+            int2 item[kIdFlight];
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u) {
+                const int32_t i = i0 + 32 * u + lane;
+                item[u] = i < p1 ? src[i] : make_int2(0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u) {
+                if (i0 + 32 * u >= p1) break;
+                const bool in = i0 + 32 * u + lane < p1;
+                const uint32_t d = in ? (static_cast<uint32_t>(item[u].x) >> shift) & 31u : 32u;
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                if (in) dst[s_count[d * 32 + warp] + __popc(same & before)] = item[u];
+                __syncwarp();
+                if (in && (same & before) == 0) s_count[d * 32 + warp] += __popc(same);
+                __syncwarp();
+            }
         }
         __syncthreads();
         int2* t = src;
@@ -307,10 +339,15 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         const int2 item = src[i];
         const int32_t r = (item.x << kClassBits) + cls;
         o.order[base + i] = item.y;
-        o.row[base + i] = r;
         int2* s = &o.seg[r];
         if (i == 0 || src[i - 1].x != item.x) s->x = base + i;
         if (i == n - 1 || src[i + 1].x != item.x) s->y = base + i + 1;
+    }
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < n; i += kOrderThreads) {
+        const int32_t r = (src[i].x << kClassBits) + cls;
+        const bool first = i == 0 || src[i - 1].x != src[i].x;
+        o.at[base + i] = make_int2(r, first ? o.seg[r].y - o.seg[r].x : 0);
     }
 }
 
@@ -352,22 +389,35 @@ struct Raw<G, 1> {
 };
 
 // g += the entries at `column` of n rows of a [*, D] array, the i-th being row
-// of(i), in that order, F rows in flight.
+// of(i), in that order, F (a power of two) rows in flight.
+template <int F, int N, typename G, typename ROW>
+__device__ __forceinline__ void add_batch(const G* column, int32_t i, ROW of, int64_t D, float (&g)[N])
+{
+    int32_t at[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u) at[u] = of(i + u);
+    Raw<G, N> x[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u) x[u].load(column + static_cast<int64_t>(at[u]) * D);
+#pragma unroll
+    for (int u = 0; u < F; ++u) x[u].add_to(g);
+}
 template <int F, int N, typename G, typename ROW>
 __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int64_t D, float (&g)[N])
 {
-    for (int32_t i0 = 0; i0 < n; i0 += F) {
-        int32_t at[F];
-#pragma unroll
-        for (int u = 0; u < F; ++u) at[u] = i0 + u < n ? of(i0 + u) : 0;
-        Raw<G, N> x[F];
-#pragma unroll
-        for (int u = 0; u < F; ++u)
-            if (i0 + u < n) x[u].load(column + static_cast<int64_t>(at[u]) * D);
-#pragma unroll
-        for (int u = 0; u < F; ++u)
-            if (i0 + u < n) x[u].add_to(g);
-    }
+    int32_t i = 0;
+    for (; i + F <= n; i += F) add_batch<F>(column, i, of, D, g);
+    if constexpr (F > 4)
+        if (n - i >= 4) {
+            add_batch<4>(column, i, of, D, g);
+            i += 4;
+        }
+    if constexpr (F > 2)
+        if (n - i >= 2) {
+            add_batch<2>(column, i, of, D, g);
+            i += 2;
+        }
+    if (n - i >= 1) add_batch<1>(column, i, of, D, g);
 }
 
 // A row with more than P = 2^piece_bits tokens (a frequent token, or one that
@@ -384,6 +434,8 @@ __global__ void __launch_bounds__(kThreads)
 {
     constexpr int kWarps = kThreads / 32;
     constexpr int N = VEC ? 4 : 1;
+    constexpr int H = kSlice / (32 * N);                        // vectors of a lane
+    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;      // in flight
     __shared__ float sh[kWarps][kSlice];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t slices = static_cast<int32_t>((D + kSlice - 1) / kSlice);
@@ -395,18 +447,18 @@ __global__ void __launch_bounds__(kThreads)
     for (int which = 0; which < 2; ++which) {
         // the last place of the block may be past the tokens: then its row is
         // that of the last token before, if that one is in the block at all
-        int32_t r = o.row[which ? p1 - 1 : p0];
+        int32_t r = o.at[which ? p1 - 1 : p0].x;
         if (r < 0) {
             if (which == 0) return;
-            int64_t a = p0, e = p1 - 1;  // row[a] >= 0, row[e] < 0
+            int64_t a = p0, e = p1 - 1;  // at[a].x >= 0, at[e].x < 0
             while (e - a > 1) {
                 const int64_t m = (a + e) >> 1;
-                if (o.row[m] >= 0)
+                if (o.at[m].x >= 0)
                     a = m;
                 else
                     e = m;
             }
-            r = o.row[a];
+            r = o.at[a].x;
         }
         if (r == row) break;
         row = r;
@@ -417,16 +469,27 @@ __global__ void __launch_bounds__(kThreads)
         const int32_t per = (e - a + kWarps - 1) / kWarps;
         const int32_t wa = a + warp * per < e ? a + warp * per : e;
         const int32_t we = wa + per < e ? wa + per : e;
+        float g[H][N] = {};
+        for (int32_t i0 = wa; i0 < we; i0 += kTokens) {
+            Raw<G, N> x[kTokens][H];
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u) {
+                const G* src = dY + c0 + static_cast<int64_t>(o.order[i0 + u < we ? i0 + u : wa]) * D;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (i0 + u < we && c0 + (32 * h + lane) * N < D) x[u][h].load(src + (32 * h + lane) * N);
+            }
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (i0 + u < we && c0 + (32 * h + lane) * N < D) x[u][h].add_to(g[h]);
+        }
         __syncthreads();
 #pragma unroll
-        for (int h = 0; h < kSlice / (32 * N); ++h) {
-            const int64_t c = c0 + (32 * h + lane) * N;
-            float g[N] = {};
-            if (c < D)
-                add_rows<8>(dY + c, we - wa, [&](int32_t i) { return o.order[wa + i]; }, D, g);
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int k = 0; k < N; ++k) sh[warp][(32 * h + lane) * N + k] = g[k];
-        }
+            for (int k = 0; k < N; ++k) sh[warp][(32 * h + lane) * N + k] = g[h][k];
         __syncthreads();
         float x = 0.0f;
 #pragma unroll
@@ -559,36 +622,25 @@ __global__ void __launch_bounds__(kThreads)
 {
     constexpr int N = VEC ? 4 : 1;
     const int64_t width = D / N;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-    const int64_t step_places = step / width, step_columns = step - step_places * width;
     const int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    int64_t i = q / width, column = q - i * width;
-    while (i < T) {
-        const int32_t r = __ldg(o.row + i);
-        if (r < 0) return;  // past the tokens, and so is what follows
-        const int2 s = __ldg(o.seg + r);
-        if (s.x == i) {
-            const int64_t c = column * N, at = r * D + c;
-            float d[N], g[N] = {};
-            if constexpr (VEC)
-                StateIO<ST_F32>::ld4(dW, at, d);
-            else
-                d[0] = StateIO<ST_F32>::ld(dW, at);
-            row_sum<4>(dY, o, partial, piece_bits, s, D, c, g);
+    const int64_t i = q / width, c = (q - i * width) * N;
+    if (i >= T) return;
+    const int2 first = __ldg(o.at + i);
+    if (first.y == 0) return;
+    const int64_t at = first.x * D + c;
+    const int2 s = make_int2(static_cast<int32_t>(i), static_cast<int32_t>(i) + first.y);
+    float d[N], g[N] = {};
+    if constexpr (VEC)
+        StateIO<ST_F32>::ld4(dW, at, d);
+    else
+        d[0] = StateIO<ST_F32>::ld(dW, at);
+    row_sum<4>(dY, o, partial, piece_bits, s, D, c, g);
 #pragma unroll
-            for (int k = 0; k < N; ++k) d[k] = fmaf(scale, g[k], d[k]);
-            if constexpr (VEC)
-                StateIO<ST_F32>::st4(dW, at, d);
-            else
-                StateIO<ST_F32>::st(dW, at, d[0]);
-        }
-        i += step_places;
-        column += step_columns;
-        if (column >= width) {
-            column -= width;
-            ++i;
-        }
-    }
+    for (int k = 0; k < N; ++k) d[k] = fmaf(scale, g[k], d[k]);
+    if constexpr (VEC)
+        StateIO<ST_F32>::st4(dW, at, d);
+    else
+        StateIO<ST_F32>::st(dW, at, d[0]);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -666,12 +718,12 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
         const int64_t pieces = T > (int64_t{1} << bits) ? (T + (int64_t{1} << bits) - 1) >> bits : 0;
         auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
         const int64_t order_b = up(T * 4), list_b = up(T * 8), seg_b = up(V * 8);
-        e = scratch_alloc(&scratch, 2 * order_b + 2 * list_b + seg_b + 2 * pieces * D * 4, s);
+        e = scratch_alloc(&scratch, order_b + 3 * list_b + seg_b + 2 * pieces * D * 4, s);
         if (e != cudaSuccess) return e;
         uint8_t* at = static_cast<uint8_t*>(scratch);
         o.order = reinterpret_cast<int32_t*>(at);
-        o.row = reinterpret_cast<int32_t*>(at += order_b);
-        o.listA = reinterpret_cast<int2*>(at += order_b);
+        o.at = reinterpret_cast<int2*>(at += order_b);
+        o.listA = reinterpret_cast<int2*>(at += list_b);
         o.listB = reinterpret_cast<int2*>(at += list_b);
         o.seg = reinterpret_cast<int2*>(at += list_b);
         partial = reinterpret_cast<float*>(at += seg_b);
@@ -687,10 +739,11 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
     if (e == cudaSuccess) {
         const int64_t width = VEC ? D / 4 : D;
         if (what == Sum::Add) {
-            const int64_t want = (T * width + kThreads - 1) / kThreads;
-            const int blocks = static_cast<int>(want < 8LL * sms ? want : 8LL * sms);
-            forge_embedding_accumulate_kernel<G, VEC>
-                <<<blocks, kThreads, 0, s>>>(dY, T, D, scale, dW, o, bits, partial);
+            const int64_t blocks = (T * width + kThreads - 1) / kThreads;
+            if (blocks > INT32_MAX) e = cudaErrorInvalidConfiguration;
+            else
+                forge_embedding_accumulate_kernel<G, VEC><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+                    dY, T, D, scale, dW, o, bits, partial);
         } else {
             // as many turns, up to eight, as leave each SM 32 blocks
             const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);

@@ -114,11 +114,11 @@ struct Vec<float> {
         return i == 0 ? pair(__uint_as_float(u.x), __uint_as_float(u.y))
                       : pair(__uint_as_float(u.z), __uint_as_float(u.w));
     }
-    static __device__ __forceinline__ float max(const uint4& u)
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     {
-        return nan_max(nan_max(__uint_as_float(u.x), __uint_as_float(u.y)),
-                       nan_max(__uint_as_float(u.z), __uint_as_float(u.w)));
+        return __float_as_uint(nan_max(__uint_as_float(a), __uint_as_float(b)));
     }
+    static __device__ __forceinline__ float top(uint32_t a) { return __uint_as_float(a); }
 };
 template <>
 struct Vec<__nv_bfloat16> {
@@ -135,12 +135,18 @@ struct Vec<__nv_bfloat16> {
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
         return y;
     }
-    static __device__ __forceinline__ float max(const uint4& u)
+    static __device__ __forceinline__ float top(uint32_t a)
     {
-        const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
-        return nan_max(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        return nan_max(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
     }
 };
+// The largest logit of a vector, still packed; a NaN wins.
+template <typename T>
+__device__ __forceinline__ uint32_t packed_max(const uint4& u)
+{
+    using X = Vec<T>;
+    return X::max2(X::max2(u.x, u.y), X::max2(u.z, u.w));
+}
 
 // A row (or a block's part of it) as whole 16-byte vectors and the elements
 // before and after them.
@@ -252,44 +258,72 @@ __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
     return n < k ? n : k;
 }
 
+// The entries a warp holds, and the rank that the next one has to reach.
+struct Held {
+    uint64_t bound;
+    int n;
+};
+
 // Adds one entry of each lane to the warp's room where it reaches the bound.
-__device__ __forceinline__ void offer(Tops& w, int& held, uint64_t& bound, float v, int64_t column,
-                                      bool live, int k, int lane)
+__device__ __forceinline__ Held offer(Tops& w, Held h, float v, int64_t column, bool live, int k,
+                                      int lane)
 {
     const uint64_t rank = rank_of(v, column);
-    const bool pass = live && rank >= bound;
+    const bool pass = live && rank >= h.bound;
     const uint32_t all = __ballot_sync(0xffffffffu, pass);
-    if (all == 0) return;
-    if (pass) w.room[held + __popc(all & ((1u << lane) - 1u))] = rank;
-    held += __popc(all);
+    if (all == 0) return h;
+    if (pass) w.room[h.n + __popc(all & ((1u << lane) - 1u))] = rank;
+    h.n += __popc(all);
     __syncwarp();
-    if (held > kRoom - 32) {
-        held = keep_best(w.room, held, k, lane);
-        if (held == k && w.room[k - 1] > bound) bound = w.room[k - 1];
+    if (h.n > kRoom - 32) {
+        h.n = keep_best(w.room, h.n, k, lane);
+        if (h.n == k && w.room[k - 1] > h.bound) h.bound = w.room[k - 1];
     }
+    return h;
 }
 
 // Reads the noted vectors again (they are in L2 as a rule) and offers their
-// entries, 32 vectors at a time.
+// entries, 32 vectors at a time; or, where a warp had more to note than its
+// list takes, all its vectors v = first + stride i < nv.
 template <typename T>
-__device__ __noinline__ void look_into(Tops& w, int noted, int& held, uint64_t& bound,
-                                       const uint4* xv, int64_t col0, int k, int lane)
+__device__ __noinline__ Held look_into(Tops& w, int noted, Held h, const uint4* xv, int64_t col0,
+                                       int k, int lane, bool listed, int32_t first, int32_t stride,
+                                       int32_t nv)
 {
     constexpr int N = Vec<T>::N;
     __syncwarp();
-    for (int i0 = 0; i0 < noted; i0 += 32) {
-        const bool live = i0 + lane < noted;
-        const int64_t v = live ? w.list[i0 + lane] : 0;
+    for (int32_t i0 = 0; i0 < noted; i0 += 32) {
+        const int32_t v = !listed ? i0 / 32 * stride + first + lane
+                                  : (i0 + lane < noted ? w.list[i0 + lane] : nv);
+        const bool live = v < nv;
         const uint4 u = live ? __ldg(xv + v) : make_uint4(0, 0, 0, 0);
+        const float least = value_of(static_cast<uint32_t>(h.bound >> 32));
+        if (!__any_sync(0xffffffffu, live && !(Vec<T>::top(packed_max<T>(u)) < least))) continue;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             float a, b;
             split(Vec<T>::two(u, i), a, b);
-            offer(w, held, bound, a, col0 + v * N + 2 * i, live, k, lane);
-            offer(w, held, bound, b, col0 + v * N + 2 * i + 1, live, k, lane);
+            h = offer(w, h, a, col0 + static_cast<int64_t>(v) * N + 2 * i, live, k, lane);
+            h = offer(w, h, b, col0 + static_cast<int64_t>(v) * N + 2 * i + 1, live, k, lane);
         }
     }
     __syncwarp();
+    return h;
+}
+
+// The joined statistics of a group of WIDTH lanes, in every lane of it.
+template <int WIDTH>
+__device__ __forceinline__ void join_lanes(Stats& st, float c)
+{
+#pragma unroll
+    for (int o = WIDTH / 2; o > 0; o >>= 1) {
+        Stats b;
+        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        b.w = __shfl_xor_sync(0xffffffffu, st.w, o);
+        b.nan = __shfl_xor_sync(0xffffffffu, st.nan ? 1 : 0, o) != 0;
+        join(st, b, c);
+    }
 }
 
 // A row is the work of WARPS warps of a block (eight, or fewer where rows are
@@ -363,6 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     }
 
     const T* x = logits + r * p.ld;
+    const float x_t = tid == 0 && p.logprob ? load1(x, t) : 0.0f;
     const float c = p.scale * kLog2e;
     const Split sp = split_row(x, p.V);
     const int64_t per = (sp.nvec + split - 1) / split;
@@ -373,10 +408,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 
     Stats st{-INFINITY, 0.0f, 0.0f, false};
     Tops& tops = s_tops[TOP ? warp : 0];
-    int held = 0, noted = 0;       // the warp's entries and vectors
+    Held held{0, 0};               // the warp's entries
+    float bound_v = -INFINITY;     // the value of held.bound
+    int noted = 0;                 // the warp's vectors
+    bool over = false;             // there were more than the list takes
     int turn = 0;                  // times the bound was set
-    uint64_t bound = 0;            // rank that an entry has to reach
-    float bound_v = -INFINITY;     // its value
 
     auto raise = [&](float m) {  // m moves the reference of the thread's sums
         if (m > st.m) {
@@ -413,8 +449,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         sync();
         const float kth = s_kth[mine];
         const uint64_t floor = static_cast<uint64_t>(key_of(kth)) << 32;
-        if (floor > bound) {
-            bound = floor;
+        if (floor > held.bound) {
+            held.bound = floor;
             bound_v = kth;
         }
     };
@@ -432,18 +468,26 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             st.s += e;
             st.w = fmaf(e, d, st.w);
         }
-        if constexpr (TOP) offer(tops, held, bound, v, column, live, k, lane);
+        if constexpr (TOP) held = offer(tops, held, v, column, live, k, lane);
     }
 
+    // whole tiles are read without a check; the last one may end early
     const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
-    auto fetch = [&](int32_t tile, uint4 (&u)[kFlight]) {
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            const int32_t v = (tile * kFlight + f) * kThreads + tid;
-            u[f] = v < nv ? __ldcs(xv + v) : none;
-        }
-    };
+    const int32_t whole = nv / (kFlight * kThreads);
     const int32_t tiles = (nv + kFlight * kThreads - 1) / (kFlight * kThreads);
+    const uint4* at = xv + tid;
+    auto fetch = [&](int32_t tile, uint4 (&u)[kFlight]) {
+        if (tile < whole) {
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) u[f] = __ldcs(at + f * kThreads);
+        } else {
+            const int32_t left = nv - tile * kFlight * kThreads - tid;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f)
+                u[f] = f * kThreads < left ? __ldcs(at + f * kThreads) : none;
+        }
+        at += kFlight * kThreads;
+    };
     uint4 next[kFlight];
     if (tiles > 0) fetch(0, next);
     for (int32_t tile = 0; tile < tiles; ++tile) {
@@ -451,10 +495,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) u[f] = next[f];
         if (tile + 1 < tiles) fetch(tile + 1, next);
-        float vm[kFlight];
+        uint32_t pm = packed_max<T>(u[0]);
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) vm[f] = Vec<T>::max(u[f]);
-        const float tm = nan_max(nan_max(vm[0], vm[1]), nan_max(vm[2], vm[3]));
+        for (int f = 1; f < kFlight; ++f) pm = Vec<T>::max2(pm, packed_max<T>(u[f]));
+        const float tm = Vec<T>::top(pm);
         st.nan = st.nan || tm != tm;
         raise(tm);
         const float mr = st.m == -INFINITY ? 0.0f : st.m;
@@ -484,14 +528,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 #pragma unroll
                 for (int f = 0; f < kFlight; ++f) {
                     const int32_t v = (tile * kFlight + f) * kThreads + tid;
-                    const bool pass = !(vm[f] < bound_v) && v < nv;
+                    const bool pass = !(Vec<T>::top(packed_max<T>(u[f])) < bound_v) && v < nv;
                     const uint32_t all = __ballot_sync(0xffffffffu, pass);
-                    if (pass) tops.list[noted + __popc(all & ((1u << lane) - 1u))] = v;
-                    noted += __popc(all);
-                    if (noted > kList - 32) {
-                        look_into<T>(tops, noted, held, bound, xv, col0, k, lane);
-                        noted = 0;
-                        bound_v = value_of(static_cast<uint32_t>(bound >> 32));
+                    if (noted <= kList - 32) {
+                        if (pass) tops.list[noted + __popc(all & ((1u << lane) - 1u))] = v;
+                        noted += __popc(all);
+                    } else {
+                        over = over || all != 0;
                     }
                 }
             }
@@ -499,34 +542,25 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     }
     if constexpr (TOP) {
         if (tiles > 1) tighten();
-        look_into<T>(tops, noted, held, bound, xv, col0, k, lane);
+        held = look_into<T>(tops, over ? (nv + kThreads - 1) / kThreads * 32 : noted, held, xv, col0, k,
+                            lane, !over, tid - lane, kThreads, nv);
     }
 
     // lanes, then warps
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats b;
-        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        b.w = __shfl_xor_sync(0xffffffffu, st.w, o);
-        b.nan = __shfl_xor_sync(0xffffffffu, st.nan ? 1 : 0, o) != 0;
-        join(st, b, c);
-    }
+    join_lanes<32>(st, c);
     if (lane == 0) {
         s_stats[warp] = st;
-        s_held[warp] = held;
+        s_held[warp] = held.n;
     }
     sync();
-    if (tid == 0) {
-        st = s_stats[warp];
-        for (int w = 1; w < WARPS; ++w) join(st, s_stats[warp + w], c);
-        s_row[mine] = st;
+    if (rwarp == 0) {
+        st = s_stats[warp + lane % WARPS];
+        join_lanes<WARPS>(st, c);
+        if (lane == 0) s_row[mine] = st;
     }
     if constexpr (TOP) {
         // the best of the row's warps: an entry's place is the number of better ones
-        int n = 0;
-        for (int w = 0; w < WARPS; ++w) n += s_held[mine * WARPS + w];
-        for (int e = lane; e < held; e += 32) {
+        for (int e = lane; e < held.n; e += 32) {
             const uint64_t own = tops.room[e];
             int rank = 0;
             for (int w = 0; w < WARPS; ++w) {
@@ -536,7 +570,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             }
             if (rank < k) s_best[mine][rank] = own;
         }
-        if (tid == 0) s_n[mine] = n < k ? n : k;
+        if (rwarp == WARPS - 1) {
+            const int n = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_held[mine * WARPS + lane] : 0);
+            if (lane == 0) s_n[mine] = n < k ? n : k;
+        }
     }
     sync();
 
@@ -545,12 +582,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         if (split > 1) {
             cluster_barrier();
             if (part == 0) {
-                if (threadIdx.x == 0)
-                    for (int q = 1; q < split; ++q) {
-                        const Stats* o = remote(&s_row[0], q);
-                        const Stats b{o->m, o->s, o->w, o->nan};
-                        join(s_row[0], b, c);
-                    }
+                if (warp == 0) {  // a lane for each block
+                    const Stats* o = remote(&s_row[0], lane % split);
+                    st = *o;
+                    if (lane >= split) st = Stats{-INFINITY, 0.0f, 0.0f, false};
+                    join_lanes<8>(st, c);
+                    if (lane == 0) s_stats[0] = st;
+                }
                 if constexpr (TOP) {
                     // every block's best, 32 to a warp's room, ranked again
                     static_assert(kWarps * kMaxTop <= kWarps * kRoom);
@@ -575,7 +613,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             if (part != 0) return;
         }
 
-    const Stats all = s_row[mine];
+    const Stats all = split > 1 ? s_stats[0] : s_row[mine];
     const bool bad = all.nan || all.m == INFINITY;
     const bool empty = !bad && all.m == -INFINITY;
     // relative to the largest logit, so that near entries keep their digits
@@ -586,7 +624,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         return fmaf(p.scale, v - all.m, -ln_s);
     };
     if (tid == 0) {
-        if (p.logprob) p.logprob[r] = logprob_of(load1(x, t));
+        if (p.logprob) p.logprob[r] = logprob_of(x_t);
         if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : fmaf(p.scale, all.m, ln_s));
         if (p.entropy) p.entropy[r] = bad ? NAN : (empty ? 0.0f : ln_s - kLn2 * all.w / all.s);
     }
