@@ -435,7 +435,8 @@ FORGE_API forge_status forge_token_logprob_grad(
  *   W       device [V, D] of w_dtype (FORGE_BF16 or FORGE_F32).
  *   Y       device [T, D] of y_dtype (FORGE_BF16, the fp32 product rounded once
  *           to nearest even, or FORGE_F32), written.
- * W and Y of any width and alignment.  Allocates nothing.  T = 0 does nothing.
+ * W and Y of any width and alignment; T <= 2^30.  Allocates nothing.  T = 0
+ * does nothing.
  */
 FORGE_API forge_status forge_embedding(const void* ids, forge_dtype id_dtype, int64_t T,
                                        const void* W, forge_dtype w_dtype, int64_t V, int64_t D,
@@ -447,7 +448,7 @@ FORGE_API forge_status forge_embedding(const void* ids, forge_dtype id_dtype, in
  *   dW[r] = scale * sum over {t : ids[t] = r} of dY[t]   (+ dW[r] if accumulate)
  *   dY      device [T, D] of dy_dtype (FORGE_BF16 or FORGE_F32); rows of padding
  *           tokens are not read.
- *   ids     as forge_embedding's.
+ *   ids     as forge_embedding's; T <= 2^30.
  *   dW      device fp32 [V, D].  accumulate = 0: written whole, rows without a
  *           token as zeros.  accumulate != 0: added to; rows without a token are
  *           neither read nor written.

@@ -189,6 +189,7 @@ struct Order {
     int2* seg;
     int2* listA;
     int2* listB;
+    int32_t later;  // rows of `partial` in front of those of pieces that go on
 };
 
 constexpr int kIdFlight = 8;  // loads of ids in flight per lane
@@ -420,99 +421,149 @@ __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int
     if (n - i >= 1) add_batch<1>(column, i, of, D, g);
 }
 
-// A row with more than P = 2^piece_bits tokens (a frequent token, or one that
-// fills the batch) is summed in pieces: its places are cut at the multiples
-// of P, and a block of this kernel adds 256 columns of one piece's tokens,
-// its warps a part each, into a row of `partial`.  Within the P places b P ..
-// there are at most two such pieces: one of a row that goes on from the places
-// before (slot 2 b) and one of a row that starts here (slot 2 b + 1).
+// Rows with more than kShort tokens (a vocabulary's frequent tokens, or one
+// that fills the batch) are summed beforehand, so that no thread of the kernels
+// below adds more than kShort rows: their places are cut into pieces at the
+// multiples of kPiece, and a warp adds 256 columns of a piece into a row of
+// `partial`: row a / kShort for the piece with which a row starts at place a
+// (the next such start is more than kShort places away), row later + a / kPiece
+// for one that goes on at a.  Rows of more than kMany pieces are then joined
+// into their first piece's row by another kernel.
+constexpr int kShort = 16;
+constexpr int kPiece = 32;
+constexpr int kMany = 16;
 constexpr int kSlice = 256;
+
+__device__ __forceinline__ int32_t pieces_of(int32_t first, int32_t end)
+{
+    return (end - 1) / kPiece - first / kPiece + 1;
+}
+
+// One warp per (kPiece places, slice): the pieces that start among these
+// places, one after the other, are at most kPiece tokens in all.
 template <typename G, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    forge_embedding_pieces_kernel(const G* dY, int64_t T, int64_t D, Order o, int32_t piece_bits,
-                                  float* partial)
+    forge_embedding_pieces_kernel(const G* dY, int64_t T, int64_t D, Order o, float* partial)
 {
-    constexpr int kWarps = kThreads / 32;
+    static_assert(kPiece == 32);
     constexpr int N = VEC ? 4 : 1;
     constexpr int H = kSlice / (32 * N);                        // vectors of a lane
     constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;      // in flight
-    __shared__ float sh[kWarps][kSlice];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t slices = static_cast<int32_t>((D + kSlice - 1) / kSlice);
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x % slices) * kSlice;
-    const int32_t b = blockIdx.x / slices, P = 1 << piece_bits;
-    const int64_t p0 = static_cast<int64_t>(b) << piece_bits;
-    const int64_t p1 = p0 + P < T ? p0 + P : T;
-    int32_t row = -1;
-    for (int which = 0; which < 2; ++which) {
-        // the last place of the block may be past the tokens: then its row is
-        // that of the last token before, if that one is in the block at all
-        int32_t r = o.at[which ? p1 - 1 : p0].x;
-        if (r < 0) {
-            if (which == 0) return;
-            int64_t a = p0, e = p1 - 1;  // at[a].x >= 0, at[e].x < 0
-            while (e - a > 1) {
-                const int64_t m = (a + e) >> 1;
-                if (o.at[m].x >= 0)
-                    a = m;
-                else
-                    e = m;
-            }
-            r = o.at[a].x;
-        }
-        if (r == row) break;
-        row = r;
-        const int2 s = o.seg[r];
-        if (s.y - s.x <= P) continue;
-        const int32_t a = s.x > p0 ? s.x : static_cast<int32_t>(p0);
-        const int32_t e = s.y < p1 ? s.y : static_cast<int32_t>(p1);
-        const int32_t per = (e - a + kWarps - 1) / kWarps;
-        const int32_t wa = a + warp * per < e ? a + warp * per : e;
-        const int32_t we = wa + per < e ? wa + per : e;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int64_t c0 = unit % slices * kSlice;
+    const int64_t p0 = unit / slices * kPiece;
+    if (p0 >= T) return;
+    const int32_t place = static_cast<int32_t>(p0) + lane;
+    const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+    const int32_t token = place < T ? __ldg(o.order + place) : 0;
+    bool start = here.y > kShort, on = false;
+    int32_t end = lane + here.y;
+    if (lane == 0 && here.y == 0 && here.x >= 0) {  // a row that goes on from before
+        const int2 s = __ldg(o.seg + here.x);
+        on = start = s.y - s.x > kShort;
+        end = s.y - place;
+    }
+    on = __shfl_sync(0xffffffffu, on ? 1 : 0, 0) != 0;
+    end = end < kPiece ? end : kPiece;
+    for (uint32_t left = __ballot_sync(0xffffffffu, start); left != 0; left &= left - 1) {
+        const int a = __ffs(left) - 1, e = __shfl_sync(0xffffffffu, end, a);
         float g[H][N] = {};
-        for (int32_t i0 = wa; i0 < we; i0 += kTokens) {
+        for (int i0 = a; i0 < e; i0 += kTokens) {
             Raw<G, N> x[kTokens][H];
 #pragma unroll
             for (int u = 0; u < kTokens; ++u) {
-                const G* src = dY + c0 + static_cast<int64_t>(o.order[i0 + u < we ? i0 + u : wa]) * D;
+                const G* src = dY + c0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, token, (i0 + u) & 31)) * D;
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    if (i0 + u < we && c0 + (32 * h + lane) * N < D) x[u][h].load(src + (32 * h + lane) * N);
+                    if (i0 + u < e && c0 + (32 * h + lane) * N < D) x[u][h].load(src + (32 * h + lane) * N);
             }
 #pragma unroll
             for (int u = 0; u < kTokens; ++u)
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    if (i0 + u < we && c0 + (32 * h + lane) * N < D) x[u][h].add_to(g[h]);
+                    if (i0 + u < e && c0 + (32 * h + lane) * N < D) x[u][h].add_to(g[h]);
         }
-        __syncthreads();
+        const int32_t slot = a == 0 && on ? o.later + static_cast<int32_t>(p0 / kPiece)
+                                          : static_cast<int32_t>((p0 + a) / kShort);
+        float* dst = partial + static_cast<int64_t>(slot) * D + c0;
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int k = 0; k < N; ++k) sh[warp][(32 * h + lane) * N + k] = g[h][k];
-        __syncthreads();
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) x += sh[w][threadIdx.x];
-        const int64_t slot = 2 * static_cast<int64_t>(b) + (s.x >= p0 ? 1 : 0);
-        if (c0 + threadIdx.x < D) partial[slot * D + c0 + threadIdx.x] = x;
+        for (int h = 0; h < H; ++h) {
+            const int c = (32 * h + lane) * N;
+            if (c0 + c >= D) continue;
+            if constexpr (VEC)
+                *reinterpret_cast<float4*>(dst + c) = make_float4(g[h][0], g[h][1], g[h][2], g[h][3]);
+            else
+                dst[c] = g[h][0];
+        }
     }
+}
+
+// One block per (kJoin places, slice): at most one row of more than kMany
+// pieces, (kMany - 1) kPiece places or more, starts there.  The warps add a
+// part of its pieces each.
+constexpr int kJoin = 256;
+static_assert(kJoin < (kMany - 1) * kPiece);
+__global__ void __launch_bounds__(kThreads)
+    forge_embedding_join_kernel(int64_t T, int64_t D, Order o, float* partial)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int32_t s_first, s_end;
+    __shared__ float sh[kWarps][kSlice];
+    const int32_t slices = static_cast<int32_t>((D + kSlice - 1) / kSlice);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % slices) * kSlice;
+    const int32_t p0 = blockIdx.x / slices * kJoin;
+    if (threadIdx.x == 0) s_end = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoin / kThreads; ++i) {
+        const int32_t a = p0 + i * kThreads + threadIdx.x;
+        const int32_t n = a < T ? __ldg(o.at + a).y : 0;
+        if (n > kShort && pieces_of(a, a + n) > kMany) {
+            s_first = a;
+            s_end = a + n;
+        }
+    }
+    __syncthreads();
+    if (s_end == 0) return;
+    const int32_t b0 = s_first / kPiece, n = pieces_of(s_first, s_end);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t per = (n + kWarps - 1) / kWarps;
+    const int32_t i0 = warp * per < n ? warp * per : n, i1 = i0 + per < n ? i0 + per : n;
+#pragma unroll
+    for (int h = 0; h < kSlice / 32; ++h) {
+        const int c = 32 * h + lane;
+        float g[1] = {0.0f};
+        if (c0 + c < D)
+            add_rows<8>(
+                static_cast<const float*>(partial) + c0 + c, i1 - i0,
+                [&](int32_t i) {
+                    return i0 + i == 0 ? s_first / kShort : o.later + b0 + i0 + i;
+                },
+                D, g);
+        sh[warp][c] = g[0];
+    }
+    __syncthreads();  // every piece has been read
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x += sh[w][threadIdx.x];
+    if (c0 + threadIdx.x < D) partial[static_cast<int64_t>(s_first / kShort) * D + c0 + threadIdx.x] = x;
 }
 
 // The sum over a row's tokens at one column (vector): token by token, or
 // piece by piece.
 template <int F, int N, typename G>
-__device__ __forceinline__ void row_sum(const G* dY, const Order& o, const float* partial,
-                                        int32_t piece_bits, int2 s, int64_t D, int64_t c, float (&g)[N])
+__device__ __forceinline__ void row_sum(const G* dY, const Order& o, const float* partial, int2 s,
+                                        int64_t D, int64_t c, float (&g)[N])
 {
-    const int32_t n = s.y - s.x;
-    if (n <= (1 << piece_bits)) {
-        add_rows<F>(dY + c, n, [&](int32_t i) { return __ldg(o.order + s.x + i); }, D, g);
+    if (s.y - s.x <= kShort) {
+        add_rows<F>(dY + c, s.y - s.x, [&](int32_t i) { return __ldg(o.order + s.x + i); }, D, g);
     } else {
-        const int32_t b0 = s.x >> piece_bits, b1 = (s.y - 1) >> piece_bits;
+        const int32_t n = pieces_of(s.x, s.y), b0 = s.x / kPiece;
         add_rows<F>(
-            partial + c, b1 - b0 + 1,
-            [&](int32_t i) { return 2 * (b0 + i) + (i == 0 ? 1 : 0); }, D, g);
+            partial + c, n > kMany ? 1 : n,
+            [&](int32_t i) { return i == 0 ? s.x / kShort : o.later + b0 + i; }, D, g);
     }
 }
 
@@ -531,10 +582,9 @@ constexpr int kUnits = VEC ? 2 : 4;
 // frequent tokens, which a vocabulary has in front, are not the last to end.
 // Bound by HBM: dW written, or W, m, v read and written, once.
 template <typename G, int MODE, int ST, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, MODE == SUM_ADAMW ? 4 : 5)
     forge_embedding_grad_kernel(const G* dY, int32_t V, int32_t D, float scale, float* dW, Order o,
-                                int32_t piece_bits, const float* partial, int32_t turns,
-                                const Params p)
+                                const float* partial, int32_t turns, const Params p)
 {
     constexpr int N = VEC ? 4 : 1;
     constexpr int U = kUnits<VEC>;
@@ -576,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int u = 0; u < U; ++u) {
             float x[N] = {};
             if (s[u].y > s[u].x)
-                row_sum<F>(dY, o, partial, piece_bits, s[u], D, column[u] * N, x);
+                row_sum<F>(dY, o, partial, s[u], D, column[u] * N, x);
 #pragma unroll
             for (int k = 0; k < N; ++k) g[u * N + k] = x[k] * scale;
         }
@@ -613,34 +663,65 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// dW += the sums, over the rows that have a token only: flat over (place,
-// column); the first place of a row takes it.
+// dW += the sums, over the rows that have a token only: flat over (place, four
+// columns); the first place of a row takes it.
 template <typename G, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_accumulate_kernel(const G* dY, int64_t T, int64_t D, float scale, float* dW,
-                                      Order o, int32_t piece_bits, const float* partial)
+                                      Order o, const float* partial)
 {
-    constexpr int N = VEC ? 4 : 1;
-    const int64_t width = D / N;
+    // four columns of a lane: side by side, or (single elements) 32 apart
+    const int64_t width = (D + 127) / 128 * 32;
     const int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t i = q / width, c = (q - i * width) * N;
+    const int64_t i = q / width;
     if (i >= T) return;
     const int2 first = __ldg(o.at + i);
     if (first.y == 0) return;
-    const int64_t at = first.x * D + c;
+    const int64_t part = q - i * width;
     const int2 s = make_int2(static_cast<int32_t>(i), static_cast<int32_t>(i) + first.y);
-    float d[N], g[N] = {};
-    if constexpr (VEC)
-        StateIO<ST_F32>::ld4(dW, at, d);
-    else
-        d[0] = StateIO<ST_F32>::ld(dW, at);
-    row_sum<4>(dY, o, partial, piece_bits, s, D, c, g);
+    const int64_t row = first.x * D;
+    if constexpr (VEC) {
+        const int64_t c = part * 4;
+        if (c >= D) return;
+        float d[4], g[4] = {};
+        StateIO<ST_F32>::ld4(dW, row + c, d);
+        row_sum<4>(dY, o, partial, s, D, c, g);
 #pragma unroll
-    for (int k = 0; k < N; ++k) d[k] = fmaf(scale, g[k], d[k]);
-    if constexpr (VEC)
-        StateIO<ST_F32>::st4(dW, at, d);
-    else
-        StateIO<ST_F32>::st(dW, at, d[0]);
+        for (int k = 0; k < 4; ++k) d[k] = fmaf(scale, g[k], d[k]);
+        StateIO<ST_F32>::st4(dW, row + c, d);
+    } else {
+        const int64_t c0 = part / 32 * 128 + part % 32;
+        float d[4], g[4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c0 + 32 * k < D) d[k] = StateIO<ST_F32>::ld(dW, row + c0 + 32 * k);
+        auto add = [&](auto* base, int32_t n, auto of) {
+            for (int32_t j = 0; j < n; j += 4) {
+                float x[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int64_t r = j + u < n ? of(j + u) : -1;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[u][k] = r >= 0 && c0 + 32 * k < D ? load1(base, r * D + c0 + 32 * k) : 0.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) g[k] += x[u][k];
+            }
+        };
+        if (first.y <= kShort) {
+            add(dY, first.y, [&](int32_t j) { return __ldg(o.order + s.x + j); });
+        } else {
+            const int32_t n = pieces_of(s.x, s.y), b0 = s.x / kPiece;
+            add(partial, n > kMany ? 1 : n,
+                [&](int32_t j) { return j == 0 ? s.x / kShort : o.later + b0 + j; });
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c0 + 32 * k < D) StateIO<ST_F32>::st(dW, row + c0 + 32 * k, fmaf(scale, g[k], d[k]));
+    }
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -650,7 +731,7 @@ bool is_id(forge_dtype t) { return t == FORGE_I32 || t == FORGE_I64; }
 
 forge_status check_sizes(int64_t T, int64_t V, int64_t D, float scale)
 {
-    if (T < 0 || V < 1 || D < 1 || T > INT32_MAX || V > INT32_MAX || D > INT32_MAX)
+    if (T < 0 || V < 1 || D < 1 || T > (1 << 30) || V > INT32_MAX || D > INT32_MAX)
         return FORGE_ERR_INVALID_ARG;
     return std::isfinite(scale) ? FORGE_OK : FORGE_ERR_INVALID_ARG;
 }
@@ -661,16 +742,6 @@ forge_status check_grad(const void* dY, forge_dtype dy_dtype, const void* ids,
     if (T > 0 && (!dY || !ids)) return FORGE_ERR_INVALID_ARG;
     if (!is_float(dy_dtype) || !is_id(id_dtype)) return FORGE_ERR_UNSUPPORTED_DTYPE;
     return FORGE_OK;
-}
-
-// Tokens of a row summed by one warp; longer rows in pieces of as many.  A
-// warp adds P rows one after the other, and T / P partial sums where one
-// token fills the batch, so P grows with the square root of T.
-int32_t piece_bits_of(int64_t T)
-{
-    int32_t bits = 6;
-    while ((int64_t{4} << (2 * bits)) < T) ++bits;
-    return bits;
 }
 
 // The order kernel's shared memory, allowed once per device.
@@ -709,16 +780,16 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
                         int sms, cudaStream_t s)
 {
     if (what == Sum::Add && T == 0) return cudaSuccess;
-    const int32_t bits = piece_bits_of(T);
     Order o{};
     float* partial = nullptr;
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
-        const int64_t pieces = T > (int64_t{1} << bits) ? (T + (int64_t{1} << bits) - 1) >> bits : 0;
+        o.later = static_cast<int32_t>((T + kShort - 1) / kShort);
+        const int64_t slots = T > kShort ? o.later + (T + kPiece - 1) / kPiece : 0;
         auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
         const int64_t order_b = up(T * 4), list_b = up(T * 8), seg_b = up(V * 8);
-        e = scratch_alloc(&scratch, order_b + 3 * list_b + seg_b + 2 * pieces * D * 4, s);
+        e = scratch_alloc(&scratch, order_b + 3 * list_b + seg_b + slots * D * 4, s);
         if (e != cudaSuccess) return e;
         uint8_t* at = static_cast<uint8_t*>(scratch);
         o.order = reinterpret_cast<int32_t*>(at);
@@ -729,21 +800,30 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
         partial = reinterpret_cast<float*>(at += seg_b);
         e = wide ? order_tokens<int64_t>(ids, T, V, o, p.status, s)
                  : order_tokens<int32_t>(ids, T, V, o, p.status, s);
-        if (e == cudaSuccess && pieces > 0) {
-            const int64_t blocks = pieces * ((D + kSlice - 1) / kSlice);
-            forge_embedding_pieces_kernel<G, VEC>
-                <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(dY, T, D, o, bits, partial);
-            e = cudaGetLastError();
+        const int64_t slices = (D + kSlice - 1) / kSlice;
+        if (e == cudaSuccess && T > kShort) {
+            const int64_t units = (T + kPiece - 1) / kPiece * slices;
+            const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
+            if (blocks > INT32_MAX) e = cudaErrorInvalidConfiguration;
+            else
+                forge_embedding_pieces_kernel<G, VEC>
+                    <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(dY, T, D, o, partial);
         }
+        if (e == cudaSuccess && T > (kMany - 1) * kPiece) {
+            const int64_t blocks = (T + kJoin - 1) / kJoin * slices;
+            forge_embedding_join_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(T, D, o,
+                                                                                         partial);
+        }
+        if (e == cudaSuccess) e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
         const int64_t width = VEC ? D / 4 : D;
         if (what == Sum::Add) {
-            const int64_t blocks = (T * width + kThreads - 1) / kThreads;
+            const int64_t blocks = (T * ((D + 127) / 128 * 32) + kThreads - 1) / kThreads;
             if (blocks > INT32_MAX) e = cudaErrorInvalidConfiguration;
             else
                 forge_embedding_accumulate_kernel<G, VEC><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-                    dY, T, D, scale, dW, o, bits, partial);
+                    dY, T, D, scale, dW, o, partial);
         } else {
             // as many turns, up to eight, as leave each SM 32 blocks
             const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);
@@ -753,7 +833,7 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
             const int blocks = static_cast<int>((tiles + turns - 1) / turns);
             auto go = [&](auto kernel) {
                 kernel<<<blocks, kThreads, 0, s>>>(dY, static_cast<int32_t>(V), static_cast<int32_t>(D),
-                                                   scale, dW, o, bits, partial,
+                                                   scale, dW, o, partial,
                                                    static_cast<int32_t>(turns), p);
             };
             if (what == Sum::Store)

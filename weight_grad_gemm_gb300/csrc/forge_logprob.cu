@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     __shared__ Stats s_stats[kWarps];
     __shared__ Stats s_row[kRows];
     __shared__ uint64_t s_best[TOP ? kRows : 1][kMaxTop];
-    __shared__ int s_n[kRows];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int mine = warp / WARPS;             // the row's place in the block
@@ -408,6 +407,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 
     Stats st{-INFINITY, 0.0f, 0.0f, false};
     Tops& tops = s_tops[TOP ? warp : 0];
+    if constexpr (TOP)
+        if (rwarp == 0) s_best[mine][lane] = 0;  // no entry
     Held held{0, 0};               // the warp's entries
     float bound_v = -INFINITY;     // the value of held.bound
     int noted = 0;                 // the warp's vectors
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         st.w += a + b;
 
         if constexpr (TOP) {
-            if (tile == 0 || tile == 3) tighten();
+            if (tile == 0 || (tile == 3 && tiles > 8)) tighten();
             if (__any_sync(0xffffffffu, !(tm < bound_v))) {
 #pragma unroll
                 for (int f = 0; f < kFlight; ++f) {
@@ -570,10 +571,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             }
             if (rank < k) s_best[mine][rank] = own;
         }
-        if (rwarp == WARPS - 1) {
-            const int n = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_held[mine * WARPS + lane] : 0);
-            if (lane == 0) s_n[mine] = n < k ? n : k;
-        }
     }
     sync();
 
@@ -590,21 +587,23 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
                     if (lane == 0) s_stats[0] = st;
                 }
                 if constexpr (TOP) {
-                    // every block's best, 32 to a warp's room, ranked again
-                    static_assert(kWarps * kMaxTop <= kWarps * kRoom);
-                    if (warp < split) {
-                        const int nq = *remote(&s_n[0], warp);
-                        const uint64_t* best = remote(&s_best[0][0], warp);
-                        if (lane < nq) tops.room[lane] = best[lane];
-                        if (lane == 0) s_held[warp] = nq;
-                    }
+                    // a warp for each block's best, which are in order: an entry's place
+                    // is its own plus those of the better ones in the other lists
+                    if (warp < split) tops.room[lane] = remote(&s_best[0][0], warp)[lane];
                     __syncthreads();
-                    if (warp < split && lane < s_held[warp]) {
+                    if (warp < split) {
                         const uint64_t own = tops.room[lane];
-                        int rank = 0;
-                        for (int w = 0; w < split; ++w)
-                            for (int j = 0; j < s_held[w]; ++j) rank += s_tops[w].room[j] > own;
-                        if (rank < k) s_best[0][rank] = own;
+                        int rank = lane;
+                        for (int w = 0; w < split; ++w) {
+                            if (w == warp) continue;
+                            int better = 0;
+#pragma unroll
+                            for (int b = kMaxTop / 2; b > 0; b >>= 1)
+                                if (s_tops[w].room[better + b - 1] > own) better += b;
+                            if (s_tops[w].room[better] > own) ++better;
+                            rank += better;
+                        }
+                        if (own != 0 && rank < k) s_best[0][rank] = own;
                     }
                 }
                 __syncthreads();
@@ -780,9 +779,11 @@ template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
-    if (nvec <= 256) return launch_forward<T, 1>(x, p, 1, s);
-    if (nvec <= 1024) return launch_forward<T, 2>(x, p, 1, s);
-    if (const char* e = getenv("FORGE_LP_W"); e && atoi(e) == 4) return launch_forward<T, 4>(x, p, 1, s);
+    const char* e = getenv("FORGE_LP_W");
+    const int w = e ? atoi(e) : nvec <= 256 ? 1 : nvec <= 1024 ? 2 : p.R >= 12 * sms ? 4 : 8;
+    if (w == 1) return launch_forward<T, 1>(x, p, 1, s);
+    if (w == 2) return launch_forward<T, 2>(x, p, 1, s);
+    if (w == 4) return launch_forward<T, 4>(x, p, 1, s);
     int split = 1;
     while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
     return launch_forward<T, 8>(x, p, split, s);
