@@ -203,38 +203,39 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     __shared__ uint32_t s_own[kOrderWarps], s_less[kOrderWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t before = (1u << lane) - 1u;
-    const int32_t cls = blockIdx.x;
+    const uint32_t cls = blockIdx.x;
 
-    // count, this warp's ids [lo, hi)
+    // count, this warp's ids [lo, hi); a row is held in 32 bits, kNoRow for
+    // padding and for ids past the vocabulary
+    constexpr uint32_t kNoRow = 0xFFFFFFFFu;
     const int64_t chunk = (T + kOrderThreads - 1) / kOrderThreads * 32;
     const int64_t lo = warp * chunk, hi = lo + chunk < T ? lo + chunk : T;
-    auto fetch = [&](int64_t i0, int32_t (&r)[kIdFlight], bool& bad) {
+    const uint32_t rows = static_cast<uint32_t>(V);
+    auto fetch = [&](int64_t i0, uint32_t (&r)[kIdFlight]) {
         ID id[kIdFlight];
+        const int32_t left = static_cast<int32_t>(hi - i0 < 32 * kIdFlight ? hi - i0 : 32 * kIdFlight) - lane;
+#pragma unroll
+        for (int u = 0; u < kIdFlight; ++u)
+            id[u] = 32 * u < left ? __ldg(ids + i0 + 32 * u + lane) : static_cast<ID>(-1);
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            const int64_t i = i0 + 32 * u + lane;
-            id[u] = i < hi ? __ldg(ids + i) : static_cast<ID>(-1);
-        }
-#pragma unroll
-        for (int u = 0; u < kIdFlight; ++u) {
-            const bool past = id[u] >= V;
-            bad = bad || past;
-            r[u] = past || id[u] < 0 ? -1 : static_cast<int32_t>(id[u]);
+            // a negative id is a large one without its sign
+            const std::make_unsigned_t<ID> x = id[u];
+            r[u] = x < rows ? static_cast<uint32_t>(x) : kNoRow;
+            if (cls == 0 && id[u] >= V) bad_id(status);
         }
     };
     uint32_t own = 0, less = 0;
-    bool bad = false;
     for (int64_t i0 = lo; i0 < hi; i0 += 32 * kIdFlight) {
-        int32_t r[kIdFlight];
-        fetch(i0, r, bad);
+        uint32_t r[kIdFlight];
+        fetch(i0, r);
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            const int32_t c = r[u] & (kClasses - 1);
-            own += r[u] >= 0 && c == cls;
-            less += r[u] >= 0 && c < cls;
+            const uint32_t c = r[u] == kNoRow ? kClasses : r[u] & (kClasses - 1);
+            own += c == cls;
+            less += c < cls;
         }
     }
-    if (bad && cls == 0) bad_id(status);
     own = __reduce_add_sync(0xffffffffu, own);
     less = __reduce_add_sync(0xffffffffu, less);
     if (lane == 0) {
@@ -261,12 +262,13 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     int2* src = shared ? s_list : o.listA + base;
     int2* dst = shared ? s_list + kOrderShared : o.listB + base;
     for (int64_t i0 = lo; i0 < hi; i0 += 32 * kIdFlight) {
-        int32_t r[kIdFlight];
-        fetch(i0, r, bad);
+        uint32_t r[kIdFlight];
+        fetch(i0, r);
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            const bool mine = r[u] >= 0 && (r[u] & (kClasses - 1)) == cls;
+            const bool mine = r[u] != kNoRow && (r[u] & (kClasses - 1)) == cls;
             const uint32_t all = __ballot_sync(0xffffffffu, mine);
+            if (all == 0) continue;
             if (mine)
                 src[at + __popc(all & before)] =
                     make_int2(r[u] >> kClassBits, static_cast<int32_t>(i0 + 32 * u + lane));
@@ -421,156 +423,210 @@ __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int
     if (n - i >= 1) add_batch<1>(column, i, of, D, g);
 }
 
-// Rows with more than kShort tokens (a vocabulary's frequent tokens, or one
-// that fills the batch) are summed beforehand, so that no thread of the kernels
-// below adds more than kShort rows: their places are cut into pieces at the
-// multiples of kPiece, and a warp adds 256 columns of a piece into a row of
-// `partial`: row a / kShort for the piece with which a row starts at place a
-// (the next such start is more than kShort places away), row later + a / kPiece
-// for one that goes on at a.  Rows of more than kMany pieces are then joined
-// into their first piece's row by another kernel.
+// How a row's tokens are added, by their number n:
+//   n <= kShort   one thread a column (four), one token after the other;
+//   n <= kMedium  (a vocabulary's frequent tokens) one block for 256 columns,
+//                 its warps a part of the tokens each;
+//   else          (a token that fills the batch) in pieces: the row's places
+//                 are cut at the multiples of kPiece, and a warp adds 256
+//                 columns of a piece into a row of `partial`: row a / kMedium
+//                 for the piece with which a row starts at place a (the next
+//                 such start is more than kMedium places away), row later +
+//                 a / kPiece for one that goes on at a.  A last kernel joins
+//                 the pieces; it is launched where a batch can need it.
 constexpr int kShort = 16;
-constexpr int kPiece = 32;
-constexpr int kMany = 16;
+constexpr int kMedium = 2048;
+constexpr int kPiece = 128;
 constexpr int kSlice = 256;
 
-__device__ __forceinline__ int32_t pieces_of(int32_t first, int32_t end)
-{
-    return (end - 1) / kPiece - first / kPiece + 1;
-}
+// What becomes of a row's sum: dW written, dW added to, or the AdamW step.
+enum Sum { SUM_STORE = 0, SUM_ADD = 1, SUM_ADAMW = 2 };
 
-// One warp per (kPiece places, slice): the pieces that start among these
-// places, one after the other, are at most kPiece tokens in all.
-template <typename G, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    forge_embedding_pieces_kernel(const G* dY, int64_t T, int64_t D, Order o, float* partial)
-{
-    static_assert(kPiece == 32);
-    constexpr int N = VEC ? 4 : 1;
-    constexpr int H = kSlice / (32 * N);                        // vectors of a lane
-    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;      // in flight
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t slices = (D + kSlice - 1) / kSlice;
-    const int64_t c0 = unit % slices * kSlice;
-    const int64_t p0 = unit / slices * kPiece;
-    if (p0 >= T) return;
-    const int32_t place = static_cast<int32_t>(p0) + lane;
-    const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
-    const int32_t token = place < T ? __ldg(o.order + place) : 0;
-    bool start = here.y > kShort, on = false;
-    int32_t end = lane + here.y;
-    if (lane == 0 && here.y == 0 && here.x >= 0) {  // a row that goes on from before
-        const int2 s = __ldg(o.seg + here.x);
-        on = start = s.y - s.x > kShort;
-        end = s.y - place;
-    }
-    on = __shfl_sync(0xffffffffu, on ? 1 : 0, 0) != 0;
-    end = end < kPiece ? end : kPiece;
-    for (uint32_t left = __ballot_sync(0xffffffffu, start); left != 0; left &= left - 1) {
-        const int a = __ffs(left) - 1, e = __shfl_sync(0xffffffffu, end, a);
-        float g[H][N] = {};
-        for (int i0 = a; i0 < e; i0 += kTokens) {
-            Raw<G, N> x[kTokens][H];
+// A warp's part of a row: H vectors of N columns a lane, 32 N columns apart,
+// `width` columns from c0 on; the columns past D are left out.
+template <bool VEC, int WIDTH>
+struct Part {
+    static constexpr int N = VEC ? 4 : 1;
+    static constexpr int H = WIDTH / (32 * N);
+    int64_t c0, D;
+    int lane;
+    __device__ __forceinline__ int column(int h) const { return (32 * h + lane) * N; }
+    __device__ __forceinline__ bool has(int h) const { return c0 + column(h) < D; }
+    // g += n rows of a [*, D] array, the i-th being row of(i), in that order, K in flight
+    template <int K, typename G, typename ROW>
+    __device__ __forceinline__ void add_rows(const G* base, int32_t n, ROW of, float (&g)[H][N]) const
+    {
+        for (int32_t i0 = 0; i0 < n; i0 += K) {
+            Raw<G, N> x[K][H];
 #pragma unroll
-            for (int u = 0; u < kTokens; ++u) {
-                const G* src = dY + c0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, token, (i0 + u) & 31)) * D;
+            for (int u = 0; u < K; ++u) {
+                const G* src = base + c0 + static_cast<int64_t>(of(i0 + u)) * D;
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    if (i0 + u < e && c0 + (32 * h + lane) * N < D) x[u][h].load(src + (32 * h + lane) * N);
+                    if (i0 + u < n && has(h)) x[u][h].load(src + column(h));
             }
 #pragma unroll
-            for (int u = 0; u < kTokens; ++u)
+            for (int u = 0; u < K; ++u)
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    if (i0 + u < e && c0 + (32 * h + lane) * N < D) x[u][h].add_to(g[h]);
-        }
-        const int32_t slot = a == 0 && on ? o.later + static_cast<int32_t>(p0 / kPiece)
-                                          : static_cast<int32_t>((p0 + a) / kShort);
-        float* dst = partial + static_cast<int64_t>(slot) * D + c0;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int c = (32 * h + lane) * N;
-            if (c0 + c >= D) continue;
-            if constexpr (VEC)
-                *reinterpret_cast<float4*>(dst + c) = make_float4(g[h][0], g[h][1], g[h][2], g[h][3]);
-            else
-                dst[c] = g[h][0];
+                    if (i0 + u < n && has(h)) x[u][h].add_to(g[h]);
         }
     }
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_state(const T* p, float (&x)[N])
+{
+    if constexpr (N == 4)
+        StateIO<sizeof(T) == 4 ? ST_F32 : ST_BF16>::ld4(p, 0, x);
+    else
+        x[0] = StateIO<sizeof(T) == 4 ? ST_F32 : ST_BF16>::ld(p, 0);
+}
+template <int N>
+__device__ __forceinline__ void store_sum(float* p, const float (&x)[N])
+{
+    if constexpr (N == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *p = x[0];
 }
 
-// One block per (kJoin places, slice): at most one row of more than kMany
-// pieces, (kMany - 1) kPiece places or more, starts there.  The warps add a
-// part of its pieces each.
-constexpr int kJoin = 256;
-static_assert(kJoin < (kMany - 1) * kPiece);
-__global__ void __launch_bounds__(kThreads)
-    forge_embedding_join_kernel(int64_t T, int64_t D, Order o, float* partial)
+// One warp per (kPiece places, slice): the pieces of huge rows that start among
+// these places; there are two at most.
+template <typename G, bool VEC>
+__device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T, int64_t D,
+                                           const Order& o, float* partial)
 {
+    static_assert(kPiece < kMedium && kMedium % kPiece == 0);
+    using P = Part<VEC, kSlice>;
+    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;  // in flight
+    const int lane = threadIdx.x & 31;
+    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int32_t p0 = static_cast<int32_t>(unit / slices * kPiece);
+    const P part{unit % slices * kSlice, D, lane};
+    if (p0 >= T) return;
+    int32_t at = -1, n = 0;  // a huge row that starts here
+#pragma unroll
+    for (int i = 0; i < kPiece / 32; ++i) {
+        const int32_t place = p0 + 32 * i + lane;
+        const int32_t here = place < T ? __ldg(o.at + place).y : 0;
+        const uint32_t found = __ballot_sync(0xffffffffu, here > kMedium);
+        if (found != 0) {
+            at = p0 + 32 * i + __ffs(found) - 1;
+            n = __shfl_sync(0xffffffffu, here, __ffs(found) - 1);
+        }
+    }
+    auto piece = [&](int32_t a, int32_t e, int32_t slot) {
+        float g[P::H][P::N] = {};
+        for (int32_t i0 = a; i0 < e; i0 += 32) {
+            const int32_t token = i0 + lane < e ? __ldg(o.order + i0 + lane) : 0;
+            part.template add_rows<kTokens>(
+                dY, e - i0 < 32 ? e - i0 : 32,
+                [&](int32_t i) { return __shfl_sync(0xffffffffu, token, i & 31); }, g);
+        }
+#pragma unroll
+        for (int h = 0; h < P::H; ++h)
+            if (part.has(h)) store_sum(partial + static_cast<int64_t>(slot) * D + part.c0 + part.column(h), g[h]);
+    };
+    const int64_t p1 = static_cast<int64_t>(p0) + kPiece;
+    const int2 first = __ldg(o.at + p0);
+    if (first.x >= 0 && first.y == 0) {
+        const int2 s = __ldg(o.seg + first.x);
+        if (s.y - s.x > kMedium)
+            piece(p0, static_cast<int32_t>(s.y < p1 ? s.y : p1), o.later + p0 / kPiece);
+    }
+    if (at >= 0) piece(at, static_cast<int32_t>(at + n < p1 ? at + n : p1), at / kMedium);
+}
+
+// The step of column c of row r from the sum of its tokens; `state` holds what
+// the column had.
+template <int MODE, int ST>
+struct Column {
+    float w, a, b;
+    __device__ __forceinline__ void load(const float* dW, const Params& p, int64_t at)
+    {
+        if constexpr (MODE == SUM_ADAMW) {
+            w = StateIO<ST_F32>::ld(p.W, at);
+            a = StateIO<ST>::ld(p.s1, at);
+            b = StateIO<ST>::ld(p.s2, at);
+        } else if constexpr (MODE == SUM_ADD) {
+            w = dW[at];
+        }
+    }
+    __device__ __forceinline__ void finish(float* dW, const Params& p, int64_t at, float sum, float scale)
+    {
+        const float x = sum * scale;
+        if constexpr (MODE == SUM_ADAMW) {
+            float gs[4] = {x, x, x, x}, ws[4] = {w, w, w, w}, as[4] = {a, a, a, a}, bs[4] = {b, b, b, b};
+            step4<OP_ADAMW>(p, gs, ws, as, bs);
+            StateIO<ST_F32>::st(p.W, at, ws[0]);
+            StateIO<ST>::st(p.s1, at, as[0]);
+            StateIO<ST>::st(p.s2, at, bs[0]);
+        } else {
+            dW[at] = MODE == SUM_ADD ? fmaf(scale, sum, w) : x;
+        }
+    }
+};
+
+// One block per (kMediumPlaces places, slice): the medium rows that start
+// there, one after the other.
+constexpr int kMediumPlaces = 64;
+template <typename G, int MODE, int ST, bool VEC>
+__device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t T, int64_t D,
+                                            float scale, float* dW, const Order& o, const Params& p)
+{
+    using P = Part<VEC, kSlice>;
     constexpr int kWarps = kThreads / 32;
-    __shared__ int32_t s_first, s_end;
+    constexpr int kMost = kMediumPlaces / (kShort + 1) + 1;
+    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;  // in flight
+    __shared__ int2 s_start[2][kMost];  // place and tokens, by the warp that found them
+    __shared__ int32_t s_row[2][kMost], s_count[2];
     __shared__ float sh[kWarps][kSlice];
-    const int32_t slices = static_cast<int32_t>((D + kSlice - 1) / kSlice);
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x % slices) * kSlice;
-    const int32_t p0 = blockIdx.x / slices * kJoin;
-    if (threadIdx.x == 0) s_end = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoin / kThreads; ++i) {
-        const int32_t a = p0 + i * kThreads + threadIdx.x;
-        const int32_t n = a < T ? __ldg(o.at + a).y : 0;
-        if (n > kShort && pieces_of(a, a + n) > kMany) {
-            s_first = a;
-            s_end = a + n;
-        }
-    }
-    __syncthreads();
-    if (s_end == 0) return;
-    const int32_t b0 = s_first / kPiece, n = pieces_of(s_first, s_end);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t per = (n + kWarps - 1) / kWarps;
-    const int32_t i0 = warp * per < n ? warp * per : n, i1 = i0 + per < n ? i0 + per : n;
-#pragma unroll
-    for (int h = 0; h < kSlice / 32; ++h) {
-        const int c = 32 * h + lane;
-        float g[1] = {0.0f};
-        if (c0 + c < D)
-            add_rows<8>(
-                static_cast<const float*>(partial) + c0 + c, i1 - i0,
-                [&](int32_t i) {
-                    return i0 + i == 0 ? s_first / kShort : o.later + b0 + i0 + i;
-                },
-                D, g);
-        sh[warp][c] = g[0];
+    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int32_t p0 = static_cast<int32_t>(block / slices * kMediumPlaces);
+    const P part{block % slices * kSlice, D, lane};
+    static_assert(kMediumPlaces == 64);
+    if (warp < 2) {
+        const int32_t place = p0 + static_cast<int32_t>(threadIdx.x);
+        const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+        const bool start = here.y > kShort && here.y <= kMedium;
+        const uint32_t found = __ballot_sync(0xffffffffu, start);
+        if (start) {
+            const int i = __popc(found & ((1u << lane) - 1u));
+            s_start[warp][i] = make_int2(place, here.y);
+            s_row[warp][i] = here.x;
+        }
+        if (lane == 0) s_count[warp] = __popc(found);
     }
-    __syncthreads();  // every piece has been read
-    float x = 0.0f;
+    __syncthreads();
+    const int first = s_count[0], rows = first + s_count[1];
+    for (int r = 0; r < rows; ++r) {
+        const int2 s = r < first ? s_start[0][r] : s_start[1][r - first];
+        const int64_t c = part.c0 + threadIdx.x;
+        const int64_t at = (r < first ? s_row[0][r] : s_row[1][r - first]) * D + c;
+        Column<MODE, ST> state;
+        if (c < D) state.load(dW, p, at);
+        // tokens warp, warp + 8, ...
+        float g[P::H][P::N] = {};
+        for (int32_t j = warp; j < s.y; j += 32 * kWarps) {
+            const int32_t mine = j + lane * kWarps;
+            const int32_t token = mine < s.y ? __ldg(o.order + s.x + mine) : 0;
+            const int32_t n = (s.y - j + kWarps - 1) / kWarps;
+            part.template add_rows<kTokens>(
+                dY, n < 32 ? n : 32, [&](int32_t i) { return __shfl_sync(0xffffffffu, token, i & 31); }, g);
+        }
+        __syncthreads();  // the row before has been read
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) x += sh[w][threadIdx.x];
-    if (c0 + threadIdx.x < D) partial[static_cast<int64_t>(s_first / kShort) * D + c0 + threadIdx.x] = x;
-}
-
-// The sum over a row's tokens at one column (vector): token by token, or
-// piece by piece.
-template <int F, int N, typename G>
-__device__ __forceinline__ void row_sum(const G* dY, const Order& o, const float* partial, int2 s,
-                                        int64_t D, int64_t c, float (&g)[N])
-{
-    if (s.y - s.x <= kShort) {
-        add_rows<F>(dY + c, s.y - s.x, [&](int32_t i) { return __ldg(o.order + s.x + i); }, D, g);
-    } else {
-        const int32_t n = pieces_of(s.x, s.y), b0 = s.x / kPiece;
-        add_rows<F>(
-            partial + c, n > kMany ? 1 : n,
-            [&](int32_t i) { return i == 0 ? s.x / kShort : o.later + b0 + i; }, D, g);
+        for (int h = 0; h < P::H; ++h)
+#pragma unroll
+            for (int k = 0; k < P::N; ++k) sh[warp][part.column(h) + k] = g[h][k];
+        __syncthreads();
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += sh[w][threadIdx.x];
+        if (c < D) state.finish(dW, p, at, sum, scale);
     }
 }
-
-enum { SUM_STORE = 0, SUM_ADAMW = 1 };
-
-template <bool VEC>
-constexpr int kUnits = VEC ? 2 : 4;
 
 // dW or the AdamW step over all V D elements, flat, so that no width leaves
 // lanes idle: a block takes `turns` tiles of U vectors a thread, one after the
@@ -578,13 +634,14 @@ constexpr int kUnits = VEC ? 2 : 4;
 // vectors (VEC; four single elements otherwise) are in hand at once, with the
 // places of the next ones already on their way: most rows of a large
 // vocabulary have no token, and their zeros (or their decay) must not wait for
-// a table.  Blocks are many and start in order of the rows, so that those with
-// frequent tokens, which a vocabulary has in front, are not the last to end.
-// Bound by HBM: dW written, or W, m, v read and written, once.
+// a table.  Rows of more than kShort tokens are left out.
+template <bool VEC>
+constexpr int kUnits = VEC ? 2 : 4;
+
 template <typename G, int MODE, int ST, bool VEC>
-__global__ void __launch_bounds__(kThreads, MODE == SUM_ADAMW ? 4 : 5)
-    forge_embedding_grad_kernel(const G* dY, int32_t V, int32_t D, float scale, float* dW, Order o,
-                                const float* partial, int32_t turns, const Params p)
+__device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t V, int32_t D,
+                                           float scale, float* dW, const Order& o, int32_t turns,
+                                           const Params& p)
 {
     constexpr int N = VEC ? 4 : 1;
     constexpr int U = kUnits<VEC>;
@@ -599,18 +656,20 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_ADAMW ? 4 : 5)
     int2 s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t q = static_cast<int64_t>(blockIdx.x) * turns * step + u * kThreads + threadIdx.x;
+        const int64_t q = block * turns * step + u * kThreads + threadIdx.x;
         row[u] = static_cast<uint32_t>(q / width);
         column[u] = static_cast<uint32_t>(q - static_cast<int64_t>(row[u]) * width);
         s[u] = places(row[u]);
     }
     for (int32_t turn = 0; turn < turns && row[0] < V; ++turn) {
         float g[U * N], w[U * N], a[U * N], b[U * N];
-        if constexpr (MODE == SUM_ADAMW) {
+        bool live[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u) {
+            live[u] = row[u] < V && s[u].y - s[u].x <= kShort;
+            if constexpr (MODE == SUM_ADAMW) {
                 const int64_t at = static_cast<int64_t>(row[u]) * D + column[u] * N;
-                if (row[u] >= V) continue;
+                if (!live[u]) continue;
                 if constexpr (VEC) {
                     StateIO<ST_F32>::ld4(p.W, at, w + 4 * u);
                     StateIO<ST>::ld4(p.s1, at, a + 4 * u);
@@ -625,19 +684,21 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_ADAMW ? 4 : 5)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float x[N] = {};
-            if (s[u].y > s[u].x)
-                row_sum<F>(dY, o, partial, s[u], D, column[u] * N, x);
+            if (live[u] && s[u].y > s[u].x)
+                add_rows<F>(dY + column[u] * N, s[u].y - s[u].x,
+                            [&](int32_t i) { return __ldg(o.order + s[u].x + i); }, D, x);
 #pragma unroll
             for (int k = 0; k < N; ++k) g[u * N + k] = x[k] * scale;
         }
+        if constexpr (MODE == SUM_ADAMW) {
 #pragma unroll
-        for (int h = 0; h < U * N / 4; ++h)
-            if constexpr (MODE == SUM_ADAMW)
+            for (int h = 0; h < U * N / 4; ++h)
                 step4<OP_ADAMW>(p, g + 4 * h, w + 4 * h, a + 4 * h, b + 4 * h);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t at = static_cast<int64_t>(row[u]) * D + column[u] * N;
-            if (row[u] < V) {
+            if (live[u]) {
                 if constexpr (MODE == SUM_ADAMW && VEC) {
                     StateIO<ST_F32>::st4(p.W, at, w + 4 * u);
                     StateIO<ST>::st4(p.s1, at, a + 4 * u);
@@ -663,65 +724,123 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_ADAMW ? 4 : 5)
     }
 }
 
-// dW += the sums, over the rows that have a token only: flat over (place, four
-// columns); the first place of a row takes it.
+// dW += the sums, over the rows that have a token only.  One warp per (four
+// places, 512 columns; 256 single ones) takes the rows of at most kShort tokens
+// that start there: two loads bring the places and all their tokens.
+constexpr int kTouchPlaces = 4;
+template <bool VEC>
+constexpr int kTouchColumns = VEC ? 512 : 256;
 template <typename G, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    forge_embedding_accumulate_kernel(const G* dY, int64_t T, int64_t D, float scale, float* dW,
-                                      Order o, const float* partial)
+__device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t T, int64_t D,
+                                             float scale, float* dW, const Order& o)
 {
-    // four columns of a lane: side by side, or (single elements) 32 apart
-    const int64_t width = (D + 127) / 128 * 32;
-    const int64_t q = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t i = q / width;
-    if (i >= T) return;
-    const int2 first = __ldg(o.at + i);
-    if (first.y == 0) return;
-    const int64_t part = q - i * width;
-    const int2 s = make_int2(static_cast<int32_t>(i), static_cast<int32_t>(i) + first.y);
-    const int64_t row = first.x * D;
-    if constexpr (VEC) {
-        const int64_t c = part * 4;
-        if (c >= D) return;
-        float d[4], g[4] = {};
-        StateIO<ST_F32>::ld4(dW, row + c, d);
-        row_sum<4>(dY, o, partial, s, D, c, g);
+    static_assert(kTouchPlaces + kShort <= 32);
+    using P = Part<VEC, kTouchColumns<VEC>>;
+    const int lane = threadIdx.x & 31;
+    const int64_t slices = (D + kTouchColumns<VEC> - 1) / kTouchColumns<VEC>;
+    const int64_t p0 = unit / slices * kTouchPlaces, c0 = unit % slices * kTouchColumns<VEC>;
+    if (p0 >= T) return;
+    const int64_t place = p0 + lane;
+    const int2 here = lane < kTouchPlaces && place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+    const int32_t token = lane < kTouchPlaces + kShort && place < T ? __ldg(o.order + place) : 0;
+    const P part{c0, D, lane};
+    for (uint32_t left = __ballot_sync(0xffffffffu, here.y > 0 && here.y <= kShort); left != 0;
+         left &= left - 1) {
+        const int a = __ffs(left) - 1;
+        const int32_t n = __shfl_sync(0xffffffffu, here.y, a);
+        float* dst = dW + static_cast<int64_t>(__shfl_sync(0xffffffffu, here.x, a)) * D + c0;
+        float d[P::H][P::N], g[P::H][P::N] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[k] = fmaf(scale, g[k], d[k]);
-        StateIO<ST_F32>::st4(dW, row + c, d);
-    } else {
-        const int64_t c0 = part / 32 * 128 + part % 32;
-        float d[4], g[4] = {};
+        for (int h = 0; h < P::H; ++h)
+            if (part.has(h)) load_state(dst + part.column(h), d[h]);
+        part.template add_rows<VEC && sizeof(G) == 4 ? 1 : 2>(
+            dY, n, [&](int32_t i) { return __shfl_sync(0xffffffffu, token, (a + i) & 31); }, g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (c0 + 32 * k < D) d[k] = StateIO<ST_F32>::ld(dW, row + c0 + 32 * k);
-        auto add = [&](auto* base, int32_t n, auto of) {
-            for (int32_t j = 0; j < n; j += 4) {
-                float x[4][4];
+        for (int h = 0; h < P::H; ++h) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int64_t r = j + u < n ? of(j + u) : -1;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        x[u][k] = r >= 0 && c0 + 32 * k < D ? load1(base, r * D + c0 + 32 * k) : 0.0f;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) g[k] += x[u][k];
-            }
-        };
-        if (first.y <= kShort) {
-            add(dY, first.y, [&](int32_t j) { return __ldg(o.order + s.x + j); });
-        } else {
-            const int32_t n = pieces_of(s.x, s.y), b0 = s.x / kPiece;
-            add(partial, n > kMany ? 1 : n,
-                [&](int32_t j) { return j == 0 ? s.x / kShort : o.later + b0 + j; });
+            for (int k = 0; k < P::N; ++k) d[h][k] = fmaf(scale, g[h][k], d[h][k]);
+            if (part.has(h)) store_sum(dst + part.column(h), d[h]);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (c0 + 32 * k < D) StateIO<ST_F32>::st(dW, row + c0 + 32 * k, fmaf(scale, g[k], d[k]));
     }
+}
+
+// All rows in one launch: the blocks for the pieces of huge rows and for medium
+// rows come first, as they take longest, then those for the others.  Bound by
+// HBM: dW written, or W, m, v read and written, once, and dY read once.
+template <typename G, int MODE, int ST, bool VEC>
+__global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
+    forge_embedding_grad_kernel(const G* dY, int64_t T, int32_t V, int32_t D, float scale,
+                                float* dW, Order o, float* partial, uint32_t piece_blocks,
+                                uint32_t medium_blocks, int32_t turns, const Params p)
+{
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5;
+    uint32_t block = blockIdx.x;
+    if (block < piece_blocks) {
+        sum_pieces<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, o, partial);
+        return;
+    }
+    block -= piece_blocks;
+    if (block < medium_blocks) {
+        medium_rows<G, MODE, ST, VEC>(dY, block, T, D, scale, dW, o, p);
+        return;
+    }
+    block -= medium_blocks;
+    if constexpr (MODE == SUM_ADD)
+        touched_rows<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, scale, dW, o);
+    else
+        dense_rows<G, MODE, ST, VEC>(dY, block, V, D, scale, dW, o, turns, p);
+}
+
+// One block per (kMedium places, slice): at most one huge row starts there;
+// its warps add a part of the pieces each.
+template <int MODE, int ST>
+__global__ void __launch_bounds__(kThreads)
+    forge_embedding_huge_rows_kernel(int64_t T, int64_t D, float scale, float* dW, Order o,
+                                     const float* partial, const Params p)
+{
+    using P = Part<false, kSlice>;
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int32_t s_first, s_n, s_row;
+    __shared__ float sh[kWarps][kSlice];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int32_t p0 = static_cast<int32_t>(blockIdx.x / slices * kMedium);
+    const P part{static_cast<int64_t>(blockIdx.x % slices) * kSlice, D, lane};
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMedium / kThreads; ++i) {
+        const int32_t place = p0 + i * kThreads + static_cast<int32_t>(threadIdx.x);
+        const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+        if (here.y > kMedium) {
+            s_first = place;
+            s_n = here.y;
+            s_row = here.x;
+        }
+    }
+    __syncthreads();
+    if (s_n == 0) return;
+    const int32_t first = s_first, b0 = first / kPiece, n = (first + s_n - 1) / kPiece - b0 + 1;
+    float g[P::H][1] = {};
+    part.template add_rows<4>(
+        partial, (n - warp + kWarps - 1) / kWarps,
+        [&](int32_t j) {
+            const int32_t i = warp + j * kWarps;
+            return i == 0 ? first / kMedium : o.later + b0 + (i < n ? i : 1);
+        },
+        g);
+#pragma unroll
+    for (int h = 0; h < P::H; ++h) sh[warp][part.column(h)] = g[h][0];
+    __syncthreads();
+    const int64_t c = part.c0 + threadIdx.x, at = s_row * D + c;
+    if (c >= D) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sh[w][threadIdx.x];
+    Column<MODE, ST> state;
+    state.load(dW, p, at);
+    state.finish(dW, p, at, sum, scale);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -771,24 +890,57 @@ cudaError_t order_tokens(const void* ids, int64_t T, int64_t V, const Order& o, 
     return cudaGetLastError();
 }
 
-// What becomes of the sums: dW written, dW added to, or the AdamW step.
-enum class Sum { Store, Add, AdamW };
+template <typename G, int MODE, int ST, bool VEC>
+cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scale, float* dW,
+                        const Order& o, float* partial, const Params& p, int sms, cudaStream_t s)
+{
+    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int64_t units = T > kMedium ? (T + kPiece - 1) / kPiece * slices : 0;
+    const int64_t piece_blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t medium_blocks = T > kShort ? (T + kMediumPlaces - 1) / kMediumPlaces * slices : 0;
+    int64_t turns = 1, blocks;
+    if (MODE == SUM_ADD) {
+        const int64_t touch_units =
+            (T + kTouchPlaces - 1) / kTouchPlaces * ((D + kTouchColumns<VEC> - 1) / kTouchColumns<VEC>);
+        blocks = (touch_units + kThreads / 32 - 1) / (kThreads / 32);
+    } else {
+        // as many turns, up to eight, as leave each SM 32 blocks
+        const int64_t width = VEC ? D / 4 : D;
+        const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);
+        turns = tiles / (32LL * sms);
+        turns = turns < 1 ? 1 : (turns > 8 ? 8 : turns);
+        while ((tiles + turns - 1) / turns > INT32_MAX / 2) turns *= 2;
+        blocks = (tiles + turns - 1) / turns;
+    }
+    const int64_t all = piece_blocks + medium_blocks + blocks;
+    if (all > INT32_MAX) return cudaErrorInvalidConfiguration;
+    forge_embedding_grad_kernel<G, MODE, ST, VEC><<<static_cast<unsigned>(all), kThreads, 0, s>>>(
+        dY, T, static_cast<int32_t>(V), static_cast<int32_t>(D), scale, dW, o, partial,
+        static_cast<uint32_t>(piece_blocks), static_cast<uint32_t>(medium_blocks),
+        static_cast<int32_t>(turns), p);
+    if (T > kMedium) {
+        const int64_t huge_blocks = (T + kMedium - 1) / kMedium * slices;
+        forge_embedding_huge_rows_kernel<MODE, ST>
+            <<<static_cast<unsigned>(huge_blocks), kThreads, 0, s>>>(T, D, scale, dW, o, partial, p);
+    }
+    return cudaGetLastError();
+}
 
 template <typename G, bool VEC>
 cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids, bool wide,
                         int64_t T, int64_t V, int64_t D, float scale, float* dW, const Params& p,
                         int sms, cudaStream_t s)
 {
-    if (what == Sum::Add && T == 0) return cudaSuccess;
+    if (what == SUM_ADD && T == 0) return cudaSuccess;
     Order o{};
     float* partial = nullptr;
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
     if (T > 0) {
-        o.later = static_cast<int32_t>((T + kShort - 1) / kShort);
-        const int64_t slots = T > kShort ? o.later + (T + kPiece - 1) / kPiece : 0;
         auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
         const int64_t order_b = up(T * 4), list_b = up(T * 8), seg_b = up(V * 8);
+        o.later = static_cast<int32_t>((T + kMedium - 1) / kMedium);
+        const int64_t slots = T > kMedium ? o.later + (T + kPiece - 1) / kPiece : 0;
         e = scratch_alloc(&scratch, order_b + 3 * list_b + seg_b + slots * D * 4, s);
         if (e != cudaSuccess) return e;
         uint8_t* at = static_cast<uint8_t*>(scratch);
@@ -800,50 +952,16 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
         partial = reinterpret_cast<float*>(at += seg_b);
         e = wide ? order_tokens<int64_t>(ids, T, V, o, p.status, s)
                  : order_tokens<int32_t>(ids, T, V, o, p.status, s);
-        const int64_t slices = (D + kSlice - 1) / kSlice;
-        if (e == cudaSuccess && T > kShort) {
-            const int64_t units = (T + kPiece - 1) / kPiece * slices;
-            const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-            if (blocks > INT32_MAX) e = cudaErrorInvalidConfiguration;
-            else
-                forge_embedding_pieces_kernel<G, VEC>
-                    <<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(dY, T, D, o, partial);
-        }
-        if (e == cudaSuccess && T > (kMany - 1) * kPiece) {
-            const int64_t blocks = (T + kJoin - 1) / kJoin * slices;
-            forge_embedding_join_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(T, D, o,
-                                                                                         partial);
-        }
-        if (e == cudaSuccess) e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
-        const int64_t width = VEC ? D / 4 : D;
-        if (what == Sum::Add) {
-            const int64_t blocks = (T * ((D + 127) / 128 * 32) + kThreads - 1) / kThreads;
-            if (blocks > INT32_MAX) e = cudaErrorInvalidConfiguration;
-            else
-                forge_embedding_accumulate_kernel<G, VEC><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-                    dY, T, D, scale, dW, o, partial);
-        } else {
-            // as many turns, up to eight, as leave each SM 32 blocks
-            const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);
-            int64_t turns = tiles / (32LL * sms);
-            turns = turns < 1 ? 1 : (turns > 8 ? 8 : turns);
-            while ((tiles + turns - 1) / turns > INT32_MAX) turns *= 2;
-            const int blocks = static_cast<int>((tiles + turns - 1) / turns);
-            auto go = [&](auto kernel) {
-                kernel<<<blocks, kThreads, 0, s>>>(dY, static_cast<int32_t>(V), static_cast<int32_t>(D),
-                                                   scale, dW, o, partial,
-                                                   static_cast<int32_t>(turns), p);
-            };
-            if (what == Sum::Store)
-                go(forge_embedding_grad_kernel<G, SUM_STORE, ST_F32, VEC>);
-            else if (state_bf16)
-                go(forge_embedding_grad_kernel<G, SUM_ADAMW, ST_BF16, VEC>);
-            else
-                go(forge_embedding_grad_kernel<G, SUM_ADAMW, ST_F32, VEC>);
-        }
-        e = cudaGetLastError();
+        if (what == SUM_STORE)
+            e = launch_sums<G, SUM_STORE, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+        else if (what == SUM_ADD)
+            e = launch_sums<G, SUM_ADD, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+        else if (state_bf16)
+            e = launch_sums<G, SUM_ADAMW, ST_BF16, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+        else
+            e = launch_sums<G, SUM_ADAMW, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
     }
     if (scratch) {
         const cudaError_t fe = scratch_free(scratch, s);
@@ -942,7 +1060,7 @@ extern "C" forge_status forge_embedding_grad(const void* dY, forge_dtype dy_dtyp
     Params p{};
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad(accumulate ? Sum::Add : Sum::Store, false, dY, dy_dtype, ids, id_dtype,
+    const cudaError_t e = grad(accumulate ? SUM_ADD : SUM_STORE, false, dY, dy_dtype, ids, id_dtype,
                                T, V, D, scale, dW, p, sms, s);
     return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }
@@ -973,7 +1091,7 @@ extern "C" forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dty
     p.s2 = v;
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad(Sum::AdamW, state_dtype == FORGE_BF16, dY, dy_dtype, ids, id_dtype, T,
+    const cudaError_t e = grad(SUM_ADAMW, state_dtype == FORGE_BF16, dY, dy_dtype, ids, id_dtype, T,
                                V, D, scale, nullptr, p, sms, s);
     return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
 }

@@ -12,7 +12,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "forge.h"
 #include "forge_device.h"
@@ -24,7 +23,7 @@ constexpr int kMaxTop = 32;
 constexpr int kFlight = 4;      // 16-byte vectors in flight per thread
 constexpr int kWarps = 8;       // of a block
 constexpr int kGroups = 64;     // most maxima that bound the top entries from below
-constexpr int kList = 128;      // vectors a warp notes before it looks into them
+constexpr int kList = 256;      // vectors a warp notes before it looks into them
 constexpr int kRoom = 128;      // entries a warp holds before it keeps its best
 constexpr float kFloor = -1000.0f;  // 2^kFloor is 0, and 0 * kFloor is not a NaN
 constexpr float kLog2e = 1.4426950408889634f;
@@ -524,7 +523,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         st.w += a + b;
 
         if constexpr (TOP) {
-            if (tile == 0 || (tile == 3 && tiles > 8)) tighten();
+            if (tile == 0 || ((tile == 3 || tile == 15 || tile == 63) && tiles > 2 * tile)) tighten();
             if (__any_sync(0xffffffffu, !(tm < bound_v))) {
 #pragma unroll
                 for (int f = 0; f < kFlight; ++f) {
@@ -772,18 +771,21 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
                        : cudaLaunchKernelEx(&cfg, forge_token_logprob_kernel<T, WARPS, false>, x, p, split);
 }
 
-// One, two or eight warps a row by its length, so that a thread has a few
-// vectors at least; long rows are split over clusters of up to eight blocks
-// while the rows alone leave SMs without work.
+// Few warps a row, so that the joins at a row's end are few and other rows'
+// loads cover them: one up to 1024 vectors (16384 rows of 8000 bf16 with five
+// alternatives: 94 us, two warps 103, eight 188), two up to 4096 (16384 x 16000
+// fp32: 185 us; four 208, one 245), four beyond (8192 x 131072 bf16: 356 us;
+// two 514, eight 370); more while the rows' warps do not fill the SMs, and
+// then clusters of up to eight blocks.
 template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
-    const char* e = getenv("FORGE_LP_W");
-    const int w = e ? atoi(e) : nvec <= 256 ? 1 : nvec <= 1024 ? 2 : p.R >= 12 * sms ? 4 : 8;
-    if (w == 1) return launch_forward<T, 1>(x, p, 1, s);
-    if (w == 2) return launch_forward<T, 2>(x, p, 1, s);
-    if (w == 4) return launch_forward<T, 4>(x, p, 1, s);
+    int warps = nvec <= 1024 ? 1 : (nvec <= 4096 ? 2 : 4);
+    while (warps < kWarps && p.R * warps < 12 * sms) warps *= 2;
+    if (warps == 1) return launch_forward<T, 1>(x, p, 1, s);
+    if (warps == 2) return launch_forward<T, 2>(x, p, 1, s);
+    if (warps == 4) return launch_forward<T, 4>(x, p, 1, s);
     int split = 1;
     while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
     return launch_forward<T, 8>(x, p, split, s);
