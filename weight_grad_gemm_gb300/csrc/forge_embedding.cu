@@ -192,7 +192,7 @@ struct Order {
     int32_t later;  // rows of `partial` in front of those of pieces that go on
 };
 
-constexpr int kIdFlight = 8;  // loads of ids in flight per lane
+constexpr int kIdFlight = 16; // loads of ids in flight per lane
 
 template <typename ID>
 __global__ void __launch_bounds__(kOrderThreads, 1)
@@ -205,24 +205,33 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     const uint32_t before = (1u << lane) - 1u;
     const uint32_t cls = blockIdx.x;
 
-    // count, this warp's ids [lo, hi); a row is held in 32 bits, kNoRow for
-    // padding and for ids past the vocabulary
-    constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+    // count, this warp's ids [lo, hi).  An id is held in 32 bits without its
+    // sign: padding and ids past the vocabulary are those not below V.
     const int64_t chunk = (T + kOrderThreads - 1) / kOrderThreads * 32;
     const int64_t lo = warp * chunk, hi = lo + chunk < T ? lo + chunk : T;
     const uint32_t rows = static_cast<uint32_t>(V);
     auto fetch = [&](int64_t i0, uint32_t (&r)[kIdFlight]) {
         ID id[kIdFlight];
-        const int32_t left = static_cast<int32_t>(hi - i0 < 32 * kIdFlight ? hi - i0 : 32 * kIdFlight) - lane;
+        if (hi - i0 >= 32 * kIdFlight) {
 #pragma unroll
-        for (int u = 0; u < kIdFlight; ++u)
-            id[u] = 32 * u < left ? __ldg(ids + i0 + 32 * u + lane) : static_cast<ID>(-1);
+            for (int u = 0; u < kIdFlight; ++u) id[u] = __ldg(ids + i0 + 32 * u + lane);
+        } else {
+            const int32_t left = static_cast<int32_t>(hi - i0) - lane;
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u)
+                id[u] = 32 * u < left ? __ldg(ids + i0 + 32 * u + lane) : static_cast<ID>(-1);
+        }
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            // a negative id is a large one without its sign
-            const std::make_unsigned_t<ID> x = id[u];
-            r[u] = x < rows ? static_cast<uint32_t>(x) : kNoRow;
-            if (cls == 0 && id[u] >= V) bad_id(status);
+            if constexpr (sizeof(ID) == 4)
+                r[u] = static_cast<uint32_t>(id[u]);
+            else
+                r[u] = static_cast<uint64_t>(id[u]) >> 32 ? 0xFFFFFFFFu : static_cast<uint32_t>(id[u]);
+        }
+        if (cls == 0) {
+#pragma unroll
+            for (int u = 0; u < kIdFlight; ++u)
+                if (id[u] >= V) bad_id(status);
         }
     };
     uint32_t own = 0, less = 0;
@@ -231,9 +240,9 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         fetch(i0, r);
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            const uint32_t c = r[u] == kNoRow ? kClasses : r[u] & (kClasses - 1);
-            own += c == cls;
-            less += c < cls;
+            const uint32_t c = r[u] & (kClasses - 1);
+            if (r[u] < rows && c == cls) ++own;
+            if (r[u] < rows && c < cls) ++less;
         }
     }
     own = __reduce_add_sync(0xffffffffu, own);
@@ -266,7 +275,7 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
         fetch(i0, r);
 #pragma unroll
         for (int u = 0; u < kIdFlight; ++u) {
-            const bool mine = r[u] != kNoRow && (r[u] & (kClasses - 1)) == cls;
+            const bool mine = r[u] < rows && (r[u] & (kClasses - 1)) == cls;
             const uint32_t all = __ballot_sync(0xffffffffu, mine);
             if (all == 0) continue;
             if (mine)
@@ -498,7 +507,7 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
 {
     static_assert(kPiece < kMedium && kMedium % kPiece == 0);
     using P = Part<VEC, kSlice>;
-    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;  // in flight
+    constexpr int kTokens = 4;  // in flight
     const int lane = threadIdx.x & 31;
     const int64_t slices = (D + kSlice - 1) / kSlice;
     const int32_t p0 = static_cast<int32_t>(unit / slices * kPiece);
@@ -577,7 +586,7 @@ __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t 
     using P = Part<VEC, kSlice>;
     constexpr int kWarps = kThreads / 32;
     constexpr int kMost = kMediumPlaces / (kShort + 1) + 1;
-    constexpr int kTokens = VEC && sizeof(G) == 2 ? 8 : 4;  // in flight
+    constexpr int kTokens = 4;  // in flight
     __shared__ int2 s_start[2][kMost];  // place and tokens, by the warp that found them
     __shared__ int32_t s_row[2][kMost], s_count[2];
     __shared__ float sh[kWarps][kSlice];

@@ -101,6 +101,12 @@ __device__ __forceinline__ const X* remote(const X* p, int q)
     return reinterpret_cast<const X*>(a);
 }
 
+// Vectors of a thread in hand at once (a tile): short rows four, with the next
+// four on their way, longer ones eight, other warps' loads covering the work on
+// them: what a tile costs beside its elements then counts half.
+template <int WARPS>
+constexpr int kTile = WARPS == 1 ? 4 : 8;
+
 // 16 bytes of a row: four fp32 or eight bf16 logits.
 template <typename T>
 struct Vec;
@@ -350,6 +356,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     constexpr int kRows = kWarps / WARPS;      // of a block
     constexpr int kGroupLanes = kThreads > kGroups ? kThreads / kGroups : 1;
     constexpr int kUsed = kThreads / kGroupLanes;  // groups of a row: 32 or 64
+    constexpr int F = kTile<WARPS>;
     __shared__ Tops s_tops[TOP ? kWarps : 1];
     __shared__ float s_group[2][kRows][kUsed];
     __shared__ float s_kth[kRows];
@@ -473,39 +480,45 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 
     // whole tiles are read without a check; the last one may end early
     const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
-    const int32_t whole = nv / (kFlight * kThreads);
-    const int32_t tiles = (nv + kFlight * kThreads - 1) / (kFlight * kThreads);
+    const int32_t whole = nv / (F * kThreads);
+    const int32_t tiles = (nv + F * kThreads - 1) / (F * kThreads);
     const uint4* at = xv + tid;
-    auto fetch = [&](int32_t tile, uint4 (&u)[kFlight]) {
+    auto fetch = [&](int32_t tile, uint4 (&u)[F]) {
         if (tile < whole) {
 #pragma unroll
-            for (int f = 0; f < kFlight; ++f) u[f] = __ldcs(at + f * kThreads);
+            for (int f = 0; f < F; ++f) u[f] = __ldcs(at + f * kThreads);
         } else {
-            const int32_t left = nv - tile * kFlight * kThreads - tid;
+            const int32_t left = nv - tile * F * kThreads - tid;
 #pragma unroll
-            for (int f = 0; f < kFlight; ++f)
-                u[f] = f * kThreads < left ? __ldcs(at + f * kThreads) : none;
+            for (int f = 0; f < F; ++f) u[f] = f * kThreads < left ? __ldcs(at + f * kThreads) : none;
         }
-        at += kFlight * kThreads;
+        at += F * kThreads;
     };
-    uint4 next[kFlight];
-    if (tiles > 0) fetch(0, next);
+    constexpr bool kAhead = F <= 4;
+    uint32_t seen = Vec<T>::kNone;  // the packed maximum of everything: keeps a NaN
+    uint4 next[kAhead ? F : 1];
+    if constexpr (kAhead)
+        if (tiles > 0) fetch(0, next);
     for (int32_t tile = 0; tile < tiles; ++tile) {
-        uint4 u[kFlight];
+        uint4 u[F];
+        if constexpr (kAhead) {
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) u[f] = next[f];
-        if (tile + 1 < tiles) fetch(tile + 1, next);
+            for (int f = 0; f < F; ++f) u[f] = next[f];
+            if (tile + 1 < tiles) fetch(tile + 1, next);
+        } else {
+            fetch(tile, u);
+        }
         uint32_t pm = packed_max<T>(u[0]);
 #pragma unroll
-        for (int f = 1; f < kFlight; ++f) pm = Vec<T>::max2(pm, packed_max<T>(u[f]));
+        for (int f = 1; f < F; ++f) pm = Vec<T>::max2(pm, packed_max<T>(u[f]));
+        seen = Vec<T>::max2(seen, pm);
         const float tm = Vec<T>::top(pm);
-        st.nan = st.nan || tm != tm;
         raise(tm);
         const float mr = st.m == -INFINITY ? 0.0f : st.m;
         const Pair mm = pair(-mr, -mr), cc = pair(c, c);
-        Pair s2 = pair(0.0f, 0.0f), w2 = pair(0.0f, 0.0f);
+        Pair s2 = pair(st.s, 0.0f), w2 = pair(st.w, 0.0f);
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f)
+        for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 float d0, d1;
@@ -518,16 +531,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             }
         float a, b;
         ::forge::logprob::split(s2, a, b);
-        st.s += a + b;
+        st.s = a + b;
         ::forge::logprob::split(w2, a, b);
-        st.w += a + b;
+        st.w = a + b;
 
         if constexpr (TOP) {
-            if (tile == 0 || ((tile == 3 || tile == 15 || tile == 63) && tiles > 2 * tile)) tighten();
+            if ((tile & (tile + 1)) == 0 && (tile == 0 || tiles > 2 * tile)) tighten();  // 0, 1, 3, 7, ...
             if (__any_sync(0xffffffffu, !(tm < bound_v))) {
 #pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
-                    const int32_t v = (tile * kFlight + f) * kThreads + tid;
+                for (int f = 0; f < F; ++f) {
+                    const int32_t v = (tile * F + f) * kThreads + tid;
                     const bool pass = !(Vec<T>::top(packed_max<T>(u[f])) < bound_v) && v < nv;
                     const uint32_t all = __ballot_sync(0xffffffffu, pass);
                     if (noted <= kList - 32) {
@@ -545,6 +558,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         held = look_into<T>(tops, over ? (nv + kThreads - 1) / kThreads * 32 : noted, held, xv, col0, k,
                             lane, !over, tid - lane, kThreads, nv);
     }
+
+    const float top = Vec<T>::top(seen);
+    st.nan = st.nan || top != top;
 
     // lanes, then warps
     join_lanes<32>(st, c);
