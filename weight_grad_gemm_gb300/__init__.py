@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from operator import attrgetter
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libforge.so")
@@ -461,14 +462,15 @@ def forge_embedding_adamw(dY, ids, W, m, v, *, lr, beta1, beta2, eps, wd, step, 
 
 def _tensor_list(ts, what):
     """Pointers, element counts and the common dtype of a list of tensors."""
-    n = len(ts)
-    if len({t.dtype for t in ts}) > 1:
+    import torch
+    T = torch.Tensor
+    if len(set(map(attrgetter("dtype"), ts))) > 1:
         raise TypeError(f"{what} must share one dtype")
-    if not all([t.is_cuda and t.is_contiguous() for t in ts]):
+    if not (all(map(attrgetter("is_cuda"), ts)) and all(map(T.is_contiguous, ts))):
         raise ValueError(f"{what} must be contiguous CUDA tensors")
-    ptrs = array("q", [t.data_ptr() for t in ts])
-    sizes = array("q", [t.numel() for t in ts])
-    return ptrs, sizes, FORGE_F32 if n == 0 else _float_code(ts[0])
+    ptrs = array("q", map(T.data_ptr, ts))
+    sizes = array("q", map(T.numel, ts))
+    return ptrs, sizes, FORGE_F32 if not ts else _float_code(ts[0])
 
 
 def _address(a):

@@ -23,7 +23,6 @@ constexpr int kMaxTop = 32;
 constexpr int kFlight = 4;      // 16-byte vectors in flight per thread
 constexpr int kWarps = 8;       // of a block
 constexpr int kGroups = 64;     // most maxima that bound the top entries from below
-constexpr int kList = 256;      // vectors a warp notes before it looks into them
 constexpr int kRoom = 128;      // entries a warp holds before it keeps its best
 constexpr float kFloor = -1000.0f;  // 2^kFloor is 0, and 0 * kFloor is not a NaN
 constexpr float kLog2e = 1.4426950408889634f;
@@ -236,12 +235,13 @@ struct Args {
     int* status;
 };
 
-// What a warp holds of the top entries' candidates: vectors whose maximum
-// reached the bound when they passed, and entries taken out of such vectors.
+// Entries a warp holds as candidates for the top ones.
 struct Tops {
     uint64_t room[kRoom];
-    int32_t list[kList];
 };
+// The vectors whose maximum reached the bound when they passed, with their
+// numbers: room for a few times what five doublings of the row seen leave.
+__host__ __device__ constexpr int list_of(int k) { return k > 0 ? 64 + 4 * k : 0; }
 
 // The warp's n entries cut to the best k, in order; returns their number.
 __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
@@ -287,29 +287,31 @@ __device__ __forceinline__ Held offer(Tops& w, Held h, float v, int64_t column, 
     return h;
 }
 
-// Reads the noted vectors again (they are in L2 as a rule) and offers their
-// entries, 32 vectors at a time; or, where a warp had more to note than its
-// list takes, all its vectors v = first + stride i < nv.
+// Offers the entries of the noted vectors that reach the bound of now, 32 at a
+// time; or, where a warp had more to note than its list takes, reads all its
+// vectors again, first + lane + stride i.
 template <typename T>
-__device__ __noinline__ Held look_into(Tops& w, int noted, Held h, const uint4* xv, int64_t col0,
-                                       int k, int lane, bool listed, int32_t first, int32_t stride,
-                                       int32_t nv)
+__device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t* number, int noted,
+                                       bool over, Held h, const uint4* xv, int64_t col0, int k,
+                                       int lane, int32_t first, int32_t stride, int32_t nv)
 {
     constexpr int N = Vec<T>::N;
     __syncwarp();
-    for (int32_t i0 = 0; i0 < noted; i0 += 32) {
-        const int32_t v = !listed ? i0 / 32 * stride + first + lane
-                                  : (i0 + lane < noted ? w.list[i0 + lane] : nv);
+    const int32_t n = over ? (nv + stride - 1) / stride * 32 : noted;
+    for (int32_t i0 = 0; i0 < n; i0 += 32) {
+        const int32_t i = i0 + lane;
+        const int32_t v = i >= n ? nv : (over ? i / 32 * stride + first + lane : number[i]);
         const bool live = v < nv;
-        const uint4 u = live ? __ldg(xv + v) : make_uint4(0, 0, 0, 0);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (live) u = over ? __ldg(xv + v) : list[i];
         const float least = value_of(static_cast<uint32_t>(h.bound >> 32));
         if (!__any_sync(0xffffffffu, live && !(Vec<T>::top(packed_max<T>(u)) < least))) continue;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
+        for (int j = 0; j < N / 2; ++j) {
             float a, b;
-            split(Vec<T>::two(u, i), a, b);
-            h = offer(w, h, a, col0 + static_cast<int64_t>(v) * N + 2 * i, live, k, lane);
-            h = offer(w, h, b, col0 + static_cast<int64_t>(v) * N + 2 * i + 1, live, k, lane);
+            split(Vec<T>::two(u, j), a, b);
+            h = offer(w, h, a, col0 + static_cast<int64_t>(v) * N + 2 * j, live, k, lane);
+            h = offer(w, h, b, col0 + static_cast<int64_t>(v) * N + 2 * j + 1, live, k, lane);
         }
     }
     __syncwarp();
@@ -342,11 +344,11 @@ __device__ __forceinline__ void join_lanes(Stats& st, float c)
 // ln s - ln 2 w / s, both terms not negative.
 //
 // Top entries: the threads' maxima so far, by groups of lanes, are distinct
-// entries of the row, so the k-th largest of them bounds the k-th largest
-// entry from below.  It becomes the bound after the first and the fourth tile
-// and after the last.  In the loop a vector costs one comparison of its
-// maximum with the bound; those that reach it are noted by number only, and
-// looked into after the last bound, which leaves a few entries more than k.
+// entries of the row, and what k of them reach bounds the k-th largest entry
+// from below.  The bound is set after tiles 0, 1, 3, 7 ... and after the last.
+// In the loop a tile costs one comparison of its maximum with the bound; its
+// vectors that reach it, some five times k in all, are kept aside and looked
+// into after the last bound, which leaves a few entries more than k.
 template <typename T, int WARPS, bool TOP>
 __global__ void __launch_bounds__(32 * kWarps, 4)
     forge_token_logprob_kernel(const T* logits, const Args p, int split)
@@ -357,9 +359,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     constexpr int kGroupLanes = kThreads > kGroups ? kThreads / kGroups : 1;
     constexpr int kUsed = kThreads / kGroupLanes;  // groups of a row: 32 or 64
     constexpr int F = kTile<WARPS>;
+    extern __shared__ uint4 s_lists[];  // each warp's noted vectors, then all their numbers
     __shared__ Tops s_tops[TOP ? kWarps : 1];
-    __shared__ float s_group[2][kRows][kUsed];
-    __shared__ float s_kth[kRows];
+    __shared__ float s_group[kRows][kUsed];
     __shared__ int s_held[kWarps];
     __shared__ Stats s_stats[kWarps];
     __shared__ Stats s_row[kRows];
@@ -413,13 +415,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 
     Stats st{-INFINITY, 0.0f, 0.0f, false};
     Tops& tops = s_tops[TOP ? warp : 0];
+    const int room = list_of(k);
+    uint4* const list = s_lists + warp * room;
+    int32_t* const number = reinterpret_cast<int32_t*>(s_lists + kWarps * room) + warp * room;
     if constexpr (TOP)
         if (rwarp == 0) s_best[mine][lane] = 0;  // no entry
     Held held{0, 0};               // the warp's entries
     float bound_v = -INFINITY;     // the value of held.bound
     int noted = 0;                 // the warp's vectors
     bool over = false;             // there were more than the list takes
-    int turn = 0;                  // times the bound was set
 
     auto raise = [&](float m) {  // m moves the reference of the thread's sums
         if (m > st.m) {
@@ -432,33 +436,39 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             st.m = m;
         }
     };
-    // The k-th largest of the groups' maxima as the bound: a thread counts its
-    // share of the groups above its own.
-    auto tighten = [&] {
+    // A bound from the groups' maxima: the largest value found in eight
+    // halvings that at least k of them reach.  Only where `wait` is set are the
+    // other warps' maxima those of now; an older one (a word is read whole, and
+    // maxima only grow) leaves the bound lower, which changes what is looked
+    // into but not what is found.
+    auto tighten = [&](bool wait) {
         float g = st.m;
 #pragma unroll
         for (int o = 1; o < kGroupLanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        const int group = tid / kGroupLanes, share = tid % kGroupLanes;
-        float* groups = s_group[turn & 1][mine];  // the other half may still be read
-        ++turn;
-        if (share == 0) groups[group] = g;
-        sync();
-        int above = 0;
-#pragma unroll
-        for (int i = 0; i < kUsed / kGroupLanes; ++i) {
-            const int j = i * kGroupLanes + share;
-            const float o = groups[j];
-            above += o > g || (o == g && j < group);
+        volatile float* groups = s_group[mine];
+        if (tid % kGroupLanes == 0) groups[tid / kGroupLanes] = g;
+        if (wait)
+            sync();
+        else
+            __syncwarp();
+        const uint32_t a = key_of(groups[lane]);
+        const uint32_t b = kUsed > 32 ? key_of(groups[lane + kUsed - 32]) : 0;
+        uint32_t high = __reduce_max_sync(0xffffffffu, a > b ? a : b);
+        uint32_t low = __reduce_min_sync(0xffffffffu, kUsed > 32 && b < a ? b : a);  // all reach it
+        low = max(low, static_cast<uint32_t>(held.bound >> 32));
+        for (int i = 0; i < 8 && low < high; ++i) {
+            const uint32_t middle = high - (high - low) / 2;
+            const int n = __popc(__ballot_sync(0xffffffffu, a >= middle)) +
+                          __popc(__ballot_sync(0xffffffffu, kUsed > 32 && b >= middle));
+            if (n >= k)
+                low = middle;
+            else
+                high = middle - 1;
         }
-#pragma unroll
-        for (int o = 1; o < kGroupLanes; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-        if (above == k - 1) s_kth[mine] = g;
-        sync();
-        const float kth = s_kth[mine];
-        const uint64_t floor = static_cast<uint64_t>(key_of(kth)) << 32;
+        const uint64_t floor = static_cast<uint64_t>(low) << 32;
         if (floor > held.bound) {
             held.bound = floor;
-            bound_v = kth;
+            bound_v = value_of(low);
         }
     };
 
@@ -514,6 +524,28 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         seen = Vec<T>::max2(seen, pm);
         const float tm = Vec<T>::top(pm);
         raise(tm);
+        if constexpr (TOP) {  // before the sums: the tile's registers end with them
+            if (tile == 0 || ((tile & (tile + 1)) == 0 && tile + 1 < tiles)) tighten(tile == 0);
+            if (__any_sync(0xffffffffu, !(tm < bound_v))) {
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const int32_t v = (tile * F + f) * kThreads + tid;
+                    const bool pass = !(Vec<T>::top(packed_max<T>(u[f])) < bound_v) && v < nv;
+                    const uint32_t all = __ballot_sync(0xffffffffu, pass);
+                    if (all == 0) continue;
+                    if (noted <= room - 32) {
+                        const int i = noted + __popc(all & ((1u << lane) - 1u));
+                        if (pass) {
+                            list[i] = u[f];
+                            number[i] = v;
+                        }
+                        noted += __popc(all);
+                    } else {
+                        over = true;
+                    }
+                }
+            }
+        }
         const float mr = st.m == -INFINITY ? 0.0f : st.m;
         const Pair mm = pair(-mr, -mr), cc = pair(c, c);
         Pair s2 = pair(st.s, 0.0f), w2 = pair(st.w, 0.0f);
@@ -534,31 +566,12 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         st.s = a + b;
         ::forge::logprob::split(w2, a, b);
         st.w = a + b;
-
-        if constexpr (TOP) {
-            if ((tile & (tile + 1)) == 0 && (tile == 0 || tiles > 2 * tile)) tighten();  // 0, 1, 3, 7, ...
-            if (__any_sync(0xffffffffu, !(tm < bound_v))) {
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    const int32_t v = (tile * F + f) * kThreads + tid;
-                    const bool pass = !(Vec<T>::top(packed_max<T>(u[f])) < bound_v) && v < nv;
-                    const uint32_t all = __ballot_sync(0xffffffffu, pass);
-                    if (noted <= kList - 32) {
-                        if (pass) tops.list[noted + __popc(all & ((1u << lane) - 1u))] = v;
-                        noted += __popc(all);
-                    } else {
-                        over = over || all != 0;
-                    }
-                }
-            }
-        }
     }
     if constexpr (TOP) {
-        if (tiles > 1) tighten();
-        held = look_into<T>(tops, over ? (nv + kThreads - 1) / kThreads * 32 : noted, held, xv, col0, k,
-                            lane, !over, tid - lane, kThreads, nv);
+        if (tiles > 1) tighten(false);
+        held = look_into<T>(tops, list, number, noted, over, held, xv, col0, k, lane, tid - lane,
+                            kThreads, nv);
     }
-
     const float top = Vec<T>::top(seen);
     st.nan = st.nan || top != top;
 
@@ -609,8 +622,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
                     if (warp < split) {
                         const uint64_t own = tops.room[lane];
                         int rank = lane;
-                        for (int w = 0; w < split; ++w) {
-                            if (w == warp) continue;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) {
+                            if (w == warp || w >= split) continue;
                             int better = 0;
 #pragma unroll
                             for (int b = kMaxTop / 2; b > 0; b >>= 1)
@@ -776,6 +790,7 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.R + rows - 1) / rows * split));
     cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = static_cast<size_t>(list_of(p.top_k)) * kWarps * (16 + 4);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
