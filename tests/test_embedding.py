@@ -28,6 +28,9 @@ def token_ids(T, V, seed, kind="zipf"):
         ids = torch.full((T,), V // 2)
     elif kind == "two":
         ids = torch.where(torch.rand(T, generator=g) < 0.5, 0, V - 1)
+    elif kind == "huge":  # rows of several thousand tokens side by side in the order, and a few medium ones
+        rows = torch.tensor([5, 133, 261, 389, 7]) % V
+        ids = rows[torch.multinomial(torch.tensor([0.4, 0.3, 0.25, 0.03, 0.02]), T, replacement=True, generator=g)]
     elif kind == "pad":
         return torch.full((T,), -1)
     elif kind == "ordered":
@@ -106,7 +109,8 @@ GRADS = [(0, 5, 3, "zipf"), (1, 1, 1, "zipf"), (1, 1000, 4096, "uniform"), (7, 3
          (130, 1000, 264, "zipf"), (1000, 50, 1023, "zipf"), (1000, 70000, 8, "uniform"),
          (5000, 300, 520, "zipf"), (4097, 2, 130, "two"), (3000, 100, 256, "one"), (20000, 1, 16, "one"),
          (513, 40, 72, "pad"), (4096, 4096, 96, "ordered"), (300, 20000, 1000, "zipf"),
-         (40000, 3000, 33, "zipf"), (2048, 128, 2056, "zipf")]
+         (40000, 3000, 33, "zipf"), (2048, 128, 2056, "zipf"), (12000, 500, 300, "huge"),
+         (9000, 400, 7, "huge"), (17, 4, 520, "one"), (16, 4, 520, "one"), (2049, 9, 264, "one")]
 
 
 @gpu
@@ -192,6 +196,27 @@ def test_gradient_bad_ids_streams_and_graphs(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dW, other)
+
+
+@gpu
+def test_gradient_past_32_bit_offsets(cuda_device):
+    T, D = 33000, 65540  # 2.2e9 elements of dY
+    dY = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    dY[-1], dY[0] = 2.0, 1.0
+    ids = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    ids[-1], ids[0] = 1, 1
+    dW = torch.empty(3, D, device="cuda")
+    fg.forge_embedding_grad(dY, ids, dW)
+    assert dW[1].eq(3).all() and not dW[0].any() and not dW[2].any()
+    del dY, dW
+    V, D = 70000, 32768  # 2.3e9 elements of dW
+    dW = torch.empty(V, D, device="cuda")
+    ids = torch.tensor([V - 1, 0, V - 1], device="cuda")
+    dY = torch.ones(3, D, device="cuda")
+    fg.forge_embedding_grad(dY, ids, dW, scale=0.5)
+    assert dW[V - 1].eq(1).all() and dW[0].eq(0.5).all() and not dW[1:V - 1].any()
+    fg.forge_embedding_grad(dY, ids, dW, scale=0.5, accumulate=True)
+    assert dW[V - 1].eq(2).all() and dW[0].eq(1).all() and not dW[V - 2].any()
 
 
 # ---- gradient + AdamW -----------------------------------------------------------

@@ -339,8 +339,8 @@ extern "C" forge_status forge_clip_grads(const void* const* grads, const int64_t
     if ((st = device_sms(&sms)) != FORGE_OK) return st;
     const void* one[] = {norm};
     if ((st = device_resident(one, 1)) != FORGE_OK) return st;
-    if ((st = check_memory(grads, n, P, dtype)) != FORGE_OK ||
-        (st = check_memory(out, n, P, out_dtype)) != FORGE_OK)
+    if ((st = check_memory(grads, n, P, dtype)) != FORGE_OK) return st;
+    if ((out != grads || out_dtype != dtype) && (st = check_memory(out, n, P, out_dtype)) != FORGE_OK)
         return st;
     if (!aligned(norm, 4)) return FORGE_ERR_MISALIGNED;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

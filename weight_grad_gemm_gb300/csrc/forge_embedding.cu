@@ -1030,7 +1030,9 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
         const int64_t columns = vec ? Span<A, true>::columns : Span<A, false>::columns;
         const int64_t units = T * ((D + columns - 1) / columns);
         const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
-        const int blocks = static_cast<int>(want < 8LL * sms ? want : 8LL * sms);
+        // 64 blocks an SM: a few spans a warp, and blocks that end are replaced
+        // (65536 x 4096 fp32 to bf16, Zipf tokens: 153 us; eight resident ones 157)
+        const int blocks = static_cast<int>(want < 64LL * sms ? want : 64LL * sms);
         if (vec)
             forge_embedding_kernel<A, B, true><<<blocks, kThreads, 0, s>>>(
                 ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
