@@ -330,20 +330,26 @@ def forge_owner_sgdm(G, W, mom, *, lr, momentum, wd, stream=None):
     _check(s, "forge_owner_sgdm")
 
 
+_codes = {}  # torch dtype -> forge_dtype, filled on first use
+
+
+def _code(t, allowed, what) -> int:
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: FORGE_BF16, torch.float32: FORGE_F32,
+                       torch.int32: FORGE_I32, torch.int64: FORGE_I64})
+    code = _codes.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{what}, got {t.dtype}")
+    return code
+
+
 def _id_code(t) -> int:
-    import torch
-    if t.dtype == torch.int32:
-        return FORGE_I32
-    if t.dtype == torch.int64:
-        return FORGE_I64
-    raise TypeError(f"token ids must be int32 or int64, got {t.dtype}")
+    return _code(t, (FORGE_I32, FORGE_I64), "token ids must be int32 or int64")
 
 
 def _float_code(t) -> int:
-    code = _dtype_code(t)
-    if code == FORGE_E4M3:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return code
+    return _code(t, (FORGE_BF16, FORGE_F32), "bfloat16 or float32 expected")
 
 
 def _rows(t, what):
@@ -362,8 +368,7 @@ def _vector(t, n, what):
     """Pointer of an fp32 tensor of n elements, or None."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.float32 or t.numel() != n:
+    if t.numel() != n or _float_code(t) != FORGE_F32:
         raise ValueError(f"{what} must be float32 with {n} elements")
     return _ptr(t)
 
@@ -375,7 +380,6 @@ def forge_token_logprob(logits, targets, logprob, *, lse=None, entropy=None, top
     entries top_index [R, k] (int32), top_logprob [R, k] of each row.  targets
     [R] int32 or int64, negative for padding; logprob and targets may both be
     None (see include/forge.h)."""
-    import torch
     lp, ld = _rows(logits, "logits")
     R, V = logits.shape
     if targets is not None and targets.numel() != R:
@@ -387,7 +391,7 @@ def forge_token_logprob(logits, targets, logprob, *, lse=None, entropy=None, top
         k = top_index.shape[-1]
         if tuple(top_index.shape) != (R, k) or tuple(top_logprob.shape) != (R, k):
             raise ValueError(f"top_index and top_logprob must be [R={R}, k]")
-        if top_index.dtype != torch.int32 or top_logprob.dtype != torch.float32:
+        if _id_code(top_index) != FORGE_I32 or _float_code(top_logprob) != FORGE_F32:
             raise TypeError("top_index must be int32 and top_logprob float32")
     s = lib().forge_token_logprob(lp, _float_code(logits), R, V, ld, _ptr(targets),
                                   FORGE_I32 if targets is None else _id_code(targets), scale,
@@ -435,9 +439,8 @@ def forge_embedding(ids, W, Y, *, scale=1.0, stream=None):
 def forge_embedding_grad(dY, ids, dW, *, scale=1.0, accumulate=False, stream=None):
     """dW [V, D] (fp32) = scale * the sum of dY [T, D] (bf16 or fp32) by ids, or
     that added to dW (accumulate)."""
-    import torch
     T, V, D = _embedding_sizes(ids, dY, dW.shape)
-    if dW.dtype != torch.float32:
+    if _float_code(dW) != FORGE_F32:
         raise TypeError("dW must be float32")
     s = lib().forge_embedding_grad(_ptr(dY), _float_code(dY), _ptr(ids), _id_code(ids), T, V, D,
                                    scale, _ptr(dW), int(bool(accumulate)), _stream(stream, dW))
@@ -448,11 +451,10 @@ def forge_embedding_adamw(dY, ids, W, m, v, *, lr, beta1, beta2, eps, wd, step, 
                           stream=None):
     """The sum of dY [T, D] by ids as the gradient of one AdamW step on W (fp32),
     m, v (fp32 or bf16), all [V, D], in one pass over them."""
-    import torch
     T, V, D = _embedding_sizes(ids, dY, W.shape)
     if tuple(m.shape) != (V, D) or tuple(v.shape) != (V, D):
         raise ValueError(f"W/m/v must be [V={V}, D={D}]")
-    if W.dtype != torch.float32 or m.dtype != v.dtype:
+    if _float_code(W) != FORGE_F32 or m.dtype != v.dtype:
         raise TypeError("W must be float32, m and v one dtype")
     s = lib().forge_embedding_adamw(_ptr(dY), _float_code(dY), _ptr(ids), _id_code(ids), T, V, D,
                                     scale, _ptr(W), _ptr(m), _ptr(v), _float_code(m), lr, beta1,

@@ -80,25 +80,20 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
         __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
 }
 
-// One warp per (token, span of columns), four 16-byte loads (VEC: rows of
-// whole vectors) or eight single ones in flight per lane, so that even a
-// decode step's few tokens spread over the SMs.  Bound by HBM; W's rows keep
-// their place in L2 (frequent tokens), Y streams past it.
-template <typename W, bool VEC>
-struct Span {
-    static constexpr int vec = VEC ? 16 / static_cast<int>(sizeof(W)) : 1;
-    static constexpr int flight = VEC ? 4 : 8;
-    static constexpr int columns = 32 * vec * flight;
-};
-
-template <typename W, typename Y, bool VEC>
+// One warp per (token, span of columns), so that even a decode step's few
+// tokens spread over the SMs, with the next token's id on its way.  VEC: rows
+// of whole 16-byte vectors, FLIGHT of them in flight per lane; otherwise single
+// elements, 32 apart.  Bound by HBM; W's rows keep their place in L2 (frequent
+// tokens), Y streams past it.
+template <typename W, typename Y, bool VEC, int FLIGHT>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_kernel(const void* ids, bool wide, const W* __restrict__ w, Y* __restrict__ y,
                            int64_t T, int64_t V, int64_t D, float scale, int* status)
 {
-    using S = Span<W, VEC>;
+    constexpr int N = VEC ? 16 / static_cast<int>(sizeof(W)) : 1;
+    constexpr int kColumns = 32 * N * FLIGHT;
     const int lane = threadIdx.x & 31;
-    const int64_t spans = (D + S::columns - 1) / S::columns;
+    const int64_t spans = (D + kColumns - 1) / kColumns;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     const int64_t step_tokens = warps / spans, step_spans = warps - step_tokens * spans;
     const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -111,13 +106,14 @@ __global__ void __launch_bounds__(kThreads)
     int64_t next = id_at(t);
     while (t < T) {
         int64_t r = next;
-        const int64_t c0 = span * S::columns + lane * S::vec;
+        const int64_t c0 = span * kColumns + lane * N;
         if (r >= V) {
             bad_id(status);
             r = -1;
         }
-        W const* const src = w + r * D;
-        Y* dst = y + t * D;
+        W const* const src = w + r * D + c0;
+        Y* const dst = y + t * D + c0;
+        const int left = static_cast<int>(D - c0 < kColumns ? D - c0 : kColumns);
         t += step_tokens;
         span += step_spans;
         if (span >= spans) {
@@ -126,32 +122,28 @@ __global__ void __launch_bounds__(kThreads)
         }
         next = id_at(t);  // on its way while this span is moved
         if constexpr (VEC) {
-            uint4 v[S::flight];
+            uint4 v[FLIGHT];
 #pragma unroll
-            for (int i = 0; i < S::flight; ++i) {
-                const int64_t c = c0 + i * 32 * S::vec;
-                v[i] = r >= 0 && c < D ? __ldg(reinterpret_cast<const uint4*>(src + c))
-                                       : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < FLIGHT; ++i)
+                v[i] = r >= 0 && i * 32 * N < left
+                           ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 * N))
+                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < S::flight; ++i) {
-                const int64_t c = c0 + i * 32 * S::vec;
-                float x[S::vec];
+            for (int i = 0; i < FLIGHT; ++i) {
+                float x[N];
                 to_float(v[i], x);
 #pragma unroll
-                for (int k = 0; k < S::vec; ++k) x[k] *= scale;
-                if (c < D) store_vec<S::vec>(dst + c, x);
+                for (int k = 0; k < N; ++k) x[k] *= scale;
+                if (i * 32 * N < left) store_vec<N>(dst + i * 32 * N, x);
             }
         } else {
-            float x[S::flight];
+            W v[FLIGHT];
 #pragma unroll
-            for (int i = 0; i < S::flight; ++i) {
-                const int64_t c = c0 + i * 32;
-                x[i] = r >= 0 && c < D ? load1(src, c) * scale : 0.0f;
-            }
+            for (int i = 0; i < FLIGHT; ++i)
+                if (r >= 0 && i * 32 < left) v[i] = __ldg(src + i * 32);
 #pragma unroll
-            for (int i = 0; i < S::flight; ++i)
-                if (c0 + i * 32 < D) store1(dst, c0 + i * 32, x[i]);
+            for (int i = 0; i < FLIGHT; ++i)
+                if (i * 32 < left) store1(dst, i * 32, r >= 0 ? static_cast<float>(v[i]) * scale : 0.0f);
         }
     }
 }
@@ -176,6 +168,7 @@ constexpr int kClasses = 1 << kClassBits;
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderWarps = kOrderThreads / 32;
 constexpr int kDigitBits = 5;
+constexpr int kFewItems = 128;     // items of a list that is sorted by counting
 constexpr int kOrderShared = 4096;  // items of a list that is sorted in shared memory
 constexpr int kOrderSmem = 2 * kOrderShared * static_cast<int>(sizeof(int2));
 
@@ -290,7 +283,23 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     const int32_t part = (n + kOrderThreads - 1) / kOrderThreads * 32;
     const int32_t p0 = warp * part < n ? warp * part : n;
     const int32_t p1 = p0 + part < n ? p0 + part : n;
-    for (int shift = 0; (local_rows - 1) >> shift; shift += kDigitBits) {
+    if (n <= kFewItems) {  // an item's place is the number of those before it
+        if (threadIdx.x < n) {
+            const int2 item = src[threadIdx.x];
+            int32_t place = 0;
+#pragma unroll 4
+            for (int32_t j = 0; j < n; ++j) {
+                const int32_t key = src[j].x;
+                place += key < item.x || (key == item.x && j < static_cast<int32_t>(threadIdx.x));
+            }
+            dst[place] = item;
+        }
+        __syncthreads();
+        int2* t = src;
+        src = dst;
+        dst = t;
+    }
+    for (int shift = 0; n > kFewItems && (local_rows - 1) >> shift; shift += kDigitBits) {
         s_count[threadIdx.x] = 0;
         __syncthreads();
         for (int32_t i0 = p0; i0 < p1; i0 += 32 * kIdFlight) {
@@ -450,6 +459,10 @@ constexpr int kSlice = 256;
 
 // What becomes of a row's sum: dW written, dW added to, or the AdamW step.
 enum Sum { SUM_STORE = 0, SUM_ADD = 1, SUM_ADAMW = 2 };
+
+// How the columns lie: vectors of four in every array; in dW, W, m, v as flat
+// arrays only; or anyhow.
+enum Lie { LIE_VECTORS = 2, LIE_FLAT = 1, LIE_ANY = 0 };
 
 // A warp's part of a row: H vectors of N columns a lane, 32 N columns apart,
 // `width` columns from c0 on; the columns past D are left out.
@@ -733,6 +746,93 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
     }
 }
 
+// The same for a width that is no multiple of four, while dW, W, m, v are
+// aligned: vectors of four elements of the flat arrays, which may belong to two
+// rows; dY is read element by element.
+template <typename G, int MODE, int ST>
+__device__ __forceinline__ void dense_ragged(const G* dY, int64_t block, uint32_t V, int32_t D,
+                                             float scale, float* dW, const Order& o, int32_t turns,
+                                             const Params& p)
+{
+    constexpr uint32_t step = kThreads * 4;
+    const int64_t total = static_cast<int64_t>(V) * D;
+    const uint32_t step_rows = step / D, step_columns = step - step_rows * D;
+    auto places = [&](uint32_t r) {
+        return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
+    };
+    int64_t at = (block * turns * kThreads + threadIdx.x) * 4;
+    uint32_t row = static_cast<uint32_t>(at / D);
+    int32_t column = static_cast<int32_t>(at - static_cast<int64_t>(row) * D);
+    int2 s = places(row), s2 = column + 3 >= D ? places(row + 1) : make_int2(0, 0);
+    for (int32_t turn = 0; turn < turns && at < total; ++turn) {
+        const bool whole = at + 4 <= total;
+        const int m = D - column < 4 ? D - column : 4;  // of the first row
+        const bool short1 = s.y - s.x <= kShort, short2 = s2.y - s2.x <= kShort;
+        float g[4] = {}, w[4], a[4], b[4];
+        if (MODE == SUM_ADAMW && whole) {
+            StateIO<ST_F32>::ld4(p.W, at, w);
+            StateIO<ST>::ld4(p.s1, at, a);
+            StateIO<ST>::ld4(p.s2, at, b);
+        }
+        auto add = [&](int2 part, int k0, int k1, int32_t c) {  // elements k0 .. k1 from column c on
+            for (int32_t i = part.x; i < part.y; i += 2) {
+                const bool two = i + 1 < part.y;
+                const G* x0 = dY + static_cast<int64_t>(__ldg(o.order + i)) * D + c;
+                const G* x1 = dY + static_cast<int64_t>(__ldg(o.order + (two ? i + 1 : i))) * D + c;
+                float u[4], v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool in = k >= k0 && k < k1;
+                    u[k] = in ? load1(x0, k) : 0.0f;
+                    v[k] = in && two ? load1(x1, k) : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] = g[k] + u[k] + v[k];
+            }
+        };
+        if (s.y > s.x && short1) add(s, 0, m, column);
+        if (s2.y > s2.x && short2) add(s2, m, 4, -m);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) g[k] *= scale;
+        if (whole && short1 && short2) {
+            if constexpr (MODE == SUM_ADAMW) {
+                step4<OP_ADAMW>(p, g, w, a, b);
+                StateIO<ST_F32>::st4(p.W, at, w);
+                StateIO<ST>::st4(p.s1, at, a);
+                StateIO<ST>::st4(p.s2, at, b);
+            } else {
+                StateIO<ST_F32>::st4(dW, at, g);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (at + k >= total || !(k < m ? short1 : short2)) continue;
+                if constexpr (MODE == SUM_ADAMW) {
+                    float gs[4] = {g[k], g[k], g[k], g[k]}, ws[4], as[4], bs[4];
+                    ws[0] = ws[1] = ws[2] = ws[3] = StateIO<ST_F32>::ld(p.W, at + k);
+                    as[0] = as[1] = as[2] = as[3] = StateIO<ST>::ld(p.s1, at + k);
+                    bs[0] = bs[1] = bs[2] = bs[3] = StateIO<ST>::ld(p.s2, at + k);
+                    step4<OP_ADAMW>(p, gs, ws, as, bs);
+                    StateIO<ST_F32>::st(p.W, at + k, ws[0]);
+                    StateIO<ST>::st(p.s1, at + k, as[0]);
+                    StateIO<ST>::st(p.s2, at + k, bs[0]);
+                } else {
+                    StateIO<ST_F32>::st(dW, at + k, g[k]);
+                }
+            }
+        }
+        at += step;
+        row += step_rows;
+        column += step_columns;
+        if (column >= D) {
+            column -= D;
+            ++row;
+        }
+        s = places(row);
+        s2 = column + 3 >= D ? places(row + 1) : make_int2(0, 0);
+    }
+}
+
 // dW += the sums, over the rows that have a token only.  One warp per (four
 // places, 512 columns; 256 single ones) takes the rows of at most kShort tokens
 // that start there: two loads bring the places and all their tokens.
@@ -776,13 +876,14 @@ __device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t 
 // All rows in one launch: the blocks for the pieces of huge rows and for medium
 // rows come first, as they take longest, then those for the others.  Bound by
 // HBM: dW written, or W, m, v read and written, once, and dY read once.
-template <typename G, int MODE, int ST, bool VEC>
+template <typename G, int MODE, int ST, int LIE>
 __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
     forge_embedding_grad_kernel(const G* dY, int64_t T, int32_t V, int32_t D, float scale,
                                 float* dW, Order o, float* partial, uint32_t piece_blocks,
                                 uint32_t medium_blocks, int32_t turns, const Params p)
 {
     constexpr int kWarps = kThreads / 32;
+    constexpr bool VEC = LIE == LIE_VECTORS;
     const int warp = threadIdx.x >> 5;
     uint32_t block = blockIdx.x;
     if (block < piece_blocks) {
@@ -797,6 +898,8 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
     block -= medium_blocks;
     if constexpr (MODE == SUM_ADD)
         touched_rows<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, scale, dW, o);
+    else if constexpr (LIE == LIE_FLAT)
+        dense_ragged<G, MODE, ST>(dY, block, V, D, scale, dW, o, turns, p);
     else
         dense_rows<G, MODE, ST, VEC>(dY, block, V, D, scale, dW, o, turns, p);
 }
@@ -899,7 +1002,7 @@ cudaError_t order_tokens(const void* ids, int64_t T, int64_t V, const Order& o, 
     return cudaGetLastError();
 }
 
-template <typename G, int MODE, int ST, bool VEC>
+template <typename G, int MODE, int ST, int LIE>
 cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scale, float* dW,
                         const Order& o, float* partial, const Params& p, int sms, cudaStream_t s)
 {
@@ -909,13 +1012,14 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     const int64_t medium_blocks = T > kShort ? (T + kMediumPlaces - 1) / kMediumPlaces * slices : 0;
     int64_t turns = 1, blocks;
     if (MODE == SUM_ADD) {
+        constexpr int columns = kTouchColumns<LIE == LIE_VECTORS>;
         const int64_t touch_units =
-            (T + kTouchPlaces - 1) / kTouchPlaces * ((D + kTouchColumns<VEC> - 1) / kTouchColumns<VEC>);
+            (T + kTouchPlaces - 1) / kTouchPlaces * ((D + columns - 1) / columns);
         blocks = (touch_units + kThreads / 32 - 1) / (kThreads / 32);
     } else {
         // as many turns, up to eight, as leave each SM 32 blocks
-        const int64_t width = VEC ? D / 4 : D;
-        const int64_t tiles = (V * width + kThreads * kUnits<VEC> - 1) / (kThreads * kUnits<VEC>);
+        const int64_t elements = V * D, tile = kThreads * (LIE == LIE_VECTORS ? 8 : 4);
+        const int64_t tiles = (elements + tile - 1) / tile;
         turns = tiles / (32LL * sms);
         turns = turns < 1 ? 1 : (turns > 8 ? 8 : turns);
         while ((tiles + turns - 1) / turns > INT32_MAX / 2) turns *= 2;
@@ -923,7 +1027,7 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     }
     const int64_t all = piece_blocks + medium_blocks + blocks;
     if (all > INT32_MAX) return cudaErrorInvalidConfiguration;
-    forge_embedding_grad_kernel<G, MODE, ST, VEC><<<static_cast<unsigned>(all), kThreads, 0, s>>>(
+    forge_embedding_grad_kernel<G, MODE, ST, LIE><<<static_cast<unsigned>(all), kThreads, 0, s>>>(
         dY, T, static_cast<int32_t>(V), static_cast<int32_t>(D), scale, dW, o, partial,
         static_cast<uint32_t>(piece_blocks), static_cast<uint32_t>(medium_blocks),
         static_cast<int32_t>(turns), p);
@@ -935,7 +1039,7 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     return cudaGetLastError();
 }
 
-template <typename G, bool VEC>
+template <typename G, int LIE>
 cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids, bool wide,
                         int64_t T, int64_t V, int64_t D, float scale, float* dW, const Params& p,
                         int sms, cudaStream_t s)
@@ -964,13 +1068,13 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
     }
     if (e == cudaSuccess) {
         if (what == SUM_STORE)
-            e = launch_sums<G, SUM_STORE, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+            e = launch_sums<G, SUM_STORE, ST_F32, LIE>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
         else if (what == SUM_ADD)
-            e = launch_sums<G, SUM_ADD, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+            e = launch_sums<G, SUM_ADD, ST_F32, LIE == LIE_VECTORS ? LIE : LIE_ANY>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
         else if (state_bf16)
-            e = launch_sums<G, SUM_ADAMW, ST_BF16, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+            e = launch_sums<G, SUM_ADAMW, ST_BF16, LIE>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
         else
-            e = launch_sums<G, SUM_ADAMW, ST_F32, VEC>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
+            e = launch_sums<G, SUM_ADAMW, ST_F32, LIE>(dY, T, V, D, scale, dW, o, partial, p, sms, s);
     }
     if (scratch) {
         const cudaError_t fe = scratch_free(scratch, s);
@@ -985,12 +1089,15 @@ cudaError_t grad(Sum what, bool state_bf16, const void* dY, forge_dtype dy_dtype
 {
     const bool wide = id_dtype == FORGE_I64;
     const uintptr_t sa = state_bf16 ? 8 : 16;
-    const bool vec = D % 4 == 0 && aligned(dY, 4 * size_of(dy_dtype)) && aligned(dW, 16) &&
-                     aligned(p.W, 16) && aligned(p.s1, sa) && aligned(p.s2, sa);
+    const bool flat = aligned(dW, 16) && aligned(p.W, 16) && aligned(p.s1, sa) && aligned(p.s2, sa);
+    const bool vec = flat && D % 4 == 0 && aligned(dY, 4 * size_of(dy_dtype));
     auto go = [&](auto* d) {
         using G = std::remove_cv_t<std::remove_pointer_t<decltype(d)>>;
-        return vec ? launch_grad<G, true>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s)
-                   : launch_grad<G, false>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s);
+        if (vec)
+            return launch_grad<G, LIE_VECTORS>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s);
+        if (flat && D >= 4)
+            return launch_grad<G, LIE_FLAT>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s);
+        return launch_grad<G, LIE_ANY>(what, state_bf16, d, ids, wide, T, V, D, scale, dW, p, sms, s);
     };
     return dy_dtype == FORGE_F32 ? go(static_cast<const float*>(dY))
                                  : go(static_cast<const __nv_bfloat16*>(dY));
@@ -1025,20 +1132,22 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
     auto go = [&](auto* w, auto* y) {
         using A = std::remove_cv_t<std::remove_pointer_t<decltype(w)>>;
         using B = std::remove_pointer_t<decltype(y)>;
-        constexpr int64_t per = Span<A, true>::vec;
-        const bool vec = D % per == 0 && aligned(w, 16) && aligned(y, sizeof(B) * per < 16 ? 8 : 16);
-        const int64_t columns = vec ? Span<A, true>::columns : Span<A, false>::columns;
-        const int64_t units = T * ((D + columns - 1) / columns);
-        const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
-        // 64 blocks an SM: a few spans a warp, and blocks that end are replaced
-        // (65536 x 4096 fp32 to bf16, Zipf tokens: 153 us; eight resident ones 157)
-        const int blocks = static_cast<int>(want < 64LL * sms ? want : 64LL * sms);
-        if (vec)
-            forge_embedding_kernel<A, B, true><<<blocks, kThreads, 0, s>>>(
-                ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
+        constexpr int64_t per = 16 / static_cast<int64_t>(sizeof(A));
+        auto launch = [&](auto kernel, int64_t columns) {
+            const int64_t units = T * ((D + columns - 1) / columns);
+            const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
+            // 64 blocks an SM: a few spans a warp, and blocks that end are replaced
+            // (65536 x 4096 fp32 to bf16, Zipf tokens: 153 us; eight resident ones 157)
+            const int blocks = static_cast<int>(want < 64LL * sms ? want : 64LL * sms);
+            kernel<<<blocks, kThreads, 0, s>>>(ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
+        };
+        // single elements: as many in flight as a row has for each lane, up to 16
+        if (D % per == 0 && aligned(w, 16) && aligned(y, sizeof(B) * per < 16 ? 8 : 16))
+            launch(forge_embedding_kernel<A, B, true, 4>, 32 * per * 4);
+        else if (D <= 256)
+            launch(forge_embedding_kernel<A, B, false, 8>, 32 * 8);
         else
-            forge_embedding_kernel<A, B, false><<<blocks, kThreads, 0, s>>>(
-                ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
+            launch(forge_embedding_kernel<A, B, false, 16>, 32 * 16);
     };
     auto out = [&](auto* w) {
         if (y_dtype == FORGE_F32)
