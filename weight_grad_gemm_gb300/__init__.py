@@ -353,15 +353,17 @@ def _float_code(t) -> int:
 
 
 def _rows(t, what):
-    """Pointer and row stride of a 2-D tensor whose rows are contiguous."""
+    """Address, row stride, rows and columns of a 2-D tensor whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what} must be [R, V] with contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
+    R, V = shape
+    ld = strides[0] if R > 1 else V
+    if ld < V:
         raise ValueError(f"the rows of {what} overlap")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld, R, V
 
 
 def _vector(t, n, what):
@@ -380,8 +382,7 @@ def forge_token_logprob(logits, targets, logprob, *, lse=None, entropy=None, top
     entries top_index [R, k] (int32), top_logprob [R, k] of each row.  targets
     [R] int32 or int64, negative for padding; logprob and targets may both be
     None (see include/forge.h)."""
-    lp, ld = _rows(logits, "logits")
-    R, V = logits.shape
+    lp, ld, R, V = _rows(logits, "logits")
     if targets is not None and targets.numel() != R:
         raise ValueError(f"targets must have {R} elements")
     k = 0
@@ -406,10 +407,9 @@ def forge_token_logprob_grad(logits, targets, lse, grad_logprob, dlogits, *, ent
     """dlogits [R, V] (bf16 or fp32, rows of any stride; may be logits itself)
     of sum(grad_logprob * logprob + grad_entropy * entropy), from the lse and
     entropy that forge_token_logprob gave."""
-    lp, ld = _rows(logits, "logits")
-    dp, ldo = _rows(dlogits, "dlogits")
-    R, V = logits.shape
-    if tuple(dlogits.shape) != (R, V) or targets.numel() != R:
+    lp, ld, R, V = _rows(logits, "logits")
+    dp, ldo, *out = _rows(dlogits, "dlogits")
+    if out != [R, V] or targets.numel() != R:
         raise ValueError(f"dlogits must be [R={R}, V={V}] and targets [R]")
     s = lib().forge_token_logprob_grad(lp, _float_code(logits), R, V, ld, _ptr(targets),
                                        _id_code(targets), scale, _vector(lse, R, "lse"),

@@ -172,13 +172,43 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
 }
 
-// out = in times the factor.  The chunks are walked from the last to the
+// N elements as they lie in memory.
+template <typename T, int N>
+struct Group;
+template <>
+struct Group<float, 4> {
+    uint4 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[4]) const { to_float(u, x); }
+};
+template <>
+struct Group<__nv_bfloat16, 8> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[8]) const { to_float(u, x); }
+};
+template <>
+struct Group<__nv_bfloat16, 4> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[4]) const
+    {
+        x[0] = __uint_as_float(u.x << 16);
+        x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(u.y << 16);
+        x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    }
+};
+
+// out = in times the factor, in vectors of 16 bytes of the wider type, so that
+// a warp stores whole sectors.  The chunks are walked from the last to the
 // first: what the norm's pass read last is still in L2.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads)
     forge_clip_kernel(const __grid_constant__ Table t, const float* norm, float max_norm)
 {
-    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    constexpr int N = 16 / (sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
+    constexpr int F = N * sizeof(T) < 16 ? 2 * kFlight : kFlight;
     const float q = max_norm / (*norm + 1e-6f);
     const float m = q > 1.0f ? 1.0f : q;  // a NaN stays
     const uint32_t chunks = t.begin[t.count];
@@ -192,19 +222,19 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t left = t.n[j] - first;
         const int n = static_cast<int>(left < (1 << t.chunk_bits) ? left : 1 << t.chunk_bits);
         int done = 0;
-        if (is_aligned(g, 16) && is_aligned(o, N * sizeof(O) < 16 ? 8 : 16)) {
+        if (is_aligned(g, N * sizeof(T)) && is_aligned(o, N * sizeof(O))) {
             const int nv = n / N;
-            for (int v0 = threadIdx.x; v0 < nv; v0 += kFlight * kThreads) {
-                uint4 u[kFlight];
+            for (int v0 = threadIdx.x; v0 < nv; v0 += F * kThreads) {
+                Group<T, N> u[F];
 #pragma unroll
-                for (int f = 0; f < kFlight; ++f)
+                for (int f = 0; f < F; ++f)
                     if (v0 + f * kThreads < nv)
-                        u[f] = __ldcs(reinterpret_cast<const uint4*>(g) + v0 + f * kThreads);
+                        u[f].load(g + (v0 + f * kThreads) * N);
 #pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
+                for (int f = 0; f < F; ++f) {
                     if (v0 + f * kThreads >= nv) continue;
                     float x[N];
-                    to_float(u[f], x);
+                    u[f].get(x);
 #pragma unroll
                     for (int k = 0; k < N; ++k) x[k] *= m;
                     store_vec<N>(o + static_cast<int64_t>(v0 + f * kThreads) * N, x);

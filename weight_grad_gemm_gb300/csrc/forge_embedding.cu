@@ -42,22 +42,47 @@ __device__ __forceinline__ void bad_id(int* status)
 
 // ------------------------------------------------------------------ lookup
 
-__device__ __forceinline__ void to_float(const uint4& u, float (&x)[4])
-{
-    x[0] = __uint_as_float(u.x);
-    x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z);
-    x[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ void to_float(const uint4& u, float (&x)[8])
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// N elements as they lie in memory.
+template <typename T, int N>
+struct Group;
+template <>
+struct Group<float, 4> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[4]) const
+    {
+        x[0] = u.x;
+        x[1] = u.y;
+        x[2] = u.z;
+        x[3] = u.w;
     }
-}
+};
+template <int N>
+struct Group<__nv_bfloat16, N> {
+    uint32_t u[N / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p)
+    {
+        if constexpr (N == 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            u[0] = v.x;
+            u[1] = v.y;
+            u[2] = v.z;
+            u[3] = v.w;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            u[0] = v.x;
+            u[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+};
 template <int N>
 __device__ __forceinline__ void store_vec(float* p, const float (&x)[N])
 {
@@ -82,15 +107,18 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
 
 // One warp per (token, span of columns), so that even a decode step's few
 // tokens spread over the SMs, with the next token's id on its way.  VEC: rows
-// of whole 16-byte vectors, FLIGHT of them in flight per lane; otherwise single
-// elements, 32 apart.  Bound by HBM; W's rows keep their place in L2 (frequent
+// of whole vectors, 16 bytes of the wider type, FLIGHT of them in flight per
+// lane; otherwise single elements, 32 apart.  Bound by HBM; W's rows keep their place in L2 (frequent
 // tokens), Y streams past it.
+template <typename W, typename Y>
+constexpr int kLookupVec = 16 / (sizeof(W) > sizeof(Y) ? sizeof(W) : sizeof(Y));
+
 template <typename W, typename Y, bool VEC, int FLIGHT>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_kernel(const void* ids, bool wide, const W* __restrict__ w, Y* __restrict__ y,
                            int64_t T, int64_t V, int64_t D, float scale, int* status)
 {
-    constexpr int N = VEC ? 16 / static_cast<int>(sizeof(W)) : 1;
+    constexpr int N = VEC ? kLookupVec<W, Y> : 1;
     constexpr int kColumns = 32 * N * FLIGHT;
     const int lane = threadIdx.x & 31;
     const int64_t spans = (D + kColumns - 1) / kColumns;
@@ -122,18 +150,16 @@ __global__ void __launch_bounds__(kThreads)
         }
         next = id_at(t);  // on its way while this span is moved
         if constexpr (VEC) {
-            uint4 v[FLIGHT];
+            Group<W, N> v[FLIGHT];
 #pragma unroll
             for (int i = 0; i < FLIGHT; ++i)
-                v[i] = r >= 0 && i * 32 * N < left
-                           ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 * N))
-                           : make_uint4(0, 0, 0, 0);
+                if (r >= 0 && i * 32 * N < left) v[i].load(src + i * 32 * N);
 #pragma unroll
             for (int i = 0; i < FLIGHT; ++i) {
                 float x[N];
-                to_float(v[i], x);
+                v[i].get(x);
 #pragma unroll
-                for (int k = 0; k < N; ++k) x[k] *= scale;
+                for (int k = 0; k < N; ++k) x[k] = r >= 0 ? x[k] * scale : 0.0f;
                 if (i * 32 * N < left) store_vec<N>(dst + i * 32 * N, x);
             }
         } else {
@@ -1132,7 +1158,8 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
     auto go = [&](auto* w, auto* y) {
         using A = std::remove_cv_t<std::remove_pointer_t<decltype(w)>>;
         using B = std::remove_pointer_t<decltype(y)>;
-        constexpr int64_t per = 16 / static_cast<int64_t>(sizeof(A));
+        constexpr int64_t per = kLookupVec<A, B>;
+        constexpr int flight = per * sizeof(A) < 16 ? 8 : 4;
         auto launch = [&](auto kernel, int64_t columns) {
             const int64_t units = T * ((D + columns - 1) / columns);
             const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
@@ -1142,8 +1169,8 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
             kernel<<<blocks, kThreads, 0, s>>>(ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
         };
         // single elements: as many in flight as a row has for each lane, up to 16
-        if (D % per == 0 && aligned(w, 16) && aligned(y, sizeof(B) * per < 16 ? 8 : 16))
-            launch(forge_embedding_kernel<A, B, true, 4>, 32 * per * 4);
+        if (D % per == 0 && aligned(w, per * sizeof(A)) && aligned(y, per * sizeof(B)))
+            launch(forge_embedding_kernel<A, B, true, flight>, 32 * per * flight);
         else if (D <= 256)
             launch(forge_embedding_kernel<A, B, false, 8>, 32 * 8);
         else
