@@ -198,6 +198,12 @@ constexpr int kFewItems = 128;     // items of a list that is sorted by counting
 constexpr int kOrderShared = 4096;  // items of a list that is sorted in shared memory
 constexpr int kOrderSmem = 2 * kOrderShared * static_cast<int>(sizeof(int2));
 
+// The kernels that follow the order are launched while it runs, so that their
+// blocks stand ready when it ends; they wait here for its end (and the one
+// before) before they read anything.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Token order: order[i] the token at place i; at[i] = {its row, and the number
 // of the row's places if this is the first of them, else 0} ({-1, 0} past the
 // tokens that are not padding); seg[r] the places [x, y) of row r.  listA,
@@ -284,6 +290,8 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     if (cls == kClasses - 1)
         for (int64_t i = base + n + threadIdx.x; i < T; i += kOrderThreads)
             o.at[i] = make_int2(-1, 0);
+
+    let_next_start();
 
     // collect
     const bool shared = n <= kOrderShared;
@@ -912,6 +920,7 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
     constexpr bool VEC = LIE == LIE_VECTORS;
     const int warp = threadIdx.x >> 5;
     uint32_t block = blockIdx.x;
+    await_previous();
     if (block < piece_blocks) {
         sum_pieces<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, o, partial);
         return;
@@ -946,6 +955,7 @@ __global__ void __launch_bounds__(kThreads)
     const int32_t p0 = static_cast<int32_t>(blockIdx.x / slices * kMedium);
     const P part{static_cast<int64_t>(blockIdx.x % slices) * kSlice, D, lane};
     if (threadIdx.x == 0) s_n = 0;
+    await_previous();
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kMedium / kThreads; ++i) {
@@ -1053,16 +1063,25 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     }
     const int64_t all = piece_blocks + medium_blocks + blocks;
     if (all > INT32_MAX) return cudaErrorInvalidConfiguration;
-    forge_embedding_grad_kernel<G, MODE, ST, LIE><<<static_cast<unsigned>(all), kThreads, 0, s>>>(
-        dY, T, static_cast<int32_t>(V), static_cast<int32_t>(D), scale, dW, o, partial,
-        static_cast<uint32_t>(piece_blocks), static_cast<uint32_t>(medium_blocks),
-        static_cast<int32_t>(turns), p);
-    if (T > kMedium) {
-        const int64_t huge_blocks = (T + kMedium - 1) / kMedium * slices;
-        forge_embedding_huge_rows_kernel<MODE, ST>
-            <<<static_cast<unsigned>(huge_blocks), kThreads, 0, s>>>(T, D, scale, dW, o, partial, p);
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(all));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = early;
+    cfg.numAttrs = T > 0 ? 1 : 0;  // without tokens there is no kernel before
+    cudaError_t e = cudaLaunchKernelEx(
+        &cfg, forge_embedding_grad_kernel<G, MODE, ST, LIE>, dY, T, static_cast<int32_t>(V),
+        static_cast<int32_t>(D), scale, dW, o, partial, static_cast<uint32_t>(piece_blocks),
+        static_cast<uint32_t>(medium_blocks), static_cast<int32_t>(turns), p);
+    if (e == cudaSuccess && T > kMedium) {
+        cfg.gridDim = dim3(static_cast<unsigned>((T + kMedium - 1) / kMedium * slices));
+        e = cudaLaunchKernelEx(&cfg, forge_embedding_huge_rows_kernel<MODE, ST>, T, D, scale, dW, o,
+                               static_cast<const float*>(partial), p);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename G, int LIE>
