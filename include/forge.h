@@ -378,8 +378,8 @@ FORGE_API forge_status forge_owner_sgdm(const float* G, float* W, void* mom, int
  *           apart (ld >= V: a padded vocabulary).  Rows of any alignment.
  *   targets device [R] of id_dtype (FORGE_I32 or FORGE_I64), or NULL (then
  *           logprob is NULL too and every row counts).  A negative target
- *           marks padding: the row is not read, its logprob, lse, entropy and
- *           top_logprob are 0 and its top_index -1.  A target >= V is recorded
+ *           marks padding: nothing of the row counts, its logprob, lse, entropy
+ *           and top_logprob are 0 and its top_index -1.  A target >= V is recorded
  *           as FORGE_ERR_INVALID_ARG in the device status word and its row
  *           taken as padding.
  *   scale   > 0: the inverse temperature.

@@ -207,18 +207,6 @@ struct Stats {
     float m, s, w;
     bool nan;
 };
-__device__ __forceinline__ void join(Stats& a, const Stats& b, float c)
-{
-    const float m = fmaxf(a.m, b.m);
-    // a part without entries has s = w = 0 and m = -inf
-    const float da = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * c, kFloor);
-    const float db = b.m == -INFINITY ? 0.0f : fmaxf((b.m - m) * c, kFloor);
-    const float fa = exp2_approx(da), fb = exp2_approx(db);
-    a.w = fa * fmaf(da, a.s, a.w) + fb * fmaf(db, b.s, b.w);
-    a.s = fa * a.s + fb * b.s;
-    a.m = m;
-    a.nan = a.nan || b.nan;
-}
 
 struct Args {
     int64_t R, V, ld;
@@ -317,19 +305,29 @@ __device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t
     return h;
 }
 
-// The joined statistics of a group of WIDTH lanes, in every lane of it.
+// The joined statistics of a group of WIDTH lanes, in every lane of it: the
+// maximum first, so that a lane rescales its sums once.
 template <int WIDTH>
 __device__ __forceinline__ void join_lanes(Stats& st, float c)
 {
+    if constexpr (WIDTH == 1) return;
+    float m = st.m;
+    int nan = st.nan ? 1 : 0;
 #pragma unroll
     for (int o = WIDTH / 2; o > 0; o >>= 1) {
-        Stats b;
-        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        b.w = __shfl_xor_sync(0xffffffffu, st.w, o);
-        b.nan = __shfl_xor_sync(0xffffffffu, st.nan ? 1 : 0, o) != 0;
-        join(st, b, c);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        nan |= __shfl_xor_sync(0xffffffffu, nan, o);
     }
+    // a part without entries has s = w = 0 and m = -inf
+    const float d = st.m == -INFINITY ? 0.0f : fmaxf((st.m - m) * c, kFloor);
+    const float f = exp2_approx(d);
+    float w = f * fmaf(d, st.s, st.w), s = f * st.s;
+#pragma unroll
+    for (int o = WIDTH / 2; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
+    st = Stats{m, s, w, nan != 0};
 }
 
 // A row is the work of WARPS warps of a block (eight, or fewer where rows are
@@ -383,7 +381,36 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     const int part = static_cast<int>(blockIdx.x - block * split);
     const int64_t r = block * kRows + mine;
     if (r >= p.R) return;
+    const T* x = logits + r * p.ld;
     const int k = p.top_k;
+    const float c = p.scale * kLog2e;
+    const Split sp = split_row<N>(x, p.V);
+    const int64_t per = (sp.nvec + split - 1) / split;
+    const int64_t v0 = part * per < sp.nvec ? part * per : sp.nvec;
+    const int32_t nv = static_cast<int32_t>(v0 + per < sp.nvec ? per : sp.nvec - v0);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head) + v0;
+    const int64_t col0 = sp.head + v0 * N;
+
+    // whole tiles are read without a check; the last one may end early
+    const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+    const int32_t whole = nv / (F * kThreads);
+    const int32_t tiles = (nv + F * kThreads - 1) / (F * kThreads);
+    const uint4* at = xv + tid;
+    auto fetch = [&](int32_t tile, uint4 (&u)[F]) {
+        if (tile < whole) {
+#pragma unroll
+            for (int f = 0; f < F; ++f) u[f] = __ldcs(at + f * kThreads);
+        } else {
+            const int32_t left = nv - tile * F * kThreads - tid;
+#pragma unroll
+            for (int f = 0; f < F; ++f) u[f] = f * kThreads < left ? __ldcs(at + f * kThreads) : none;
+        }
+        at += F * kThreads;
+    };
+    constexpr bool kAhead = F <= 4;
+    uint4 next[kAhead ? F : 1];
+    if constexpr (kAhead)  // on its way while the target comes
+        if (tiles > 0) fetch(0, next);
     int64_t t = 0;
     if (p.targets) t = target_of(p.targets, p.wide, r, p.V, p.status);
     if (t < 0) {  // padding: all the row's warps leave
@@ -402,15 +429,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         return;
     }
 
-    const T* x = logits + r * p.ld;
     const float x_t = tid == 0 && p.logprob ? load1(x, t) : 0.0f;
-    const float c = p.scale * kLog2e;
-    const Split sp = split_row<N>(x, p.V);
-    const int64_t per = (sp.nvec + split - 1) / split;
-    const int64_t v0 = part * per < sp.nvec ? part * per : sp.nvec;
-    const int32_t nv = static_cast<int32_t>(v0 + per < sp.nvec ? per : sp.nvec - v0);
-    const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head) + v0;
-    const int64_t col0 = sp.head + v0 * N;
 
     Stats st{-INFINITY, 0.0f, 0.0f, false};
     Tops& tops = s_tops[TOP ? warp : 0];
@@ -487,27 +506,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         if constexpr (TOP) held = offer(tops, held, v, column, live, k, lane);
     }
 
-    // whole tiles are read without a check; the last one may end early
-    const uint4 none = make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
-    const int32_t whole = nv / (F * kThreads);
-    const int32_t tiles = (nv + F * kThreads - 1) / (F * kThreads);
-    const uint4* at = xv + tid;
-    auto fetch = [&](int32_t tile, uint4 (&u)[F]) {
-        if (tile < whole) {
-#pragma unroll
-            for (int f = 0; f < F; ++f) u[f] = __ldcs(at + f * kThreads);
-        } else {
-            const int32_t left = nv - tile * F * kThreads - tid;
-#pragma unroll
-            for (int f = 0; f < F; ++f) u[f] = f * kThreads < left ? __ldcs(at + f * kThreads) : none;
-        }
-        at += F * kThreads;
-    };
-    constexpr bool kAhead = F <= 4;
     uint32_t seen = Vec<T>::kNone;  // the packed maximum of everything: keeps a NaN
-    uint4 next[kAhead ? F : 1];
-    if constexpr (kAhead)
-        if (tiles > 0) fetch(0, next);
     for (int32_t tile = 0; tile < tiles; ++tile) {
         uint4 u[F];
         if constexpr (kAhead) {
