@@ -227,8 +227,10 @@ struct Tops {
     uint64_t room[kRoom];
 };
 // The vectors whose maximum reached the bound when they passed, with their
-// numbers: room for a few times what five doublings of the row seen leave.
-__host__ __device__ constexpr int list_of(int k) { return k > 0 ? 64 + 4 * k : 0; }
+// numbers: room for what the doublings of the row seen leave as a rule (with
+// 64 + 4 k, 8192 x 131072 bf16 on one warp a row and five alternatives ran over
+// and took 639 instead of 338 us).
+__host__ __device__ constexpr int list_of(int k) { return k > 0 ? 160 + 2 * k : 0; }
 
 // The warp's n entries cut to the best k, in order; returns their number.
 __device__ __forceinline__ int keep_best(uint64_t* room, int n, int k, int lane)
@@ -830,16 +832,19 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
 }
 
 // Few warps a row, so that the joins at a row's end are few and other rows'
-// loads cover them: one up to 1024 vectors (16384 rows of 8000 bf16 with five
-// alternatives: 94 us, two warps 103, eight 188), two up to 4096 (16384 x 16000
-// fp32: 185 us; four 208, one 245), four beyond (8192 x 131072 bf16: 356 us;
-// two 514, eight 370); more while the rows' warps do not fill the SMs, and
-// then clusters of up to eight blocks.
+// loads cover them, but not so few that the last rows end late, and enough to
+// bound many alternatives well.  With five alternatives: 8000 x 7397 fp32 (1849
+// vectors) one warp 50 us, two 62, four 78; 8192 x 50001 bf16 (6250) 153, 164,
+// 190; 8192 x 131072 bf16 (16384) 338, 345, 350, and without any 332, 328, 310.
+// With twenty: 63, 70, 88; 410, 189, 213; 962, 376, 385.  With 32: 161, 79, 94;
+// 490, 207, 231; 1056, 497, 414.  More warps while the rows' warps do not fill
+// the SMs, then clusters of up to eight blocks.
 template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
-    int warps = nvec <= 1024 ? 1 : (nvec <= 4096 ? 2 : 4);
+    const int64_t one = p.top_k <= 8 ? 4096 : (p.top_k <= 20 ? 2048 : 0);
+    int warps = nvec <= one ? 1 : (nvec <= 12288 ? 2 : 4);
     while (warps < kWarps && p.R * warps < 12 * sms) warps *= 2;
     if (warps == 1) return launch_forward<T, 1>(x, p, 1, s);
     if (warps == 2) return launch_forward<T, 2>(x, p, 1, s);
