@@ -382,7 +382,7 @@ FORGE_API forge_status forge_owner_sgdm(const float* G, float* W, void* mom, int
  *           and top_logprob are 0 and its top_index -1.  A target >= V is recorded
  *           as FORGE_ERR_INVALID_ARG in the device status word and its row
  *           taken as padding.
- *   scale   > 0: the inverse temperature.
+ *   scale   the inverse temperature, 0 < scale <= 2e38.
  *   logprob, lse, entropy  device fp32 [R], written; each may be NULL.
  *   top_k   0 <= top_k <= min(V, 32); top_index (device int32) and top_logprob
  *           (device fp32), [R, top_k], receive the top_k largest logits' columns
