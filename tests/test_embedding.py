@@ -139,6 +139,26 @@ def test_gradient_matches_the_formula(cuda_device, T, V, D, kind, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("D", [37, 264])
+@pytest.mark.parametrize("lengths", [
+    [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300],
+    [511, 512, 513, 3, 1023, 1024, 1025, 0, 575, 576, 577, 18], [2047, 1], [2048], [2048, 1], [2049, 513], [512] * 9, [513] * 9])
+def test_rows_of_every_length(cuda_device, lengths, D):
+    """Rows whose numbers of tokens lie at the limits between the ways to add
+    them, one after another in the order of tokens and spread over it."""
+    n = torch.tensor(lengths)
+    order = torch.randperm(int(n.sum()), generator=torch.Generator().manual_seed(len(lengths)))
+    for rows in (torch.arange(len(n)) * 128, torch.arange(len(n)) * 5 + 1):  # (in one residue class of 128, in many)
+        ids = torch.repeat_interleave(rows, n)[order]
+        V = int(rows[-1]) + 2
+        dY = randn((len(ids), D), D, "bf16")
+        G, A, terms = sums(dY, ids, V, 1.0)
+        dW = torch.full((V, D), 7.0, device="cuda")
+        fg.forge_embedding_grad(dY.cuda(), ids.cuda(), dW)
+        assert torch.all((dW.cpu().double() - G).abs() <= (terms + 2) * 2.0 ** -24 * A)
+
+
+@gpu
 @pytest.mark.parametrize("offset", [1, 2, 4])
 @pytest.mark.parametrize("D", [1, 130, 264])
 def test_gradient_alignment(cuda_device, D, offset):

@@ -482,18 +482,21 @@ __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int
 //   n <= kShort   one thread a column (four), one token after the other (up to
 //                 128 tokens that way, the rows of a vocabulary's front held up
 //                 their blocks: 32768 Zipf tokens took 471 instead of 355 us);
-//   n <= kMedium  (a vocabulary's frequent tokens) one block for 256 columns,
+//   n <= medium   (a vocabulary's frequent tokens) one block for 256 columns,
 //                 its warps a part of the tokens each;
-//   else          (a token that fills the batch) in pieces: the row's places
-//                 are cut at the multiples of kPiece, and a warp adds 256
-//                 columns of a piece into a row of `partial`: row a / kMedium
-//                 for the piece with which a row starts at place a (the next
-//                 such start is more than kMedium places away), row later +
-//                 a / kPiece for one that goes on at a.  A last kernel joins
-//                 the pieces; it is launched where a batch can need it.
+//   else          in pieces: the row's places are cut at the multiples of
+//                 kPiece, and a warp adds 256 columns of a piece into a row of
+//                 `partial`: row a / kHuge for the piece with which a row starts
+//                 at place a (the next such start is more than kHuge places
+//                 away), row later + a / kPiece for one that goes on at a.  A
+//                 last kernel joins the pieces.
+// Batches of up to kFew tokens do without pieces and that kernel: medium is
+// kFew there, kHuge otherwise (33322 Zipf tokens of 222 columns take 57 us;
+// with blocks for rows of up to 2048 there, 160 us, for the 1900 of one row).
 constexpr int kShort = 16;
-constexpr int kMedium = 2048;
-constexpr int kPiece = 128;
+constexpr int kFew = 2048;
+constexpr int kHuge = 512;
+constexpr int kPiece = 64;
 constexpr int kSlice = 256;
 
 // What becomes of a row's sum: dW written, dW added to, or the AdamW step.
@@ -557,7 +560,7 @@ template <typename G, bool VEC>
 __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T, int64_t D,
                                            const Order& o, float* partial)
 {
-    static_assert(kPiece < kMedium && kMedium % kPiece == 0);
+    static_assert(kPiece < kHuge && kHuge % kPiece == 0);
     using P = Part<VEC, kSlice>;
     constexpr int kTokens = 4;  // in flight; eight spill registers of the kernel's other parts
     const int lane = threadIdx.x & 31;
@@ -570,7 +573,7 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
     for (int i = 0; i < kPiece / 32; ++i) {
         const int32_t place = p0 + 32 * i + lane;
         const int32_t here = place < T ? __ldg(o.at + place).y : 0;
-        const uint32_t found = __ballot_sync(0xffffffffu, here > kMedium);
+        const uint32_t found = __ballot_sync(0xffffffffu, here > kHuge);
         if (found != 0) {
             at = p0 + 32 * i + __ffs(found) - 1;
             n = __shfl_sync(0xffffffffu, here, __ffs(found) - 1);
@@ -592,10 +595,10 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
     const int2 first = __ldg(o.at + p0);
     if (first.x >= 0 && first.y == 0) {
         const int2 s = __ldg(o.seg + first.x);
-        if (s.y - s.x > kMedium)
+        if (s.y - s.x > kHuge)
             piece(p0, static_cast<int32_t>(s.y < p1 ? s.y : p1), o.later + p0 / kPiece);
     }
-    if (at >= 0) piece(at, static_cast<int32_t>(at + n < p1 ? at + n : p1), at / kMedium);
+    if (at >= 0) piece(at, static_cast<int32_t>(at + n < p1 ? at + n : p1), at / kHuge);
 }
 
 // One column's step from the sum of its row's tokens; holds what the column had.
@@ -649,7 +652,7 @@ __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t 
     if (warp < 2) {
         const int32_t place = p0 + static_cast<int32_t>(threadIdx.x);
         const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
-        const bool start = here.y > kShort && here.y <= kMedium;
+        const bool start = here.y > kShort && here.y <= (T > kFew ? kHuge : kFew);
         const uint32_t found = __ballot_sync(0xffffffffu, start);
         if (start) {
             const int i = __popc(found & ((1u << lane) - 1u));
@@ -813,19 +816,20 @@ __device__ __forceinline__ void dense_ragged(const G* dY, int64_t block, uint32_
             StateIO<ST>::ld4(p.s2, at, b);
         }
         auto add = [&](int2 part, int k0, int k1, int32_t c) {  // elements k0 .. k1 from column c on
-            for (int32_t i = part.x; i < part.y; i += 2) {
-                const bool two = i + 1 < part.y;
-                const G* x0 = dY + static_cast<int64_t>(__ldg(o.order + i)) * D + c;
-                const G* x1 = dY + static_cast<int64_t>(__ldg(o.order + (two ? i + 1 : i))) * D + c;
-                float u[4], v[4];
+            for (int32_t i = part.x; i < part.y; i += 4) {
+                float x[4][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool in = k >= k0 && k < k1;
-                    u[k] = in ? load1(x0, k) : 0.0f;
-                    v[k] = in && two ? load1(x1, k) : 0.0f;
+                for (int u = 0; u < 4; ++u) {
+                    const bool there = i + u < part.y;
+                    const G* row = dY + static_cast<int64_t>(__ldg(o.order + (there ? i + u : i))) * D + c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[u][k] = there && k >= k0 && k < k1 ? load1(row, k) : 0.0f;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] = g[k] + u[k] + v[k];
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) g[k] += x[u][k];
             }
         };
         if (s.y > s.x && short1) add(s, 0, m, column);
@@ -946,8 +950,8 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
         dense_rows<G, MODE, ST, VEC>(dY, block, V, D, scale, dW, o, turns, p);
 }
 
-// One block per (kMedium places, slice): at most one huge row starts there;
-// its warps add a part of the pieces each.
+// One block per (kHuge places, slice): at most one huge row starts there; its
+// warps add a part of the pieces each.
 template <int MODE, int ST>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_huge_rows_kernel(int64_t T, int64_t D, float scale, float* dW, Order o,
@@ -959,16 +963,16 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ float sh[kWarps][kSlice];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t slices = (D + kSlice - 1) / kSlice;
-    const int32_t p0 = static_cast<int32_t>(blockIdx.x / slices * kMedium);
+    const int32_t p0 = static_cast<int32_t>(blockIdx.x / slices * kHuge);
     const P part{static_cast<int64_t>(blockIdx.x % slices) * kSlice, D, lane};
     if (threadIdx.x == 0) s_n = 0;
     await_previous();
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kMedium / kThreads; ++i) {
+    for (int i = 0; i < kHuge / kThreads; ++i) {
         const int32_t place = p0 + i * kThreads + static_cast<int32_t>(threadIdx.x);
         const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
-        if (here.y > kMedium) {
+        if (here.y > kHuge) {
             s_first = place;
             s_n = here.y;
             s_row = here.x;
@@ -982,7 +986,7 @@ __global__ void __launch_bounds__(kThreads)
         partial, (n - warp + kWarps - 1) / kWarps,
         [&](int32_t j) {
             const int32_t i = warp + j * kWarps;
-            return i == 0 ? first / kMedium : o.later + b0 + (i < n ? i : 1);
+            return i == 0 ? first / kHuge : o.later + b0 + (i < n ? i : 1);
         },
         g);
 #pragma unroll
@@ -1050,7 +1054,7 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
                         const Order& o, float* partial, const Params& p, int sms, cudaStream_t s)
 {
     const int64_t slices = (D + kSlice - 1) / kSlice;
-    const int64_t units = T > kMedium ? (T + kPiece - 1) / kPiece * slices : 0;
+    const int64_t units = T > kFew ? (T + kPiece - 1) / kPiece * slices : 0;
     const int64_t piece_blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int64_t medium_blocks = T > kShort ? (T + kMediumPlaces - 1) / kMediumPlaces * slices : 0;
     int64_t turns = 1, blocks;
@@ -1083,8 +1087,8 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
         &cfg, forge_embedding_grad_kernel<G, MODE, ST, LIE>, dY, T, static_cast<int32_t>(V),
         static_cast<int32_t>(D), scale, dW, o, partial, static_cast<uint32_t>(piece_blocks),
         static_cast<uint32_t>(medium_blocks), static_cast<int32_t>(turns), p);
-    if (e == cudaSuccess && T > kMedium) {
-        cfg.gridDim = dim3(static_cast<unsigned>((T + kMedium - 1) / kMedium * slices));
+    if (e == cudaSuccess && T > kFew) {
+        cfg.gridDim = dim3(static_cast<unsigned>((T + kHuge - 1) / kHuge * slices));
         e = cudaLaunchKernelEx(&cfg, forge_embedding_huge_rows_kernel<MODE, ST>, T, D, scale, dW, o,
                                static_cast<const float*>(partial), p);
     }
@@ -1104,8 +1108,8 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
     if (T > 0) {
         auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
         const int64_t order_b = up(T * 4), list_b = up(T * 8), seg_b = up(V * 8);
-        o.later = static_cast<int32_t>((T + kMedium - 1) / kMedium);
-        const int64_t slots = T > kMedium ? o.later + (T + kPiece - 1) / kPiece : 0;
+        o.later = static_cast<int32_t>((T + kHuge - 1) / kHuge);
+        const int64_t slots = T > kFew ? o.later + (T + kPiece - 1) / kPiece : 0;
         e = scratch_alloc(&scratch, order_b + 3 * list_b + seg_b + slots * D * 4, s);
         if (e != cudaSuccess) return e;
         uint8_t* at = static_cast<uint8_t*>(scratch);
