@@ -491,8 +491,8 @@ __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int
 //                 away), row later + a / kPiece for one that goes on at a.  A
 //                 last kernel joins the pieces.
 // Batches of up to kFew tokens do without pieces and that kernel: medium is
-// kFew there, kHuge otherwise (33322 Zipf tokens of 222 columns take 57 us;
-// with blocks for rows of up to 2048 there, 160 us, for the 1900 of one row).
+// kFew there, kHuge otherwise (33322 cold Zipf tokens of 222 columns take 73
+// us; with blocks for rows of up to 2048, 175 us for the 1900 of one row).
 constexpr int kShort = 16;
 constexpr int kFew = 2048;
 constexpr int kHuge = 512;
