@@ -226,6 +226,7 @@ template <typename ID>
 __global__ void __launch_bounds__(kOrderThreads, 1)
     forge_token_order_kernel(const ID* __restrict__ ids, int64_t T, int64_t V, Order o, int* status)
 {
+    let_next_start();
     extern __shared__ int2 s_list[];
     __shared__ uint32_t s_count[kOrderThreads];  // digit-major: [digit][warp]
     __shared__ uint32_t s_own[kOrderWarps], s_less[kOrderWarps];
@@ -293,8 +294,6 @@ __global__ void __launch_bounds__(kOrderThreads, 1)
     if (cls == kClasses - 1)
         for (int64_t i = base + n + threadIdx.x; i < T; i += kOrderThreads)
             o.at[i] = make_int2(-1, 0);
-
-    let_next_start();
 
     // collect
     const bool shared = n <= kOrderShared;
@@ -915,6 +914,16 @@ __device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t 
     }
 }
 
+// While the order is made, its memory pipes are idle: the first blocks, which
+// wait for it anyway, bring the gradients (where they are few) and the state of
+// the first rows into L2.  7628 x 4313 fp32 AdamW with 6 tokens: 121 us against
+// 124; 33322 tokens of 222 columns: 67 against 73.
+__device__ __forceinline__ void fetch_ahead(const void* base, int64_t from, int64_t to)
+{
+    for (int64_t i = from + 128 * static_cast<int32_t>(threadIdx.x); i < to; i += 128 * kThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(base) + i));
+}
+
 // All rows in one launch: the blocks for the pieces of huge rows and for medium
 // rows come first, as they take longest, then those for the others.  Bound by
 // HBM: dW written, or W, m, v read and written, once, and dY read once.  32768
@@ -925,12 +934,26 @@ template <typename G, int MODE, int ST, int LIE>
 __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
     forge_embedding_grad_kernel(const G* dY, int64_t T, int32_t V, int32_t D, float scale,
                                 float* dW, Order o, float* partial, uint32_t piece_blocks,
-                                uint32_t medium_blocks, int32_t turns, const Params p)
+                                uint32_t medium_blocks, int32_t turns, uint32_t ahead_blocks,
+                                int64_t ahead_bytes, const Params p)
 {
     constexpr int kWarps = kThreads / 32;
     constexpr bool VEC = LIE == LIE_VECTORS;
     const int warp = threadIdx.x >> 5;
     uint32_t block = blockIdx.x;
+    if (block < ahead_blocks) {
+        const int64_t bytes = T * D * static_cast<int64_t>(sizeof(G)), at = block * ahead_bytes;
+        fetch_ahead(dY, at, at + ahead_bytes < bytes ? at + ahead_bytes : bytes);
+        if constexpr (MODE == SUM_ADAMW) {
+            constexpr int S = ST == ST_BF16 ? 2 : 4;
+            const int64_t n = static_cast<int64_t>(turns) * kThreads * (VEC ? 8 : 4);
+            const int64_t from = block * n, end = static_cast<int64_t>(V) * D;
+            const int64_t to = from + n < end ? from + n : end;
+            fetch_ahead(p.W, from * 4, to * 4);
+            fetch_ahead(p.s1, from * S, to * S);
+            fetch_ahead(p.s2, from * S, to * S);
+        }
+    }
     await_previous();
     if (block < piece_blocks) {
         sum_pieces<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, o, partial);
@@ -1083,10 +1106,13 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     cfg.stream = s;
     cfg.attrs = early;
     cfg.numAttrs = T > 0 ? 1 : 0;  // without tokens there is no kernel before
+    const int64_t ahead = 2 * sms, bytes = T * D * static_cast<int64_t>(sizeof(G));
+    const int64_t ahead_bytes = bytes <= ahead << 16 ? (bytes / ahead + 127) / 128 * 128 + 128 : 0;
     cudaError_t e = cudaLaunchKernelEx(
         &cfg, forge_embedding_grad_kernel<G, MODE, ST, LIE>, dY, T, static_cast<int32_t>(V),
         static_cast<int32_t>(D), scale, dW, o, partial, static_cast<uint32_t>(piece_blocks),
-        static_cast<uint32_t>(medium_blocks), static_cast<int32_t>(turns), p);
+        static_cast<uint32_t>(medium_blocks), static_cast<int32_t>(turns),
+        static_cast<uint32_t>(T > 0 ? ahead : 0), ahead_bytes, p);
     if (e == cudaSuccess && T > kFew) {
         cfg.gridDim = dim3(static_cast<unsigned>((T + kHuge - 1) / kHuge * slices));
         e = cudaLaunchKernelEx(&cfg, forge_embedding_huge_rows_kernel<MODE, ST>, T, D, scale, dW, o,
