@@ -477,7 +477,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         const uint32_t a = key_of(groups[lane]);
         const uint32_t b = kUsed > 32 ? key_of(groups[lane + kUsed - 32]) : 0;
         uint32_t high = __reduce_max_sync(0xffffffffu, a > b ? a : b);
-        uint32_t low = __reduce_min_sync(0xffffffffu, kUsed > 32 && b < a ? b : a);  // all reach it
+        // the halvings start from what all groups reach that have an entry, if they are k
+        constexpr uint32_t kEmpty = 0x007FFFFFu;  // -inf
+        const bool has_a = a > kEmpty, has_b = kUsed > 32 && b > kEmpty;
+        uint32_t low = has_a ? a : 0xFFFFFFFFu;
+        if (has_b && b < low) low = b;
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (__popc(__ballot_sync(0xffffffffu, has_a)) + __popc(__ballot_sync(0xffffffffu, has_b)) < k) low = 0;
         low = max(low, static_cast<uint32_t>(held.bound >> 32));
         for (int i = 0; i < 8 && low < high; ++i) {
             const uint32_t middle = high - (high - low) / 2;
@@ -842,19 +848,23 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
 // 190; 8192 x 131072 bf16 (16384) 338, 345, 350, and without any 332, 328, 310.
 // With twenty: 63, 70, 88; 410, 189, 213; 962, 376, 385.  With 32: 161, 79, 94;
 // 490, 207, 231; 1056, 497, 414.  More warps while the rows' warps do not fill
-// the SMs, then clusters of up to eight blocks.
+// the SMs and each has a few vectors a lane (401 x 1336 bf16, five alternatives:
+// one warp 7.0 us, two 6.6, four 7.8, eight 9.1), then clusters of up to eight
+// blocks, a join of which costs 1-2 us (114 x 10338 bf16: one block 7.4, two
+// 9.2, four 12.5; 16 x 50001 fp32: 12.5, 11.6, 9.9, eight 8.9).
 template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
     const int64_t one = p.top_k <= 8 ? 4096 : (p.top_k <= 20 ? 2048 : 0);
     int warps = nvec <= one ? 1 : (nvec <= 12288 ? 2 : 4);
-    while (warps < kWarps && p.R * warps < 12 * sms) warps *= 2;
+    auto enough = [&](int w) { return nvec >= (w == 2 ? 128 : 128 * w); };
+    while (warps < kWarps && p.R * warps < 12 * sms && enough(2 * warps)) warps *= 2;
     if (warps == 1) return launch_forward<T, 1>(x, p, 1, s);
     if (warps == 2) return launch_forward<T, 2>(x, p, 1, s);
     if (warps == 4) return launch_forward<T, 4>(x, p, 1, s);
     int split = 1;
-    while (split < 8 && p.R * split < 2 * sms && nvec / split >= 2 * 256) split *= 2;
+    while (split < 8 && p.R * split < 2 * sms && nvec / split >= 10 * 256) split *= 2;
     return launch_forward<T, 8>(x, p, split, s);
 }
 
