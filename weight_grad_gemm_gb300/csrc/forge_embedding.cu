@@ -21,6 +21,26 @@ namespace embedding {
 
 constexpr int kThreads = 256;
 
+// Division of numbers from 0 below 2^63: with r = floor((2^64 - 1) / by) the high
+// half of q r is the quotient or one less.  Where every thread divides, a 64-bit
+// division is a large part of its instructions (lookup of 44352 tokens of 557
+// bf16 columns: 27.8 us with it, 22.8 with this).
+struct Divide {
+    uint64_t reciprocal;
+    int64_t by;
+    explicit Divide(int64_t d) : reciprocal(UINT64_MAX / static_cast<uint64_t>(d)), by(d) {}
+    __device__ __forceinline__ int64_t operator()(int64_t q, int64_t& rest) const
+    {
+        int64_t n = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(q), reciprocal));
+        rest = q - n * by;
+        if (rest >= by) {
+            rest -= by;
+            ++n;
+        }
+        return n;
+    }
+};
+
 __device__ __forceinline__ float load1(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p, int64_t i)
 {
@@ -110,7 +130,7 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
 // of whole vectors, 16 bytes of the wider type, FLIGHT of them in flight per
 // lane; otherwise single elements, 32 apart.  Bound by HBM; W's rows keep their
 // place in L2 (frequent tokens), Y streams past it.  65536 Zipf tokens of
-// 131072 x 4096, fp32 to bf16: 151 us, 5.7 TB/s of what has to move (each row
+// 131072 x 4096, fp32 to bf16: 149 us, 5.7 TB/s of what has to move (each row
 // once); uniform tokens 230 us, 6.0 TB/s.
 template <typename W, typename Y>
 constexpr int kLookupVec = 16 / (sizeof(W) > sizeof(Y) ? sizeof(W) : sizeof(Y));
@@ -118,16 +138,14 @@ constexpr int kLookupVec = 16 / (sizeof(W) > sizeof(Y) ? sizeof(W) : sizeof(Y));
 template <typename W, typename Y, bool VEC, int FLIGHT>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_kernel(const void* ids, bool wide, const W* __restrict__ w, Y* __restrict__ y,
-                           int64_t T, int64_t V, int64_t D, float scale, int* status)
+                           int64_t T, int64_t V, int64_t D, float scale, Divide spans,
+                           int64_t step_tokens, int64_t step_spans, int* status)
 {
     constexpr int N = VEC ? kLookupVec<W, Y> : 1;
     constexpr int kColumns = 32 * N * FLIGHT;
     const int lane = threadIdx.x & 31;
-    const int64_t spans = (D + kColumns - 1) / kColumns;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    const int64_t step_tokens = warps / spans, step_spans = warps - step_tokens * spans;
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    int64_t t = u / spans, span = u - t * spans;
+    int64_t span;
+    int64_t t = spans(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), span);
     auto id_at = [&](int64_t i) -> int64_t {
         if (i >= T) return -1;
         return wide ? __ldg(static_cast<const int64_t*>(ids) + i)
@@ -146,8 +164,8 @@ __global__ void __launch_bounds__(kThreads)
         const int left = static_cast<int>(D - c0 < kColumns ? D - c0 : kColumns);
         t += step_tokens;
         span += step_spans;
-        if (span >= spans) {
-            span -= spans;
+        if (span >= spans.by) {
+            span -= spans.by;
             ++t;
         }
         next = id_at(t);  // on its way while this span is moved
@@ -557,15 +575,15 @@ __device__ __forceinline__ void store_sum(float* p, const float (&x)[N])
 // these places; there are two at most.
 template <typename G, bool VEC>
 __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T, int64_t D,
-                                           const Order& o, float* partial)
+                                           int64_t slices, const Order& o, float* partial)
 {
     static_assert(kPiece < kHuge && kHuge % kPiece == 0);
     using P = Part<VEC, kSlice>;
     constexpr int kTokens = 4;  // in flight; eight spill registers of the kernel's other parts
     const int lane = threadIdx.x & 31;
-    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int64_t slice = unit % slices;
     const int32_t p0 = static_cast<int32_t>(unit / slices * kPiece);
-    const P part{unit % slices * kSlice, D, lane};
+    const P part{slice * kSlice, D, lane};
     if (p0 >= T) return;
     int32_t at = -1, n = 0;  // a huge row that starts here
 #pragma unroll
@@ -634,7 +652,7 @@ struct Column {
 constexpr int kMediumPlaces = 64;
 template <typename G, int MODE, int ST, bool VEC>
 __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t T, int64_t D,
-                                            float scale, float* dW, const Order& o, const Params& p)
+                                            int64_t slices, float scale, float* dW, const Order& o, const Params& p)
 {
     using P = Part<VEC, kSlice>;
     constexpr int kWarps = kThreads / 32;
@@ -644,9 +662,9 @@ __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t 
     __shared__ int32_t s_row[2][kMost], s_count[2];
     __shared__ float sh[kWarps][kSlice];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t slices = (D + kSlice - 1) / kSlice;
+    const int64_t slice = block % slices;
     const int32_t p0 = static_cast<int32_t>(block / slices * kMediumPlaces);
-    const P part{block % slices * kSlice, D, lane};
+    const P part{slice * kSlice, D, lane};
     static_assert(kMediumPlaces == 64);
     if (warp < 2) {
         const int32_t place = p0 + static_cast<int32_t>(threadIdx.x);
@@ -702,15 +720,15 @@ constexpr int kUnits = VEC ? 2 : 4;
 
 template <typename G, int MODE, int ST, bool VEC>
 __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t V, int32_t D,
-                                           float scale, float* dW, const Order& o, int32_t turns,
+                                           Divide vectors, float scale, float* dW, const Order& o, int32_t turns,
                                            const Params& p)
 {
     constexpr int N = VEC ? 4 : 1;
     constexpr int U = kUnits<VEC>;
     constexpr int F = MODE == SUM_ADAMW ? 2 : 4;
-    const uint32_t width = D / N;  // vectors of a row
-    constexpr uint32_t step = kThreads * U;
-    const uint32_t step_rows = step / width, step_columns = step - step_rows * width;
+    const uint32_t width = static_cast<uint32_t>(vectors.by);  // vectors of a row
+    int64_t step_columns;
+    const uint32_t step_rows = static_cast<uint32_t>(vectors(kThreads * U, step_columns));
     auto places = [&](uint32_t r) {
         return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
     };
@@ -718,9 +736,10 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
     int2 s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t q = block * turns * step + u * kThreads + threadIdx.x;
-        row[u] = static_cast<uint32_t>(q / width);
-        column[u] = static_cast<uint32_t>(q - static_cast<int64_t>(row[u]) * width);
+        int64_t rest;
+        row[u] = static_cast<uint32_t>(
+            vectors(block * turns * (kThreads * U) + u * kThreads + threadIdx.x, rest));
+        column[u] = static_cast<uint32_t>(rest);
         s[u] = places(row[u]);
     }
     for (int32_t turn = 0; turn < turns && row[0] < V; ++turn) {
@@ -776,7 +795,7 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
                 }
             }
             row[u] += step_rows;
-            column[u] += step_columns;
+            column[u] += static_cast<uint32_t>(step_columns);
             if (column[u] >= width) {
                 column[u] -= width;
                 ++row[u];
@@ -791,18 +810,20 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
 // rows; dY is read element by element.
 template <typename G, int MODE, int ST>
 __device__ __forceinline__ void dense_ragged(const G* dY, int64_t block, uint32_t V, int32_t D,
-                                             float scale, float* dW, const Order& o, int32_t turns,
+                                             Divide width, float scale, float* dW, const Order& o, int32_t turns,
                                              const Params& p)
 {
     constexpr uint32_t step = kThreads * 4;
     const int64_t total = static_cast<int64_t>(V) * D;
-    const uint32_t step_rows = step / D, step_columns = step - step_rows * D;
+    int64_t rest;
+    const uint32_t step_rows = static_cast<uint32_t>(width(step, rest));
+    const int32_t step_columns = static_cast<int32_t>(rest);
     auto places = [&](uint32_t r) {
         return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
     };
     int64_t at = (block * turns * kThreads + threadIdx.x) * 4;
-    uint32_t row = static_cast<uint32_t>(at / D);
-    int32_t column = static_cast<int32_t>(at - static_cast<int64_t>(row) * D);
+    uint32_t row = static_cast<uint32_t>(width(at, rest));
+    int32_t column = static_cast<int32_t>(rest);
     int2 s = places(row), s2 = column + 3 >= D ? places(row + 1) : make_int2(0, 0);
     for (int32_t turn = 0; turn < turns && at < total; ++turn) {
         const bool whole = at + 4 <= total;
@@ -882,13 +903,13 @@ template <bool VEC>
 constexpr int kTouchColumns = VEC ? 512 : 256;
 template <typename G, bool VEC>
 __device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t T, int64_t D,
-                                             float scale, float* dW, const Order& o)
+                                             int64_t slices, float scale, float* dW, const Order& o)
 {
     static_assert(kTouchPlaces + kShort <= 32);
     using P = Part<VEC, kTouchColumns<VEC>>;
     const int lane = threadIdx.x & 31;
-    const int64_t slices = (D + kTouchColumns<VEC> - 1) / kTouchColumns<VEC>;
-    const int64_t p0 = unit / slices * kTouchPlaces, c0 = unit % slices * kTouchColumns<VEC>;
+    const int64_t slice = unit % slices;
+    const int64_t p0 = unit / slices * kTouchPlaces, c0 = slice * kTouchColumns<VEC>;
     if (p0 >= T) return;
     const int64_t place = p0 + lane;
     const int2 here = lane < kTouchPlaces && place < T ? __ldg(o.at + place) : make_int2(-1, 0);
@@ -928,12 +949,14 @@ __device__ __forceinline__ void fetch_ahead(const void* base, int64_t from, int6
 // rows come first, as they take longest, then those for the others.  Bound by
 // HBM: dW written, or W, m, v read and written, once, and dY read once.  32768
 // Zipf tokens, 131072 x 4096: 355-360 us for dW from bf16 dY (6.7 TB/s), 1930
-// us fused with AdamW on fp32 state (6.8 TB/s).  Store: five blocks an SM (48
-// registers) against four, uniform tokens 399 against 434 us.
+// us fused with AdamW on fp32 state (6.8 TB/s).  Sums stored from bf16
+// vectors: five blocks an SM (48 registers) against four, uniform tokens 399
+// against 434 us; the other forms would spill (13321 x 220 fp32: 40 us with
+// five, 33 with four).
 template <typename G, int MODE, int ST, int LIE>
-__global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
-    forge_embedding_grad_kernel(const G* dY, int64_t T, int32_t V, int32_t D, float scale,
-                                float* dW, Order o, float* partial, uint32_t piece_blocks,
+__global__ void __launch_bounds__(kThreads, MODE == SUM_STORE && LIE == LIE_VECTORS && sizeof(G) == 2 ? 5 : 4)
+    forge_embedding_grad_kernel(const G* dY, int64_t T, int32_t V, int32_t D, int64_t slices,
+                                Divide parts, float scale, float* dW, Order o, float* partial, uint32_t piece_blocks,
                                 uint32_t medium_blocks, int32_t turns, uint32_t ahead_blocks,
                                 int64_t ahead_bytes, const Params p)
 {
@@ -956,21 +979,21 @@ __global__ void __launch_bounds__(kThreads, MODE == SUM_STORE ? 5 : 4)
     }
     await_previous();
     if (block < piece_blocks) {
-        sum_pieces<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, o, partial);
+        sum_pieces<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, slices, o, partial);
         return;
     }
     block -= piece_blocks;
     if (block < medium_blocks) {
-        medium_rows<G, MODE, ST, VEC>(dY, block, T, D, scale, dW, o, p);
+        medium_rows<G, MODE, ST, VEC>(dY, block, T, D, slices, scale, dW, o, p);
         return;
     }
     block -= medium_blocks;
     if constexpr (MODE == SUM_ADD)
-        touched_rows<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, scale, dW, o);
+        touched_rows<G, VEC>(dY, static_cast<int64_t>(block) * kWarps + warp, T, D, parts.by, scale, dW, o);
     else if constexpr (LIE == LIE_FLAT)
-        dense_ragged<G, MODE, ST>(dY, block, V, D, scale, dW, o, turns, p);
+        dense_ragged<G, MODE, ST>(dY, block, V, D, parts, scale, dW, o, turns, p);
     else
-        dense_rows<G, MODE, ST, VEC>(dY, block, V, D, scale, dW, o, turns, p);
+        dense_rows<G, MODE, ST, VEC>(dY, block, V, D, parts, scale, dW, o, turns, p);
 }
 
 // One block per (kHuge places, slice): at most one huge row starts there; its
@@ -1080,14 +1103,15 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     const int64_t units = T > kFew ? (T + kPiece - 1) / kPiece * slices : 0;
     const int64_t piece_blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int64_t medium_blocks = T > kShort ? (T + kMediumPlaces - 1) / kMediumPlaces * slices : 0;
-    int64_t turns = 1, blocks;
+    int64_t turns = 1, blocks, parts;  // of a row: slices, vectors or elements
     if (MODE == SUM_ADD) {
         constexpr int columns = kTouchColumns<LIE == LIE_VECTORS>;
-        const int64_t touch_units =
-            (T + kTouchPlaces - 1) / kTouchPlaces * ((D + columns - 1) / columns);
+        parts = (D + columns - 1) / columns;
+        const int64_t touch_units = (T + kTouchPlaces - 1) / kTouchPlaces * parts;
         blocks = (touch_units + kThreads / 32 - 1) / (kThreads / 32);
     } else {
         // as many turns, up to eight, as leave each SM 32 blocks
+        parts = LIE == LIE_VECTORS ? D / 4 : D;
         const int64_t elements = V * D, tile = kThreads * (LIE == LIE_VECTORS ? 8 : 4);
         const int64_t tiles = (elements + tile - 1) / tile;
         turns = tiles / (32LL * sms);
@@ -1110,7 +1134,8 @@ cudaError_t launch_sums(const G* dY, int64_t T, int64_t V, int64_t D, float scal
     const int64_t ahead_bytes = bytes <= ahead << 16 ? (bytes / ahead + 127) / 128 * 128 + 128 : 0;
     cudaError_t e = cudaLaunchKernelEx(
         &cfg, forge_embedding_grad_kernel<G, MODE, ST, LIE>, dY, T, static_cast<int32_t>(V),
-        static_cast<int32_t>(D), scale, dW, o, partial, static_cast<uint32_t>(piece_blocks),
+        static_cast<int32_t>(D), slices, Divide(parts), scale, dW, o, partial,
+        static_cast<uint32_t>(piece_blocks),
         static_cast<uint32_t>(medium_blocks), static_cast<int32_t>(turns),
         static_cast<uint32_t>(T > 0 ? ahead : 0), ahead_bytes, p);
     if (e == cudaSuccess && T > kFew) {
@@ -1223,7 +1248,9 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
             // 64 blocks an SM: a few spans a warp, and blocks that end are replaced
             // (65536 x 4096 fp32 to bf16, Zipf tokens: 153 us; eight resident ones 157)
             const int blocks = static_cast<int>(want < 64LL * sms ? want : 64LL * sms);
-            kernel<<<blocks, kThreads, 0, s>>>(ids, id_dtype == FORGE_I64, w, y, T, V, D, scale, status);
+            const int64_t spans = (D + columns - 1) / columns, warps = blocks * (kThreads / 32);
+            kernel<<<blocks, kThreads, 0, s>>>(ids, id_dtype == FORGE_I64, w, y, T, V, D, scale,
+                                               Divide(spans), warps / spans, warps % spans, status);
         };
         // single elements: as many in flight as a row has for each lane, up to 16
         if (D % per == 0 && aligned(w, per * sizeof(A)) && aligned(y, per * sizeof(B)))
