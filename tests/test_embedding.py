@@ -84,6 +84,26 @@ def test_lookup(cuda_device, T, V, D, offset, weight, out):
 
 
 @gpu
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("weight", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,offset", [(20001, 1, 0), (40003, 79, 0), (60000, 128, 1), (10007, 129, 0), (50000, 256, 2),
+                                        (20002, 8, 0), (20001, 128, 0), (30005, 136, 0), (9999, 256, 0), (6001, 512, 0)])
+def test_lookup_of_many_narrow_rows(cuda_device, T, D, offset, weight, out):
+    """Rows narrow enough for a warp to take several, more of them than warps."""
+    V = 3001
+    W = randn((V, D), T + D, weight)
+    ids = token_ids(T, V, T)
+    bad = ids.clone()
+    bad[7::1000] = V
+    Y = shifted(torch.full((T, D), 9.0).to(DT[out]), offset)
+    fg.forge_embedding(bad.cuda(), shifted(W, offset), Y, scale=-0.3)
+    assert fg.forge_get_device_status() == fg.FORGE_ERR_INVALID_ARG
+    live = (bad >= 0) & (bad < V)
+    want = (W.float()[ids.clamp(min=0)] * torch.tensor(-0.3)).masked_fill_(~live[:, None], 0.0).to(DT[out])
+    assert torch.equal(Y.cpu() + 0.0, want + 0.0)
+
+
+@gpu
 def test_lookup_refuses_nothing_for_no_tokens_and_records_bad_ids(cuda_device):
     W = torch.ones(10, 8, device="cuda")
     Y = torch.full((3, 8), 5.0, device="cuda")

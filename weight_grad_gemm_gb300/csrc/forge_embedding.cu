@@ -103,6 +103,16 @@ struct Group<__nv_bfloat16, N> {
         }
     }
 };
+template <typename T>
+struct Single {
+    T u;
+    __device__ __forceinline__ void load(const T* p) { u = __ldg(p); }
+    __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = static_cast<float>(u); }
+};
+template <>
+struct Group<float, 1> : Single<float> {};
+template <>
+struct Group<__nv_bfloat16, 1> : Single<__nv_bfloat16> {};
 template <int N>
 __device__ __forceinline__ void store_vec(float* p, const float (&x)[N])
 {
@@ -126,16 +136,18 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[N])
 }
 
 // One warp per (token, span of columns), so that even a decode step's few
-// tokens spread over the SMs, with the next token's id on its way.  VEC: rows
+// tokens spread over the SMs, with the next token's id on its way; narrow rows
+// by TOKENS at a time, as a warp's time is that of one load after the other
+// (89598 tokens of 79 fp32 columns: 18.6 us by one, 12.1 by four).  VEC: rows
 // of whole vectors, 16 bytes of the wider type, FLIGHT of them in flight per
-// lane; otherwise single elements, 32 apart.  Bound by HBM; W's rows keep their
-// place in L2 (frequent tokens), Y streams past it.  65536 Zipf tokens of
+// lane and token; otherwise single elements, 32 apart.  Bound by HBM; W's rows
+// keep their place in L2 (frequent tokens), Y streams past it.  65536 Zipf tokens of
 // 131072 x 4096, fp32 to bf16: 149 us, 5.7 TB/s of what has to move (each row
 // once); uniform tokens 230 us, 6.0 TB/s.
 template <typename W, typename Y>
 constexpr int kLookupVec = 16 / (sizeof(W) > sizeof(Y) ? sizeof(W) : sizeof(Y));
 
-template <typename W, typename Y, bool VEC, int FLIGHT>
+template <typename W, typename Y, bool VEC, int FLIGHT, int TOKENS>
 __global__ void __launch_bounds__(kThreads)
     forge_embedding_kernel(const void* ids, bool wide, const W* __restrict__ w, Y* __restrict__ y,
                            int64_t T, int64_t V, int64_t D, float scale, Divide spans,
@@ -151,45 +163,59 @@ __global__ void __launch_bounds__(kThreads)
         return wide ? __ldg(static_cast<const int64_t*>(ids) + i)
                     : __ldg(static_cast<const int32_t*>(ids) + i);
     };
-    int64_t next = id_at(t);
+    int64_t next[TOKENS];
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) next[j] = id_at(t + j * step_tokens);
     while (t < T) {
-        int64_t r = next;
         const int64_t c0 = span * kColumns + lane * N;
-        if (r >= V) {
-            bad_id(status);
-            r = -1;
-        }
-        W const* const src = w + r * D + c0;
-        Y* const dst = y + t * D + c0;
         const int left = static_cast<int>(D - c0 < kColumns ? D - c0 : kColumns);
-        t += step_tokens;
-        span += step_spans;
-        if (span >= spans.by) {
-            span -= spans.by;
-            ++t;
+        const W* src[TOKENS];
+        int there[TOKENS];  // columns to load
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            int64_t r = next[j];
+            if (r >= V) {
+                bad_id(status);
+                r = -1;
+            }
+            there[j] = r >= 0 ? left : 0;
+            src[j] = w + r * D + c0;
         }
-        next = id_at(t);  // on its way while this span is moved
-        if constexpr (VEC) {
-            Group<W, N> v[FLIGHT];
+        Y* const dst = y + t * D + c0;
+        const int64_t now = t;
+        t += TOKENS * step_tokens;
+        if constexpr (TOKENS == 1) {
+            span += step_spans;
+            if (span >= spans.by) {
+                span -= spans.by;
+                ++t;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j)  // on their way while these rows are moved
+            next[j] = id_at(t + j * step_tokens);
+        Group<W, N> v[TOKENS][FLIGHT];
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j)
 #pragma unroll
             for (int i = 0; i < FLIGHT; ++i)
-                if (r >= 0 && i * 32 * N < left) v[i].load(src + i * 32 * N);
+                if (i * 32 * N < there[j]) v[j][i].load(src[j] + i * 32 * N);
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            if (j > 0 && now + j * step_tokens >= T) break;
+            Y* const out = dst + j * step_tokens * D;
 #pragma unroll
             for (int i = 0; i < FLIGHT; ++i) {
                 float x[N];
-                v[i].get(x);
+                v[j][i].get(x);
 #pragma unroll
-                for (int k = 0; k < N; ++k) x[k] = r >= 0 ? x[k] * scale : 0.0f;
-                if (i * 32 * N < left) store_vec<N>(dst + i * 32 * N, x);
+                for (int k = 0; k < N; ++k) x[k] = there[j] > 0 ? x[k] * scale : 0.0f;
+                if (i * 32 * N >= left) continue;
+                if constexpr (VEC)
+                    store_vec<N>(out + i * 32 * N, x);
+                else
+                    store1(out, i * 32, x[0]);
             }
-        } else {
-            W v[FLIGHT];
-#pragma unroll
-            for (int i = 0; i < FLIGHT; ++i)
-                if (r >= 0 && i * 32 < left) v[i] = __ldg(src + i * 32);
-#pragma unroll
-            for (int i = 0; i < FLIGHT; ++i)
-                if (i * 32 < left) store1(dst, i * 32, r >= 0 ? static_cast<float>(v[i]) * scale : 0.0f);
         }
     }
 }
@@ -1242,8 +1268,9 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
         using B = std::remove_pointer_t<decltype(y)>;
         constexpr int64_t per = kLookupVec<A, B>;
         constexpr int flight = per * sizeof(A) < 16 ? 8 : 4;
-        auto launch = [&](auto kernel, int64_t columns) {
-            const int64_t units = T * ((D + columns - 1) / columns);
+        auto launch = [&](auto kernel, int64_t columns, int tokens = 1) {
+            if (T < 32LL * sms) tokens = 1;  // a warp each
+            const int64_t units = (T + tokens - 1) / tokens * ((D + columns - 1) / columns);
             const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
             // 64 blocks an SM: a few spans a warp, and blocks that end are replaced
             // (65536 x 4096 fp32 to bf16, Zipf tokens: 153 us; eight resident ones 157)
@@ -1252,13 +1279,20 @@ extern "C" forge_status forge_embedding(const void* ids, forge_dtype id_dtype, i
             kernel<<<blocks, kThreads, 0, s>>>(ids, id_dtype == FORGE_I64, w, y, T, V, D, scale,
                                                Divide(spans), warps / spans, warps % spans, status);
         };
-        // single elements: as many in flight as a row has for each lane, up to 16
-        if (D % per == 0 && aligned(w, per * sizeof(A)) && aligned(y, per * sizeof(B)))
-            launch(forge_embedding_kernel<A, B, true, flight>, 32 * per * flight);
-        else if (D <= 256)
-            launch(forge_embedding_kernel<A, B, false, 8>, 32 * 8);
-        else
-            launch(forge_embedding_kernel<A, B, false, 16>, 32 * 16);
+        if (D % per == 0 && aligned(w, per * sizeof(A)) && aligned(y, per * sizeof(B))) {
+            if (D <= 32 * per)
+                launch(forge_embedding_kernel<A, B, true, 1, 4>, 32 * per, 4);
+            else if (D <= 64 * per)
+                launch(forge_embedding_kernel<A, B, true, 2, 2>, 64 * per, 2);
+            else
+                launch(forge_embedding_kernel<A, B, true, flight, 1>, 32 * per * flight);
+        } else if (D <= 128) {
+            launch(forge_embedding_kernel<A, B, false, 4, 4>, 128, 4);
+        } else if (D <= 256) {
+            launch(forge_embedding_kernel<A, B, false, 8, 2>, 256, 2);
+        } else {
+            launch(forge_embedding_kernel<A, B, false, 16, 1>, 512);
+        }
     };
     auto out = [&](auto* w) {
         if (y_dtype == FORGE_F32)
