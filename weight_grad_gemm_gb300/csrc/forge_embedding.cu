@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads)
 // 32 x 32 counters gives the places, and the items are moved in order.
 // Reading all ids in every block costs T x kClasses reads from L2, a few
 // percent of the T x D gradient elements that follow.  Bound by the latency of
-// its steps: 7-8 us for 2048 tokens of 50001 rows, 16 us for 32768 of 131072.
+// its steps: 8-9 us for 8192 tokens of 16384 rows, 11-12 us for 16384 of 65536.
 constexpr int kClassBits = 7;
 constexpr int kClasses = 1 << kClassBits;
 constexpr int kOrderThreads = 1024;
@@ -264,7 +264,7 @@ struct Order {
     int32_t later;  // rows of `partial` in front of those of pieces that go on
 };
 
-constexpr int kIdFlight = 16;  // loads of ids in flight per lane
+constexpr int kIdFlight = 4;  // loads of ids in flight per lane (16 made 2048 to 18000 tokens 2-3 us slower)
 
 template <typename ID>
 __global__ void __launch_bounds__(kOrderThreads, 1)
