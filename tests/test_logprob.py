@@ -186,6 +186,35 @@ def test_top_ties_and_orders(cuda_device, V, kind):
 
 
 @gpu
+@pytest.mark.parametrize("k", [5, 32])
+@pytest.mark.parametrize("R,V", [(1900, 3001), (1900, 33000), (500, 100003), (40, 100003), (3, 3001)])
+def test_top_of_masked_and_equal_rows(cuda_device, R, V, k):
+    """Constrained decoding: few entries above a mask of -inf or of a finite
+    value, in rows by one to eight warps and by clusters.  Indices are exact."""
+    g = torch.Generator(device="cuda").manual_seed(R + V)
+    y = torch.randn(R, V, generator=g, device="cuda").mul_(3).bfloat16()
+    row = torch.arange(R, device="cuda")[:, None]
+    keep = torch.tensor([0, 1, 3, 4, 31, 33, 200], device="cuda")[row % 7]
+    rank = torch.rand(R, V, generator=g, device="cuda").argsort(1).argsort(1)
+    for mask in (-math.inf, torch.finfo(torch.bfloat16).min, -1e4, 0.0):
+        x = torch.where(rank < keep, y, mask)
+        x[:, V // 2:] = torch.where(row % 5 == 4, mask, x[:, V // 2:])
+        x = torch.where(row % 11 == 10, y, x).bfloat16()
+        o = forward(x, None, k=k)
+        value, index = torch.sort(x.float() + 0.0, dim=1, descending=True, stable=True)
+        assert torch.equal(o["top_index"], index[:, :k].int())
+        # relative to the largest entry: the lowest finite value takes all digits of a sum
+        top = value[:, :1].double().clamp(min=-1e39)
+        want = value[:, :k].double() - top - torch.exp(x.double() - top).sum(1, keepdim=True).log()
+        want = torch.where(top == -1e39, -math.inf, want)
+        fine = torch.isfinite(want)
+        assert torch.equal(o["top_logprob"][~fine].double(), want[~fine])
+        bound = (value[:, :1].double().abs().clamp(max=1e4) + want.abs().clamp(max=1e30) + 16) * 2.0 ** -21
+        ok = (o["top_logprob"].double() - want).abs() <= bound
+        assert ok[fine].all()
+
+
+@gpu
 def test_optional_outputs_and_no_targets(cuda_device):
     x, xg = logits_of(4, 3001, 5)
     check(x, xg, None, k=6)

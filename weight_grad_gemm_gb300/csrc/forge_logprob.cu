@@ -190,6 +190,7 @@ __device__ __forceinline__ uint32_t key_of(float v)
     const uint32_t b = __float_as_uint(v + 0.0f);
     return v != v ? 0xFFFFFFFFu : b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
+constexpr uint32_t kLowest = 0x00800000u;  // of the lowest finite number
 __device__ __forceinline__ float value_of(uint32_t key)
 {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
@@ -257,6 +258,13 @@ struct Held {
     int n;
 };
 
+__device__ __forceinline__ Held cut(Tops& w, Held h, int k, int lane)
+{
+    h.n = keep_best(w.room, h.n, k, lane);
+    if (h.n == k && w.room[k - 1] > h.bound) h.bound = w.room[k - 1];
+    return h;
+}
+
 // Adds one entry of each lane to the warp's room where it reaches the bound.
 __device__ __forceinline__ Held offer(Tops& w, Held h, float v, int64_t column, bool live, int k,
                                       int lane)
@@ -268,16 +276,12 @@ __device__ __forceinline__ Held offer(Tops& w, Held h, float v, int64_t column, 
     if (pass) w.room[h.n + __popc(all & ((1u << lane) - 1u))] = rank;
     h.n += __popc(all);
     __syncwarp();
-    if (h.n > kRoom - 32) {
-        h.n = keep_best(w.room, h.n, k, lane);
-        if (h.n == k && w.room[k - 1] > h.bound) h.bound = w.room[k - 1];
-    }
-    return h;
+    return h.n > kRoom - 32 ? cut(w, h, k, lane) : h;
 }
 
-// Offers the entries of the noted vectors that reach the bound of now, 32 at a
-// time; or, where a warp had more to note than its list takes, reads all its
-// vectors again, first + lane + stride i.
+// Keeps the entries of the noted vectors that reach the bound of now, a lane a
+// vector; or, where a warp had more to note than its list takes, reads all its
+// vectors again, first + lane + stride i, and offers their entries.
 template <typename T>
 __device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t* number, int noted,
                                        bool over, Held h, const uint4* xv, int64_t col0, int k,
@@ -285,21 +289,66 @@ __device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t
 {
     constexpr int N = Vec<T>::N;
     __syncwarp();
-    const int32_t n = over ? (nv + stride - 1) / stride * 32 : noted;
-    for (int32_t i0 = 0; i0 < n; i0 += 32) {
+    for (int32_t i0 = 0; i0 < noted && !over; i0 += 32) {
         const int32_t i = i0 + lane;
-        const int32_t v = i >= n ? nv : (over ? i / 32 * stride + first + lane : number[i]);
-        const bool live = v < nv;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (live) u = over ? __ldg(xv + v) : list[i];
+        const bool live = i < noted;
+        const uint4 u = live ? list[i] : make_uint4(0, 0, 0, 0);
+        const int64_t column = col0 + static_cast<int64_t>(live ? number[i] : 0) * N;
         const float least = value_of(static_cast<uint32_t>(h.bound >> 32));
-        if (!__any_sync(0xffffffffu, live && !(Vec<T>::top(packed_max<T>(u)) < least))) continue;
+        uint32_t mask = 0;
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-            float a, b;
-            split(Vec<T>::two(u, j), a, b);
-            h = offer(w, h, a, col0 + static_cast<int64_t>(v) * N + 2 * j, live, k, lane);
-            h = offer(w, h, b, col0 + static_cast<int64_t>(v) * N + 2 * j + 1, live, k, lane);
+            float x, y;
+            split(Vec<T>::two(u, j), x, y);
+            mask |= (!(x < least) ? 1u : 0u) << (2 * j) | (!(y < least) ? 2u : 0u) << (2 * j);
+        }
+        if (!live) mask = 0;
+        if (!__any_sync(0xffffffffu, mask != 0)) continue;
+        const int own = __popc(mask);
+        int upto = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += up;
+        }
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        const T* x = reinterpret_cast<const T*>(list + (live ? i : 0));
+        if (h.n + all <= kRoom) {
+            for (int at = h.n + upto - own; mask != 0; mask &= mask - 1) {
+                const int j = __ffs(mask) - 1;
+                w.room[at++] = rank_of(load1(x, j), column + j);
+            }
+            h.n += all;
+            __syncwarp();
+            if (h.n > kRoom - 32) h = cut(w, h, k, lane);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) h = offer(w, h, load1(x, j), column + j, live, k, lane);
+        }
+    }
+    constexpr int kLoads = 2;  // in flight
+    for (int32_t v0 = first; v0 < nv && over; v0 += kLoads * stride) {
+        uint4 u[kLoads];
+#pragma unroll
+        for (int f = 0; f < kLoads; ++f) {
+            const int32_t v = v0 + f * stride + lane;
+            u[f] = v < nv ? __ldg(xv + v) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < kLoads; ++f) {
+            const int32_t v = v0 + f * stride + lane;
+            const bool live = v < nv;
+            // a bound that is an entry found already, in a lower column, has to be exceeded
+            const float least = value_of(static_cast<uint32_t>(h.bound >> 32)), top = Vec<T>::top(packed_max<T>(u[f]));
+            const bool found = static_cast<uint32_t>(h.bound) != 0;
+            if (!__any_sync(0xffffffffu, live && !(found ? top <= least : top < least))) continue;
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                float a, b;
+                split(Vec<T>::two(u[f], j), a, b);
+                h = offer(w, h, a, col0 + static_cast<int64_t>(v) * N + 2 * j, live, k, lane);
+                h = offer(w, h, b, col0 + static_cast<int64_t>(v) * N + 2 * j + 1, live, k, lane);
+            }
         }
     }
     __syncwarp();
@@ -443,8 +492,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     int32_t* const number = reinterpret_cast<int32_t*>(s_lists + kWarps * room) + warp * room;
     if constexpr (TOP)
         if (rwarp == 0) s_best[mine][lane] = 0;  // no entry
-    Held held{0, 0};               // the warp's entries
-    float bound_v = -INFINITY;     // the value of held.bound
+    // the warp's entries; -inf is never among them
+    Held held{static_cast<uint64_t>(kLowest) << 32, 0};
+    float bound_v = value_of(kLowest);  // the value of held.bound
     int noted = 0;                 // the warp's vectors
     bool over = false;             // there were more than the list takes
 
@@ -469,23 +519,24 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 #pragma unroll
         for (int o = 1; o < kGroupLanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
         volatile float* groups = s_group[mine];
-        if (tid % kGroupLanes == 0) groups[tid / kGroupLanes] = g;
-        if (wait)
-            sync();
-        else
-            __syncwarp();
-        const uint32_t a = key_of(groups[lane]);
+        if constexpr (WARPS > 1) {
+            if (tid % kGroupLanes == 0) groups[tid / kGroupLanes] = g;
+            if (wait)
+                sync();
+            else
+                __syncwarp();
+        }
+        const uint32_t a = key_of(WARPS > 1 ? groups[lane] : g);
         const uint32_t b = kUsed > 32 ? key_of(groups[lane + kUsed - 32]) : 0;
         uint32_t high = __reduce_max_sync(0xffffffffu, a > b ? a : b);
         // the halvings start from what all groups reach that have an entry, if they are k
-        constexpr uint32_t kEmpty = 0x007FFFFFu;  // -inf
-        const bool has_a = a > kEmpty, has_b = kUsed > 32 && b > kEmpty;
+        const bool has_a = a >= kLowest, has_b = kUsed > 32 && b >= kLowest;
         uint32_t low = has_a ? a : 0xFFFFFFFFu;
         if (has_b && b < low) low = b;
         low = __reduce_min_sync(0xffffffffu, low);
         if (__popc(__ballot_sync(0xffffffffu, has_a)) + __popc(__ballot_sync(0xffffffffu, has_b)) < k) low = 0;
         low = max(low, static_cast<uint32_t>(held.bound >> 32));
-        for (int i = 0; i < 8 && low < high; ++i) {
+        for (int i = 0; i < 6 && low < high; ++i) {
             const uint32_t middle = high - (high - low) / 2;
             const int n = __popc(__ballot_sync(0xffffffffu, a >= middle)) +
                           __popc(__ballot_sync(0xffffffffu, kUsed > 32 && b >= middle));
@@ -665,6 +716,19 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         if (p.lse) p.lse[r] = bad ? NAN : (empty ? -INFINITY : fmaf(p.scale, all.m, ln_s));
         if (p.entropy) p.entropy[r] = bad ? NAN : (empty ? 0.0f : ln_s - kLn2 * all.w / all.s);
     }
+    if constexpr (TOP)
+        if (rwarp == 0) {
+            // fewer than k entries above -inf: the first columns of -inf follow, and as
+            // fewer than k columns are not -inf they are among the first k
+            const int have = __popc(__ballot_sync(0xffffffffu, lane < k && s_best[mine][lane] != 0));
+            if (have < k) {
+                const bool masked = lane < k && load1(x, lane) == -INFINITY;
+                const uint32_t all = __ballot_sync(0xffffffffu, masked);
+                const int at = have + __popc(all & ((1u << lane) - 1u));
+                if (masked && at < k) s_best[mine][at] = rank_of(-INFINITY, lane);
+                __syncwarp();
+            }
+        }
     if constexpr (TOP)
         for (int i = tid; i < k; i += kThreads) {
             const uint64_t e = s_best[mine][i];
