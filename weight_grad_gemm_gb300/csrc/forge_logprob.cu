@@ -397,9 +397,13 @@ __device__ __forceinline__ void join_lanes(Stats& st, float c)
 // In the loop a tile costs one comparison of its maximum with the bound; its
 // vectors that reach it, some five times k in all, are kept aside and looked
 // into after the last bound, which leaves a few entries more than k.  What this
-// costs is instructions: the same rows with five alternatives take 340 us, 6.3
-// TB/s, with 32 412 us; looking at every vector's entries as they passed took
-// 1149 and 3642 us.
+// costs is instructions: the same rows with five alternatives take 341 us, 6.3
+// TB/s, with 32 402 us; looking at every vector's entries as they passed took
+// 1149 and 3642 us.  Entries of -inf are never among them: where fewer than k
+// others are, the first columns of -inf are added at the end (2048 x 131072 rows
+// masked to three entries: 100 us, 400 with -inf in the lists).  More vectors
+// than the list takes (masks of a finite value, equal logits) means that the
+// warp reads its part again: 225 us.
 template <typename T, int WARPS, bool TOP>
 __global__ void __launch_bounds__(32 * kWarps, 4)
     forge_token_logprob_kernel(const T* logits, const Args p, int split)
@@ -509,12 +513,12 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             st.m = m;
         }
     };
-    // A bound from the groups' maxima: the largest value found in eight
-    // halvings that at least k of them reach.  Only where `wait` is set are the
+    // A bound from the groups' maxima: the largest value found in some halvings
+    // that at least k of them reach.  Only where `wait` is set are the
     // other warps' maxima those of now; an older one (a word is read whole, and
     // maxima only grow) leaves the bound lower, which changes what is looked
     // into but not what is found.
-    auto tighten = [&](bool wait) {
+    auto tighten = [&](bool wait, int steps) {
         float g = st.m;
 #pragma unroll
         for (int o = 1; o < kGroupLanes; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -526,29 +530,36 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             else
                 __syncwarp();
         }
-        const uint32_t a = key_of(WARPS > 1 ? groups[lane] : g);
-        const uint32_t b = kUsed > 32 ? key_of(groups[lane + kUsed - 32]) : 0;
-        uint32_t high = __reduce_max_sync(0xffffffffu, a > b ? a : b);
-        // the halvings start from what all groups reach that have an entry, if they are k
-        const bool has_a = a >= kLowest, has_b = kUsed > 32 && b >= kLowest;
-        uint32_t low = has_a ? a : 0xFFFFFFFFu;
-        if (has_b && b < low) low = b;
-        low = __reduce_min_sync(0xffffffffu, low);
-        if (__popc(__ballot_sync(0xffffffffu, has_a)) + __popc(__ballot_sync(0xffffffffu, has_b)) < k) low = 0;
-        low = max(low, static_cast<uint32_t>(held.bound >> 32));
-        for (int i = 0; i < 6 && low < high; ++i) {
-            const uint32_t middle = high - (high - low) / 2;
-            const int n = __popc(__ballot_sync(0xffffffffu, a >= middle)) +
-                          __popc(__ballot_sync(0xffffffffu, kUsed > 32 && b >= middle));
-            if (n >= k)
-                low = middle;
-            else
-                high = middle - 1;
-        }
-        const uint64_t floor = static_cast<uint64_t>(low) << 32;
+        const float a = WARPS > 1 ? groups[lane] : g;
+        const float b = kUsed > 32 ? groups[lane + kUsed - 32] : -INFINITY;
+        auto reach = [&](float v) {
+            return __popc(__ballot_sync(0xffffffffu, a >= v)) +
+                   (kUsed > 32 ? __popc(__ballot_sync(0xffffffffu, b >= v)) : 0);
+        };
+        // what all groups reach that have an entry, if they are k
+        const uint32_t ka = key_of(a), kb = kUsed > 32 ? key_of(b) : 0;
+        uint32_t least = ka >= kLowest ? ka : 0xFFFFFFFFu;
+        if (kUsed > 32 && kb >= kLowest && kb < least) least = kb;
+        float low = value_of(__reduce_min_sync(0xffffffffu, least));
+        if (reach(value_of(kLowest)) < k) return;
+        low = fmaxf(low, value_of(static_cast<uint32_t>(held.bound >> 32)));
+        float high = value_of(__reduce_max_sync(0xffffffffu, ka > kb ? ka : kb));
+        // only what lies within 2^256 in probability of the largest entry is halved: below
+        // that stand masks, and all groups' bound serves
+        const float down = high - __fdividef(256.0f, c);
+        if (low < down && reach(down) >= k) low = down;
+        if (low >= down)
+            for (int i = 0; i < steps; ++i) {
+                const float middle = 0.5f * (low + high);
+                if (reach(middle) >= k)
+                    low = middle;
+                else
+                    high = middle;
+            }
+        const uint64_t floor = static_cast<uint64_t>(key_of(low)) << 32;
         if (floor > held.bound) {
             held.bound = floor;
-            bound_v = value_of(low);
+            bound_v = low;
         }
     };
 
@@ -585,7 +596,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         const float tm = Vec<T>::top(pm);
         raise(tm);
         if constexpr (TOP) {  // before the sums: the tile's registers end with them
-            if (tile == 0 || ((tile & (tile + 1)) == 0 && tile + 1 < tiles)) tighten(tile == 0);
+            if (tile == 0 || ((tile & (tile + 1)) == 0 && tile + 1 < tiles)) tighten(tile == 0, 5);
             if (__any_sync(0xffffffffu, !(tm < bound_v))) {
 #pragma unroll
                 for (int f = 0; f < F; ++f) {
@@ -628,7 +639,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         st.w = a + b;
     }
     if constexpr (TOP) {
-        if (tiles > 1) tighten(false);
+        if (tiles > 1) tighten(false, 8);
         held = look_into<T>(tops, list, number, noted, over, held, xv, col0, k, lane, tid - lane,
                             kThreads, nv);
     }
