@@ -203,7 +203,7 @@ struct Group<__nv_bfloat16, 4> {
 // out = in times the factor, in vectors of 16 bytes of the wider type, so that
 // a warp stores whole sectors.  The chunks are walked from the last to the
 // first: what the norm's pass read last is still in L2.  Bound by HBM: 973 M
-// fp32 gradients into bf16, the norm's pass with it, 1430-1460 us for the 9.7 GB
+// fp32 gradients into bf16, the norm's pass with it, 1430-1470 us for the 9.7 GB
 // that two passes move, 6.7 TB/s.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads)

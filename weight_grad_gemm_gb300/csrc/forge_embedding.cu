@@ -974,8 +974,8 @@ __device__ __forceinline__ void fetch_ahead(const void* base, int64_t from, int6
 // All rows in one launch: the blocks for the pieces of huge rows and for medium
 // rows come first, as they take longest, then those for the others.  Bound by
 // HBM: dW written, or W, m, v read and written, once, and dY read once.  32768
-// Zipf tokens, 131072 x 4096: 355-360 us for dW from bf16 dY (6.7 TB/s), 1930
-// us fused with AdamW on fp32 state (6.8 TB/s).  Sums stored from bf16
+// Zipf tokens, 131072 x 4096: 377 us for dW from bf16 dY (6.4 TB/s), 1956 us
+// fused with AdamW on fp32 state (6.7 TB/s), the order before included.  Sums stored from bf16
 // vectors: five blocks an SM (48 registers) against four, uniform tokens 399
 // against 434 us; the other forms would spill (13321 x 220 fp32: 40 us with
 // five, 33 with four).
