@@ -238,6 +238,41 @@ def test_gradient_bad_ids_streams_and_graphs(cuda_device):
         assert torch.equal(dW, other)
 
 
+def test_what_the_order_writes_is_read_by_plain_loads():
+    """The kernels behind the order live while it writes its tables, and
+    read-only loads (__ldg) ask for data that nothing writes meanwhile."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(fg.__file__), "csrc", "forge_embedding.cu")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    assert not re.findall(r"__ld\w+\(\s*(?:o\.|partial)\w*", code)
+
+
+@gpu
+@pytest.mark.parametrize("T,V,D", [(600, 5000, 264), (3000, 9000, 37), (6000, 700, 520)])
+def test_calls_one_after_another_see_their_own_order(cuda_device, T, V, D):
+    """Calls on one stream without a wait share their scratch: what one reads
+    of the order must not be what the call before left there."""
+    dY = randn((T, D), 1, "bf16").cuda()
+    ids = [token_ids(T, V, s, kind).cuda() for s in range(4) for kind in ("zipf", "uniform", "one", "ordered")]
+    alone, together = [], [torch.empty(V, D, device="cuda") for _ in ids]
+    for i in ids:
+        dW = torch.empty(V, D, device="cuda")
+        fg.forge_embedding_grad(dY, i, dW)
+        torch.cuda.synchronize()
+        alone.append(dW)
+    for _ in range(3):
+        for i, dW in zip(ids, together):
+            fg.forge_embedding_grad(dY, i, dW)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, together))
+        for dW in together:
+            dW.fill_(9.0)
+    for i, dW in zip(ids, alone):
+        G, A, n = sums(dY.cpu(), i.cpu(), V, 1.0)
+        assert torch.all((dW.cpu().double() - G).abs() <= (n + 2) * 2.0 ** -24 * A)
+
+
 @gpu
 def test_gradient_past_32_bit_offsets(cuda_device):
     T, D = 33000, 65540  # 2.2e9 elements of dY

@@ -247,7 +247,9 @@ constexpr int kOrderSmem = 2 * kOrderShared * static_cast<int>(sizeof(int2));
 
 // The kernels that follow the order are launched while it runs, so that their
 // blocks stand ready when it ends; they wait here for its end (and the one
-// before) before they read anything.
+// before) before they read anything.  What the kernel before wrote (order, at,
+// seg, partial) is read by plain loads only: __ldg asks for data that nothing
+// writes while the reading kernel lives, and this one lives by then.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -615,7 +617,7 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
 #pragma unroll
     for (int i = 0; i < kPiece / 32; ++i) {
         const int32_t place = p0 + 32 * i + lane;
-        const int32_t here = place < T ? __ldg(o.at + place).y : 0;
+        const int32_t here = place < T ? o.at[place].y : 0;
         const uint32_t found = __ballot_sync(0xffffffffu, here > kHuge);
         if (found != 0) {
             at = p0 + 32 * i + __ffs(found) - 1;
@@ -625,7 +627,7 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
     auto piece = [&](int32_t a, int32_t e, int32_t slot) {
         float g[P::H][P::N] = {};
         for (int32_t i0 = a; i0 < e; i0 += 32) {
-            const int32_t token = i0 + lane < e ? __ldg(o.order + i0 + lane) : 0;
+            const int32_t token = i0 + lane < e ? o.order[i0 + lane] : 0;
             part.template add_rows<kTokens>(
                 dY, e - i0 < 32 ? e - i0 : 32,
                 [&](int32_t i) { return __shfl_sync(0xffffffffu, token, i & 31); }, g);
@@ -635,9 +637,9 @@ __device__ __forceinline__ void sum_pieces(const G* dY, int64_t unit, int64_t T,
             if (part.has(h)) store_sum(partial + static_cast<int64_t>(slot) * D + part.c0 + part.column(h), g[h]);
     };
     const int64_t p1 = static_cast<int64_t>(p0) + kPiece;
-    const int2 first = __ldg(o.at + p0);
+    const int2 first = o.at[p0];
     if (first.x >= 0 && first.y == 0) {
-        const int2 s = __ldg(o.seg + first.x);
+        const int2 s = o.seg[first.x];
         if (s.y - s.x > kHuge)
             piece(p0, static_cast<int32_t>(s.y < p1 ? s.y : p1), o.later + p0 / kPiece);
     }
@@ -694,7 +696,7 @@ __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t 
     static_assert(kMediumPlaces == 64);
     if (warp < 2) {
         const int32_t place = p0 + static_cast<int32_t>(threadIdx.x);
-        const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+        const int2 here = place < T ? o.at[place] : make_int2(-1, 0);
         const bool start = here.y > kShort && here.y <= (T > kFew ? kHuge : kFew);
         const uint32_t found = __ballot_sync(0xffffffffu, start);
         if (start) {
@@ -716,7 +718,7 @@ __device__ __forceinline__ void medium_rows(const G* dY, int64_t block, int64_t 
         float g[P::H][P::N] = {};
         for (int32_t j = warp; j < s.y; j += 32 * kWarps) {
             const int32_t mine = j + lane * kWarps;
-            const int32_t token = mine < s.y ? __ldg(o.order + s.x + mine) : 0;
+            const int32_t token = mine < s.y ? o.order[s.x + mine] : 0;
             const int32_t n = (s.y - j + kWarps - 1) / kWarps;
             part.template add_rows<kTokens>(
                 dY, n < 32 ? n : 32, [&](int32_t i) { return __shfl_sync(0xffffffffu, token, i & 31); }, g);
@@ -756,7 +758,7 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
     int64_t step_columns;
     const uint32_t step_rows = static_cast<uint32_t>(vectors(kThreads * U, step_columns));
     auto places = [&](uint32_t r) {
-        return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
+        return r < V && o.seg ? o.seg[r] : make_int2(0, 0);
     };
     uint32_t row[U], column[U];
     int2 s[U];
@@ -793,7 +795,7 @@ __device__ __forceinline__ void dense_rows(const G* dY, int64_t block, uint32_t 
             float x[N] = {};
             if (live[u] && s[u].y > s[u].x)
                 add_rows<F>(dY + column[u] * N, s[u].y - s[u].x,
-                            [&](int32_t i) { return __ldg(o.order + s[u].x + i); }, D, x);
+                            [&](int32_t i) { return o.order[s[u].x + i]; }, D, x);
 #pragma unroll
             for (int k = 0; k < N; ++k) g[u * N + k] = x[k] * scale;
         }
@@ -845,7 +847,7 @@ __device__ __forceinline__ void dense_ragged(const G* dY, int64_t block, uint32_
     const uint32_t step_rows = static_cast<uint32_t>(width(step, rest));
     const int32_t step_columns = static_cast<int32_t>(rest);
     auto places = [&](uint32_t r) {
-        return r < V && o.seg ? __ldg(o.seg + r) : make_int2(0, 0);
+        return r < V && o.seg ? o.seg[r] : make_int2(0, 0);
     };
     int64_t at = (block * turns * kThreads + threadIdx.x) * 4;
     uint32_t row = static_cast<uint32_t>(width(at, rest));
@@ -867,7 +869,7 @@ __device__ __forceinline__ void dense_ragged(const G* dY, int64_t block, uint32_
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const bool there = i + u < part.y;
-                    const G* row = dY + static_cast<int64_t>(__ldg(o.order + (there ? i + u : i))) * D + c;
+                    const G* row = dY + static_cast<int64_t>(o.order[there ? i + u : i]) * D + c;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         x[u][k] = there && k >= k0 && k < k1 ? load1(row, k) : 0.0f;
@@ -938,8 +940,8 @@ __device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t 
     const int64_t p0 = unit / slices * kTouchPlaces, c0 = slice * kTouchColumns<VEC>;
     if (p0 >= T) return;
     const int64_t place = p0 + lane;
-    const int2 here = lane < kTouchPlaces && place < T ? __ldg(o.at + place) : make_int2(-1, 0);
-    const int32_t token = lane < kTouchPlaces + kShort && place < T ? __ldg(o.order + place) : 0;
+    const int2 here = lane < kTouchPlaces && place < T ? o.at[place] : make_int2(-1, 0);
+    const int32_t token = lane < kTouchPlaces + kShort && place < T ? o.order[place] : 0;
     const P part{c0, D, lane};
     for (uint32_t left = __ballot_sync(0xffffffffu, here.y > 0 && here.y <= kShort); left != 0;
          left &= left - 1) {
@@ -1043,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kHuge / kThreads; ++i) {
         const int32_t place = p0 + i * kThreads + static_cast<int32_t>(threadIdx.x);
-        const int2 here = place < T ? __ldg(o.at + place) : make_int2(-1, 0);
+        const int2 here = place < T ? o.at[place] : make_int2(-1, 0);
         if (here.y > kHuge) {
             s_first = place;
             s_n = here.y;
