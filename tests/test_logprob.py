@@ -215,6 +215,51 @@ def test_top_of_masked_and_equal_rows(cuda_device, R, V, k):
 
 
 @gpu
+@pytest.mark.parametrize("plateau", [0.0, -1e4])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,vectors,offset", [(2000, 1024, 0), (2000, 1400, 1), (600, 5000, 0), (600, 14000, 3),
+                                              (40, 3000, 0), (3, 20000, 0), (1, 12500, 1)])
+def test_top_ties_between_the_end_of_a_row_and_its_middle(cuda_device, R, vectors, offset, dtype, plateau):
+    """Equal allowed tokens over a plateau, some in the unaligned end of the
+    row: the lower column comes first.  The entries lie in vectors 8 modulo 256
+    and in the first entry of the end, so that few maxima of a row's threads
+    exceed the plateau and its warps read their vectors again; rows by one to
+    eight warps and by clusters."""
+    N = 4 if dtype == "f32" else 8
+    head = (N - offset) % N
+    reach = vectors // 8 if R < 300 else vectors  # of the first block of a cluster
+    for end in (1, 2, N - 1):
+        V = head + vectors * N + end
+        ld = (V + N - 1) // N * N
+        x = torch.full((R, V), plateau)
+        g = torch.Generator().manual_seed(V)
+        row = torch.arange(R)
+        for i in range(3):  # tied entries of the middle: one, two or three
+            v = torch.randint(0, max(1, reach // 256), (R,), generator=g) * 256 + 8
+            x[row, torch.where(i <= row % 3, head + v * N + (row + i) % N, V - end)] = 1.0
+        x[row, V - end] = 1.0
+        x[row[row % 4 != 0], head + 8 * N + 1] = 2.0
+        if head:
+            x[row[row % 5 == 0], 0] = 1.0
+        for k in (1, 2, 3, 4, 9):
+            xg = to_gpu(x.to(DT[dtype]), ld, offset)
+            o = forward(xg, None, k=k)
+            want = torch.sort(xg.float(), dim=1, descending=True, stable=True).indices[:, :k]
+            wrong = (o["top_index"] != want).any(1)
+            assert not wrong.any(), (end, k, int(wrong.sum()), o["top_index"][wrong][0].tolist(), want[wrong][0].tolist())
+
+
+@gpu
+def test_top_ties_of_a_row_end_that_reaches_the_bound_first(cuda_device):
+    x = torch.zeros(2000, 4097)  # rows 4100 apart
+    x[:, 32], x[:, 2592], x[:, 4096] = 2.0, 1.0, 1.0
+    assert forward(to_gpu(x, 4100), None, k=2)["top_index"].unique(dim=0).tolist() == [[32, 2592]]
+    x = torch.zeros(1, 50002)
+    x[:, 1056], x[:, 50000], x[:, 50001] = 1.0, 1.0, 1.0
+    assert forward(to_gpu(x, 50004), None, k=2)["top_index"].tolist() == [[1056, 50000]]
+
+
+@gpu
 def test_optional_outputs_and_no_targets(cuda_device):
     x, xg = logits_of(4, 3001, 5)
     check(x, xg, None, k=6)

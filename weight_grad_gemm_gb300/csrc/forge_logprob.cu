@@ -327,6 +327,7 @@ __device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t
         }
     }
     constexpr int kLoads = 2;  // in flight
+    const uint32_t end = static_cast<uint32_t>(col0) + static_cast<uint32_t>(nv) * N;
     for (int32_t v0 = first; v0 < nv && over; v0 += kLoads * stride) {
         uint4 u[kLoads];
 #pragma unroll
@@ -338,9 +339,11 @@ __device__ __noinline__ Held look_into(Tops& w, const uint4* list, const int32_t
         for (int f = 0; f < kLoads; ++f) {
             const int32_t v = v0 + f * stride + lane;
             const bool live = v < nv;
-            // a bound that is an entry found already, in a lower column, has to be exceeded
+            // a bound that is the rank of a vector's entry, found already in a lower column, has
+            // to be exceeded; the row's end was offered before and lies past all vectors, as does
+            // the column of a bound that is no entry
             const float least = value_of(static_cast<uint32_t>(h.bound >> 32)), top = Vec<T>::top(packed_max<T>(u[f]));
-            const bool found = static_cast<uint32_t>(h.bound) != 0;
+            const bool found = ~static_cast<uint32_t>(h.bound) < end;
             if (!__any_sync(0xffffffffu, live && !(found ? top <= least : top < least))) continue;
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
