@@ -488,10 +488,12 @@ FORGE_API forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dtyp
  *   grads   host array of P device pointers (NULL only where n[j] = 0) to n[j]
  *           elements of dtype (FORGE_BF16 or FORGE_F32); read during the call only.
  *   norm    device fp32[1], written (0 for P = 0).
- * Squares are summed in fp32 over at most a few hundred elements and in fp64
- * from there, in a fixed order: bitwise reproducible.  NaN and infinities
- * propagate; a |g| above 1.8e19 counts as infinite.  Takes a few KB of
- * stream-ordered scratch from the library's memory pool.
+ * Squares are summed in fp32 over at most a few hundred elements (in fp64 where
+ * such a sum leaves fp32's range or its terms lose digits at the range's lower
+ * end) and in fp64 from there, in a fixed order: bitwise reproducible, and as
+ * exact for gradients of any size that dtype holds.  NaN and infinities
+ * propagate.  Takes a few KB of stream-ordered scratch from the library's
+ * memory pool.
  */
 FORGE_API forge_status forge_grad_norm(const void* const* grads, const int64_t* n, int32_t P,
                                        forge_dtype dtype, float* norm, forge_stream_t stream);

@@ -52,6 +52,30 @@ def test_norm(cuda_device, kind, dtype, offset):
 
 
 @gpu
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("std", [1e-37, 1e-30, 1e-23, 1e-18, 1e-15, 1e15, 1e18, 1e25, 1e33])
+def test_norm_over_the_whole_range(cuda_device, std, dtype, offset):
+    """Gradients whose squares fp32 does not hold (below 2^-149, above 2^128) or
+    holds with few digits (below 2^-126); the bound is that of ordinary ones."""
+    for sizes in ([1], [7, 4096], SIZES["mixed"]):
+        ts = tensors(sizes, dtype, offset=offset, std=std)
+        norm = torch.full((1,), 9.0, device="cuda")
+        fg.forge_grad_norm(ts, norm)
+        want = norm_of(ts)
+        assert abs(norm.item() - want) <= 2.0 ** -15 * want + 2.0 ** -149
+        # beside ordinary ones, zeros of both signs among them
+        zeros = torch.zeros(50001, dtype=DT[dtype], device="cuda")
+        zeros[::3] = -0.0
+        usual = tensors([3000], dtype, std=max(std, 1e-19))
+        fg.forge_grad_norm([zeros, *ts, *usual], norm)
+        want = norm_of([*ts, *usual])
+        assert abs(norm.item() - want) <= 2.0 ** -15 * want
+        fg.forge_grad_norm([zeros], norm)
+        assert norm.item() == 0.0
+
+
+@gpu
 @pytest.mark.parametrize("offset", [0, 1, 3])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -115,9 +115,29 @@ __device__ __forceinline__ double block_sum(double x, double* sh)
     return s;
 }
 
+// The squares of a thread's part of a chunk, nv vectors and the elements behind
+// them, in fp64.
+template <typename T>
+__device__ __noinline__ double wide_square_sum(const T* g, int nv, int n)
+{
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    double s = 0.0;
+    auto add = [&](int i) {
+        const double x = static_cast<double>(load1(g, i));
+        s = fma(x, x, s);
+    };
+    for (int v = threadIdx.x; v < nv; v += kThreads)
+        for (int k = 0; k < N; ++k) add(v * N + k);
+    for (int i = nv * N + threadIdx.x; i < n; i += kThreads) add(i);
+    return s;
+}
+
 // part[block] = the sum of squares over this block's chunks.  A thread adds at
-// most 2^15 / 256 = 128 squares in fp32 before it goes on in fp64.  Bound by
-// HBM: each gradient is read once.
+// most 2^15 / 256 = 128 squares in fp32 before it goes on in fp64; where that sum
+// is infinite, or so small that squares may have lost digits below 2^-149 or
+// vanished, it adds them again in fp64.  The bits of all elements together tell
+// zeros, which need no second look, from squares that vanished.  Bound by HBM:
+// each gradient is read once.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     forge_square_sum_kernel(const __grid_constant__ Table t, double* part)
@@ -132,6 +152,7 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t left = t.n[j] - first;
         const int n = static_cast<int>(left < (1 << t.chunk_bits) ? left : 1 << t.chunk_bits);
         float s[4] = {};
+        uint32_t bits = 0;
         int done = 0;
         if (is_aligned(g, 16)) {
             const int nv = n / N;
@@ -146,6 +167,7 @@ __global__ void __launch_bounds__(kThreads)
                 for (int f = 0; f < kFlight; ++f) {
                     float x[N];
                     to_float(u[f], x);
+                    bits |= (u[f].x | u[f].y) | (u[f].z | u[f].w);
 #pragma unroll
                     for (int k = 0; k < N; ++k) s[k & 3] = fmaf(x[k], x[k], s[k & 3]);
                 }
@@ -154,9 +176,15 @@ __global__ void __launch_bounds__(kThreads)
         }
         for (int i = done + threadIdx.x; i < n; i += kThreads) {
             const float x = load1(g, i);
+            bits |= __float_as_uint(x);
             s[0] = fmaf(x, x, s[0]);
         }
-        total += static_cast<double>((s[0] + s[1]) + (s[2] + s[3]));
+        const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        constexpr uint32_t kNoSigns = sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+        if ((sum < 0x1p-100f && (bits & kNoSigns) != 0) || sum == INFINITY)
+            total += wide_square_sum(g, done / N, n);
+        else
+            total += static_cast<double>(sum);
     }
     total = block_sum(total, sh);
     if (threadIdx.x == 0) part[blockIdx.x] = total;
