@@ -505,7 +505,8 @@ FORGE_API forge_status forge_grad_norm(const void* const* grads, const int64_t* 
  *   norm    device fp32[1]: forge_grad_norm's (under data parallelism, after
  *           its square was summed over the ranks).  A NaN norm makes every
  *           output NaN, as torch.nn.utils.clip_grad_norm_ does.
- *   max_norm  >= 0 (infinity: never clips).
+ *   max_norm  >= 0 (infinity: never clips, not even by an infinite norm, where
+ *           torch.nn.utils.clip_grad_norm_ makes every output NaN).
  *   out     host array of P device pointers to n[j] elements of out_dtype.
  *           out[j] may be grads[j] (clipping in place) when out_dtype is dtype;
  *           a tensor clipped in place by a factor of exactly 1 is left as it is.

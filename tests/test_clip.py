@@ -132,6 +132,24 @@ def test_zero_nan_and_infinite_gradients(cuda_device):
 
 
 @gpu
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_no_limit_clips_nothing_even_by_an_infinite_norm(cuda_device, out):
+    ts = tensors([1000, 77], "f32")
+    ts[1][5] = -math.inf
+    norm = torch.empty(1, device="cuda")
+    fg.forge_grad_norm(ts, norm)
+    assert norm.item() == math.inf
+    os_ = [torch.full_like(t, 3.0, dtype=DT[out]) for t in ts]
+    fg.forge_clip_grads(ts, norm, os_, max_norm=math.inf)
+    assert all(torch.equal(o, t.to(DT[out])) for o, t in zip(os_, ts))
+    kept = [t.clone() for t in ts]
+    fg.forge_clip_grads(ts, norm, max_norm=math.inf)
+    assert all(torch.equal(t, u) for t, u in zip(ts, kept))
+    fg.forge_clip_grads(ts, torch.full((1,), math.nan, device="cuda"), max_norm=math.inf)
+    assert all(torch.isnan(t).all() for t in ts)
+
+
+@gpu
 def test_large_tensor_past_32_bit_offsets(cuda_device):
     n = (1 << 31) + 12345
     t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")

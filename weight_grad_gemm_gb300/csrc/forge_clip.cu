@@ -239,8 +239,10 @@ __global__ void __launch_bounds__(kThreads)
 {
     constexpr int N = 16 / (sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
     constexpr int F = N * sizeof(T) < 16 ? 2 * kFlight : kFlight;
-    const float q = max_norm / (*norm + 1e-6f);
-    const float m = q > 1.0f ? 1.0f : q;  // a NaN stays
+    const float all = *norm;
+    const float q = max_norm / (all + 1e-6f);
+    // without a limit nothing is clipped, an infinite norm neither; a NaN stays
+    const float m = q > 1.0f || (all == INFINITY && max_norm == INFINITY) ? 1.0f : q;
     const uint32_t chunks = t.begin[t.count];
     for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
         const uint32_t c = chunks - 1 - b;
