@@ -390,6 +390,27 @@ def test_refusals_before_any_launch():
 
 
 @gpu
+def test_scratch_that_cannot_be_had_is_one_calls_error(cuda_device):
+    """A call whose scratch exceeds the address space fails before any launch,
+    and the calls after it are not told of it."""
+    x, ids = torch.zeros(64, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    p, L = ctypes.c_void_p(x.data_ptr()), fg.lib()
+    W, Y = torch.ones(4, 8, device="cuda"), torch.empty(3, 8, device="cuda")
+    tokens, width = 1 << 30, 1 << 24  # 2^24 columns of partial sums for 18 M pieces: 1.3 PB
+    for call in (
+            lambda: L.forge_embedding_grad(p, fg.FORGE_F32, ctypes.c_void_p(ids.data_ptr()), fg.FORGE_I32, tokens, 4,
+                                           width, 1.0, p, 0, None),
+            lambda: L.forge_embedding_adamw(p, fg.FORGE_F32, ctypes.c_void_p(ids.data_ptr()), fg.FORGE_I32, tokens, 4,
+                                            width, 1.0, p, p, p, fg.FORGE_F32, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1, None)):
+        assert call() == fg.FORGE_ERR_CUDA
+        fg.forge_embedding(ids, W, Y)
+        assert Y.eq(1).all()
+        assert call() == fg.FORGE_ERR_CUDA
+        Y.fill_(3.0)
+        assert Y.eq(3).all()
+
+
+@gpu
 def test_binding_refuses_what_does_not_fit(cuda_device):
     W = torch.zeros(6, 8, device="cuda")
     Y = torch.zeros(3, 8, device="cuda")

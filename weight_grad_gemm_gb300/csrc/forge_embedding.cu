@@ -1219,6 +1219,15 @@ cudaError_t launch_grad(Sum what, bool state_bf16, const G* dY, const void* ids,
     return e;
 }
 
+// A refused allocation or launch is this call's to report: the runtime's record of
+// it is cleared, so that the next call's check of its own launch does not find it.
+forge_status reported(cudaError_t e)
+{
+    if (e == cudaSuccess) return FORGE_OK;
+    cudaGetLastError();
+    return FORGE_ERR_CUDA;
+}
+
 cudaError_t grad(Sum what, bool state_bf16, const void* dY, forge_dtype dy_dtype, const void* ids,
                  forge_dtype id_dtype, int64_t T, int64_t V, int64_t D, float scale, float* dW,
                  const Params& p, int sms, cudaStream_t s)
@@ -1327,9 +1336,8 @@ extern "C" forge_status forge_embedding_grad(const void* dY, forge_dtype dy_dtyp
     Params p{};
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad(accumulate ? SUM_ADD : SUM_STORE, false, dY, dy_dtype, ids, id_dtype,
-                               T, V, D, scale, dW, p, sms, s);
-    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    return reported(grad(accumulate ? SUM_ADD : SUM_STORE, false, dY, dy_dtype, ids, id_dtype,
+                         T, V, D, scale, dW, p, sms, s));
 }
 
 extern "C" forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dtype,
@@ -1358,7 +1366,6 @@ extern "C" forge_status forge_embedding_adamw(const void* dY, forge_dtype dy_dty
     p.s2 = v;
     p.status = device_status_word();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad(SUM_ADAMW, state_dtype == FORGE_BF16, dY, dy_dtype, ids, id_dtype, T,
-                               V, D, scale, nullptr, p, sms, s);
-    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    return reported(grad(SUM_ADAMW, state_dtype == FORGE_BF16, dY, dy_dtype, ids, id_dtype, T,
+                         V, D, scale, nullptr, p, sms, s));
 }
