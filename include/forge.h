@@ -418,7 +418,8 @@ FORGE_API forge_status forge_token_logprob(const void* logits, forge_dtype dtype
  *   dlogits device [R, V] of out_dtype (FORGE_BF16, rounded once to nearest
  *           even, or FORGE_F32), rows ld_out >= V elements apart, written.  It
  *           may be logits itself when out_dtype and ld_out equal dtype and ld;
- *           any other overlap is not supported.
+ *           rows that share memory in any other way are refused
+ *           (FORGE_ERR_INVALID_ARG).
  * Allocates nothing.
  */
 FORGE_API forge_status forge_token_logprob_grad(

@@ -448,6 +448,52 @@ def test_refusals_before_any_launch():
     assert g(lse=ctypes.c_void_p(0x10002)) == fg.FORGE_ERR_MISALIGNED
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="without a GPU what is not refused stops at the device check")
+def test_gradient_refuses_rows_that_share_memory():
+    """Every kind of overlap by the bytes of all rows; in place is none."""
+    L = fg.lib()
+    g = np.random.default_rng(5)
+    seen = set()
+    for _ in range(20000):
+        R, V = int(g.integers(1, 6)), int(g.integers(1, 9))
+        es, eo = (int(x) for x in g.choice([2, 4], 2))
+        ld, ldo = V + int(g.choice([0, 1, 7, 12])), V + int(g.choice([0, 1, 7, 12]))
+        if g.random() < 0.5:
+            ldo = max(V, ld * es // eo)
+        base = 1 << 20
+        other = base + 4 * int(g.integers(-60, 60))
+        own = {base + (r * ld + j) * es + i for r in range(R) for j in range(V) for i in range(es)}
+        theirs = {other + (r * ldo + j) * eo + i for r in range(R) for j in range(V) for i in range(eo)}
+        in_place = other == base and es == eo and (ld == ldo or R == 1)
+        bad = not in_place and bool(own & theirs)
+        code = {2: fg.FORGE_BF16, 4: fg.FORGE_F32}
+        s = L.forge_token_logprob_grad(ctypes.c_void_p(base), code[es], R, V, ld, FAKE, fg.FORGE_I32, 1.0, FAKE, FAKE,
+                                       None, None, ctypes.c_void_p(other), code[eo], ldo, None)
+        assert s == (fg.FORGE_ERR_INVALID_ARG if bad else fg.FORGE_ERR_UNSUPPORTED_DEVICE), \
+            (R, V, es, eo, ld, ldo, other - base, bad)
+        seen.add((bad, in_place, es == eo, ld * es == ldo * eo))
+    assert len(seen) > 8
+
+
+@gpu
+def test_gradient_beside_its_logits_in_one_buffer(cuda_device):
+    R, V = 9, 1000
+    x, _ = logits_of(R, V, 3)
+    t = targets(R, V, 3)
+    f = forward(x.cuda(), t.cuda())
+    a = torch.ones(R, device="cuda")
+    want = grad(x.cuda(), t.cuda(), f["lse"], a)
+    buf = torch.zeros(R, 2 * V, device="cuda")
+    buf[:, :V] = x.cuda()
+    assert torch.equal(grad(buf[:, :V], t.cuda(), f["lse"], a, dest=buf[:, V:]), want)
+    assert torch.equal(buf[:, :V].cpu(), x)
+    for dest in (buf[:, 1:V + 1], buf[:, V - 1:2 * V - 1], buf.view(-1)[: R * V].view(R, V),
+                 buf.view(torch.bfloat16)[:, :V]):
+        with pytest.raises(fg.ForgeError):
+            fg.forge_token_logprob_grad(buf[:, :V], t.cuda(), f["lse"], a, dest)
+    assert torch.equal(buf[:, :V].cpu(), x)
+
+
 @gpu
 def test_binding_refuses_what_does_not_fit(cuda_device):
     x = torch.zeros(4, 8, device="cuda")

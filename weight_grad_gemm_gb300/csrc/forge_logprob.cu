@@ -998,6 +998,26 @@ forge_status check_rows(int64_t R, int64_t V, int64_t ld, float scale)
     return FORGE_OK;
 }
 
+// Whether rows of `a` bytes, `pa` apart from x on, and rows of `b` bytes, `pb` apart
+// from y on, share a byte (R of each; a <= pa, b <= pb).
+bool rows_overlap(uintptr_t x, int64_t a, int64_t pa, uintptr_t y, int64_t b, int64_t pb, int64_t R)
+{
+    using Wide = __int128;  // no product of R and a pitch overflows
+    if (y < x) return rows_overlap(y, b, pb, x, a, pa, R);
+    const Wide d = y - x;
+    if (d >= Wide{R - 1} * pa + a) return false;
+    if (pa == pb) {  // each row of y starts r behind a row of x, the first behind row q
+        const Wide q = d / pa, r = d % pa;
+        return (q < R && r < a) || (q + 1 < R && r + b > pa);
+    }
+    for (int64_t j = 0; j < R; ++j) {
+        const Wide at = d + Wide{j} * pb;                  // of row j of y
+        const Wide i = at < a ? 0 : (at - a) / pa + 1;  // the first row of x that ends behind it
+        if (i < R && i * pa < at + b) return true;
+    }
+    return false;
+}
+
 }  // namespace logprob
 }  // namespace forge
 
@@ -1057,6 +1077,12 @@ extern "C" forge_status forge_token_logprob_grad(
         !aligned(lse, 4) || !aligned(grad_logprob, 4) || !aligned(entropy, 4) ||
         !aligned(grad_entropy, 4) || !aligned(dlogits, size_of(out_dtype)))
         return FORGE_ERR_MISALIGNED;
+    const int64_t es = size_of(dtype), eo = size_of(out_dtype);
+    const bool in_place = logits == dlogits && es == eo && (ld == ld_out || R == 1);
+    if (R > 0 && !in_place &&
+        rows_overlap(reinterpret_cast<uintptr_t>(logits), V * es, ld * es,
+                     reinterpret_cast<uintptr_t>(dlogits), V * eo, ld_out * eo, R))
+        return FORGE_ERR_INVALID_ARG;
     int sms = 0;
     if ((st = device_sms(&sms)) != FORGE_OK) return st;
     if (R == 0) return FORGE_OK;
