@@ -511,7 +511,8 @@ FORGE_API forge_status forge_grad_norm(const void* const* grads, const int64_t* 
  *   out     host array of P device pointers to n[j] elements of out_dtype.
  *           out[j] may be grads[j] (clipping in place) when out_dtype is dtype;
  *           a tensor clipped in place by a factor of exactly 1 is left as it is.
- *           Other overlaps are not supported.
+ *           Any other overlap of the two is refused (FORGE_ERR_INVALID_ARG);
+ *           overlaps with another tensor of the lists are not supported.
  * Allocates nothing.
  */
 FORGE_API forge_status forge_clip_grads(const void* const* grads, const int64_t* n, int32_t P,

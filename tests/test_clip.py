@@ -205,6 +205,24 @@ def test_refusals_before_any_launch():
     assert c(odt=fg.FORGE_I32) == fg.FORGE_ERR_UNSUPPORTED_DTYPE
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="without a GPU what is not refused stops at the device check")
+def test_clip_refuses_outputs_that_overlap_their_gradients():
+    L = fg.lib()
+    es = {fg.FORGE_F32: 4, fg.FORGE_BF16: 2}
+    n = 24
+    for dt in es:
+        for odt in es:
+            for d in range(-100, 101, 4):
+                for size in (n, 0):
+                    g = (ctypes.c_void_p * 2)(0x90000, 0x10000)
+                    o = (ctypes.c_void_p * 2)(0x80000, 0x10000 + d)
+                    sizes = (ctypes.c_int64 * 2)(5, size)
+                    s = L.forge_clip_grads(g, sizes, 2, dt, FAKE, 1.0, o, odt, None)
+                    apart = d >= size * es[dt] or -d >= size * es[odt] or size == 0
+                    fine = apart or (d == 0 and dt == odt)
+                    assert s == (fg.FORGE_ERR_UNSUPPORTED_DEVICE if fine else fg.FORGE_ERR_INVALID_ARG), (dt, odt, d)
+
+
 @gpu
 def test_binding_refuses_what_does_not_fit(cuda_device):
     ts = tensors([4, 5], "f32")

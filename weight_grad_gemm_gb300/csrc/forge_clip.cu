@@ -290,6 +290,19 @@ forge_status check_list(const void* const* ptr, const int64_t* n, int32_t P)
     return FORGE_OK;
 }
 
+// No tensor shares memory with its own output but in place.
+forge_status check_overlap(const void* const* in, int64_t es, void* const* out, int64_t eo,
+                           const int64_t* n, int32_t P)
+{
+    for (int32_t j = 0; j < P; ++j) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(in[j]), y = reinterpret_cast<uintptr_t>(out[j]);
+        if (n[j] == 0 || (x == y && es == eo)) continue;
+        const uintptr_t size = y < x ? n[j] * eo : n[j] * es;  // of the lower one
+        if ((y < x ? x - y : y - x) < size) return FORGE_ERR_INVALID_ARG;
+    }
+    return FORGE_OK;
+}
+
 forge_status check_memory(const void* const* ptr, const int64_t* n, int32_t P, forge_dtype dt)
 {
     // runs of tensors with elements (an empty tensor's pointer means nothing)
@@ -397,6 +410,7 @@ extern "C" forge_status forge_clip_grads(const void* const* grads, const int64_t
     forge_status st = check_list(grads, n, P);
     if (st != FORGE_OK || (st = check_list(out, n, P)) != FORGE_OK) return st;
     if (!is_float(dtype) || !is_float(out_dtype)) return FORGE_ERR_UNSUPPORTED_DTYPE;
+    if ((st = check_overlap(grads, size_of(dtype), out, size_of(out_dtype), n, P)) != FORGE_OK) return st;
     int sms = 0;
     if ((st = device_sms(&sms)) != FORGE_OK) return st;
     const void* one[] = {norm};
