@@ -210,3 +210,19 @@ def test_valid_call_without_gpu_fails_closed(L):
     assert L.forge_owner_adamw(FAKE, FAKE, FAKE, FAKE, 64, fg.FORGE_F32, *HP, 1, None) == \
         fg.FORGE_ERR_UNSUPPORTED_DEVICE
     assert fg.forge_get_device_status() == fg.FORGE_ERR_UNSUPPORTED_DEVICE
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_with_and_without_pytorchs_own_accessor(monkeypatch, private):
+    import types
+
+    import torch
+    like = types.SimpleNamespace(device=types.SimpleNamespace(index=3))
+    monkeypatch.setattr(fg, "_current_stream", None, raising=False)
+    if private:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda i: types.SimpleNamespace(cuda_stream=100 + i))
+    assert [fg._stream(None, like) for _ in range(2)] == [103, 103]
+    assert fg._stream(types.SimpleNamespace(cuda_stream=7), like).value == 7

@@ -131,12 +131,24 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_current_stream = None  # device index -> the current stream's handle, found on first use
+
+
+def _find_current_stream():
+    """PyTorch's own accessor, without a Stream object around the handle (0.2
+    instead of 2 us a call), or the public one where a PyTorch lacks it."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream, like):
-    if stream is None:
-        import torch
-        # the current stream's handle without a Stream object around it: 0.2 instead of 2 us a call
-        return torch._C._cuda_getCurrentRawStream(like.device.index)
-    return ctypes.c_void_p(stream.cuda_stream)
+    global _current_stream
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _current_stream is None:
+        _current_stream = _find_current_stream()
+    return _current_stream(like.device.index)
 
 
 def _check(status: int, where: str):
