@@ -178,6 +178,54 @@ def test_rows_of_every_length(cuda_device, lengths, D):
         assert torch.all((dW.cpu().double() - G).abs() <= (terms + 2) * 2.0 ** -24 * A)
 
 
+def in_class(n, c, rows, seed):
+    """n tokens of the rows c, c + 128, ... (`rows` of them): one residue class of the order."""
+    return torch.randint(0, rows, (n,), generator=torch.Generator().manual_seed(seed)) * 128 + c
+
+
+ORDERS = {  # ids, vocabulary: sorts by one, two and three digits, lists in shared and in global memory
+    "two digits": lambda: (torch.randint(0, 10000, (30000,), generator=torch.Generator().manual_seed(1)), 10000),
+    "three digits": lambda: (torch.randint(0, 200000, (30000,), generator=torch.Generator().manual_seed(2)), 200000),
+    "one digit in global memory": lambda: (in_class(5000, 5, 30, 3), 4000),
+    "two digits in global memory": lambda: (in_class(5000, 127, 78, 4), 10000),
+    "three digits in global memory": lambda: (in_class(9001, 0, 1562, 5), 200000),
+    "three digits, every class": lambda: (torch.cat([in_class(150 + c, c, 1200, c) for c in range(128)]), 1200 * 128),
+    "limits of the lists": lambda: (torch.cat([in_class(n, c, 70, c) for c, n in enumerate((128, 129, 4096, 4097, 0, 1))]),
+                                    9000),
+    "global beside shared": lambda: (torch.cat([in_class(4500, 2, 1500, 6), in_class(6000, 1, 1500, 7),
+                                                in_class(300, 3, 1500, 8)]), 192001)}
+
+
+@gpu
+@pytest.mark.parametrize("D", [12, 5])
+@pytest.mark.parametrize("kind", list(ORDERS))
+def test_order_of_many_tokens(cuda_device, kind, D):
+    """Integers, whose sums are exact in any order: each token in its row, once."""
+    ids, V = ORDERS[kind]()
+    g = torch.Generator().manual_seed(9)
+    ids = ids[torch.randperm(len(ids), generator=g)]
+    ids = torch.where(torch.rand(len(ids), generator=g) < 0.02, -1, ids)
+    dY = torch.randint(-64, 65, (len(ids), D), generator=g).float()
+    G, _, n = sums(dY, ids, V, 1.0)
+    start = torch.randint(-64, 65, (V, D), generator=g).float()
+    for idt in (torch.int32, torch.int64):
+        for dt in (torch.float32, torch.bfloat16):
+            dW, acc = torch.full((V, D), 7.0, device="cuda"), start.cuda()
+            fg.forge_embedding_grad(dY.to(dt).cuda(), ids.to(idt).cuda(), dW)
+            fg.forge_embedding_grad(dY.to(dt).cuda(), ids.to(idt).cuda(), acc, accumulate=True)
+            assert torch.equal(dW.cpu().double(), G)
+            assert torch.equal(acc.cpu().double(), G + start)
+    # rows of up to 16 tokens: token after token, as the ids lie
+    dY = randn((len(ids), D), 8, "f32")
+    fg.forge_embedding_grad(dY.cuda(), ids.cuda(), dW)
+    want = torch.zeros(V, D)
+    few = (n[:, 0] <= 16)
+    for t in torch.nonzero((ids >= 0) & few[ids.clamp(min=0)])[:, 0].tolist():
+        want[ids[t]] += dY[t]
+    assert torch.equal(dW.cpu()[few], want[few])
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+
+
 @gpu
 @pytest.mark.parametrize("offset", [1, 2, 4])
 @pytest.mark.parametrize("D", [1, 130, 264])
@@ -350,6 +398,65 @@ def test_fused_step_equals_gradient_then_owner_step(cuda_device):
     fg.forge_embedding_adamw(dY, ids, *b, scale=2.0, **HP)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@gpu
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,kind,offset", [(12000, 500, 301, "huge", 0), (9000, 400, 7, "huge", 0),
+                                               (12000, 500, 301, "huge", 1), (9000, 400, 264, "huge", 3),
+                                               (6000, 30, 1023, "zipf", 0), (40000, 3000, 33, "zipf", 0),
+                                               (30000, 200000, 6, "uniform", 0)])
+def test_fused_step_with_rows_of_many_tokens(cuda_device, T, V, D, kind, offset, dtype, state):
+    ids = token_ids(T, V, T + 1, kind)
+    dY = randn((T, D), 3, dtype, 1e-2)
+    W, m = randn((V, D), 4, "f32", 0.02), randn((V, D), 5, state, 1e-3)
+    v = (randn((V, D), 6, "f32", 1e-3) ** 2 + 1e-9).to(DT[state])
+    G, A, n = sums(dY, ids, V, 0.5)
+    fused = [shifted(t, offset) for t in (W, m, v)]
+    fg.forge_embedding_adamw(shifted(dY, offset), ids.cuda(), *fused, scale=0.5, **HP)
+    want = adamw_reference(G, A, n, W.double(), m.double(), v.double(), HP)
+    for name, got, (x, tol) in zip("Wmv", fused, want):
+        if name != "W" and state == "bf16":
+            tol = tol + x.abs() * 2.0 ** -8
+        err = (got.cpu().double() - x).abs()
+        assert torch.all(err <= tol), (name, float((err / tol.clamp(min=1e-300)).max()))
+    dW, owner = torch.empty(V, D, device="cuda"), [t.cuda() for t in (W, m, v)]
+    fg.forge_embedding_grad(dY.cuda(), ids.cuda(), dW, scale=0.5)
+    fg.forge_owner_adamw(dW, *owner, **HP)
+    assert all(torch.equal(a, b) for a, b in zip(fused, owner))
+
+
+@gpu
+@pytest.mark.parametrize("D", [32768, 32769])
+def test_fused_step_past_32_bit_offsets(cuda_device, D):
+    V = 70000  # 2.3e9 elements of W, m, v
+    W, m, v = (torch.zeros(V, D, device="cuda", dtype=dt) for dt in (torch.float32, torch.bfloat16, torch.bfloat16))
+    rows = torch.tensor([0, V // 2, V - 2, V - 1])
+    ids = torch.cat([rows[torch.tensor([3, 0, 3, 1])], rows[2].repeat(40)]).cuda()  # one row of 40 tokens
+    dY = randn((len(ids), D), 1, "f32").cuda()
+    start = [randn((4, D), 2 + i, "f32").abs().to(t.dtype).cuda() for i, t in enumerate((W, m, v))]
+    for t, a in zip((W, m, v), start):
+        t[rows] = a
+    fg.forge_embedding_adamw(dY, ids, W, m, v, **HP)
+    small = [a.clone() for a in start]  # the same four rows alone
+    fg.forge_embedding_adamw(dY, torch.searchsorted(rows.cuda(), ids), *small, **HP)
+    for t, a in zip((W, m, v), small):
+        assert torch.equal(t[rows], a)
+        assert not t[1:100].any() and not t[V - 100:V - 2].any()
+    del W, m, v
+    T, D = 33000, 65541  # 2.2e9 elements of dY
+    dY = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    dY[-1], dY[0], dY[-20:-1] = 2.0, 1.0, 0.5
+    ids = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    ids[-1] = ids[0] = 1
+    ids[-20:-1] = 2
+    got = [torch.zeros(3, D, device="cuda") for _ in range(3)]
+    fg.forge_embedding_adamw(dY, ids, *got, **HP)
+    want = [torch.zeros(3, D, device="cuda") for _ in range(3)]
+    G = torch.tensor([0.0, 3.0, 9.5], device="cuda")[:, None].expand(3, D).contiguous()
+    fg.forge_owner_adamw(G, *want, **HP)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # ---- refusals --------------------------------------------------------------------
