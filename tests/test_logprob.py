@@ -260,6 +260,37 @@ def test_top_ties_of_a_row_end_that_reaches_the_bound_first(cuda_device):
 
 
 @gpu
+@pytest.mark.parametrize("k", [0, 5, 20])
+@pytest.mark.parametrize("R,V,dtype", [(4000, 32768, "bf16"), (4000, 16000, "f32"), (4000, 98304, "bf16"),
+                                       (2000, 131072, "bf16"), (2000, 400003, "bf16"), (2000, 49152, "f32"),
+                                       (20, 400003, "f32")])
+def test_long_rows_of_equal_logits(cuda_device, R, V, dtype, k):
+    """Equal terms round the same way each time they are added, below an entry
+    of any size; the bound is that of all rows (runs of a tile and of tiles)."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for kind in ("one above", "some above"):
+        x = torch.zeros(R, V, device="cuda", dtype=DT[dtype])
+        if kind == "one above":
+            x[:, 7] = torch.linspace(0, 16, R, device="cuda").to(DT[dtype])
+        else:
+            x.scatter_(1, torch.randint(0, V, (R, 200), generator=g, device="cuda"),
+                       torch.randn(R, 200, generator=g, device="cuda").mul_(3).to(DT[dtype]))
+        t = torch.arange(R, device="cuda") % V
+        o = forward(x, t, k=k)
+        for i in range(0, R, 250):
+            z = x[i:i + 250].double()
+            u = (z.abs().amax(1) + 16) * 2.0 ** -21
+            lse = torch.logsumexp(z, 1)
+            z -= lse[:, None]
+            assert torch.all((o["lse"][i:i + 250] - lse).abs() <= u)
+            assert torch.all((o["logprob"][i:i + 250] - z.gather(1, t[i:i + 250, None])[:, 0]).abs() <= u)
+            if k:
+                assert torch.all((o["top_logprob"][i:i + 250] - z.topk(k, 1).values).abs() <= u[:, None])
+            entropy = -(z.exp() * z).sum(1)
+            assert torch.all((o["entropy"][i:i + 250] - entropy).abs() <= u * (1 + math.log(V)))
+
+
+@gpu
 def test_optional_outputs_and_no_targets(cuda_device):
     x, xg = logits_of(4, 3001, 5)
     check(x, xg, None, k=6)

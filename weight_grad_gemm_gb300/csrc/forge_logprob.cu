@@ -389,8 +389,10 @@ __device__ __forceinline__ void join_lanes(Stats& st, float c)
 //
 // The maximum of a thread's tile moves its reference only where it grows, so an
 // element costs one exponential (of fp32, as are all sums), one addition to s
-// and one to w, two elements an instruction; the parts are joined by lanes,
-// warps and blocks.  The entropy follows from the same sums: H = ln s -
+// and one to w, two elements an instruction.  A tile's sums start at zero and are
+// added to the thread's (in one run over its part of the row, equal logits, whose
+// roundings go one way, put lse off by up to 8e-5 in rows of 400000); the parts
+// are joined by lanes, warps and blocks.  The entropy follows from the same sums: H = ln s -
 // ln 2 w / s, both terms not negative.  Bound by HBM: 8192 x 131072 bf16 takes
 // 297-301 us, 7.1 TB/s.
 //
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         if (rwarp == 0) s_best[mine][lane] = 0;  // no entry
     // the warp's entries; -inf is never among them
     Held held{static_cast<uint64_t>(kLowest) << 32, 0};
-    float bound_v = value_of(kLowest);  // the value of held.bound
+    float bound_v = value_of(kLowest);  // the value that the loop's vectors have to reach
     int noted = 0;                 // the warp's vectors
     bool over = false;             // there were more than the list takes
 
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         if (kUsed > 32 && kb >= kLowest && kb < least) least = kb;
         float low = value_of(__reduce_min_sync(0xffffffffu, least));
         if (reach(value_of(kLowest)) < k) return;
-        low = fmaxf(low, value_of(static_cast<uint32_t>(held.bound >> 32)));
+        low = fmaxf(low, bound_v);
         float high = value_of(__reduce_max_sync(0xffffffffu, ka > kb ? ka : kb));
         // only what lies within 2^256 in probability of the largest entry is halved: below
         // that stand masks, and all groups' bound serves
@@ -559,11 +561,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
                 else
                     high = middle;
             }
-        const uint64_t floor = static_cast<uint64_t>(key_of(low)) << 32;
-        if (floor > held.bound) {
-            held.bound = floor;
-            bound_v = low;
-        }
+        bound_v = fmaxf(bound_v, low);
     };
 
     // the elements outside whole vectors: the first warp of the row
@@ -622,7 +620,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         }
         const float mr = st.m == -INFINITY ? 0.0f : st.m;
         const Pair mm = pair(-mr, -mr), cc = pair(c, c);
-        Pair s2 = pair(st.s, 0.0f), w2 = pair(st.w, 0.0f);
+        Pair s2 = pair(0.0f, 0.0f), w2 = s2;
 #pragma unroll
         for (int f = 0; f < F; ++f)
 #pragma unroll
@@ -637,12 +635,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
             }
         float a, b;
         ::forge::logprob::split(s2, a, b);
-        st.s = a + b;
+        st.s += a + b;
         ::forge::logprob::split(w2, a, b);
-        st.w = a + b;
+        st.w += a + b;
     }
     if constexpr (TOP) {
         if (tiles > 1) tighten(false, 8);
+        held.bound = static_cast<uint64_t>(key_of(bound_v)) << 32;
         held = look_into<T>(tops, list, number, noted, over, held, xv, col0, k, lane, tid - lane,
                             kThreads, nv);
     }
