@@ -924,23 +924,35 @@ cudaError_t launch_forward(const T* x, const Args& p, int split, cudaStream_t s)
 }
 
 // Few warps a row, so that the joins at a row's end are few and other rows'
-// loads cover them, but not so few that the last rows end late, and enough to
-// bound many alternatives well.  With five alternatives: 8000 x 7397 fp32 (1849
-// vectors) one warp 50 us, two 62, four 78; 8192 x 50001 bf16 (6250) 153, 164,
-// 190; 8192 x 131072 bf16 (16384) 338, 345, 350, and without any 332, 328, 310.
-// With twenty: 63, 70, 88; 410, 189, 213; 962, 376, 385.  With 32: 161, 79, 94;
-// 490, 207, 231; 1056, 497, 414.  More warps while the rows' warps do not fill
-// the SMs and each has a few vectors a lane (401 x 1336 bf16, five alternatives:
-// one warp 7.0 us, two 6.6, four 7.8, eight 9.1), then clusters of up to eight
-// blocks, a join of which costs 1-2 us (114 x 10338 bf16: one block 7.4, two
-// 9.2, four 12.5; 16 x 50001 fp32: 12.5, 11.6, 9.9, eight 8.9).
+// loads cover them, but enough to bound many alternatives well.  us by one, two,
+// four warps a row, 8192 rows of bf16 (vectors a row):
+//   alternatives   none           5              20             32
+//   1000           27  29  33     39  47  59     47  53  66     140 59  70
+//   2000           47  48  49     60  70  88     98  80  96     212 88  103  (nine: 66 74 90)
+//   4096           89  87  85     100 111 127    224 128 144    324 140 156
+//   6250           133 133 133    142 157 181    324 181 205    429 196 220
+//   8192           171 162 155    176 184 197    405 211 225    509 230 242
+//   12288          252 239 228    250 260 266    577 289 301    680 325 322
+//   16384          330 313 298    324 335 335    746 367 375    849 453 400
+// Other numbers of rows end elsewhere in a wave, which costs one warp on a long
+// row most.  Five alternatives, 6250 vectors: 1900 rows 50, 49, 53; 3600: 68, 81,
+// 86; 5200: 108, 109, 121.  8192: 1900 rows 61, 57, 58; 3600: 83, 95, 94; 5200:
+// 133, 127, 132.  12288: 2500 rows 114, 108, 99; 5200: 192, 180, 179.  16384: 2500
+// rows 146, 138, 124; 6000: 273, 254, 251; with twenty 2500: 150 by two, 133 by
+// four; 7000: 312, 324.
+// More warps while the rows' warps do not fill the SMs and fewer would take the
+// row in several tiles (bf16, five alternatives, 250 vectors, 1500 rows 6.9, 8.2;
+// 400: 9.2, 8.2; 512 vectors, 600 rows 7.7, 5.9, 7.2; 700: 9.7, 7.7, 6.9; with
+// twenty 137 vectors, 300 rows 7.4, 6.4, 6.9), then clusters of up to eight
+// blocks, a join of which costs 1-2 us (114 x 10338 bf16, five: one block 7.2, two
+// 8.7, four 11.7; 16 x 50001 fp32: 12.0, 11.0, 9.5, eight 9.0).
 template <typename T>
 cudaError_t forward(const T* x, const Args& p, int sms, cudaStream_t s)
 {
     const int64_t nvec = p.V / Vec<T>::N;
-    const int64_t one = p.top_k <= 8 ? 4096 : (p.top_k <= 20 ? 2048 : 0);
+    const int64_t one = p.top_k == 0 ? 4096 : (p.top_k <= 8 ? 7168 : (p.top_k <= 20 ? 1536 : 0));
     int warps = nvec <= one ? 1 : (nvec <= 12288 ? 2 : 4);
-    auto enough = [&](int w) { return nvec >= (w == 2 ? 128 : 128 * w); };
+    auto enough = [&](int w) { return nvec > (w > 2 ? 128 * w : (p.top_k <= 8 ? 320 : 128)); };
     while (warps < kWarps && p.R * warps < 12 * sms && enough(2 * warps)) warps *= 2;
     if (warps == 1) return launch_forward<T, 1>(x, p, 1, s);
     if (warps == 2) return launch_forward<T, 2>(x, p, 1, s);
