@@ -233,9 +233,12 @@ __global__ void __launch_bounds__(kThreads)
 // part of the list into its own 32 counters (equal digits of a warp
 // instruction are found by a match, their lowest lane adds), a scan over the
 // 32 x 32 counters gives the places, and the items are moved in order.
-// Reading all ids in every block costs T x kClasses reads from L2, a few
-// percent of the T x D gradient elements that follow.  Bound by the latency of
-// its steps: 8-9 us for 8192 tokens of 16384 rows, 11-12 us for 16384 of 65536.
+// Reading all ids twice in every block costs 2 T kClasses reads from L2, 1 KB a
+// token of 32-bit ids: an eighth of a row of 4096 bf16 gradients, eight times one
+// of 64.  Bound by the latency of its steps up to some 8192 tokens, by these reads
+// beyond: 6-7 us for 2048 tokens, 7-9 for 8192, 10-12 for 16384, 16 for 32768, 28
+// for 65536, on 128 blocks at any number; 65536 tokens of 131072 x 64 bf16 take 46
+// us in all, with 32768 x 512 66.
 constexpr int kClassBits = 7;
 constexpr int kClasses = 1 << kClassBits;
 constexpr int kOrderThreads = 1024;
@@ -536,8 +539,8 @@ __device__ __forceinline__ void add_rows(const G* column, int32_t n, ROW of, int
 //                 away), row later + a / kPiece for one that goes on at a.  A
 //                 last kernel joins the pieces.
 // Batches of up to kFew tokens do without pieces and that kernel: medium is
-// kFew there, kHuge otherwise (33322 cold Zipf tokens of 222 columns take 73
-// us; with blocks for rows of up to 2048, 175 us for the 1900 of one row).
+// kFew there, kHuge otherwise (33322 Zipf tokens of 123650 x 222 bf16 take 55 us,
+// with blocks for rows of up to 2048 tokens 86; 65536 of 32768 x 512: 66, 86).
 constexpr int kShort = 16;
 constexpr int kFew = 2048;
 constexpr int kHuge = 512;
@@ -966,7 +969,7 @@ __device__ __forceinline__ void touched_rows(const G* dY, int64_t unit, int64_t 
 // While the order is made, its memory pipes are idle: the first blocks, which
 // wait for it anyway, bring the gradients (where they are few) and the state of
 // the first rows into L2.  7628 x 4313 fp32 AdamW with 6 tokens: 121 us against
-// 124; 33322 tokens of 222 columns: 67 against 73.
+// 124; 33322 tokens of 123650 x 222 bf16: 55 against 59.
 __device__ __forceinline__ void fetch_ahead(const void* base, int64_t from, int64_t to)
 {
     for (int64_t i = from + 128 * static_cast<int32_t>(threadIdx.x); i < to; i += 128 * kThreads)

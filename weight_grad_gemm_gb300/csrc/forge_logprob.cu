@@ -228,8 +228,8 @@ struct Tops {
 };
 // The vectors whose maximum reached the bound when they passed, with their
 // numbers: room for what the doublings of the row seen leave as a rule (with
-// 64 + 4 k, 8192 x 131072 bf16 on one warp a row and five alternatives ran over
-// and took 639 instead of 338 us).
+// 64 + 4 k, 8192 x 131072 bf16 on one warp a row and five alternatives run over
+// and take 512 instead of 324 us).
 __host__ __device__ constexpr int list_of(int k) { return k > 0 ? 160 + 2 * k : 0; }
 
 // The warp's n entries cut to the best k, in order; returns their number.
@@ -392,9 +392,9 @@ __device__ __forceinline__ void join_lanes(Stats& st, float c)
 // and one to w, two elements an instruction.  A tile's sums start at zero and are
 // added to the thread's (in one run over its part of the row, equal logits, whose
 // roundings go one way, put lse off by up to 8e-5 in rows of 400000); the parts
-// are joined by lanes, warps and blocks.  The entropy follows from the same sums: H = ln s -
-// ln 2 w / s, both terms not negative.  Bound by HBM: 8192 x 131072 bf16 takes
-// 297-301 us, 7.1 TB/s.
+// are joined by lanes, warps and blocks.  The entropy follows from the same sums:
+// H = ln s - ln 2 w / s, both terms not negative.  Bound by HBM: 8192 x 131072
+// bf16, no row padding, takes 297 us, 7.2 TB/s.
 //
 // Top entries: the threads' maxima so far, by groups of lanes, are distinct
 // entries of the row, and what k of them reach bounds the k-th largest entry
@@ -402,13 +402,13 @@ __device__ __forceinline__ void join_lanes(Stats& st, float c)
 // In the loop a tile costs one comparison of its maximum with the bound; its
 // vectors that reach it, some five times k in all, are kept aside and looked
 // into after the last bound, which leaves a few entries more than k.  What this
-// costs is instructions: the same rows with five alternatives take 341 us, 6.3
-// TB/s, with 32 402 us; looking at every vector's entries as they passed took
+// costs is instructions: the same rows with five alternatives take 334 us, 6.4
+// TB/s, with 32 396 us; looking at every vector's entries as they passed took
 // 1149 and 3642 us.  Entries of -inf are never among them: where fewer than k
 // others are, the first columns of -inf are added at the end (2048 x 131072 rows
-// masked to three entries: 100 us, 400 with -inf in the lists).  More vectors
+// masked to three entries: 96 us, 400 with -inf in the lists).  More vectors
 // than the list takes (masks of a finite value, equal logits) means that the
-// warp reads its part again: 225 us.
+// warp reads its part again: 218-231 us.
 template <typename T, int WARPS, bool TOP>
 __global__ void __launch_bounds__(32 * kWarps, 4)
     forge_token_logprob_kernel(const T* logits, const Args p, int split)
