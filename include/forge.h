@@ -41,11 +41,11 @@
  * the current device (cudaMalloc, a memory pool or a virtual-memory mapping;
  * host memory, managed memory and a peer GPU's memory are refused) and the
  * library keeps no pointer after the call returns.  Calls whose operands TMA
- * can address allocate nothing.  Four cases take stream-ordered scratch from
+ * can address allocate nothing.  These cases take stream-ordered scratch from
  * a memory pool the library creates per device (allocated and freed on
  * `stream`; the pool keeps what it has reserved, at most the largest scratch
  * in use at once, until the process ends):
- *   - an operand (X or dY; for dX, dY or Wb) whose base is not 16-byte
+ *   - an operand (X or dY; for dX, dY or Wb; A or W of the e4m3 products) whose base is not 16-byte
  *     aligned or whose row stride is not a multiple of 16 bytes (any odd
  *     bf16 width, any e4m3 width not divisible by 16) is first copied into
  *     rows padded to 16 bytes (one extra read and write of that operand).
@@ -57,7 +57,9 @@
  *     into a fixed buffer instead;
  *   - forge_backward_adamw without a bf16 weight copy (see there);
  *   - forge_embedding_grad and forge_embedding_adamw (the order of the tokens);
- *   - forge_grad_norm (partial sums).
+ *   - forge_grad_norm (partial sums);
+ *   - forge_layer_norm_grad (partial sums), forge_moe_route (counts of blocks of
+ *     tokens).
  * W, m, v, buf are updated in place.  Calls are asynchronous and ordered on
  * `stream`, and can be captured in a CUDA graph once a first call has run
  * on the device; the return value reports only host-side validation and
@@ -80,6 +82,9 @@
  *                      do not depend on it
  *   FORGE_DGRAD_KERNEL = single | pair the dX kernel form (default: pairs
  *                      unless K fits one 128-token tile)
+ *   FORGE_LINEAR_KERNEL = pair | single[n]  the e4m3 product's form: CTA pairs, or
+ *                      one CTA a tile with n (1-8) CTAs sharing its contraction
+ *                      (default: by the number of tiles)
  *   FORGE_WAIT_TIMEOUT_MS = ms         limit of every device-side wait
  *                      (read once per process; default 10000)
  *
@@ -519,6 +524,165 @@ FORGE_API forge_status forge_clip_grads(const void* const* grads, const int64_t*
                                         forge_dtype dtype, const float* norm, float max_norm,
                                         void* const* out, forge_dtype out_dtype,
                                         forge_stream_t stream);
+
+/*
+ * Layer norm over the rows of x: with mu and var the mean and the mean squared
+ * deviation of a row,
+ *   rstd = 1 / sqrt(var + eps),   y = (x - mu) rstd weight + bias.
+ *   x       device [R, D] of x_dtype (FORGE_BF16 or FORGE_F32), rows ldx >= D
+ *           elements apart, of any width and alignment.
+ *   weight, bias  device fp32 [D]; bias may be NULL (none).
+ *   eps     > 0 and finite.
+ *   y       device [R, D] of y_dtype (FORGE_BF16, rounded once to nearest even,
+ *           or FORGE_F32), rows ldy >= D apart, written.  It may be x itself when
+ *           y_dtype and ldy equal x_dtype and ldx; rows that share memory in any
+ *           other way are refused (FORGE_ERR_INVALID_ARG).
+ *   mean, rstd  device fp32 [R], written for the gradient; each may be NULL.
+ * Statistics are taken in fp32, the deviations from the row's own mean.  A row
+ * with a NaN or an infinity gives NaN.  Allocates nothing.  R = 0 does nothing.
+ */
+FORGE_API forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int64_t ldx,
+                                        const float* weight, const float* bias, int64_t R,
+                                        int64_t D, float eps, void* y, forge_dtype y_dtype,
+                                        int64_t ldy, float* mean, float* rstd,
+                                        forge_stream_t stream);
+
+/*
+ * The gradient of forge_layer_norm: with g = dy weight and xh = (x - mean) rstd,
+ *   dx = rstd (g - mean_row(g) - xh mean_row(g xh)),
+ *   dweight = sum_r dy xh,   dbias = sum_r dy   (+ what is there if accumulate).
+ *   dy, x   device [R, D], each FORGE_BF16 or FORGE_F32, rows lddy, ldx >= D apart.
+ *   weight  device fp32 [D];  mean, rstd  device fp32 [R], from forge_layer_norm.
+ *   dx      device [R, D] of dx_dtype, rows lddx >= D apart, written.  It may be dy
+ *           or x itself where type and row distance agree; rows that share
+ *           memory in any other way are refused.
+ *   dweight device fp32 [D], dbias device fp32 [D] or NULL: written, or added to
+ *           (accumulate != 0).  R = 0 writes zeros (or adds nothing).
+ * Sums over the rows are taken in fp32 in an order that the sizes alone
+ * determine: bitwise reproducible on one GPU.  They take stream-ordered scratch from the
+ * library's memory pool (at most 8 blocks an SM x 2 D floats); a failed
+ * allocation returns FORGE_ERR_CUDA.
+ */
+FORGE_API forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dtype, int64_t lddy,
+                                             const void* x, forge_dtype x_dtype, int64_t ldx,
+                                             const float* weight, const float* mean,
+                                             const float* rstd, int64_t R, int64_t D, void* dx,
+                                             forge_dtype dx_dtype, int64_t lddx, float* dweight,
+                                             float* dbias, int32_t accumulate,
+                                             forge_stream_t stream);
+
+/*
+ * A router: k of E experts for each token, the choices' places in a buffer
+ * packed by expert (the rows that forge_grouped_linear_e4m3 and
+ * forge_grouped_wgrad_adamw take), per-expert counts and the balance loss.  For
+ * token t with logits z, p = softmax(z):
+ *   experts[t]  the k experts with the largest logits, largest first; equal
+ *               logits by the lower expert, NaN above every number.
+ *   weights[t]  their p, over the sum of the chosen p if normalize != 0.
+ *   counts[e], offsets[e]  tokens that chose e, and the sum of the counts before e.
+ *   slots[t]    the choices' rows in the packed buffer: by expert, tokens in order.
+ *   rows[s]     the token of packed row s; -1 behind the last (ids for
+ *               forge_embedding, which gathers the packed rows).
+ *   live, loss  with n the tokens that count and P_e the mean of p_te over them,
+ *               loss = E / (k n) sum_e counts[e] P_e.
+ * Masked experts are -inf: their p is 0 and they are not chosen.  A token with
+ * fewer than k other logits has expert and slot -1 and weight 0 in the places
+ * left; a token with none is padding and counts nowhere.  A NaN or +inf among a
+ * token's logits makes its weights and the loss NaN.
+ *   logits  device [T, E] of dtype (FORGE_BF16 or FORGE_F32), rows ld >= E apart.
+ *   k       1 <= k <= min(E, 32);  E <= 1024;  T k < 2^31.
+ *   experts (int32), weights (fp32)  device [T, k], written.
+ *   counts, offsets  device int32 [E], [E + 1], written.
+ *   slots   device int32 [T, k] or NULL;  rows  device int32 [T k] or NULL.
+ *   live, loss  device int32[1] and fp32[1]; each may be NULL.
+ * No atomics: bitwise reproducible.  More tokens than one block takes (256 at
+ * most) take stream-ordered scratch from the library's memory pool; a failed
+ * allocation returns FORGE_ERR_CUDA.  T = 0 writes zero counts, offsets, live, loss.
+ */
+FORGE_API forge_status forge_moe_route(const void* logits, forge_dtype dtype, int64_t T, int32_t E,
+                                       int64_t ld, int32_t k, int32_t normalize, int32_t* experts,
+                                       float* weights, int32_t* counts, int32_t* offsets,
+                                       int32_t* slots, int32_t* rows, int32_t* live, float* loss,
+                                       forge_stream_t stream);
+
+/*
+ * The gradient of sum_tj grad_weights[t][j] weights[t][j] + grad_loss[0] loss by
+ * the logits of forge_moe_route; the choices and counts are constants.
+ *   logits, dtype, T, E, ld, k, normalize  as given to forge_moe_route.
+ *   experts, counts, live  from it (experts only with grad_weights, counts and
+ *           live only with grad_loss).
+ *   grad_weights  device fp32 [T, k] or NULL;  grad_loss  device fp32[1] or NULL.
+ *   dlogits device [T, E] of out_dtype, rows ld_out >= E apart, written; zeros for
+ *           padding and masked experts.  It may be logits itself when type
+ *           and row distance agree; rows that share memory in any other way are
+ *           refused.
+ * Allocates nothing.
+ */
+FORGE_API forge_status forge_moe_route_grad(const void* logits, forge_dtype dtype, int64_t T,
+                                            int32_t E, int64_t ld, int32_t k, int32_t normalize,
+                                            const int32_t* experts, const int32_t* counts,
+                                            const int32_t* live, const float* grad_weights,
+                                            const float* grad_loss, void* dlogits,
+                                            forge_dtype out_dtype, int64_t ld_out,
+                                            forge_stream_t stream);
+
+/*
+ * e4m3 codes with one scale for each block: forge_quantize_e4m3's recipe
+ * (s = amax / 448; codes nearest to x / s, saturating), block by block; s is 1
+ * where the quotient is 0 (blocks of zeros, or of amax below 2^-141).
+ *   x       device [E, R, C] of x_dtype (FORGE_F32 or FORGE_BF16), rows ldx >= C
+ *           elements apart, matrices R ldx apart.
+ *   block_rows  1: a scale for each 128 entries of a row (activations, gradients);
+ *           128: for each square of 128 x 128 (weights).  Blocks begin at each
+ *           matrix's first row and column; those at its end may be smaller.
+ *   codes   device [E, R, C] bytes, packed, written.
+ *   scales  device fp32 [E, ceil(R / block_rows), ceil(C / 128)], written.
+ * NaN entries are left out of a block's amax (their codes are NaN).  codes and
+ * scales must not overlap x.  Allocates nothing.  E R = 0 does nothing.
+ */
+FORGE_API forge_status forge_quantize_e4m3_blocks(const void* x, forge_dtype x_dtype, int64_t ldx,
+                                                  int64_t E, int64_t R, int64_t C,
+                                                  int32_t block_rows, uint8_t* codes,
+                                                  float* scales, forge_stream_t stream);
+
+/*
+ * The product of e4m3 codes with a scale for each block of 128, in either
+ * direction of a linear layer with the weight W [N, M] (d_in x d_out):
+ *   transpose = 0:  Y [T, M] = A [T, N] W      (the layer's output)
+ *   transpose = 1:  Y [T, N] = A [T, M] W^T    (the input gradient)
+ * both from the same codes and scales of W.
+ *   A, sA   device [T, K] codes and fp32 [T, ceil(K / 128)] scales, K = N or M
+ *           (forge_quantize_e4m3_blocks, block_rows = 1).
+ *   W, sW   device [N, M] codes and fp32 [ceil(N / 128), ceil(M / 128)] scales
+ *           (block_rows = 128).
+ *   Y       device of y_dtype (FORGE_BF16, rounded once to nearest even, or
+ *           FORGE_F32), packed, written; must not overlap an operand.
+ * Each block's products are summed in fp32, and the blocks, times their two
+ * scales, in fp32.  Rows of codes of any width are accepted: an operand whose
+ * base is not 16-byte aligned or whose width is not a multiple of 16 is first
+ * copied into padded rows in stream-ordered scratch from the library's memory
+ * pool (a failed allocation returns FORGE_ERR_CUDA).  T = 0 does nothing.
+ */
+FORGE_API forge_status forge_linear_e4m3(const uint8_t* A, const float* sA, const uint8_t* W,
+                                         const float* sW, void* Y, forge_dtype y_dtype, int64_t T,
+                                         int64_t N, int64_t M, int32_t transpose,
+                                         forge_stream_t stream);
+
+/*
+ * forge_linear_e4m3 by experts: W [E, N, M] and sW [E, ceil(N / 128), ceil(M / 128)],
+ * and expert e's rows of A and Y are [offsets[e], offsets[e + 1]) (device int32
+ * [E + 1], as forge_grouped_wgrad_adamw's; read on the device).  Rows of no
+ * expert, before the first and behind the last, are left as they are in Y.
+ * T_max: the rows of A and Y.  1 <= E <= 1024.  Offsets that descend, are negative
+ * or pass T_max are recorded as FORGE_ERR_INVALID_ARG in the device status word,
+ * and nothing is written.
+ */
+FORGE_API forge_status forge_grouped_linear_e4m3(const uint8_t* A, const float* sA,
+                                                 const uint8_t* W, const float* sW,
+                                                 const int32_t* offsets, int32_t E, void* Y,
+                                                 forge_dtype y_dtype, int64_t T_max, int64_t N,
+                                                 int64_t M, int32_t transpose,
+                                                 forge_stream_t stream);
 
 /* Static description of a status code; never NULL. */
 FORGE_API const char* forge_status_string(forge_status status);

@@ -1,0 +1,361 @@
+"""e4m3 codes by blocks of 128 and the products of such codes, against 64 bits.
+
+Codes and scales follow an exact recipe (a maximum, one fp32 quotient for the
+scale, one for each entry, one rounding to e4m3) and have to be equal.
+
+Product bound.  A product of two e4m3 values is exact in fp32.  The tensor core
+adds 32 of them and its sum at a time; were each addend cut at the largest's
+last fp32 bit, four steps of 33 addends would lose 132 2^-23 < 2^-15 of the sum
+of magnitudes.  The product of the two scales, its product with a block's sum and
+the sums over nk blocks and up to eight shares add (nk + 12) 2^-24.  So
+    |error| <= (2^-15 + (nk + 12) 2^-24) sum |terms|,
+and a bf16 output 2^-8 of the value more.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import weight_grad_gemm_gb300 as fg
+
+gpu = pytest.mark.gpu
+FAKE = ctypes.c_void_p(0x10000)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+F8 = torch.float8_e4m3fn
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+def spread(s, rows, cols, br):
+    return s.repeat_interleave(br, -2)[..., :rows, :].repeat_interleave(128, -1)[..., :cols]
+
+
+def recipe(x, br):
+    """Codes and scales of x [..., R, C] on the CPU."""
+    x = x.detach().cpu().float()
+    R, C = x.shape[-2:]
+    a = torch.nn.functional.pad(torch.nan_to_num(x.abs(), nan=0.0, posinf=float("inf")), (0, -C % 128, 0, -R % br))
+    a = a.unflatten(-1, (-1, 128)).amax(-1).unflatten(-2, (-1, br)).amax(-2)
+    s = a / torch.tensor(448.0)
+    s = torch.where(s > 0, s, torch.tensor(1.0))
+    q = x / spread(s, R, C, br)
+    codes = q.clamp(-448, 448).to(F8)
+    codes = torch.where(torch.isnan(q), torch.tensor(float("nan")).to(F8).float(), codes.float()).to(F8)
+    return codes, s
+
+
+def quantize(x, br, **kw):
+    codes = torch.empty(x.shape, dtype=F8, device="cuda")
+    shape = (*x.shape[:-2], -(-x.shape[-2] // br), blocks(x.shape[-1]))
+    scales = torch.full(shape, 9.0, device="cuda")
+    fg.forge_quantize_e4m3_blocks(x, codes, scales, block_rows=br, **kw)
+    return codes, scales
+
+
+def check_codes(x, br):
+    codes, scales = quantize(x, br)
+    want, ws = recipe(x, br)
+    assert torch.equal(scales.cpu(), ws)
+    got, want = codes.cpu().float(), want.float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+    return codes, scales
+
+
+def values(R, C, dtype, seed=0, E=None):
+    g = torch.Generator().manual_seed(seed)
+    shape = (R, C) if E is None else (E, R, C)
+    x = torch.randn(shape, generator=g) * torch.exp(torch.randn(shape[:-2] + (R, 1), generator=g))
+    return x.to(DT[dtype]).cuda()
+
+
+@gpu
+@pytest.mark.parametrize("br", [1, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 127), (2, 128), (5, 129), (128, 256), (129, 260), (300, 1000), (513, 4100), (256, 4096), (1000, 36), (3, 100000)])
+def test_codes(cuda_device, R, C, dtype, br):
+    check_codes(values(R, C, dtype, seed=R + C), br)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,R,C", [(3, 130, 200), (2, 1, 5), (4, 128, 128), (7, 257, 48)])
+def test_codes_of_stacked_weights(cuda_device, E, R, C, dtype):
+    x = values(R, C, dtype, E=E)
+    for br in (1, 128):
+        codes, scales = check_codes(x, br)
+        for e in range(E):
+            c, s = quantize(x[e], br)
+            assert torch.equal(c.view(torch.uint8), codes[e].view(torch.uint8)) and torch.equal(s, scales[e])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(3, 0), (8, 8), (4, 4), (0, 1)])
+def test_codes_of_strided_rows(cuda_device, pad, offset, dtype):
+    R, C = 140, 392
+    buf = torch.randn(R * (C + pad) + offset, device="cuda").to(DT[dtype])
+    x = buf[offset:].view(R, C + pad)[:, :C]
+    for br in (1, 128):
+        codes, scales = quantize(x, br)
+        c, s = quantize(x.contiguous(), br)
+        assert torch.equal(codes.view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales, s)
+
+
+@gpu
+@pytest.mark.parametrize("br", [1, 128])
+def test_codes_at_the_ends_of_the_range(cuda_device, br):
+    x = torch.zeros(130, 300, device="cuda")
+    x[1, 5] = 3e38
+    x[2, :200] = torch.linspace(-1e-44, 1e-44, 200, device="cuda")
+    x[3, 140] = float("nan")
+    x[3, 141:150] = torch.arange(9, device="cuda").float()
+    x[4, 290:] = 2.0 ** -126
+    x[5, 260] = -float("inf")
+    x[6] = torch.linspace(-1, 1, 300, device="cuda") * 1e-37
+    x[129, 299] = 1.5e-40
+    x[7, 130:140] = torch.tensor([448.0, 432.0, 440.0, 424.0, 1.0, 2.0 ** -9, 2.0 ** -10, 1.5 * 2.0 ** -10, 0.0, -0.0], device="cuda")
+    check_codes(x, br)
+
+
+def operands(T, N, M, transpose, E=None, seed=0):
+    K = M if transpose else N
+    A, sA = quantize(values(T, K, "f32", seed), 1)
+    W, sW = quantize(values(N, M, "f32", seed + 1, E) * 0.02, 128)
+    return A, sA, W, sW
+
+
+def products(A, sA, W, sW, transpose):
+    """The value and the sum of magnitudes of every output, in 64 bits."""
+    a = A.double() * spread(sA, *A.shape, 1).double()
+    w = W.double() * spread(sW, *W.shape[-2:], 128).double()
+    if transpose:
+        w = w.transpose(-1, -2)
+    return a @ w, a.abs() @ w.abs()
+
+
+def check(y, want, mag, K):
+    bound = (2.0 ** -15 + (blocks(K) + 12) * 2.0 ** -24) * mag
+    if y.dtype == torch.bfloat16:
+        bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    bad = (y.double() - want).abs() > bound
+    assert not bad.any(), (int(bad.sum()), float(((y.double() - want).abs() / mag.clamp(min=1e-300)).max()))
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (3, 130, 40), (16, 4096, 256), (17, 129, 257), (127, 256, 384), (128, 512, 512), (129, 300, 700),
+         (256, 384, 512), (300, 1000, 264), (257, 4100, 1024), (1000, 640, 1040), (2100, 1030, 2050), (64, 16, 14336)]
+
+
+@gpu
+@pytest.mark.parametrize("form", ["", "pair", "single", "single3", "single8"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("T,N,M", SIZES)
+def test_product(cuda_device, monkeypatch, T, N, M, transpose, form):
+    if form:
+        monkeypatch.setenv("FORGE_LINEAR_KERNEL", form)
+    A, sA, W, sW = operands(T, N, M, transpose, seed=T)
+    want, mag = products(A, sA, W, sW, transpose)
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((want.numel() + 64,), 5.0, dtype=dtype, device="cuda")
+        Y = buf[: want.numel()].view(want.shape)
+        fg.forge_linear_e4m3(A, sA, W, sW, Y, transpose=transpose)
+        check(Y, want, mag, M if transpose else N)
+        assert (buf[want.numel():] == 5.0).all()
+        again = torch.empty_like(Y)
+        fg.forge_linear_e4m3(A, sA, W, sW, again, transpose=transpose)
+        assert torch.equal(again, Y)
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+
+
+@gpu
+@pytest.mark.parametrize("transpose", [False, True])
+def test_every_block_takes_its_own_scales(cuda_device, transpose):
+    """Scales 2^-20 to 2^20 apart, and zeros and NaN among the codes."""
+    T, N, M = 140, 400, 520
+    A, sA, W, sW = operands(T, N, M, transpose)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for s in (sA, sW):
+        s.copy_(2.0 ** torch.randint(-20, 20, s.shape, generator=g, device="cuda"))
+    want, mag = products(A, sA, W, sW, transpose)
+    Y = torch.empty(want.shape, device="cuda")
+    fg.forge_linear_e4m3(A, sA, W, sW, Y, transpose=transpose)
+    check(Y, want, mag, M if transpose else N)
+    A.view(torch.uint8)[7, 130] = 0x7F
+    fg.forge_linear_e4m3(A, sA, W, sW, Y, transpose=transpose)
+    nan = torch.isnan(Y)
+    assert nan[7].all() and int(nan.sum()) == Y.shape[1]
+
+
+def groups(T, E, seed, slack=3):
+    g = torch.Generator().manual_seed(seed)
+    e = torch.randint(0, E, (max(0, T - 2 * slack),), generator=g)
+    e[torch.rand(e.numel(), generator=g) < 0.4] = 0
+    counts = torch.bincount(e, minlength=E)
+    if E > 2:
+        counts[1] = 0
+    return (torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)]) + min(slack, T)).clamp(max=T).int()
+
+
+@gpu
+@pytest.mark.parametrize("form", ["", "pair", "single", "single3"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("T,N,M,E", [(1, 64, 48, 3), (40, 200, 136, 1), (300, 130, 260, 5), (1500, 384, 260, 4), (900, 520, 512, 40),
+                                     (700, 33, 65, 200), (1200, 128, 128, 1024)])
+def test_product_by_experts(cuda_device, monkeypatch, T, N, M, E, transpose, form):
+    if form:
+        monkeypatch.setenv("FORGE_LINEAR_KERNEL", form)
+    A, sA, W, sW = operands(T, N, M, transpose, E, seed=E)
+    offsets = groups(T, E, seed=T)
+    K, O = (M, N) if transpose else (N, M)
+    for dtype in (torch.float32, torch.bfloat16):
+        Y = torch.full((T, O), 7.0, dtype=dtype, device="cuda")
+        fg.forge_grouped_linear_e4m3(A, sA, W, sW, offsets.cuda(), Y, transpose=transpose)
+        lo, hi = int(offsets[0]), int(offsets[-1])
+        assert (Y[:lo] == 7.0).all() and (Y[hi:] == 7.0).all()
+        for e in range(E):
+            a, b = int(offsets[e]), int(offsets[e + 1])
+            if b > a:
+                want, mag = products(A[a:b], sA[a:b], W[e], sW[e], transpose)
+                check(Y[a:b], want, mag, K)
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+
+
+@gpu
+def test_nothing_leaks_between_experts(cuda_device):
+    """NaN codes in the rows of one expert and in the weight of another: neither
+    reaches a third, with ends inside tiles and blocks."""
+    E, T, N, M = 3, 330, 200, 144
+    A, sA, W, sW = operands(T, N, M, False, E)
+    offsets = torch.tensor([0, 100, 230, 330], dtype=torch.int32, device="cuda")
+    Y = torch.empty(T, M, device="cuda")
+    fg.forge_grouped_linear_e4m3(A, sA, W, sW, offsets, Y)
+    A.view(torch.uint8)[100:230] = 0x7F
+    W.view(torch.uint8)[2] = 0x7F
+    Z = torch.empty(T, M, device="cuda")
+    fg.forge_grouped_linear_e4m3(A, sA, W, sW, offsets, Z)
+    assert torch.equal(Z[:100], Y[:100]) and torch.isnan(Z[100:]).all()
+
+
+@gpu
+def test_bad_offsets_write_nothing(cuda_device):
+    A, sA, W, sW = operands(50, 64, 64, False, 3)
+    assert fg.forge_get_device_status() == fg.FORGE_OK
+    for bad in ([0, 20, 10, 50], [0, 20, 30, 51], [-1, 20, 30, 50]):
+        Y = torch.full((50, 64), 7.0, device="cuda")
+        fg.forge_grouped_linear_e4m3(A, sA, W, sW, torch.tensor(bad, dtype=torch.int32, device="cuda"), Y)
+        assert fg.forge_get_device_status() == fg.FORGE_ERR_INVALID_ARG
+        assert (Y == 7.0).all()
+    none = torch.zeros(4, dtype=torch.int32, device="cuda")
+    fg.forge_grouped_linear_e4m3(A, sA, W, sW, none, Y)
+    assert (Y == 7.0).all() and fg.forge_get_device_status() == fg.FORGE_OK
+    empty = torch.empty(0, 64, device="cuda")
+    fg.forge_grouped_linear_e4m3(A[:0], sA[:0], W, sW, none, empty)
+
+
+@gpu
+@pytest.mark.parametrize("offset", [1, 4, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_misaligned_operands(cuda_device, offset, dtype):
+    T, N, M = 200, 256, 272
+    A, sA, W, sW = operands(T, N, M, False)
+    want = torch.empty(T, M, dtype=dtype, device="cuda")
+    fg.forge_linear_e4m3(A, sA, W, sW, want)
+
+    def moved(t):
+        raw = t.reshape(-1).view(torch.uint8)
+        buf = torch.zeros(raw.numel() + offset, dtype=torch.uint8, device="cuda")
+        buf[offset:] = raw
+        return buf[offset:].view(t.shape)
+    Y = torch.empty(T * M + 1, dtype=dtype, device="cuda")[1:].view(T, M)
+    fg.forge_linear_e4m3(moved(A), sA, moved(W), sW, Y)
+    assert torch.equal(Y, want)
+
+
+@gpu
+@pytest.mark.parametrize("T,N,M,transpose", [(20, 1024, 600, False), (900, 300, 1100, True)])
+def test_streams_and_graphs(cuda_device, T, N, M, transpose):
+    A, sA, W, sW = operands(T, N, M, transpose)
+    want = torch.empty(T, N if transpose else M, device="cuda")
+    fg.forge_linear_e4m3(A, sA, W, sW, want, transpose=transpose)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = torch.empty_like(want)
+    fg.forge_linear_e4m3(A, sA, W, sW, got, transpose=transpose, stream=side)
+    side.synchronize()
+    graphs, held = [], []
+    for _ in range(2):
+        y = torch.zeros_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fg.forge_linear_e4m3(A, sA, W, sW, y, transpose=transpose)
+        graphs.append(g)
+        held.append(y)
+    for _ in range(3):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for y in (got, *held):
+        assert torch.equal(y, want)
+
+
+@gpu
+def test_rows_past_32_bits(cuda_device):
+    """More than 2^32 codes of A and outputs of Y: the last rows' results."""
+    T, N, M = 70000, 64, 65536
+    A, sA, W, sW = operands(T, N, M, False)
+    Y = torch.empty(T, M, dtype=torch.bfloat16, device="cuda")
+    fg.forge_linear_e4m3(A, sA, W, sW, Y)
+    for rows in (slice(0, 40), slice(T - 40, T)):
+        want, mag = products(A[rows], sA[rows], W, sW, False)
+        check(Y[rows], want, mag, N)
+
+
+def test_refusals_before_any_launch():
+    L = fg.lib()
+    F = fg.FORGE_F32
+
+    def q(x=FAKE, t=F, ld=64, E=1, R=4, C=64, br=1, codes=FAKE, scales=FAKE):
+        return L.forge_quantize_e4m3_blocks(x, t, ld, E, R, C, br, codes, scales, None)
+
+    def m(A=FAKE, sA=FAKE, W=FAKE, sW=FAKE, Y=FAKE, t=F, T=4, N=64, M=64):
+        return L.forge_linear_e4m3(A, sA, W, sW, Y, t, T, N, M, 0, None)
+
+    def g(A=FAKE, sA=FAKE, W=FAKE, sW=FAKE, offs=FAKE, E=3, Y=FAKE, t=F, T=4, N=64, M=64):
+        return L.forge_grouped_linear_e4m3(A, sA, W, sW, offs, E, Y, t, T, N, M, 1, None)
+    bad = fg.FORGE_ERR_INVALID_ARG
+    for kw in (dict(x=None), dict(codes=None), dict(scales=None), dict(R=-1), dict(E=-1), dict(C=0), dict(ld=63), dict(br=2),
+               dict(br=0), dict(br=64)):
+        assert q(**kw) == bad, kw
+    for kw in (dict(A=None), dict(sA=None), dict(W=None), dict(sW=None), dict(Y=None), dict(T=-1), dict(N=0), dict(M=0),
+               dict(T=1 << 31), dict(N=1 << 31), dict(M=1 << 31)):
+        assert m(**kw) == g(**kw) == bad, kw
+    assert g(offs=None) == g(E=0) == g(E=1025) == bad
+    for t in (fg.FORGE_E4M3, fg.FORGE_I32, 9):
+        assert q(t=t) == m(t=t) == g(t=t) == fg.FORGE_ERR_UNSUPPORTED_DTYPE
+    odd = ctypes.c_void_p(0x10002)
+    for n in ("sA", "sW", "Y"):
+        assert m(**{n: odd}) == g(**{n: odd}) == fg.FORGE_ERR_MISALIGNED
+    assert q(x=odd) == q(scales=odd) == g(offs=odd) == fg.FORGE_ERR_MISALIGNED
+    assert m(Y=ctypes.c_void_p(0x10001), t=fg.FORGE_BF16) == fg.FORGE_ERR_MISALIGNED
+
+
+@gpu
+def test_binding_refuses_what_does_not_fit(cuda_device):
+    A, sA, W, sW = operands(8, 64, 48, False)
+    Y = torch.empty(8, 48, device="cuda")
+    for args in ((A, sA, W, sW, Y[:, :47]), (A, sA[:7], W, sW, Y), (A, sA, W, sW[:, :0], Y), (A[:, :63], sA, W, sW, Y)):
+        with pytest.raises(ValueError):
+            fg.forge_linear_e4m3(*args)
+    with pytest.raises(TypeError):
+        fg.forge_linear_e4m3(A.float(), sA, W, sW, Y)
+    with pytest.raises(ValueError):
+        fg.forge_linear_e4m3(A, sA, W, sW, Y, transpose=True)
+    with pytest.raises(ValueError):
+        fg.forge_grouped_linear_e4m3(A, sA, W, sW, torch.zeros(2, dtype=torch.int32, device="cuda"), Y)
+    with pytest.raises(ValueError):
+        fg.forge_quantize_e4m3_blocks(Y, A, sA)
+    with pytest.raises(ValueError):
+        fg.forge_quantize_e4m3_blocks(Y, torch.empty(8, 48, dtype=F8, device="cuda"), sA, block_rows=64)

@@ -43,6 +43,8 @@ EXPORTS = ("forge_wgrad_adamw", "forge_wgrad_adamw_noalloc", "forge_wgrad_adamw_
            "forge_grouped_wgrad_adamw", "forge_owner_adamw", "forge_owner_sgdm",
            "forge_token_logprob", "forge_token_logprob_grad", "forge_embedding",
            "forge_embedding_grad", "forge_embedding_adamw", "forge_grad_norm", "forge_clip_grads",
+           "forge_layer_norm", "forge_layer_norm_grad", "forge_moe_route", "forge_moe_route_grad",
+           "forge_quantize_e4m3_blocks", "forge_linear_e4m3", "forge_grouped_linear_e4m3",
            "forge_status_string", "forge_get_device_status",
            "forge_selftest_wait_timeout", "forge_version")
 
@@ -88,7 +90,18 @@ def lib() -> ctypes.CDLL:
                                         I64, P]
     L.forge_grad_norm.argtypes = [P, P, I32, I, P, P]
     L.forge_clip_grads.argtypes = [P, P, I32, I, P, F, P, I, P]
-    for f in ("forge_token_logprob", "forge_token_logprob_grad", "forge_embedding",
+    L.forge_layer_norm.argtypes = [P, I, I64, P, P, I64, I64, F, P, I, I64, P, P, P]
+    L.forge_layer_norm_grad.argtypes = [P, I, I64, P, I, I64, P, P, P, I64, I64, P, I, I64, P, P,
+                                        I32, P]
+    L.forge_moe_route.argtypes = [P, I, I64, I32, I64, I32, I32, P, P, P, P, P, P, P, P, P]
+    L.forge_moe_route_grad.argtypes = [P, I, I64, I32, I64, I32, I32, P, P, P, P, P, P, I, I64, P]
+    L.forge_quantize_e4m3_blocks.argtypes = [P, I, I64, I64, I64, I64, I32, P, P, P]
+    L.forge_linear_e4m3.argtypes = [P, P, P, P, P, I, I64, I64, I64, I32, P]
+    L.forge_grouped_linear_e4m3.argtypes = [P, P, P, P, P, I32, P, I, I64, I64, I64, I32, P]
+    for f in ("forge_layer_norm", "forge_layer_norm_grad", "forge_moe_route",
+              "forge_moe_route_grad", "forge_quantize_e4m3_blocks", "forge_linear_e4m3",
+              "forge_grouped_linear_e4m3",
+              "forge_token_logprob", "forge_token_logprob_grad", "forge_embedding",
               "forge_embedding_grad", "forge_embedding_adamw", "forge_grad_norm",
               "forge_clip_grads",
               "forge_wgrad_adamw", "forge_wgrad_adamw_noalloc", "forge_wgrad_adamw_multi",
@@ -513,6 +526,160 @@ def forge_clip_grads(grads, norm, out=None, *, max_norm, stream=None):
     s = lib().forge_clip_grads(_address(ptrs), _address(sizes), len(grads), code,
                                _vector(norm, 1, "norm"), max_norm, _address(optrs), ocode, _stream(stream, norm))
     _check(s, "forge_clip_grads")
+
+
+def forge_layer_norm(x, weight, bias, y, *, mean=None, rstd=None, eps=1e-5, stream=None):
+    """y [R, D] = (x - mean) * rstd * weight + bias over the rows of x [R, D] (bf16
+    or fp32 each, rows of any stride; y may be x itself); weight and bias (or
+    None) fp32 [D].  mean and rstd [R] (fp32) are kept where given."""
+    xp, ldx, R, D = _rows(x, "x")
+    yp, ldy, *out = _rows(y, "y")
+    if out != [R, D]:
+        raise ValueError(f"y must be [R={R}, D={D}]")
+    s = lib().forge_layer_norm(xp, _float_code(x), ldx, _vector(weight, D, "weight"),
+                               _vector(bias, D, "bias"), R, D, eps, yp, _float_code(y), ldy,
+                               _vector(mean, R, "mean"), _vector(rstd, R, "rstd"),
+                               _stream(stream, x))
+    _check(s, "forge_layer_norm")
+
+
+def forge_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias=None, *, accumulate=False,
+                          stream=None):
+    """dx [R, D], dweight and dbias (or None) [D] (fp32, written or added to) of
+    forge_layer_norm's output gradient dy [R, D], from its x, mean and rstd; dx
+    may be dy or x itself."""
+    gp, ldg, R, D = _rows(dy, "dy")
+    xp, ldx, *in_ = _rows(x, "x")
+    op, ldo, *out = _rows(dx, "dx")
+    if in_ != [R, D] or out != [R, D]:
+        raise ValueError(f"x and dx must be [R={R}, D={D}]")
+    s = lib().forge_layer_norm_grad(gp, _float_code(dy), ldg, xp, _float_code(x), ldx,
+                                    _vector(weight, D, "weight"), _vector(mean, R, "mean"),
+                                    _vector(rstd, R, "rstd"), R, D, op, _float_code(dx), ldo,
+                                    _vector(dweight, D, "dweight"), _vector(dbias, D, "dbias"),
+                                    int(bool(accumulate)), _stream(stream, dy))
+    _check(s, "forge_layer_norm_grad")
+
+
+def _ints(t, n, what):
+    """Pointer of an int32 tensor of n elements, or None."""
+    if t is None:
+        return None
+    if t.numel() != n or _id_code(t) != FORGE_I32:
+        raise ValueError(f"{what} must be int32 with {n} elements")
+    return _ptr(t)
+
+
+def forge_moe_route(logits, experts, weights, counts, offsets, *, slots=None, rows=None, live=None,
+                    loss=None, normalize=True, stream=None):
+    """The k experts of each token of logits [T, E] (bf16 or fp32, rows of any
+    stride): experts (int32) and weights (fp32) [T, k], counts [E] and offsets
+    [E + 1] (int32); where given the choices' packed rows slots [T, k], each
+    packed row's token rows [T * k], the number of tokens that count live [1]
+    (int32) and the balance loss [1] (fp32)."""
+    lp, ld, T, E = _rows(logits, "logits")
+    k = experts.shape[-1]
+    if tuple(experts.shape) != (T, k) or tuple(weights.shape) != (T, k):
+        raise ValueError(f"experts and weights must be [T={T}, k]")
+    s = lib().forge_moe_route(lp, _float_code(logits), T, E, ld, k, int(bool(normalize)),
+                              _ints(experts, T * k, "experts"), _vector(weights, T * k, "weights"),
+                              _ints(counts, E, "counts"), _ints(offsets, E + 1, "offsets"),
+                              _ints(slots, T * k, "slots"), _ints(rows, T * k, "rows"),
+                              _ints(live, 1, "live"), _vector(loss, 1, "loss"),
+                              _stream(stream, logits))
+    _check(s, "forge_moe_route")
+
+
+def forge_moe_route_grad(logits, experts, counts, live, dlogits, *, grad_weights=None,
+                         grad_loss=None, normalize=True, stream=None):
+    """dlogits [T, E] (bf16 or fp32, rows of any stride; may be logits itself) of
+    sum(grad_weights * weights) + grad_loss * loss, from what forge_moe_route
+    gave."""
+    lp, ld, T, E = _rows(logits, "logits")
+    dp, ldo, *out = _rows(dlogits, "dlogits")
+    k = experts.shape[-1]
+    if out != [T, E] or tuple(experts.shape) != (T, k):
+        raise ValueError(f"dlogits must be [T={T}, E={E}] and experts [T, k]")
+    s = lib().forge_moe_route_grad(lp, _float_code(logits), T, E, ld, k, int(bool(normalize)),
+                                   _ints(experts, T * k, "experts"), _ints(counts, E, "counts"),
+                                   _ints(live, 1, "live"),
+                                   _vector(grad_weights, T * k, "grad_weights"),
+                                   _vector(grad_loss, 1, "grad_loss"), dp, _float_code(dlogits),
+                                   ldo, _stream(stream, logits))
+    _check(s, "forge_moe_route_grad")
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _byte_codes(t, what):
+    """Pointer of a contiguous tensor of e4m3 codes (float8_e4m3fn, or uint8)."""
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{what} must be float8_e4m3fn or uint8, got {t.dtype}")
+    return _ptr(t)
+
+
+def forge_quantize_e4m3_blocks(x, codes, scales, *, block_rows=1, stream=None):
+    """codes (float8_e4m3fn or uint8, x's shape) and scales (fp32) of x [R, C] or
+    [E, R, C] (fp32 or bf16; rows of any stride in the 2-D form), a scale for each
+    128 entries of a row (block_rows=1) or each square of 128 x 128 (128): [...,
+    ceil(R / block_rows), ceil(C / 128)]."""
+    if x.dim() == 3:
+        E, R, C = x.shape
+        xp, ldx = _ptr(x), C
+    else:
+        xp, ldx, R, C = _rows(x, "x")
+        E = 1
+    if tuple(codes.shape) != tuple(x.shape):
+        raise ValueError("codes must have x's shape")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    s = lib().forge_quantize_e4m3_blocks(xp, _float_code(x), ldx, E, R, C, block_rows,
+                                         _byte_codes(codes, "codes"),
+                                         _vector(scales, E * -(-R // block_rows) * _blocks(C),
+                                                 "scales"), _stream(stream, x))
+    _check(s, "forge_quantize_e4m3_blocks")
+
+
+def _linear_sizes(A, sA, W, sW, Y, transpose):
+    """Pointers of the operands and (T, N, M), for W [N, M] or [E, N, M]."""
+    *E, N, M = W.shape
+    K, O = (M, N) if transpose else (N, M)
+    T = A.shape[0]
+    if tuple(A.shape) != (T, K) or tuple(Y.shape) != (T, O):
+        raise ValueError(f"A [T, {K}] and Y [T, {O}] expected, got {tuple(A.shape)}, {tuple(Y.shape)}")
+    blocks = _blocks(N) * _blocks(M) * (E[0] if E else 1)
+    return (_byte_codes(A, "A"), _vector(sA, T * _blocks(K), "sA"), _byte_codes(W, "W"),
+            _vector(sW, blocks, "sW")), (T, N, M)
+
+
+def forge_linear_e4m3(A, sA, W, sW, Y, *, transpose=False, stream=None):
+    """Y [T, M] (bf16 or fp32) = A [T, N] times W [N, M], or with transpose Y [T, N]
+    = A [T, M] times W transposed, of e4m3 codes: sA holds a scale for each 128
+    entries of A's rows, sW for each 128 x 128 square of W (see
+    forge_quantize_e4m3_blocks)."""
+    if W.dim() != 2:
+        raise ValueError("W must be [N, M]")
+    ptrs, sizes = _linear_sizes(A, sA, W, sW, Y, transpose)
+    s = lib().forge_linear_e4m3(*ptrs, _ptr(Y), _float_code(Y), *sizes, int(bool(transpose)),
+                                _stream(stream, Y))
+    _check(s, "forge_linear_e4m3")
+
+
+def forge_grouped_linear_e4m3(A, sA, W, sW, offsets, Y, *, transpose=False, stream=None):
+    """forge_linear_e4m3 by experts: W [E, N, M], sW [E, ...], and expert e's rows of A
+    and Y are offsets[e] to offsets[e + 1] (int32 [E + 1] on the device); rows
+    of no expert stay as they are in Y."""
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, M]")
+    ptrs, sizes = _linear_sizes(A, sA, W, sW, Y, transpose)
+    E = W.shape[0]
+    s = lib().forge_grouped_linear_e4m3(*ptrs, _ints(offsets, E + 1, "offsets"), E, _ptr(Y),
+                                        _float_code(Y), *sizes, int(bool(transpose)),
+                                        _stream(stream, Y))
+    _check(s, "forge_grouped_linear_e4m3")
 
 
 def forge_status_string(status: int) -> str:

@@ -24,9 +24,10 @@ LIB = os.path.join(PKG, "libforge.so")
 
 SOURCES = ["forge_api.cu", "kernels_bf16.cu", "kernels_e4m3.cu", "kernels_pair_bf16.cu",
            "kernels_pair_e4m3.cu", "forge_static_stage.cu", "forge_quant.cu", "forge_dgrad.cu",
-           "forge_owner.cu", "forge_logprob.cu", "forge_embedding.cu", "forge_clip.cu"]
+           "forge_owner.cu", "forge_logprob.cu", "forge_embedding.cu", "forge_clip.cu",
+           "forge_layer_norm.cu", "forge_route.cu", "forge_block_quant.cu", "forge_linear.cu"]
 HEADERS = ["forge_ptx.cuh", "forge_kernel.cuh", "forge_launch.cuh", "forge_static_stage.h",
-           "forge_device.h"]
+           "forge_device.h", "forge_rows.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -817,6 +817,24 @@ cudaError_t forge::encode_bf16_kmajor(CUtensorMap* map, const void* base, int64_
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t forge::encode_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                                int64_t depth, int64_t ld_bytes, uint32_t box_rows)
+{
+    if (!ensure_encode()) return cudaErrorNotSupported;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_bytes),
+                             static_cast<cuuint64_t>(ld_bytes * rows)};
+    cuuint32_t box[3] = {128, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r =
+        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, depth > 0 ? 3 : 2, const_cast<void*>(base),
+                 dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t forge::stage_padded_rows(const void* src, void* dst, int64_t rows, int64_t row_bytes,
                                      int64_t dst_row_bytes, cudaStream_t stream)
 {

@@ -34,6 +34,13 @@ int64_t wait_timeout();
 cudaError_t encode_bf16_kmajor(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
                                uint32_t box_rows, int64_t ld_bytes);
 
+// Bytes [depth, rows, inner], rows ld_bytes apart (a multiple of 16) from a 16-byte
+// aligned base on, read in boxes of 128 bytes x box_rows rows with 128-byte swizzle:
+// an operand of 8-bit codes, K-major or MN-major.  Depth 0 makes a 2-D map.  What
+// lies outside the tensor reads as zeros.
+cudaError_t encode_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                         int64_t depth, int64_t ld_bytes, uint32_t box_rows);
+
 // Copies [rows, row_bytes] from src (rows packed, base aligned to at least the
 // element size) into dst (256-byte aligned) with rows dst_row_bytes apart (a
 // multiple of 16 and >= row_bytes), on `stream`: the staging copy that makes
@@ -48,6 +55,26 @@ cudaError_t stage_padded_rows(const void* src, void* dst, int64_t rows, int64_t 
 // once.  scratch_free returns the block in stream order.
 cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 cudaError_t scratch_free(void* ptr, cudaStream_t stream);
+
+// Whether rows of `a` bytes, `pa` apart from x on, and rows of `b` bytes, `pb` apart
+// from y on, share a byte (R of each; a <= pa, b <= pb).
+inline bool rows_overlap(uintptr_t x, int64_t a, int64_t pa, uintptr_t y, int64_t b, int64_t pb, int64_t R)
+{
+    using Wide = __int128;  // no product of R and a pitch overflows
+    if (y < x) return rows_overlap(y, b, pb, x, a, pa, R);
+    const Wide d = y - x;
+    if (d >= Wide{R - 1} * pa + a) return false;
+    if (pa == pb) {  // each row of y starts r behind a row of x, the first behind row q
+        const Wide q = d / pa, r = d % pa;
+        return (q < R && r < a) || (q + 1 < R && r + b > pa);
+    }
+    for (int64_t j = 0; j < R; ++j) {
+        const Wide at = d + Wide{j} * pb;                  // of row j of y
+        const Wide i = at < a ? 0 : (at - a) / pa + 1;  // the first row of x that ends behind it
+        if (i < R && i * pa < at + b) return true;
+    }
+    return false;
+}
 
 struct Params;
 

@@ -1,0 +1,578 @@
+// forge_layer_norm.cu -- layer norm and its gradient, with the reduction of the
+// weight's and the bias's gradients over the rows.
+//
+// A row x [D], weight w and bias b give
+//   mu = mean x,  rstd = 1 / sqrt(mean (x - mu)^2 + eps),  xh = (x - mu) rstd,
+//   y = xh w + b,
+// and a gradient dy of y, with g = dy w,
+//   dx = rstd (g - mean g - xh mean(g xh)),  dw = sum_r dy xh,  db = sum_r dy.
+//
+// Both are bound by memory: a row is read once into registers, by one warp
+// or by a block of W warps, and everything is computed from there (mu first and
+// the squares of x - mu after it, so that no digits are lost to a mean that is
+// large against the deviations).  Each thread owns the same columns of every
+// row its block takes, so dw and db are sums in its registers; a block writes
+// them once, and a second kernel adds the blocks' in a fixed order: bitwise the
+// same from run to run.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "forge.h"
+#include "forge_device.h"
+#include "forge_rows.cuh"
+
+namespace forge {
+namespace norm {
+
+constexpr int kRowWarps = 8;      // warps of a block whose warps take a row each
+constexpr int kLongThreads = 1024;  // of a block on a row too wide for registers
+constexpr int64_t kMaxForward = 16384, kMaxBackward = 8192;  // widths that registers hold
+
+struct Forward {
+    int64_t R, D, ldx, ldy;
+    const float *weight, *bias;
+    void* y;
+    bool y_f32;
+    float *mean, *rstd;
+    float eps;
+};
+
+struct Backward {
+    int64_t R, D, ldg, ldx, ldo;
+    const float *weight, *mean, *rstd;
+    void* dx;
+    bool dx_f32;
+    float* part;  // [blocks][2][D]
+};
+
+// E entries a thread in vectors of V, W warps a row.
+template <typename X, int V, int E, int W>
+__global__ void __launch_bounds__(32 * (W == 1 ? kRowWarps : W))
+    forge_layer_norm_kernel(const X* __restrict__ x, const Forward p)
+{
+    constexpr int NV = E / V;
+    __shared__ float sh[2][W];
+    const int rows = W == 1 ? kRowWarps : 1;
+    const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + (W == 1 ? threadIdx.x >> 5 : 0);
+    const float inv = 1.0f / static_cast<float>(p.D);
+    for (int64_t r = first; r < p.R; r += static_cast<int64_t>(gridDim.x) * rows) {
+        const X* row = x + r * p.ldx;
+        Packed<X, V> raw[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * W * 32 + t) * V;
+            raw[i] = c < p.D ? load_packed<X, V>(row + c) : zero_packed<X, V>();
+        }
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += entry(raw[i], j);
+        block_sums<W>(s, sh[0]);
+        const float mu = s[0] * inv;
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((i * W * 32 + t) * V < p.D) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = entry(raw[i], j) - mu;
+                    q[0] = fmaf(d, d, q[0]);
+                }
+            }
+        }
+        block_sums<W>(q, sh[1]);
+        const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, p.eps));
+        if (t == 0) {
+            if (p.mean) p.mean[r] = mu;
+            if (p.rstd) p.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * W * 32 + t) * V;
+            if (c < p.D) {
+                const Packed<float, V> w = load_packed<float, V>(p.weight + c);
+                const Packed<float, V> b =
+                    p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
+                float v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = fmaf((entry(raw[i], j) - mu) * rstd, entry(w, j), entry(b, j));
+                store_as(p.y, p.y_f32, r * p.ldy + c, v);
+            }
+        }
+    }
+}
+
+// Rows wider than the registers hold: three passes over a row, the second and
+// third from L2.
+template <typename X, int V>
+__global__ void __launch_bounds__(kLongThreads)
+    forge_layer_norm_long_kernel(const X* __restrict__ x, const Forward p)
+{
+    __shared__ float sh[2][kLongThreads / 32];
+    const float inv = 1.0f / static_cast<float>(p.D);
+    const int64_t step = static_cast<int64_t>(kLongThreads) * V;
+    for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x) {
+        const X* row = x + r * p.ldx;
+        float s[1] = {0.0f};
+        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
+            const Packed<X, V> raw = load_packed<X, V>(row + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += entry(raw, j);
+        }
+        block_sums<kLongThreads / 32>(s, sh[0]);
+        const float mu = s[0] * inv;
+        float q[1] = {0.0f};
+        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
+            const Packed<X, V> raw = load_packed<X, V>(row + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = entry(raw, j) - mu;
+                q[0] = fmaf(d, d, q[0]);
+            }
+        }
+        block_sums<kLongThreads / 32>(q, sh[1]);
+        const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, p.eps));
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[r] = mu;
+            if (p.rstd) p.rstd[r] = rstd;
+        }
+        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
+            const Packed<X, V> raw = load_packed<X, V>(row + c);
+            const Packed<float, V> w = load_packed<float, V>(p.weight + c);
+            const Packed<float, V> b =
+                p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = fmaf((entry(raw, j) - mu) * rstd, entry(w, j), entry(b, j));
+            store_as(p.y, p.y_f32, r * p.ldy + c, v);
+        }
+    }
+}
+
+template <typename G, typename X, int V, int E, int W>
+__global__ void __launch_bounds__(32 * (W == 1 ? kRowWarps : W))
+    forge_layer_norm_grad_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+                                 const Backward p)
+{
+    constexpr int NV = E / V;
+    __shared__ float sh[2][2 * W];
+    const int rows = W == 1 ? kRowWarps : 1;
+    const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + (W == 1 ? threadIdx.x >> 5 : 0);
+    const float inv = 1.0f / static_cast<float>(p.D);
+    float w[E], dw[E], db[E];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * W * 32 + t) * V;
+        const Packed<float, V> raw =
+            c < p.D ? load_packed<float, V>(p.weight + c) : zero_packed<float, V>();
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[i * V + j] = entry(raw, j);
+            dw[i * V + j] = db[i * V + j] = 0.0f;
+        }
+    }
+    int turn = 0;
+    for (int64_t r = first; r < p.R; r += static_cast<int64_t>(gridDim.x) * rows, turn ^= 1) {
+        const G* grow = dy + r * p.ldg;
+        const X* xrow = x + r * p.ldx;
+        Packed<G, V> graw[NV];
+        Packed<X, V> xraw[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * W * 32 + t) * V;
+            graw[i] = c < p.D ? load_packed<G, V>(grow + c) : zero_packed<G, V>();
+            xraw[i] = c < p.D ? load_packed<X, V>(xrow + c) : zero_packed<X, V>();
+        }
+        const float mu = p.mean[r], rstd = p.rstd[r];
+        float s[2] = {0.0f, 0.0f};  // of g and of g xh (columns past D have dy = 0)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = entry(graw[i], j);
+                const float xh = (entry(xraw[i], j) - mu) * rstd;
+                const float g = d * w[i * V + j];
+                s[0] += g;
+                s[1] = fmaf(g, xh, s[1]);
+                dw[i * V + j] = fmaf(d, xh, dw[i * V + j]);
+                db[i * V + j] += d;
+            }
+        block_sums<W>(s, sh[turn]);
+        const float a = s[0] * inv, b = s[1] * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * W * 32 + t) * V;
+            if (c < p.D) {
+                float v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (entry(xraw[i], j) - mu) * rstd;
+                    v[j] = rstd * (fmaf(entry(graw[i], j), w[i * V + j], -a) - xh * b);
+                }
+                store_as(p.dx, p.dx_f32, r * p.ldo + c, v);
+            }
+        }
+    }
+    let_dependents_start();
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    if constexpr (W == 1) {
+        // the block's warps one after another
+        __shared__ float acc[2][E * 32];
+        for (int k = 0; k < kRowWarps; ++k) {
+            if (static_cast<int>(threadIdx.x >> 5) == k) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int c = (i * 32 + t) * V + j;
+                        acc[0][c] = (k ? acc[0][c] : 0.0f) + dw[i * V + j];
+                        acc[1][c] = (k ? acc[1][c] : 0.0f) + db[i * V + j];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < p.D; c += 32 * kRowWarps) {
+            part[c] = acc[0][c];
+            part[p.D + c] = acc[1][c];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * W * 32 + t) * V;
+            if (c < p.D) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    part[c + j] = dw[i * V + j];
+                    part[p.D + c + j] = db[i * V + j];
+                }
+            }
+        }
+    }
+}
+
+// dx of rows wider than the registers hold: two passes over a row.
+template <typename G, typename X, int V>
+__global__ void __launch_bounds__(kLongThreads)
+    forge_layer_norm_grad_long_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+                                      const Backward p)
+{
+    __shared__ float sh[2][2 * kLongThreads / 32];
+    const float inv = 1.0f / static_cast<float>(p.D);
+    const int64_t step = static_cast<int64_t>(kLongThreads) * V;
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x, turn ^= 1) {
+        const G* grow = dy + r * p.ldg;
+        const X* xrow = x + r * p.ldx;
+        const float mu = p.mean[r], rstd = p.rstd[r];
+        float s[2] = {0.0f, 0.0f};
+        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
+            const Packed<G, V> graw = load_packed<G, V>(grow + c);
+            const Packed<X, V> xraw = load_packed<X, V>(xrow + c);
+            const Packed<float, V> w = load_packed<float, V>(p.weight + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float g = entry(graw, j) * entry(w, j);
+                s[0] += g;
+                s[1] = fmaf(g, (entry(xraw, j) - mu) * rstd, s[1]);
+            }
+        }
+        block_sums<kLongThreads / 32>(s, sh[turn]);
+        const float a = s[0] * inv, b = s[1] * inv;
+        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
+            const Packed<G, V> graw = load_packed<G, V>(grow + c);
+            const Packed<X, V> xraw = load_packed<X, V>(xrow + c);
+            const Packed<float, V> w = load_packed<float, V>(p.weight + c);
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = rstd * (fmaf(entry(graw, j), entry(w, j), -a) -
+                               (entry(xraw, j) - mu) * rstd * b);
+            store_as(p.dx, p.dx_f32, r * p.ldo + c, v);
+        }
+    }
+}
+
+// dw and db of such rows, before dx (which may be written over dy): a block
+// takes 32 x kLongWarps columns of every gridDim.y-th group of rows.
+constexpr int kLongWarps = 4;
+template <typename G, typename X>
+__global__ void __launch_bounds__(32 * kLongWarps)
+    forge_layer_norm_columns_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+                                    const Backward p)
+{
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * (32 * kLongWarps) + threadIdx.x;
+    if (c >= p.D) return;
+    float dw = 0.0f, db = 0.0f;
+#pragma unroll 4
+    for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
+        const float d = entry(load_packed<G, 1>(dy + r * p.ldg + c), 0);
+        const float xh = (entry(load_packed<X, 1>(x + r * p.ldx + c), 0) - p.mean[r]) * p.rstd[r];
+        dw = fmaf(d, xh, dw);
+        db += d;
+    }
+    float* part = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.D;
+    part[c] = dw;
+    part[p.D + c] = db;
+}
+
+// The sum of the blocks' parts, 32 columns a block, its warps every eighth part.
+constexpr int kFoldWarps = 8;
+__global__ void __launch_bounds__(32 * kFoldWarps)
+    forge_layer_norm_fold_kernel(const float* part, int32_t parts, int64_t D, float* dweight,
+                                 float* dbias, int32_t accumulate)
+{
+    __shared__ float sh[kFoldWarps][33];
+    await_prerequisites();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // of [2][D]
+    float s = 0.0f;
+    if (c < 2 * D) {
+#pragma unroll 8
+        for (int k = warp; k < parts; k += kFoldWarps)
+            s += part[static_cast<int64_t>(k) * 2 * D + c];
+    }
+    sh[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < 2 * D) {
+#pragma unroll
+        for (int k = 1; k < kFoldWarps; ++k) s += sh[k][lane];
+        float* out = c < D ? dweight : dbias;
+        if (out) {
+            const int64_t at = c < D ? c : c - D;
+            out[at] = accumulate ? out[at] + s : s;
+        }
+    }
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t size_of(forge_dtype t) { return t == FORGE_BF16 ? 2 : 4; }
+bool is_float(forge_dtype t) { return t == FORGE_F32 || t == FORGE_BF16; }
+
+// Whether rows of `ld` elements of `es` bytes from `p` on can be taken in
+// vectors of V elements (of at most 16 bytes an instruction).
+bool rows_fit(const void* p, int64_t es, int64_t ld, int V)
+{
+    const int64_t bytes = V * es < 16 ? V * es : 16;
+    return aligned(p, bytes) && ld % V == 0;
+}
+
+int blocks_for(int64_t rows, int64_t rows_a_block, int64_t most)
+{
+    const int64_t want = (rows + rows_a_block - 1) / rows_a_block;
+    return static_cast<int>(want < most ? want : most);
+}
+
+template <typename X, int V>
+void forward(const X* x, const Forward& p, int sms, cudaStream_t s)
+{
+    const int64_t D = p.D;
+    auto go = [&](auto kernel, int W) {
+        const int rows = W == 1 ? kRowWarps : 1, threads = 32 * (W == 1 ? kRowWarps : W);
+        kernel<<<blocks_for(p.R, rows, static_cast<int64_t>(sms) * (2048 / threads)), threads, 0,
+                 s>>>(x, p);
+    };
+    if (D <= 256)
+        go(forge_layer_norm_kernel<X, V, 8, 1>, 1);
+    else if (D <= 512)
+        go(forge_layer_norm_kernel<X, V, 16, 1>, 1);
+    else if (D <= 1024)
+        go(forge_layer_norm_kernel<X, V, 16, 2>, 2);
+    else if (D <= 2048)
+        go(forge_layer_norm_kernel<X, V, 16, 4>, 4);
+    else if (D <= 4096)
+        go(forge_layer_norm_kernel<X, V, 16, 8>, 8);
+    else if (D <= 8192)
+        go(forge_layer_norm_kernel<X, V, 16, 16>, 16);
+    else if (D <= kMaxForward)
+        go(forge_layer_norm_kernel<X, V, 16, 32>, 32);
+    else
+        forge_layer_norm_long_kernel<X, V>
+            <<<blocks_for(p.R, 1, 2LL * sms), kLongThreads, 0, s>>>(x, p);
+}
+
+// The rows in registers; returns the number of parts of dw and db.
+template <typename G, typename X, int V>
+int backward(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s)
+{
+    const int64_t D = p.D;
+    auto go = [&](auto kernel, int W) {
+        const int rows = W == 1 ? kRowWarps : 1, threads = 32 * (W == 1 ? kRowWarps : W);
+        const int blocks = blocks_for(p.R, rows, static_cast<int64_t>(sms) * (512 / threads < 1 ? 1 : 512 / threads));
+        kernel<<<blocks, threads, 0, s>>>(dy, x, p);
+        return blocks;
+    };
+    if (D <= 256) return go(forge_layer_norm_grad_kernel<G, X, V, 8, 1>, 1);
+    if (D <= 512) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 1>, 1);
+    if (D <= 1024) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 2>, 2);
+    if (D <= 2048) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 4>, 4);
+    if (D <= 4096) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 8>, 8);
+    return go(forge_layer_norm_grad_kernel<G, X, V, 16, 16>, 16);
+}
+
+// Most parts that backward() or the column kernel writes.
+int64_t most_parts(int64_t R, int64_t D, int sms)
+{
+    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * 8;
+    return R < most ? R : most;
+}
+
+template <typename G, typename X>
+int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cudaStream_t s)
+{
+    if (p.D <= kMaxBackward)
+        return V == 8   ? backward<G, X, 8>(dy, x, p, sms, s)
+               : V == 4 ? backward<G, X, 4>(dy, x, p, sms, s)
+                        : backward<G, X, 1>(dy, x, p, sms, s);
+    const int64_t slabs = (p.D + 32 * kLongWarps - 1) / (32 * kLongWarps);
+    const int parts = static_cast<int>(most_parts(p.R, p.D, sms));
+    forge_layer_norm_columns_kernel<G, X>
+        <<<dim3(static_cast<unsigned>(slabs), parts), 32 * kLongWarps, 0, s>>>(dy, x, p);
+    const int blocks = blocks_for(p.R, 1, 2LL * sms);
+    if (V == 1)
+        forge_layer_norm_grad_long_kernel<G, X, 1><<<blocks, kLongThreads, 0, s>>>(dy, x, p);
+    else
+        forge_layer_norm_grad_long_kernel<G, X, 4><<<blocks, kLongThreads, 0, s>>>(dy, x, p);
+    return parts;
+}
+
+forge_status check_sizes(int64_t R, int64_t D)
+{
+    return R < 0 || D < 1 || R > INT32_MAX || D > (1 << 30) ? FORGE_ERR_INVALID_ARG : FORGE_OK;
+}
+
+// Whether `out` is `in` itself, row by row, or shares no memory with it.
+bool apart_or_same(const void* in, forge_dtype ti, int64_t ldi, const void* out, forge_dtype to,
+                   int64_t ldo, int64_t R, int64_t D)
+{
+    const int64_t ei = size_of(ti), eo = size_of(to);
+    if (in == out && ti == to && (ldi == ldo || R == 1)) return true;
+    return R == 0 || !rows_overlap(reinterpret_cast<uintptr_t>(in), D * ei, ldi * ei,
+                                   reinterpret_cast<uintptr_t>(out), D * eo, ldo * eo, R);
+}
+
+}  // namespace norm
+}  // namespace forge
+
+using namespace forge;
+
+extern "C" forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int64_t ldx,
+                                         const float* weight, const float* bias, int64_t R,
+                                         int64_t D, float eps, void* y, forge_dtype y_dtype,
+                                         int64_t ldy, float* mean, float* rstd,
+                                         forge_stream_t stream)
+{
+    using namespace norm;
+    if (!weight || (R > 0 && (!x || !y))) return FORGE_ERR_INVALID_ARG;
+    forge_status st = check_sizes(R, D);
+    if (st != FORGE_OK) return st;
+    if (ldx < D || ldy < D || !(eps > 0.0f) || !std::isfinite(eps)) return FORGE_ERR_INVALID_ARG;
+    if (!is_float(x_dtype) || !is_float(y_dtype)) return FORGE_ERR_UNSUPPORTED_DTYPE;
+    if (!aligned(x, size_of(x_dtype)) || !aligned(y, size_of(y_dtype)) || !aligned(weight, 4) ||
+        !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return FORGE_ERR_MISALIGNED;
+    if (!apart_or_same(x, x_dtype, ldx, y, y_dtype, ldy, R, D)) return FORGE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != FORGE_OK) return st;
+    if (R == 0) return FORGE_OK;
+    const void* ptrs[] = {x, weight, bias, y, mean, rstd};
+    if ((st = device_resident(ptrs, 6)) != FORGE_OK) return st;
+    const Forward p{R, D, ldx, ldy, weight, bias, y, y_dtype == FORGE_F32, mean, rstd, eps};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int V = x_dtype == FORGE_BF16 ? 8 : 4;
+    const bool fits = D % V == 0 && rows_fit(x, size_of(x_dtype), ldx, V) &&
+                      rows_fit(y, size_of(y_dtype), ldy, V) && aligned(weight, 16) &&
+                      aligned(bias, 16);
+    if (x_dtype == FORGE_F32) {
+        const float* f = static_cast<const float*>(x);
+        fits ? forward<float, 4>(f, p, sms, s) : forward<float, 1>(f, p, sms, s);
+    } else {
+        const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(x);
+        fits ? forward<__nv_bfloat16, 8>(h, p, sms, s) : forward<__nv_bfloat16, 1>(h, p, sms, s);
+    }
+    return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+}
+
+extern "C" forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dtype, int64_t lddy,
+                                              const void* x, forge_dtype x_dtype, int64_t ldx,
+                                              const float* weight, const float* mean,
+                                              const float* rstd, int64_t R, int64_t D, void* dx,
+                                              forge_dtype dx_dtype, int64_t lddx, float* dweight,
+                                              float* dbias, int32_t accumulate,
+                                              forge_stream_t stream)
+{
+    using namespace norm;
+    if (!weight || !dweight || (R > 0 && (!dy || !x || !mean || !rstd || !dx)))
+        return FORGE_ERR_INVALID_ARG;
+    forge_status st = check_sizes(R, D);
+    if (st != FORGE_OK) return st;
+    if (lddy < D || ldx < D || lddx < D) return FORGE_ERR_INVALID_ARG;
+    if (!is_float(dy_dtype) || !is_float(x_dtype) || !is_float(dx_dtype))
+        return FORGE_ERR_UNSUPPORTED_DTYPE;
+    if (!aligned(dy, size_of(dy_dtype)) || !aligned(x, size_of(x_dtype)) ||
+        !aligned(dx, size_of(dx_dtype)) || !aligned(weight, 4) || !aligned(mean, 4) ||
+        !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return FORGE_ERR_MISALIGNED;
+    if (!apart_or_same(dy, dy_dtype, lddy, dx, dx_dtype, lddx, R, D) ||
+        !apart_or_same(x, x_dtype, ldx, dx, dx_dtype, lddx, R, D))
+        return FORGE_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != FORGE_OK) return st;
+    const void* ptrs[] = {R > 0 ? dy : nullptr,   R > 0 ? x : nullptr,  weight,
+                          R > 0 ? mean : nullptr, R > 0 ? rstd : nullptr, R > 0 ? dx : nullptr,
+                          dweight,                dbias};
+    if ((st = device_resident(ptrs, 8)) != FORGE_OK) return st;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    void* scratch = nullptr;
+    if (R > 0 && scratch_alloc(&scratch, most_parts(R, D, sms) * 2 * D * sizeof(float), s) !=
+                     cudaSuccess) {
+        cudaGetLastError();
+        return FORGE_ERR_CUDA;
+    }
+    const Backward p{R,    D,  lddy, ldx, lddx, weight, mean,
+                     rstd, dx, dx_dtype == FORGE_F32, static_cast<float*>(scratch)};
+    const bool wide = dy_dtype == FORGE_BF16 && x_dtype == FORGE_BF16 && D <= kMaxBackward;
+    int V = wide ? 8 : 4;
+    if (D % V != 0 || !rows_fit(dy, size_of(dy_dtype), lddy, V) ||
+        !rows_fit(x, size_of(x_dtype), ldx, V) || !rows_fit(dx, size_of(dx_dtype), lddx, V) ||
+        !aligned(weight, 16))
+        V = 1;
+    int parts = 0;
+    if (R > 0) {
+        auto by_x = [&](auto* g) {
+            return x_dtype == FORGE_F32
+                       ? backward_any(g, static_cast<const float*>(x), p, V, sms, s)
+                       : backward_any(g, static_cast<const __nv_bfloat16*>(x), p, V, sms, s);
+        };
+        parts = dy_dtype == FORGE_F32 ? by_x(static_cast<const float*>(dy))
+                                      : by_x(static_cast<const __nv_bfloat16*>(dy));
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        cudaLaunchAttribute early[1];
+        early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>((2 * D + 31) / 32));
+        cfg.blockDim = dim3(32 * kFoldWarps);
+        cfg.stream = s;
+        cfg.attrs = early;
+        cfg.numAttrs = R > 0 && D <= kMaxBackward ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, forge_layer_norm_fold_kernel,
+                               static_cast<const float*>(p.part), parts, D, dweight, dbias,
+                               accumulate);
+    }
+    if (scratch) {
+        const cudaError_t fe = scratch_free(scratch, s);
+        if (e == cudaSuccess) e = fe;
+    }
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+}

@@ -1,0 +1,680 @@
+// forge_linear.cu -- products of e4m3 codes that carry a scale for each block
+// of 128: a linear layer's Y = A W, and its input gradient Y = A W^T, dense or
+// by experts.
+//
+// With A [T, K] (a scale for each 128 entries of a row) and W (a scale for each
+// 128 x 128 square),
+//   Y[t][o] = sum over blocks b of 128 of K:  sA[t][b] sW[b][o / 128] P_b[t][o],
+//   P_b[t][o] = sum over k in block b of A[t][k] W[k][o].
+// The tensor core sums a block's products P_b in fp32 in tensor memory, and the
+// epilogue warps add it, times its two scales, to the tile's sum in their
+// registers (fp32): every block has its own scale, so no two blocks meet
+// in one accumulator before they are scaled.  Two P_b alternate in tensor memory;
+// while one is read the tensor core fills the other.
+//
+// The contraction runs over A's contiguous index, so A is K-major.  W [N, M]
+// (d_in x d_out, row-major) is MN-major for Y = A W and K-major for A W^T: the
+// same codes and scales serve both, because a square's scale does not depend
+// on the direction.
+//
+// Two forms.  Many tokens: CTA pairs (tcgen05.mma.cta_group::2) on tiles of 256
+// tokens x 256 outputs, persistent.  Few tokens: one CTA a tile of 128 x 128 and
+// a share of K; the CTAs of a cluster hold a tile's shares and add them through
+// distributed shared memory, in rank order, so that a weight is read by all
+// SMs however few its tiles are.  By experts, a tile lies within one expert's
+// rows; rows of A behind the expert's end reach only lanes that are not stored.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+
+#include "forge.h"
+#include "forge_device.h"
+#include "forge_kernel.cuh"
+#include "forge_rows.cuh"
+
+namespace forge {
+namespace linear {
+
+constexpr int kBlock = 128;       // entries under one scale, and k of a stage
+constexpr int kThreads = 320;     // producer, MMA issuer, eight epilogue warps
+constexpr int kEpiWarp0 = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kStageA = 128 * kBlock;  // 128 token rows
+constexpr int kStageB = 128 * kBlock;  // 128 outputs
+constexpr int kStageBytes = kStageA + kStageB;
+constexpr int kMostSplit = 8;     // CTAs that share a tile's K
+constexpr int kBand = 8;          // token tiles of a band of the tile walk
+
+template <bool PAIR>
+struct Form {
+    static constexpr int stages = PAIR ? 6 : 3;
+    static constexpr int rows = PAIR ? 256 : 128;  // tokens of a tile
+    static constexpr int cols = PAIR ? 256 : 128;  // outputs of a tile
+    static constexpr int warp_cols = cols / 2;
+    static constexpr int tmem_cols = 2 * cols;
+    static constexpr int bar_at = stages * kStageBytes;
+    static constexpr int table_at = bar_at + 256;
+    static constexpr int bytes(int E) { return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024; }
+};
+constexpr int kPitch = 132;  // floats between the rows of a share in shared memory
+static_assert(128 * kPitch * 4 <= Form<false>::bar_at, "a share fits the ring");
+
+struct LParams {
+    int64_t T, K, O;       // tokens, contraction, outputs
+    const float *sA, *sW;
+    int64_t sw_k, sw_o, sw_e;  // strides of W's scales along K, outputs, experts
+    void* Y;
+    int32_t f32, vec;      // Y's type; rows of Y take 16-byte stores
+    int32_t E;             // experts, 0: dense
+    const int32_t* offsets;
+    int32_t tiles_o, nk;
+    Params w;              // timeout_ns and status for the bounded waits
+};
+
+struct Tile {
+    int32_t expert, t0, t_end, o0;
+};
+
+// Tile t: dense calls walk bands of kBand token tiles, tokens fastest, so that
+// the CTAs at work share both operands' blocks in L2; by experts, one expert's
+// tiles after another's, each walked the same way.
+template <bool PAIR, bool GROUPED>
+__device__ __forceinline__ Tile tile_of(int32_t t, const LParams& p, const int32_t* offs,
+                                        const int32_t* begin)
+{
+    using F = Form<PAIR>;
+    Tile r;
+    int32_t lo = 0, hi = static_cast<int32_t>(p.T);
+    r.expert = 0;
+    if constexpr (GROUPED) {
+        int a = 0, b = p.E;  // begin[a] <= t < begin[b]
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (begin[m] <= t)
+                a = m;
+            else
+                b = m;
+        }
+        r.expert = a;
+        t -= begin[a];
+        lo = offs[a];
+        hi = offs[a + 1];
+    }
+    const int32_t tiles_t = (hi - lo + F::rows - 1) / F::rows;
+    const int32_t band = t / (kBand * p.tiles_o), in = t - band * kBand * p.tiles_o;
+    const int32_t left = tiles_t - band * kBand, high = left < kBand ? left : kBand;
+    r.t0 = lo + (band * kBand + in % high) * F::rows;
+    r.t_end = hi;
+    r.o0 = in / high * F::cols;
+    return r;
+}
+
+// Offsets into shared memory, checked, and the first tile of each expert;
+// false (and the status word set) where the offsets are not an ascending list
+// within the T rows.  All threads of the CTA.
+template <bool PAIR>
+__device__ bool group_table(const LParams& p, int32_t* offs, int32_t* begin)
+{
+    int bad = 0;
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
+        const int32_t v = p.offsets[e], before = e > 0 ? p.offsets[e - 1] : 0;
+        offs[e] = v;
+        bad |= v < before || v > p.T;
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(p.w.status) = kDevInvalidArg;
+        return false;
+    }
+    if (threadIdx.x < 32) {
+        int32_t sum = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + threadIdx.x;
+            int32_t n = 0;
+            if (e < p.E)
+                n = (offs[e + 1] - offs[e] + Form<PAIR>::rows - 1) / Form<PAIR>::rows * p.tiles_o;
+            int32_t up = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
+                if (static_cast<int>(threadIdx.x) >= o) up += v;
+            }
+            if (e < p.E) begin[e] = sum + up - n;
+            sum += __shfl_sync(0xffffffffu, up, 31);
+        }
+        if (threadIdx.x == 0) begin[p.E] = sum;
+    }
+    __syncthreads();
+    return true;
+}
+
+// N outputs of one row, in registers, from column c on.
+template <int N>
+__device__ __forceinline__ void store_row(const LParams& p, int64_t row, int64_t c,
+                                          const float (&v)[N])
+{
+    const int64_t at = row * p.O + c;
+    if (p.vec && c + N <= p.O) {
+        store_as(p.Y, p.f32, at, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float one[1] = {v[j]};
+            if (c + j < p.O) store_as(p.Y, p.f32, at + j, one);
+        }
+    }
+}
+
+template <bool PAIR, bool W_MN, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
+    forge_linear_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K]
+                        const __grid_constant__ CUtensorMap tmW,  // W [E][N][M]
+                        const LParams p)
+{
+    using F = Form<PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::bar_at);
+    uint64_t* empty = full + F::stages;
+    uint64_t* tfull = empty + F::stages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int32_t* offs = reinterpret_cast<int32_t*>(smem + F::table_at);
+    int32_t* begin = offs + p.E + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t split = PAIR ? 1 : gridDim.y;  // CTAs that share a tile (a cluster along y)
+    const bool leader = !PAIR || rank == 0;       // of the pair: issues its MMAs
+    if constexpr (GROUPED) {
+        // every CTA of a cluster reads the same offsets and leaves alike
+        if (!group_table<PAIR>(p, offs, begin)) return;
+    }
+    int32_t total;
+    if constexpr (GROUPED) {
+        total = begin[p.E];
+    } else {
+        total = static_cast<int32_t>((p.T + F::rows - 1) / F::rows) * p.tiles_o;
+    }
+    const int32_t first = static_cast<int32_t>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+    const int32_t step = static_cast<int32_t>(PAIR ? gridDim.x >> 1 : gridDim.x);
+    if (first >= total) return;  // (the whole cluster)
+    const int32_t k_lo = PAIR ? 0 : static_cast<int32_t>(int64_t{p.nk} * rank / split);
+    const int32_t k_hi = PAIR ? p.nk : static_cast<int32_t>(int64_t{p.nk} * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F::stages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmW);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(tmem_slot, F::tmem_cols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_slot, F::tmem_cols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (PAIR)
+        ptx::cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        if (lane == 0) {
+            const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&full[0]), 0) : 0;
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t issued_mask = 0, last_parity = 0;
+            bool ok = true;
+            for (int32_t t = first; ok && t < total; t += step) {
+                const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+                const int32_t ta = tl.t0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
+                const int32_t ob = tl.o0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
+                for (int32_t kb = k_lo; kb < k_hi; ++kb) {
+                    if (!wait_bounded(&empty[s], ph ^ 1u, abort_flag, p.w)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sa = smem + s * kStageBytes;
+                    const int32_t k = kb * kBlock;
+                    const int32_t wx = W_MN ? ob : k, wy = W_MN ? k : ob;
+                    if constexpr (PAIR) {
+                        if (leader) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        const uint32_t bar = full0 + s * 8;
+                        ptx::tma_load_2d_pair(sa, &tmA, bar, k, ta);
+                        ptx::tma_load_3d_pair(sa + kStageA, &tmW, bar, wx, wy, tl.expert);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
+                        ptx::tma_load_2d(sa, &tmA, &full[s], k, ta);
+                        ptx::tma_load_3d(sa + kStageA, &tmW, &full[s], wx, wy, tl.expert);
+                    }
+                    issued_mask |= 1u << s;
+                    last_parity = (last_parity & ~(1u << s)) | (ph << s);
+                    if (++s == F::stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && leader) {
+                // wait (bounded) for the copies still in flight
+                const uint64_t tw = ptx::globaltimer_ns();
+                for (int q = 0; q < F::stages; ++q) {
+                    if (!(issued_mask & (1u << q))) continue;
+                    const uint32_t a = ptx::smem_addr(&full[q]);
+                    while (!ptx::mbar_try_wait(a, (last_parity >> q) & 1u)) {
+                        if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns)
+                            break;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer (lane 0)
+        if (leader && lane == 0) {
+            constexpr uint32_t idesc = ptx::make_idesc(0, 0, false, W_MN, F::rows, F::cols);
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t ct = 0;
+            bool ok = true;
+            bool issued_any = false;
+            for (int32_t t = first; ok && t < total; t += step) {
+                for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
+                    const uint32_t b = ct & 1u;
+                    ok = wait_bounded(&tempty[b], ((ct >> 1) & 1u) ^ 1u, abort_flag, p.w) &&
+                         wait_bounded(&full[s], ph, abort_flag, p.w);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + b * F::cols;
+                    const uint32_t sa = ptx::smem_addr(smem + s * kStageBytes);
+                    const uint32_t sb = sa + kStageA;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        // K-major: a step of 32 k is 32 bytes inside the swizzle row, groups
+                        // of eight rows lie 1024 bytes apart.  MN-major: 32 rows of 128 bytes.
+                        const uint64_t ad = ptx::smem_desc_sw128(sa + ks * 32, 16, 1024);
+                        const uint64_t bd =
+                            W_MN ? ptx::smem_desc_sw128(sb + ks * 32 * 128, kStageB, 1024)
+                                 : ptx::smem_desc_sw128(sb + ks * 32, 16, 1024);
+                        if constexpr (PAIR)
+                            ptx::umma_f8_pair(d_tmem, ad, bd, idesc, ks != 0 ? 1u : 0u);
+                        else
+                            ptx::umma_f8(d_tmem, ad, bd, idesc, ks != 0 ? 1u : 0u);
+                    }
+                    if constexpr (PAIR) {
+                        ptx::umma_commit_pair(&empty[s], 0x3);
+                        ptx::umma_commit_pair(&tfull[b], 0x3);
+                    } else {
+                        ptx::umma_commit(&empty[s]);
+                        ptx::umma_commit(&tfull[b]);
+                    }
+                    issued_any = true;
+                    if (++s == F::stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && issued_any) {
+                if constexpr (PAIR)
+                    ptx::umma_commit_pair(drain, 0x1);
+                else
+                    ptx::umma_commit(drain);
+                const uint32_t a = ptx::smem_addr(drain);
+                const uint64_t tw = ptx::globaltimer_ns();
+                while (!ptx::mbar_try_wait(a, 0)) {
+                    if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        // Warp (q, half): TMEM lanes 32 q .. (tokens) x warp_cols columns; a lane
+        // owns one token row.
+        constexpr int C = F::warp_cols;
+        const int q = warp & 3;
+        const int half = (warp - kEpiWarp0) >> 2;
+        const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&tempty[0]), 0) : 0;
+        const int32_t my_row = (PAIR ? static_cast<int32_t>(rank) * 128 : 0) + 32 * q + lane;
+        uint32_t ct = 0;
+        bool ok = true;
+        for (int32_t t = first; ok && t < total; t += step) {
+            const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+            const int64_t row = int64_t{tl.t0} + my_row;
+            const bool live = row < tl.t_end;
+            const int64_t c0 = int64_t{tl.o0} + C * half;
+            // (scales of rows and columns outside the call are read from its first)
+            const float* sa = p.sA + (live ? row : 0) * p.nk;
+            const float* sw = p.sW + tl.expert * p.sw_e + (c0 < p.O ? c0 / kBlock : 0) * p.sw_o;
+            float acc[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) acc[j] = 0.0f;
+            float fa = 0.0f, fw = 0.0f;
+            if (k_lo < k_hi) {
+                fa = __ldg(sa + k_lo);
+                fw = __ldg(sw + k_lo * p.sw_k);
+            }
+            for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
+                const uint32_t b = ct & 1u;
+                const float f = fa * fw;
+                if (kb + 1 < k_hi) {
+                    fa = __ldg(sa + kb + 1);
+                    fw = __ldg(sw + (kb + 1) * p.sw_k);
+                }
+                ok = warp_wait(&tfull[b], (ct >> 1) & 1u, abort_flag, p.w, lane);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t tcol =
+                    tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * F::cols + C * half;
+#pragma unroll
+                for (int c = 0; c < C / 32; ++c) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(tcol + 32 * c, r);
+                    ptx::tmem_ld_wait_for(r);
+                    if (c == C / 32 - 1) {  // this P_b is read: the issuer may fill it again
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (leader)
+                                ptx::mbar_arrive(&tempty[b]);
+                            else
+                                ptx::mbar_arrive_cluster(tempty0 + 8 * b);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        acc[32 * c + j] = fmaf(__uint_as_float(r[j]), f, acc[32 * c + j]);
+                }
+            }
+            if (!ok) break;
+            if (PAIR || split == 1) {
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < C; j += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+                        if (c0 + j < p.O) store_row(p, row, c0 + j, v);
+                    }
+                }
+            } else if (live) {
+                // the share into this CTA's ring (every copy and MMA of it is complete)
+                float* mine = reinterpret_cast<float*>(smem) + my_row * kPitch + C * half;
+#pragma unroll
+                for (int j = 0; j < C; j += 4)
+                    *reinterpret_cast<float4*>(mine + j) =
+                        make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+            }
+        }
+    }
+
+    if constexpr (!PAIR) {
+        if (split > 1) {
+            __syncthreads();
+            ptx::cluster_sync();  // every share of the tile is written
+            if (*abort_flag == 0) {
+                const Tile tl = tile_of<PAIR, GROUPED>(first, p, offs, begin);
+                const int32_t left = tl.t_end - tl.t0;
+                const int32_t rows = left < F::rows ? left : F::rows;
+                // vectors of four outputs, dealt to the cluster's threads
+                const int32_t units = rows * (F::cols / 4);
+                const uint32_t ring = ptx::smem_addr(smem);
+                for (int32_t u = static_cast<int32_t>(rank) * kThreads + threadIdx.x; u < units;
+                     u += static_cast<int32_t>(split) * kThreads) {
+                    const int32_t r = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
+                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (uint32_t k = 0; k < split; ++k) {
+                        const float4 x =
+                            ptx::ld_cluster_f4(ptx::mapa_shared(ring + (r * kPitch + c) * 4, k));
+                        v[0] += x.x;
+                        v[1] += x.y;
+                        v[2] += x.z;
+                        v[3] += x.w;
+                    }
+                    if (tl.o0 + c < p.O) store_row(p, int64_t{tl.t0} + r, int64_t{tl.o0} + c, v);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    if (PAIR || split > 1)
+        ptx::cluster_sync();  // no CTA leaves while another may still read or signal it
+    else
+        __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem_base, F::tmem_cols);
+        else
+            ptx::tmem_dealloc(tmem_base, F::tmem_cols);
+    }
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+struct Launch {
+    const CUtensorMap &a, &w;
+    const LParams& p;
+    int sms;
+    int split;  // of the one-CTA form
+    cudaStream_t stream;
+};
+
+template <bool PAIR, bool W_MN, bool GROUPED>
+cudaError_t launch(const Launch& l)
+{
+    using F = Form<PAIR>;
+    auto kern = forge_linear_kernel<PAIR, W_MN, GROUPED>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    constexpr int most = F::bytes(GROUPED ? kMaxExperts : 0);
+    static_assert(most <= 227 * 1024, "ring and table within one CTA's shared memory");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = PAIR ? 1 : l.split;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = l.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static int ready[64] = {0};  // per device: resident pairs, or 1
+    int& mc = ready[dev & 63];
+    if (__atomic_load_n(&mc, __ATOMIC_ACQUIRE) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+        int n = 1;
+        if (PAIR) {
+            cfg.gridDim = dim3(2);
+            cfg.dynamicSmemBytes = most;
+            cfg.stream = nullptr;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            cfg.stream = l.stream;
+        }
+        __atomic_store_n(&mc, n, __ATOMIC_RELEASE);
+    }
+    // by experts the tiles are known on the device only: at most one more a
+    // column of tiles for each expert than the rows alone would make
+    const int64_t rows = (l.p.T + F::rows - 1) / F::rows;
+    const int64_t extra = GROUPED ? (l.p.E < l.p.T ? l.p.E : l.p.T) : 0;
+    const int64_t total = (rows + extra) * l.p.tiles_o;
+    if (total > INT32_MAX / 16) return cudaErrorInvalidValue;
+    if (PAIR)
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * (total < mc ? total : mc)));
+    else
+        cfg.gridDim = dim3(static_cast<unsigned>(total), static_cast<unsigned>(l.split));
+    cfg.dynamicSmemBytes = static_cast<size_t>(F::bytes(GROUPED ? l.p.E : 0));
+    return cudaLaunchKernelEx(&cfg, kern, l.a, l.w, l.p);
+}
+
+// The form, and the CTAs that share a tile's K.
+struct Choice {
+    bool pair;
+    int split;
+};
+Choice choose(const LParams& p, int sms)
+{
+    if (const char* e = std::getenv("FORGE_LINEAR_KERNEL")) {
+        if (std::strcmp(e, "pair") == 0) return {true, 1};
+        if (std::strncmp(e, "single", 6) == 0) {
+            int n = std::atoi(e + 6);
+            n = n < 1 ? 1 : (n > kMostSplit ? kMostSplit : n);
+            return {false, n < p.nk ? n : p.nk};
+        }
+    }
+    const int64_t experts = p.E > 0 ? (p.E < p.T ? p.E : p.T) : 1;
+    const int64_t each = (p.T + experts - 1) / experts;  // tokens of an expert
+    const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
+    if (each > 128 && pairs >= sms / 4) return {true, 1};
+    const int64_t tiles = (each + 127) / 128 * experts * ((p.O + 127) / 128);
+    int64_t split = 2LL * sms / tiles;
+    if (split > kMostSplit) split = kMostSplit;
+    if (split > p.nk) split = p.nk;
+    return {false, split < 1 ? 1 : static_cast<int>(split)};
+}
+
+struct Operands {
+    const uint8_t *A, *W;
+    int64_t ldA, ldW;  // bytes between rows, multiples of 16
+};
+
+cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams p, int sms,
+                cudaStream_t stream)
+{
+    const int64_t E = p.E > 0 ? p.E : 1;
+    CUtensorMap ta, tw;
+    if (encode_bytes(&ta, o.A, p.K, p.T, 0, o.ldA, 128) != cudaSuccess ||
+        encode_bytes(&tw, o.W, M, N, E, o.ldW, 128) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    const Choice c = choose(p, sms);
+    p.tiles_o = static_cast<int32_t>((p.O + (c.pair ? 255 : 127)) / (c.pair ? 256 : 128));
+    const Launch l{ta, tw, p, sms, c.split, stream};
+    if (c.pair) {
+        if (p.E > 0) return transpose ? launch<true, false, true>(l) : launch<true, true, true>(l);
+        return transpose ? launch<true, false, false>(l) : launch<true, true, false>(l);
+    }
+    if (p.E > 0) return transpose ? launch<false, false, true>(l) : launch<false, true, true>(l);
+    return transpose ? launch<false, false, false>(l) : launch<false, true, false>(l);
+}
+
+forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW, void* Y,
+                    forge_dtype y_dtype, const int32_t* offsets, int32_t E, int64_t T, int64_t N,
+                    int64_t M, int32_t transpose, forge_stream_t stream)
+{
+    if (T < 0 || N < 1 || M < 1 || T > INT32_MAX - 512 || N > INT32_MAX - 512 ||
+        M > INT32_MAX - 512)
+        return FORGE_ERR_INVALID_ARG;
+    if (!W || !sW || (T > 0 && (!A || !sA || !Y))) return FORGE_ERR_INVALID_ARG;
+    if (y_dtype != FORGE_F32 && y_dtype != FORGE_BF16) return FORGE_ERR_UNSUPPORTED_DTYPE;
+    if (!aligned(sA, 4) || !aligned(sW, 4) || !aligned(offsets, 4) ||
+        !aligned(Y, y_dtype == FORGE_F32 ? 4 : 2))
+        return FORGE_ERR_MISALIGNED;
+    int sms = 0;
+    forge_status st = device_sms(&sms);
+    if (st != FORGE_OK) return st;
+    if (T == 0) return FORGE_OK;
+    const void* ptrs[] = {A, sA, W, sW, Y, offsets};
+    if ((st = device_resident(ptrs, 6)) != FORGE_OK) return st;
+    LParams p{};
+    p.T = T;
+    p.K = transpose ? M : N;
+    p.O = transpose ? N : M;
+    p.sA = sA;
+    p.sW = sW;
+    const int64_t across = (M + kBlock - 1) / kBlock, down = (N + kBlock - 1) / kBlock;
+    p.sw_k = transpose ? 1 : across;
+    p.sw_o = transpose ? across : 1;
+    p.sw_e = across * down;
+    p.Y = Y;
+    p.f32 = y_dtype == FORGE_F32;
+    p.vec = p.O % (p.f32 ? 4 : 8) == 0 && aligned(Y, 16);
+    p.E = E;
+    p.offsets = offsets;
+    p.nk = static_cast<int32_t>((p.K + kBlock - 1) / kBlock);
+    p.w.timeout_ns = wait_timeout();
+    p.w.status = device_status_word();
+
+    // rows that TMA cannot address go through rows padded to 16 bytes
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t rows_w = (E > 0 ? E : 1) * N;
+    const int64_t pad_a = (p.K + 15) / 16 * 16, pad_w = (M + 15) / 16 * 16;
+    const bool stage_a = p.K % 16 != 0 || !aligned(A, 16);
+    const bool stage_w = M % 16 != 0 || !aligned(W, 16);
+    Operands o{A, W, p.K, M};
+    void* scratch = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (stage_a || stage_w) {
+        const int64_t a_bytes = stage_a ? (pad_a * T + 255) / 256 * 256 : 0;
+        e = scratch_alloc(&scratch, a_bytes + (stage_w ? pad_w * rows_w : 0), s);
+        uint8_t* at = static_cast<uint8_t*>(scratch);
+        if (e == cudaSuccess && stage_a) {
+            e = stage_padded_rows(A, at, T, p.K, pad_a, s);
+            o.A = at;
+            o.ldA = pad_a;
+            at += a_bytes;
+        }
+        if (e == cudaSuccess && stage_w) {
+            e = stage_padded_rows(W, at, rows_w, M, pad_w, s);
+            o.W = at;
+            o.ldW = pad_w;
+        }
+    }
+    if (e == cudaSuccess) e = run(o, N, M, transpose != 0, p, sms, s);
+    if (scratch) {
+        const cudaError_t fe = scratch_free(scratch, s);
+        if (e == cudaSuccess) e = fe;
+    }
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+}
+
+}  // namespace linear
+}  // namespace forge
+
+extern "C" forge_status forge_linear_e4m3(const uint8_t* A, const float* sA, const uint8_t* W,
+                                          const float* sW, void* Y, forge_dtype y_dtype, int64_t T,
+                                          int64_t N, int64_t M, int32_t transpose,
+                                          forge_stream_t stream)
+{
+    return forge::linear::linear(A, sA, W, sW, Y, y_dtype, nullptr, 0, T, N, M, transpose, stream);
+}
+
+extern "C" forge_status forge_grouped_linear_e4m3(const uint8_t* A, const float* sA,
+                                                  const uint8_t* W, const float* sW,
+                                                  const int32_t* offsets, int32_t E, void* Y,
+                                                  forge_dtype y_dtype, int64_t T_max, int64_t N,
+                                                  int64_t M, int32_t transpose,
+                                                  forge_stream_t stream)
+{
+    if (!offsets || E < 1 || E > forge::kMaxExperts) return FORGE_ERR_INVALID_ARG;
+    return forge::linear::linear(A, sA, W, sW, Y, y_dtype, offsets, E, T_max, N, M, transpose,
+                                 stream);
+}
