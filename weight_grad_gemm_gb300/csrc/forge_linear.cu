@@ -40,12 +40,14 @@ namespace forge {
 namespace linear {
 
 constexpr int kBlock = 128;       // entries under one scale, and k of a stage
-constexpr int kThreads = 320;     // producer, MMA issuer, eight epilogue warps
-constexpr int kEpiWarp0 = 2;
+constexpr int kThreads = 384;     // producer, MMA issuer, two idle and eight epilogue warps
+constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kStageA = 128 * kBlock;  // 128 token rows
 constexpr int kStageB = 128 * kBlock;  // 128 outputs
 constexpr int kStageBytes = kStageA + kStageB;
+constexpr int kSlots = 2;         // P_b in tensor memory
+constexpr int kStoreBytes = 2048;  // 32 rows x 64 bytes of Y on their way out
 constexpr int kMostSplit = 8;     // CTAs that share a tile's K
 constexpr int kBand = 8;          // token tiles of a band of the tile walk
 
@@ -55,9 +57,16 @@ struct Form {
     static constexpr int rows = PAIR ? 256 : 128;  // tokens of a tile
     static constexpr int cols = PAIR ? 256 : 128;  // outputs of a tile
     static constexpr int warp_cols = cols / 2;
-    static constexpr int tmem_cols = 2 * cols;
+    static constexpr int tmem_cols = kSlots * cols;
+    static constexpr int chunk = PAIR ? 32 : 16;  // columns of a tensor memory load
+    // registers a thread: 168 (or 80 with two CTAs an SM) at launch, moved from the
+    // first warpgroup to the two that hold the sums (3 x 168 = 56 + 2 x 224; 3 x 80 >=
+    // 40 + 2 x 96)
+    static constexpr int few = PAIR ? 56 : 40;
+    static constexpr int many = PAIR ? 224 : 96;
     static constexpr int bar_at = stages * kStageBytes;
-    static constexpr int table_at = bar_at + 256;
+    static constexpr int stage_at = bar_at + 256;  // 2 KB for each epilogue warp's stores
+    static constexpr int table_at = stage_at + (PAIR ? kEpiWarps * kStoreBytes : 0);
     static constexpr int bytes(int E) { return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024; }
 };
 constexpr int kPitch = 132;  // floats between the rows of a share in shared memory
@@ -69,6 +78,7 @@ struct LParams {
     int64_t sw_k, sw_o, sw_e;  // strides of W's scales along K, outputs, experts
     void* Y;
     int32_t f32, vec;      // Y's type; rows of Y take 16-byte stores
+    int32_t sa_vec;        // rows of A's scales take 16-byte loads
     int32_t E;             // experts, 0: dense
     const int32_t* offsets;
     int32_t tiles_o, nk;
@@ -113,6 +123,19 @@ __device__ __forceinline__ Tile tile_of(int32_t t, const LParams& p, const int32
     return r;
 }
 
+// wait_bounded for waits that mostly fail at first: a block's hand-over between
+// the tensor core and the epilogue comes every 0.3 us, and reading the global
+// timer before the second try alone takes longer than that.
+__device__ __forceinline__ bool wait_often(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag, const Params& p)
+{
+    const uint32_t a = ptx::smem_addr(bar);
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (ptx::mbar_try_wait(a, parity)) return true;
+    return wait_bounded(bar, parity, abort_flag, p);
+}
+
 // Offsets into shared memory, checked, and the first tile of each expert;
 // false (and the status word set) where the offsets are not an ascending list
 // within the T rows.  All threads of the CTA.
@@ -151,6 +174,15 @@ __device__ bool group_table(const LParams& p, int32_t* offs, int32_t* begin)
     return true;
 }
 
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32])
+{
+    ptx::tmem_ld_32x32b_x32(taddr, r);
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16])
+{
+    ptx::tmem_ld_32x32b_x16(taddr, r);
+}
+
 // N outputs of one row, in registers, from column c on.
 template <int N>
 __device__ __forceinline__ void store_row(const LParams& p, int64_t row, int64_t c,
@@ -168,6 +200,67 @@ __device__ __forceinline__ void store_row(const LParams& p, int64_t row, int64_t
     }
 }
 
+// A warp's 32 rows x 128 outputs, a lane a row, from row r0 and column c0 on: through
+// shared memory, 64 bytes of a row at a time, so that four lanes write a row's
+// neighbouring 16 bytes (a lane writing its own row instead, 16 bytes an
+// instruction, took 7,000 cycles a tile).
+__device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int64_t r0,
+                                           int64_t r_end, int64_t c0, const float (&acc)[128],
+                                           int lane)
+{
+    if (!p.vec) {
+        if (r0 + lane < r_end) {
+#pragma unroll
+            for (int j = 0; j < 128; j += 8) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+                if (c0 + j < p.O) store_row(p, r0 + lane, c0 + j, v);
+            }
+        }
+        return;
+    }
+    // the 16-byte unit u of row r lies at place u ^ (r / 2 % 4): no bank conflicts
+    uint4* mine = reinterpret_cast<uint4*>(stage) + 4 * lane;
+    const int turn = lane >> 1 & 3;
+    const int from = lane & 3, down = lane >> 2;
+    auto out = [&](int es, int64_t c) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = 8 * k + down;
+            const uint4 v = reinterpret_cast<const uint4*>(stage)[4 * r + (from ^ (r >> 1 & 3))];
+            const int64_t col = c + from * (16 / es);
+            if (r0 + r < r_end && col < p.O)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) +
+                                          ((r0 + r) * p.O + col) * es) = v;
+        }
+        __syncwarp();
+    };
+    if (p.f32) {
+#pragma unroll
+        for (int j = 0; j < 128; j += 16) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                mine[u ^ turn] = make_uint4(
+                    __float_as_uint(acc[j + 4 * u]), __float_as_uint(acc[j + 4 * u + 1]),
+                    __float_as_uint(acc[j + 4 * u + 2]), __float_as_uint(acc[j + 4 * u + 3]));
+            out(4, c0 + j);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 128; j += 32) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float* a = acc + j + 8 * u;
+                mine[u ^ turn] = make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]),
+                                            bf16x2(a[4], a[5]), bf16x2(a[6], a[7]));
+            }
+            out(2, c0 + j);
+        }
+    }
+}
+
 template <bool PAIR, bool W_MN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     forge_linear_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K]
@@ -181,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::bar_at);
     uint64_t* empty = full + F::stages;
     uint64_t* tfull = empty + F::stages;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
+    uint64_t* tempty = tfull + kSlots;
+    uint64_t* drain = tempty + kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* offs = reinterpret_cast<int32_t*>(smem + F::table_at);
@@ -214,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kSlots; ++b) {
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
@@ -243,188 +336,217 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    if (warp == 0) {
-        // ---------------------------------------------------- TMA producer
-        if (lane == 0) {
-            const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&full[0]), 0) : 0;
-            int s = 0;
-            uint32_t ph = 0;
-            uint32_t issued_mask = 0, last_parity = 0;
-            bool ok = true;
-            for (int32_t t = first; ok && t < total; t += step) {
-                const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
-                const int32_t ta = tl.t0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
-                const int32_t ob = tl.o0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
-                for (int32_t kb = k_lo; kb < k_hi; ++kb) {
-                    if (!wait_bounded(&empty[s], ph ^ 1u, abort_flag, p.w)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* sa = smem + s * kStageBytes;
-                    const int32_t k = kb * kBlock;
-                    const int32_t wx = W_MN ? ob : k, wy = W_MN ? k : ob;
-                    if constexpr (PAIR) {
-                        if (leader) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                        const uint32_t bar = full0 + s * 8;
-                        ptx::tma_load_2d_pair(sa, &tmA, bar, k, ta);
-                        ptx::tma_load_3d_pair(sa + kStageA, &tmW, bar, wx, wy, tl.expert);
-                    } else {
-                        ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
-                        ptx::tma_load_2d(sa, &tmA, &full[s], k, ta);
-                        ptx::tma_load_3d(sa + kStageA, &tmW, &full[s], wx, wy, tl.expert);
-                    }
-                    issued_mask |= 1u << s;
-                    last_parity = (last_parity & ~(1u << s)) | (ph << s);
-                    if (++s == F::stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
-            if (!ok && leader) {
-                // wait (bounded) for the copies still in flight
-                const uint64_t tw = ptx::globaltimer_ns();
-                for (int q = 0; q < F::stages; ++q) {
-                    if (!(issued_mask & (1u << q))) continue;
-                    const uint32_t a = ptx::smem_addr(&full[q]);
-                    while (!ptx::mbar_try_wait(a, (last_parity >> q) & 1u)) {
-                        if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns)
+    if (warp < kEpiWarp0) {
+        ptx::registers_down<F::few>();
+        if (warp == 0) {
+            // ---------------------------------------------------- TMA producer
+            if (lane == 0) {
+                const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&full[0]), 0) : 0;
+                int s = 0;
+                uint32_t ph = 0;
+                uint32_t issued_mask = 0, last_parity = 0;
+                bool ok = true;
+                for (int32_t t = first; ok && t < total; t += step) {
+                    const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+                    const int32_t ta = tl.t0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
+                    const int32_t ob = tl.o0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
+                    for (int32_t kb = k_lo; kb < k_hi; ++kb) {
+                        if (!wait_often(&empty[s], ph ^ 1u, abort_flag, p.w)) {
+                            ok = false;
                             break;
+                        }
+                        uint8_t* sa = smem + s * kStageBytes;
+                        const int32_t k = kb * kBlock;
+                        const int32_t wx = W_MN ? ob : k, wy = W_MN ? k : ob;
+                        if constexpr (PAIR) {
+                            if (leader) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                            const uint32_t bar = full0 + s * 8;
+                            ptx::tma_load_2d_pair(sa, &tmA, bar, k, ta);
+                            ptx::tma_load_3d_pair(sa + kStageA, &tmW, bar, wx, wy, tl.expert);
+                        } else {
+                            ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
+                            ptx::tma_load_2d(sa, &tmA, &full[s], k, ta);
+                            ptx::tma_load_3d(sa + kStageA, &tmW, &full[s], wx, wy, tl.expert);
+                        }
+                        issued_mask |= 1u << s;
+                        last_parity = (last_parity & ~(1u << s)) | (ph << s);
+                        if (++s == F::stages) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (!ok && leader) {
+                    // wait (bounded) for the copies still in flight
+                    const uint64_t tw = ptx::globaltimer_ns();
+                    for (int q = 0; q < F::stages; ++q) {
+                        if (!(issued_mask & (1u << q))) continue;
+                        const uint32_t a = ptx::smem_addr(&full[q]);
+                        while (!ptx::mbar_try_wait(a, (last_parity >> q) & 1u)) {
+                            if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns)
+                                break;
+                        }
                     }
                 }
             }
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (lane 0)
-        if (leader && lane == 0) {
-            constexpr uint32_t idesc = ptx::make_idesc(0, 0, false, W_MN, F::rows, F::cols);
-            int s = 0;
-            uint32_t ph = 0;
-            uint32_t ct = 0;
-            bool ok = true;
-            bool issued_any = false;
-            for (int32_t t = first; ok && t < total; t += step) {
-                for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
-                    const uint32_t b = ct & 1u;
-                    ok = wait_bounded(&tempty[b], ((ct >> 1) & 1u) ^ 1u, abort_flag, p.w) &&
-                         wait_bounded(&full[s], ph, abort_flag, p.w);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + b * F::cols;
-                    const uint32_t sa = ptx::smem_addr(smem + s * kStageBytes);
-                    const uint32_t sb = sa + kStageA;
+        } else if (warp == 1) {
+            // ---------------------------------------------------- MMA issuer (lane 0)
+            if (leader && lane == 0) {
+                constexpr uint32_t idesc = ptx::make_idesc(0, 0, false, W_MN, F::rows, F::cols);
+                // K-major: a step of 32 k is 32 bytes inside the swizzle row, groups of eight
+                // rows lie 1024 bytes apart.  MN-major: 32 rows of 128 bytes.  (In 16-byte
+                // units: an address below 256 KB never carries out of its field.)
+                constexpr uint64_t kStepA = 32 >> 4, kStepB = (W_MN ? 32 * 128 : 32) >> 4;
+                const uint32_t ring = ptx::smem_addr(smem);
+                const uint64_t a_desc = ptx::smem_desc_sw128(ring, 16, 1024);
+                const uint64_t b_desc =
+                    ptx::smem_desc_sw128(ring + kStageA, W_MN ? kStageB : 16, 1024);
+                int s = 0;
+                uint32_t ph = 0;
+                uint32_t ct = 0;  // k-blocks
+                bool ok = true;
+                bool issued_any = false;
+                for (int32_t t = first; ok && t < total; t += step) {
+                    for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
+                        // (the operands are there long before the place for the sums is:
+                        // nothing but the instructions themselves follows the second wait)
+                        ok = wait_often(&full[s], ph, abort_flag, p.w);
+                        if (!ok) break;
+                        const uint32_t b = ct % kSlots;
+                        const uint32_t d_tmem = tmem_base + b * F::cols;
+                        const uint64_t ad = a_desc + s * (kStageBytes >> 4);
+                        const uint64_t bd = b_desc + s * (kStageBytes >> 4);
+                        ok = wait_often(&tempty[b], (ct / kSlots & 1u) ^ 1u, abort_flag, p.w);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        // K-major: a step of 32 k is 32 bytes inside the swizzle row, groups
-                        // of eight rows lie 1024 bytes apart.  MN-major: 32 rows of 128 bytes.
-                        const uint64_t ad = ptx::smem_desc_sw128(sa + ks * 32, 16, 1024);
-                        const uint64_t bd =
-                            W_MN ? ptx::smem_desc_sw128(sb + ks * 32 * 128, kStageB, 1024)
-                                 : ptx::smem_desc_sw128(sb + ks * 32, 16, 1024);
-                        if constexpr (PAIR)
-                            ptx::umma_f8_pair(d_tmem, ad, bd, idesc, ks != 0 ? 1u : 0u);
-                        else
-                            ptx::umma_f8(d_tmem, ad, bd, idesc, ks != 0 ? 1u : 0u);
-                    }
-                    if constexpr (PAIR) {
-                        ptx::umma_commit_pair(&empty[s], 0x3);
-                        ptx::umma_commit_pair(&tfull[b], 0x3);
-                    } else {
-                        ptx::umma_commit(&empty[s]);
-                        ptx::umma_commit(&tfull[b]);
-                    }
-                    issued_any = true;
-                    if (++s == F::stages) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (int ks = 0; ks < 4; ++ks) {
+                            if constexpr (PAIR)
+                                ptx::umma_f8_pair(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
+                                                  ks != 0 ? 1u : 0u);
+                            else
+                                ptx::umma_f8(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
+                                             ks != 0 ? 1u : 0u);
+                        }
+                        issued_any = true;
+                        if constexpr (PAIR) {
+                            ptx::umma_commit_pair(&tfull[b], 0x3);
+                            ptx::umma_commit_pair(&empty[s], 0x3);
+                        } else {
+                            ptx::umma_commit(&tfull[b]);
+                            ptx::umma_commit(&empty[s]);
+                        }
+                        if (++s == F::stages) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
-            }
-            if (!ok && issued_any) {
-                if constexpr (PAIR)
-                    ptx::umma_commit_pair(drain, 0x1);
-                else
-                    ptx::umma_commit(drain);
-                const uint32_t a = ptx::smem_addr(drain);
-                const uint64_t tw = ptx::globaltimer_ns();
-                while (!ptx::mbar_try_wait(a, 0)) {
-                    if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
+                if (!ok && issued_any) {
+                    if constexpr (PAIR)
+                        ptx::umma_commit_pair(drain, 0x1);
+                    else
+                        ptx::umma_commit(drain);
+                    const uint32_t a = ptx::smem_addr(drain);
+                    const uint64_t tw = ptx::globaltimer_ns();
+                    while (!ptx::mbar_try_wait(a, 0)) {
+                        if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
+                    }
                 }
             }
         }
     } else {
         // ---------------------------------------------------- epilogue
-        // Warp (q, half): TMEM lanes 32 q .. (tokens) x warp_cols columns; a lane
-        // owns one token row.
-        constexpr int C = F::warp_cols;
+        ptx::registers_up<F::many>();
+        // Warp (q, g): TMEM lanes 32 q .. (tokens) x columns C g ..; a lane owns one
+        // token row.
+        constexpr int C = F::warp_cols, N = F::chunk;
         const int q = warp & 3;
-        const int half = (warp - kEpiWarp0) >> 2;
+        const int g = (warp - kEpiWarp0) >> 2;
         const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&tempty[0]), 0) : 0;
         const int32_t my_row = (PAIR ? static_cast<int32_t>(rank) * 128 : 0) + 32 * q + lane;
+        const int32_t my_col = C * g;
+        const uint32_t my_tmem = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + C * g;
         uint32_t ct = 0;
         bool ok = true;
         for (int32_t t = first; ok && t < total; t += step) {
             const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
             const int64_t row = int64_t{tl.t0} + my_row;
             const bool live = row < tl.t_end;
-            const int64_t c0 = int64_t{tl.o0} + C * half;
+            const int64_t c0 = int64_t{tl.o0} + my_col;
             // (scales of rows and columns outside the call are read from its first)
             const float* sa = p.sA + (live ? row : 0) * p.nk;
             const float* sw = p.sW + tl.expert * p.sw_e + (c0 < p.O ? c0 / kBlock : 0) * p.sw_o;
             float acc[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = 0.0f;
-            float fa = 0.0f, fw = 0.0f;
-            if (k_lo < k_hi) {
-                fa = __ldg(sa + k_lo);
-                fw = __ldg(sw + k_lo * p.sw_k);
-            }
-            for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
-                const uint32_t b = ct & 1u;
-                const float f = fa * fw;
-                if (kb + 1 < k_hi) {
-                    fa = __ldg(sa + kb + 1);
-                    fw = __ldg(sw + (kb + 1) * p.sw_k);
+            // scales four blocks ahead (their product is taken when they are needed, so
+            // that nothing waits for the loads)
+            float na[4], nw[4];
+            const bool vec = p.sa_vec && k_lo % 4 == 0;
+            auto load_scales = [&](int32_t kb) {
+                if (vec && kb + 4 <= k_hi) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(sa + kb));
+                    na[0] = v.x;
+                    na[1] = v.y;
+                    na[2] = v.z;
+                    na[3] = v.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        na[i] = __ldg(sa + (kb + i < k_hi ? kb + i : k_hi - 1));
                 }
-                ok = warp_wait(&tfull[b], (ct >> 1) & 1u, abort_flag, p.w, lane);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t tcol =
-                    tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * F::cols + C * half;
 #pragma unroll
-                for (int c = 0; c < C / 32; ++c) {
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(tcol + 32 * c, r);
-                    ptx::tmem_ld_wait_for(r);
-                    if (c == C / 32 - 1) {  // this P_b is read: the issuer may fill it again
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (leader)
-                                ptx::mbar_arrive(&tempty[b]);
-                            else
-                                ptx::mbar_arrive_cluster(tempty0 + 8 * b);
+                for (int i = 0; i < 4; ++i)
+                    nw[i] = __ldg(sw + (kb + i < k_hi ? kb + i : k_hi - 1) * p.sw_k);
+            };
+            load_scales(k_lo);
+            for (int32_t k0 = k_lo; ok && k0 < k_hi; k0 += 4) {
+                float now[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = na[i] * nw[i];
+                if (k0 + 4 < k_hi) load_scales(k0 + 4);
+                const int n = k_hi - k0 < 4 ? k_hi - k0 : 4;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, ++ct) {
+                    const float f = i < 2 ? (i == 0 ? now[0] : now[1]) : (i == 2 ? now[2] : now[3]);
+                    const uint32_t b = ct % kSlots;
+                    ok = wait_often(&tfull[b], ct / kSlots & 1u, abort_flag, p.w);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t tcol = my_tmem + b * F::cols;
+                    uint32_t r[2][N];
+                    tmem_load(tcol, r[0]);
+#pragma unroll
+                    for (int c = 0; c < C / N; ++c) {
+                        ptx::tmem_ld_wait_for(r[c & 1]);
+                        if (c + 1 < C / N) {
+                            tmem_load(tcol + N * (c + 1), r[(c + 1) & 1]);
+                        } else {  // this P_b is read: the issuer may fill it again
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (leader)
+                                    ptx::mbar_arrive(&tempty[b]);
+                                else
+                                    ptx::mbar_arrive_cluster_unordered(tempty0 + 8 * b);
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        acc[32 * c + j] = fmaf(__uint_as_float(r[j]), f, acc[32 * c + j]);
+                        for (int j = 0; j < N; ++j)
+                            acc[N * c + j] =
+                                fmaf(__uint_as_float(r[c & 1][j]), f, acc[N * c + j]);
+                    }
                 }
             }
             if (!ok) break;
-            if (PAIR || split == 1) {
-                if (live) {
-#pragma unroll
-                    for (int j = 0; j < C; j += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
-                        if (c0 + j < p.O) store_row(p, row, c0 + j, v);
-                    }
-                }
+            if constexpr (PAIR) {
+                store_tile(p, smem + F::stage_at + (warp - kEpiWarp0) * kStoreBytes, row - lane,
+                           tl.t_end, c0, acc, lane);
             } else if (live) {
-                // the share into this CTA's ring (every copy and MMA of it is complete)
-                float* mine = reinterpret_cast<float*>(smem) + my_row * kPitch + C * half;
+                // this CTA's share into its ring (every copy and MMA of it is complete)
+                float* mine = reinterpret_cast<float*>(smem) + my_row * kPitch + my_col;
 #pragma unroll
                 for (int j = 0; j < C; j += 4)
                     *reinterpret_cast<float4*>(mine + j) =
@@ -434,30 +556,28 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     }
 
     if constexpr (!PAIR) {
-        if (split > 1) {
-            __syncthreads();
-            ptx::cluster_sync();  // every share of the tile is written
-            if (*abort_flag == 0) {
-                const Tile tl = tile_of<PAIR, GROUPED>(first, p, offs, begin);
-                const int32_t left = tl.t_end - tl.t0;
-                const int32_t rows = left < F::rows ? left : F::rows;
-                // vectors of four outputs, dealt to the cluster's threads
-                const int32_t units = rows * (F::cols / 4);
-                const uint32_t ring = ptx::smem_addr(smem);
-                for (int32_t u = static_cast<int32_t>(rank) * kThreads + threadIdx.x; u < units;
-                     u += static_cast<int32_t>(split) * kThreads) {
-                    const int32_t r = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
-                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (uint32_t k = 0; k < split; ++k) {
-                        const float4 x =
-                            ptx::ld_cluster_f4(ptx::mapa_shared(ring + (r * kPitch + c) * 4, k));
-                        v[0] += x.x;
-                        v[1] += x.y;
-                        v[2] += x.z;
-                        v[3] += x.w;
-                    }
-                    if (tl.o0 + c < p.O) store_row(p, int64_t{tl.t0} + r, int64_t{tl.o0} + c, v);
+        // the sum of the tile's shares, rows of it dealt to the cluster's threads
+        __syncthreads();
+        if (split > 1) ptx::cluster_sync();
+        if (*abort_flag == 0) {
+            const Tile tl = tile_of<PAIR, GROUPED>(first, p, offs, begin);
+            const int32_t left = tl.t_end - tl.t0;
+            const int32_t rows = left < F::rows ? left : F::rows;
+            const int32_t units = rows * (F::cols / 4);  // of four outputs
+            const uint32_t ring = ptx::smem_addr(smem);
+            for (int32_t u = static_cast<int32_t>(rank) * kThreads + threadIdx.x; u < units;
+                 u += static_cast<int32_t>(split) * kThreads) {
+                const int32_t r = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (uint32_t k = 0; k < split; ++k) {
+                    const uint32_t at = ring + (r * kPitch + c) * 4;
+                    const float4 x = ptx::ld_cluster_f4(ptx::mapa_shared(at, k));
+                    v[0] += x.x;
+                    v[1] += x.y;
+                    v[2] += x.z;
+                    v[3] += x.w;
                 }
+                if (tl.o0 + c < p.O) store_row(p, int64_t{tl.t0} + r, int64_t{tl.o0} + c, v);
             }
         }
     }
@@ -619,6 +739,7 @@ forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const f
     p.E = E;
     p.offsets = offsets;
     p.nk = static_cast<int32_t>((p.K + kBlock - 1) / kBlock);
+    p.sa_vec = p.nk % 4 == 0 && aligned(sA, 16);
     p.w.timeout_ns = wait_timeout();
     p.w.status = device_status_word();
 
