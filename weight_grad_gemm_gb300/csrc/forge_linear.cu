@@ -40,37 +40,50 @@ namespace forge {
 namespace linear {
 
 constexpr int kBlock = 128;       // entries under one scale, and k of a stage
-constexpr int kThreads = 384;     // producer, MMA issuer, two idle and eight epilogue warps
+constexpr int kThreads = 384;     // producer, two MMA issuers, scales, eight epilogue warps
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kStageA = 128 * kBlock;  // 128 token rows
 constexpr int kStageB = 128 * kBlock;  // 128 outputs
 constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kSlots = 2;         // P_b in tensor memory
-constexpr int kStoreBytes = 2048;  // 32 rows x 64 bytes of Y on their way out
+constexpr int kStoreBytes = 8192;  // 32 rows x 256 bytes of Y on their way out, a warp
+constexpr int kScaleRing = 4;     // chunks of four k-blocks' scales on their way in
 constexpr int kMostSplit = 8;     // CTAs that share a tile's K
 constexpr int kBand = 8;          // token tiles of a band of the tile walk
 
+// The scales of four k-blocks for a CTA's 128 token rows and its two blocks of
+// outputs, and the tile that they belong to.
+struct Scales {
+    float a[4][128];
+    float w[4][2];
+    int32_t t0, t_end, o0, pad;
+};
+
 template <bool PAIR>
 struct Form {
-    static constexpr int stages = PAIR ? 6 : 3;
+    static constexpr int stages = 4;
+    static_assert(stages % kSlots == 0,
+                  "a stage belongs to one issuer, which so waits for each of its rounds");
     static constexpr int rows = PAIR ? 256 : 128;  // tokens of a tile
     static constexpr int cols = PAIR ? 256 : 128;  // outputs of a tile
     static constexpr int warp_cols = cols / 2;
     static constexpr int tmem_cols = kSlots * cols;
-    static constexpr int chunk = PAIR ? 32 : 16;  // columns of a tensor memory load
-    // registers a thread: 168 (or 80 with two CTAs an SM) at launch, moved from the
-    // first warpgroup to the two that hold the sums (3 x 168 = 56 + 2 x 224; 3 x 80 >=
-    // 40 + 2 x 96)
-    static constexpr int few = PAIR ? 56 : 40;
-    static constexpr int many = PAIR ? 224 : 96;
-    static constexpr int bar_at = stages * kStageBytes;
-    static constexpr int stage_at = bar_at + 256;  // 2 KB for each epilogue warp's stores
-    static constexpr int table_at = stage_at + (PAIR ? kEpiWarps * kStoreBytes : 0);
-    static constexpr int bytes(int E) { return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024; }
+    static constexpr int chunk = 32;  // columns of a tensor memory load
+    // registers a thread: 168 at launch, moved from the first warpgroup to the two
+    // that hold the sums (3 x 168 = 56 + 2 x 224)
+    static constexpr int few = 56, many = 224;
+    static constexpr int scale_at = stages * kStageBytes;
+    static constexpr int bar_at = scale_at + kScaleRing * static_cast<int>(sizeof(Scales));
+    static constexpr int store_at = (bar_at + 256 + 1023) / 1024 * 1024;
+    static constexpr int table_at = store_at + (PAIR ? kEpiWarps * kStoreBytes : 0);
+    __host__ __device__ static constexpr int bytes(int E)
+    {
+        return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024;
+    }
 };
 constexpr int kPitch = 132;  // floats between the rows of a share in shared memory
-static_assert(128 * kPitch * 4 <= Form<false>::bar_at, "a share fits the ring");
+static_assert(128 * kPitch * 4 <= Form<false>::scale_at, "a share fits the ring");
 
 struct LParams {
     int64_t T, K, O;       // tokens, contraction, outputs
@@ -201,14 +214,16 @@ __device__ __forceinline__ void store_row(const LParams& p, int64_t row, int64_t
 }
 
 // A warp's 32 rows x 128 outputs, a lane a row, from row r0 and column c0 on: through
-// shared memory, 64 bytes of a row at a time, so that four lanes write a row's
-// neighbouring 16 bytes (a lane writing its own row instead, 16 bytes an
-// instruction, took 7,000 cycles a tile).
-__device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int64_t r0,
-                                           int64_t r_end, int64_t c0, const float (&acc)[128],
-                                           int lane)
+// shared memory and out by TMA in boxes of 64 bytes of each row, while the next tile
+// is under way; TMA clips what lies outside Y.  A lane that writes its own row instead,
+// 16 bytes an instruction, keeps the load-store unit busy for 7,000 cycles a tile;
+// that is left for rows that TMA cannot address and for the tile in which an expert
+// ends.
+__device__ __forceinline__ void store_tile(const LParams& p, const CUtensorMap* tmY,
+                                           uint8_t* place, int64_t r0, int64_t r_end, int64_t c0,
+                                           const float (&acc)[128], int lane)
 {
-    if (!p.vec) {
+    if (!p.vec || (r0 + 32 > r_end && r_end < p.T)) {
         if (r0 + lane < r_end) {
 #pragma unroll
             for (int j = 0; j < 128; j += 8) {
@@ -220,51 +235,58 @@ __device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int
         }
         return;
     }
-    // the 16-byte unit u of row r lies at place u ^ (r / 2 % 4): no bank conflicts
-    uint4* mine = reinterpret_cast<uint4*>(stage) + 4 * lane;
+    if (r0 >= p.T) return;
+    // 64-byte swizzle: the 16-byte unit u of row r lies at place u ^ (r / 2 % 4), so that
+    // the lanes' writes meet no bank twice.  Box n: 2 KB.
     const int turn = lane >> 1 & 3;
-    const int from = lane & 3, down = lane >> 2;
-    auto out = [&](int es, int64_t c) {
+    auto unit = [&](int n, int u) { return reinterpret_cast<uint4*>(place + 2048 * n) + 4 * lane + (u ^ turn); };
+    auto wait = [&]() {  // the copies that went out from here have left
+        if (lane == 0) ptx::bulk_wait_read<0>();
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = 8 * k + down;
-            const uint4 v = reinterpret_cast<const uint4*>(stage)[4 * r + (from ^ (r >> 1 & 3))];
-            const int64_t col = c + from * (16 / es);
-            if (r0 + r < r_end && col < p.O)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) +
-                                          ((r0 + r) * p.O + col) * es) = v;
+    };
+    auto out = [&](int64_t c, int step) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            for (int n = 0; n < 4 && c + n * step < p.O; ++n)
+                ptx::tma_store_2d(tmY, place + 2048 * n, static_cast<int32_t>(c) + n * step,
+                                  static_cast<int32_t>(r0));
+            ptx::bulk_commit();
         }
-        __syncwarp();
     };
     if (p.f32) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 16) {
+        for (int h = 0; h < 2; ++h) {
+            wait();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                mine[u ^ turn] = make_uint4(
-                    __float_as_uint(acc[j + 4 * u]), __float_as_uint(acc[j + 4 * u + 1]),
-                    __float_as_uint(acc[j + 4 * u + 2]), __float_as_uint(acc[j + 4 * u + 3]));
-            out(4, c0 + j);
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float* a = acc + 64 * h + 16 * n + 4 * u;
+                    *unit(n, u) = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]),
+                                             __float_as_uint(a[2]), __float_as_uint(a[3]));
+                }
+            out(c0 + 64 * h, 16);
         }
     } else {
+        wait();
 #pragma unroll
-        for (int j = 0; j < 128; j += 32) {
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float* a = acc + j + 8 * u;
-                mine[u ^ turn] = make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]),
-                                            bf16x2(a[4], a[5]), bf16x2(a[6], a[7]));
+                const float* a = acc + 32 * n + 8 * u;
+                *unit(n, u) = make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]),
+                                         bf16x2(a[4], a[5]), bf16x2(a[6], a[7]));
             }
-            out(2, c0 + j);
-        }
+        out(c0, 32);
     }
 }
 
 template <bool PAIR, bool W_MN, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 1)
     forge_linear_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K]
                         const __grid_constant__ CUtensorMap tmW,  // W [E][N][M]
+                        const __grid_constant__ CUtensorMap tmY,  // Y [T, O], where p.vec
                         const LParams p)
 {
     using F = Form<PAIR>;
@@ -276,8 +298,11 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
     uint64_t* tfull = empty + F::stages;
     uint64_t* tempty = tfull + kSlots;
     uint64_t* drain = tempty + kSlots;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* sfull = drain + kSlots;
+    uint64_t* sempty = sfull + kScaleRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kScaleRing);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    Scales* scales = reinterpret_cast<Scales*>(smem + F::scale_at);
     int32_t* offs = reinterpret_cast<int32_t*>(smem + F::table_at);
     int32_t* begin = offs + p.E + 1;
 
@@ -307,11 +332,15 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
+        for (int c = 0; c < kScaleRing; ++c) {
+            ptx::mbar_init(&sfull[c], 1);
+            ptx::mbar_init(&sempty[c], kEpiWarps);
+        }
         for (int b = 0; b < kSlots; ++b) {
+            ptx::mbar_init(&drain[b], 1);
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
-        ptx::mbar_init(drain, 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
     }
@@ -389,8 +418,11 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
                     }
                 }
             }
-        } else if (warp == 1) {
-            // ---------------------------------------------------- MMA issuer (lane 0)
+        } else if (warp <= kSlots) {
+            // ---------------------------------------------------- MMA issuers (lane 0)
+            // Warp 1 + b fills slot b with every other k-block's products: one thread's
+            // waits, instructions and commits take 1,200 cycles a k-block, more than
+            // the tensor core's 512.
             if (leader && lane == 0) {
                 constexpr uint32_t idesc = ptx::make_idesc(0, 0, false, W_MN, F::rows, F::cols);
                 // K-major: a step of 32 k is 32 bytes inside the swizzle row, groups of eight
@@ -401,58 +433,117 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
                 const uint64_t a_desc = ptx::smem_desc_sw128(ring, 16, 1024);
                 const uint64_t b_desc =
                     ptx::smem_desc_sw128(ring + kStageA, W_MN ? kStageB : 16, 1024);
-                int s = 0;
-                uint32_t ph = 0;
-                uint32_t ct = 0;  // k-blocks
+                const int b = warp - 1;
+                const uint32_t d_tmem = tmem_base + b * F::cols;
+                const int64_t blocks =
+                    int64_t{k_hi - k_lo} * ((total - first + step - 1) / step);
+                int s = b;
+                uint32_t ph = 0, turn = 1;
                 bool ok = true;
                 bool issued_any = false;
-                for (int32_t t = first; ok && t < total; t += step) {
-                    for (int32_t kb = k_lo; kb < k_hi; ++kb, ++ct) {
-                        // (the operands are there long before the place for the sums is:
-                        // nothing but the instructions themselves follows the second wait)
-                        ok = wait_often(&full[s], ph, abort_flag, p.w);
-                        if (!ok) break;
-                        const uint32_t b = ct % kSlots;
-                        const uint32_t d_tmem = tmem_base + b * F::cols;
-                        const uint64_t ad = a_desc + s * (kStageBytes >> 4);
-                        const uint64_t bd = b_desc + s * (kStageBytes >> 4);
-                        ok = wait_often(&tempty[b], (ct / kSlots & 1u) ^ 1u, abort_flag, p.w);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
+                for (int64_t ct = b; ct < blocks; ct += kSlots, turn ^= 1u) {
+                    // (the operands are there long before the place for the sums is:
+                    // nothing but the instructions themselves follows the second wait)
+                    ok = wait_often(&full[s], ph, abort_flag, p.w) &&
+                         wait_often(&tempty[b], turn, abort_flag, p.w);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t ad = a_desc + s * (kStageBytes >> 4);
+                    const uint64_t bd = b_desc + s * (kStageBytes >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            if constexpr (PAIR)
-                                ptx::umma_f8_pair(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
-                                                  ks != 0 ? 1u : 0u);
-                            else
-                                ptx::umma_f8(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
-                                             ks != 0 ? 1u : 0u);
-                        }
-                        issued_any = true;
-                        if constexpr (PAIR) {
-                            ptx::umma_commit_pair(&tfull[b], 0x3);
-                            ptx::umma_commit_pair(&empty[s], 0x3);
-                        } else {
-                            ptx::umma_commit(&tfull[b]);
-                            ptx::umma_commit(&empty[s]);
-                        }
-                        if (++s == F::stages) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if constexpr (PAIR)
+                            ptx::umma_f8_pair(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
+                                              ks != 0 ? 1u : 0u);
+                        else
+                            ptx::umma_f8(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
+                                         ks != 0 ? 1u : 0u);
+                    }
+                    issued_any = true;
+                    if constexpr (PAIR) {
+                        ptx::umma_commit_pair(&tfull[b], 0x3);
+                        ptx::umma_commit_pair(&empty[s], 0x3);
+                    } else {
+                        ptx::umma_commit(&tfull[b]);
+                        ptx::umma_commit(&empty[s]);
+                    }
+                    s += kSlots;
+                    if (s >= F::stages) {
+                        s -= F::stages;
+                        ph ^= 1u;
                     }
                 }
                 if (!ok && issued_any) {
                     if constexpr (PAIR)
-                        ptx::umma_commit_pair(drain, 0x1);
+                        ptx::umma_commit_pair(&drain[b], 0x1);
                     else
-                        ptx::umma_commit(drain);
-                    const uint32_t a = ptx::smem_addr(drain);
+                        ptx::umma_commit(&drain[b]);
+                    const uint32_t a = ptx::smem_addr(&drain[b]);
                     const uint64_t tw = ptx::globaltimer_ns();
                     while (!ptx::mbar_try_wait(a, 0)) {
                         if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
                     }
                 }
+            }
+        } else {
+            // ---------------------------------------------------- scales
+            // A chunk of four k-blocks ahead in registers and up to four in shared memory:
+            // a load of the epilogue's own comes 2,000 cycles late, two k-blocks.
+            const int32_t ra = PAIR ? static_cast<int32_t>(rank) * 128 : 0;
+            float4 va[4];
+            float vw = 0.0f;
+            Tile tl;
+            auto load = [&](int32_t kb) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // (rows and columns outside the tile take the call's first scales)
+                    const int64_t row = int64_t{tl.t0} + ra + 32 * i + lane;
+                    const float* a = p.sA + (row < tl.t_end ? row : 0) * p.nk;
+                    if (p.sa_vec && kb % 4 == 0) {
+                        va[i] = __ldg(reinterpret_cast<const float4*>(a + kb));
+                    } else {
+                        const int32_t last = k_hi - 1;
+                        va[i] = make_float4(__ldg(a + kb), __ldg(a + min(kb + 1, last)),
+                                            __ldg(a + min(kb + 2, last)),
+                                            __ldg(a + min(kb + 3, last)));
+                    }
+                }
+                if (lane < 8) {
+                    const int64_t o = int64_t{tl.o0} + (lane & 1) * F::warp_cols;
+                    vw = __ldg(p.sW + tl.expert * p.sw_e + (o < p.O ? o / kBlock : 0) * p.sw_o +
+                                    min(kb + (lane >> 1), k_hi - 1) * p.sw_k);
+                }
+            };
+            int32_t t = first, kb = k_lo;
+            tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+            load(kb);
+            for (uint32_t c = 0; t < total; ++c) {
+                const uint32_t at = c % kScaleRing;
+                bool ok = wait_often(&sempty[at], (c / kScaleRing & 1u) ^ 1u, abort_flag, p.w);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                Scales& s = scales[at];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s.a[0][32 * i + lane] = va[i].x;
+                    s.a[1][32 * i + lane] = va[i].y;
+                    s.a[2][32 * i + lane] = va[i].z;
+                    s.a[3][32 * i + lane] = va[i].w;
+                }
+                if (lane < 8) s.w[lane >> 1][lane & 1] = vw;
+                if (lane == 0) {
+                    s.t0 = tl.t0;
+                    s.t_end = tl.t_end;
+                    s.o0 = tl.o0;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sfull[at]);
+                kb += 4;
+                if (kb >= k_hi) {
+                    kb = k_lo;
+                    t += step;
+                    if (t < total) tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+                }
+                if (t < total) load(kb);
             }
         }
     } else {
@@ -469,43 +560,26 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
         const uint32_t my_tmem = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + C * g;
         uint32_t ct = 0;
         bool ok = true;
+        uint32_t chunk = 0;
         for (int32_t t = first; ok && t < total; t += step) {
-            const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
-            const int64_t row = int64_t{tl.t0} + my_row;
-            const bool live = row < tl.t_end;
-            const int64_t c0 = int64_t{tl.o0} + my_col;
-            // (scales of rows and columns outside the call are read from its first)
-            const float* sa = p.sA + (live ? row : 0) * p.nk;
-            const float* sw = p.sW + tl.expert * p.sw_e + (c0 < p.O ? c0 / kBlock : 0) * p.sw_o;
             float acc[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = 0.0f;
-            // scales four blocks ahead (their product is taken when they are needed, so
-            // that nothing waits for the loads)
-            float na[4], nw[4];
-            const bool vec = p.sa_vec && k_lo % 4 == 0;
-            auto load_scales = [&](int32_t kb) {
-                if (vec && kb + 4 <= k_hi) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(sa + kb));
-                    na[0] = v.x;
-                    na[1] = v.y;
-                    na[2] = v.z;
-                    na[3] = v.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        na[i] = __ldg(sa + (kb + i < k_hi ? kb + i : k_hi - 1));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    nw[i] = __ldg(sw + (kb + i < k_hi ? kb + i : k_hi - 1) * p.sw_k);
-            };
-            load_scales(k_lo);
-            for (int32_t k0 = k_lo; ok && k0 < k_hi; k0 += 4) {
+            int32_t t0 = 0, t_end = 0, o0 = 0;
+            for (int32_t k0 = k_lo; ok && k0 < k_hi; k0 += 4, ++chunk) {
+                const uint32_t at = chunk % kScaleRing;
+                ok = wait_often(&sfull[at], chunk / kScaleRing & 1u, abort_flag, p.w);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const Scales& s = scales[at];
                 float now[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) now[i] = na[i] * nw[i];
-                if (k0 + 4 < k_hi) load_scales(k0 + 4);
+                for (int i = 0; i < 4; ++i) now[i] = s.a[i][32 * q + lane] * s.w[i][g];
+                t0 = s.t0;
+                t_end = s.t_end;
+                o0 = s.o0;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sempty[at]);
                 const int n = k_hi - k0 < 4 ? k_hi - k0 : 4;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++ct) {
@@ -542,9 +616,9 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
             }
             if (!ok) break;
             if constexpr (PAIR) {
-                store_tile(p, smem + F::stage_at + (warp - kEpiWarp0) * kStoreBytes, row - lane,
-                           tl.t_end, c0, acc, lane);
-            } else if (live) {
+                store_tile(p, &tmY, smem + F::store_at + (warp - kEpiWarp0) * kStoreBytes,
+                           int64_t{t0} + my_row - lane, t_end, int64_t{o0} + my_col, acc, lane);
+            } else if (t0 + my_row < t_end) {
                 // this CTA's share into its ring (every copy and MMA of it is complete)
                 float* mine = reinterpret_cast<float*>(smem) + my_row * kPitch + my_col;
 #pragma unroll
@@ -553,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
                         make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             }
         }
+        if (lane == 0) ptx::bulk_wait_read<0>();  // no copy reads shared memory that is gone
     }
 
     if constexpr (!PAIR) {
@@ -598,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, PAIR ? 1 : 2)
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 struct Launch {
-    const CUtensorMap &a, &w;
+    const CUtensorMap &a, &w, &y;
     const LParams& p;
     int sms;
     int split;  // of the one-CTA form
@@ -652,7 +727,7 @@ cudaError_t launch(const Launch& l)
     else
         cfg.gridDim = dim3(static_cast<unsigned>(total), static_cast<unsigned>(l.split));
     cfg.dynamicSmemBytes = static_cast<size_t>(F::bytes(GROUPED ? l.p.E : 0));
-    return cudaLaunchKernelEx(&cfg, kern, l.a, l.w, l.p);
+    return cudaLaunchKernelEx(&cfg, kern, l.a, l.w, l.y, l.p);
 }
 
 // The form, and the CTAs that share a tile's K.
@@ -695,8 +770,11 @@ cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams
         encode_bytes(&tw, o.W, M, N, E, o.ldW, 128) != cudaSuccess)
         return cudaErrorInvalidValue;
     const Choice c = choose(p, sms);
+    CUtensorMap ty{};
+    if (c.pair && p.vec && encode_rows64(&ty, p.Y, p.f32 ? 4 : 2, p.O, p.T) != cudaSuccess)
+        return cudaErrorInvalidValue;
     p.tiles_o = static_cast<int32_t>((p.O + (c.pair ? 255 : 127)) / (c.pair ? 256 : 128));
-    const Launch l{ta, tw, p, sms, c.split, stream};
+    const Launch l{ta, tw, ty, p, sms, c.split, stream};
     if (c.pair) {
         if (p.E > 0) return transpose ? launch<true, false, true>(l) : launch<true, true, true>(l);
         return transpose ? launch<true, false, false>(l) : launch<true, true, false>(l);

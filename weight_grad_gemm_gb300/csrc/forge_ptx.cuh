@@ -136,6 +136,27 @@ __device__ __forceinline__ uint64_t policy_evict_last()
     return p;
 }
 
+// 2-D tiled bulk tensor copy shared -> global; what lies outside the tensor is not
+// written.  The thread's bulk group: commit, then wait until at most N of its
+// groups still read shared memory.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x,
+                                             int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_addr(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // cp.async of `bytes` (4, 8 or 16) from global to shared; only `src_bytes`
 // are read and the rest of the destination is zero-filled.
 __device__ __forceinline__ void cp_async(void* dst, const void* src, int bytes, int src_bytes)
