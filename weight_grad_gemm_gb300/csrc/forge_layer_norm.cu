@@ -29,7 +29,11 @@ namespace norm {
 
 constexpr int kRowWarps = 8;      // warps of a block whose warps take a row each
 constexpr int kLongThreads = 1024;  // of a block on a row too wide for registers
+constexpr int kThreadsAtWork = 512;  // of an SM: 128 registers each
 constexpr int64_t kMaxForward = 16384, kMaxBackward = 8192;  // widths that registers hold
+
+// Threads of a block with W warps a row.
+__host__ __device__ constexpr int threads_of(int W) { return 32 * (W == 1 ? kRowWarps : W); }
 
 struct Forward {
     int64_t R, D, ldx, ldy;
@@ -48,61 +52,97 @@ struct Backward {
     float* part;  // [blocks][2][D]
 };
 
-// E entries a thread in vectors of V, W warps a row.
-template <typename X, int V, int E, int W>
-__global__ void __launch_bounds__(32 * (W == 1 ? kRowWarps : W))
+// E entries a thread in vectors of V, W warps a row, RB rows at a time; the rows after
+// them are on their way while these are computed.  Few threads with many registers
+// hold the weights too: read for every row, from L1, they kept the load-store unit
+// busy for most of a row's time (16384 x 4096 bf16: 56 us, with them in registers and
+// two rows at a time 48; 2 x the threads and half the registers 56).
+template <typename X, int V, int E, int W, int RB>
+__global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threads_of(W) : 1)
     forge_layer_norm_kernel(const X* __restrict__ x, const Forward p)
 {
     constexpr int NV = E / V;
-    __shared__ float sh[2][W];
-    const int rows = W == 1 ? kRowWarps : 1;
+    __shared__ float sh[2][W * RB];
+    const int teams = W == 1 ? kRowWarps : 1;
     const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + (W == 1 ? threadIdx.x >> 5 : 0);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams * RB;
     const float inv = 1.0f / static_cast<float>(p.D);
-    for (int64_t r = first; r < p.R; r += static_cast<int64_t>(gridDim.x) * rows) {
-        const X* row = x + r * p.ldx;
-        Packed<X, V> raw[NV];
+    int64_t r = (static_cast<int64_t>(blockIdx.x) * teams + (W == 1 ? threadIdx.x >> 5 : 0)) * RB;
+    Packed<X, V> next[RB][NV];
+    auto load = [&](int64_t r) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * W * 32 + t) * V;
-            raw[i] = c < p.D ? load_packed<X, V>(row + c) : zero_packed<X, V>();
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * W * 32 + t) * V;
+                next[k][i] = c < p.D && r + k < p.R ? load_packed<X, V>(x + (r + k) * p.ldx + c)
+                                                    : zero_packed<X, V>();
+            }
+    };
+    load(r);
+    constexpr bool kHold = W < 32;  // (1024 threads have 64 registers each)
+    Packed<float, V> w[NV], b[NV];
+    auto load_weights = [&](int i) {
+        const int c = (i * W * 32 + t) * V;
+        w[i] = c < p.D ? load_packed<float, V>(p.weight + c) : zero_packed<float, V>();
+        b[i] = c < p.D && p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (kHold) load_weights(i);
+    for (; r < p.R; r += step) {
+        float d[RB][E];
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[k][i] = entry(next[k][i / V], i % V);
+        if (r + step < p.R) load(r + step);
+        float mu[RB], rstd[RB];
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+            mu[k] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) mu[k] += d[k][i];
         }
-        float s[1] = {0.0f};
+        block_sums<W>(mu, sh[0]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int k = 0; k < RB; ++k) {
+            mu[k] *= inv;
+            rstd[k] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[0] += entry(raw[i], j);
-        block_sums<W>(s, sh[0]);
-        const float mu = s[0] * inv;
-        float q[1] = {0.0f};
+            for (int i = 0; i < NV; ++i) {
+                if ((i * W * 32 + t) * V < p.D) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if ((i * W * 32 + t) * V < p.D) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = entry(raw[i], j) - mu;
-                    q[0] = fmaf(d, d, q[0]);
+                    for (int j = 0; j < V; ++j) {
+                        d[k][i * V + j] -= mu[k];
+                        rstd[k] = fmaf(d[k][i * V + j], d[k][i * V + j], rstd[k]);
+                    }
                 }
             }
         }
-        block_sums<W>(q, sh[1]);
-        const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, p.eps));
-        if (t == 0) {
-            if (p.mean) p.mean[r] = mu;
-            if (p.rstd) p.rstd[r] = rstd;
+        block_sums<W>(rstd, sh[1]);
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+            rstd[k] = 1.0f / sqrtf(fmaf(rstd[k], inv, p.eps));
+            if (t == 0 && r + k < p.R) {
+                if (p.mean) p.mean[r + k] = mu[k];
+                if (p.rstd) p.rstd[r + k] = rstd[k];
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * W * 32 + t) * V;
             if (c < p.D) {
-                const Packed<float, V> w = load_packed<float, V>(p.weight + c);
-                const Packed<float, V> b =
-                    p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
-                float v[V];
+                if (!kHold) load_weights(i);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[j] = fmaf((entry(raw[i], j) - mu) * rstd, entry(w, j), entry(b, j));
-                store_as(p.y, p.y_f32, r * p.ldy + c, v);
+                for (int k = 0; k < RB; ++k) {
+                    if (r + k >= p.R) break;
+                    float v[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        v[j] = fmaf(d[k][i * V + j] * rstd[k], entry(w[i], j), entry(b[i], j));
+                    store_as(p.y, p.y_f32, (r + k) * p.ldy + c, v);
+                }
             }
         }
     }
@@ -156,55 +196,68 @@ __global__ void __launch_bounds__(kLongThreads)
     }
 }
 
+// E entries a thread in vectors of V, W warps a row; the next row is on its way while
+// this one is computed.  The weights lie in shared memory, a thread's vectors of
+// four apart by the block, so that no two lanes meet in a bank.
 template <typename G, typename X, int V, int E, int W>
-__global__ void __launch_bounds__(32 * (W == 1 ? kRowWarps : W))
+__global__ void __launch_bounds__(threads_of(W), kThreadsAtWork / threads_of(W))
     forge_layer_norm_grad_kernel(const G* __restrict__ dy, const X* __restrict__ x,
                                  const Backward p)
 {
     constexpr int NV = E / V;
     __shared__ float sh[2][2 * W];
-    const int rows = W == 1 ? kRowWarps : 1;
+    __shared__ float4 weight[E / 4][32 * W];
+    const int teams = W == 1 ? kRowWarps : 1;
     const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + (W == 1 ? threadIdx.x >> 5 : 0);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t r = static_cast<int64_t>(blockIdx.x) * teams + (W == 1 ? threadIdx.x >> 5 : 0);
     const float inv = 1.0f / static_cast<float>(p.D);
-    float w[E], dw[E], db[E];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * W * 32 + t) * V;
-        const Packed<float, V> raw =
-            c < p.D ? load_packed<float, V>(p.weight + c) : zero_packed<float, V>();
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[i * V + j] = entry(raw, j);
-            dw[i * V + j] = db[i * V + j] = 0.0f;
-        }
-    }
-    int turn = 0;
-    for (int64_t r = first; r < p.R; r += static_cast<int64_t>(gridDim.x) * rows, turn ^= 1) {
-        const G* grow = dy + r * p.ldg;
-        const X* xrow = x + r * p.ldx;
-        Packed<G, V> graw[NV];
-        Packed<X, V> xraw[NV];
+    Packed<G, V> gnext[NV];
+    Packed<X, V> xnext[NV];
+    float mu = 0.0f, rstd = 0.0f;
+    auto load = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * W * 32 + t) * V;
-            graw[i] = c < p.D ? load_packed<G, V>(grow + c) : zero_packed<G, V>();
-            xraw[i] = c < p.D ? load_packed<X, V>(xrow + c) : zero_packed<X, V>();
+            gnext[i] = c < p.D ? load_packed<G, V>(dy + r * p.ldg + c) : zero_packed<G, V>();
+            xnext[i] = c < p.D ? load_packed<X, V>(x + r * p.ldx + c) : zero_packed<X, V>();
         }
-        const float mu = p.mean[r], rstd = p.rstd[r];
+        mu = __ldg(p.mean + r);
+        rstd = __ldg(p.rstd + r);
+    };
+    if (r < p.R) load(r);
+    if (W > 1 || threadIdx.x < 32) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = (i / V * W * 32 + t) * V + i % V;
+            reinterpret_cast<float*>(&weight[i / 4][t])[i % 4] = c < p.D ? p.weight[c] : 0.0f;
+        }
+    }
+    __syncthreads();
+    float dw[E], db[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+    int turn = 0;
+    for (; r < p.R; r += step, turn ^= 1) {
+        float g[E], xh[E];
         float s[2] = {0.0f, 0.0f};  // of g and of g xh (columns past D have dy = 0)
+        const float scale = rstd;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < E; i += 4) {
+            const float4 w4 = weight[i / 4][t];
+            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = entry(graw[i], j);
-                const float xh = (entry(xraw[i], j) - mu) * rstd;
-                const float g = d * w[i * V + j];
-                s[0] += g;
-                s[1] = fmaf(g, xh, s[1]);
-                dw[i * V + j] = fmaf(d, xh, dw[i * V + j]);
-                db[i * V + j] += d;
+            for (int j = 0; j < 4; ++j) {
+                const float d = entry(gnext[(i + j) / V], (i + j) % V);
+                xh[i + j] = (entry(xnext[(i + j) / V], (i + j) % V) - mu) * rstd;
+                g[i + j] = d * w[j];
+                s[0] += g[i + j];
+                s[1] = fmaf(g[i + j], xh[i + j], s[1]);
+                dw[i + j] = fmaf(d, xh[i + j], dw[i + j]);
+                db[i + j] += d;
             }
+        }
+        if (r + step < p.R) load(r + step);
         block_sums<W>(s, sh[turn]);
         const float a = s[0] * inv, b = s[1] * inv;
 #pragma unroll
@@ -213,10 +266,8 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kRowWarps : W))
             if (c < p.D) {
                 float v[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xh = (entry(xraw[i], j) - mu) * rstd;
-                    v[j] = rstd * (fmaf(entry(graw[i], j), w[i * V + j], -a) - xh * b);
-                }
+                for (int j = 0; j < V; ++j)
+                    v[j] = scale * (g[i * V + j] - a - xh[i * V + j] * b);
                 store_as(p.dx, p.dx_f32, r * p.ldo + c, v);
             }
         }
@@ -323,8 +374,8 @@ __global__ void __launch_bounds__(32 * kLongWarps)
     part[p.D + c] = db;
 }
 
-// The sum of the blocks' parts, 32 columns a block, its warps every eighth part.
-constexpr int kFoldWarps = 8;
+// The sum of the blocks' parts, 32 columns a block, its warps every 32nd part.
+constexpr int kFoldWarps = 32;
 __global__ void __launch_bounds__(32 * kFoldWarps)
     forge_layer_norm_fold_kernel(const float* part, int32_t parts, int64_t D, float* dweight,
                                  float* dbias, int32_t accumulate)
@@ -374,63 +425,67 @@ template <typename X, int V>
 void forward(const X* x, const Forward& p, int sms, cudaStream_t s)
 {
     const int64_t D = p.D;
-    auto go = [&](auto kernel, int W) {
-        const int rows = W == 1 ? kRowWarps : 1, threads = 32 * (W == 1 ? kRowWarps : W);
-        kernel<<<blocks_for(p.R, rows, static_cast<int64_t>(sms) * (2048 / threads)), threads, 0,
-                 s>>>(x, p);
+    auto go = [&](auto kernel, int W, int RB) {
+        const int teams = W == 1 ? kRowWarps : 1, threads = threads_of(W);
+        const int64_t at_work = W < 32 ? kThreadsAtWork / threads : 1;
+        kernel<<<blocks_for(p.R, teams * RB, sms * at_work), threads, 0, s>>>(x, p);
     };
     if (D <= 256)
-        go(forge_layer_norm_kernel<X, V, 8, 1>, 1);
+        go(forge_layer_norm_kernel<X, V, 8, 1, 4>, 1, 4);
     else if (D <= 512)
-        go(forge_layer_norm_kernel<X, V, 16, 1>, 1);
+        go(forge_layer_norm_kernel<X, V, 16, 1, 2>, 1, 2);
     else if (D <= 1024)
-        go(forge_layer_norm_kernel<X, V, 16, 2>, 2);
+        go(forge_layer_norm_kernel<X, V, 16, 2, 2>, 2, 2);
     else if (D <= 2048)
-        go(forge_layer_norm_kernel<X, V, 16, 4>, 4);
+        go(forge_layer_norm_kernel<X, V, 16, 4, 2>, 4, 2);
     else if (D <= 4096)
-        go(forge_layer_norm_kernel<X, V, 16, 8>, 8);
+        go(forge_layer_norm_kernel<X, V, 16, 8, 2>, 8, 2);
     else if (D <= 8192)
-        go(forge_layer_norm_kernel<X, V, 16, 16>, 16);
+        go(forge_layer_norm_kernel<X, V, 16, 16, 2>, 16, 2);
     else if (D <= kMaxForward)
-        go(forge_layer_norm_kernel<X, V, 16, 32>, 32);
+        go(forge_layer_norm_kernel<X, V, 16, 32, 1>, 32, 1);
     else
         forge_layer_norm_long_kernel<X, V>
             <<<blocks_for(p.R, 1, 2LL * sms), kLongThreads, 0, s>>>(x, p);
 }
 
-// The rows in registers; returns the number of parts of dw and db.
-template <typename G, typename X, int V>
+// The rows in registers; returns the number of parts of dw and db: a block has two rows
+// at least, so that few rows leave few parts to add.
+template <typename G, typename X, int V, int E>
 int backward(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s)
 {
     const int64_t D = p.D;
     auto go = [&](auto kernel, int W) {
-        const int rows = W == 1 ? kRowWarps : 1, threads = 32 * (W == 1 ? kRowWarps : W);
-        const int blocks = blocks_for(p.R, rows, static_cast<int64_t>(sms) * (512 / threads < 1 ? 1 : 512 / threads));
+        const int teams = W == 1 ? kRowWarps : 1, threads = threads_of(W);
+        const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * kThreadsAtWork / threads);
         kernel<<<blocks, threads, 0, s>>>(dy, x, p);
         return blocks;
     };
     if (D <= 256) return go(forge_layer_norm_grad_kernel<G, X, V, 8, 1>, 1);
-    if (D <= 512) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 1>, 1);
-    if (D <= 1024) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 2>, 2);
-    if (D <= 2048) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 4>, 4);
-    if (D <= 4096) return go(forge_layer_norm_grad_kernel<G, X, V, 16, 8>, 8);
+    if (D <= 512) return go(forge_layer_norm_grad_kernel<G, X, V, E, 16 / E>, 16 / E);
+    if (D <= 1024) return go(forge_layer_norm_grad_kernel<G, X, V, E, 32 / E>, 32 / E);
+    if (D <= 2048) return go(forge_layer_norm_grad_kernel<G, X, V, E, 64 / E>, 64 / E);
+    if (D <= 4096) return go(forge_layer_norm_grad_kernel<G, X, V, E, 128 / E>, 128 / E);
     return go(forge_layer_norm_grad_kernel<G, X, V, 16, 16>, 16);
 }
 
 // Most parts that backward() or the column kernel writes.
 int64_t most_parts(int64_t R, int64_t D, int sms)
 {
-    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * 8;
+    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * (kThreadsAtWork / 64);
     return R < most ? R : most;
 }
 
 template <typename G, typename X>
 int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cudaStream_t s)
 {
-    if (p.D <= kMaxBackward)
-        return V == 8   ? backward<G, X, 8>(dy, x, p, sms, s)
-               : V == 4 ? backward<G, X, 4>(dy, x, p, sms, s)
-                        : backward<G, X, 1>(dy, x, p, sms, s);
+    if (p.D <= kMaxBackward) {
+        if constexpr (sizeof(G) == 2 && sizeof(X) == 2) {
+            if (V == 8) return backward<G, X, 8, 16>(dy, x, p, sms, s);
+        }
+        return V == 4 ? backward<G, X, 4, 8>(dy, x, p, sms, s)
+                      : backward<G, X, 1, 8>(dy, x, p, sms, s);
+    }
     const int64_t slabs = (p.D + 32 * kLongWarps - 1) / (32 * kLongWarps);
     const int parts = static_cast<int>(most_parts(p.R, p.D, sms));
     forge_layer_norm_columns_kernel<G, X>
