@@ -120,6 +120,29 @@ def test_codes_at_the_ends_of_the_range(cuda_device, br):
     check_codes(x, br)
 
 
+@gpu
+@pytest.mark.parametrize("br", [1, 128])
+@pytest.mark.parametrize("power", [-100, -40, -7, 0, 3, 60, 100])
+def test_codes_next_to_the_borders(cuda_device, br, power):
+    """Entries a few fp32 steps around s times each border between two codes (and
+    around the codes themselves), for scales of any mantissa: a quotient that is off by
+    one step shows here."""
+    g = torch.Generator().manual_seed(power + 200)
+    codes = torch.arange(127, dtype=torch.uint8).view(F8).float()
+    border = torch.cat([(codes[1:] + codes[:-1]) / 2, codes])
+    R = 512
+    amax = (1 + torch.rand(R, 1, generator=g)) * 2.0 ** power
+    if br == 128:
+        amax = amax[::128].repeat_interleave(128, 0)
+    s = amax / torch.tensor(448.0)
+    pick = border[torch.randint(0, border.numel(), (R, 256), generator=g)]
+    x = (pick * s).view(torch.int32) + torch.randint(-3, 4, (R, 256), generator=g, dtype=torch.int32)
+    x = x.clamp(min=0).view(torch.float32)
+    x = torch.minimum(x, amax) * (1 - 2 * torch.randint(0, 2, x.shape, generator=g))
+    x[:, ::128] = amax
+    check_codes(x.cuda(), br)
+
+
 def operands(T, N, M, transpose, E=None, seed=0):
     K = M if transpose else N
     A, sA = quantize(values(T, K, "f32", seed), 1)

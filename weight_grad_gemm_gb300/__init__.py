@@ -358,12 +358,15 @@ def forge_owner_sgdm(G, W, mom, *, lr, momentum, wd, stream=None):
 _codes = {}  # torch dtype -> forge_dtype, filled on first use
 
 
+def _all_codes():
+    import torch
+    _codes.update({torch.bfloat16: FORGE_BF16, torch.float32: FORGE_F32,
+                   torch.int32: FORGE_I32, torch.int64: FORGE_I64})
+    return _codes
+
+
 def _code(t, allowed, what) -> int:
-    if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: FORGE_BF16, torch.float32: FORGE_F32,
-                       torch.int32: FORGE_I32, torch.int64: FORGE_I64})
-    code = _codes.get(t.dtype)
+    code = (_codes or _all_codes()).get(t.dtype)
     if code not in allowed:
         raise TypeError(f"{what}, got {t.dtype}")
     return code
@@ -395,6 +398,9 @@ def _vector(t, n, what):
     """Pointer of an fp32 tensor of n elements, or None."""
     if t is None:
         return None
+    if (_codes or _all_codes()).get(t.dtype) == FORGE_F32 and t.numel() == n and t.is_cuda and \
+            t.is_contiguous():
+        return t.data_ptr()
     if t.numel() != n or _float_code(t) != FORGE_F32:
         raise ValueError(f"{what} must be float32 with {n} elements")
     return _ptr(t)
@@ -565,6 +571,9 @@ def _ints(t, n, what):
     """Pointer of an int32 tensor of n elements, or None."""
     if t is None:
         return None
+    if (_codes or _all_codes()).get(t.dtype) == FORGE_I32 and t.numel() == n and t.is_cuda and \
+            t.is_contiguous():
+        return t.data_ptr()
     if t.numel() != n or _id_code(t) != FORGE_I32:
         raise ValueError(f"{what} must be int32 with {n} elements")
     return _ptr(t)

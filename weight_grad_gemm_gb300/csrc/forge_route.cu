@@ -12,15 +12,15 @@
 //   dz = p (q - sum_e p q),   a_te = gw_tj where e is choice j, or normalised
 //   (gw_tj - sum_i gw_ti w_ti) / S_t with S_t the sum of the chosen p.
 //
-// Three launches.  Tokens: a group of lanes a token (each lane up to eight,
-// sixteen or thirty-two neighbouring experts in registers), k rounds of the
-// group's maximum; per block of tokens the counts and the sums of p.  Scan: a
-// warp an expert over the blocks.  Place: a choice's slot is its expert's
-// offset, plus the earlier blocks' count, plus the earlier tokens of its own
-// block, which 32-bit masks (one bit a token, a token chooses an expert at
-// most once) count with popc.  No atomics: slots are in token order and sums in
-// a fixed one, so that results are bitwise the same from run to run.  Batches
-// of one block's tokens take one launch.
+// Tokens: a group of lanes a token (each lane up to eight, sixteen or thirty-two
+// neighbouring experts in registers), the k largest, and per block of tokens the
+// counts, the sums of p and each choice's place among the block's choices of its
+// expert: 32-bit masks (one bit a token, a token chooses an expert at most once) are
+// counted with popc.  Scan: prefix sums over the blocks.  Place: a choice's slot is its
+// expert's offset, the earlier blocks' count and its place in its own.  Few blocks
+// scan in the place kernel; batches of one block's tokens take one launch.  No
+// atomics: slots are in token order and sums in a fixed one, so that results are
+// bitwise the same from run to run.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,36 +42,49 @@ constexpr int kMaxTop = 32;
 constexpr int kMostChoices = 2048;   // tokens of a block x k
 constexpr int kMostMasks = 4096;     // words of 32 tokens of a block x E
 constexpr int kMostWords = 8;
+constexpr int kFewCounts = 4096;     // blocks x E that every place block scans by itself
 
 struct Args {
     int64_t T, ld;
     int32_t E, k, words;  // words: a block's tokens / 32
-    bool normalize;
+    bool normalize, vec;  // vec: rows of logits in 16-byte loads
     int32_t* experts;
     float* weights;
     int32_t *counts, *offsets, *slots, *rows, *live;
     float* loss;
-    // scratch: [E + 1][blocks] counts (the last row: tokens that count), [E][blocks]
-    // sums of p, then the totals of both
+    // scratch: [blocks][E + 1] counts (the last column: tokens that count), [blocks][E]
+    // sums of p, the totals of both, and the choices' places in their blocks
     int32_t blocks;
     int32_t* part;
     float* psum;
     int32_t* total;
     float* ptotal;
+    uint16_t* place;
 };
 
-// Logits as integers of the same order: equal values are equal (-0 as 0), NaN
-// is above all.
+// Logits as integers of the same order: equal values are equal (-0 as 0), a NaN without
+// its sign above all.  (One with its sign is below all: rows with a NaN sum take
+// any_key_of.)
 __device__ __forceinline__ int32_t key_of(float v)
 {
     const int32_t b = __float_as_int(v + 0.0f);
-    return v != v ? INT_MAX : (b < 0 ? b ^ 0x7FFFFFFF : b);
+    return b ^ (b >> 31 & 0x7FFFFFFF);
 }
+__device__ __forceinline__ int32_t any_key_of(float v) { return v != v ? INT_MAX : key_of(v); }
 __device__ __forceinline__ float value_of(int32_t key)
 {
     return __int_as_float(key < 0 ? key ^ 0x7FFFFFFF : key);
 }
 constexpr int32_t kNone = static_cast<int32_t>(0x807FFFFF);  // key_of(-inf)
+
+// exp(v - m) from c = -m log2 e.  (c's rounding is a factor that all of a row's have.)
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_from(float v, float c)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(v, kLog2e, c)));
+    return y;
+}
 
 template <int LANES>
 __device__ __forceinline__ int32_t lanes_max(int32_t v)
@@ -85,10 +98,24 @@ __device__ __forceinline__ int32_t lanes_max(int32_t v)
     }
 }
 
-template <typename X>
-__device__ __forceinline__ float load1(const X* p)
+// EPL neighbouring logits of a row from x on, -inf past E (or everywhere: !in).
+template <typename X, int EPL>
+__device__ __forceinline__ void load_logits(float (&v)[EPL], const X* row, int x, int E, bool in,
+                                            bool vec)
 {
-    return entry(load_packed<X, 1>(p), 0);
+    constexpr int V = 16 / sizeof(X);
+    if (vec && in && x + EPL <= E) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += V) {
+            const Packed<X, V> q = load_packed<X, V>(row + x + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i + j] = entry(q, j);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            v[i] = in && x + i < E ? entry(load_packed<X, 1>(row + x + i), 0) : -INFINITY;
+    }
 }
 
 // The masks of a block's choices: bit i of mask[w][e] is set where token 32 w + i
@@ -143,46 +170,86 @@ __device__ __forceinline__ void write_totals(const Args& p, const int32_t* offs,
         if (e < p.E) p.counts[e] = count(e);
     }
     if (threadIdx.x < 32) {
-        double s = 0.0;
-        for (int e = threadIdx.x; e < p.E; e += 32) s += static_cast<double>(count(e)) * mass(e);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float n = live > 0 ? static_cast<float>(live) : 1.0f;
+        float s = 0.0f;
+        for (int e = threadIdx.x; e < p.E; e += 32)
+            s = fmaf(static_cast<float>(count(e)) / n, mass(e), s);
+        s = lanes_sum<32>(s);
         if (threadIdx.x == 0) {
-            const double n = live > 0 ? live : 1;
-            if (p.loss) *p.loss = static_cast<float>(s * p.E / (n * n * p.k));
+            if (p.loss) *p.loss = s * (static_cast<float>(p.E) / (static_cast<float>(p.k) * n));
             if (p.live) *p.live = live;
         }
     }
 }
 
-// Slots and packed rows of a block's choices; base[e]: the first slot of the
-// block's choices of e.  `first`: the block's first token.
-template <typename F>
-__device__ __forceinline__ void place(const Args& p, int64_t first, const uint32_t* mask,
-                                      int32_t* base, F choice)
+// The k largest of a row of E > 128 logits, a warp a row, each lane EPL of them as keys:
+// calls take(rank, key, expert) in one lane for each.  The k-th largest of the
+// lanes' maxima bounds them from below; the few keys that reach it are gathered, one
+// a lane, and ranked by comparing each with each.  Rows with more than 32 such keys
+// (equal ones) take k rounds of the maximum.
+template <int EPL, typename F>
+__device__ __forceinline__ void top_of_warp(int32_t (&key)[EPL], int k, uint64_t* list, F take)
 {
-    // base[w][e]: the earlier words' choices added
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        int32_t at = base[e];
-        for (int w = 0; w < p.words; ++w) {
-            base[w * p.E + e] = at;
-            at += __popc(mask[w * p.E + e]);
-        }
-    }
-    __syncthreads();
     const int lane = threadIdx.x & 31;
-    for (int w = threadIdx.x >> 5; w < p.words; w += kWarps) {
-        const int64_t t = first + 32 * w + lane;
-        if (t >= p.T) continue;
-        for (int j = 0; j < p.k; ++j) {
-            const int e = choice(32 * w + lane, j);
-            int32_t slot = -1;
-            if (e >= 0)
-                slot = base[w * p.E + e] + __popc(mask[w * p.E + e] & ((1u << lane) - 1));
-            if (p.slots) p.slots[t * p.k + j] = slot;
-            if (p.rows && slot >= 0) p.rows[slot] = static_cast<int32_t>(t);
+    int32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+    int32_t bound = kNone, left = best;
+    for (int n = 0; n < k;) {
+        bound = __reduce_max_sync(0xffffffffu, left);
+        if (bound == kNone) break;
+        const bool is = left == bound;
+        n += __popc(__ballot_sync(0xffffffffu, is));
+        left = is ? kNone : left;
+    }
+    bound = max(bound, kNone + 1);
+    int here = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) here += key[i] >= bound;
+    int at = here;  // the lanes' before this one's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+    }
+    const int found = __shfl_sync(0xffffffffu, at, 31);
+    at -= here;
+    if (here > 0 && found <= 32) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] >= bound)
+                list[at++] = static_cast<uint64_t>(static_cast<uint32_t>(key[i]) ^ 0x80000000u) << 32 |
+                             (0xFFFFFFFFu - (lane * EPL + i));  // larger: larger key, lower expert
+    }
+    __syncwarp();
+    if (found <= 32) {
+        const uint64_t mine = lane < found ? list[lane] : 0;
+        int rank = 0;
+        for (int j = 0; j < found; ++j) rank += list[j] > mine;
+        if (lane < found && rank < k)
+            take(rank, static_cast<int32_t>(static_cast<uint32_t>(mine >> 32) ^ 0x80000000u),
+                 static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(mine)));
+        if (lane >= found && lane < k) take(lane, kNone, -1);
+    } else {
+        for (int j = 0; j < k; ++j) {
+            const int32_t t = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t who = __ballot_sync(0xffffffffu, best == t);
+            if (lane == __ffs(who) - 1) {
+                int at = -1;
+                best = kNone;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const bool it = at < 0 && key[i] == t;
+                    at = it ? i : at;
+                    key[i] = it ? kNone : key[i];
+                    best = max(best, key[i]);
+                }
+                take(j, t, t > kNone ? lane * EPL + at : -1);
+            }
+            __syncwarp();
         }
     }
+    __syncwarp();
 }
 
 // LPR lanes a token, EPL experts a lane.  ONE: the call's only block.
@@ -192,13 +259,13 @@ __global__ void __launch_bounds__(kThreads)
 {
     extern __shared__ uint8_t smem[];
     const int C = 32 * p.words;
-    int32_t* chosen = reinterpret_cast<int32_t*>(smem);                 // [C][k]
+    uint64_t* lists = reinterpret_cast<uint64_t*>(smem);                // [warps][32]
+    int32_t* chosen = reinterpret_cast<int32_t*>(lists + kWarps * 32);  // [C][k]
     float* weight = reinterpret_cast<float*>(chosen + C * p.k);         // [C][k], before division
     float* inverse = weight + C * p.k;                                  // [C]
     uint32_t* mask = reinterpret_cast<uint32_t*>(inverse + C);          // [words][E]
     float* mass = reinterpret_cast<float*>(mask + p.words * p.E);       // [warps][E]
-    int32_t* base = reinterpret_cast<int32_t*>(mass + kWarps * p.E);    // ONE: [words][E]
-    int32_t* offs = base + p.words * p.E;                               // ONE: [E + 1]
+    int32_t* offs = reinterpret_cast<int32_t*>(mass + kWarps * p.E);    // ONE: [E + 1]
     __shared__ int32_t lives[kWarps];
 
     constexpr int G = kThreads / LPR;  // tokens at once
@@ -210,53 +277,76 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sums[i] = 0.0f;
     int32_t live_count = 0;
+    float ahead[EPL];
+    auto load = [&](int r) {
+        const bool in = r < C && first + r < p.T;
+        load_logits(ahead, logits + (in ? (first + r) * p.ld : 0), l * EPL, p.E, in, p.vec);
+    };
+    load(g);
     for (int r0 = 0; r0 < C; r0 += G) {
         const int r = r0 + g;
-        const bool in = r < C && first + r < p.T;
-        const X* row = logits + (in ? (first + r) * p.ld : 0);
-        int32_t key[EPL];
         float e[EPL];
-        int32_t best = kNone;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) e[i] = ahead[i];
+        if (r0 + G < C) load(r + G);
+        int32_t key[EPL];
+        int32_t best, top;
+        auto keys = [&](auto of) {
+            best = kNone;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                key[i] = of(e[i]);
+                best = max(best, key[i]);
+            }
+            top = lanes_max<LPR>(best);
+        };
+        keys(key_of);
+        const float c = top > kNone ? -value_of(top) * kLog2e : 0.0f;
+        float s = 0.0f, exps[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int x = l * EPL + i;
-            key[i] = in && x < p.E ? key_of(load1(row + x)) : kNone;
-            best = max(best, key[i]);
-        }
-        const int32_t top = lanes_max<LPR>(best);
-        const bool live = top > kNone;
-        live_count += live && l == 0;
-        const float m = live ? value_of(top) : 0.0f;
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            e[i] = __expf(value_of(key[i]) - m);
-            s += e[i];
+            exps[i] = exp_from(e[i], c);
+            s += exps[i];
         }
         s = lanes_sum<LPR>(s);
+        if (__any_sync(0xffffffffu, s != s)) keys(any_key_of);  // a NaN, or +inf
+        const bool live = top > kNone;
+        live_count += live && l == 0;
         const float inv = live ? 1.0f / s : 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) sums[i] = live ? fmaf(e[i], inv, sums[i]) : sums[i];
+        for (int i = 0; i < EPL; ++i) sums[i] = fmaf(exps[i], inv, sums[i]);
         float sum = 0.0f;  // of the chosen
-        for (int j = 0; j < p.k; ++j) {
-            const int32_t t = lanes_max<LPR>(best);
-            const uint32_t who = __ballot_sync(0xffffffffu, best == t) & group;
-            const bool mine = lane == __ffs(who) - 1;
-            const float w = t > kNone ? __expf(value_of(t) - m) : 0.0f;
-            sum += w;
-            if (mine) {
-                int at = -1;
-                best = kNone;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    const bool it = at < 0 && key[i] == t;
-                    at = it ? i : at;
-                    key[i] = it ? kNone : key[i];
-                    best = max(best, key[i]);
-                }
-                if (r < C) {
-                    chosen[r * p.k + j] = t > kNone ? l * EPL + at : -1;
+        if constexpr (LPR == 32) {
+            if (r < C) {  // (the same for the whole warp)
+                float mine = 0.0f;
+                top_of_warp(key, p.k, lists + warp * 32, [&](int j, int32_t t, int x) {
+                    const float w = t > kNone ? exp_from(value_of(t), c) : 0.0f;
+                    mine += w;
+                    chosen[r * p.k + j] = x;
                     weight[r * p.k + j] = w;
+                });
+                sum = lanes_sum<32>(mine);
+            }
+        } else {
+            for (int j = 0; j < p.k; ++j) {
+                const int32_t t = lanes_max<LPR>(best);
+                const uint32_t who = __ballot_sync(0xffffffffu, best == t) & group;
+                const float w = t > kNone ? exp_from(value_of(t), c) : 0.0f;
+                sum += w;
+                if (lane == __ffs(who) - 1) {
+                    int at = -1;
+                    best = kNone;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) {
+                        const bool it = at < 0 && key[i] == t;
+                        at = it ? i : at;
+                        key[i] = it ? kNone : key[i];
+                        best = max(best, key[i]);
+                    }
+                    if (r < C) {
+                        chosen[r * p.k + j] = t > kNone ? l * EPL + at : -1;
+                        weight[r * p.k + j] = w;
+                    }
                 }
             }
         }
@@ -269,8 +359,7 @@ __global__ void __launch_bounds__(kThreads)
         p.experts[first * p.k + i] = chosen[i];
         p.weights[first * p.k + i] = weight[i] * inverse[i / p.k];
     }
-    auto choice = [&](int t, int j) { return chosen[t * p.k + j]; };
-    make_masks(mask, p, choice);
+    make_masks(mask, p, [&](int t, int j) { return chosen[t * p.k + j]; });
     // sums of p: lanes with the same experts, then the warps in order
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -296,81 +385,159 @@ __global__ void __launch_bounds__(kThreads)
         for (int w = 0; w < kWarps; ++w) s += mass[w * p.E + x];
         return s;
     };
+    // a choice's place among the block's choices of its expert
+    auto place_of = [&](int i, int x) {
+        const int t = i / p.k;
+        int32_t n = __popc(mask[(t >> 5) * p.E + x] & ((1u << (t & 31)) - 1));
+        for (int w = 0; w < t >> 5; ++w) n += __popc(mask[w * p.E + x]);
+        return n;
+    };
     if constexpr (ONE) {
         make_offsets(offs, p.E, count_of);
         write_totals(p, offs, lives_here, count_of, mass_of);
-        for (int x = threadIdx.x; x < p.E; x += kThreads) base[x] = offs[x];
-        __syncthreads();
-        place(p, first, mask, base, choice);
+        for (int i = threadIdx.x; i < tokens * p.k; i += kThreads) {
+            const int x = chosen[i];
+            const int32_t slot = x >= 0 ? offs[x] + place_of(i, x) : -1;
+            if (p.slots) p.slots[i] = slot;
+            if (p.rows && slot >= 0) p.rows[slot] = i / p.k;
+        }
         if (p.rows)
             for (int64_t i = offs[p.E] + threadIdx.x; i < p.T * p.k; i += kThreads) p.rows[i] = -1;
     } else {
+        if (p.place)
+            for (int i = threadIdx.x; i < tokens * p.k; i += kThreads) {
+                const int x = chosen[i];
+                p.place[first * p.k + i] = static_cast<uint16_t>(x >= 0 ? place_of(i, x) : 0);
+            }
+        int32_t* part = p.part + static_cast<int64_t>(blockIdx.x) * (p.E + 1);
         for (int x = threadIdx.x; x < p.E; x += kThreads) {
-            p.part[static_cast<int64_t>(x) * p.blocks + blockIdx.x] = count_of(x);
-            p.psum[static_cast<int64_t>(x) * p.blocks + blockIdx.x] = mass_of(x);
+            part[x] = count_of(x);
+            p.psum[static_cast<int64_t>(blockIdx.x) * p.E + x] = mass_of(x);
         }
-        if (threadIdx.x == 0)
-            p.part[static_cast<int64_t>(p.E) * p.blocks + blockIdx.x] = lives_here;
+        if (threadIdx.x == 0) part[p.E] = lives_here;
         let_dependents_start();
     }
 }
 
-// A warp a row of part: its exclusive sums over the blocks in place, and the totals.
-__global__ void __launch_bounds__(kThreads) forge_route_scan_kernel(const Args p)
+// Eight columns of part and psum a block, 128 threads a column, each a run of blocks:
+// exclusive sums over the blocks in place, and the totals.
+constexpr int kScanColumns = 8, kScanRuns = 128;
+__global__ void __launch_bounds__(kScanColumns * kScanRuns) forge_route_scan_kernel(const Args p)
 {
+    __shared__ int32_t runs[kScanRuns][kScanColumns];
+    __shared__ float masses[kScanRuns][kScanColumns];
     await_prerequisites();
-    const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int col = threadIdx.x % kScanColumns, run = threadIdx.x / kScanColumns;
+    const int e = blockIdx.x * kScanColumns + col;
+    const int per = (p.blocks + kScanRuns - 1) / kScanRuns;
+    const int lo = run * per, hi = min(lo + per, p.blocks);
+    int32_t sum = 0;
+    float mass = 0.0f;
     if (e <= p.E) {
-        int32_t* part = p.part + static_cast<int64_t>(e) * p.blocks;
-        const float* psum = p.psum + static_cast<int64_t>(e) * p.blocks;
-        int32_t sum = 0;
-        float mass = 0.0f;
-        for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-            const int b = b0 + lane;
-            const int32_t n = b < p.blocks ? part[b] : 0;
-            if (e < p.E && b < p.blocks) mass += psum[b];
-            int32_t up = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
-                if (lane >= o) up += v;
-            }
-            if (b < p.blocks) part[b] = sum + up - n;
-            sum += __shfl_sync(0xffffffffu, up, 31);
+#pragma unroll 8
+        for (int b = lo; b < hi; ++b) {
+            sum += p.part[static_cast<int64_t>(b) * (p.E + 1) + e];
+            if (e < p.E) mass += p.psum[static_cast<int64_t>(b) * p.E + e];
         }
-        mass = lanes_sum<32>(mass);
-        if (lane == 0) {
-            p.total[e] = sum;
-            if (e < p.E) p.ptotal[e] = mass;
+    }
+    int32_t up = sum;
+    runs[run][col] = sum;
+    masses[run][col] = mass;
+    __syncthreads();
+    for (int o = 1; o < kScanRuns; o <<= 1) {
+        const int32_t v = run >= o ? runs[run - o][col] : 0;
+        const float m = run % (2 * o) == 0 ? masses[run + o][col] : 0.0f;
+        __syncthreads();
+        up += v;
+        mass += m;
+        runs[run][col] = up;
+        masses[run][col] = mass;
+        __syncthreads();
+    }
+    if (e <= p.E) {
+        if (run == kScanRuns - 1) p.total[e] = up;
+        if (run == 0 && e < p.E) p.ptotal[e] = mass;
+        int32_t at = up - sum;
+#pragma unroll 8
+        for (int b = lo; b < hi; ++b) {
+            int32_t* cell = p.part + static_cast<int64_t>(b) * (p.E + 1) + e;
+            const int32_t n = *cell;
+            *cell = at;
+            at += n;
         }
     }
     let_dependents_start();
 }
 
+// SCAN: from the blocks' own counts, else from their exclusive sums.
+template <bool SCAN>
 __global__ void __launch_bounds__(kThreads) forge_route_place_kernel(const Args p)
 {
     extern __shared__ uint8_t smem[];
-    uint32_t* mask = reinterpret_cast<uint32_t*>(smem);                  // [words][E]
-    int32_t* base = reinterpret_cast<int32_t*>(mask + p.words * p.E);    // [words][E]
-    int32_t* offs = base + p.words * p.E;                                // [E + 1]
+    int32_t* offs = reinterpret_cast<int32_t*>(smem);  // [E + 1]
+    int32_t* base = offs + p.E + 1;                    // [E + 1]: the earlier blocks' choices
+    int32_t* total = base + p.E + 1;                   // SCAN: [E + 1]
+    float* mass = reinterpret_cast<float*>(total + p.E + 1);  // SCAN, first block: [E]
     await_prerequisites();
-    make_offsets(offs, p.E, [&](int e) { return p.total[e]; });
-    if (blockIdx.x == 0)
-        write_totals(
-            p, offs, p.total[p.E], [&](int e) { return p.total[e]; },
-            [&](int e) { return p.ptotal[e]; });
-    if (!p.slots && !p.rows) return;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * 32 * p.words;
-    auto choice = [&](int t, int j) {
-        return first + t < p.T ? p.experts[(first + t) * p.k + j] : -1;
-    };
-    for (int e = threadIdx.x; e < p.E; e += kThreads)
-        base[e] = offs[e] + p.part[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
-    make_masks(mask, p, choice);
-    place(p, first, mask, base, choice);
+    const int E1 = p.E + 1, b = blockIdx.x;
+    if constexpr (SCAN) {
+        // `ways` threads an expert, every ways-th block each
+        __shared__ int32_t befores[kThreads], alls[kThreads];
+        __shared__ float masses[kThreads];
+        const int ways = E1 < kThreads ? kThreads / E1 : 1;
+        for (int e0 = 0; e0 <= p.E; e0 += kThreads) {
+            const int e = e0 + (ways > 1 ? threadIdx.x % E1 : threadIdx.x), way = ways > 1 ? threadIdx.x / E1 : 0;
+            int32_t before = 0, all = 0;
+            float s = 0.0f;
+            if (e <= p.E && way < ways) {
+#pragma unroll 4
+                for (int i = way; i < p.blocks; i += ways) {
+                    const int32_t n = p.part[i * E1 + e];
+                    all += n;
+                    before += i < b ? n : 0;
+                    if (b == 0 && e < p.E) s += p.psum[i * p.E + e];
+                }
+            }
+            befores[threadIdx.x] = before;
+            alls[threadIdx.x] = all;
+            masses[threadIdx.x] = s;
+            __syncthreads();
+            if (e <= p.E && way == 0) {
+                for (int k = 1; k < ways; ++k) {
+                    before += befores[threadIdx.x + k * E1];
+                    all += alls[threadIdx.x + k * E1];
+                    s += masses[threadIdx.x + k * E1];
+                }
+                base[e] = before;
+                total[e] = all;
+                if (e < p.E) mass[e] = s;
+            }
+            __syncthreads();
+        }
+    } else {
+        for (int e = threadIdx.x; e <= p.E; e += kThreads)
+            base[e] = p.part[static_cast<int64_t>(b) * E1 + e];
+    }
+    __syncthreads();
+    auto count = [&](int e) { return SCAN ? total[e] : p.total[e]; };
+    make_offsets(offs, p.E, count);
+    if (b == 0)
+        write_totals(p, offs, count(p.E), count,
+                     [&](int e) { return SCAN ? mass[e] : p.ptotal[e]; });
+    if (!p.place) return;
+    const int64_t first = static_cast<int64_t>(b) * 32 * p.words;
+    const int64_t left = p.T - first;
+    const int tokens = left < 32 * p.words ? static_cast<int>(left) : 32 * p.words;
+    for (int i = threadIdx.x; i < tokens * p.k; i += kThreads) {
+        const int64_t at = first * p.k + i;
+        const int e = p.experts[at];
+        const int32_t slot = e >= 0 ? offs[e] + base[e] + p.place[at] : -1;
+        if (p.slots) p.slots[at] = slot;
+        if (p.rows && slot >= 0) p.rows[slot] = static_cast<int32_t>(first + i / p.k);
+    }
     if (p.rows) {
         const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-        for (int64_t i = offs[p.E] + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+        for (int64_t i = offs[p.E] + static_cast<int64_t>(b) * kThreads + threadIdx.x;
              i < p.T * p.k; i += step)
             p.rows[i] = -1;
     }
@@ -383,67 +550,86 @@ struct GradArgs {
     const int32_t *experts, *counts, *live;
     const float *grad_weights, *grad_loss;
     void* dlogits;
-    bool f32;
+    bool f32, vec;  // vec: rows of logits and dlogits in vectors
 };
 
+__device__ __forceinline__ float nan_max(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// A token's row is written without its weights' part, p (c - sum p q); the lanes that
+// take its choices (each loads its expert's logit for itself) then write theirs over it.
 template <typename X, int LPR, int EPL>
 __global__ void __launch_bounds__(kThreads)
     forge_route_grad_kernel(const X* __restrict__ logits, const GradArgs p)
 {
     constexpr int G = kThreads / LPR;
-    const int l = threadIdx.x % LPR;
-    float c[EPL];  // the loss's q
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = 0.0f;
+    constexpr int kMost = LPR * EPL < kMaxTop ? LPR * EPL : kMaxTop;  // k <= E <= LPR EPL
+    constexpr int kPer = (kMost + LPR - 1) / LPR;                      // choices of a lane
+    const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
+    float f = 0.0f;  // of a count in the loss's q
     if (p.grad_loss) {
         const float n = fmaxf(1.0f, static_cast<float>(*p.live));
-        const float f = *p.grad_loss * static_cast<float>(p.E) / (static_cast<float>(p.k) * n);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (l * EPL + i < p.E) c[i] = f * (static_cast<float>(p.counts[l * EPL + i]) / n);
+        f = *p.grad_loss * static_cast<float>(p.E) / (static_cast<float>(p.k) * n) / n;
     }
+    float c[EPL];  // the loss's q
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        c[i] = p.grad_loss && l * EPL + i < p.E ? f * static_cast<float>(p.counts[l * EPL + i]) : 0.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+    // a token's row and its choices l, l + LPR, .. in this lane, the next token's on their
+    // way while this one's are computed
+    float ahead[EPL], gws_ahead[kPer];
+    int xs_ahead[kPer];
+    auto load = [&](int64_t t) {
+        const bool in = t < p.T;
+        load_logits(ahead, logits + (in ? t * p.ld : 0), l * EPL, p.E, in, p.vec);
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+            const int j = l + n * LPR;
+            const bool is = p.grad_weights && in && j < p.k;
+            xs_ahead[n] = is ? p.experts[t * p.k + j] : -1;
+            gws_ahead[n] = is ? p.grad_weights[t * p.k + j] : 0.0f;
+        }
+    };
+    load(static_cast<int64_t>(blockIdx.x) * G + g);
     for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * G; t0 < p.T; t0 += step) {
-        const int64_t t = t0 + threadIdx.x / LPR;
+        const int64_t t = t0 + g;
         const bool in = t < p.T;
         const X* row = logits + (in ? t * p.ld : 0);
-        float v[EPL];
-        float m = -INFINITY;
-        bool nan = false;
+        float v[EPL], gws[kPer], es[kPer];
+        int xs[kPer];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            v[i] = in && l * EPL + i < p.E ? load1(row + l * EPL + i) : -INFINITY;
-            nan |= v[i] != v[i];
-            m = fmaxf(m, v[i]);
+        for (int i = 0; i < EPL; ++i) v[i] = ahead[i];
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+            xs[n] = xs_ahead[n] < p.E ? xs_ahead[n] : -1;
+            gws[n] = gws_ahead[n];
+            es[n] = xs[n] >= 0 ? entry(load_packed<X, 1>(row + xs[n]), 0) : 0.0f;
         }
-        m = nan ? INFINITY : m;  // (every p of a row with a NaN is NaN, as with +inf)
+        load(t + step);
+        float m = v[0];
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m == -INFINITY ? 0.0f : m;
-        float gw[EPL];
-        uint32_t hit = 0;
+        for (int i = 1; i < EPL; ++i) m = nan_max(m, v[i]);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) gw[i] = 0.0f;
-        if (p.grad_weights && in) {
-            for (int j = 0; j < p.k; ++j) {
-                const int e = p.experts[t * p.k + j];
-                const float w = p.grad_weights[t * p.k + j];
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (e == l * EPL + i) {
-                        gw[i] = w;
-                        hit |= 1u << i;
-                    }
-            }
-        }
+        for (int o = LPR / 2; o > 0; o >>= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m == -INFINITY ? 0.0f : -m * kLog2e;  // (a NaN makes all p NaN)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // exp, exp c, chosen exp, chosen exp gw
 #pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+            if (xs[n] < 0) continue;
+            es[n] = exp_from(es[n], ref);
+            s[2] += es[n];
+            s[3] = fmaf(es[n], gws[n], s[3]);
+        }
+#pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            v[i] = __expf(v[i] - ref);
+            v[i] = exp_from(v[i], ref);
             s[0] += v[i];
             s[1] = fmaf(v[i], c[i], s[1]);
-            s[2] += hit >> i & 1 ? v[i] : 0.0f;
-            s[3] = fmaf(v[i], gw[i], s[3]);
         }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1)
@@ -456,18 +642,28 @@ __global__ void __launch_bounds__(kThreads)
         const float mean = norm ? s[3] / s[2] : 0.0f;
         const float over = norm ? s[0] / s[2] : 1.0f;
         const float pq = (s[1] + (p.normalize ? 0.0f : s[3])) * inv;
-        float out[EPL];
+        const int64_t at = t * p.ld_out;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float by = hit >> i & 1 ? (gw[i] - mean) * over : 0.0f;
-            out[i] = v[i] * inv * (c[i] + by - pq);
-        }
+        for (int i = 0; i < EPL; ++i) v[i] = v[i] * inv * (c[i] - pq);
+        __syncwarp();  // (in place: every lane has read the row)
         if (in) {
+            if (p.vec && l * EPL + EPL <= p.E) {
+                store_as(p.dlogits, p.f32, at + l * EPL, v);
+            } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const float one[1] = {out[i]};
-                if (l * EPL + i < p.E) store_as(p.dlogits, p.f32, t * p.ld_out + l * EPL + i, one);
+                for (int i = 0; i < EPL; ++i) {
+                    const float one[1] = {v[i]};
+                    if (l * EPL + i < p.E) store_as(p.dlogits, p.f32, at + l * EPL + i, one);
+                }
             }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+            if (xs[n] < 0) continue;
+            const float q = p.grad_loss ? f * static_cast<float>(p.counts[xs[n]]) : 0.0f;
+            const float one[1] = {es[n] * inv * (q + (gws[n] - mean) * over - pq)};
+            store_as(p.dlogits, p.f32, at + xs[n], one);
         }
     }
 }
@@ -495,14 +691,15 @@ cudaError_t by_experts(int E, F f)
     return f(Shape<32, 32>());
 }
 
-cudaError_t after(void (*kernel)(const Args), int grid, size_t smem, const Args& p, cudaStream_t s)
+cudaError_t after(void (*kernel)(const Args), int grid, int threads, size_t smem, const Args& p,
+                  cudaStream_t s)
 {
     cudaLaunchAttribute early[1];
     early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = early;
@@ -513,33 +710,41 @@ cudaError_t after(void (*kernel)(const Args), int grid, size_t smem, const Args&
 template <typename X>
 cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
 {
-    // a block's words: as many as leave every SM four blocks, within the room
+    // a block's words: the tokens that its groups take at once, and from there as many as
+    // leave every SM four blocks, within the room
     int most = kMostChoices / (32 * p.k);
     if (most > kMostMasks / p.E) most = kMostMasks / p.E;
     if (most > kMostWords) most = kMostWords;
     if (most < 1) most = 1;
     const int64_t all = (p.T + 31) / 32;
-    int64_t words = all <= most ? all : all / (4LL * sms);
+    int lanes = 1;  // a token
+    while (lanes < 32 && 8 * lanes < p.E) lanes *= 2;
+    const int64_t at_once = 8 / lanes;
+    int64_t words = all / (4LL * sms);
+    if (words < at_once) words = at_once;
+    // one block for up to four turns of its groups: there a second and third launch
+    // cost more than they save
+    if (all <= most && all * lanes <= 32) words = all;
     p.words = static_cast<int>(words < 1 ? 1 : (words > most ? most : words));
     const int64_t blocks = (all + p.words - 1) / p.words;
     if (blocks > INT32_MAX / 2) return cudaErrorInvalidValue;
     p.blocks = static_cast<int32_t>(blocks < 1 ? 1 : blocks);
-    const bool one = p.blocks == 1;
-    const size_t C = 32 * p.words;
-    const size_t tokens_smem =
-        4 * (2 * C * p.k + C + static_cast<size_t>(p.words) * p.E + static_cast<size_t>(kWarps) * p.E +
-             (one ? static_cast<size_t>(p.words) * p.E + p.E + 1 : 0));
-    const size_t place_smem = 4 * (2 * static_cast<size_t>(p.words) * p.E + p.E + 1);
+    const bool one = p.blocks == 1, place = p.slots || p.rows;
+    const size_t C = 32 * p.words, E = p.E;
+    const size_t tokens_smem = 8 * kWarps * 32 +
+                               4 * (2 * C * p.k + C + p.words * E + kWarps * E + (one ? E + 1 : 0));
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
     if (!one) {
-        const int64_t rows = p.E + 1, cells = rows * p.blocks;
-        e = scratch_alloc(&scratch, 4 * (2 * cells + 2 * rows), s);
+        const int64_t counts = (E + 1) * p.blocks, masses = E * p.blocks;
+        const int64_t choices = place ? p.T * p.k : 0;
+        e = scratch_alloc(&scratch, 4 * (counts + masses + 2 * (E + 1)) + 2 * choices, s);
         if (e != cudaSuccess) return e;
         p.part = static_cast<int32_t*>(scratch);
-        p.psum = reinterpret_cast<float*>(p.part + cells);
-        p.total = reinterpret_cast<int32_t*>(p.psum + cells);
-        p.ptotal = reinterpret_cast<float*>(p.total + rows);
+        p.psum = reinterpret_cast<float*>(p.part + counts);
+        p.total = reinterpret_cast<int32_t*>(p.psum + masses);
+        p.ptotal = reinterpret_cast<float*>(p.total + E + 1);
+        if (place) p.place = reinterpret_cast<uint16_t*>(p.ptotal + E + 1);
     }
     e = by_experts(p.E, [&](auto shape) {
         auto kernel = one ? forge_route_tokens_kernel<X, shape.lpr, shape.epl, true>
@@ -553,9 +758,16 @@ cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
         return cudaGetLastError();
     });
     if (e == cudaSuccess && !one) {
-        e = after(forge_route_scan_kernel, (p.E + kWarps) / kWarps, 0, p, s);
-        if (e == cudaSuccess)
-            e = after(forge_route_place_kernel, p.slots || p.rows ? p.blocks : 1, place_smem, p, s);
+        const int grid = place ? p.blocks : 1;
+        const size_t smem = 4 * 4 * (E + 1);
+        if (p.blocks * (E + 1) <= kFewCounts) {
+            e = after(forge_route_place_kernel<true>, grid, kThreads, smem, p, s);
+        } else {
+            e = after(forge_route_scan_kernel, static_cast<int>((E + kScanColumns) / kScanColumns),
+                      kScanColumns * kScanRuns, 0, p, s);
+            if (e == cudaSuccess)
+                e = after(forge_route_place_kernel<false>, grid, kThreads, smem, p, s);
+        }
     }
     if (scratch) {
         const cudaError_t fe = scratch_free(scratch, s);
@@ -608,6 +820,7 @@ extern "C" forge_status forge_moe_route(const void* logits, forge_dtype dtype, i
     p.E = E;
     p.k = k;
     p.normalize = normalize != 0;
+    p.vec = aligned(logits, 16) && ld * size_of(dtype) % 16 == 0;
     p.experts = experts;
     p.weights = weights;
     p.counts = counts;
@@ -656,7 +869,9 @@ extern "C" forge_status forge_moe_route_grad(const void* logits, forge_dtype dty
     const void* ptrs[] = {logits, experts, counts, live, grad_weights, grad_loss, dlogits};
     if ((st = device_resident(ptrs, 7)) != FORGE_OK) return st;
     const GradArgs p{T,      ld,   ld_out,       E,         k,       normalize != 0,
-                     experts, counts, live, grad_weights, grad_loss, dlogits, out_dtype == FORGE_F32};
+                     experts, counts, live, grad_weights, grad_loss, dlogits, out_dtype == FORGE_F32,
+                     aligned(logits, 16) && ld * es % 16 == 0 && aligned(dlogits, 16) &&
+                         ld_out * eo % 16 == 0};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto* x) {
         return by_experts(E, [&](auto shape) {
