@@ -82,9 +82,9 @@
  *                      do not depend on it
  *   FORGE_DGRAD_KERNEL = single | pair the dX kernel form (default: pairs
  *                      unless K fits one 128-token tile)
- *   FORGE_LINEAR_KERNEL = pair | single[n]  the e4m3 product's form: CTA pairs, or
- *                      one CTA a tile with n (1-8) CTAs sharing its contraction
- *                      (default: by the number of tiles)
+ *   FORGE_LINEAR_KERNEL = pair | few[n]  the e4m3 product's form: CTA pairs on 256
+ *                      tokens, or tiles of at most 128 tokens with n (1-8) CTAs
+ *                      sharing a tile's contraction (default: by the tokens and tiles)
  *   FORGE_WAIT_TIMEOUT_MS = ms         limit of every device-side wait
  *                      (read once per process; default 10000)
  *

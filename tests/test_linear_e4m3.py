@@ -172,7 +172,7 @@ SIZES = [(1, 1, 1), (1, 128, 128), (3, 130, 40), (16, 4096, 256), (17, 129, 257)
 
 
 @gpu
-@pytest.mark.parametrize("form", ["", "pair", "single", "single3", "single8"])
+@pytest.mark.parametrize("form", ["", "pair", "few", "few3", "few8"])
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("T,N,M", SIZES)
 def test_product(cuda_device, monkeypatch, T, N, M, transpose, form):
@@ -222,7 +222,7 @@ def groups(T, E, seed, slack=3):
 
 
 @gpu
-@pytest.mark.parametrize("form", ["", "pair", "single", "single3"])
+@pytest.mark.parametrize("form", ["", "pair", "few1", "few3"])
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("T,N,M,E", [(1, 64, 48, 3), (40, 200, 136, 1), (300, 130, 260, 5), (1500, 384, 260, 4), (900, 520, 512, 40),
                                      (700, 33, 65, 200), (1200, 128, 128, 1024)])

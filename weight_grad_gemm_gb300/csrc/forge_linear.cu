@@ -18,11 +18,14 @@
 // on the direction.
 //
 // Two forms.  Many tokens: CTA pairs (tcgen05.mma.cta_group::2) on tiles of 256
-// tokens x 256 outputs, persistent.  Few tokens: one CTA a tile of 128 x 128 and
-// a share of K; the CTAs of a cluster hold a tile's shares and add them through
-// distributed shared memory, in rank order, so that a weight is read by all
-// SMs however few its tiles are.  By experts, a tile lies within one expert's
-// rows; rows of A behind the expert's end reach only lanes that are not stored.
+// tokens x 256 outputs, persistent; tokens are the rows (lanes) of the accumulator.
+// Few tokens: the product is turned round, 128 outputs are the rows and 16 to 128
+// tokens the columns, so that the tensor core and the epilogue do no more than the
+// tokens ask for while the weight streams; the CTAs of a cluster share a tile's
+// contraction and add their sums through distributed shared memory, in rank order,
+// so that all SMs read the weight however few its tiles are.  By experts, a tile
+// lies within one expert's rows; rows of A behind the expert's end reach only rows or
+// columns of the accumulator that are not stored.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,6 +33,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include "forge.h"
 #include "forge_device.h"
@@ -48,28 +52,43 @@ constexpr int kStageB = 128 * kBlock;  // 128 outputs
 constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kSlots = 2;         // P_b in tensor memory
 constexpr int kStoreBytes = 2048;  // 32 rows x 64 bytes of Y on their way out
-constexpr int kMostSplit = 8;     // CTAs that share a tile's K
+constexpr int kMostSplit = 8;     // CTAs that share a tile's contraction
+constexpr int kFewThreads = 224;  // producer, MMA issuer, four epilogue warps, scales
+constexpr int kScaleRing = 4;     // chunks of four k-blocks' scales
 constexpr int kBand = 8;          // token tiles of a band of the tile walk
 
-template <bool PAIR>
-struct Form {
+// Tiles of the forms: tokens x outputs.
+struct Many {
+    static constexpr int rows = 256, cols = 256;
     static constexpr int stages = 6;
     static_assert(stages % kSlots == 0,
                   "a stage belongs to one issuer, which so waits for each of its rounds");
-    static constexpr int rows = PAIR ? 256 : 128;  // tokens of a tile
-    static constexpr int cols = PAIR ? 256 : 128;  // outputs of a tile
     static constexpr int warp_cols = cols / 2;
     static constexpr int tmem_cols = kSlots * cols;
     // registers a thread: 168 at launch, moved from the first warpgroup to the two
     // that hold the sums (3 x 168 = 56 + 2 x 224)
-    static constexpr int few = 56, many = 224;
+    static constexpr int few_regs = 56, many_regs = 224;
     static constexpr int bar_at = stages * kStageBytes;
-    static constexpr int stage_at = bar_at + 256;  // 2 KB for each epilogue warp's stores
-    static constexpr int table_at = stage_at + (PAIR ? kEpiWarps * kStoreBytes : 0);
+    static constexpr int store_at = bar_at + 256;
+    static constexpr int table_at = store_at + kEpiWarps * kStoreBytes;
     static constexpr int bytes(int E) { return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024; }
 };
-constexpr int kPitch = 132;  // floats between the rows of a share in shared memory
-static_assert(128 * kPitch * 4 <= Form<false>::bar_at, "a share fits the ring");
+template <int NT>
+struct Few {
+    static constexpr int rows = NT, cols = 128;
+    static constexpr int stages = NT <= 64 ? 4 : 6;
+    static constexpr int slots = NT <= 64 ? 4 : 2;
+    static constexpr int stage_bytes = kStageB + NT * kBlock;
+    static constexpr int tmem_cols = slots * NT;
+    static constexpr int ctas = NT <= 64 ? 2 : 1;  // an SM
+    static constexpr int pitch = 132;              // floats between the tokens of a share
+    static constexpr int scale_at = stages * stage_bytes;
+    static constexpr int bar_at = scale_at + kScaleRing * 4 * NT * 4;
+    static constexpr int table_at = bar_at + 256;
+    static constexpr int bytes(int E) { return table_at + (E > 0 ? 8 * (E + 1) : 0) + 1024; }
+    static_assert(NT * pitch * 4 <= scale_at, "a share fits the ring");
+    static_assert(ctas * (bytes(kMaxExperts) + 1024) <= 228 * 1024, "the CTAs of an SM");
+};
 
 struct LParams {
     int64_t T, K, O;       // tokens, contraction, outputs
@@ -91,11 +110,10 @@ struct Tile {
 // Tile t: dense calls walk bands of kBand token tiles, tokens fastest, so that
 // the CTAs at work share both operands' blocks in L2; by experts, one expert's
 // tiles after another's, each walked the same way.
-template <bool PAIR, bool GROUPED>
+template <typename F, bool GROUPED>
 __device__ __forceinline__ Tile tile_of(int32_t t, const LParams& p, const int32_t* offs,
                                         const int32_t* begin)
 {
-    using F = Form<PAIR>;
     Tile r;
     int32_t lo = 0, hi = static_cast<int32_t>(p.T);
     r.expert = 0;
@@ -138,11 +156,11 @@ __device__ __forceinline__ bool wait_often(uint64_t* bar, uint32_t parity,
 // Offsets into shared memory, checked, and the first tile of each expert;
 // false (and the status word set) where the offsets are not an ascending list
 // within the T rows.  All threads of the CTA.
-template <bool PAIR>
+template <typename F>
 __device__ bool group_table(const LParams& p, int32_t* offs, int32_t* begin)
 {
     int bad = 0;
-    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
         const int32_t v = p.offsets[e], before = e > 0 ? p.offsets[e - 1] : 0;
         offs[e] = v;
         bad |= v < before || v > p.T;
@@ -157,7 +175,7 @@ __device__ bool group_table(const LParams& p, int32_t* offs, int32_t* begin)
             const int e = e0 + threadIdx.x;
             int32_t n = 0;
             if (e < p.E)
-                n = (offs[e + 1] - offs[e] + Form<PAIR>::rows - 1) / Form<PAIR>::rows * p.tiles_o;
+                n = (offs[e + 1] - offs[e] + F::rows - 1) / F::rows * p.tiles_o;
             int32_t up = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -268,13 +286,13 @@ __device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int
     }
 }
 
-template <bool PAIR, bool W_MN, bool GROUPED>
+template <bool W_MN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1)
     forge_linear_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K]
                         const __grid_constant__ CUtensorMap tmW,  // W [E][N][M]
                         const LParams p)
 {
-    using F = Form<PAIR>;
+    using F = Many;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -291,11 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
-    const uint32_t split = PAIR ? 1 : gridDim.y;  // CTAs that share a tile (a cluster along y)
-    const bool leader = !PAIR || rank == 0;       // of the pair: issues its MMAs
+    const bool leader = rank == 0;  // of the pair: issues its MMAs
     if constexpr (GROUPED) {
         // every CTA of a cluster reads the same offsets and leaves alike
-        if (!group_table<PAIR>(p, offs, begin)) return;
+        if (!group_table<F>(p, offs, begin)) return;
     }
     int32_t total;
     if constexpr (GROUPED) {
@@ -303,11 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         total = static_cast<int32_t>((p.T + F::rows - 1) / F::rows) * p.tiles_o;
     }
-    const int32_t first = static_cast<int32_t>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
-    const int32_t step = static_cast<int32_t>(PAIR ? gridDim.x >> 1 : gridDim.x);
-    if (first >= total) return;  // (the whole cluster)
-    const int32_t k_lo = PAIR ? 0 : static_cast<int32_t>(int64_t{p.nk} * rank / split);
-    const int32_t k_hi = PAIR ? p.nk : static_cast<int32_t>(int64_t{p.nk} * (rank + 1) / split);
+    const int32_t first = static_cast<int32_t>(blockIdx.x >> 1);
+    const int32_t step = static_cast<int32_t>(gridDim.x >> 1);
+    if (first >= total) return;  // (the whole pair)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::stages; ++s) {
@@ -317,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < kSlots; ++b) {
             ptx::mbar_init(&drain[b], 1);
             ptx::mbar_init(&tfull[b], 1);
-            ptx::mbar_init(&tempty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
+            ptx::mbar_init(&tempty[b], 2 * kEpiWarps);
         }
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
@@ -327,37 +342,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tensormap(&tmW);
     }
     if (warp == 1) {
-        if constexpr (PAIR) {
-            ptx::tmem_alloc_pair(tmem_slot, F::tmem_cols);
-            ptx::tmem_relinquish_pair();
-        } else {
-            ptx::tmem_alloc(tmem_slot, F::tmem_cols);
-            ptx::tmem_relinquish();
-        }
+        ptx::tmem_alloc_pair(tmem_slot, F::tmem_cols);
+        ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
-    if constexpr (PAIR)
-        ptx::cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
-    else
-        __syncthreads();
+    ptx::cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp < kEpiWarp0) {
-        ptx::registers_down<F::few>();
+        ptx::registers_down<F::few_regs>();
         if (warp == 0) {
             // ---------------------------------------------------- TMA producer
             if (lane == 0) {
-                const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&full[0]), 0) : 0;
+                const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&full[0]), 0);
                 int s = 0;
                 uint32_t ph = 0;
                 uint32_t issued_mask = 0, last_parity = 0;
                 bool ok = true;
                 for (int32_t t = first; ok && t < total; t += step) {
-                    const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
-                    const int32_t ta = tl.t0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
-                    const int32_t ob = tl.o0 + (PAIR ? static_cast<int32_t>(rank) * 128 : 0);
-                    for (int32_t kb = k_lo; kb < k_hi; ++kb) {
+                    const Tile tl = tile_of<F, GROUPED>(t, p, offs, begin);
+                    const int32_t ta = tl.t0 + static_cast<int32_t>(rank) * 128;
+                    const int32_t ob = tl.o0 + static_cast<int32_t>(rank) * 128;
+                    for (int32_t kb = 0; kb < p.nk; ++kb) {
                         if (!wait_often(&empty[s], ph ^ 1u, abort_flag, p.w)) {
                             ok = false;
                             break;
@@ -365,16 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* sa = smem + s * kStageBytes;
                         const int32_t k = kb * kBlock;
                         const int32_t wx = W_MN ? ob : k, wy = W_MN ? k : ob;
-                        if constexpr (PAIR) {
-                            if (leader) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                            const uint32_t bar = full0 + s * 8;
-                            ptx::tma_load_2d_pair(sa, &tmA, bar, k, ta);
-                            ptx::tma_load_3d_pair(sa + kStageA, &tmW, bar, wx, wy, tl.expert);
-                        } else {
-                            ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
-                            ptx::tma_load_2d(sa, &tmA, &full[s], k, ta);
-                            ptx::tma_load_3d(sa + kStageA, &tmW, &full[s], wx, wy, tl.expert);
-                        }
+                        if (leader) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        const uint32_t bar = full0 + s * 8;
+                        ptx::tma_load_2d_pair(sa, &tmA, bar, k, ta);
+                        ptx::tma_load_3d_pair(sa + kStageA, &tmW, bar, wx, wy, tl.expert);
                         issued_mask |= 1u << s;
                         last_parity = (last_parity & ~(1u << s)) | (ph << s);
                         if (++s == F::stages) {
@@ -413,8 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::smem_desc_sw128(ring + kStageA, W_MN ? kStageB : 16, 1024);
                 const int b = warp - 1;
                 const uint32_t d_tmem = tmem_base + b * F::cols;
-                const int64_t blocks =
-                    int64_t{k_hi - k_lo} * ((total - first + step - 1) / step);
+                const int64_t blocks = int64_t{p.nk} * ((total - first + step - 1) / step);
                 int s = b;
                 uint32_t ph = 0, turn = 1;
                 bool ok = true;
@@ -430,21 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t bd = b_desc + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
-                        if constexpr (PAIR)
-                            ptx::umma_f8_pair(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
-                                              ks != 0 ? 1u : 0u);
-                        else
-                            ptx::umma_f8(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
-                                         ks != 0 ? 1u : 0u);
+                        ptx::umma_f8_pair(d_tmem, ad + ks * kStepA, bd + ks * kStepB, idesc,
+                                          ks != 0 ? 1u : 0u);
                     }
                     issued_any = true;
-                    if constexpr (PAIR) {
-                        ptx::umma_commit_pair(&tfull[b], 0x3);
-                        ptx::umma_commit_pair(&empty[s], 0x3);
-                    } else {
-                        ptx::umma_commit(&tfull[b]);
-                        ptx::umma_commit(&empty[s]);
-                    }
+                    ptx::umma_commit_pair(&tfull[b], 0x3);
+                    ptx::umma_commit_pair(&empty[s], 0x3);
                     s += kSlots;
                     if (s >= F::stages) {
                         s -= F::stages;
@@ -452,10 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok && issued_any) {
-                    if constexpr (PAIR)
-                        ptx::umma_commit_pair(&drain[b], 0x1);
-                    else
-                        ptx::umma_commit(&drain[b]);
+                    ptx::umma_commit_pair(&drain[b], 0x1);
                     const uint32_t a = ptx::smem_addr(&drain[b]);
                     const uint64_t tw = ptx::globaltimer_ns();
                     while (!ptx::mbar_try_wait(a, 0)) {
@@ -466,14 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------- epilogue
-        ptx::registers_up<F::many>();
+        ptx::registers_up<F::many_regs>();
         // Warp (q, g): TMEM lanes 32 q .. (tokens) x columns C g ..; a lane owns one
         // token row.
         constexpr int C = F::warp_cols;
         const int q = warp & 3;
         const int g = (warp - kEpiWarp0) >> 2;
-        const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_addr(&tempty[0]), 0) : 0;
-        const int32_t my_row = (PAIR ? static_cast<int32_t>(rank) * 128 : 0) + 32 * q + lane;
+        const uint32_t tempty0 = ptx::mapa_shared(ptx::smem_addr(&tempty[0]), 0);
+        const int32_t my_row = static_cast<int32_t>(rank) * 128 + 32 * q + lane;
         const int32_t my_col = C * g;
         const uint32_t my_tmem = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + C * g;
         uint32_t ct = 0;
@@ -481,11 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t row, row_end, c0;
         const float *sa, *sw;
         float na[4], nw[4];
-        const bool vec = p.sa_vec && k_lo % 4 == 0;
         // Scales four blocks ahead (their product is taken when they are needed, so that
         // nothing waits for the loads), a tile's first before the last one's stores.
         auto load_scales = [&](int32_t kb) {
-            if (vec && kb + 4 <= k_hi) {
+            if (p.sa_vec) {
                 const float4 v = load4_early(sa + kb);
                 na[0] = v.x;
                 na[1] = v.y;
@@ -494,33 +481,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    na[i] = load_early(sa + (kb + i < k_hi ? kb + i : k_hi - 1));
+                    na[i] = load_early(sa + min(kb + i, p.nk - 1));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                nw[i] = load_early(sw + (kb + i < k_hi ? kb + i : k_hi - 1) * p.sw_k);
+                nw[i] = load_early(sw + min(kb + i, p.nk - 1) * p.sw_k);
         };
         auto begin_tile = [&](int32_t t) {
-            const Tile tl = tile_of<PAIR, GROUPED>(t, p, offs, begin);
+            const Tile tl = tile_of<F, GROUPED>(t, p, offs, begin);
             row = int64_t{tl.t0} + my_row;
             row_end = tl.t_end;
             c0 = int64_t{tl.o0} + my_col;
             // (scales of rows and columns outside the call are read from its first)
             sa = p.sA + (row < row_end ? row : 0) * p.nk;
             sw = p.sW + tl.expert * p.sw_e + (c0 < p.O ? c0 / kBlock : 0) * p.sw_o;
-            load_scales(k_lo);
+            load_scales(0);
         };
         begin_tile(first);
         for (int32_t t = first; ok && t < total; t += step) {
             float acc[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = 0.0f;
-            for (int32_t k0 = k_lo; ok && k0 < k_hi; k0 += 4) {
+            for (int32_t k0 = 0; ok && k0 < p.nk; k0 += 4) {
                 float now[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) now[i] = na[i] * nw[i];
-                if (k0 + 4 < k_hi) load_scales(k0 + 4);
-                const int n = k_hi - k0 < 4 ? k_hi - k0 : 4;
+                if (k0 + 4 < p.nk) load_scales(k0 + 4);
+                const int n = min(4, p.nk - k0);
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++ct) {
                     const float f = i < 2 ? (i == 0 ? now[0] : now[1]) : (i == 2 ? now[2] : now[3]);
@@ -549,13 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load(0);
                     load(1);
                     wait();
-                    if constexpr (C == 128) {
-                        add(0);
-                        load(2);
-                        add(1);
-                        load(3);
-                        wait();
-                    }
+                    add(0);
+                    load(2);
+                    add(1);
+                    load(3);
+                    wait();
                     // this P_b is read: its issuer may fill the slot again
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -565,64 +550,303 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             ptx::mbar_arrive_cluster_unordered(tempty0 + 8 * b);
                     }
-                    add(C / 32 - 2);
-                    add(C / 32 - 1);
+                    add(2);
+                    add(3);
                 }
             }
             if (!ok) break;
-            if constexpr (PAIR) {
-                const int64_t r0 = row - lane, r_end = row_end, c = c0;
-                if (t + step < total) begin_tile(t + step);
-                store_tile(p, smem + F::stage_at + (warp - kEpiWarp0) * kStoreBytes, r0, r_end, c,
-                           acc, lane);
-            } else if (row < row_end) {
-                // this CTA's share into its ring (every copy and MMA of it is complete)
-                float* mine = reinterpret_cast<float*>(smem) + my_row * kPitch + my_col;
-#pragma unroll
-                for (int j = 0; j < C; j += 4)
-                    *reinterpret_cast<float4*>(mine + j) =
-                        make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-            }
+            const int64_t r0 = row - lane, r_end = row_end, c = c0;
+            if (t + step < total) begin_tile(t + step);
+            store_tile(p, smem + F::store_at + (warp - kEpiWarp0) * kStoreBytes, r0, r_end, c, acc,
+                       lane);
         }
     }
 
-    if constexpr (!PAIR) {
-        // the sum of the tile's shares, rows of it dealt to the cluster's threads
-        __syncthreads();
-        if (split > 1) ptx::cluster_sync();
-        if (*abort_flag == 0) {
-            const Tile tl = tile_of<PAIR, GROUPED>(first, p, offs, begin);
-            const int32_t left = tl.t_end - tl.t0;
-            const int32_t rows = left < F::rows ? left : F::rows;
-            const int32_t units = rows * (F::cols / 4);  // of four outputs
+    ptx::tc_fence_before();
+    ptx::cluster_sync();  // no CTA leaves while the other may still signal it
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, F::tmem_cols);
+    }
+}
+
+// The form for few tokens: a CTA has one tile of 128 outputs x NT tokens and blocks
+// k_lo to k_hi of its contraction; the CTAs of a cluster (along y) have the others.
+template <int NT, bool W_MN, bool GROUPED>
+__global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
+    forge_linear_few_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K], NT rows a box
+                            const __grid_constant__ CUtensorMap tmW,  // W [E][N][M]
+                            const LParams p)
+{
+    using F = Few<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::bar_at);
+    uint64_t* empty = full + F::stages;
+    uint64_t* tfull = empty + F::stages;
+    uint64_t* tempty = tfull + F::slots;
+    uint64_t* sfull = tempty + F::slots;
+    uint64_t* sempty = sfull + kScaleRing;
+    uint64_t* drain = sempty + kScaleRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* scales = reinterpret_cast<float*>(smem + F::scale_at);  // [ring][4][NT]
+    int32_t* offs = reinterpret_cast<int32_t*>(smem + F::table_at);
+    int32_t* begin = offs + p.E + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t split = gridDim.y;
+    int32_t total;
+    if constexpr (GROUPED) {
+        // every CTA of a cluster reads the same offsets and leaves alike
+        if (!group_table<F>(p, offs, begin)) return;
+        total = begin[p.E];
+    } else {
+        total = static_cast<int32_t>((p.T + F::rows - 1) / F::rows) * p.tiles_o;
+    }
+    if (static_cast<int32_t>(blockIdx.x) >= total) return;  // (the whole cluster)
+    const Tile tl = tile_of<F, GROUPED>(static_cast<int32_t>(blockIdx.x), p, offs, begin);
+    const int32_t k_lo = static_cast<int32_t>(int64_t{p.nk} * rank / split);
+    const int32_t n = static_cast<int32_t>(int64_t{p.nk} * (rank + 1) / split) - k_lo;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F::stages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < F::slots; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], 4);
+        }
+        for (int c = 0; c < kScaleRing; ++c) {
+            ptx::mbar_init(&sfull[c], 1);
+            ptx::mbar_init(&sempty[c], 4);
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmW);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, F::tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int64_t o = int64_t{tl.o0} + 32 * (warp & 3) + lane;  // an epilogue lane's output
+    float acc[NT];
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        if (lane == 0) {
+            bool ok = true;
+            int32_t i = 0;
+            for (; i < n; ++i) {
+                const int s = i % F::stages;
+                ok = wait_often(&empty[s], (i / F::stages & 1u) ^ 1u, abort_flag, p.w);
+                if (!ok) break;
+                ptx::mbar_arrive_expect_tx(&full[s], F::stage_bytes);
+                uint8_t* sw = smem + s * F::stage_bytes;
+                const int32_t k = (k_lo + i) * kBlock;
+                ptx::tma_load_3d(sw, &tmW, &full[s], W_MN ? tl.o0 : k, W_MN ? k : tl.o0, tl.expert);
+                ptx::tma_load_2d(sw + kStageB, &tmA, &full[s], k, tl.t0);
+            }
+            if (!ok) {
+                // wait (bounded) for the copies still in flight: the last ones issued
+                const uint64_t tw = ptx::globaltimer_ns();
+                for (int32_t c = max(0, i - F::stages); c < i; ++c) {
+                    const uint32_t a = ptx::smem_addr(&full[c % F::stages]);
+                    while (!ptx::mbar_try_wait(a, c / F::stages & 1u)) {
+                        if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns)
+                            break;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer (lane 0)
+        if (lane == 0) {
+            constexpr uint32_t idesc = ptx::make_idesc(0, 0, W_MN, false, 128, NT);
+            constexpr uint64_t kStepW = (W_MN ? 32 * 128 : 32) >> 4, kStepA = 32 >> 4;
             const uint32_t ring = ptx::smem_addr(smem);
-            for (int32_t u = static_cast<int32_t>(rank) * kThreads + threadIdx.x; u < units;
-                 u += static_cast<int32_t>(split) * kThreads) {
-                const int32_t r = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
+            const uint64_t w_desc = ptx::smem_desc_sw128(ring, W_MN ? kStageB : 16, 1024);
+            const uint64_t a_desc = ptx::smem_desc_sw128(ring + kStageB, 16, 1024);
+            bool ok = true;
+            bool issued_any = false;
+            for (int32_t i = 0; i < n; ++i) {
+                const int s = i % F::stages, b = i % F::slots;
+                ok = wait_often(&full[s], i / F::stages & 1u, abort_flag, p.w) &&
+                     wait_often(&tempty[b], (i / F::slots & 1u) ^ 1u, abort_flag, p.w);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t wd = w_desc + s * (F::stage_bytes >> 4);
+                const uint64_t ad = a_desc + s * (F::stage_bytes >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::umma_f8(tmem_base + b * NT, wd + ks * kStepW, ad + ks * kStepA, idesc,
+                                 ks != 0 ? 1u : 0u);
+                issued_any = true;
+                ptx::umma_commit(&tfull[b]);
+                ptx::umma_commit(&empty[s]);
+            }
+            if (!ok && issued_any) {
+                ptx::umma_commit(drain);
+                const uint32_t a = ptx::smem_addr(drain);
+                const uint64_t tw = ptx::globaltimer_ns();
+                while (!ptx::mbar_try_wait(a, 0)) {
+                    if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
+                }
+            }
+        }
+    } else if (warp < 6) {
+        // ---------------------------------------------------- epilogue
+        // Warp q: TMEM lanes 32 q .. (outputs); a lane owns one output's NT tokens.
+        const uint32_t mine = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+        bool ok = true;
+#pragma unroll 1
+        for (int32_t i = 0; i < n; ++i) {
+            const int b = i % F::slots, c = i / 4 % kScaleRing;
+            if (i % 4 == 0) ok = wait_often(&sfull[c], i / 4 / kScaleRing & 1u, abort_flag, p.w);
+            ok = ok && wait_often(&tfull[b], i / F::slots & 1u, abort_flag, p.w);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const float4* f = reinterpret_cast<const float4*>(scales + (c * 4 + i % 4) * NT);
+            const uint32_t from = mine + b * NT;
+            auto add = [&](const auto& r, int j0, int N) {
+#pragma unroll
+                for (int j = 0; j < N; j += 4) {
+                    const float4 q = f[(j0 + j) / 4];
+                    acc[j0 + j] = fmaf(__uint_as_float(r[j]), q.x, acc[j0 + j]);
+                    acc[j0 + j + 1] = fmaf(__uint_as_float(r[j + 1]), q.y, acc[j0 + j + 1]);
+                    acc[j0 + j + 2] = fmaf(__uint_as_float(r[j + 2]), q.z, acc[j0 + j + 2]);
+                    acc[j0 + j + 3] = fmaf(__uint_as_float(r[j + 3]), q.w, acc[j0 + j + 3]);
+                }
+            };
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&tempty[b]);
+            };
+            if constexpr (NT == 16) {
+                uint32_t r[16];
+                ptx::tmem_ld_32x32b_x16(from, r);
+                ptx::tmem_ld_wait_for(r);
+                release();
+                add(r, 0, 16);
+            } else {
+#pragma unroll
+                for (int h = 0; h < NT / 32; ++h) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(from + 32 * h, r);
+                    ptx::tmem_ld_wait_for(r);
+                    if (h == NT / 32 - 1) release();
+                    add(r, 32 * h, 32);
+                }
+            }
+            if (i % 4 == 3) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sempty[c]);
+            }
+        }
+        if (split == 1) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float one[1] = {acc[j]};
+                if (ok && tl.t0 + j < tl.t_end && o < p.O)
+                    store_as(p.Y, p.f32, (int64_t{tl.t0} + j) * p.O + o, one);
+            }
+        } else {
+            // this CTA's share into its ring: the last slot that it waited for was the last
+            // to be filled, so every copy into the ring and every MMA on it is complete
+            float* share = reinterpret_cast<float*>(smem) + 32 * (warp & 3) + lane;
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (tl.t0 + j < tl.t_end) share[j * F::pitch] = acc[j];
+            }
+        }
+    } else {
+        // ---------------------------------------------------- scales
+        // Of four blocks at a time, for each token the product of its scale and the
+        // weight's, up to four chunks ahead.
+        const float* sw = p.sW + tl.expert * p.sw_e + tl.o0 / kBlock * p.sw_o;
+        const int32_t last = k_lo + n - 1;
+        for (int32_t c = 0; c < (n + 3) / 4; ++c) {
+            const int32_t kb = k_lo + 4 * c;
+            float w[4], a[(NT + 31) / 32][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(sw + min(kb + i, last) * p.sw_k);
+#pragma unroll
+            for (int h = 0; h < (NT + 31) / 32; ++h) {
+                // (tokens outside the tile take the call's first scales)
+                const int64_t row = int64_t{tl.t0} + 32 * h + lane;
+                const float* at = p.sA + (row < tl.t_end ? row : 0) * p.nk;
+                if (p.sa_vec && kb % 4 == 0) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(at + kb));
+                    a[h][0] = v.x;
+                    a[h][1] = v.y;
+                    a[h][2] = v.z;
+                    a[h][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[h][i] = __ldg(at + min(kb + i, last));
+                }
+            }
+            const int r = c % kScaleRing;
+            const bool ok = wait_often(&sempty[r], (c / kScaleRing & 1u) ^ 1u, abort_flag, p.w);
+            if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+            for (int h = 0; h < (NT + 31) / 32; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (32 * h + lane < NT) scales[(r * 4 + i) * NT + 32 * h + lane] = a[h][i] * w[i];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sfull[r]);
+        }
+    }
+
+    __syncthreads();
+    if (split > 1) {
+        ptx::cluster_sync();  // every share of the tile is written
+        if (*abort_flag == 0) {
+            const int32_t tokens = min(NT, tl.t_end - tl.t0);
+            const int32_t units = tokens * (F::cols / 4);  // of four outputs
+            const uint32_t ring = ptx::smem_addr(smem);
+            for (int32_t u = static_cast<int32_t>(rank) * kFewThreads + threadIdx.x; u < units;
+                 u += static_cast<int32_t>(split) * kFewThreads) {
+                const int32_t j = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (uint32_t k = 0; k < split; ++k) {
-                    const uint32_t at = ring + (r * kPitch + c) * 4;
+                    const uint32_t at = ring + (j * F::pitch + c) * 4;
                     const float4 x = ptx::ld_cluster_f4(ptx::mapa_shared(at, k));
                     v[0] += x.x;
                     v[1] += x.y;
                     v[2] += x.z;
                     v[3] += x.w;
                 }
-                if (tl.o0 + c < p.O) store_row(p, int64_t{tl.t0} + r, int64_t{tl.o0} + c, v);
+                if (tl.o0 + c < p.O) store_row(p, int64_t{tl.t0} + j, int64_t{tl.o0} + c, v);
             }
         }
     }
     ptx::tc_fence_before();
-    if (PAIR || split > 1)
-        ptx::cluster_sync();  // no CTA leaves while another may still read or signal it
+    if (split > 1)
+        ptx::cluster_sync();  // no CTA leaves while another may still read its share
     else
         __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        if constexpr (PAIR)
-            ptx::tmem_dealloc_pair(tmem_base, F::tmem_cols);
-        else
-            ptx::tmem_dealloc(tmem_base, F::tmem_cols);
+        ptx::tmem_dealloc(tmem_base, F::tmem_cols);
     }
 }
 
@@ -631,16 +855,18 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 struct Launch {
     const CUtensorMap &a, &w;
     const LParams& p;
-    int sms;
-    int split;  // of the one-CTA form
+    int split;  // few tokens: CTAs that share a tile's contraction
     cudaStream_t stream;
 };
 
-template <bool PAIR, bool W_MN, bool GROUPED>
+// KERN, of the form F.  Pairs: as many as can be resident at once; else a cluster of
+// `split` CTAs for each tile.
+template <typename F, bool GROUPED, auto KERN>
 cudaError_t launch(const Launch& l)
 {
-    using F = Form<PAIR>;
-    auto kern = forge_linear_kernel<PAIR, W_MN, GROUPED>;
+    constexpr bool pairs = std::is_same<F, Many>::value;
+    constexpr int threads = pairs ? kThreads : kFewThreads;
+    auto kern = KERN;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -648,27 +874,24 @@ cudaError_t launch(const Launch& l)
     static_assert(most <= 227 * 1024, "ring and table within one CTA's shared memory");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
-    attr[0].val.clusterDim.y = PAIR ? 1 : l.split;
+    attr[0].val.clusterDim.x = pairs ? 2 : 1;
+    attr[0].val.clusterDim.y = pairs ? 1 : l.split;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = l.stream;
+    cfg.blockDim = dim3(threads);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    static int ready[64] = {0};  // per device: resident pairs, or 1
+    static int ready[64] = {0};  // per device (and kernel): resident pairs, or 1
     int& mc = ready[dev & 63];
     if (__atomic_load_n(&mc, __ATOMIC_ACQUIRE) == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         int n = 1;
-        if (PAIR) {
+        if (pairs) {
             cfg.gridDim = dim3(2);
             cfg.dynamicSmemBytes = most;
-            cfg.stream = nullptr;
             if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
             if (n < 1) return cudaErrorInvalidConfiguration;
-            cfg.stream = l.stream;
         }
         __atomic_store_n(&mc, n, __ATOMIC_RELEASE);
     }
@@ -678,38 +901,60 @@ cudaError_t launch(const Launch& l)
     const int64_t extra = GROUPED ? (l.p.E < l.p.T ? l.p.E : l.p.T) : 0;
     const int64_t total = (rows + extra) * l.p.tiles_o;
     if (total > INT32_MAX / 16) return cudaErrorInvalidValue;
-    if (PAIR)
+    if (pairs)
         cfg.gridDim = dim3(static_cast<unsigned>(2 * (total < mc ? total : mc)));
     else
         cfg.gridDim = dim3(static_cast<unsigned>(total), static_cast<unsigned>(l.split));
     cfg.dynamicSmemBytes = static_cast<size_t>(F::bytes(GROUPED ? l.p.E : 0));
+    cfg.stream = l.stream;
     return cudaLaunchKernelEx(&cfg, kern, l.a, l.w, l.p);
 }
 
-// The form, and the CTAs that share a tile's K.
+template <bool W_MN, bool GROUPED>
+cudaError_t launch_form(int tokens, const Launch& l)
+{
+    switch (tokens) {
+    case 16: return launch<Few<16>, GROUPED, forge_linear_few_kernel<16, W_MN, GROUPED>>(l);
+    case 32: return launch<Few<32>, GROUPED, forge_linear_few_kernel<32, W_MN, GROUPED>>(l);
+    case 64: return launch<Few<64>, GROUPED, forge_linear_few_kernel<64, W_MN, GROUPED>>(l);
+    case 128: return launch<Few<128>, GROUPED, forge_linear_few_kernel<128, W_MN, GROUPED>>(l);
+    default: return launch<Many, GROUPED, forge_linear_kernel<W_MN, GROUPED>>(l);
+    }
+}
+
+// The tokens of a tile (256: pairs), and the CTAs that share its contraction.
 struct Choice {
-    bool pair;
-    int split;
+    int tokens, split;
 };
 Choice choose(const LParams& p, int sms)
 {
-    if (const char* e = std::getenv("FORGE_LINEAR_KERNEL")) {
-        if (std::strcmp(e, "pair") == 0) return {true, 1};
-        if (std::strncmp(e, "single", 6) == 0) {
-            int n = std::atoi(e + 6);
-            n = n < 1 ? 1 : (n > kMostSplit ? kMostSplit : n);
-            return {false, n < p.nk ? n : p.nk};
-        }
-    }
+    const char* env = std::getenv("FORGE_LINEAR_KERNEL");
+    const bool pair = env && std::strcmp(env, "pair") == 0;
+    const bool few = env && std::strncmp(env, "few", 3) == 0;
     const int64_t experts = p.E > 0 ? (p.E < p.T ? p.E : p.T) : 1;
     const int64_t each = (p.T + experts - 1) / experts;  // tokens of an expert
     const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
-    if (each > 128 && pairs >= sms / 4) return {true, 1};
-    const int64_t tiles = (each + 127) / 128 * experts * ((p.O + 127) / 128);
-    int64_t split = 2LL * sms / tiles;
-    if (split > kMostSplit) split = kMostSplit;
-    if (split > p.nk) split = p.nk;
-    return {false, split < 1 ? 1 : static_cast<int>(split)};
+    if (pair || (!few && each > 128 && pairs >= sms / 4)) return {256, 1};
+    Choice c{each <= 16 ? 16 : (each <= 32 ? 32 : (each <= 64 ? 64 : 128)), 1};
+    if (few && env[3]) {
+        c.split = std::atoi(env + 3);
+        c.split = c.split < 1 ? 1 : (c.split > kMostSplit ? kMostSplit : c.split);
+        if (c.split > p.nk) c.split = p.nk;
+        return c;
+    }
+    // The split that takes the fewest turns of the SMs, a CTA's start and end counted as
+    // six blocks and the joining as three.
+    const int64_t tiles = (each + c.tokens - 1) / c.tokens * experts * ((p.O + 127) / 128);
+    const int64_t at_once = static_cast<int64_t>(sms) * (c.tokens <= 64 ? 2 : 1);
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= kMostSplit && s <= p.nk; ++s) {
+        const int64_t cost = (tiles * s + at_once - 1) / at_once * ((p.nk + s - 1) / s + 6) + (s > 1 ? 3 : 0);
+        if (cost < best) {
+            best = cost;
+            c.split = s;
+        }
+    }
+    return c;
 }
 
 struct Operands {
@@ -721,19 +966,17 @@ cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams
                 cudaStream_t stream)
 {
     const int64_t E = p.E > 0 ? p.E : 1;
+    const Choice c = choose(p, sms);
     CUtensorMap ta, tw;
-    if (encode_bytes(&ta, o.A, p.K, p.T, 0, o.ldA, 128) != cudaSuccess ||
+    if (encode_bytes(&ta, o.A, p.K, p.T, 0, o.ldA, c.tokens < 128 ? c.tokens : 128) != cudaSuccess ||
         encode_bytes(&tw, o.W, M, N, E, o.ldW, 128) != cudaSuccess)
         return cudaErrorInvalidValue;
-    const Choice c = choose(p, sms);
-    p.tiles_o = static_cast<int32_t>((p.O + (c.pair ? 255 : 127)) / (c.pair ? 256 : 128));
-    const Launch l{ta, tw, p, sms, c.split, stream};
-    if (c.pair) {
-        if (p.E > 0) return transpose ? launch<true, false, true>(l) : launch<true, true, true>(l);
-        return transpose ? launch<true, false, false>(l) : launch<true, true, false>(l);
-    }
-    if (p.E > 0) return transpose ? launch<false, false, true>(l) : launch<false, true, true>(l);
-    return transpose ? launch<false, false, false>(l) : launch<false, true, false>(l);
+    const int cols = c.tokens == 256 ? 256 : 128;
+    p.tiles_o = static_cast<int32_t>((p.O + cols - 1) / cols);
+    const Launch l{ta, tw, p, c.split, stream};
+    if (p.E > 0)
+        return transpose ? launch_form<false, true>(c.tokens, l) : launch_form<true, true>(c.tokens, l);
+    return transpose ? launch_form<false, false>(c.tokens, l) : launch_form<true, false>(c.tokens, l);
 }
 
 forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const float* sW, void* Y,
