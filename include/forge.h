@@ -560,7 +560,7 @@ FORGE_API forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int6
  *           (accumulate != 0).  R = 0 writes zeros (or adds nothing).
  * Sums over the rows are taken in fp32 in an order that the sizes alone
  * determine: bitwise reproducible on one GPU.  They take stream-ordered scratch from the
- * library's memory pool (at most 8 blocks an SM x 2 D floats); a failed
+ * library's memory pool (at most 16 blocks an SM x 2 D floats); a failed
  * allocation returns FORGE_ERR_CUDA.
  */
 FORGE_API forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dtype, int64_t lddy,
@@ -661,7 +661,8 @@ FORGE_API forge_status forge_quantize_e4m3_blocks(const void* x, forge_dtype x_d
  * scales, in fp32.  Rows of codes of any width are accepted: an operand whose
  * base is not 16-byte aligned or whose width is not a multiple of 16 is first
  * copied into padded rows in stream-ordered scratch from the library's memory
- * pool (a failed allocation returns FORGE_ERR_CUDA).  T = 0 does nothing.
+ * pool (a failed allocation returns FORGE_ERR_CUDA); with many tokens so are rows of
+ * sA that are no multiple of four scales.  T = 0 does nothing.
  */
 FORGE_API forge_status forge_linear_e4m3(const uint8_t* A, const float* sA, const uint8_t* W,
                                          const float* sW, void* Y, forge_dtype y_dtype, int64_t T,

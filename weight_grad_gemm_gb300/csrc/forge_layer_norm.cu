@@ -22,6 +22,7 @@
 
 #include "forge.h"
 #include "forge_device.h"
+#include "forge_ptx.cuh"
 #include "forge_rows.cuh"
 
 namespace forge {
@@ -30,6 +31,10 @@ namespace norm {
 constexpr int kRowWarps = 8;      // warps of a block whose warps take a row each
 constexpr int kLongThreads = 1024;  // of a block on a row too wide for registers
 constexpr int kThreadsAtWork = 512;  // of an SM: 128 registers each
+// Of an SM in the gradient.  fp32 rows have the fewest entries a byte, and are
+// quicker with twice the threads of half the registers (8192 x 4096 fp32: 71 us, with
+// 512 threads 75; 16384 x 4096 bf16: 87 and 82; 16384 x 1023 bf16, entry by entry: 38 and 32).
+__host__ __device__ constexpr int grad_threads(int V, int E) { return V == 4 && E == 8 ? 1024 : 512; }
 constexpr int64_t kMaxForward = 16384, kMaxBackward = 8192;  // widths that registers hold
 
 // Threads of a block with W warps a row.
@@ -196,15 +201,25 @@ __global__ void __launch_bounds__(kLongThreads)
     }
 }
 
-// E entries a thread in vectors of V, W warps a row; the next row is on its way while
-// this one is computed.  The weights lie in shared memory, a thread's vectors of
-// four apart by the block, so that no two lanes meet in a bank.
+// E entries a thread in vectors of V, W warps a row.  The weights lie in shared memory,
+// a thread's vectors of four apart by the block, so that no two lanes meet in a bank.
+// The next rows are on their way while one is computed: each thread copies its own
+// vectors of the kDepth rows ahead into shared memory (cp.async: no thread reads
+// another's, so no barrier), or, entry by entry, the one row ahead into registers.
+// (One row ahead for vectors too: 16384 x 4096 bf16 in 88 instead of 82 us.)
+constexpr int kDepth = 3;
+template <int V, int E, int W, typename G, typename X>
+constexpr int ring_bytes()
+{
+    return V == 1 ? 0 : kDepth * 32 * (W == 1 ? kRowWarps : W) * E * static_cast<int>(sizeof(G) + sizeof(X));
+}
 template <typename G, typename X, int V, int E, int W>
-__global__ void __launch_bounds__(threads_of(W), kThreadsAtWork / threads_of(W))
+__global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of(W))
     forge_layer_norm_grad_kernel(const G* __restrict__ dy, const X* __restrict__ x,
                                  const Backward p)
 {
     constexpr int NV = E / V;
+    extern __shared__ __align__(16) uint8_t ring[];  // [kDepth]{[NV][threads] of dy, of x}
     __shared__ float sh[2][2 * W];
     __shared__ float4 weight[E / 4][32 * W];
     const int teams = W == 1 ? kRowWarps : 1;
@@ -215,17 +230,50 @@ __global__ void __launch_bounds__(threads_of(W), kThreadsAtWork / threads_of(W))
     Packed<G, V> gnext[NV];
     Packed<X, V> xnext[NV];
     float mu = 0.0f, rstd = 0.0f;
-    auto load = [&](int64_t r) {
+    auto places = [&](int slot, Packed<G, V>*& g, Packed<X, V>*& x) {
+        constexpr int kRow = threads_of(W) * E;
+        uint8_t* at = ring + slot * (kRow * static_cast<int>(sizeof(G) + sizeof(X)));
+        g = reinterpret_cast<Packed<G, V>*>(at) + threadIdx.x;
+        x = reinterpret_cast<Packed<X, V>*>(at + kRow * sizeof(G)) + threadIdx.x;
+    };
+    // row r on its way (into `slot` of the ring); every call is one copy group
+    auto fetch = [&](int64_t r, int slot) {
+        if constexpr (V == 1) {
+            if (r >= p.R) return;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * W * 32 + t) * V;
-            gnext[i] = c < p.D ? load_packed<G, V>(dy + r * p.ldg + c) : zero_packed<G, V>();
-            xnext[i] = c < p.D ? load_packed<X, V>(x + r * p.ldx + c) : zero_packed<X, V>();
+            for (int i = 0; i < NV; ++i) {
+                const int c = i * W * 32 + t;
+                gnext[i] = c < p.D ? load_packed<G, V>(dy + r * p.ldg + c) : zero_packed<G, V>();
+                xnext[i] = c < p.D ? load_packed<X, V>(x + r * p.ldx + c) : zero_packed<X, V>();
+            }
+        } else {
+            Packed<G, V>* g;
+            Packed<X, V>* q;
+            places(slot, g, q);
+            if (r < p.R) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * W * 32 + t) * V;
+                    const bool in = c < p.D;  // (else zeros)
+                    ptx::cp_async(g + i * threads_of(W), dy + r * p.ldg + (in ? c : 0),
+                                  g->kBytes, in ? g->kBytes : 0);
+                    ptx::cp_async(q + i * threads_of(W), x + r * p.ldx + (in ? c : 0), q->kBytes,
+                                  in ? q->kBytes : 0);
+                }
+            }
+            ptx::cp_async_commit();
         }
+    };
+    auto statistics = [&](int64_t r) {
         mu = __ldg(p.mean + r);
         rstd = __ldg(p.rstd + r);
     };
-    if (r < p.R) load(r);
+    if (V == 1) {
+        fetch(r, 0);
+    } else {
+        for (int d = 0; d < kDepth; ++d) fetch(r + d * step, d);
+    }
+    if (r < p.R) statistics(r);
     if (W > 1 || threadIdx.x < 32) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -237,8 +285,19 @@ __global__ void __launch_bounds__(threads_of(W), kThreadsAtWork / threads_of(W))
     float dw[E], db[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
-    int turn = 0;
+    int turn = 0, slot = 0;
     for (; r < p.R; r += step, turn ^= 1) {
+        if constexpr (V > 1) {
+            ptx::cp_async_wait<kDepth - 1>();  // the oldest row is here
+            Packed<G, V>* g;
+            Packed<X, V>* q;
+            places(slot, g, q);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                gnext[i] = g[i * threads_of(W)];
+                xnext[i] = q[i * threads_of(W)];
+            }
+        }
         float g[E], xh[E];
         float s[2] = {0.0f, 0.0f};  // of g and of g xh (columns past D have dy = 0)
         const float scale = rstd;
@@ -257,7 +316,14 @@ __global__ void __launch_bounds__(threads_of(W), kThreadsAtWork / threads_of(W))
                 db[i + j] += d;
             }
         }
-        if (r + step < p.R) load(r + step);
+        // (its values are in registers, and used: its place may be written)
+        if constexpr (V == 1) {
+            fetch(r + step, 0);
+        } else {
+            fetch(r + kDepth * step, slot);
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+        }
+        if (r + step < p.R) statistics(r + step);
         block_sums<W>(s, sh[turn]);
         const float a = s[0] * inv, b = s[1] * inv;
 #pragma unroll
@@ -451,28 +517,38 @@ void forward(const X* x, const Forward& p, int sms, cudaStream_t s)
 
 // The rows in registers; returns the number of parts of dw and db: a block has two rows
 // at least, so that few rows leave few parts to add.
+template <typename G, typename X, int V, int E, int W>
+int backward_with(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s)
+{
+    constexpr int teams = W == 1 ? kRowWarps : 1, threads = threads_of(W);
+    constexpr int bytes = ring_bytes<V, E, W, G, X>();
+    auto kernel = forge_layer_norm_grad_kernel<G, X, V, E, W>;
+    if (bytes > 16 * 1024) {  // (with the weights beyond what a launch has by itself)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess)
+            return 0;  // (the error stays for the caller)
+    }
+    const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * grad_threads(V, E) / threads);
+    kernel<<<blocks, threads, bytes, s>>>(dy, x, p);
+    return blocks;
+}
+
 template <typename G, typename X, int V, int E>
 int backward(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s)
 {
     const int64_t D = p.D;
-    auto go = [&](auto kernel, int W) {
-        const int teams = W == 1 ? kRowWarps : 1, threads = threads_of(W);
-        const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * kThreadsAtWork / threads);
-        kernel<<<blocks, threads, 0, s>>>(dy, x, p);
-        return blocks;
-    };
-    if (D <= 256) return go(forge_layer_norm_grad_kernel<G, X, V, 8, 1>, 1);
-    if (D <= 512) return go(forge_layer_norm_grad_kernel<G, X, V, E, 16 / E>, 16 / E);
-    if (D <= 1024) return go(forge_layer_norm_grad_kernel<G, X, V, E, 32 / E>, 32 / E);
-    if (D <= 2048) return go(forge_layer_norm_grad_kernel<G, X, V, E, 64 / E>, 64 / E);
-    if (D <= 4096) return go(forge_layer_norm_grad_kernel<G, X, V, E, 128 / E>, 128 / E);
-    return go(forge_layer_norm_grad_kernel<G, X, V, 16, 16>, 16);
+    if (D <= 256) return backward_with<G, X, V, 8, 1>(dy, x, p, sms, s);
+    if (D <= 512) return backward_with<G, X, V, E, 16 / E>(dy, x, p, sms, s);
+    if (D <= 1024) return backward_with<G, X, V, E, 32 / E>(dy, x, p, sms, s);
+    if (D <= 2048) return backward_with<G, X, V, E, 64 / E>(dy, x, p, sms, s);
+    if (D <= 4096) return backward_with<G, X, V, E, 128 / E>(dy, x, p, sms, s);
+    return backward_with<G, X, V, 16, 16>(dy, x, p, sms, s);
 }
 
 // Most parts that backward() or the column kernel writes.
 int64_t most_parts(int64_t R, int64_t D, int sms)
 {
-    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * (kThreadsAtWork / 64);
+    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * (1024 / 64);
     return R < most ? R : most;
 }
 

@@ -93,6 +93,7 @@ struct Few {
 struct LParams {
     int64_t T, K, O;       // tokens, contraction, outputs
     const float *sA, *sW;
+    int64_t sa_ld;             // between rows of A's scales
     int64_t sw_k, sw_o, sw_e;  // strides of W's scales along K, outputs, experts
     void* Y;
     int32_t f32, vec;      // Y's type; rows of Y take 16-byte stores
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_end = tl.t_end;
             c0 = int64_t{tl.o0} + my_col;
             // (scales of rows and columns outside the call are read from its first)
-            sa = p.sA + (row < row_end ? row : 0) * p.nk;
+            sa = p.sA + (row < row_end ? row : 0) * p.sa_ld;
             sw = p.sW + tl.expert * p.sw_e + (c0 < p.O ? c0 / kBlock : 0) * p.sw_o;
             load_scales(0);
         };
@@ -612,6 +613,14 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
     const int32_t k_lo = static_cast<int32_t>(int64_t{p.nk} * rank / split);
     const int32_t n = static_cast<int32_t>(int64_t{p.nk} * (rank + 1) / split) - k_lo;
 
+    auto load = [&](int32_t i) {
+        const int s = i % F::stages;
+        ptx::mbar_arrive_expect_tx(&full[s], F::stage_bytes);
+        uint8_t* sw = smem + s * F::stage_bytes;
+        const int32_t k = (k_lo + i) * kBlock;
+        ptx::tma_load_3d(sw, &tmW, &full[s], W_MN ? tl.o0 : k, W_MN ? k : tl.o0, tl.expert);
+        ptx::tma_load_2d(sw + kStageB, &tmA, &full[s], k, tl.t0);
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::stages; ++s) {
             ptx::mbar_init(&full[s], 1);
@@ -628,10 +637,8 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        ptx::prefetch_tensormap(&tmA);
-        ptx::prefetch_tensormap(&tmW);
+        // the first stages are on their way while the other warps set up
+        for (int32_t i = 0; i < F::stages && i < n; ++i) load(i);
     }
     if (warp == 1) {
         ptx::tmem_alloc(tmem_slot, F::tmem_cols);
@@ -648,16 +655,12 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
         // ---------------------------------------------------- TMA producer
         if (lane == 0) {
             bool ok = true;
-            int32_t i = 0;
+            int32_t i = min(F::stages, n);
             for (; i < n; ++i) {
                 const int s = i % F::stages;
                 ok = wait_often(&empty[s], (i / F::stages & 1u) ^ 1u, abort_flag, p.w);
                 if (!ok) break;
-                ptx::mbar_arrive_expect_tx(&full[s], F::stage_bytes);
-                uint8_t* sw = smem + s * F::stage_bytes;
-                const int32_t k = (k_lo + i) * kBlock;
-                ptx::tma_load_3d(sw, &tmW, &full[s], W_MN ? tl.o0 : k, W_MN ? k : tl.o0, tl.expert);
-                ptx::tma_load_2d(sw + kStageB, &tmA, &full[s], k, tl.t0);
+                load(i);
             }
             if (!ok) {
                 // wait (bounded) for the copies still in flight: the last ones issued
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
                                  ks != 0 ? 1u : 0u);
                 issued_any = true;
                 ptx::umma_commit(&tfull[b]);
-                ptx::umma_commit(&empty[s]);
+                if (i + F::stages < n) ptx::umma_commit(&empty[s]);  // (a stage that is used again)
             }
             if (!ok && issued_any) {
                 ptx::umma_commit(drain);
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
             for (int h = 0; h < (NT + 31) / 32; ++h) {
                 // (tokens outside the tile take the call's first scales)
                 const int64_t row = int64_t{tl.t0} + 32 * h + lane;
-                const float* at = p.sA + (row < tl.t_end ? row : 0) * p.nk;
+                const float* at = p.sA + (row < tl.t_end ? row : 0) * p.sa_ld;
                 if (p.sa_vec && kb % 4 == 0) {
                     const float4 v = __ldg(reinterpret_cast<const float4*>(at + kb));
                     a[h][0] = v.x;
@@ -934,7 +937,7 @@ Choice choose(const LParams& p, int sms)
     const int64_t experts = p.E > 0 ? (p.E < p.T ? p.E : p.T) : 1;
     const int64_t each = (p.T + experts - 1) / experts;  // tokens of an expert
     const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
-    if (pair || (!few && each > 128 && pairs >= sms / 4)) return {256, 1};
+    if (pair || (!few && each > 64 && pairs >= sms / 8)) return {256, 1};
     Choice c{each <= 16 ? 16 : (each <= 32 ? 32 : (each <= 64 ? 64 : 128)), 1};
     if (few && env[3]) {
         c.split = std::atoi(env + 3);
@@ -943,12 +946,13 @@ Choice choose(const LParams& p, int sms)
         return c;
     }
     // The split that takes the fewest turns of the SMs, a CTA's start and end counted as
-    // six blocks and the joining as three.
+    // six blocks, the joining as one and more with its bytes.
     const int64_t tiles = (each + c.tokens - 1) / c.tokens * experts * ((p.O + 127) / 128);
     const int64_t at_once = static_cast<int64_t>(sms) * (c.tokens <= 64 ? 2 : 1);
     int64_t best = INT64_MAX;
     for (int s = 1; s <= kMostSplit && s <= p.nk; ++s) {
-        const int64_t cost = (tiles * s + at_once - 1) / at_once * ((p.nk + s - 1) / s + 6) + (s > 1 ? 3 : 0);
+        const int64_t cost = (tiles * s + at_once - 1) / at_once * ((p.nk + s - 1) / s + 6) +
+                             (s > 1 ? 1 + s * c.tokens / 512 : 0);
         if (cost < best) {
             best = cost;
             c.split = s;
@@ -962,11 +966,10 @@ struct Operands {
     int64_t ldA, ldW;  // bytes between rows, multiples of 16
 };
 
-cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams p, int sms,
-                cudaStream_t stream)
+cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams p,
+                const Choice& c, cudaStream_t stream)
 {
     const int64_t E = p.E > 0 ? p.E : 1;
-    const Choice c = choose(p, sms);
     CUtensorMap ta, tw;
     if (encode_bytes(&ta, o.A, p.K, p.T, 0, o.ldA, c.tokens < 128 ? c.tokens : 128) != cudaSuccess ||
         encode_bytes(&tw, o.W, M, N, E, o.ldW, 128) != cudaSuccess)
@@ -1013,22 +1016,30 @@ forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const f
     p.E = E;
     p.offsets = offsets;
     p.nk = static_cast<int32_t>((p.K + kBlock - 1) / kBlock);
+    p.sa_ld = p.nk;
     p.sa_vec = p.nk % 4 == 0 && aligned(sA, 16);
     p.w.timeout_ns = wait_timeout();
     p.w.status = device_status_word();
 
-    // rows that TMA cannot address go through rows padded to 16 bytes
+    // Rows that TMA cannot address go through rows padded to 16 bytes, and so do, for many
+    // tokens, rows of A's scales that no 16-byte load can address: a load for each
+    // scale keeps the load-store unit, and with it the barriers, busy.
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const Choice c = choose(p, sms);
     const int64_t rows_w = (E > 0 ? E : 1) * N;
     const int64_t pad_a = (p.K + 15) / 16 * 16, pad_w = (M + 15) / 16 * 16;
+    const int64_t pad_s = (int64_t{p.nk} * 4 + 15) / 16 * 16;
     const bool stage_a = p.K % 16 != 0 || !aligned(A, 16);
     const bool stage_w = M % 16 != 0 || !aligned(W, 16);
+    const bool stage_s = c.tokens == 256 && !p.sa_vec;
     Operands o{A, W, p.K, M};
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
-    if (stage_a || stage_w) {
-        const int64_t a_bytes = stage_a ? (pad_a * T + 255) / 256 * 256 : 0;
-        e = scratch_alloc(&scratch, a_bytes + (stage_w ? pad_w * rows_w : 0), s);
+    if (stage_a || stage_w || stage_s) {
+        auto whole = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+        const int64_t a_bytes = stage_a ? whole(pad_a * T) : 0;
+        const int64_t s_bytes = stage_s ? whole(pad_s * T) : 0;
+        e = scratch_alloc(&scratch, a_bytes + s_bytes + (stage_w ? pad_w * rows_w : 0), s);
         uint8_t* at = static_cast<uint8_t*>(scratch);
         if (e == cudaSuccess && stage_a) {
             e = stage_padded_rows(A, at, T, p.K, pad_a, s);
@@ -1036,13 +1047,20 @@ forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const f
             o.ldA = pad_a;
             at += a_bytes;
         }
+        if (e == cudaSuccess && stage_s) {
+            e = stage_padded_rows(sA, at, T, int64_t{p.nk} * 4, pad_s, s);
+            p.sA = reinterpret_cast<const float*>(at);
+            p.sa_ld = pad_s / 4;
+            p.sa_vec = 1;
+            at += s_bytes;
+        }
         if (e == cudaSuccess && stage_w) {
             e = stage_padded_rows(W, at, rows_w, M, pad_w, s);
             o.W = at;
             o.ldW = pad_w;
         }
     }
-    if (e == cudaSuccess) e = run(o, N, M, transpose != 0, p, sms, s);
+    if (e == cudaSuccess) e = run(o, N, M, transpose != 0, p, c, s);
     if (scratch) {
         const cudaError_t fe = scratch_free(scratch, s);
         if (e == cudaSuccess) e = fe;

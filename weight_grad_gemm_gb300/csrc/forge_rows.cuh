@@ -12,7 +12,7 @@ namespace forge {
 // V consecutive entries of T as they lie in memory, in 32-bit registers (one
 // entry of bf16 takes a whole one).
 template <typename T, int V>
-struct Packed {
+struct alignas(V * sizeof(T) >= 16 ? 16 : (V * sizeof(T) == 8 ? 8 : 4)) Packed {
     static constexpr int kBytes = V * static_cast<int>(sizeof(T));
     static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
     uint32_t w[kWords];
