@@ -3,7 +3,8 @@
 The model is an embedding and a head: X = scale * E[ids], logits = X W, with
 E [V, D] and W [D, V] fp32 masters; the loss is the mean cross-entropy of the
 next tokens, and rows whose target is negative are padding.  A full model puts
-its layers between the two; their steps are the library's other calls.
+its layers between the two: step takes an expert layer (moe.py), whose forward and
+backward pass stand between the embedding and the head's.
 
 step           the fused form: no gradient of a weight reaches memory.
                    X = forge_embedding(ids, E)
@@ -18,9 +19,12 @@ step_clipped   the form with global-norm clipping, which needs every gradient
                forge_embedding_grad, then forge_grad_norm and forge_clip_grads
                over both and forge_owner_adamw on each weight.
 
-    python -m weight_grad_gemm_gb300.lm       trains on a repeated sequence
+    python -m weight_grad_gemm_gb300.lm       trains on a repeated sequence, the ends
+                                              alone and with an expert layer
 """
 from __future__ import annotations
+
+from weight_grad_gemm_gb300 import moe
 
 
 class Ends:
@@ -43,14 +47,17 @@ class Ends:
         self.t = 0
 
 
-def forward(ends: Ends, ids, targets):
-    """X, the bf16 copy of W it met, logits (bf16), and logprob, lse of the targets."""
+def forward(ends: Ends, ids, targets, layer=None):
+    """X (the head's input), the bf16 copy of W it met, logits (bf16), and logprob, lse of
+    the targets."""
     import torch
 
     import weight_grad_gemm_gb300 as fg
     T, D = ids.numel(), ends.E.shape[1]
     X = torch.empty((T, D), dtype=torch.bfloat16, device=ids.device)
     fg.forge_embedding(ids, ends.E, X, scale=ends.scale)
+    if layer is not None:
+        X = moe.forward(layer, X)
     Wb = ends.W.to(torch.bfloat16)
     logits = X @ Wb
     logprob, lse = (torch.empty(T, device=ids.device) for _ in range(2))
@@ -58,9 +65,9 @@ def forward(ends: Ends, ids, targets):
     return X, Wb, logits, logprob, lse
 
 
-def _loss_and_dlogits(ends, ids, targets):
+def _loss_and_dlogits(ends, ids, targets, layer=None):
     import weight_grad_gemm_gb300 as fg
-    X, Wb, logits, logprob, lse = forward(ends, ids, targets)
+    X, Wb, logits, logprob, lse = forward(ends, ids, targets, layer)
     count = (targets >= 0).sum().clamp(min=1)
     loss = -logprob.sum() / count
     weight = (-1.0 / count).to(logprob.dtype).expand(targets.numel()).contiguous()
@@ -68,15 +75,18 @@ def _loss_and_dlogits(ends, ids, targets):
     return X, Wb, logits, loss
 
 
-def step(ends: Ends, ids, targets):
-    """One training step; returns the loss before it (a device scalar)."""
+def step(ends: Ends, ids, targets, layer=None):
+    """One training step, with an expert layer (moe.Experts) between the ends where one is
+    given; returns the loss before it (a device scalar, without the layer's balance loss)."""
     import torch
 
     import weight_grad_gemm_gb300 as fg
-    X, Wb, dlogits, loss = _loss_and_dlogits(ends, ids, targets)
+    X, Wb, dlogits, loss = _loss_and_dlogits(ends, ids, targets, layer)
     ends.t += 1
     dX = torch.empty_like(X)
     fg.forge_backward_adamw(X, dlogits, ends.W, ends.Wm, ends.Wv, dX, Wb=Wb, step=ends.t, **ends.hp)
+    if layer is not None:
+        dX = moe.backward(layer, dX)
     fg.forge_embedding_adamw(dX, ids, ends.E, ends.Em, ends.Ev, scale=ends.scale, step=ends.t,
                              **ends.hp)
     return loss
@@ -109,16 +119,18 @@ def main(vocab=5000, width=256, tokens=4096, steps=30):
     g.manual_seed(1)
     ids = torch.randint(0, vocab, (tokens + 1,), generator=g, device="cuda")
     ids = ids[torch.arange(tokens + 1, device="cuda") % 300]  # a sequence that repeats
-    for clipped in (False, True):
+    for form in ("fused", "clipped", "with experts"):
         ends = Ends(vocab, width)
+        clipped = form == "clipped"
+        layer = moe.Experts(width, 8, 2) if form == "with experts" else None
         losses = []
         for _ in range(steps):
             if clipped:
                 loss, norm = step_clipped(ends, ids[:-1], ids[1:], 0.25)
             else:
-                loss = step(ends, ids[:-1], ids[1:])
+                loss = step(ends, ids[:-1], ids[1:], layer)
             losses.append(loss)
-        print(f"{'clipped' if clipped else 'fused'}: loss {float(losses[0]):.3f} -> "
+        print(f"{form}: loss {float(losses[0]):.3f} -> "
               f"{float(losses[-1]):.3f} in {steps} steps"
               + (f", last norm {float(norm):.3f}" if clipped else ""))
 
