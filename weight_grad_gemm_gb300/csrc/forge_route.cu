@@ -42,11 +42,14 @@ constexpr int kMaxTop = 32;
 constexpr int kMostChoices = 2048;   // tokens of a block x k
 constexpr int kMostMasks = 4096;     // words of 32 tokens of a block x E
 constexpr int kMostWords = 8;
+// 65536 x 256 logits (the whole call): by rounds of the maximum 46 us at k = 1, 51 at 4, 56
+// at 6, 60 at 8 and 71 at 12; by comparing all lanes 52, 54, 56, 59 and 64
+constexpr int kMostRounds = 6;
 constexpr int kFewCounts = 4096;     // blocks x E that every place block scans by itself
 
 struct Args {
     int64_t T, ld;
-    int32_t E, k, words;  // words: a block's tokens / 32
+    int32_t E, k, tokens, words;  // a block's tokens, and its masks' words of 32
     bool normalize, vec;  // vec: rows of logits in 16-byte loads
     int32_t* experts;
     float* weights;
@@ -137,25 +140,28 @@ __device__ __forceinline__ void make_masks(uint32_t* mask, const Args& p, F choi
     __syncthreads();
 }
 
-// offsets [E + 1] (shared memory) of counts that `count(e)` gives; all threads.
+// offsets [E + 1] (shared memory) of counts that `count(e)` gives; all threads.  A lane of
+// the first warp has a run of experts.
 template <typename F>
 __device__ __forceinline__ void make_offsets(int32_t* offs, int E, F count)
 {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
+        const int run = (E + 31) / 32, lo = min(lane * run, E), hi = min(lo + run, E);
         int32_t sum = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int32_t n = e0 + lane < E ? count(e0 + lane) : 0;
-            int32_t up = n;
+        for (int e = lo; e < hi; ++e) sum += count(e);
+        int32_t up = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
-                if (lane >= o) up += v;
-            }
-            if (e0 + lane < E) offs[e0 + lane] = sum + up - n;
-            sum += __shfl_sync(0xffffffffu, up, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += v;
         }
-        if (lane == 0) offs[E] = sum;
+        if (lane == 31) offs[E] = up;
+        up -= sum;
+        for (int e = lo; e < hi; ++e) {
+            offs[e] = up;
+            up += count(e);
+        }
     }
     __syncthreads();
 }
@@ -188,19 +194,34 @@ __device__ __forceinline__ void write_totals(const Args& p, const int32_t* offs,
 // a lane, and ranked by comparing each with each.  Rows with more than 32 such keys
 // (equal ones) take k rounds of the maximum.
 template <int EPL, typename F>
-__device__ __forceinline__ void top_of_warp(int32_t (&key)[EPL], int k, uint64_t* list, F take)
+__device__ __forceinline__ void top_of_warp(int32_t (&key)[EPL], int k, int32_t* list, F take)
 {
     const int lane = threadIdx.x & 31;
     int32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
-    int32_t bound = kNone, left = best;
-    for (int n = 0; n < k;) {
-        bound = __reduce_max_sync(0xffffffffu, left);
-        if (bound == kNone) break;
-        const bool is = left == bound;
-        n += __popc(__ballot_sync(0xffffffffu, is));
-        left = is ? kNone : left;
+    int32_t bound = kNone;
+    if (k > kMostRounds) {
+        // (the lanes' maxima that fewer than k others exceed)
+        list[lane] = best;
+        __syncwarp();
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(list + j);
+            above += (q.x > best) + (q.y > best) + (q.z > best) + (q.w > best);
+        }
+        bound = __reduce_min_sync(0xffffffffu, above < k ? best : INT_MAX);
+        __syncwarp();
+    } else {
+        int32_t left = best;
+        for (int n = 0; n < k;) {
+            bound = __reduce_max_sync(0xffffffffu, left);
+            if (bound == kNone) break;
+            const bool is = left == bound;
+            n += __popc(__ballot_sync(0xffffffffu, is));
+            left = is ? kNone : left;
+        }
     }
     bound = max(bound, kNone + 1);
     int here = 0;
@@ -217,18 +238,27 @@ __device__ __forceinline__ void top_of_warp(int32_t (&key)[EPL], int k, uint64_t
     if (here > 0 && found <= 32) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i] >= bound)
-                list[at++] = static_cast<uint64_t>(static_cast<uint32_t>(key[i]) ^ 0x80000000u) << 32 |
-                             (0xFFFFFFFFu - (lane * EPL + i));  // larger: larger key, lower expert
+            if (key[i] >= bound) {
+                list[at] = key[i];
+                list[32 + at++] = lane * EPL + i;
+            }
     }
     __syncwarp();
     if (found <= 32) {
-        const uint64_t mine = lane < found ? list[lane] : 0;
+        // (the list is in the experts' order: of equal keys the earlier goes first.
+        // What lies behind its end is below every key: -inf is not gathered)
+        if (lane >= found) list[lane] = kNone;
+        __syncwarp();
+        const int32_t mine = list[lane], from = mine - 1;
         int rank = 0;
-        for (int j = 0; j < found; ++j) rank += list[j] > mine;
-        if (lane < found && rank < k)
-            take(rank, static_cast<int32_t>(static_cast<uint32_t>(mine >> 32) ^ 0x80000000u),
-                 static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(mine)));
+        for (int j = 0; j < found; j += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(list + j);
+            rank += q.x > (j < lane ? from : mine);
+            rank += q.y > (j + 1 < lane ? from : mine);
+            rank += q.z > (j + 2 < lane ? from : mine);
+            rank += q.w > (j + 3 < lane ? from : mine);
+        }
+        if (lane < found && rank < k) take(rank, mine, list[32 + lane]);
         if (lane >= found && lane < k) take(lane, kNone, -1);
     } else {
         for (int j = 0; j < k; ++j) {
@@ -257,10 +287,10 @@ template <typename X, int LPR, int EPL, bool ONE>
 __global__ void __launch_bounds__(kThreads)
     forge_route_tokens_kernel(const X* __restrict__ logits, const Args p)
 {
-    extern __shared__ uint8_t smem[];
-    const int C = 32 * p.words;
-    uint64_t* lists = reinterpret_cast<uint64_t*>(smem);                // [warps][32]
-    int32_t* chosen = reinterpret_cast<int32_t*>(lists + kWarps * 32);  // [C][k]
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int C = p.tokens;
+    int32_t* lists = reinterpret_cast<int32_t*>(smem);  // [warps][2][32]: keys, experts
+    int32_t* chosen = lists + kWarps * 64;              // [C][k]
     float* weight = reinterpret_cast<float*>(chosen + C * p.k);         // [C][k], before division
     float* inverse = weight + C * p.k;                                  // [C]
     uint32_t* mask = reinterpret_cast<uint32_t*>(inverse + C);          // [words][E]
@@ -319,7 +349,7 @@ __global__ void __launch_bounds__(kThreads)
         if constexpr (LPR == 32) {
             if (r < C) {  // (the same for the whole warp)
                 float mine = 0.0f;
-                top_of_warp(key, p.k, lists + warp * 32, [&](int j, int32_t t, int x) {
+                top_of_warp(key, p.k, lists + warp * 64, [&](int j, int32_t t, int x) {
                     const float w = t > kNone ? exp_from(value_of(t), c) : 0.0f;
                     mine += w;
                     chosen[r * p.k + j] = x;
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kThreads)
         p.experts[first * p.k + i] = chosen[i];
         p.weights[first * p.k + i] = weight[i] * inverse[i / p.k];
     }
-    make_masks(mask, p, [&](int t, int j) { return chosen[t * p.k + j]; });
+    make_masks(mask, p, [&](int t, int j) { return t < C ? chosen[t * p.k + j] : -1; });
     // sums of p: lanes with the same experts, then the warps in order
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -421,49 +451,74 @@ __global__ void __launch_bounds__(kThreads)
 
 // Eight columns of part and psum a block, 128 threads a column, each a run of blocks:
 // exclusive sums over the blocks in place, and the totals.
-constexpr int kScanColumns = 8, kScanRuns = 128;
+constexpr int kScanColumns = 8, kScanRuns = 128, kScanAhead = 8;
 __global__ void __launch_bounds__(kScanColumns * kScanRuns) forge_route_scan_kernel(const Args p)
 {
-    __shared__ int32_t runs[kScanRuns][kScanColumns];
-    __shared__ float masses[kScanRuns][kScanColumns];
+    constexpr int kWarpsHere = kScanColumns * kScanRuns / 32;
+    static_assert(kWarpsHere == 32 && 32 % kScanColumns == 0, "a lane for each warp's sums");
+    __shared__ int32_t runs[kWarpsHere][kScanColumns + 1];
+    __shared__ float masses[kWarpsHere][kScanColumns + 1];
     await_prerequisites();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = threadIdx.x % kScanColumns, run = threadIdx.x / kScanColumns;
     const int e = blockIdx.x * kScanColumns + col;
     const int per = (p.blocks + kScanRuns - 1) / kScanRuns;
     const int lo = run * per, hi = min(lo + per, p.blocks);
+    int32_t n[kScanAhead];  // a run's first counts: the whole of it, but for very many blocks
     int32_t sum = 0;
     float mass = 0.0f;
-    if (e <= p.E) {
-#pragma unroll 8
-        for (int b = lo; b < hi; ++b) {
-            sum += p.part[static_cast<int64_t>(b) * (p.E + 1) + e];
-            if (e < p.E) mass += p.psum[static_cast<int64_t>(b) * p.E + e];
+    for (int b0 = lo; b0 < hi; b0 += kScanAhead) {
+        float m[kScanAhead];
+#pragma unroll
+        for (int i = 0; i < kScanAhead; ++i) {
+            const int64_t b = b0 + i;
+            n[i] = b < hi && e <= p.E ? p.part[b * (p.E + 1) + e] : 0;
+            m[i] = b < hi && e < p.E ? p.psum[b * p.E + e] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kScanAhead; ++i) {
+            sum += n[i];
+            mass += m[i];
         }
     }
+    // within the warp (four runs of each column), then over the warps: warp c has column c
     int32_t up = sum;
-    runs[run][col] = sum;
-    masses[run][col] = mass;
-    __syncthreads();
-    for (int o = 1; o < kScanRuns; o <<= 1) {
-        const int32_t v = run >= o ? runs[run - o][col] : 0;
-        const float m = run % (2 * o) == 0 ? masses[run + o][col] : 0.0f;
-        __syncthreads();
-        up += v;
-        mass += m;
-        runs[run][col] = up;
-        masses[run][col] = mass;
-        __syncthreads();
+#pragma unroll
+    for (int o = kScanColumns; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += v;
+        mass += __shfl_xor_sync(0xffffffffu, mass, o);
     }
-    if (e <= p.E) {
-        if (run == kScanRuns - 1) p.total[e] = up;
-        if (run == 0 && e < p.E) p.ptotal[e] = mass;
-        int32_t at = up - sum;
-#pragma unroll 8
-        for (int b = lo; b < hi; ++b) {
-            int32_t* cell = p.part + static_cast<int64_t>(b) * (p.E + 1) + e;
-            const int32_t n = *cell;
+    if (lane >= 32 - kScanColumns) {
+        runs[warp][col] = up;
+        masses[warp][col] = mass;
+    }
+    __syncthreads();
+    if (warp < kScanColumns) {
+        const int32_t own = runs[lane][warp];
+        int32_t all = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, all, o);
+            if (lane >= o) all += v;
+        }
+        const float m = lanes_sum<32>(masses[lane][warp]);
+        runs[lane][warp] = all - own;
+        const int c = blockIdx.x * kScanColumns + warp;
+        if (lane == 31 && c <= p.E) p.total[c] = all;
+        if (lane == 31 && c < p.E) p.ptotal[c] = m;
+    }
+    __syncthreads();
+    int32_t at = runs[warp][col] + up - sum;
+    for (int b0 = lo; e <= p.E && b0 < hi; b0 += kScanAhead) {
+#pragma unroll
+        for (int i = 0; i < kScanAhead; ++i) {
+            const int64_t b = b0 + i;
+            if (b >= hi) continue;
+            int32_t* cell = p.part + b * (p.E + 1) + e;
+            const int32_t here = per <= kScanAhead ? n[i] : *cell;
             *cell = at;
-            at += n;
+            at += here;
         }
     }
     let_dependents_start();
@@ -473,10 +528,10 @@ __global__ void __launch_bounds__(kScanColumns * kScanRuns) forge_route_scan_ker
 template <bool SCAN>
 __global__ void __launch_bounds__(kThreads) forge_route_place_kernel(const Args p)
 {
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     int32_t* offs = reinterpret_cast<int32_t*>(smem);  // [E + 1]
     int32_t* base = offs + p.E + 1;                    // [E + 1]: the earlier blocks' choices
-    int32_t* total = base + p.E + 1;                   // SCAN: [E + 1]
+    int32_t* total = base + p.E + 1;                   // [E + 1]
     float* mass = reinterpret_cast<float*>(total + p.E + 1);  // SCAN, first block: [E]
     await_prerequisites();
     const int E1 = p.E + 1, b = blockIdx.x;
@@ -515,19 +570,21 @@ __global__ void __launch_bounds__(kThreads) forge_route_place_kernel(const Args 
             __syncthreads();
         }
     } else {
-        for (int e = threadIdx.x; e <= p.E; e += kThreads)
+        for (int e = threadIdx.x; e <= p.E; e += kThreads) {
             base[e] = p.part[static_cast<int64_t>(b) * E1 + e];
+            total[e] = p.total[e];
+        }
     }
     __syncthreads();
-    auto count = [&](int e) { return SCAN ? total[e] : p.total[e]; };
+    auto count = [&](int e) { return total[e]; };
     make_offsets(offs, p.E, count);
     if (b == 0)
         write_totals(p, offs, count(p.E), count,
                      [&](int e) { return SCAN ? mass[e] : p.ptotal[e]; });
     if (!p.place) return;
-    const int64_t first = static_cast<int64_t>(b) * 32 * p.words;
+    const int64_t first = static_cast<int64_t>(b) * p.tokens;
     const int64_t left = p.T - first;
-    const int tokens = left < 32 * p.words ? static_cast<int>(left) : 32 * p.words;
+    const int tokens = left < p.tokens ? static_cast<int>(left) : p.tokens;
     for (int i = threadIdx.x; i < tokens * p.k; i += kThreads) {
         const int64_t at = first * p.k + i;
         const int e = p.experts[at];
@@ -560,10 +617,35 @@ __device__ __forceinline__ float nan_max(float a, float b)
     return y;
 }
 
+// Four sums over a token's lanes, in all of them: each half of the lanes takes two of them
+// on, each quarter one.
+template <int LPR>
+__device__ __forceinline__ void sum_four(float (&s)[4])
+{
+    if constexpr (LPR < 8) {
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+    } else {
+        constexpr int H = LPR / 2, Q = LPR / 4;
+        const int lane = threadIdx.x & 31;
+        const bool h = lane & H, q = lane & Q;
+        const float a = (h ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, h ? s[0] : s[2], H);
+        const float b = (h ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, h ? s[1] : s[3], H);
+        float v = (q ? b : a) + __shfl_xor_sync(0xffffffffu, q ? a : b, Q);
+#pragma unroll
+        for (int o = Q / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            s[n] = __shfl_sync(0xffffffffu, v, (n >> 1) * H + (n & 1) * Q, LPR);
+    }
+}
+
 // A token's row is written without its weights' part, p (c - sum p q); the lanes that
 // take its choices (each loads its expert's logit for itself) then write theirs over it.
 template <typename X, int LPR, int EPL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, EPL == 8 && LPR >= 8 ? 4 : 1)
     forge_route_grad_kernel(const X* __restrict__ logits, const GradArgs p)
 {
     constexpr int G = kThreads / LPR;
@@ -631,10 +713,7 @@ __global__ void __launch_bounds__(kThreads)
             s[0] += v[i];
             s[1] = fmaf(v[i], c[i], s[1]);
         }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+        sum_four<LPR>(s);
         const float inv = s[0] != 0.0f ? 1.0f / s[0] : 0.0f;
         // normalised weights: (gw - sum gw w) / S; else gw as it is.  Then
         // sum p q = (exp c + exp by) / sum exp, the second sum 0 when normalised.
@@ -710,27 +789,28 @@ cudaError_t after(void (*kernel)(const Args), int grid, int threads, size_t smem
 template <typename X>
 cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
 {
-    // a block's words: the tokens that its groups take at once, and from there as many as
-    // leave every SM four blocks, within the room
+    // a block's tokens: whole turns of its groups, as many as give every SM four blocks
+    // (which run at once: a fifth would run alone), 32 at least, within the room
     int most = kMostChoices / (32 * p.k);
     if (most > kMostMasks / p.E) most = kMostMasks / p.E;
     if (most > kMostWords) most = kMostWords;
     if (most < 1) most = 1;
-    const int64_t all = (p.T + 31) / 32;
     int lanes = 1;  // a token
     while (lanes < 32 && 8 * lanes < p.E) lanes *= 2;
-    const int64_t at_once = 8 / lanes;
-    int64_t words = all / (4LL * sms);
-    if (words < at_once) words = at_once;
+    const int64_t at_once = kThreads / lanes;
+    int64_t tokens = (p.T + 4LL * sms - 1) / (4LL * sms);
+    tokens = ((tokens < 32 ? 32 : tokens) + at_once - 1) / at_once * at_once;
     // one block for up to four turns of its groups: there a second and third launch
     // cost more than they save
-    if (all <= most && all * lanes <= 32) words = all;
-    p.words = static_cast<int>(words < 1 ? 1 : (words > most ? most : words));
-    const int64_t blocks = (all + p.words - 1) / p.words;
+    if (p.T <= 32 * most && p.T <= 4 * at_once) tokens = p.T;
+    if (tokens > 32 * most) tokens = 32 * most;
+    p.tokens = static_cast<int>(tokens < 1 ? 1 : tokens);
+    p.words = (p.tokens + 31) / 32;
+    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens;
     if (blocks > INT32_MAX / 2) return cudaErrorInvalidValue;
     p.blocks = static_cast<int32_t>(blocks < 1 ? 1 : blocks);
     const bool one = p.blocks == 1, place = p.slots || p.rows;
-    const size_t C = 32 * p.words, E = p.E;
+    const size_t C = p.tokens, E = p.E;
     const size_t tokens_smem = 8 * kWarps * 32 +
                                4 * (2 * C * p.k + C + p.words * E + kWarps * E + (one ? E + 1 : 0));
     void* scratch = nullptr;
@@ -875,7 +955,7 @@ extern "C" forge_status forge_moe_route_grad(const void* logits, forge_dtype dty
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto* x) {
         return by_experts(E, [&](auto shape) {
-            const int64_t want = (T * shape.lpr + kThreads - 1) / kThreads, most = 8LL * sms;
+            const int64_t want = (T * shape.lpr + kThreads - 1) / kThreads, most = 4LL * sms;
             using X = std::remove_cv_t<std::remove_pointer_t<decltype(x)>>;
             forge_route_grad_kernel<X, shape.lpr, shape.epl>
                 <<<static_cast<unsigned>(want < most ? want : most), kThreads, 0, s>>>(x, p);
