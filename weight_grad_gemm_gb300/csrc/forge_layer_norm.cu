@@ -19,6 +19,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "forge.h"
 #include "forge_device.h"
@@ -29,6 +30,9 @@ namespace forge {
 namespace norm {
 
 constexpr int kRowWarps = 8;      // warps of a block whose warps take a row each
+// Of a block in the gradient of rows too wide for registers, two blocks an SM (4096 x 16384
+// bf16, all kernels: 144 us, with one block of 1024 threads 154; 2048 x 16384 fp32: 134, 134)
+constexpr int kWideThreads = 512;
 constexpr int kLongThreads = 1024;  // of a block on a row too wide for registers
 constexpr int kThreadsAtWork = 512;  // of an SM: 128 registers each
 // Of an SM in the gradient.  fp32 rows have the fewest entries a byte, and are
@@ -375,24 +379,35 @@ __global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of
     }
 }
 
-// dx of rows wider than the registers hold: two passes over a row.
+// dx of rows too wide for dw and db to stay in registers beside them: two passes over
+// a row, the first kHeld vectors of a thread kept from the first, the rest from L2
+// (4096 x 16384 bf16 with dw and db: 144 us, all from L2 162; 2048 x 16384 fp32 134, with
+// eight vectors of its twice as many registers 158).
 template <typename G, typename X, int V>
-__global__ void __launch_bounds__(kLongThreads)
+__global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
     forge_layer_norm_grad_long_kernel(const G* __restrict__ dy, const X* __restrict__ x,
                                       const Backward p)
 {
-    __shared__ float sh[2][2 * kLongThreads / 32];
+    constexpr int kHeld = sizeof(G) + sizeof(X) <= 4 ? 8 : 4;  // (registers)
+    __shared__ float sh[2][2 * kWideThreads / 32];
     const float inv = 1.0f / static_cast<float>(p.D);
-    const int64_t step = static_cast<int64_t>(kLongThreads) * V;
+    const int64_t step = static_cast<int64_t>(kWideThreads) * V;
+    const int64_t c0 = threadIdx.x * V;
     int turn = 0;
     for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x, turn ^= 1) {
         const G* grow = dy + r * p.ldg;
         const X* xrow = x + r * p.ldx;
+        Packed<G, V> gheld[kHeld];
+        Packed<X, V> xheld[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = c0 + i * step;
+            gheld[i] = c < p.D ? load_packed<G, V>(grow + c) : zero_packed<G, V>();
+            xheld[i] = c < p.D ? load_packed<X, V>(xrow + c) : zero_packed<X, V>();
+        }
         const float mu = p.mean[r], rstd = p.rstd[r];
         float s[2] = {0.0f, 0.0f};
-        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
-            const Packed<G, V> graw = load_packed<G, V>(grow + c);
-            const Packed<X, V> xraw = load_packed<X, V>(xrow + c);
+        auto add = [&](const Packed<G, V>& graw, const Packed<X, V>& xraw, int64_t c) {
             const Packed<float, V> w = load_packed<float, V>(p.weight + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -400,12 +415,15 @@ __global__ void __launch_bounds__(kLongThreads)
                 s[0] += g;
                 s[1] = fmaf(g, (entry(xraw, j) - mu) * rstd, s[1]);
             }
-        }
-        block_sums<kLongThreads / 32>(s, sh[turn]);
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (c0 + i * step < p.D) add(gheld[i], xheld[i], c0 + i * step);
+        for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
+            add(load_packed<G, V>(grow + c), load_packed<X, V>(xrow + c), c);
+        block_sums<kWideThreads / 32>(s, sh[turn]);
         const float a = s[0] * inv, b = s[1] * inv;
-        for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
-            const Packed<G, V> graw = load_packed<G, V>(grow + c);
-            const Packed<X, V> xraw = load_packed<X, V>(xrow + c);
+        auto store = [&](const Packed<G, V>& graw, const Packed<X, V>& xraw, int64_t c) {
             const Packed<float, V> w = load_packed<float, V>(p.weight + c);
             float v[V];
 #pragma unroll
@@ -413,31 +431,47 @@ __global__ void __launch_bounds__(kLongThreads)
                 v[j] = rstd * (fmaf(entry(graw, j), entry(w, j), -a) -
                                (entry(xraw, j) - mu) * rstd * b);
             store_as(p.dx, p.dx_f32, r * p.ldo + c, v);
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (c0 + i * step < p.D) store(gheld[i], xheld[i], c0 + i * step);
+        for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
+            store(load_packed<G, V>(grow + c), load_packed<X, V>(xrow + c), c);
     }
 }
 
 // dw and db of such rows, before dx (which may be written over dy): a block
-// takes 32 x kLongWarps columns of every gridDim.y-th group of rows.
+// takes 32 x kLongWarps vectors of columns of every gridDim.y-th row (4096 x 16384 bf16,
+// entry by entry: 204 us for the whole call, in vectors of four 162).
 constexpr int kLongWarps = 4;
-template <typename G, typename X>
+template <typename G, typename X, int V>
 __global__ void __launch_bounds__(32 * kLongWarps)
     forge_layer_norm_columns_kernel(const G* __restrict__ dy, const X* __restrict__ x,
                                     const Backward p)
 {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * (32 * kLongWarps) + threadIdx.x;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * (32 * kLongWarps) + threadIdx.x) * V;
     if (c >= p.D) return;
-    float dw = 0.0f, db = 0.0f;
+    float dw[V], db[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
 #pragma unroll 4
     for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
-        const float d = entry(load_packed<G, 1>(dy + r * p.ldg + c), 0);
-        const float xh = (entry(load_packed<X, 1>(x + r * p.ldx + c), 0) - p.mean[r]) * p.rstd[r];
-        dw = fmaf(d, xh, dw);
-        db += d;
+        const Packed<G, V> graw = load_packed<G, V>(dy + r * p.ldg + c);
+        const Packed<X, V> xraw = load_packed<X, V>(x + r * p.ldx + c);
+        const float mu = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = entry(graw, j);
+            dw[j] = fmaf(d, (entry(xraw, j) - mu) * rstd, dw[j]);
+            db[j] += d;
+        }
     }
     float* part = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.D;
-    part[c] = dw;
-    part[p.D + c] = db;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        part[c + j] = dw[j];
+        part[p.D + c + j] = db[j];
+    }
 }
 
 // The sum of the blocks' parts, 32 columns a block, its warps every 32nd part.
@@ -562,15 +596,19 @@ int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cud
         return V == 4 ? backward<G, X, 4, 8>(dy, x, p, sms, s)
                       : backward<G, X, 1, 8>(dy, x, p, sms, s);
     }
-    const int64_t slabs = (p.D + 32 * kLongWarps - 1) / (32 * kLongWarps);
     const int parts = static_cast<int>(most_parts(p.R, p.D, sms));
-    forge_layer_norm_columns_kernel<G, X>
-        <<<dim3(static_cast<unsigned>(slabs), parts), 32 * kLongWarps, 0, s>>>(dy, x, p);
-    const int blocks = blocks_for(p.R, 1, 2LL * sms);
+    auto go = [&](auto v) {
+        constexpr int N = decltype(v)::value;
+        constexpr int slab = 32 * kLongWarps * N;
+        const unsigned slabs = static_cast<unsigned>((p.D + slab - 1) / slab);
+        forge_layer_norm_columns_kernel<G, X, N><<<dim3(slabs, parts), 32 * kLongWarps, 0, s>>>(dy, x, p);
+        forge_layer_norm_grad_long_kernel<G, X, N>
+            <<<blocks_for(p.R, 1, 1024LL / kWideThreads * sms), kWideThreads, 0, s>>>(dy, x, p);
+    };
     if (V == 1)
-        forge_layer_norm_grad_long_kernel<G, X, 1><<<blocks, kLongThreads, 0, s>>>(dy, x, p);
+        go(std::integral_constant<int, 1>());
     else
-        forge_layer_norm_grad_long_kernel<G, X, 4><<<blocks, kLongThreads, 0, s>>>(dy, x, p);
+        go(std::integral_constant<int, 4>());
     return parts;
 }
 

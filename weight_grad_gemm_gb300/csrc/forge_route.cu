@@ -45,7 +45,9 @@ constexpr int kMostWords = 8;
 // 65536 x 256 logits (the whole call): by rounds of the maximum 46 us at k = 1, 51 at 4, 56
 // at 6, 60 at 8 and 71 at 12; by comparing all lanes 52, 54, 56, 59 and 64
 constexpr int kMostRounds = 6;
-constexpr int kFewCounts = 4096;     // blocks x E that every place block scans by itself
+// blocks x E that every place block scans by itself, which spares a launch: 1000 x 16 (2,016)
+// in 10.4 us, with the scan kernel 10.5; 4096 x 64 (8,192) 26.6 and 13.5
+constexpr int kFewCounts = 2048;
 
 struct Args {
     int64_t T, ld;
@@ -790,7 +792,8 @@ template <typename X>
 cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
 {
     // a block's tokens: whole turns of its groups, as many as give every SM four blocks
-    // (which run at once: a fifth would run alone), 32 at least, within the room
+    // (which run at once: a fifth would run alone), 8 at least (1024 x 256: 16.7 us, with 32
+    // 19.9), within the room
     int most = kMostChoices / (32 * p.k);
     if (most > kMostMasks / p.E) most = kMostMasks / p.E;
     if (most > kMostWords) most = kMostWords;
@@ -799,10 +802,11 @@ cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
     while (lanes < 32 && 8 * lanes < p.E) lanes *= 2;
     const int64_t at_once = kThreads / lanes;
     int64_t tokens = (p.T + 4LL * sms - 1) / (4LL * sms);
-    tokens = ((tokens < 32 ? 32 : tokens) + at_once - 1) / at_once * at_once;
-    // one block for up to four turns of its groups: there a second and third launch
-    // cost more than they save
-    if (p.T <= 32 * most && p.T <= 4 * at_once) tokens = p.T;
+    tokens = ((tokens < 8 ? 8 : tokens) + at_once - 1) / at_once * at_once;
+    // one block for up to two turns of its groups: there a second launch costs more than it
+    // saves (256 x 16: 8.3 us, in two launches 10.4; four turns, 128 x 64 and 32 x 256: 15.8
+    // and 16.6, in two or three 12.4 and 13.3)
+    if (p.T <= 32 * most && p.T <= 2 * at_once) tokens = p.T;
     if (tokens > 32 * most) tokens = 32 * most;
     p.tokens = static_cast<int>(tokens < 1 ? 1 : tokens);
     p.words = (p.tokens + 31) / 32;
