@@ -229,37 +229,39 @@ __device__ __forceinline__ void store_row(const LParams& p, int64_t row, int64_t
 // A warp's 32 rows x 128 outputs, a lane a row, from row r0 and column c0 on: through
 // shared memory, 64 bytes of a row at a time, so that four lanes write a row's
 // neighbouring 16 bytes (a lane writing its own row instead, 16 bytes an
-// instruction, took 7,000 cycles a tile).
+// instruction, took 7,000 cycles a tile).  Rows of Y that no 16-byte store can address take
+// a lane an output (3001 x 5003 bf16 by 2777: 84 us, a lane a row 207).
 __device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int64_t r0,
                                            int64_t r_end, int64_t c0, const float (&acc)[128],
                                            int lane)
 {
-    if (!p.vec) {
-        if (r0 + lane < r_end) {
-#pragma unroll
-            for (int j = 0; j < 128; j += 8) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
-                if (c0 + j < p.O) store_row(p, r0 + lane, c0 + j, v);
-            }
-        }
-        return;
-    }
     // the 16-byte unit u of row r lies at place u ^ (r / 2 % 4): no bank conflicts
     uint4* mine = reinterpret_cast<uint4*>(stage) + 4 * lane;
     const int turn = lane >> 1 & 3;
     const int from = lane & 3, down = lane >> 2;
-    auto out = [&](int es, int64_t c) {
+    auto out = [&](auto one, int64_t c) {
+        using U = decltype(one);  // an output's bits
+        constexpr int kUnit = 16 / sizeof(U), kRow = 64 / sizeof(U);
+        U* y = static_cast<U*>(p.Y);
         __syncwarp();
+        if (p.vec) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = 8 * k + down;
-            const uint4 v = reinterpret_cast<const uint4*>(stage)[4 * r + (from ^ (r >> 1 & 3))];
-            const int64_t col = c + from * (16 / es);
-            if (r0 + r < r_end && col < p.O)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.Y) +
-                                          ((r0 + r) * p.O + col) * es) = v;
+            for (int k = 0; k < 4; ++k) {
+                const int r = 8 * k + down;
+                const uint4 v = reinterpret_cast<const uint4*>(stage)[4 * r + (from ^ (r >> 1 & 3))];
+                const int64_t col = c + from * kUnit;
+                if (r0 + r < r_end && col < p.O)
+                    *reinterpret_cast<uint4*>(y + (r0 + r) * p.O + col) = v;
+            }
+        } else {
+            // a lane an output, 32 / kRow rows at once
+            const int in = lane % kRow;
+#pragma unroll 8
+            for (int r = lane / kRow; r < 32; r += 32 / kRow) {
+                const U v = reinterpret_cast<const U*>(
+                    stage)[(4 * r + (in / kUnit ^ (r >> 1 & 3))) * kUnit + in % kUnit];
+                if (r0 + r < r_end && c + in < p.O) y[(r0 + r) * p.O + c + in] = v;
+            }
         }
         __syncwarp();
     };
@@ -271,7 +273,7 @@ __device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int
                 mine[u ^ turn] = make_uint4(
                     __float_as_uint(acc[j + 4 * u]), __float_as_uint(acc[j + 4 * u + 1]),
                     __float_as_uint(acc[j + 4 * u + 2]), __float_as_uint(acc[j + 4 * u + 3]));
-            out(4, c0 + j);
+            out(uint32_t{}, c0 + j);
         }
     } else {
 #pragma unroll
@@ -282,7 +284,7 @@ __device__ __forceinline__ void store_tile(const LParams& p, uint8_t* stage, int
                 mine[u ^ turn] = make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]),
                                             bf16x2(a[4], a[5]), bf16x2(a[6], a[7]));
             }
-            out(2, c0 + j);
+            out(uint16_t{}, c0 + j);
         }
     }
 }
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = rank == 0;  // of the pair: issues its MMAs
     if constexpr (GROUPED) {
         // every CTA of a cluster reads the same offsets and leaves alike
-        if (!group_table<F>(p, offs, begin)) return;
+        if (!group_table<F>(p, offs, begin)) return await_prerequisites();
     }
     int32_t total;
     if constexpr (GROUPED) {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int32_t first = static_cast<int32_t>(blockIdx.x >> 1);
     const int32_t step = static_cast<int32_t>(gridDim.x >> 1);
-    if (first >= total) return;  // (the whole pair)
+    if (first >= total) return await_prerequisites();  // (the whole pair)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::stages; ++s) {
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    await_prerequisites();  // rows copied in front of this launch
 
     if (warp < kEpiWarp0) {
         ptx::registers_down<F::few_regs>();
@@ -603,12 +606,13 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
     int32_t total;
     if constexpr (GROUPED) {
         // every CTA of a cluster reads the same offsets and leaves alike
-        if (!group_table<F>(p, offs, begin)) return;
+        if (!group_table<F>(p, offs, begin)) return await_prerequisites();
         total = begin[p.E];
     } else {
         total = static_cast<int32_t>((p.T + F::rows - 1) / F::rows) * p.tiles_o;
     }
-    if (static_cast<int32_t>(blockIdx.x) >= total) return;  // (the whole cluster)
+    if (static_cast<int32_t>(blockIdx.x) >= total)
+        return await_prerequisites();  // (the whole cluster)
     const Tile tl = tile_of<F, GROUPED>(static_cast<int32_t>(blockIdx.x), p, offs, begin);
     const int32_t k_lo = static_cast<int32_t>(int64_t{p.nk} * rank / split);
     const int32_t n = static_cast<int32_t>(int64_t{p.nk} * (rank + 1) / split) - k_lo;
@@ -638,6 +642,7 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
         // the first stages are on their way while the other warps set up
+        await_prerequisites();  // rows copied in front of this launch
         for (int32_t i = 0; i < F::stages && i < n; ++i) load(i);
     }
     if (warp == 1) {
@@ -858,7 +863,8 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 struct Launch {
     const CUtensorMap &a, &w;
     const LParams& p;
-    int split;  // few tokens: CTAs that share a tile's contraction
+    int split;    // few tokens: CTAs that share a tile's contraction
+    bool staged;  // behind a copy of rows: may start before that ends
     cudaStream_t stream;
 };
 
@@ -875,11 +881,13 @@ cudaError_t launch(const Launch& l)
     if (e != cudaSuccess) return e;
     constexpr int most = F::bytes(GROUPED ? kMaxExperts : 0);
     static_assert(most <= 227 * 1024, "ring and table within one CTA's shared memory");
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = pairs ? 2 : 1;
     attr[0].val.clusterDim.y = pairs ? 1 : l.split;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(threads);
     cfg.attrs = attr;
@@ -910,6 +918,7 @@ cudaError_t launch(const Launch& l)
         cfg.gridDim = dim3(static_cast<unsigned>(total), static_cast<unsigned>(l.split));
     cfg.dynamicSmemBytes = static_cast<size_t>(F::bytes(GROUPED ? l.p.E : 0));
     cfg.stream = l.stream;
+    cfg.numAttrs = l.staged ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, l.a, l.w, l.p);
 }
 
@@ -961,13 +970,79 @@ Choice choose(const LParams& p, int sms)
     return c;
 }
 
+// Rows that TMA, or a 16-byte load, cannot address, copied to 16-byte boundaries: up to
+// three arrays in one launch, behind which the product's starts early (4099 x 4100 codes,
+// their scales and 4096 x 4100 codes: 102 us with the product, by a launch each 112; 16
+// tokens of 4099 to 4101: 23, 39).  A thread builds four chunks of 16 bytes, from words at
+// any byte; what lies behind a row's end within its last word goes into the padding.
+constexpr int kStageThreads = 256, kStageChunks = 4;
+struct StageJob {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t rows, row_bytes, pitch;  // pitch: of dst
+    int64_t block0;                  // the job's first block
+};
+struct StageJobs {
+    StageJob job[3];
+    int n;
+};
+__global__ void __launch_bounds__(kStageThreads) forge_linear_stage_kernel(const StageJobs jobs)
+{
+    let_dependents_start();
+    int which = 0;
+    while (which + 1 < jobs.n && jobs.job[which + 1].block0 <= blockIdx.x) ++which;
+    const StageJob& b = jobs.job[which];
+    const uint32_t per_row = static_cast<uint32_t>((b.row_bytes + 15) / 16);
+    const int64_t first = (blockIdx.x - b.block0) * (kStageThreads * kStageChunks);
+    const int64_t left = b.rows * per_row - first;
+    const int64_t r0 = first / per_row;
+    const uint32_t c0 = static_cast<uint32_t>(first - r0 * per_row);
+    uint4 v[kStageChunks];
+    uint8_t* to[kStageChunks];
+#pragma unroll
+    for (int j = 0; j < kStageChunks; ++j) {
+        const uint32_t i = threadIdx.x + kStageThreads * j;
+        to[j] = nullptr;
+        if (i >= left) continue;
+        const uint32_t down = (c0 + i) / per_row, c = c0 + i - down * per_row;
+        to[j] = b.dst + (r0 + down) * b.pitch + int64_t{16} * c;
+        const uint8_t* from = b.src + (r0 + down) * b.row_bytes + int64_t{16} * c;
+        const int64_t end = b.row_bytes - int64_t{16} * c;
+        const int n = end < 16 ? static_cast<int>(end) : 16;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 3);
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(from - off);
+        uint32_t w[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = 4 * k < off + n ? __ldcs(words + k) : 0u;
+        v[j] = make_uint4(__funnelshift_r(w[0], w[1], 8 * off), __funnelshift_r(w[1], w[2], 8 * off),
+                          __funnelshift_r(w[2], w[3], 8 * off), __funnelshift_r(w[3], w[4], 8 * off));
+    }
+#pragma unroll
+    for (int j = 0; j < kStageChunks; ++j)
+        if (to[j]) *reinterpret_cast<uint4*>(to[j]) = v[j];
+}
+
+cudaError_t stage(StageJobs& jobs, cudaStream_t s)
+{
+    int64_t blocks = 0;
+    for (int i = 0; i < jobs.n; ++i) {
+        StageJob& b = jobs.job[i];
+        constexpr int64_t each = kStageThreads * kStageChunks;
+        b.block0 = blocks;
+        blocks += (b.rows * ((b.row_bytes + 15) / 16) + each - 1) / each;
+    }
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    forge_linear_stage_kernel<<<static_cast<unsigned>(blocks), kStageThreads, 0, s>>>(jobs);
+    return cudaGetLastError();
+}
+
 struct Operands {
     const uint8_t *A, *W;
     int64_t ldA, ldW;  // bytes between rows, multiples of 16
 };
 
 cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams p,
-                const Choice& c, cudaStream_t stream)
+                const Choice& c, bool staged, cudaStream_t stream)
 {
     const int64_t E = p.E > 0 ? p.E : 1;
     CUtensorMap ta, tw;
@@ -976,7 +1051,7 @@ cudaError_t run(const Operands& o, int64_t N, int64_t M, bool transpose, LParams
         return cudaErrorInvalidValue;
     const int cols = c.tokens == 256 ? 256 : 128;
     p.tiles_o = static_cast<int32_t>((p.O + cols - 1) / cols);
-    const Launch l{ta, tw, p, c.split, stream};
+    const Launch l{ta, tw, p, c.split, staged, stream};
     if (p.E > 0)
         return transpose ? launch_form<false, true>(c.tokens, l) : launch_form<true, true>(c.tokens, l);
     return transpose ? launch_form<false, false>(c.tokens, l) : launch_form<true, false>(c.tokens, l);
@@ -1041,26 +1116,31 @@ forge_status linear(const uint8_t* A, const float* sA, const uint8_t* W, const f
         const int64_t s_bytes = stage_s ? whole(pad_s * T) : 0;
         e = scratch_alloc(&scratch, a_bytes + s_bytes + (stage_w ? pad_w * rows_w : 0), s);
         uint8_t* at = static_cast<uint8_t*>(scratch);
-        if (e == cudaSuccess && stage_a) {
-            e = stage_padded_rows(A, at, T, p.K, pad_a, s);
-            o.A = at;
-            o.ldA = pad_a;
-            at += a_bytes;
-        }
-        if (e == cudaSuccess && stage_s) {
-            e = stage_padded_rows(sA, at, T, int64_t{p.nk} * 4, pad_s, s);
-            p.sA = reinterpret_cast<const float*>(at);
-            p.sa_ld = pad_s / 4;
-            p.sa_vec = 1;
-            at += s_bytes;
-        }
-        if (e == cudaSuccess && stage_w) {
-            e = stage_padded_rows(W, at, rows_w, M, pad_w, s);
-            o.W = at;
-            o.ldW = pad_w;
+        StageJobs jobs{};
+        auto copy = [&](const void* src, int64_t rows, int64_t row_bytes, int64_t pitch) {
+            jobs.job[jobs.n++] = {static_cast<const uint8_t*>(src), at, rows, row_bytes, pitch, 0};
+            uint8_t* to = at;
+            at += whole(pitch * rows);
+            return to;
+        };
+        if (e == cudaSuccess) {
+            if (stage_a) {
+                o.A = copy(A, T, p.K, pad_a);
+                o.ldA = pad_a;
+            }
+            if (stage_s) {
+                p.sA = reinterpret_cast<const float*>(copy(sA, T, int64_t{p.nk} * 4, pad_s));
+                p.sa_ld = pad_s / 4;
+                p.sa_vec = 1;
+            }
+            if (stage_w) {
+                o.W = copy(W, rows_w, M, pad_w);
+                o.ldW = pad_w;
+            }
+            e = stage(jobs, s);
         }
     }
-    if (e == cudaSuccess) e = run(o, N, M, transpose != 0, p, c, s);
+    if (e == cudaSuccess) e = run(o, N, M, transpose != 0, p, c, scratch != nullptr, s);
     if (scratch) {
         const cudaError_t fe = scratch_free(scratch, s);
         if (e == cudaSuccess) e = fe;
