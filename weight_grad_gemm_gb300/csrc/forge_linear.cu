@@ -934,7 +934,45 @@ cudaError_t launch_form(int tokens, const Launch& l)
     }
 }
 
-// The tokens of a tile (256: pairs), and the CTAs that share its contraction.
+// Clusters of `split` CTAs, one CTA an SM, that are resident at once: GPCs hold whole
+// clusters (of 152 CTAs in clusters of 2 all are, in clusters of 8 120).
+int resident(int dev, int split, int sms)
+{
+    static int known[64][kMostSplit + 1];  // per device
+    int& n = known[dev & 63][split];
+    int got = __atomic_load_n(&n, __ATOMIC_ACQUIRE);
+    if (got > 0) return got;
+    using F = Few<128>;
+    auto kern = forge_linear_few_kernel<128, false, false>;
+    static_assert(F::ctas == 1, "one CTA an SM");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = split;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, split);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = F::bytes(kMaxExperts);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             F::bytes(kMaxExperts)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess || got < 1) {
+        cudaGetLastError();
+        return sms / split;  // (an estimate; the launch itself reports what is wrong)
+    }
+    __atomic_store_n(&n, got, __ATOMIC_RELEASE);
+    return got;
+}
+
+// The tokens of a tile (256: pairs), and the CTAs that share its contraction: the form and
+// split that take the least time by what was measured.  Pairs: 0.46 us a block and 2.5 a
+// tile, turn by turn, and 5.7 once.  Few tokens, a turn of the resident clusters: 0.55 us a
+// block (128 tokens) and 16 blocks' time for a CTA's start and end, 6 where two CTAs an
+// SM overlap theirs; the joining one block and more with its bytes.  (128 tokens, 5776 x
+// 6048: by two CTAs a tile 22.8 us, by three, not all of them resident, 34.9, by pairs
+// 31.7; 4096 x 14336: by pairs 23, by one CTA a tile 29.)
 struct Choice {
     int tokens, split;
 };
@@ -943,10 +981,9 @@ Choice choose(const LParams& p, int sms)
     const char* env = std::getenv("FORGE_LINEAR_KERNEL");
     const bool pair = env && std::strcmp(env, "pair") == 0;
     const bool few = env && std::strncmp(env, "few", 3) == 0;
+    if (pair) return {256, 1};
     const int64_t experts = p.E > 0 ? (p.E < p.T ? p.E : p.T) : 1;
     const int64_t each = (p.T + experts - 1) / experts;  // tokens of an expert
-    const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
-    if (pair || (!few && each > 64 && pairs >= sms / 8)) return {256, 1};
     Choice c{each <= 16 ? 16 : (each <= 32 ? 32 : (each <= 64 ? 64 : 128)), 1};
     if (few && env[3]) {
         c.split = std::atoi(env + 3);
@@ -954,20 +991,25 @@ Choice choose(const LParams& p, int sms)
         if (c.split > p.nk) c.split = p.nk;
         return c;
     }
-    // The split that takes the fewest turns of the SMs, a CTA's start and end counted as
-    // six blocks, the joining as one and more with its bytes.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return {256, 1};  // (the launch reports it)
+    const bool two = c.tokens <= 64;  // CTAs an SM
     const int64_t tiles = (each + c.tokens - 1) / c.tokens * experts * ((p.O + 127) / 128);
-    const int64_t at_once = static_cast<int64_t>(sms) * (c.tokens <= 64 ? 2 : 1);
     int64_t best = INT64_MAX;
     for (int s = 1; s <= kMostSplit && s <= p.nk; ++s) {
-        const int64_t cost = (tiles * s + at_once - 1) / at_once * ((p.nk + s - 1) / s + 6) +
-                             (s > 1 ? 1 + s * c.tokens / 512 : 0);
+        const int64_t at_once = int64_t{resident(dev, s, sms)} * (two ? 2 : 1);
+        const int64_t cost =
+            (tiles + at_once - 1) / at_once * ((p.nk + s - 1) / s + (two ? 6 : 16)) +
+            (s > 1 ? 1 + s * c.tokens / 512 : 0);
         if (cost < best) {
             best = cost;
             c.split = s;
         }
     }
-    return c;
+    if (few || two) return c;
+    const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
+    const int64_t turns = (pairs + sms / 2 - 1) / (sms / 2);
+    return 570 + turns * (250 + 46 * int64_t{p.nk}) <= 55 * best ? Choice{256, 1} : c;
 }
 
 // Rows that TMA, or a 16-byte load, cannot address, copied to 16-byte boundaries: up to
