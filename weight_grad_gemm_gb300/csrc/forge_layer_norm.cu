@@ -563,9 +563,15 @@ int backward_with(const G* dy, const X* x, const Backward& p, int sms, cudaStrea
     constexpr int bytes = ring_bytes<V, E, W, G, X>();
     auto kernel = forge_layer_norm_grad_kernel<G, X, V, E, W>;
     if (bytes > 16 * 1024) {  // (with the weights beyond what a launch has by itself)
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-            cudaSuccess)
-            return 0;  // (the error stays for the caller)
+        static int ready[64];  // per device (and kernel)
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return 0;  // (the error stays for the caller)
+        if (__atomic_load_n(&ready[dev & 63], __ATOMIC_ACQUIRE) == 0) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+                cudaSuccess)
+                return 0;
+            __atomic_store_n(&ready[dev & 63], 1, __ATOMIC_RELEASE);
+        }
     }
     const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * grad_threads(V, E) / threads);
     kernel<<<blocks, threads, bytes, s>>>(dy, x, p);

@@ -65,7 +65,6 @@ constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kSlots = 2;         // P_b in tensor memory
 constexpr int kStoreBytes = 2048;  // 32 rows x 64 bytes of Y on their way out
 constexpr int kMostSplit = 8;     // CTAs that share a tile's contraction
-constexpr int kFewThreads = 224;  // producer, MMA issuer, four epilogue warps, scales
 constexpr int kScaleRing = 4;     // chunks of four k-blocks' scales
 constexpr int kBand = 8;          // token tiles of a band of the tile walk
 
@@ -93,6 +92,9 @@ struct Few {
     static constexpr int stage_bytes = kStageB + NT * kBlock;
     static constexpr int tmem_cols = slots * NT;
     static constexpr int ctas = NT <= 64 ? 2 : 1;  // an SM
+    // producer, MMA issuer, four or eight epilogue warps (with MINE tokens each), scales
+    static constexpr int groups = NT <= 64 ? 1 : 2, mine = NT / groups;
+    static constexpr int threads = 32 * (3 + 4 * groups);
     static constexpr int pitch = 132;              // floats between the tokens of a share
     static constexpr int scale_at = stages * stage_bytes;
     static constexpr int bar_at = scale_at + kScaleRing * 4 * NT * 4;
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The form for few tokens: a CTA has one tile of 128 outputs x NT tokens and blocks
 // k_lo to k_hi of its contraction; the CTAs of a cluster (along y) have the others.
 template <int NT, bool W_MN, bool GROUPED>
-__global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
+__global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
     forge_linear_few_kernel(const __grid_constant__ CUtensorMap tmA,  // A [T, K], NT rows a box
                             const __grid_constant__ CUtensorMap tmW,  // W [E][N][M]
                             const LParams p)
@@ -644,11 +646,11 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
         }
         for (int b = 0; b < F::slots; ++b) {
             ptx::mbar_init(&tfull[b], 1);
-            ptx::mbar_init(&tempty[b], 4);
+            ptx::mbar_init(&tempty[b], 4 * F::groups);
         }
         for (int c = 0; c < kScaleRing; ++c) {
             ptx::mbar_init(&sfull[c], 1);
-            ptx::mbar_init(&sempty[c], 4);
+            ptx::mbar_init(&sempty[c], 4 * F::groups);
         }
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -666,7 +668,9 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int64_t o = int64_t{tl.o0} + 32 * (warp & 3) + lane;  // an epilogue lane's output
-    float acc[NT];
+    constexpr int C = F::mine;  // tokens of an epilogue warp, from c0 on
+    const int c0 = F::groups == 1 ? 0 : (warp - 2) / 4 * C;
+    float acc[C];
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
@@ -726,12 +730,13 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
                 }
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 2 + 4 * F::groups) {
         // ---------------------------------------------------- epilogue
-        // Warp q: TMEM lanes 32 q .. (outputs); a lane owns one output's NT tokens.
-        const uint32_t mine = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        // Warp (q, g): TMEM lanes 32 q .. (outputs) x columns C g ..; a lane owns one output's
+        // C tokens.
+        const uint32_t mine = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c0;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+        for (int j = 0; j < C; ++j) acc[j] = 0.0f;
         bool ok = true;
 #pragma unroll 1
         for (int32_t i = 0; i < n; ++i) {
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            const float4* f = reinterpret_cast<const float4*>(scales + (c * 4 + i % 4) * NT);
+            const float4* f = reinterpret_cast<const float4*>(scales + (c * 4 + i % 4) * NT + c0);
             const uint32_t from = mine + b * NT;
             auto add = [&](const auto& r, int j0, int N) {
 #pragma unroll
@@ -766,11 +771,11 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
                 add(r, 0, 16);
             } else {
 #pragma unroll
-                for (int h = 0; h < NT / 32; ++h) {
+                for (int h = 0; h < C / 32; ++h) {
                     uint32_t r[32];
                     ptx::tmem_ld_32x32b_x32(from + 32 * h, r);
                     ptx::tmem_ld_wait_for(r);
-                    if (h == NT / 32 - 1) release();
+                    if (h == C / 32 - 1) release();
                     add(r, 32 * h, 32);
                 }
             }
@@ -781,10 +786,10 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
         }
         if (split == 1) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int j = 0; j < C; ++j) {
                 const float one[1] = {acc[j]};
-                if (ok && tl.t0 + j < tl.t_end && o < p.O)
-                    store_as(p.Y, p.f32, (int64_t{tl.t0} + j) * p.O + o, one);
+                if (ok && tl.t0 + c0 + j < tl.t_end && o < p.O)
+                    store_as(p.Y, p.f32, (int64_t{tl.t0} + c0 + j) * p.O + o, one);
             }
         } else {
             // this CTA's share into its ring: the last slot that it waited for was the last
@@ -792,8 +797,8 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
             float* share = reinterpret_cast<float*>(smem) + 32 * (warp & 3) + lane;
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (tl.t0 + j < tl.t_end) share[j * F::pitch] = acc[j];
+                for (int j = 0; j < C; ++j)
+                    if (tl.t0 + c0 + j < tl.t_end) share[(c0 + j) * F::pitch] = acc[j];
             }
         }
     } else {
@@ -843,8 +848,8 @@ __global__ void __launch_bounds__(kFewThreads, Few<NT>::ctas)
             const int32_t tokens = min(NT, tl.t_end - tl.t0);
             const int32_t units = tokens * (F::cols / 4);  // of four outputs
             const uint32_t ring = ptx::smem_addr(smem);
-            for (int32_t u = static_cast<int32_t>(rank) * kFewThreads + threadIdx.x; u < units;
-                 u += static_cast<int32_t>(split) * kFewThreads) {
+            for (int32_t u = static_cast<int32_t>(rank) * F::threads + threadIdx.x; u < units;
+                 u += static_cast<int32_t>(split) * F::threads) {
                 const int32_t j = u / (F::cols / 4), c = u % (F::cols / 4) * 4;
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (uint32_t k = 0; k < split; ++k) {
@@ -886,7 +891,12 @@ template <typename F, bool GROUPED, auto KERN>
 cudaError_t launch(const Launch& l)
 {
     constexpr bool pairs = std::is_same<F, Many>::value;
-    constexpr int threads = pairs ? kThreads : kFewThreads;
+    constexpr int threads = [] {
+        if constexpr (pairs)
+            return kThreads;
+        else
+            return F::threads;
+    }();
     auto kern = KERN;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -964,7 +974,7 @@ int resident(int dev, int split, int sms)
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, split);
-    cfg.blockDim = dim3(kFewThreads);
+    cfg.blockDim = dim3(F::threads);
     cfg.dynamicSmemBytes = F::bytes(kMaxExperts);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
