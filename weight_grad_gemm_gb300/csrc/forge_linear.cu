@@ -36,8 +36,8 @@
 // sums it would be 308 us, with half the loads 326, without the scales' loads 361.
 // Slower were: three slots of 160 columns (517 us), tiles of 128 columns, Y by TMA
 // stores, scales through shared memory, packed pairs of sums, one lane's load and
-// shuffles for the weight's scales (401 to 403).  Few tokens: 16 x 4096 x 14336 16.5 us (3.6
-// TB/s: the weight's 59 MB, and the start and end of two CTAs an SM), 16 x 4096 x 4096 10.5.
+// shuffles for the weight's scales (401 to 403).  Few tokens: 16 x 4096 x 14336 13.1 us (4.5
+// TB/s: the weight's 59 MB, and the start and end of two CTAs an SM), 128 x 14336 x 4096 22.8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -92,9 +92,13 @@ struct Few {
     static constexpr int stage_bytes = kStageB + NT * kBlock;
     static constexpr int tmem_cols = slots * NT;
     static constexpr int ctas = NT <= 64 ? 2 : 1;  // an SM
-    // producer, MMA issuer, four or eight epilogue warps (with MINE tokens each), scales
+    // producer, two MMA issuers, four or eight epilogue warps (`mine` tokens each), scales
+    static constexpr int issuers = 2;
+    static_assert(stages % issuers == 0 && slots % issuers == 0,
+                  "a stage and a slot belong to one issuer, which so waits for each round");
     static constexpr int groups = NT <= 64 ? 1 : 2, mine = NT / groups;
-    static constexpr int threads = 32 * (3 + 4 * groups);
+    static constexpr int epi_warp0 = 1 + issuers;
+    static constexpr int threads = 32 * (epi_warp0 + 4 * groups + 1);
     static constexpr int pitch = 132;              // floats between the tokens of a share
     static constexpr int scale_at = stages * stage_bytes;
     static constexpr int bar_at = scale_at + kScaleRing * 4 * NT * 4;
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
     uint64_t* sfull = tempty + F::slots;
     uint64_t* sempty = sfull + kScaleRing;
     uint64_t* drain = sempty + kScaleRing;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + F::issuers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* scales = reinterpret_cast<float*>(smem + F::scale_at);  // [ring][4][NT]
     int32_t* offs = reinterpret_cast<int32_t*>(smem + F::table_at);
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
             ptx::mbar_init(&sfull[c], 1);
             ptx::mbar_init(&sempty[c], 4 * F::groups);
         }
-        ptx::mbar_init(drain, 1);
+        for (int w = 0; w < F::issuers; ++w) ptx::mbar_init(&drain[w], 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
         // the first stages are on their way while the other warps set up
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
     const uint32_t tmem_base = *tmem_slot;
     const int64_t o = int64_t{tl.o0} + 32 * (warp & 3) + lane;  // an epilogue lane's output
     constexpr int C = F::mine;  // tokens of an epilogue warp, from c0 on
-    const int c0 = F::groups == 1 ? 0 : (warp - 2) / 4 * C;
+    const int c0 = F::groups == 1 ? 0 : (warp - F::epi_warp0) / 4 * C;
     float acc[C];
 
     if (warp == 0) {
@@ -695,8 +699,10 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
                 }
             }
         }
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (lane 0)
+    } else if (warp <= F::issuers) {
+        // ---------------------------------------------------- MMA issuers (lane 0)
+        // Every other block each, as the pairs' (16 tokens of 4096 x 14336: 13.0 us, by one
+        // issuer 16.4; 128 of 14336 x 4096: 22.8, 25.0).
         if (lane == 0) {
             constexpr uint32_t idesc = ptx::make_idesc(0, 0, W_MN, false, 128, NT);
             constexpr uint64_t kStepW = (W_MN ? 32 * 128 : 32) >> 4, kStepA = 32 >> 4;
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
             const uint64_t a_desc = ptx::smem_desc_sw128(ring + kStageB, 16, 1024);
             bool ok = true;
             bool issued_any = false;
-            for (int32_t i = 0; i < n; ++i) {
+            for (int32_t i = warp - 1; i < n; i += F::issuers) {
                 const int s = i % F::stages, b = i % F::slots;
                 ok = wait_often(&full[s], i / F::stages & 1u, abort_flag, p.w) &&
                      wait_often(&tempty[b], (i / F::slots & 1u) ^ 1u, abort_flag, p.w);
@@ -722,15 +728,15 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
                 if (i + F::stages < n) ptx::umma_commit(&empty[s]);  // (a stage that is used again)
             }
             if (!ok && issued_any) {
-                ptx::umma_commit(drain);
-                const uint32_t a = ptx::smem_addr(drain);
+                ptx::umma_commit(&drain[warp - 1]);
+                const uint32_t a = ptx::smem_addr(&drain[warp - 1]);
                 const uint64_t tw = ptx::globaltimer_ns();
                 while (!ptx::mbar_try_wait(a, 0)) {
                     if (static_cast<int64_t>(ptx::globaltimer_ns() - tw) > p.w.timeout_ns) break;
                 }
             }
         }
-    } else if (warp < 2 + 4 * F::groups) {
+    } else if (warp < F::epi_warp0 + 4 * F::groups) {
         // ---------------------------------------------------- epilogue
         // Warp (q, g): TMEM lanes 32 q .. (outputs) x columns C g ..; a lane owns one output's
         // C tokens.
@@ -990,11 +996,12 @@ int resident(int dev, int split, int sms)
 
 // The tokens of a tile (256: pairs), and the CTAs that share its contraction: the form and
 // split that take the least time by what was measured.  Pairs: 0.46 us a block and 2.5 a
-// tile, turn by turn, and 5.7 once.  Few tokens, a turn of the resident clusters: 0.55 us a
-// block (128 tokens) and 16 blocks' time for a CTA's start and end, 6 where two CTAs an
-// SM overlap theirs; the joining one block and more with its bytes.  (128 tokens, 5776 x
-// 6048: by two CTAs a tile 22.8 us, by three, not all of them resident, 34.9, by pairs
-// 31.7; 4096 x 14336: by pairs 23, by one CTA a tile 29.)
+// tile, turn by turn, 5.7 once, and 2.5 where the scales' rows are copied first.  Few
+// tokens, a turn of the resident clusters: 0.46 us a block (128 tokens) and 18 blocks' time
+// for a CTA's start and end, 6 where two CTAs an SM overlap theirs; the joining one block and
+// more with its bytes.  (128 tokens, 5776 x 6048: by two CTAs a tile 20.7 us, by three,
+// not all of them resident, 30.3, by pairs 31.7; 4096 x 14336: by pairs 23.1, by one CTA
+// a tile 23.0.)
 struct Choice {
     int tokens, split;
 };
@@ -1021,7 +1028,7 @@ Choice choose(const LParams& p, int sms)
     for (int s = 1; s <= kMostSplit && s <= p.nk; ++s) {
         const int64_t at_once = int64_t{resident(dev, s, sms)} * (two ? 2 : 1);
         const int64_t cost =
-            (tiles + at_once - 1) / at_once * ((p.nk + s - 1) / s + (two ? 6 : 16)) +
+            (tiles + at_once - 1) / at_once * ((p.nk + s - 1) / s + (two ? 6 : 18)) +
             (s > 1 ? 1 + s * c.tokens / 512 : 0);
         if (cost < best) {
             best = cost;
@@ -1031,7 +1038,8 @@ Choice choose(const LParams& p, int sms)
     if (few || two) return c;
     const int64_t pairs = (each + 255) / 256 * experts * ((p.O + 255) / 256);
     const int64_t turns = (pairs + sms / 2 - 1) / (sms / 2);
-    return 570 + turns * (250 + 46 * int64_t{p.nk}) <= 55 * best ? Choice{256, 1} : c;
+    const int64_t once = p.sa_vec ? 570 : 820;
+    return once + turns * (250 + 46 * int64_t{p.nk}) <= 46 * best ? Choice{256, 1} : c;
 }
 
 // Rows that TMA, or a 16-byte load, cannot address, copied to 16-byte boundaries: up to
