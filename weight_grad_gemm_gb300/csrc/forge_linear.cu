@@ -36,8 +36,9 @@
 // sums it would be 308 us, with half the loads 326, without the scales' loads 361.
 // Slower were: three slots of 160 columns (517 us), tiles of 128 columns, Y by TMA
 // stores, scales through shared memory, packed pairs of sums, one lane's load and
-// shuffles for the weight's scales (401 to 403).  Few tokens: 16 x 4096 x 14336 13.1 us (4.5
-// TB/s: the weight's 59 MB, and the start and end of two CTAs an SM), 128 x 14336 x 4096 22.8.
+// shuffles for the weight's scales (401 to 403).  Few tokens: 16 x 4096 x 14336 16.5 us
+// (3.6 TB/s of the weight's 59 MB, and the start and end of two CTAs an SM; 13.1 where the
+// weight is in L2), 128 x 14336 x 4096 22.8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
