@@ -587,8 +587,10 @@ FORGE_API forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dtyp
  *               loss = E / (k n) sum_e counts[e] P_e.
  * Masked experts are -inf: their p is 0 and they are not chosen.  A token with
  * fewer than k other logits has expert and slot -1 and weight 0 in the places
- * left; a token with none is padding and counts nowhere.  A NaN or +inf among a
- * token's logits makes its weights and the loss NaN.
+ * left; a token with none is padding and counts nowhere.  Finite logits of any
+ * size are taken: a token whose experts are all masked by a finite number (the
+ * type's lowest, say) is no padding and chooses among equals.  A NaN or +inf among
+ * a token's logits makes its weights and the loss NaN.
  *   logits  device [T, E] of dtype (FORGE_BF16 or FORGE_F32), rows ld >= E apart.
  *   k       1 <= k <= min(E, 32);  E <= 1024;  T k < 2^31.
  *   experts (int32), weights (fp32)  device [T, k], written.

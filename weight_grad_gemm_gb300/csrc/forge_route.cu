@@ -87,12 +87,16 @@ __device__ __forceinline__ float value_of(int32_t key)
 }
 constexpr int32_t kNone = static_cast<int32_t>(0x807FFFFF);  // key_of(-inf)
 
-// exp(v - m) from c = -m log2 e.  (c's rounding is a factor that all of a row's have.)
+// exp(v - m), m the row's largest logit.  The subtraction comes first: it is exact to half
+// a step whatever the row's size, and 0 at the largest.  (As fma(v, log2 e, -m log2 e) the
+// second product's rounding stays in the exponent, a factor that all of a row's terms have
+// but that from |m| of some 1e9 on leaves fp32's range; 65536 x 256 to 8 and back takes 86 us
+// either way.)
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp_from(float v, float c)
+__device__ __forceinline__ float exp_from(float v, float m)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(v, kLog2e, c)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((v - m) * kLog2e));
     return y;
 }
 
@@ -338,11 +342,11 @@ __global__ void __launch_bounds__(kThreads)
             top = lanes_max<LPR>(best);
         };
         keys(key_of);
-        const float c = top > kNone ? -value_of(top) * kLog2e : 0.0f;
+        const float m = top > kNone ? value_of(top) : 0.0f;
         float s = 0.0f, exps[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            exps[i] = exp_from(e[i], c);
+            exps[i] = exp_from(e[i], m);
             s += exps[i];
         }
         s = lanes_sum<LPR>(s);
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kThreads)
             if (r < C) {  // (the same for the whole warp)
                 float mine = 0.0f;
                 top_of_warp(key, p.k, lists + warp * 64, [&](int j, int32_t t, int x) {
-                    const float w = t > kNone ? exp_from(value_of(t), c) : 0.0f;
+                    const float w = t > kNone ? exp_from(value_of(t), m) : 0.0f;
                     mine += w;
                     chosen[r * p.k + j] = x;
                     weight[r * p.k + j] = w;
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int j = 0; j < p.k; ++j) {
                 const int32_t t = lanes_max<LPR>(best);
                 const uint32_t who = __ballot_sync(0xffffffffu, best == t) & group;
-                const float w = t > kNone ? exp_from(value_of(t), c) : 0.0f;
+                const float w = t > kNone ? exp_from(value_of(t), m) : 0.0f;
                 sum += w;
                 if (lane == __ffs(who) - 1) {
                     int at = -1;
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, EPL == 8 && LPR >= 8 ? 4 : 1)
         for (int i = 1; i < EPL; ++i) m = nan_max(m, v[i]);
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m == -INFINITY ? 0.0f : -m * kLog2e;  // (a NaN makes all p NaN)
+        const float ref = m == -INFINITY ? 0.0f : m;  // (a NaN makes all p NaN)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // exp, exp c, chosen exp, chosen exp gw
 #pragma unroll
         for (int n = 0; n < kPer; ++n) {
