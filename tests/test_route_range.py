@@ -8,6 +8,10 @@ relatively), so a term is off by |z - max| 2^-22 + 2^-22 relatively; with |z - m
 (below that exp is 0 in fp32 as well: 2^-100 absolutely) that is 2^-15, and a quotient of
 sums of such terms within 2^-14.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -15,6 +19,7 @@ import weight_grad_gemm_gb300 as fg
 from test_route import DT, reference, route
 
 gpu = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SIZES = [(8, 2), (64, 8), (200, 4), (256, 8), (600, 7)]
 SHIFTS = [-1e10, 1e10, -3e10, 2e9, 1e12, -1e30, 1e30, "min", "max"]
 
@@ -118,3 +123,24 @@ def test_padding_by_the_lowest_number_leaves_the_others_alone(cuda_device, dtype
     assert torch.equal(o["weights"][:50], alone["weights"]) and torch.equal(o["experts"][:50], alone["experts"])
     assert torch.equal(o["weights"][50:], torch.full((20, k), 1 / k, device="cuda"))
     assert torch.isfinite(o["loss"]).all()
+
+
+@gpu
+@pytest.mark.parametrize("E,k,tokens", [(496, 7, 200000), (917, 32, 19457), (1024, 16, 64)])
+def test_blocks_whose_shared_memory_is_just_above_the_default(cuda_device, E, k, tokens):
+    """Static and dynamic shared memory count together; in a process of its own, where no other
+    size has asked for more."""
+    code = f"""
+import sys
+sys.path[:0] = [{ROOT!r}, {os.path.join(ROOT, "tests")!r}]
+import torch
+from test_route import route
+g = torch.Generator(device="cuda").manual_seed(1)
+z = torch.randn({tokens}, {E}, device="cuda", generator=g).bfloat16()
+o = route(z, {k}, True)
+want = torch.sort(z.float(), dim=1, descending=True, stable=True).indices[:, :{k}]
+assert torch.equal(o["experts"].long(), want)
+assert torch.equal(o["counts"].long(), torch.bincount(want.reshape(-1), minlength={E}))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(kThreads)
     float* inverse = weight + C * p.k;                                  // [C]
     uint32_t* mask = reinterpret_cast<uint32_t*>(inverse + C);          // [words][E]
     float* mass = reinterpret_cast<float*>(mask + p.words * p.E);       // [warps][E]
-    int32_t* offs = reinterpret_cast<int32_t*>(mass + kWarps * p.E);    // ONE: [E + 1]
-    __shared__ int32_t lives[kWarps];
+    int32_t* lives = reinterpret_cast<int32_t*>(mass + kWarps * p.E);   // [warps]
+    int32_t* offs = lives + kWarps;                                     // ONE: [E + 1]
 
     constexpr int G = kThreads / LPR;  // tokens at once
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -824,8 +824,9 @@ cudaError_t forward(const X* logits, Args p, int sms, cudaStream_t s)
     p.blocks = static_cast<int32_t>(blocks < 1 ? 1 : blocks);
     const bool one = p.blocks == 1, place = p.slots || p.rows;
     const size_t C = p.tokens, E = p.E;
-    const size_t tokens_smem = 8 * kWarps * 32 +
-                               4 * (2 * C * p.k + C + p.words * E + kWarps * E + (one ? E + 1 : 0));
+    // (all of the tokens kernel's shared memory: static arrays would count in the 48 KB too)
+    const size_t tokens_smem = 8 * kWarps * 32 + 4 * (2 * C * p.k + C + p.words * E + kWarps * E +
+                                                      kWarps + (one ? E + 1 : 0));
     void* scratch = nullptr;
     cudaError_t e = cudaSuccess;
     if (!one) {
