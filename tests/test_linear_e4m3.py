@@ -382,3 +382,41 @@ def test_binding_refuses_what_does_not_fit(cuda_device):
         fg.forge_quantize_e4m3_blocks(Y, A, sA)
     with pytest.raises(ValueError):
         fg.forge_quantize_e4m3_blocks(Y, torch.empty(8, 48, dtype=F8, device="cuda"), sA, block_rows=64)
+
+
+def test_copied_scales_are_read_by_plain_loads():
+    """The product starts while its rows and scales are still copied, and read-only loads ask
+    for data that nothing writes while the reading kernel lives."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(fg.__file__), "csrc", "forge_linear.cu")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    assert "ld.global.nc" not in code
+    pair, few = code.split("forge_linear_few_kernel(", 1)
+    assert not re.findall(r"__ld(?:g|cs|cg|lu)\(", pair[pair.index("forge_linear_kernel("):])
+    assert few
+
+
+@gpu
+@pytest.mark.parametrize("T,N,M", [(700, 300, 256), (1300, 640, 272), (900, 1201, 500)])
+def test_calls_one_after_another_see_their_own_copies(cuda_device, T, N, M):
+    """Calls on one stream without a wait share their scratch: what one reads of its copied
+    scales and rows must not be what the call before left there."""
+    sets = [operands(T, N, M, False, seed=s) for s in range(6)]
+    for s, (A, sA, W, sW) in enumerate(sets):
+        sA.mul_(2.0 ** s)
+    alone, together = [], [torch.full((T, M), 9.0, device="cuda") for _ in sets]
+    for ops in sets:
+        Y = torch.empty(T, M, device="cuda")
+        fg.forge_linear_e4m3(*ops, Y)
+        torch.cuda.synchronize()
+        want, mag = products(*ops, False)
+        assert torch.all((Y.double() - want).abs() <= (2.0 ** -15 + (blocks(N) + 12) * 2.0 ** -24) * mag)
+        alone.append(Y)
+    for _ in range(3):
+        for ops, Y in zip(sets, together):
+            fg.forge_linear_e4m3(*ops, Y)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, together))
+        for Y in together:
+            Y.fill_(9.0)

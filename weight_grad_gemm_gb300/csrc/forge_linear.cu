@@ -212,19 +212,21 @@ __device__ bool group_table(const LParams& p, int32_t* offs, int32_t* begin)
 }
 
 // Loads that stay where they are written: the compiler moves an ordinary load
-// down to its first use, and the wait for it with it.
+// down to its first use, and the wait for it with it.  Plain, not read-only ones: scales whose
+// rows are copied in front are still being written when this kernel starts.
 __device__ __forceinline__ float load_early(const float* p)
 {
     float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
     return v;
 }
 __device__ __forceinline__ float4 load4_early(const float* p)
 {
     float4 v;
-    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
