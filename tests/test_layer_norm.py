@@ -364,3 +364,14 @@ def test_binding_refuses_what_does_not_fit(cuda_device):
         fg.forge_layer_norm(X, w, None, X, eps=0.0)
     with pytest.raises(ValueError):
         fg.forge_layer_norm_grad(X, X[:3], w, w[:4], w[:4], X, w, None)
+
+
+def test_rows_that_may_be_written_over_are_read_by_plain_loads():
+    """y may be x, and dx may be dy or x: read-only loads (load_packed, and pointers that promise
+    no overlap) ask for data that nothing writes while the kernel lives."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(fg.__file__), "csrc", "forge_layer_norm.cu")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    assert not re.findall(r"load_packed<[GX],", code)
+    assert not re.findall(r"const [GX]\* __restrict__", code)

@@ -364,3 +364,15 @@ def test_binding_refuses_what_does_not_fit(cuda_device):
         fg.forge_moe_route_grad(z, o["experts"], o["counts"], o["live"], z[:, :7])
     with pytest.raises(fg.ForgeError):
         fg.forge_moe_route(z[:, :1], o["experts"], o["weights"], o["counts"][:1], o["offsets"][:2])
+
+
+def test_logits_that_may_be_written_over_are_read_by_plain_loads():
+    """dlogits may be the logits: read-only loads ask for data that nothing writes while the
+    kernel lives."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(fg.__file__), "csrc", "forge_route.cu")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    grad = code[code.index("forge_route_grad_kernel("):]
+    assert not re.findall(r"load_packed<X,", code[code.index("load_logits("):code.index("make_masks(")])
+    assert "load_packed<X," not in grad and "__restrict__" not in grad

@@ -73,7 +73,7 @@ struct Backward {
 // two rows at a time 48; 2 x the threads and half the registers 56).
 template <typename X, int V, int E, int W, int RB>
 __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threads_of(W) : 1)
-    forge_layer_norm_kernel(const X* __restrict__ x, const Forward p)
+    forge_layer_norm_kernel(const X* x, const Forward p)
 {
     constexpr int NV = E / V;
     __shared__ float sh[2][W * RB];
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * W * 32 + t) * V;
-                next[k][i] = c < p.D && r + k < p.R ? load_packed<X, V>(x + (r + k) * p.ldx + c)
+                next[k][i] = c < p.D && r + k < p.R ? load_plain<X, V>(x + (r + k) * p.ldx + c)
                                                     : zero_packed<X, V>();
             }
     };
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
 // third from L2.
 template <typename X, int V>
 __global__ void __launch_bounds__(kLongThreads)
-    forge_layer_norm_long_kernel(const X* __restrict__ x, const Forward p)
+    forge_layer_norm_long_kernel(const X* x, const Forward p)
 {
     __shared__ float sh[2][kLongThreads / 32];
     const float inv = 1.0f / static_cast<float>(p.D);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kLongThreads)
         const X* row = x + r * p.ldx;
         float s[1] = {0.0f};
         for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_packed<X, V>(row + c);
+            const Packed<X, V> raw = load_plain<X, V>(row + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) s[0] += entry(raw, j);
         }
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kLongThreads)
         const float mu = s[0] * inv;
         float q[1] = {0.0f};
         for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_packed<X, V>(row + c);
+            const Packed<X, V> raw = load_plain<X, V>(row + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float d = entry(raw, j) - mu;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kLongThreads)
             if (p.rstd) p.rstd[r] = rstd;
         }
         for (int64_t c = threadIdx.x * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_packed<X, V>(row + c);
+            const Packed<X, V> raw = load_plain<X, V>(row + c);
             const Packed<float, V> w = load_packed<float, V>(p.weight + c);
             const Packed<float, V> b =
                 p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
@@ -224,7 +224,7 @@ constexpr int ring_bytes()
 }
 template <typename G, typename X, int V, int E, int W>
 __global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of(W))
-    forge_layer_norm_grad_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+    forge_layer_norm_grad_kernel(const G* dy, const X* x,
                                  const Backward p)
 {
     constexpr int NV = E / V;
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = i * W * 32 + t;
-                gnext[i] = c < p.D ? load_packed<G, V>(dy + r * p.ldg + c) : zero_packed<G, V>();
-                xnext[i] = c < p.D ? load_packed<X, V>(x + r * p.ldx + c) : zero_packed<X, V>();
+                gnext[i] = c < p.D ? load_plain<G, V>(dy + r * p.ldg + c) : zero_packed<G, V>();
+                xnext[i] = c < p.D ? load_plain<X, V>(x + r * p.ldx + c) : zero_packed<X, V>();
             }
         } else {
             Packed<G, V>* g;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of
 // eight vectors of its twice as many registers 158).
 template <typename G, typename X, int V>
 __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
-    forge_layer_norm_grad_long_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+    forge_layer_norm_grad_long_kernel(const G* dy, const X* x,
                                       const Backward p)
 {
     constexpr int kHeld = sizeof(G) + sizeof(X) <= 4 ? 8 : 4;  // (registers)
@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int64_t c = c0 + i * step;
-            gheld[i] = c < p.D ? load_packed<G, V>(grow + c) : zero_packed<G, V>();
-            xheld[i] = c < p.D ? load_packed<X, V>(xrow + c) : zero_packed<X, V>();
+            gheld[i] = c < p.D ? load_plain<G, V>(grow + c) : zero_packed<G, V>();
+            xheld[i] = c < p.D ? load_plain<X, V>(xrow + c) : zero_packed<X, V>();
         }
         const float mu = p.mean[r], rstd = p.rstd[r];
         float s[2] = {0.0f, 0.0f};
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
         for (int i = 0; i < kHeld; ++i)
             if (c0 + i * step < p.D) add(gheld[i], xheld[i], c0 + i * step);
         for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
-            add(load_packed<G, V>(grow + c), load_packed<X, V>(xrow + c), c);
+            add(load_plain<G, V>(grow + c), load_plain<X, V>(xrow + c), c);
         block_sums<kWideThreads / 32>(s, sh[turn]);
         const float a = s[0] * inv, b = s[1] * inv;
         auto store = [&](const Packed<G, V>& graw, const Packed<X, V>& xraw, int64_t c) {
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
         for (int i = 0; i < kHeld; ++i)
             if (c0 + i * step < p.D) store(gheld[i], xheld[i], c0 + i * step);
         for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
-            store(load_packed<G, V>(grow + c), load_packed<X, V>(xrow + c), c);
+            store(load_plain<G, V>(grow + c), load_plain<X, V>(xrow + c), c);
     }
 }
 
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
 constexpr int kLongWarps = 4;
 template <typename G, typename X, int V>
 __global__ void __launch_bounds__(32 * kLongWarps)
-    forge_layer_norm_columns_kernel(const G* __restrict__ dy, const X* __restrict__ x,
+    forge_layer_norm_columns_kernel(const G* dy, const X* x,
                                     const Backward p)
 {
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * (32 * kLongWarps) + threadIdx.x) * V;
@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(32 * kLongWarps)
     for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
 #pragma unroll 4
     for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
-        const Packed<G, V> graw = load_packed<G, V>(dy + r * p.ldg + c);
-        const Packed<X, V> xraw = load_packed<X, V>(x + r * p.ldx + c);
+        const Packed<G, V> graw = load_plain<G, V>(dy + r * p.ldg + c);
+        const Packed<X, V> xraw = load_plain<X, V>(x + r * p.ldx + c);
         const float mu = p.mean[r], rstd = p.rstd[r];
 #pragma unroll
         for (int j = 0; j < V; ++j) {

@@ -121,14 +121,14 @@ __device__ __forceinline__ void load_logits(float (&v)[EPL], const X* row, int x
     if (vec && in && x + EPL <= E) {
 #pragma unroll
         for (int i = 0; i < EPL; i += V) {
-            const Packed<X, V> q = load_packed<X, V>(row + x + i);
+            const Packed<X, V> q = load_plain<X, V>(row + x + i);
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i + j] = entry(q, j);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            v[i] = in && x + i < E ? entry(load_packed<X, 1>(row + x + i), 0) : -INFINITY;
+            v[i] = in && x + i < E ? entry(load_plain<X, 1>(row + x + i), 0) : -INFINITY;
     }
 }
 
@@ -657,7 +657,7 @@ __device__ __forceinline__ void sum_four(float (&s)[4])
 // take its choices (each loads its expert's logit for itself) then write theirs over it.
 template <typename X, int LPR, int EPL>
 __global__ void __launch_bounds__(kThreads, EPL == 8 && LPR >= 8 ? 4 : 1)
-    forge_route_grad_kernel(const X* __restrict__ logits, const GradArgs p)
+    forge_route_grad_kernel(const X* logits, const GradArgs p)
 {
     constexpr int G = kThreads / LPR;
     constexpr int kMost = LPR * EPL < kMaxTop ? LPR * EPL : kMaxTop;  // k <= E <= LPR EPL
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, EPL == 8 && LPR >= 8 ? 4 : 1)
         for (int n = 0; n < kPer; ++n) {
             xs[n] = xs_ahead[n] < p.E ? xs_ahead[n] : -1;
             gws[n] = gws_ahead[n];
-            es[n] = xs[n] >= 0 ? entry(load_packed<X, 1>(row + xs[n]), 0) : 0.0f;
+            es[n] = xs[n] >= 0 ? entry(load_plain<X, 1>(row + xs[n]), 0) : 0.0f;
         }
         load(t + step);
         float m = v[0];

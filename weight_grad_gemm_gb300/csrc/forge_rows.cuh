@@ -18,7 +18,8 @@ struct alignas(V * sizeof(T) >= 16 ? 16 : (V * sizeof(T) == 8 ? 8 : 4)) Packed {
     uint32_t w[kWords];
 };
 
-// From an address aligned to the vector, at most 16 bytes an instruction.
+// From an address aligned to the vector, at most 16 bytes an instruction.  Read-only
+// loads: for what nothing writes while the kernel lives.
 template <typename T, int V>
 __device__ __forceinline__ Packed<T, V> load_packed(const T* p)
 {
@@ -35,6 +36,32 @@ __device__ __forceinline__ Packed<T, V> load_packed(const T* p)
 #pragma unroll
         for (int i = 0; i < r.kWords / 4; ++i) {
             const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            r.w[4 * i] = u.x;
+            r.w[4 * i + 1] = u.y;
+            r.w[4 * i + 2] = u.z;
+            r.w[4 * i + 3] = u.w;
+        }
+    }
+    return r;
+}
+
+// The same by plain loads: for rows that the kernel itself may write over (calls in place).
+template <typename T, int V>
+__device__ __forceinline__ Packed<T, V> load_plain(const T* p)
+{
+    Packed<T, V> r;
+    if constexpr (r.kBytes == 2) {
+        r.w[0] = *reinterpret_cast<const unsigned short*>(p);
+    } else if constexpr (r.kBytes == 4) {
+        r.w[0] = *reinterpret_cast<const unsigned int*>(p);
+    } else if constexpr (r.kBytes == 8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = u.x;
+        r.w[1] = u.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < r.kWords / 4; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(p)[i];
             r.w[4 * i] = u.x;
             r.w[4 * i + 1] = u.y;
             r.w[4 * i + 2] = u.z;
