@@ -420,3 +420,26 @@ def test_calls_one_after_another_see_their_own_copies(cuda_device, T, N, M):
         assert all(torch.equal(a, b) for a, b in zip(alone, together))
         for Y in together:
             Y.fill_(9.0)
+
+
+@gpu
+@pytest.mark.parametrize("br", [1, 128])
+@pytest.mark.parametrize("dtype,C,ldx", [("f32", 256, 256), ("f32", 255, 255), ("bf16", 256, 256), ("bf16", 260, 260), ("bf16", 255, 257)])
+def test_codes_keep_the_sign_of_zero(cuda_device, C, ldx, dtype, br):
+    """Bit for bit the recipe's codes, -0 (0x80) among them, whatever the block's scale: in
+    ordinary blocks, in blocks whose scale is too small or too large for quotients by
+    corrections, and in blocks of zeros."""
+    g = torch.Generator().manual_seed(C)
+    x = torch.randn(3 * 128, ldx, generator=g)
+    x[torch.rand(x.shape, generator=g) < 0.3] = -0.0
+    x[torch.rand(x.shape, generator=g) < 0.1] = 0.0
+    x[::7] *= 1e-5  # (codes that round to -0)
+    x[128:256] *= 2.0 ** -100
+    x[130] = -0.0
+    x[256:] *= 2.0 ** 100
+    x = x.to(DT[dtype]).cuda()[:, :C]
+    codes, scales = quantize(x, br)
+    want, ws = recipe(x, br)
+    assert torch.equal(scales.cpu(), ws)
+    assert (want.view(torch.uint8) == 0x80).any()
+    assert torch.equal(codes.cpu().view(torch.uint8), want.view(torch.uint8))

@@ -76,8 +76,10 @@ __device__ __forceinline__ void store_codes(uint8_t* out, const Packed<X, V>& x,
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         q[j] = entry(x, j) * by.r;
-        q[j] = fmaf(fmaf(-q[j], by.s, entry(x, j)), by.r, q[j]);
-        q[j] = fmaf(fmaf(-q[j], by.s, entry(x, j)), by.r, q[j]);
+        // (the remainder with its sign turned: it is +0 where q s = x, and taking +0 from q
+        // leaves -0 as it is, which adding it does not)
+        q[j] = fmaf(-fmaf(q[j], by.s, -entry(x, j)), by.r, q[j]);
+        q[j] = fmaf(-fmaf(q[j], by.s, -entry(x, j)), by.r, q[j]);
     }
     if (!by.fast) {
 #pragma unroll 1
