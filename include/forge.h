@@ -538,8 +538,10 @@ FORGE_API forge_status forge_clip_grads(const void* const* grads, const int64_t*
  *           y_dtype and ldy equal x_dtype and ldx; rows that share memory in any
  *           other way are refused (FORGE_ERR_INVALID_ARG).
  *   mean, rstd  device fp32 [R], written for the gradient; each may be NULL.
- * Statistics are taken in fp32, the deviations from the row's own mean.  A row
- * with a NaN or an infinity gives NaN.  Allocates nothing.  R = 0 does nothing.
+ * Statistics are taken in fp32, the deviations from the row's own mean; finite rows
+ * of any size are taken (where a sum passes the largest number, at a fraction of
+ * their size).  A row with a NaN or an infinity gives NaN.  Allocates nothing.  R = 0
+ * does nothing.
  */
 FORGE_API forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int64_t ldx,
                                         const float* weight, const float* bias, int64_t R,
@@ -552,7 +554,8 @@ FORGE_API forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int6
  *   dx = rstd (g - mean_row(g) - xh mean_row(g xh)),
  *   dweight = sum_r dy xh,   dbias = sum_r dy   (+ what is there if accumulate).
  *   dy, x   device [R, D], each FORGE_BF16 or FORGE_F32, rows lddy, ldx >= D apart.
- *   weight  device fp32 [D];  mean, rstd  device fp32 [R], from forge_layer_norm.
+ *   weight  device fp32 [D];  mean, rstd  device fp32 [R], from forge_layer_norm
+ *           (x - mean has to be a number of fp32).
  *   dx      device [R, D] of dx_dtype, rows lddx >= D apart, written.  It may be dy
  *           or x itself where type and row distance agree; rows that share
  *           memory in any other way are refused.

@@ -375,3 +375,41 @@ def test_rows_that_may_be_written_over_are_read_by_plain_loads():
     code = re.sub(r"//[^\n]*", "", open(path).read())
     assert not re.findall(r"load_packed<[GX],", code)
     assert not re.findall(r"const [GX]\* __restrict__", code)
+
+
+@gpu
+@pytest.mark.parametrize("x,y", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D", [2, 65, 256, 500, 1024, 2000, 4096, 8192, 16384, 16400, 20001])
+def test_rows_whose_squares_pass_the_largest_number(cuda_device, D, x, y):
+    """Finite rows keep their results up to the type's largest numbers: the deviations' squares,
+    and the sum of the row itself, may pass fp32's range.  The bound of ordinary rows holds:
+    it is relative to the row's size.  (rstd of the largest rows is below 2^-126, where
+    fp32's step is 2^-149.)"""
+    X = make(9, D, x, seed=D, mean=0.0).float()
+    for r, size in ((1, 1e18), (2, 3e19), (3, 1e25), (5, 1e30), (6, 3e37), (7, 1e38)):
+        X[r] = X[r].clamp(-3, 3) * size
+    X[8] = torch.finfo(DT[x]).max
+    X[8, 0] = 0.0
+    X = X.to(DT[x])
+    w, b = params(D)
+    Y = torch.empty(9, D, dtype=DT[y], device="cuda")
+    mean, rstd = torch.empty(9, device="cuda"), torch.empty(9, device="cuda")
+    fg.forge_layer_norm(X, w, b, Y, mean=mean, rstd=rstd, eps=EPS)
+    check_forward(X, w, b, Y, mean, None)
+    _, _, rs, _ = reference(X, w, b)
+    off = tree(D) * X.double().abs().mean(1) * rs
+    assert torch.all((rstd.double() - rs).abs() <= (tree(D) + 8 * U + off ** 2) * rs + 2.0 ** -149)
+    Z = X.clone()
+    if x == y:
+        fg.forge_layer_norm(Z, w, b, Z, eps=EPS)  # in place
+        assert torch.equal(Z, Y)
+    bad = X.clone()
+    bad[1, 0], bad[3, D - 1], bad[5, 0] = float("inf"), -float("inf"), float("nan")
+    fg.forge_layer_norm(bad, w, b, Y, mean=mean, rstd=rstd, eps=EPS)
+    assert torch.isnan(Y[[1, 3, 5]]).all()
+    good = torch.tensor([0, 2, 4, 6, 7, 8], device="cuda")
+    check_forward(X[good], w, b, Y[good], mean[good], None)
+    calm = torch.tensor([0, 4], device="cuda")  # bitwise as without such rows beside them
+    alone = torch.empty(2, D, dtype=DT[y], device="cuda")
+    fg.forge_layer_norm(X[calm], w, b, alone, eps=EPS)
+    assert torch.equal(Y[calm], alone)
