@@ -563,8 +563,8 @@ FORGE_API forge_status forge_layer_norm(const void* x, forge_dtype x_dtype, int6
  *           (accumulate != 0).  R = 0 writes zeros (or adds nothing).
  * Sums over the rows are taken in fp32 in an order that the sizes alone
  * determine: bitwise reproducible on one GPU.  They take stream-ordered scratch from the
- * library's memory pool (at most 16 blocks an SM x 2 D floats); a failed
- * allocation returns FORGE_ERR_CUDA.
+ * library's memory pool (at most 64 KB an SM, or 512 bytes a column where D > 8192);
+ * a failed allocation returns FORGE_ERR_CUDA.
  */
 FORGE_API forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dtype, int64_t lddy,
                                              const void* x, forge_dtype x_dtype, int64_t ldx,

@@ -413,3 +413,36 @@ def test_rows_whose_squares_pass_the_largest_number(cuda_device, D, x, y):
     alone = torch.empty(2, D, dtype=DT[y], device="cuda")
     fg.forge_layer_norm(X[calm], w, b, alone, eps=EPS)
     assert torch.equal(Y[calm], alone)
+
+
+@gpu
+@pytest.mark.parametrize("D,dtype", [(4096, "bfloat16"), (8192, "float32"), (64, "float32")])
+def test_scratch_of_the_gradient_is_what_its_blocks_write(cuda_device, D, dtype):
+    """The library's pool keeps what it has reserved: a block's parts are 2 D floats, and the
+    blocks that run at once have 64 KB an SM of them (10 MB of 152 SMs; the pool
+    reserves in steps of 32 MB).  In a process of its own, whose pool is new."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"""
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import weight_grad_gemm_gb300 as fg
+R, D = 16384, {D}
+x = torch.randn(R, D, device="cuda").to(torch.{dtype})
+w, dw, db = torch.ones(3, D, device="cuda")
+mean, rstd = torch.zeros(R, device="cuda"), torch.ones(R, device="cuda")
+dx = torch.empty_like(x)
+def run(n):
+    fg.forge_layer_norm_grad(x[:n], x[:n], w, mean[:n], rstd[:n], dx[:n], dw, db)
+    torch.cuda.synchronize()
+run(1)
+before = torch.cuda.mem_get_info()[0]
+run(R)
+used = before - torch.cuda.mem_get_info()[0]
+assert used <= 40 << 20, used
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -64,7 +64,7 @@ struct Backward {
     const float *weight, *mean, *rstd;
     void* dx;
     bool dx_f32;
-    float* part;  // [blocks][2][D]
+    float* part;  // [blocks][2][D]; null: launch nothing, tell how many blocks write one
 };
 
 // A row by 32 W threads (thread t of them) in three passes, the second and third from L2.
@@ -588,13 +588,15 @@ void forward(const X* x, const Forward& p, int sms, cudaStream_t s)
             <<<blocks_for(p.R, 1, 2LL * sms), kLongThreads, 0, s>>>(x, p);
 }
 
-// The rows in registers; returns the number of parts of dw and db: a block has two rows
-// at least, so that few rows leave few parts to add.
+// The rows in registers; returns the number of parts of dw and db (0 with an error): a block
+// has two rows at least, so that few rows leave few parts to add.
 template <typename G, typename X, int V, int E, int W>
 int backward_with(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s)
 {
     constexpr int teams = W == 1 ? kRowWarps : 1, threads = threads_of(W);
     constexpr int bytes = ring_bytes<V, E, W, G, X>();
+    const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * grad_threads(V, E) / threads);
+    if (!p.part) return blocks;
     auto kernel = forge_layer_norm_grad_kernel<G, X, V, E, W>;
     if (bytes > 16 * 1024) {  // (with the weights beyond what a launch has by itself)
         static int ready[64];  // per device (and kernel)
@@ -607,7 +609,6 @@ int backward_with(const G* dy, const X* x, const Backward& p, int sms, cudaStrea
             __atomic_store_n(&ready[dev & 63], 1, __ATOMIC_RELEASE);
         }
     }
-    const int blocks = blocks_for(p.R, 2 * teams, static_cast<int64_t>(sms) * grad_threads(V, E) / threads);
     kernel<<<blocks, threads, bytes, s>>>(dy, x, p);
     return blocks;
 }
@@ -624,13 +625,7 @@ int backward(const G* dy, const X* x, const Backward& p, int sms, cudaStream_t s
     return backward_with<G, X, V, 16, 16>(dy, x, p, sms, s);
 }
 
-// Most parts that backward() or the column kernel writes.
-int64_t most_parts(int64_t R, int64_t D, int sms)
-{
-    const int64_t most = D > kMaxBackward ? 64 : static_cast<int64_t>(sms) * (1024 / 64);
-    return R < most ? R : most;
-}
-
+constexpr int kColumnParts = 64;  // of the column kernel at most
 template <typename G, typename X>
 int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cudaStream_t s)
 {
@@ -641,7 +636,8 @@ int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cud
         return V == 4 ? backward<G, X, 4, 8>(dy, x, p, sms, s)
                       : backward<G, X, 1, 8>(dy, x, p, sms, s);
     }
-    const int parts = static_cast<int>(most_parts(p.R, p.D, sms));
+    const int parts = blocks_for(p.R, 1, kColumnParts);
+    if (!p.part) return parts;
     auto go = [&](auto v) {
         constexpr int N = decltype(v)::value;
         constexpr int slab = 32 * kLongWarps * N;
@@ -744,29 +740,35 @@ extern "C" forge_status forge_layer_norm_grad(const void* dy, forge_dtype dy_dty
                           dweight,                dbias};
     if ((st = device_resident(ptrs, 8)) != FORGE_OK) return st;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    void* scratch = nullptr;
-    if (R > 0 && scratch_alloc(&scratch, most_parts(R, D, sms) * 2 * D * sizeof(float), s) !=
-                     cudaSuccess) {
-        cudaGetLastError();
-        return FORGE_ERR_CUDA;
-    }
-    const Backward p{R,    D,  lddy, ldx, lddx, weight, mean,
-                     rstd, dx, dx_dtype == FORGE_F32, static_cast<float*>(scratch)};
     const bool wide = dy_dtype == FORGE_BF16 && x_dtype == FORGE_BF16 && D <= kMaxBackward;
     int V = wide ? 8 : 4;
     if (D % V != 0 || !rows_fit(dy, size_of(dy_dtype), lddy, V) ||
         !rows_fit(x, size_of(x_dtype), ldx, V) || !rows_fit(dx, size_of(dx_dtype), lddx, V) ||
         !aligned(weight, 16))
         V = 1;
-    int parts = 0;
-    if (R > 0) {
+    Backward p{R,    D,  lddy, ldx, lddx, weight, mean,
+               rstd, dx, dx_dtype == FORGE_F32, nullptr};
+    auto backward_of = [&]() {
         auto by_x = [&](auto* g) {
             return x_dtype == FORGE_F32
                        ? backward_any(g, static_cast<const float*>(x), p, V, sms, s)
                        : backward_any(g, static_cast<const __nv_bfloat16*>(x), p, V, sms, s);
         };
-        parts = dy_dtype == FORGE_F32 ? by_x(static_cast<const float*>(dy))
-                                      : by_x(static_cast<const __nv_bfloat16*>(dy));
+        return dy_dtype == FORGE_F32 ? by_x(static_cast<const float*>(dy))
+                                     : by_x(static_cast<const __nv_bfloat16*>(dy));
+    };
+    // scratch for the parts that are written, and no more: the pool keeps what it has given
+    // once (16384 x 4096 bf16: 10 MB; sixteen blocks an SM, which only rows of at
+    // most 512 entries have, would be 80)
+    void* scratch = nullptr;
+    int parts = R > 0 ? backward_of() : 0;
+    if (R > 0) {
+        if (scratch_alloc(&scratch, sizeof(float) * 2 * D * parts, s) != cudaSuccess) {
+            cudaGetLastError();
+            return FORGE_ERR_CUDA;
+        }
+        p.part = static_cast<float*>(scratch);
+        parts = backward_of();
     }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
