@@ -443,3 +443,33 @@ def test_codes_keep_the_sign_of_zero(cuda_device, C, ldx, dtype, br):
     assert torch.equal(scales.cpu(), ws)
     assert (want.view(torch.uint8) == 0x80).any()
     assert torch.equal(codes.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@gpu
+def test_scales_laid_out_another_way_are_refused(cuda_device):
+    """[blocks, T] holds as many scales as [T, blocks], and other libraries keep them so."""
+    T, N, M, E = 8, 512, 384, 3
+    A, sA, W, sW = operands(T, N, M, False)
+    Y = torch.empty(T, M, device="cuda")
+    turned = lambda s: s.transpose(-1, -2).contiguous()  # noqa: E731
+    for args in ((A, turned(sA), W, sW, Y), (A, sA, W, turned(sW), Y), (A, sA[:, None], W, sW, Y)):
+        with pytest.raises(ValueError):
+            fg.forge_linear_e4m3(*args)
+    fg.forge_linear_e4m3(A, sA, W, sW, Y)
+    flat = torch.empty_like(Y)
+    fg.forge_linear_e4m3(A, sA.reshape(-1), W, sW.reshape(-1), flat)
+    assert torch.equal(flat, Y)
+    offsets = torch.tensor([0, 2, 5, 8], dtype=torch.int32, device="cuda")
+    A, sA, W, sW = operands(T, N, M, False, E)
+    for a, w in ((turned(sA), sW), (sA, turned(sW)), (sA, sW.permute(1, 2, 0).contiguous())):
+        with pytest.raises(ValueError):
+            fg.forge_grouped_linear_e4m3(A, a, W, w, offsets, Y)
+    x = torch.randn(300, 512, device="cuda")
+    codes = torch.empty(x.shape, dtype=F8, device="cuda")
+    for br, shape in ((1, (4, 300)), (128, (4, 3)), (1, (300, 4, 1))):
+        with pytest.raises(ValueError):
+            fg.forge_quantize_e4m3_blocks(x, codes, torch.empty(shape, device="cuda"), block_rows=br)
+    s3 = torch.empty(3, 1, 1, device="cuda")
+    with pytest.raises(ValueError):
+        fg.forge_quantize_e4m3_blocks(x[:3, :128].reshape(3, 1, 128).contiguous(), codes[:3, :128].reshape(3, 1, 128).contiguous(),
+                                      s3.reshape(1, 3, 1), block_rows=128)

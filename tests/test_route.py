@@ -376,3 +376,18 @@ def test_logits_that_may_be_written_over_are_read_by_plain_loads():
     grad = code[code.index("forge_route_grad_kernel("):]
     assert not re.findall(r"load_packed<X,", code[code.index("load_logits("):code.index("make_masks(")])
     assert "load_packed<X," not in grad and "__restrict__" not in grad
+
+
+@gpu
+def test_choices_laid_out_another_way_are_refused(cuda_device):
+    z = make(12, 8)
+    o = route(z, 2, True)
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError):
+        fg.forge_moe_route(z, o["experts"], o["weights"], o["counts"], o["offsets"], slots=i(2, 12))
+    d = torch.empty(12, 8, device="cuda")
+    with pytest.raises(ValueError):
+        fg.forge_moe_route_grad(z, o["experts"], o["counts"], o["live"], d, grad_weights=torch.ones(2, 12, device="cuda"))
+    flat = i(24)
+    fg.forge_moe_route(z, o["experts"], o["weights"], o["counts"], o["offsets"], slots=flat)
+    assert torch.equal(flat, o["slots"].reshape(-1))

@@ -15,6 +15,7 @@ int32 offsets [E+1] on the device.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from array import array
 from operator import attrgetter
@@ -593,7 +594,8 @@ def forge_moe_route(logits, experts, weights, counts, offsets, *, slots=None, ro
     s = lib().forge_moe_route(lp, _float_code(logits), T, E, ld, k, int(bool(normalize)),
                               _ints(experts, T * k, "experts"), _vector(weights, T * k, "weights"),
                               _ints(counts, E, "counts"), _ints(offsets, E + 1, "offsets"),
-                              _ints(slots, T * k, "slots"), _ints(rows, T * k, "rows"),
+                              _ints(_laid_out(slots, (T, k), "slots"), T * k, "slots"),
+                              _ints(rows, T * k, "rows"),
                               _ints(live, 1, "live"), _vector(loss, 1, "loss"),
                               _stream(stream, logits))
     _check(s, "forge_moe_route")
@@ -612,7 +614,8 @@ def forge_moe_route_grad(logits, experts, counts, live, dlogits, *, grad_weights
     s = lib().forge_moe_route_grad(lp, _float_code(logits), T, E, ld, k, int(bool(normalize)),
                                    _ints(experts, T * k, "experts"), _ints(counts, E, "counts"),
                                    _ints(live, 1, "live"),
-                                   _vector(grad_weights, T * k, "grad_weights"),
+                                   _vector(_laid_out(grad_weights, (T, k), "grad_weights"), T * k,
+                                           "grad_weights"),
                                    _vector(grad_loss, 1, "grad_loss"), dp, _float_code(dlogits),
                                    ldo, _stream(stream, logits))
     _check(s, "forge_moe_route_grad")
@@ -620,6 +623,14 @@ def forge_moe_route_grad(logits, experts, counts, live, dlogits, *, grad_weights
 
 def _blocks(n):
     return -(-n // 128)
+
+
+def _laid_out(t, shape, what):
+    """t itself (or None), refused where its entries lie in another order than `shape`'s:
+    [b, a] has as many as [a, b].  One dimension leaves the order to the caller."""
+    if t is not None and t.dim() != 1 and t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    return t
 
 
 def _byte_codes(t, what):
@@ -645,10 +656,12 @@ def forge_quantize_e4m3_blocks(x, codes, scales, *, block_rows=1, stream=None):
         raise ValueError("codes must have x's shape")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
+    down, across = -(-R // block_rows), _blocks(C)
+    _laid_out(scales, (E, down, across) if x.dim() == 3 else (down, across), "scales")
     s = lib().forge_quantize_e4m3_blocks(xp, _float_code(x), ldx, E, R, C, block_rows,
                                          _byte_codes(codes, "codes"),
-                                         _vector(scales, E * -(-R // block_rows) * _blocks(C),
-                                                 "scales"), _stream(stream, x))
+                                         _vector(scales, E * down * across, "scales"),
+                                         _stream(stream, x))
     _check(s, "forge_quantize_e4m3_blocks")
 
 
@@ -659,9 +672,9 @@ def _linear_sizes(A, sA, W, sW, Y, transpose):
     T = A.shape[0]
     if tuple(A.shape) != (T, K) or tuple(Y.shape) != (T, O):
         raise ValueError(f"A [T, {K}] and Y [T, {O}] expected, got {tuple(A.shape)}, {tuple(Y.shape)}")
-    blocks = _blocks(N) * _blocks(M) * (E[0] if E else 1)
-    return (_byte_codes(A, "A"), _vector(sA, T * _blocks(K), "sA"), _byte_codes(W, "W"),
-            _vector(sW, blocks, "sW")), (T, N, M)
+    of_A, of_W = (T, _blocks(K)), (*E, _blocks(N), _blocks(M))
+    return (_byte_codes(A, "A"), _vector(_laid_out(sA, of_A, "sA"), math.prod(of_A), "sA"),
+            _byte_codes(W, "W"), _vector(_laid_out(sW, of_W, "sW"), math.prod(of_W), "sW")), (T, N, M)
 
 
 def forge_linear_e4m3(A, sA, W, sW, Y, *, transpose=False, stream=None):
