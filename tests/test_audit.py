@@ -92,3 +92,21 @@ def test_no_closed_batch_copy_calls():
             code = open(f).read()
             for n in names:
                 assert n not in code, (f, n)
+
+
+def test_every_shared_helper_is_called():
+    """What forge_ptx.cuh, forge_rows.cuh and forge_device.h define or declare is used beside
+    its own definition and declaration."""
+    code = {os.path.basename(f): strip_comments(open(f).read())
+            for f in files(os.path.join(PKG, "csrc"), (".cu", ".cuh", ".h"))}
+    everything = "\n".join(code.values())
+    helper = re.compile(r"^(?:__device__ __forceinline__|inline|[a-z][\w:]*\*?)\s[\w:<>,* ]*?\b(\w+)\(", re.M)
+    idle = []
+    for f in ("forge_ptx.cuh", "forge_rows.cuh", "forge_device.h"):
+        for name in set(helper.findall(code[f])):
+            calls = re.findall(r"\b%s\b" % name, everything)
+            own = re.findall(r"^(?:__device__ __forceinline__|inline|cudaError_t|forge_status|int64_t|int\*)"
+                             r"[^;{}()]*\b(?:forge::)?%s\(" % name, everything, re.M)
+            if len(calls) <= len(own):
+                idle.append((f, name))
+    assert not idle, idle

@@ -835,20 +835,6 @@ cudaError_t forge::encode_bytes(CUtensorMap* map, const void* base, int64_t inne
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t forge::encode_rows64(CUtensorMap* map, void* base, int es, int64_t inner, int64_t rows)
-{
-    if (!ensure_encode()) return cudaErrorNotSupported;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner * es)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(
-        map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
-        dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 cudaError_t forge::stage_padded_rows(const void* src, void* dst, int64_t rows, int64_t row_bytes,
                                      int64_t dst_row_bytes, cudaStream_t stream)
 {

@@ -41,10 +41,6 @@ cudaError_t encode_bf16_kmajor(CUtensorMap* map, const void* base, int64_t inner
 cudaError_t encode_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
                          int64_t depth, int64_t ld_bytes, uint32_t box_rows);
 
-// fp32 (es 4) or bf16 (es 2) [rows, inner], packed, 16-byte aligned base and rows,
-// written in boxes of 64 bytes x 32 rows with 64-byte swizzle.
-cudaError_t encode_rows64(CUtensorMap* map, void* base, int es, int64_t inner, int64_t rows);
-
 // Copies [rows, row_bytes] from src (rows packed, base aligned to at least the
 // element size) into dst (256-byte aligned) with rows dst_row_bytes apart (a
 // multiple of 16 and >= row_bytes), on `stream`: the staging copy that makes

@@ -136,27 +136,6 @@ __device__ __forceinline__ uint64_t policy_evict_last()
     return p;
 }
 
-// 2-D tiled bulk tensor copy shared -> global; what lies outside the tensor is not
-// written.  The thread's bulk group: commit, then wait until at most N of its
-// groups still read shared memory.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x,
-                                             int32_t y)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(smem_addr(src))
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit()
-{
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait_read()
-{
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // cp.async of `bytes` (4, 8 or 16) from global to shared; only `src_bytes`
 // are read and the rest of the destination is zero-filled.
 __device__ __forceinline__ void cp_async(void* dst, const void* src, int bytes, int src_bytes)
@@ -179,32 +158,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Wait until at most n (0..3) of this thread's copy groups are outstanding.
-__device__ __forceinline__ void cp_async_wait_dyn(int n)
-{
-    switch (n) {
-    case 0: cp_async_wait<0>(); break;
-    case 1: cp_async_wait<1>(); break;
-    case 2: cp_async_wait<2>(); break;
-    default: cp_async_wait<3>(); break;
-    }
-}
-
-// Prefetch a tensor box into L2 (no shared-memory destination, no barrier).
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
-// Prefetch the 128-byte line holding `p` into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p)
-{
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 
 // Make this thread's generic-proxy shared-memory writes visible to the
 // async proxy (TMA, tensor core) before a later async operation reads them.
