@@ -45,7 +45,9 @@
  * a memory pool the library creates per device (allocated and freed on
  * `stream`; the pool keeps what it has reserved, at most the largest scratch
  * in use at once, until the process ends):
- *   - an operand (X or dY; for dX, dY or Wb; A or W of the e4m3 products) whose base is not 16-byte
+ *   - an operand (X or dY; for dX, dY or Wb; A or W of the e4m3 products, and,
+ *     on tiles of 256 tokens, rows of sA that are no multiple of four scales,
+ *     so any K with ceil(K / 128) no multiple of four) whose base is not 16-byte
  *     aligned or whose row stride is not a multiple of 16 bytes (any odd
  *     bf16 width, any e4m3 width not divisible by 16) is first copied into
  *     rows padded to 16 bytes (one extra read and write of that operand).
@@ -662,8 +664,9 @@ FORGE_API forge_status forge_quantize_e4m3_blocks(const void* x, forge_dtype x_d
  *           (block_rows = 128).
  *   Y       device of y_dtype (FORGE_BF16, rounded once to nearest even, or
  *           FORGE_F32), packed, written; must not overlap an operand.
- * Each block's products are summed in fp32, and the blocks, times their two
- * scales, in fp32.  Rows of codes of any width are accepted: an operand whose
+ * Each block's products are summed in fp32, and the blocks, times the product of
+ * their two scales, in fp32 (that product is taken first: below 2^-126 it loses
+ * digits, and from 2^128 on it is an infinity).  Rows of codes of any width are accepted: an operand whose
  * base is not 16-byte aligned or whose width is not a multiple of 16 is first
  * copied into padded rows in stream-ordered scratch from the library's memory
  * pool (a failed allocation returns FORGE_ERR_CUDA); with many tokens so are rows of

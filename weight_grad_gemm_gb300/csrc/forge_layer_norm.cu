@@ -17,8 +17,9 @@
 //
 // Measured (the copy bandwidth is 6.68 TB/s): 16384 x 4096 bf16 forward 48 us (5.6 TB/s;
 // captured, 4.6 TB/s reach DRAM, the rest of y is in L2 yet, and the two barriers of
-// a row leave 60% of the issue slots), there and back 81 (5.0 TB/s; 75 for the rows, 6 for the
-// fold).  64 x 4096: 10.5 us, two kernels' latency.  16 x 4096 forward: 4.3 us.
+// a row leave 57% of the issue slots), the gradient 81 (5.0 TB/s; 75 for the rows, 6 for the
+// fold).  The gradient of 777 x 1023 fp32: 10.4 us, two kernels' latency.  16 x 4096 forward:
+// 4.3 us; 4096 x 16384 bf16 68 (a block of 32 warps a row, weights read again for each).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -29,7 +29,8 @@
 //
 // Measured (cuBLAS reaches 3.86 PFLOP/s with e4m3): 8192 x 14336 x 4096 400 us (2.40
 // PFLOP/s; captured, the tensor core is busy 53% of the time), 8192 x 4096 x 4096 132
-// (2.09), 32768 tokens by 8 experts of 14336 x 4096 1626 (2.37).  What bounds them is the
+// (2.09), 32768 tokens by 8 experts of 14336 x 4096 1630 to 1750 from box to box (2.20 to
+// 2.36).  What bounds them is the
 // hand-over: a block's MMAs take 512 cycles, but from the last of them through the
 // epilogue's wait, its four loads, the sums of the first two and back to the issuer takes
 // some 1,100, so that with two slots a block comes every 820 to 870.  Without the
@@ -704,8 +705,9 @@ __global__ void __launch_bounds__(Few<NT>::threads, Few<NT>::ctas)
         }
     } else if (warp <= F::issuers) {
         // ---------------------------------------------------- MMA issuers (lane 0)
-        // Every other block each, as the pairs' (16 tokens of 4096 x 14336: 13.0 us, by one
-        // issuer 16.4; 128 of 14336 x 4096: 22.8, 25.0).
+        // Every other block each, as the pairs' (128 tokens of 14336 x 4096: 22.8 us, by one
+        // issuer 25.0; 16 of 4096 x 14336 where L2 holds the weight 13.0 and 16.4, and 16.4 by
+        // either where it comes from memory).
         if (lane == 0) {
             constexpr uint32_t idesc = ptx::make_idesc(0, 0, W_MN, false, 128, NT);
             constexpr uint64_t kStepW = (W_MN ? 32 * 128 : 32) >> 4, kStepA = 32 >> 4;

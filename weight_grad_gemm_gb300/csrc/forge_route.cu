@@ -24,7 +24,7 @@
 //
 // Measured: 65536 x 256 fp32 to 8 and back 86 us, of it the tokens kernel 47 (bound by
 // instructions: 74% of the issue slots beside 1.4 TB/s), scan 6 and place 12 (latency), the
-// gradient 28 (4.7 TB/s over both ways, a third of it in L2; 61% of the issue slots).
+// gradient 28 (4.7 TB/s over both ways, a third of it in L2; 65% of the issue slots).
 // 16384 x 8 bf16 to 2 and back: 17 to 22 us for three launches; 16 x 8, one launch: 6.4.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
