@@ -69,62 +69,57 @@ struct Backward {
 };
 
 // A row by 32 W threads (thread t of them) in three passes, the second and third from L2.
-// Rows whose squares, or whose sum, pass the largest number are taken at kSmall times their
-// size, which is far from the other end of the range (one of their deviations is above
-// some 1e14); rows with a NaN or an infinity end as NaN all the same.
+// Rows whose squares, or whose sum, pass the largest number are taken at kSmall times
+// their size, which is far from the other end of the range (one of their deviations is
+// above some 1e14); rows with a NaN or an infinity end as NaN all the same.
 constexpr float kSmall = 0x1p-96f;
-template <typename X, int V, int W>
+template <bool OVER, typename X, int V, int W>
 __device__ __forceinline__ void row_in_passes(const X* row, const Forward& p, int64_t r, int t,
                                               float* sh0, float* sh1)
 {
     const float inv = 1.0f / static_cast<float>(p.D);
     const int64_t step = 32 * W * V;
     float s[1], q[1], mu;
+    auto each = [&](auto use) {
+        for (int64_t c = t * V; c < p.D; c += step) use(load_row<OVER, X, V>(row + c), c);
+    };
     // mean and sum of squares of f times the row
     auto statistics = [&](float f) {
         s[0] = q[0] = 0.0f;
-        for (int64_t c = t * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_plain<X, V>(row + c);
+        each([&](const Packed<X, V>& raw, int64_t) {
 #pragma unroll
             for (int j = 0; j < V; ++j) s[0] = fmaf(entry(raw, j), f, s[0]);
-        }
+        });
         block_sums<W>(s, sh0);
         mu = s[0] * inv;
-        for (int64_t c = t * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_plain<X, V>(row + c);
+        each([&](const Packed<X, V>& raw, int64_t) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float d = fmaf(entry(raw, j), f, -mu);
                 q[0] = fmaf(d, d, q[0]);
             }
-        }
+        });
         block_sums<W>(q, sh1);
     };
-    auto finish = [&](float f) {
-        const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, p.eps * f * f));
-        if (t == 0) {
-            if (p.mean) p.mean[r] = mu * (1.0f / f);
-            if (p.rstd) p.rstd[r] = rstd * f;
-        }
-        for (int64_t c = t * V; c < p.D; c += step) {
-            const Packed<X, V> raw = load_plain<X, V>(row + c);
-            const Packed<float, V> w = load_packed<float, V>(p.weight + c);
-            const Packed<float, V> b =
-                p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
-            float v[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] = fmaf(fmaf(entry(raw, j), f, -mu) * rstd, entry(w, j), entry(b, j));
-            store_as(p.y, p.y_f32, r * p.ldy + c, v);
-        }
-    };
     statistics(1.0f);
-    if (q[0] <= FLT_MAX) {  // (alike in all of the row's threads)
-        finish(1.0f);
-    } else {
-        statistics(kSmall);
-        finish(kSmall);
+    const bool far = !(q[0] <= FLT_MAX);  // (alike in all of the row's threads)
+    if (far) statistics(kSmall);
+    const float f = far ? kSmall : 1.0f;
+    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, far ? p.eps * kSmall * kSmall : p.eps));
+    if (t == 0) {
+        if (p.mean) p.mean[r] = far ? mu * (1.0f / kSmall) : mu;
+        if (p.rstd) p.rstd[r] = rstd * f;
     }
+    each([&](const Packed<X, V>& raw, int64_t c) {
+        const Packed<float, V> w = load_packed<float, V>(p.weight + c);
+        const Packed<float, V> b =
+            p.bias ? load_packed<float, V>(p.bias + c) : zero_packed<float, V>();
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            v[j] = fmaf(fmaf(entry(raw, j), f, -mu) * rstd, entry(w, j), entry(b, j));
+        store_as(p.y, p.y_f32, r * p.ldy + c, v);
+    });
 }
 
 // E entries a thread in vectors of V, W warps a row, RB rows at a time; the rows after
@@ -196,10 +191,14 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
             }
         }
         block_sums<W>(rstd, sh[1]);
-        bool far = false;  // a row of the turn is not for registers
+        // A row of the turn is not for registers (alike in all threads of the rows): the loop
+        // ends before the turn's stores.  (By a vote 16384 x 4099 bf16 124 us, by the flag
+        // alone 134; 32 warps with their 64 registers the flag behind the stores that
+        // it skips, 2048 x 16383 bf16 70.4 and 72.3.)
+        bool far = false;
 #pragma unroll
         for (int k = 0; k < RB; ++k) far |= !(rstd[k] <= FLT_MAX);
-        if (far) break;  // (alike in all threads of the rows)
+        if (W < 32 && __any_sync(0xffffffffu, far)) break;
 #pragma unroll
         for (int k = 0; k < RB; ++k) {
             rstd[k] = 1.0f / sqrtf(fmaf(rstd[k], inv, p.eps));
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * W * 32 + t) * V;
-            if (c < p.D) {
+            if (c < p.D && (W < 32 || !far)) {
                 if (!kHold) load_weights(i);
 #pragma unroll
                 for (int k = 0; k < RB; ++k) {
@@ -224,24 +223,28 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
                 }
             }
         }
+        if (W == 32 && far) break;
     }
-    // from the first turn with such a row on, one row after another (ordinary ones to the
-    // same bits: their sums run in the same order)
+    // from the first turn with such a row on, one row after another (ordinary ones to the same
+    // bits: their sums run in the same order)
     for (; r < p.R; r += step)
 #pragma unroll 1
         for (int k = 0; k < RB && r + k < p.R; ++k)
-            row_in_passes<X, V, W>(x + static_cast<int64_t>(r + k) * p.ldx, p, r + k, t, sh[0],
-                                   sh[1]);
+            row_in_passes<true, X, V, W>(x + static_cast<int64_t>(r + k) * p.ldx, p, r + k, t,
+                                         sh[0], sh[1]);
 }
 
-// Rows wider than the registers hold.
-template <typename X, int V>
+// Rows wider than the registers hold; OVER: y is x.  (Rows that nothing writes are read by
+// read-only loads, which the compiler takes over the stores before them: 2048 x 20001 fp32
+// 93 us, by plain loads 122.)
+template <bool OVER, typename X, int V>
 __global__ void __launch_bounds__(kLongThreads)
     forge_layer_norm_long_kernel(const X* x, const Forward p)
 {
     __shared__ float sh[2][kLongThreads / 32];
     for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x)
-        row_in_passes<X, V, kLongThreads / 32>(x + r * p.ldx, p, r, threadIdx.x, sh[0], sh[1]);
+        row_in_passes<OVER, X, V, kLongThreads / 32>(x + r * p.ldx, p, r, threadIdx.x, sh[0],
+                                                     sh[1]);
 }
 
 // E entries a thread in vectors of V, W warps a row.  The weights lie in shared memory,
@@ -422,7 +425,8 @@ __global__ void __launch_bounds__(threads_of(W), grad_threads(V, E) / threads_of
 // a row, the first kHeld vectors of a thread kept from the first, the rest from L2
 // (4096 x 16384 bf16 with dw and db: 144 us, all from L2 162; 2048 x 16384 fp32 134, with
 // eight vectors of its twice as many registers 158).
-template <typename G, typename X, int V>
+// OVER: dx is dy or x, as above (2048 x 20001 bf16 164 us, by plain loads 215).
+template <bool OVER, typename G, typename X, int V>
 __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
     forge_layer_norm_grad_long_kernel(const G* dy, const X* x,
                                       const Backward p)
@@ -441,8 +445,8 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             const int64_t c = c0 + i * step;
-            gheld[i] = c < p.D ? load_plain<G, V>(grow + c) : zero_packed<G, V>();
-            xheld[i] = c < p.D ? load_plain<X, V>(xrow + c) : zero_packed<X, V>();
+            gheld[i] = c < p.D ? load_row<OVER, G, V>(grow + c) : zero_packed<G, V>();
+            xheld[i] = c < p.D ? load_row<OVER, X, V>(xrow + c) : zero_packed<X, V>();
         }
         const float mu = p.mean[r], rstd = p.rstd[r];
         float s[2] = {0.0f, 0.0f};
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
         for (int i = 0; i < kHeld; ++i)
             if (c0 + i * step < p.D) add(gheld[i], xheld[i], c0 + i * step);
         for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
-            add(load_plain<G, V>(grow + c), load_plain<X, V>(xrow + c), c);
+            add(load_row<OVER, G, V>(grow + c), load_row<OVER, X, V>(xrow + c), c);
         block_sums<kWideThreads / 32>(s, sh[turn]);
         const float a = s[0] * inv, b = s[1] * inv;
         auto store = [&](const Packed<G, V>& graw, const Packed<X, V>& xraw, int64_t c) {
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kWideThreads, 1024 / kWideThreads)
         for (int i = 0; i < kHeld; ++i)
             if (c0 + i * step < p.D) store(gheld[i], xheld[i], c0 + i * step);
         for (int64_t c = c0 + kHeld * step; c < p.D; c += step)
-            store(load_plain<G, V>(grow + c), load_plain<X, V>(xrow + c), c);
+            store(load_row<OVER, G, V>(grow + c), load_row<OVER, X, V>(xrow + c), c);
     }
 }
 
@@ -495,8 +499,8 @@ __global__ void __launch_bounds__(32 * kLongWarps)
     for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
 #pragma unroll 4
     for (int64_t r = blockIdx.y; r < p.R; r += gridDim.y) {
-        const Packed<G, V> graw = load_plain<G, V>(dy + r * p.ldg + c);
-        const Packed<X, V> xraw = load_plain<X, V>(x + r * p.ldx + c);
+        const Packed<G, V> graw = load_row<false, G, V>(dy + r * p.ldg + c);
+        const Packed<X, V> xraw = load_row<false, X, V>(x + r * p.ldx + c);
         const float mu = p.mean[r], rstd = p.rstd[r];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -584,8 +588,11 @@ void forward(const X* x, const Forward& p, int sms, cudaStream_t s)
         go(forge_layer_norm_kernel<X, V, 16, 16, 2>, 16, 2);
     else if (D <= kMaxForward)
         go(forge_layer_norm_kernel<X, V, 16, 32, 1>, 32, 1);
+    else if (x == p.y)
+        forge_layer_norm_long_kernel<true, X, V>
+            <<<blocks_for(p.R, 1, 2LL * sms), kLongThreads, 0, s>>>(x, p);
     else
-        forge_layer_norm_long_kernel<X, V>
+        forge_layer_norm_long_kernel<false, X, V>
             <<<blocks_for(p.R, 1, 2LL * sms), kLongThreads, 0, s>>>(x, p);
 }
 
@@ -644,8 +651,10 @@ int backward_any(const G* dy, const X* x, const Backward& p, int V, int sms, cud
         constexpr int slab = 32 * kLongWarps * N;
         const unsigned slabs = static_cast<unsigned>((p.D + slab - 1) / slab);
         forge_layer_norm_columns_kernel<G, X, N><<<dim3(slabs, parts), 32 * kLongWarps, 0, s>>>(dy, x, p);
-        forge_layer_norm_grad_long_kernel<G, X, N>
-            <<<blocks_for(p.R, 1, 1024LL / kWideThreads * sms), kWideThreads, 0, s>>>(dy, x, p);
+        auto rows = p.dx == static_cast<const void*>(dy) || p.dx == static_cast<const void*>(x)
+                        ? forge_layer_norm_grad_long_kernel<true, G, X, N>
+                        : forge_layer_norm_grad_long_kernel<false, G, X, N>;
+        rows<<<blocks_for(p.R, 1, 1024LL / kWideThreads * sms), kWideThreads, 0, s>>>(dy, x, p);
     };
     if (V == 1)
         go(std::integral_constant<int, 1>());

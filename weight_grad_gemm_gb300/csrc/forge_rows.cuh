@@ -71,6 +71,16 @@ __device__ __forceinline__ Packed<T, V> load_plain(const T* p)
     return r;
 }
 
+// Of rows that the call writes over (OVER), or leaves alone.
+template <bool OVER, typename T, int V>
+__device__ __forceinline__ Packed<T, V> load_row(const T* p)
+{
+    if constexpr (OVER)
+        return load_plain<T, V>(p);
+    else
+        return load_packed<T, V>(p);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ Packed<T, V> zero_packed()
 {
