@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(threads_of(W), W < 32 ? kThreadsAtWork / threa
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * W * 32 + t) * V;
-                next[k][i] = c < p.D && r + k < p.R ? load_plain<X, V>(x + static_cast<int64_t>(r + k) * p.ldx + c)
-                                                    : zero_packed<X, V>();
+                next[k][i] = c < p.D && r + k < p.R
+                                 ? load_plain<X, V>(x + static_cast<int64_t>(r + k) * p.ldx + c)
+                                 : zero_packed<X, V>();
             }
     };
     constexpr bool kHold = W < 32;  // (1024 threads have 64 registers each)
